@@ -51,7 +51,21 @@ typedef enum {
  * being code * dims->k_scale (K) or code * dims->v_scale (V); q, out and the
  * new rows of kv_append are bf16 ("KV cache & Flash Attention", section
  * "Practical use": an fp8 KV cache halves the bytes attention reads). */
-typedef enum { SVP_F32 = 0, SVP_BF16 = 1, SVP_FP8_E4M3 = 2 } svp_dtype;
+
+/* SVP_FP4_E2M1: the caches hold 4-bit rows.  A row of head_dim elements is
+ * head_dim/2 bytes of E2M1 codes (1 sign bit, 2 exponent bits, bias 1, 1
+ * mantissa bit: magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6; element 2i in the low
+ * nibble of byte i) followed by head_dim/16 E4M3 scales, one for each 16
+ * consecutive elements: 9/16 byte per element in all, so a cache is
+ * [num_blocks, num_kv_heads, 16, 9*head_dim/16] bytes.  A value is
+ * code * scale * dims->k_scale (K) or * dims->v_scale (V); q, out and the
+ * new rows are bf16. */
+typedef enum {
+  SVP_F32 = 0,
+  SVP_BF16 = 1,
+  SVP_FP8_E4M3 = 2,
+  SVP_FP4_E2M1 = 3
+} svp_dtype;
 
 /* Flags returned by svp_read_device_status(). */
 enum {
@@ -63,9 +77,10 @@ enum {
 
 /* Shapes shared by kv_append and paged_decode_attention.
  *   q, out           [batch, q_len, num_q_heads, head_dim]        dtype
- *                    (bf16 when dtype is SVP_FP8_E4M3)
+ *                    (bf16 when dtype is SVP_FP8_E4M3 or SVP_FP4_E2M1)
  *   k_cache, v_cache [num_blocks, num_kv_heads, block_size, head_dim] dtype
- *                    (one head's page is one contiguous run)
+ *                    (one head's page is one contiguous run; rows of
+ *                    9*head_dim/16 bytes for SVP_FP4_E2M1)
  *   block_table      [batch, max_blocks_per_seq] int32; entry lb of row b
  *                    is the physical page of logical block lb of sequence b
  *                    (positions lb*16 .. lb*16+15).  Entries of pages that
@@ -89,13 +104,15 @@ typedef struct {
   size_t workspace_bytes; /* size of `workspace`                           */
   int split_pages;        /* fewest pages per CTA slice; 0 = automatic (8) */
   int kernel_path;        /* svp_kernel_path; SVP_PATH_AUTO by default     */
-  float k_scale;          /* SVP_FP8_E4M3 caches: value = code * scale    */
+  float k_scale;          /* FP8 and FP4 caches: the cache's scale factor */
   float v_scale;          /* (finite, > 0); ignored for other dtypes      */
 } svp_dims;
 
 /* Which attention kernel variant runs.  AUTO picks tensor cores (bf16 only)
  * when a kv head serves at least 3 query rows (GQA group x q_len): TCGEN05
  * for head_dim 128, TENSOR_CORES for head_dim 64; CUDA cores otherwise.
+ * An SVP_FP4_E2M1 cache always takes warp-level mma.sync (fp16 operands
+ * built from the codes in registers, fp32 accumulate).
  * All compute the same quantity; forcing a path exists for testing and
  * tuning.
  *   CUDA_CORES    fp32 FMA dot products, any dtype.
@@ -104,8 +121,9 @@ typedef struct {
  *                 accumulators in tensor memory, keys as the 128-row M
  *                 dimension (bf16, head_dim 128, 512 sequences per
  *                 kernel launch).
- * A forced tensor path on data it cannot take (fp32; head_dim 64 for
- * TCGEN05) is SVP_ERR_UNSUPPORTED. */
+ * A forced path on data it cannot take (a tensor path on fp32 or FP8;
+ * head_dim 64 for TCGEN05; anything but TENSOR_CORES on FP4) is
+ * SVP_ERR_UNSUPPORTED. */
 typedef enum {
   SVP_PATH_AUTO = 0,
   SVP_PATH_CUDA_CORES = 1,
@@ -238,13 +256,100 @@ size_t paged_decode_workspace_size(const svp_dims *dims, int q_len,
  * "PagedAttention").  seq_lens are the lengths AFTER the append.  A byte
  * copy; into an FP8 cache each value x is stored as the E4M3 code of the
  * fp32 quotient x / k_scale (resp. v_scale), nearest with ties to even,
- * saturating at +-448.  Uses no workspace.
+ * saturating at +-448.  Into an FP4 cache, with y the fp32 quotient
+ * x / k_scale and 16 elements sharing a scale: scale = E4M3(max|y| / 6) kept
+ * in [2^-9, 448], code = E2M1(y / scale), both quotients in fp32 and both
+ * roundings to nearest with ties to even, saturating.  E2M1 has no infinity
+ * or NaN: an infinite element is stored as +-6 of its block's scale, a NaN
+ * as +6, and neither counts towards max|y| unless it is infinite.  Uses no
+ * workspace.
  * Errors as for paged_decode_attention; n_new in [0, 64]; k_new, v_new,
  * k_cache and v_cache must be 16-byte aligned (else SVP_ERR_INVALID_ARG,
  * before any launch). */
 int kv_append(const svp_dims *dims, const void *k_new, const void *v_new,
               void *k_cache, void *v_cache, const int32_t *block_table,
               const int32_t *seq_lens, int n_new, cudaStream_t stream);
+
+/* KV gather: the inverse of kv_append.  Row i of sequence b of
+ * k_out/v_out [batch, n_rows, num_kv_heads, head_dim] (fp32 for an SVP_F32
+ * cache, else bf16) is the value the caches hold at logical position
+ * start + i, start = starts[b] or, with starts == NULL, seq_lens[b] - n_rows
+ * (the newest rows).  Positions outside [0, seq_lens[b]) give zero rows.
+ * FP8 and FP4 values are code (* scale) * k_scale rounded once to bf16.
+ * For dense kernels over a cached prefix, and for moving rows between
+ * caches.  A sequence length outside [0, max_blocks_per_seq*16] gives zero
+ * rows and SVP_DEV_BAD_SEQ_LEN, a bad block id a zero row and
+ * SVP_DEV_BAD_BLOCK_ID.  Uses no workspace.
+ * Errors as for kv_append, with n_rows in [0, 2^31). */
+int kv_gather(const svp_dims *dims, const void *k_cache, const void *v_cache,
+              const int32_t *block_table, const int32_t *seq_lens,
+              const int32_t *starts, int n_rows, void *k_out, void *v_out,
+              cudaStream_t stream);
+
+/* ---- eviction by accumulated attention weight -------------------------
+ * A cached key's score is the attention weight it has received.  The caller
+ * holds one fp32 score per cached row, paged like the cache:
+ * scores [num_blocks, num_kv_heads, 16], and with every step calls
+ * paged_score_update after the attention call; when sequences have outgrown
+ * their budget, kv_evict keeps the best rows. */
+
+/* Score update: for every key j that a query row sees,
+ *   scores[page(j), g, j % 16] += sum over the rows (i, h) of kv head g that
+ *                                 see j of exp(scale * <q[b,i,h], K_j> - lse[b,i,h])
+ * with lse as paged_decode_attention returned it for the same q, caches,
+ * lengths and mask (n_sink and window, or tree_mask if not NULL, as there).
+ * The newest n_fresh positions (0 <= n_fresh <= q_len; q_len for the rows
+ * just appended) start from zero: their old score is not read.  Other keys'
+ * scores stay as they are.  Rows with lse = -inf add nothing.  Reads K
+ * only; one launch for each 128 query rows of a kv head (group * q_len); no
+ * workspace, no atomics: the result does not depend on the order of the
+ * CTAs.  No page may appear twice in the call's visible
+ * block-table entries (a page's scores belong to one sequence).
+ * Errors: those of paged_decode_attention (tree_mask: of
+ * paged_tree_attention), SVP_ERR_INVALID_ARG for n_fresh outside [0, q_len]
+ * or lse / scores not 4-byte aligned.  dims->workspace, split_pages,
+ * kernel_path and v_scale are not used. */
+int paged_score_update(const svp_dims *dims, const void *q,
+                       const void *k_cache, const float *lse,
+                       const int32_t *block_table, const int32_t *seq_lens,
+                       int q_len, int n_sink, int window,
+                       const uint32_t *tree_mask, float scale, int n_fresh,
+                       float *scores, cudaStream_t stream);
+
+/* Eviction: every (sequence b, kv head g) longer than `budget` keeps its
+ * first n_sink positions, its newest n_recent and, of those between, the
+ * budget - n_sink - n_recent with the largest scores (ties: the lower
+ * position; a NaN score counts as -inf).  A sequence of at most budget rows
+ * keeps all of them.  Kept rows stay in position order: slot i of the
+ * result is row kept[b, g, i] of K, of V and of scores.
+ *   kept      [batch, num_kv_heads, budget] int32, written: the kept
+ *             positions in increasing order, then -1
+ *   new_lens  [batch] int32, written: min(seq_lens[b], budget); may be
+ *             seq_lens itself
+ * dst_block_table [batch, dst_max_blocks] int32 names the pages the kept
+ * rows go to, slot i to page dst_block_table[b][i/16], row i%16; NULL
+ * (dst_max_blocks ignored): block_table itself, i.e. in place.  Per
+ * sequence, the destination entries are either exactly block_table's first
+ * ones (in place; pages that no other sequence uses) or pages that hold no
+ * row of the call (then the source pages are not written: shared prefixes
+ * stay intact).  Different heads keep different rows in the same slots; the
+ * pages past the new length are the caller's to free.  Keys are moved as
+ * stored: a rotary embedding stays that of the row's old position, and
+ * windows and sinks of later calls count slots.
+ * A sequence length outside [0, max_blocks_per_seq*16] gives new_lens -1,
+ * kept all -1 and SVP_DEV_BAD_SEQ_LEN; a row on a bad page id is not moved
+ * (score read as -inf), with SVP_DEV_BAD_BLOCK_ID.  Two launches, no
+ * workspace; deterministic.
+ * Errors: SVP_ERR_INVALID_ARG for null pointers, misaligned caches (16
+ * bytes) or scores (4), budget < 1, n_sink < 0, n_recent < 0, n_sink +
+ * n_recent > budget, budget > 16 * the destination's blocks per sequence;
+ * SVP_ERR_UNSUPPORTED as for kv_append and for max_blocks_per_seq >
+ * 2^26. */
+int kv_evict(const svp_dims *dims, void *k_cache, void *v_cache, float *scores,
+             const int32_t *block_table, const int32_t *seq_lens, int budget,
+             int n_sink, int n_recent, const int32_t *dst_block_table,
+             int dst_max_blocks, int32_t *kept, int32_t *new_lens,
+             cudaStream_t stream);
 
 /* Speculative acceptance (pages: "How speculative decoding doubles LLM
  * speed", step 3 (sampling) and section "Absolute mathematical exactness";

@@ -8,10 +8,14 @@ nothing; the first call loads the library and raises if it is not built.
 from .binding import (  # noqa: F401
     StepRunner,
     SvpError,
+    fp4_row_bytes,
     kv_append,
+    kv_evict,
+    kv_gather,
     last_launch_count,
     load_library,
     paged_decode_attention,
+    paged_score_update,
     paged_tree_attention,
     read_device_status,
     spec_accept,

@@ -22,13 +22,14 @@ LIB_PATH = os.path.join(_HERE, "libsvp.so")
 
 SVP_OK, SVP_ERR_INVALID_ARG, SVP_ERR_UNSUPPORTED, SVP_ERR_CUDA, SVP_ERR_WORKSPACE = (
     0, -1, -2, -3, -4)
-SVP_F32, SVP_BF16, SVP_FP8_E4M3 = 0, 1, 2
+SVP_F32, SVP_BF16, SVP_FP8_E4M3, SVP_FP4_E2M1 = 0, 1, 2, 3
 PATH_AUTO, PATH_CUDA_CORES, PATH_TENSOR_CORES, PATH_TCGEN05 = 0, 1, 2, 3
 DEV_BAD_BLOCK_ID, DEV_BAD_SEQ_LEN, DEV_BAD_TOKEN, DEV_TIMEOUT = 1, 2, 4, 8
 EXPORTED = ("paged_decode_attention", "paged_decode_attention_noalloc",
             "paged_tree_attention",
             "paged_decode_workspace_size",
-            "kv_append", "spec_accept", "spec_accept_ex", "spec_accept_tree",
+            "kv_append", "kv_gather", "paged_score_update", "kv_evict",
+            "spec_accept", "spec_accept_ex", "spec_accept_tree",
             "svp_read_device_status",
             "svp_step_create", "svp_step_host_buffer", "svp_step_launch",
             "svp_step_wait", "svp_step_stream", "svp_step_destroy",
@@ -114,6 +115,14 @@ def load_library(path: str = LIB_PATH):
         lib.paged_decode_workspace_size.restype = sz
         lib.kv_append.argtypes = [dims_p, vp, vp, vp, vp, vp, vp, i32, vp]
         lib.kv_append.restype = i32
+        lib.kv_gather.argtypes = [dims_p, vp, vp, vp, vp, vp, i32, vp, vp, vp]
+        lib.kv_gather.restype = i32
+        lib.paged_score_update.argtypes = [dims_p, vp, vp, vp, vp, vp, i32, i32,
+                                           i32, vp, f32, i32, vp, vp]
+        lib.paged_score_update.restype = i32
+        lib.kv_evict.argtypes = [dims_p, vp, vp, vp, vp, vp, i32, i32, i32, vp,
+                                 i32, vp, vp, vp]
+        lib.kv_evict.restype = i32
         lib.spec_accept.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp, vp, vp]
         lib.spec_accept.restype = i32
         lib.spec_accept_ex.argtypes = ([i32, i32, i32] + [vp] * 4 +
@@ -171,13 +180,35 @@ def _dtype_code(t: torch.Tensor) -> int:
 _FP8_TYPES = (torch.uint8, getattr(torch, "float8_e4m3fn", torch.uint8))
 
 
+def fp4_row_bytes(head_dim: int) -> int:
+    """Bytes of a 4-bit cache row: head_dim/2 of E2M1 codes (element 2i in the
+    low nibble of byte i), then head_dim/16 E4M3 scales.  A 4-bit cache is a
+    uint8 tensor [num_blocks, Hkv, 16, fp4_row_bytes(head_dim)]."""
+    return head_dim // 2 + head_dim // 16
+
+
+_FP4_DIMS = {fp4_row_bytes(d): d for d in (64, 128)}
+
+
+def _head_dim(cache):
+    """head_dim of a cache: its last dimension, or what a 4-bit row holds
+    (36 and 72 bytes are no FP8 head_dim)."""
+    n = cache.shape[-1]
+    return _FP4_DIMS.get(n, n) if cache.dtype == torch.uint8 else n
+
+
+def _is_fp4(cache):
+    return cache.dtype == torch.uint8 and cache.shape[-1] in _FP4_DIMS
+
+
 def _cache_code(k_cache, q_dtype):
     """dtype code of a call: the cache's; an FP8 E4M3 cache (uint8 codes or
-    float8_e4m3fn) pairs with bf16 q / out / new rows."""
+    float8_e4m3fn) and a 4-bit cache (uint8 rows of fp4_row_bytes) pair with
+    bf16 q / out / new rows."""
     if k_cache.dtype in _FP8_TYPES:
         _need(q_dtype == torch.bfloat16,
-              "an FP8 cache takes bf16 q, out and new rows")
-        return SVP_FP8_E4M3
+              "an FP8 or FP4 cache takes bf16 q, out and new rows")
+        return SVP_FP4_E2M1 if _is_fp4(k_cache) else SVP_FP8_E4M3
     _need(k_cache.dtype == q_dtype, "q and the caches must share a dtype")
     return _dtype_code(k_cache)
 
@@ -238,8 +269,8 @@ def paged_decode_attention(q, k_cache, v_cache, block_table, seq_lens,
                            v_scale=1.0):
     """out [B, q_len, Hq, D] (q's dtype) and lse [B, q_len, Hq] fp32 of paged
     decode/verify attention (include/svp.h: paged_decode_attention).  FP8
-    E4M3 caches (uint8 codes or float8_e4m3fn) take bf16 q and their
-    k_scale / v_scale."""
+    E4M3 caches (uint8 codes or float8_e4m3fn) and 4-bit caches (uint8 rows of
+    fp4_row_bytes(D)) take bf16 q and their k_scale / v_scale."""
     return _attention(q, k_cache, v_cache, block_table, seq_lens, q_len,
                       n_sink, window, None, scale, out, lse, workspace,
                       split_pages, kernel_path, stream, k_scale, v_scale)
@@ -269,6 +300,9 @@ def _attention(q, k_cache, v_cache, block_table, seq_lens, q_len, n_sink,
                  (block_table, "block_table"), (seq_lens, "seq_lens")):
         _cuda_contig(t, n)
     code = _cache_code(k_cache, q.dtype)
+    if code == SVP_FP4_E2M1:
+        _fp4_call(q, k_cache, v_cache, block_table, seq_lens, tree_mask, out,
+                  lse, workspace)
     _need(v_cache.dtype == k_cache.dtype, "k_cache and v_cache must share a dtype")
     _need(k_cache.shape == v_cache.shape and k_cache.dim() == 4,
           "k_cache/v_cache must be [num_blocks, Hkv, block_size, D]")
@@ -281,6 +315,12 @@ def _attention(q, k_cache, v_cache, block_table, seq_lens, q_len, n_sink,
     _need(ql == q_len, "q.shape[1] must equal q_len")
     if scale is None:
         scale = 1.0 / math.sqrt(D)
+    if code == SVP_FP4_E2M1:
+        with _on(q.device, stream):
+            return _attention_fp4(lib, q, k_cache, v_cache, block_table,
+                                  seq_lens, n_sink, window, tree_mask, scale,
+                                  out, lse, workspace, split_pages, kernel_path,
+                                  stream, k_scale, v_scale)
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
@@ -311,11 +351,131 @@ def _attention(q, k_cache, v_cache, block_table, seq_lens, q_len, n_sink,
     return out, lse
 
 
+class _on:
+    """The device of a call's tensors made current, and the stream the call
+    was given (torch's current one otherwise), so that memory allocated in
+    between belongs to the stream that uses it."""
+
+    __slots__ = ("dev", "stream", "back")
+
+    def __init__(self, device, stream):
+        self.dev = (None if device.index is None or
+                    device.index == torch.cuda.current_device()
+                    else torch.cuda.device(device))
+        self.stream = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.dev is not None:
+            self.dev.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+
+    def __exit__(self, *exc):
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        if self.dev is not None:
+            self.dev.__exit__(*exc)
+
+
+def _args(device, *named):
+    """Checks (tensor, name, dtype or None, shape or None) tuples: on
+    `device`, contiguous, of that type and shape."""
+    for t, name, dtype, shape in named:
+        if t.device != device or not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor on {device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if dtype is not None and t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if shape is not None and tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _check_pages(k_cache, block_table, seq_lens, batch, v_cache=None):
+    """The paged arguments of a call for `batch` sequences."""
+    dev = k_cache.device
+    _need(k_cache.dim() == 4, "caches must be [num_blocks, Hkv, block_size, row]")
+    _need(block_table.dim() == 2, "block_table must be int32 [B, max_blocks]")
+    _args(dev, (k_cache, "k_cache", None, None),
+          (block_table, "block_table", torch.int32, (batch, block_table.shape[1])),
+          (seq_lens, "seq_lens", torch.int32, (batch,)))
+    if v_cache is not None:
+        _args(dev, (v_cache, "v_cache", k_cache.dtype, tuple(k_cache.shape)))
+
+
+def _paged_dims(batch, num_q_heads, cache, max_blocks, code, k_scale=1.0,
+                v_scale=1.0, workspace=None, split_pages=0, kernel_path=0):
+    return SvpDims(batch, num_q_heads, cache.shape[1], _head_dim(cache),
+                   cache.shape[2], max_blocks, cache.shape[0], code,
+                   None if workspace is None else workspace.data_ptr(),
+                   0 if workspace is None else
+                   workspace.numel() * workspace.element_size(),
+                   int(split_pages), int(kernel_path), float(k_scale),
+                   float(v_scale))
+
+
+def _fp4_call(q, k_cache, v_cache, block_table, seq_lens, tree_mask, out, lse,
+              workspace):
+    _need(q.dim() == 4, "q must be [B, q_len, Hq, D]")
+    _check_pages(k_cache, block_table, seq_lens, q.shape[0], v_cache)
+    B, ql, Hq, D = q.shape
+    _need(_head_dim(k_cache) == D, f"a 4-bit cache row for head_dim {D} has "
+          f"{fp4_row_bytes(D)} bytes, got {k_cache.shape[-1]}")
+    dev = k_cache.device
+    _args(dev, (q, "q", torch.bfloat16, None))
+    for t, name, dtype, shape in ((tree_mask, "tree_mask", None, (B, ql)),
+                                  (out, "out", torch.bfloat16, (B, ql, Hq, D)),
+                                  (lse, "lse", torch.float32, (B, ql, Hq)),
+                                  (workspace, "workspace", None, None)):
+        if t is not None:
+            _args(dev, (t, name, dtype, shape))
+
+
+def _attention_fp4(lib, q, k_cache, v_cache, block_table, seq_lens, n_sink,
+                   window, tree_mask, scale, out, lse, workspace, split_pages,
+                   kernel_path, stream, k_scale, v_scale):
+    """Attention over a 4-bit cache.  Without a workspace of the caller's one
+    is allocated for this call alone, so calls on other streams and captured
+    graphs share nothing."""
+    B, ql, Hq, _ = q.shape
+    dev = q.device
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((B, ql, Hq), dtype=torch.float32, device=dev)
+    dims = _paged_dims(B, Hq, k_cache, block_table.shape[1], SVP_FP4_E2M1,
+                       k_scale, v_scale, workspace, split_pages, kernel_path)
+    ref = ctypes.byref(dims)
+    n_sink, window = int(n_sink), int(window)
+    if workspace is None:
+        need = lib.paged_decode_workspace_size(ref, ql, n_sink, window)
+        if need:  # 0: an invalid request, which the call reports
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            dims.workspace = workspace.data_ptr()
+            dims.workspace_bytes = need
+    handle = _stream_handle(stream, dev)
+    if tree_mask is None:
+        st = lib.paged_decode_attention(
+            ref, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), ql, n_sink, window,
+            float(scale), out.data_ptr(), lse.data_ptr(), handle)
+        _check("paged_decode_attention", st)
+    else:
+        st = lib.paged_tree_attention(
+            ref, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), ql,
+            tree_mask.data_ptr(), float(scale), out.data_ptr(), lse.data_ptr(),
+            handle)
+        _check("paged_tree_attention", st)
+    return out, lse
+
+
 def kv_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens,
               stream=None, k_scale=1.0, v_scale=1.0):
     """Scatter k_new/v_new [B, n_new, Hkv, D] into the paged caches in place
     (include/svp.h: kv_append).  seq_lens are the lengths after the append.
-    Into FP8 caches the bf16 rows are quantised with k_scale / v_scale."""
+    Into FP8 and 4-bit caches the bf16 rows are quantised with k_scale /
+    v_scale."""
     lib = load_library()
     for t, n in ((k_new, "k_new"), (v_new, "v_new"), (k_cache, "k_cache"),
                  (v_cache, "v_cache"), (block_table, "block_table"),
@@ -325,6 +485,21 @@ def kv_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens,
     _need(v_new.dtype == k_new.dtype and v_cache.dtype == k_cache.dtype,
           "k_new/v_new and k_cache/v_cache must pair up")
     B, n_new, Hkv, D = k_new.shape
+    if code == SVP_FP4_E2M1:
+        _check_pages(k_cache, block_table, seq_lens, B, v_cache)
+        shape = (B, n_new, k_cache.shape[1], _head_dim(k_cache))
+        _args(k_cache.device, (k_new, "k_new", torch.bfloat16, shape),
+              (v_new, "v_new", torch.bfloat16, shape))
+        dims = _paged_dims(B, Hkv, k_cache, block_table.shape[1], code, k_scale,
+                           v_scale)
+        with _on(k_cache.device, None):
+            st = lib.kv_append(
+                ctypes.byref(dims), k_new.data_ptr(), v_new.data_ptr(),
+                k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                seq_lens.data_ptr(), n_new,
+                _stream_handle(stream, k_cache.device))
+        _check("kv_append", st)
+        return
     dims = make_dims((B, n_new, Hkv, D), k_cache, block_table, code,
                      k_scale=k_scale, v_scale=v_scale)
     st = lib.kv_append(ctypes.byref(dims), k_new.data_ptr(), v_new.data_ptr(),
@@ -332,6 +507,124 @@ def kv_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens,
                        block_table.data_ptr(), seq_lens.data_ptr(), int(n_new),
                        _stream_handle(stream, k_cache.device))
     _check("kv_append", st)
+
+
+def _any_cache_code(cache):
+    if _is_fp4(cache):
+        return SVP_FP4_E2M1
+    return SVP_FP8_E4M3 if cache.dtype in _FP8_TYPES else _dtype_code(cache)
+
+
+def kv_gather(k_cache, v_cache, block_table, seq_lens, n_rows, starts=None,
+              k_out=None, v_out=None, stream=None, k_scale=1.0, v_scale=1.0):
+    """The inverse of kv_append (include/svp.h: kv_gather): k and v
+    [B, n_rows, Hkv, D] (fp32 of an fp32 cache, else bf16), the values at
+    logical positions starts[b] .. starts[b] + n_rows - 1 (int32 [B]; without
+    it the newest n_rows); zeros outside the sequence."""
+    lib = load_library()
+    code = _any_cache_code(k_cache)
+    _need(seq_lens.dim() == 1, "seq_lens must be int32 [B]")
+    B, dev, n_rows = seq_lens.shape[0], k_cache.device, int(n_rows)
+    _check_pages(k_cache, block_table, seq_lens, B, v_cache)
+    _need(n_rows >= 0, "n_rows must not be negative")
+    shape = (B, n_rows, k_cache.shape[1], _head_dim(k_cache))
+    dtype = torch.float32 if code == SVP_F32 else torch.bfloat16
+    for t, name, dt, sh in ((starts, "starts", torch.int32, (B,)),
+                            (k_out, "k_out", dtype, shape),
+                            (v_out, "v_out", dtype, shape)):
+        if t is not None:
+            _args(dev, (t, name, dt, sh))
+    dims = _paged_dims(B, shape[2], k_cache, block_table.shape[1], code, k_scale,
+                       v_scale)
+    with _on(dev, stream):
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=dtype, device=dev)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=dtype, device=dev)
+        st = lib.kv_gather(
+            ctypes.byref(dims), k_cache.data_ptr(), v_cache.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(),
+            None if starts is None else starts.data_ptr(), n_rows,
+            k_out.data_ptr(), v_out.data_ptr(), _stream_handle(stream, dev))
+    _check("kv_gather", st)
+    return k_out, v_out
+
+
+def paged_score_update(q, k_cache, lse, block_table, seq_lens, scores,
+                       n_fresh=None, n_sink=0, window=0, tree_mask=None,
+                       scale=None, k_scale=1.0, stream=None):
+    """Adds to scores [num_blocks, Hkv, 16] fp32, in place, the attention
+    weight that every cached key received from the query rows q
+    [B, q_len, Hq, D], lse [B, q_len, Hq] being what the attention call with
+    the same arguments returned (include/svp.h: paged_score_update).  The
+    newest n_fresh positions (default: q_len) start from zero.  Returns
+    scores."""
+    lib = load_library()
+    _need(q.dim() == 4, "q must be [B, q_len, Hq, D]")
+    B, ql, Hq, D = q.shape
+    dev = k_cache.device
+    code = _cache_code(k_cache, q.dtype)
+    _check_pages(k_cache, block_table, seq_lens, B)
+    _need(_head_dim(k_cache) == D, "q and k_cache must share head_dim")
+    _args(dev, (q, "q", None, None), (lse, "lse", torch.float32, (B, ql, Hq)),
+          (scores, "scores", torch.float32, tuple(k_cache.shape[:3])))
+    if tree_mask is not None:
+        _args(dev, (tree_mask, "tree_mask", None, (B, ql)))
+        _need(tree_mask.element_size() == 4 and not tree_mask.is_floating_point(),
+              "tree_mask must be int32/uint32 [B, q_len]")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    dims = _paged_dims(B, Hq, k_cache, block_table.shape[1], code, k_scale)
+    with _on(dev, None):
+        st = lib.paged_score_update(
+            ctypes.byref(dims), q.data_ptr(), k_cache.data_ptr(),
+            lse.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), ql,
+            int(n_sink), int(window),
+            None if tree_mask is None else tree_mask.data_ptr(), float(scale),
+            ql if n_fresh is None else int(n_fresh), scores.data_ptr(),
+            _stream_handle(stream, dev))
+    _check("paged_score_update", st)
+    return scores
+
+
+def kv_evict(k_cache, v_cache, scores, block_table, seq_lens, budget, n_sink=0,
+             n_recent=0, dst_block_table=None, kept=None, new_lens=None,
+             stream=None):
+    """Every (sequence, kv head) longer than `budget` keeps its first n_sink
+    rows, its newest n_recent and the best-scored others, in order, as the
+    first rows of dst_block_table's pages (default: in place); scores move
+    along (include/svp.h: kv_evict).  Returns (kept [B, Hkv, budget] int32
+    positions, -1 padded, new_lens [B] int32)."""
+    lib = load_library()
+    code = _any_cache_code(k_cache)
+    _need(seq_lens.dim() == 1, "seq_lens must be int32 [B]")
+    B, dev, budget = seq_lens.shape[0], k_cache.device, int(budget)
+    _check_pages(k_cache, block_table, seq_lens, B, v_cache)
+    _need(budget >= 1, "budget must be at least 1")
+    shape = (B, k_cache.shape[1], budget)
+    _args(dev, (scores, "scores", torch.float32, tuple(k_cache.shape[:3])))
+    if dst_block_table is not None:
+        _need(dst_block_table.dim() == 2, "dst_block_table must be int32 [B, n]")
+        _args(dev, (dst_block_table, "dst_block_table", torch.int32,
+                    (B, dst_block_table.shape[1])))
+    for t, name, sh in ((kept, "kept", shape), (new_lens, "new_lens", (B,))):
+        if t is not None:
+            _args(dev, (t, name, torch.int32, sh))
+    dims = _paged_dims(B, shape[1], k_cache, block_table.shape[1], code)
+    with _on(dev, stream):
+        if kept is None:
+            kept = torch.empty(shape, dtype=torch.int32, device=dev)
+        if new_lens is None:
+            new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+        st = lib.kv_evict(
+            ctypes.byref(dims), k_cache.data_ptr(), v_cache.data_ptr(),
+            scores.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+            budget, int(n_sink), int(n_recent),
+            None if dst_block_table is None else dst_block_table.data_ptr(),
+            0 if dst_block_table is None else dst_block_table.shape[1],
+            kept.data_ptr(), new_lens.data_ptr(), _stream_handle(stream, dev))
+    _check("kv_evict", st)
+    return kept, new_lens
 
 
 def spec_accept(target_logits, draft_logits, draft_tokens, uniforms,
@@ -453,9 +746,9 @@ class StepRunner:
         lib = load_library()
         _cuda_contig(k_cache, "k_cache")
         _cuda_contig(v_cache, "v_cache")
-        nb, Hkv, bs, D = k_cache.shape
-        code = (SVP_FP8_E4M3 if k_cache.dtype in _FP8_TYPES
-                else _dtype_code(k_cache))
+        nb, Hkv, bs, _ = k_cache.shape
+        D = _head_dim(k_cache)
+        code = _any_cache_code(k_cache)
         dims = SvpDims(batch, num_q_heads, Hkv, D, bs, max_blocks_per_seq, nb,
                        code, None, 0, split_pages, kernel_path, k_scale,
                        v_scale)

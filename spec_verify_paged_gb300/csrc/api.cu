@@ -76,9 +76,10 @@ static int check_dims(const svp_dims *d) {
       d->kernel_path > SVP_PATH_TCGEN05)
     return SVP_ERR_INVALID_ARG;
   if (d->num_q_heads % d->num_kv_heads != 0) return SVP_ERR_INVALID_ARG;
-  if (d->dtype != SVP_F32 && d->dtype != SVP_BF16 && d->dtype != SVP_FP8_E4M3)
+  if (d->dtype != SVP_F32 && d->dtype != SVP_BF16 &&
+      d->dtype != SVP_FP8_E4M3 && d->dtype != SVP_FP4_E2M1)
     return SVP_ERR_INVALID_ARG;
-  if (d->dtype == SVP_FP8_E4M3 &&
+  if ((d->dtype == SVP_FP8_E4M3 || d->dtype == SVP_FP4_E2M1) &&
       !(std::isfinite(d->k_scale) && d->k_scale > 0.f &&
         std::isfinite(d->v_scale) && d->v_scale > 0.f))
     return SVP_ERR_INVALID_ARG;
@@ -108,6 +109,11 @@ static int select_path(int dtype, int head_dim, int rows, int kernel_path,
   // the tensor paths address the cache as a 2-D tensor with int32 rows
   const bool tma_ok = tensor_maps_available() &&
                       num_blocks * num_kv_heads * kBlockSize < (1LL << 31);
+  if (dtype == SVP_FP4_E2M1) {  // one kernel, on mma.sync
+    if (kernel_path != SVP_PATH_AUTO && kernel_path != SVP_PATH_TENSOR_CORES)
+      return SVP_ERR_UNSUPPORTED;
+    return SVP_PATH_TENSOR_CORES;
+  }
   switch (kernel_path) {
     case SVP_PATH_CUDA_CORES:
       return SVP_PATH_CUDA_CORES;
@@ -134,16 +140,19 @@ int plan_attention(int batch, int num_q_heads, int num_kv_heads, int head_dim,
   int path = select_path(dtype, head_dim, rows, kernel_path, num_blocks,
                          num_kv_heads);
   if (path < 0) return path;
-  const bool mma = path == SVP_PATH_TENSOR_CORES;
+  const bool fp4 = dtype == SVP_FP4_E2M1;
+  const bool mma = path == SVP_PATH_TENSOR_CORES && !fp4;
   const bool tc = path == SVP_PATH_TCGEN05;
   // mma.sync: one m16 tile per warp, two warps share a page beyond 16 rows;
   // tcgen05: the rows are the MMA's N (16 or 32), or two 32-row groups
   // sharing each K/V tile beyond 32 rows
-  int rb = tc    ? (rows <= 16 ? 16 : rows <= 32 ? 32 : 64)
+  int rb = fp4   ? attention_fp4_rows(rows)
+           : tc  ? (rows <= 16 ? 16 : rows <= 32 ? 32 : 64)
            : mma ? (rows <= 16 ? 16 : 32)
                  : rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : 8;
   const int n_rg = (rows + rb - 1) / rb;
-  const int ctas = tc ? attention_tc_ctas_per_sm(rb, batch)
+  const int ctas = fp4  ? attention_fp4_ctas_per_sm(head_dim, rb, batch)
+                   : tc ? attention_tc_ctas_per_sm(rb, batch)
                       : attention_ctas_per_sm(dtype, head_dim, rb, mma, batch);
   const long long groups = (long long)batch * num_kv_heads * n_rg;
   // Every CTA of the persistent grid takes an equal slice of all pages;
@@ -158,9 +167,10 @@ int plan_attention(int batch, int num_q_heads, int num_kv_heads, int head_dim,
   plan->n_rg = n_rg;
   plan->mma = mma;
   plan->tc = tc;
+  plan->fp4 = fp4;
   plan->batch_cap = tc ? tc_batch_cap() : kBatchPerLaunch;
   plan->min_pages = min_pages;
-  plan->seg_items = tc ? kSegItemsTc : kSegItemsCc;
+  plan->seg_items = fp4 ? kSegItemsFp4 : tc ? kSegItemsTc : kSegItemsCc;
   plan->grid = (int)grid;
   plan->ctas_per_sm = ctas;
   plan->ws_head = 256;
@@ -199,7 +209,9 @@ static int plan_call(const svp_dims *d, int q_len, int n_sink, int window,
   if (path < 0) return path;
   const int cap = path == SVP_PATH_TCGEN05 ? tc_batch_cap() : kBatchPerLaunch;
   const int bl = batch_per_launch(d, q_len, n_sink, window, cap,
-                                  path == SVP_PATH_TCGEN05 ? kSegItemsTc : kSegItemsCc);
+                                  d->dtype == SVP_FP4_E2M1   ? kSegItemsFp4
+                                  : path == SVP_PATH_TCGEN05 ? kSegItemsTc
+                                                             : kSegItemsCc);
   const int st = plan_attention(bl, d->num_q_heads, d->num_kv_heads,
                                 d->head_dim, d->dtype, d->max_blocks_per_seq,
                                 q_len, n_sink, window, d->split_pages, path,
@@ -289,7 +301,7 @@ static int attention_call(const svp_dims *dims, const void *q,
   char *wp = static_cast<char *>(ws);
   const size_t eb = dims->dtype == SVP_F32 ? 4 : 2;  // q / out (bf16 for FP8)
   const size_t row_elems = (size_t)dims->num_q_heads * dims->head_dim;
-  const bool fp8 = dims->dtype == SVP_FP8_E4M3;
+  const bool scaled = dims->dtype == SVP_FP8_E4M3 || plan.fp4;
   int launches = 0;
   for (int b0 = 0; b0 < dims->batch; b0 += bl) {
     const int nb = dims->batch - b0 < bl ? dims->batch - b0 : bl;
@@ -318,15 +330,15 @@ static int attention_call(const svp_dims *dims, const void *q,
     p.rows = p.group * q_len;
     p.rb = plan.rb;
     p.n_rg = plan.n_rg;
-    // tcgen05: items are 8-page tiles (a slice's minimum in tiles)
-    p.ppi = plan.tc ? kTilePagesTc : 1;
-    p.min_pages = plan.tc ? std::max(1, plan.min_pages / kTilePagesTc)
-                          : plan.min_pages;
+    // tcgen05: items are 8-page tiles, 4-bit caches: 2-page stages (a
+    // slice's minimum in items)
+    p.ppi = plan.fp4 ? kTilePagesFp4 : plan.tc ? kTilePagesTc : 1;
+    p.min_pages = std::max(1, plan.min_pages / p.ppi);
     p.seg_items = plan.seg_items;
-    // an FP8 cache's K scale folds into the query scale, its V scale
+    // an FP8 or FP4 cache's K scale folds into the query scale, its V scale
     // multiplies the outputs
-    p.qscale = scale * 1.4426950408889634f * (fp8 ? dims->k_scale : 1.0f);
-    p.v_scale = fp8 ? dims->v_scale : 1.0f;
+    p.qscale = scale * 1.4426950408889634f * (scaled ? dims->k_scale : 1.0f);
+    p.v_scale = scaled ? dims->v_scale : 1.0f;
     p.tree_mask = tree_mask ? tree_mask + (size_t)b0 * q_len : nullptr;
     // only the first launch follows the append: a later one follows the
     // previous launch's merge, which reads the workspace it would reset
@@ -336,13 +348,14 @@ static int attention_call(const svp_dims *dims, const void *q,
       plan_attention(nb, dims->num_q_heads, dims->num_kv_heads,
                      dims->head_dim, dims->dtype, dims->max_blocks_per_seq,
                      q_len, n_sink, window, plan.min_pages,
-                     plan.tc    ? SVP_PATH_TCGEN05
-                     : plan.mma ? SVP_PATH_TENSOR_CORES
-                                : SVP_PATH_CUDA_CORES,
+                     plan.tc                 ? SVP_PATH_TCGEN05
+                     : plan.mma || plan.fp4  ? SVP_PATH_TENSOR_CORES
+                                             : SVP_PATH_CUDA_CORES,
                      sms, dims->num_blocks, &sub);
     }
     cudaError_t e =
-        plan.tc ? launch_attention_tc(p, sub.grid, stream)
+        plan.fp4  ? launch_attention_fp4(p, sub.grid, stream)
+        : plan.tc ? launch_attention_tc(p, sub.grid, stream)
                 : launch_attention(p, dims->dtype, plan.mma, sub.grid, stream);
     if (e != cudaSuccess) return SVP_ERR_CUDA;
     // groups split over several CTAs are finished by the merge kernel
@@ -422,10 +435,169 @@ int kv_append(const svp_dims *dims, const void *k_new, const void *v_new,
   p.num_blocks = dims->num_blocks;
   p.elem_bytes = dims->dtype == SVP_F32 ? 4 : 2;
   p.fp8 = dims->dtype == SVP_FP8_E4M3;
-  p.k_scale = p.fp8 ? dims->k_scale : 1.0f;
-  p.v_scale = p.fp8 ? dims->v_scale : 1.0f;
+  p.fp4 = dims->dtype == SVP_FP4_E2M1;
+  p.k_scale = p.fp8 || p.fp4 ? dims->k_scale : 1.0f;
+  p.v_scale = p.fp8 || p.fp4 ? dims->v_scale : 1.0f;
   if (launch_kv_append(p, stream) != cudaSuccess) return SVP_ERR_CUDA;
   t_last_launches = 1;
+  return SVP_OK;
+}
+
+int kv_gather(const svp_dims *dims, const void *k_cache, const void *v_cache,
+              const int32_t *block_table, const int32_t *seq_lens,
+              const int32_t *starts, int n_rows, void *k_out, void *v_out,
+              cudaStream_t stream) {
+  t_last_launches = 0;
+  const int st = check_dims(dims);
+  if (st != SVP_OK) return st;
+  if (n_rows < 0) return SVP_ERR_INVALID_ARG;
+  if (dims->batch == 0 || n_rows == 0) return SVP_OK;
+  if (!k_cache || !v_cache || !block_table || !seq_lens || !k_out || !v_out)
+    return SVP_ERR_INVALID_ARG;
+  if (dims->num_blocks == 0 || dims->max_blocks_per_seq == 0)
+    return SVP_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(k_cache) |
+       reinterpret_cast<uintptr_t>(v_cache) |
+       reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) %
+          16 != 0)
+    return SVP_ERR_INVALID_ARG;
+  // the largest grid, in blocks of 256 lanes of 16 output bytes
+  const long long rows = (long long)dims->batch * n_rows;
+  if (rows > (1LL << 38) / ((long long)dims->num_kv_heads * dims->head_dim))
+    return SVP_ERR_UNSUPPORTED;
+  GatherParams p;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.starts = starts;
+  p.k_out = k_out;
+  p.v_out = v_out;
+  p.batch = dims->batch;
+  p.num_kv_heads = dims->num_kv_heads;
+  p.head_dim = dims->head_dim;
+  p.n_rows = n_rows;
+  p.max_blocks = dims->max_blocks_per_seq;
+  p.num_blocks = dims->num_blocks;
+  p.dtype = dims->dtype;
+  const bool scaled =
+      dims->dtype == SVP_FP8_E4M3 || dims->dtype == SVP_FP4_E2M1;
+  p.k_scale = scaled ? dims->k_scale : 1.0f;
+  p.v_scale = scaled ? dims->v_scale : 1.0f;
+  if (launch_kv_gather(p, stream) != cudaSuccess) return SVP_ERR_CUDA;
+  t_last_launches = 1;
+  return SVP_OK;
+}
+
+int paged_score_update(const svp_dims *dims, const void *q,
+                       const void *k_cache, const float *lse,
+                       const int32_t *block_table, const int32_t *seq_lens,
+                       int q_len, int n_sink, int window,
+                       const uint32_t *tree_mask, float scale, int n_fresh,
+                       float *scores, cudaStream_t stream) {
+  t_last_launches = 0;
+  if (tree_mask && (n_sink != 0 || window != 0)) return SVP_ERR_INVALID_ARG;
+  const int st = check_attention_args(dims, q_len, n_sink, window, scale);
+  if (st != SVP_OK) return st;
+  if (n_fresh < 0 || n_fresh > q_len) return SVP_ERR_INVALID_ARG;
+  if (dims->batch == 0) return SVP_OK;
+  if (!q || !k_cache || !lse || !block_table || !seq_lens || !scores)
+    return SVP_ERR_INVALID_ARG;
+  if (dims->num_blocks == 0 || dims->max_blocks_per_seq == 0)
+    return SVP_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_cache)) %
+              16 != 0 ||
+      (reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(scores) |
+       reinterpret_cast<uintptr_t>(tree_mask)) % 4 != 0)
+    return SVP_ERR_INVALID_ARG;
+  const int sms = device_sms();
+  if (sms <= 0) return SVP_ERR_CUDA;
+  const bool scaled =
+      dims->dtype == SVP_FP8_E4M3 || dims->dtype == SVP_FP4_E2M1;
+  ScoreParams p;
+  p.q = q;
+  p.k_cache = k_cache;
+  p.lse = lse;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.tree_mask = tree_mask;
+  p.scores = scores;
+  p.batch = dims->batch;
+  p.num_q_heads = dims->num_q_heads;
+  p.num_kv_heads = dims->num_kv_heads;
+  p.head_dim = dims->head_dim;
+  p.group = dims->num_q_heads / dims->num_kv_heads;
+  p.q_len = q_len;
+  p.n_sink = n_sink;
+  p.window = window;
+  p.max_blocks = dims->max_blocks_per_seq;
+  p.num_blocks = dims->num_blocks;
+  p.max_pages =
+      max_visible_pages(dims->max_blocks_per_seq, q_len, n_sink, window);
+  p.dtype = dims->dtype;
+  p.qscale = scale * 1.4426950408889634f * (scaled ? dims->k_scale : 1.0f);
+  const long long rows = (long long)p.group * q_len;
+  int launches = 0;
+  for (long long r0 = 0; r0 < rows; r0 += kScoreRows, ++launches) {
+    p.row0 = (int)r0;
+    p.rows = (int)std::min<long long>(kScoreRows, rows - r0);
+    p.n_fresh = r0 == 0 ? n_fresh : 0;  // later rows add to the first ones'
+    if (launch_score_update(p, sms, stream) != cudaSuccess) return SVP_ERR_CUDA;
+  }
+  t_last_launches = launches;
+  return SVP_OK;
+}
+
+int kv_evict(const svp_dims *dims, void *k_cache, void *v_cache, float *scores,
+             const int32_t *block_table, const int32_t *seq_lens, int budget,
+             int n_sink, int n_recent, const int32_t *dst_block_table,
+             int dst_max_blocks, int32_t *kept, int32_t *new_lens,
+             cudaStream_t stream) {
+  t_last_launches = 0;
+  const int st = check_dims(dims);
+  if (st != SVP_OK) return st;
+  if (budget < 1 || n_sink < 0 || n_recent < 0 ||
+      (long long)n_sink + n_recent > budget)
+    return SVP_ERR_INVALID_ARG;
+  if (dims->max_blocks_per_seq > (1 << 26)) return SVP_ERR_UNSUPPORTED;
+  if (dims->batch == 0) return SVP_OK;
+  if (!k_cache || !v_cache || !scores || !block_table || !seq_lens || !kept ||
+      !new_lens)
+    return SVP_ERR_INVALID_ARG;
+  if (dims->num_blocks == 0 || dims->max_blocks_per_seq == 0)
+    return SVP_ERR_INVALID_ARG;
+  const int dst_blocks =
+      dst_block_table ? dst_max_blocks : dims->max_blocks_per_seq;
+  if (budget > (long long)dst_blocks * kBlockSize) return SVP_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(k_cache) |
+       reinterpret_cast<uintptr_t>(v_cache)) % 16 != 0 ||
+      reinterpret_cast<uintptr_t>(scores) % 4 != 0)
+    return SVP_ERR_INVALID_ARG;
+  const int sms = device_sms();
+  if (sms <= 0) return SVP_ERR_CUDA;
+  EvictParams p;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.scores = scores;
+  p.block_table = block_table;
+  p.dst_table = dst_block_table ? dst_block_table : block_table;
+  p.seq_lens = seq_lens;
+  p.kept = kept;
+  p.new_lens = new_lens;
+  p.batch = dims->batch;
+  p.num_kv_heads = dims->num_kv_heads;
+  p.row_bytes = dims->dtype == SVP_F32        ? 4 * dims->head_dim
+                : dims->dtype == SVP_BF16     ? 2 * dims->head_dim
+                : dims->dtype == SVP_FP8_E4M3 ? dims->head_dim
+                                              : 9 * dims->head_dim / 16;
+  p.max_blocks = dims->max_blocks_per_seq;
+  p.dst_blocks = dst_blocks;
+  p.num_blocks = dims->num_blocks;
+  p.budget = budget;
+  p.n_sink = n_sink;
+  p.n_recent = n_recent;
+  if (launch_kv_evict(p, sms, stream) != cudaSuccess) return SVP_ERR_CUDA;
+  t_last_launches = 2;
   return SVP_OK;
 }
 
@@ -514,7 +686,10 @@ int svp_read_device_status(cudaStream_t stream, int *flags) {
   unsigned f = 0;
   if (read_status_attention(stream, &f) != cudaSuccess) return SVP_ERR_CUDA;
   if (read_status_attention_tc(stream, &f) != cudaSuccess) return SVP_ERR_CUDA;
+  if (read_status_attention_fp4(stream, &f) != cudaSuccess) return SVP_ERR_CUDA;
   if (read_status_append(stream, &f) != cudaSuccess) return SVP_ERR_CUDA;
+  if (read_status_score(stream, &f) != cudaSuccess) return SVP_ERR_CUDA;
+  if (read_status_evict(stream, &f) != cudaSuccess) return SVP_ERR_CUDA;
   if (read_status_accept(stream, &f) != cudaSuccess) return SVP_ERR_CUDA;
   if (flags) *flags = (int)f;
   return SVP_OK;

@@ -100,9 +100,13 @@ __device__ __forceinline__ bool key_visible(int j, int t, uint32_t tm, int base,
 }
 
 // Ancestor bits of query position i of sequence b (all ones without a tree).
+__device__ __forceinline__ uint32_t row_tree_bits(const uint32_t *tree_mask,
+                                                  int q_len, int b, int i) {
+  return tree_mask ? __ldg(tree_mask + (size_t)b * q_len + i) : ~0u;
+}
 __device__ __forceinline__ uint32_t row_tree_bits(const AttnParams &p, int b,
                                                   int i) {
-  return p.tree_mask ? __ldg(p.tree_mask + (size_t)b * p.q_len + i) : ~0u;
+  return row_tree_bits(p.tree_mask, p.q_len, b, i);
 }
 
 // Logical block of the pidx-th visible page.

@@ -1,4 +1,5 @@
-// kv_append.cu -- scatter the new tokens' K/V rows into the paged cache.
+// kv_append.cu -- scatter the new tokens' K/V rows into the paged cache, and
+// the inverse (kv_gather).
 //
 // Page: "KV cache & Flash Attention", sections "KV cache" (store K and V of
 // every token once) and "PagedAttention" (logical position -> physical
@@ -6,11 +7,17 @@
 // position pos = seq_lens[b] - n_new + k, i.e. page block_table[b][pos/16],
 // row pos % 16, kv head g.  A byte copy: one warp moves one K row and one V
 // row with 16-byte vector accesses.  Into an FP8 E4M3 cache each bf16 value
-// x becomes the code of x / scale (round to nearest even, saturating).
+// x becomes the code of x / scale (round to nearest even, saturating).  Into
+// a 4-bit cache a lane takes one block of 16 values: the block's scale is
+// the E4M3 value of max|y| / 6 (y = x / k_scale), so the largest value maps
+// to the largest code, and the codes are E2M1 of y / scale.
+#include <cuda_bf16.h>
+#include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
 #include <cstdint>
 
+#include "fp4.cuh"
 #include "ptx.cuh"
 #include "svp.h"
 #include "svp_internal.h"
@@ -95,9 +102,170 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
   }
 }
 
+// Logical position `pos` of sequence b: its page, or -1 with the flag
+// raised for a page id outside the cache.
+__device__ __forceinline__ int page_of(const int32_t *table, int max_blocks,
+                                       int num_blocks, int b, int pos) {
+  const int phys = table[(size_t)b * max_blocks + pos / kBlockSize];
+  if (phys >= 0 && phys < num_blocks) return phys;
+  atomicOr(&g_status_append, (unsigned)SVP_DEV_BAD_BLOCK_ID);
+  return -1;
+}
+
+// Rows into a 4-bit cache: one lane per block of 16 elements, the K and V
+// blocks of a row on neighbouring lanes.  Bound by the new rows' bytes (32
+// in, 9 out per block) or, for a decode step's few rows, by one round trip
+// through the block table.
+__global__ void __launch_bounds__(32 * kAppendWarps)
+    kv_append_fp4_kernel(const AppendParams p) {
+  pdl_launch_dependents();
+  const int nb = p.head_dim / kFp4Group;  // blocks of a row
+  const long long idx =
+      (long long)blockIdx.x * (32 * kAppendWarps) + threadIdx.x;
+  const long long n_rows = (long long)p.batch * p.n_new * p.num_kv_heads;
+  const long long row = idx / (2 * nb);
+  if (row >= n_rows) return;
+  const int r = (int)(idx % (2 * nb));
+  const bool is_v = r >= nb;
+  const int blk = is_v ? r - nb : r;
+  const int g = (int)(row % p.num_kv_heads);
+  const int k = (int)((row / p.num_kv_heads) % p.n_new);
+  const int b = (int)(row / ((long long)p.num_kv_heads * p.n_new));
+  // the new values do not depend on the table: load them first
+  const uint4 *src = reinterpret_cast<const uint4 *>(
+      static_cast<const uint16_t *>(is_v ? p.v_new : p.k_new) +
+      (size_t)row * p.head_dim + blk * kFp4Group);
+  const uint4 in[2] = {src[0], src[1]};
+  const int L = p.seq_lens[b];
+  if (L < p.n_new || L > (long long)p.max_blocks * kBlockSize) {
+    if (r == 0) atomicOr(&g_status_append, (unsigned)SVP_DEV_BAD_SEQ_LEN);
+    return;
+  }
+  const int pos = L - p.n_new + k;
+  const int phys = page_of(p.block_table, p.max_blocks, p.num_blocks, b, pos);
+  if (phys < 0) return;
+  const float inv_of = is_v ? p.v_scale : p.k_scale;
+  float y[kFp4Group];
+  const uint32_t w[8] = {in[0].x, in[0].y, in[0].z, in[0].w,
+                         in[1].x, in[1].y, in[1].z, in[1].w};
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    y[2 * i] = __uint_as_float(w[i] << 16) / inv_of;
+    y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) / inv_of;
+    top = fmaxf(top, fmaxf(fabsf(y[2 * i]), fabsf(y[2 * i + 1])));
+  }
+  __nv_fp8_storage_t sc =
+      __nv_cvt_float_to_fp8(top / 6.f, __NV_SATFINITE, __NV_E4M3);
+  if (sc == 0) sc = 1;  // the smallest scale, 2^-9: finer than no scale
+  const float s =
+      __half2float(__half(__nv_cvt_fp8_to_halfraw(sc, __NV_E4M3)));
+  uint32_t code[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __nv_fp4x2_storage_t c = __nv_cvt_float2_to_fp4x2(
+        make_float2(y[2 * i] / s, y[2 * i + 1] / s), __NV_E2M1,
+        cudaRoundNearest);
+    code[i >> 2] |= (uint32_t)c << (8 * (i & 3));
+  }
+  unsigned char *dst =
+      static_cast<unsigned char *>(is_v ? p.v_cache : p.k_cache) +
+      (((size_t)phys * p.num_kv_heads + g) * kBlockSize + pos % kBlockSize) *
+          (size_t)fp4_row_bytes(p.head_dim);
+  uint32_t *d32 = reinterpret_cast<uint32_t *>(dst + 8 * blk);
+  d32[0] = code[0];  // rows are 4-byte aligned (36 or 72 bytes)
+  d32[1] = code[1];
+  dst[p.head_dim / 2 + blk] = sc;
+}
+
+// Rows back as values: one lane per 16 output bytes (8 bf16 or 4 fp32
+// elements) of a K or V row.  Bound by the output bytes.
+__global__ void __launch_bounds__(32 * kAppendWarps)
+    kv_gather_kernel(const GatherParams p) {
+  pdl_launch_dependents();
+  const int per = p.dtype == SVP_F32 ? 4 : 8;  // elements of a lane
+  const int nc = p.head_dim / per;             // lanes of a row
+  const long long idx =
+      (long long)blockIdx.x * (32 * kAppendWarps) + threadIdx.x;
+  const long long n_rows = (long long)p.batch * p.n_rows * p.num_kv_heads;
+  const long long row = idx / (2 * nc);
+  if (row >= n_rows) return;
+  const int r = (int)(idx % (2 * nc));
+  const bool is_v = r >= nc;
+  const int c = is_v ? r - nc : r;
+  const int g = (int)(row % p.num_kv_heads);
+  const long long i = (row / p.num_kv_heads) % p.n_rows;
+  const int b = (int)(row / ((long long)p.num_kv_heads * p.n_rows));
+  const int L = p.seq_lens[b];
+  int phys = -1;
+  long long pos = 0;
+  if (L < 0 || L > (long long)p.max_blocks * kBlockSize) {
+    if (r == 0) atomicOr(&g_status_append, (unsigned)SVP_DEV_BAD_SEQ_LEN);
+  } else {
+    pos = (p.starts ? (long long)p.starts[b] : (long long)L - p.n_rows) + i;
+    if (pos >= 0 && pos < L)
+      phys = page_of(p.block_table, p.max_blocks, p.num_blocks, b, (int)pos);
+  }
+  uint4 out = make_uint4(0, 0, 0, 0);
+  if (phys >= 0) {
+    const size_t at = ((size_t)phys * p.num_kv_heads + g) * kBlockSize +
+                      (size_t)(pos % kBlockSize);
+    const unsigned char *cache =
+        static_cast<const unsigned char *>(is_v ? p.v_cache : p.k_cache);
+    const float scale = is_v ? p.v_scale : p.k_scale;
+    uint32_t h[4];  // fp16 pairs of the 8 values before the scale factor
+    if (p.dtype == SVP_F32 || p.dtype == SVP_BF16) {
+      out = *reinterpret_cast<const uint4 *>(
+          cache + at * p.head_dim * (p.dtype == SVP_F32 ? 4 : 2) + 16 * c);
+    } else {
+      if (p.dtype == SVP_FP8_E4M3) {
+        const uint2 w =
+            *reinterpret_cast<const uint2 *>(cache + at * p.head_dim + 8 * c);
+        h[0] = e4m3x2_f16x2(w.x);
+        h[1] = e4m3x2_f16x2(w.x >> 16);
+        h[2] = e4m3x2_f16x2(w.y);
+        h[3] = e4m3x2_f16x2(w.y >> 16);
+      } else {
+        const unsigned char *src = cache + at * fp4_row_bytes(p.head_dim);
+        const uint32_t s =
+            e4m3x2_f16x2((uint32_t)src[p.head_dim / 2 + c / 2] * 0x101u);
+        e2m1x8_h2(*reinterpret_cast<const uint32_t *>(src + 4 * c), h);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = hmul2(h[j], s);
+      }
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f =
+            __half22float2(*reinterpret_cast<const __half2 *>(&h[j]));
+        const __nv_bfloat162 v =
+            __floats2bfloat162_rn(f.x * scale, f.y * scale);
+        o[j] = *reinterpret_cast<const uint32_t *>(&v);
+      }
+      out = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+  reinterpret_cast<uint4 *>(is_v ? p.v_out : p.k_out)[(size_t)row * nc + c] = out;
+}
+
+cudaError_t launch_kv_gather(const GatherParams &p, cudaStream_t stream) {
+  const long long lanes = (long long)p.batch * p.n_rows * p.num_kv_heads *
+                          (2 * p.head_dim / (p.dtype == SVP_F32 ? 4 : 8));
+  if (lanes == 0) return cudaSuccess;
+  constexpr int T = 32 * kAppendWarps;
+  kv_gather_kernel<<<(unsigned)((lanes + T - 1) / T), T, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_kv_append(const AppendParams &p, cudaStream_t stream) {
   const long long n_rows = (long long)p.batch * p.n_new * p.num_kv_heads;
   if (n_rows == 0) return cudaSuccess;
+  if (p.fp4) {
+    const long long lanes = n_rows * (2 * p.head_dim / kFp4Group);
+    constexpr int T = 32 * kAppendWarps;
+    kv_append_fp4_kernel<<<(unsigned)((lanes + T - 1) / T), T, 0, stream>>>(p);
+    return cudaGetLastError();
+  }
   const long long grid = (n_rows + kAppendWarps - 1) / kAppendWarps;
   kv_append_kernel<<<(unsigned)grid, 32 * kAppendWarps, 0, stream>>>(p);
   return cudaGetLastError();

@@ -55,6 +55,7 @@ struct AttnPlan {
   int rb, n_rg, min_pages, seg_items, grid, ctas_per_sm;
   bool mma;            // warp-level mma.sync path
   bool tc;             // tcgen05 path (tensor-memory accumulators)
+  bool fp4;            // 4-bit cache kernel
   int batch_cap;       // sequences per launch
   size_t ws_head, ws_desc, ws_part_o, ws_part_lse, ws_total;
 };
@@ -86,6 +87,11 @@ constexpr int kSegItemsTc = 2;
 // counted as this many pages.
 constexpr int kSegItemsCc = 12;
 
+// The 4-bit kernel's items are the two pages of a stage; a segment's
+// epilogue counts as this many.
+constexpr int kTilePagesFp4 = 2;
+constexpr int kSegItemsFp4 = 8;
+
 // Query rows per kv head (GQA group x q_len) from which the automatic path
 // choice uses tensor cores (bf16 only): tcgen05 for head_dim 128, warp-level
 // mma.sync for head_dim 64.
@@ -113,6 +119,14 @@ int attention_tc_ctas_per_sm(int rb, int batch);
 cudaError_t launch_attention_tc(const AttnParams &p, int grid,
                                 cudaStream_t stream);
 
+// The 4-bit cache kernel (attention_fp4.cu): the unit's row count (8, 16,
+// 24, 32, 48 or 64) for this many query rows per kv head, its CTAs per SM
+// and its launch (at most 4096 sequences).
+int attention_fp4_rows(int rows);
+int attention_fp4_ctas_per_sm(int head_dim, int rb, int batch);
+cudaError_t launch_attention_fp4(const AttnParams &p, int grid,
+                                 cudaStream_t stream);
+
 struct AppendParams {
   const void *k_new;
   const void *v_new;
@@ -123,9 +137,60 @@ struct AppendParams {
   int batch, num_kv_heads, head_dim, n_new, max_blocks, num_blocks;
   int elem_bytes;
   int fp8;                   // bf16 rows quantised into E4M3 caches
+  int fp4;                   // bf16 rows quantised into 4-bit caches
   float k_scale, v_scale;
 };
 cudaError_t launch_kv_append(const AppendParams &p, cudaStream_t stream);
+
+struct GatherParams {
+  const void *k_cache;
+  const void *v_cache;
+  const int32_t *block_table;
+  const int32_t *seq_lens;
+  const int32_t *starts;     // or null: the newest n_rows positions
+  void *k_out;
+  void *v_out;
+  int batch, num_kv_heads, head_dim, n_rows, max_blocks, num_blocks;
+  int dtype;                 // svp_dtype of the caches
+  float k_scale, v_scale;
+};
+cudaError_t launch_kv_gather(const GatherParams &p, cudaStream_t stream);
+
+// One paged_score_update launch: query rows [row0, row0 + rows) of every kv
+// head's group * q_len.
+struct ScoreParams {
+  const void *q;
+  const void *k_cache;
+  const float *lse;
+  const int32_t *block_table;
+  const int32_t *seq_lens;
+  const uint32_t *tree_mask;  // [batch, q_len] ancestor bits, or null
+  float *scores;
+  int batch, num_q_heads, num_kv_heads, head_dim, group;
+  int q_len, n_sink, window, n_fresh;
+  int row0, rows;
+  int max_blocks, num_blocks;
+  int max_pages;              // bound of a sequence's visible pages
+  int dtype;
+  float qscale;               // scale * k_scale * log2(e)
+};
+constexpr int kScoreRows = 128;  // query rows of one launch
+cudaError_t launch_score_update(const ScoreParams &p, int sms,
+                                cudaStream_t stream);
+
+struct EvictParams {
+  void *k_cache;
+  void *v_cache;
+  float *scores;
+  const int32_t *block_table;
+  const int32_t *dst_table;   // the destination's block table
+  const int32_t *seq_lens;
+  int32_t *kept;
+  int32_t *new_lens;
+  int batch, num_kv_heads, row_bytes, max_blocks, dst_blocks, num_blocks;
+  int budget, n_sink, n_recent;
+};
+cudaError_t launch_kv_evict(const EvictParams &p, int sms, cudaStream_t stream);
 
 struct AcceptParams {
   const float *target_logits;
@@ -160,7 +225,10 @@ cudaError_t launch_spec_accept_tree(const AcceptTreeParams &p,
 // Device status words (one per translation unit): read-and-clear.
 cudaError_t read_status_attention(cudaStream_t s, unsigned *flags);
 cudaError_t read_status_attention_tc(cudaStream_t s, unsigned *flags);
+cudaError_t read_status_attention_fp4(cudaStream_t s, unsigned *flags);
 cudaError_t read_status_append(cudaStream_t s, unsigned *flags);
+cudaError_t read_status_score(cudaStream_t s, unsigned *flags);
+cudaError_t read_status_evict(cudaStream_t s, unsigned *flags);
 cudaError_t read_status_accept(cudaStream_t s, unsigned *flags);
 
 #ifdef __CUDACC__
