@@ -47,18 +47,31 @@ static __device__ unsigned int g_status_attn4;
 
 namespace {
 
-constexpr int kWarps4 = 4;                    // consumer warps
-constexpr int kThreads4 = 32 * (kWarps4 + 1);
 constexpr int kStagePages = 2;
-constexpr int kStages4 = 8;
 constexpr int kNoPage = 0x7fffff00;           // j0 of a page that is not there
 constexpr float kRefOffset = 6.f;             // P = 2^6 at the reference
 constexpr float kRefSlack = 14.f;             // largest log2 P before a move
 constexpr float kNoRef = -3e38f;              // below any finite score
 
-// NT n8 tiles of query rows per warp, MT warps sharing a stage.
+// The CTA's shape for NT n8 tiles of query rows per warp.  Up to two tiles:
+// four consumer warps and the producer warp, several CTAs per SM.  From
+// three on a consumer holds 32 accumulators per tile: one CTA per SM, two
+// warpgroups of consumers and one whose first warp produces; 384 threads
+// launched with 168 registers each are split 224 / 56 (2 x 128 x 224 + 128 x
+// 56 = 384 x 168).
+template <int NT>
+struct Shape4 {
+  static constexpr bool kWide = NT > 2;
+  static constexpr int W = kWide ? 8 : 4;  // consumer warps
+  static constexpr int THREADS = kWide ? 384 : 160;
+  static constexpr int CTAS = NT == 1 ? 3 : kWide ? 1 : 2;  // per SM
+  static constexpr int STAGES = kWide ? 16 : 8;
+};
+
+// MT warps share a stage.
 template <int D, int NT, int MT>
 struct Smem4 {
+  static constexpr int kWarps4 = Shape4<NT>::W, kStages4 = Shape4<NT>::STAGES;
   static constexpr int PAGE = 9 * D;  // bytes of one head's 16 rows
   static constexpr int RW = 8 * NT;
   static constexpr int RB = RW * MT;
@@ -73,6 +86,7 @@ struct Smem4 {
   float wf[kWarps4][RB];
   UnitInfo unit[kUnitRing];
   int j0[kStages4][kStagePages];
+  int checked[kStages4];  // the stage's keys need the visibility test
   uint64_t full[kStages4], empty[kStages4];
   uint64_t ufull[kUnitRing], uempty[kUnitRing];
   uint64_t epi;
@@ -87,83 +101,136 @@ __device__ __forceinline__ void raise4(unsigned f) {
   atomicOr(&g_status_attn4, f);
 }
 
-// n consecutive bytes (8 or 4) at a 4-byte aligned shared address
-template <int D>
-__device__ __forceinline__ uint2 lds_codes8(const unsigned char *p) {
-  if constexpr (D == 128) {
-    return *reinterpret_cast<const uint2 *>(p);  // rows of 72 bytes
-  } else {
-    const uint32_t *w = reinterpret_cast<const uint32_t *>(p);
-    return make_uint2(w[0], w[1]);               // rows of 36 bytes
-  }
+// Shared-memory reads by 32-bit address: volatile keeps them behind the
+// barrier waits (and nothing else in order), and the address arithmetic
+// stays 32-bit.
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
 }
 
-// One page's scores: S += K Q^T for the 16 keys at kp.  qb(c, kk, nt) gives
-// the Q fragment of code chunk c, k-step kk.
+// Dims of k-step ks, lane t: four from q_dim on.  A lane's steps cover D/4
+// consecutive dims: one or two scale blocks.
+template <int D>
+__device__ __forceinline__ constexpr int q_dim(int ks, int t) {
+  return (D / 4) * t + 4 * ks;
+}
+
+// One page's scores: S += K Q^T for 16 keys.  kp: the page's address plus
+// this lane's offset k_lane<D>(); qb(ks, nt) gives the Q fragment of a
+// k-step.  With one tile the even and the odd k-steps form two chains.
+template <int D>
+__device__ __forceinline__ uint32_t k_lane(int g, int t) {
+  return fp4_key(g, 0) * fp4_row_bytes(D) + (D / 8) * t;
+}
 template <int D, int NT, typename QB>
-__device__ __forceinline__ void page_scores(const unsigned char *kp, int g,
-                                            int t, float (&s)[NT][4], QB qb) {
-  constexpr int ROW = fp4_row_bytes(D);
-  const unsigned char *r0 = kp + fp4_key(g, 0) * ROW;
-  const unsigned char *r1 = kp + fp4_key(g, 1) * ROW;
+__device__ __forceinline__ void page_scores(uint32_t kp, int t,
+                                            float (&s)[NT][4], QB qb) {
+  constexpr int ROW = fp4_row_bytes(D), C = D / 64;  // scale blocks per lane
+  uint2 w[2][C];
+  uint32_t sc[2][C];  // fp16 pairs of the block scales
 #pragma unroll
-  for (int c = 0; c < D / 64; ++c) {
-    const uint2 w0 = lds_codes8<D>(r0 + 8 * (t + 4 * c));
-    const uint2 w1 = lds_codes8<D>(r1 + 8 * (t + 4 * c));
-    const uint32_t x0 = *reinterpret_cast<const uint32_t *>(r0 + D / 2 + 4 * c);
-    const uint32_t x1 = *reinterpret_cast<const uint32_t *>(r1 + D / 2 + 4 * c);
-    const uint32_t s0 = e4m3x2_f16x2(__byte_perm(x0, 0, t * 0x11));
-    const uint32_t s1 = e4m3x2_f16x2(__byte_perm(x1, 0, t * 0x11));
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t row = kp + 2 * h * ROW;  // keys fp4_key(g, h)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int c = 0; c < C; ++c)
+      w[h][c] = D == 128 ? lds64(row + 8 * c)
+                         : make_uint2(lds32(row), lds32(row + 4));
+    // the scales lie D/2 bytes from the row's start, C bytes per lane
+    const uint32_t at = row + D / 2 - (D / 8 - C) * t;
+    if constexpr (C == 2) {
+      const uint32_t both = e4m3x2_f16x2(lds_u16(at));
+      sc[h][0] = __byte_perm(both, 0, 0x1010);
+      sc[h][C - 1] = __byte_perm(both, 0, 0x3232);
+    } else {
+      sc[h][0] = e4m3x2_f16x2(lds_u8(at) * 0x101u);
+    }
+  }
+  float odd[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int hw = 0; hw < 2; ++hw) {
       uint32_t k0[4], k1[4];
-      e2m1x8_h2(h ? w0.y : w0.x, k0);
-      e2m1x8_h2(h ? w1.y : w1.x, k1);
+      e2m1x8_h2(hw ? w[0][c].y : w[0][c].x, k0);
+      e2m1x8_h2(hw ? w[1][c].y : w[1][c].x, k1);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint32_t a[4] = {hmul2(k0[2 * i], s0), hmul2(k1[2 * i], s1),
-                               hmul2(k0[2 * i + 1], s0), hmul2(k1[2 * i + 1], s1)};
+        const uint32_t a[4] = {hmul2(k0[2 * i], sc[0][c]),
+                               hmul2(k1[2 * i], sc[1][c]),
+                               hmul2(k0[2 * i + 1], sc[0][c]),
+                               hmul2(k1[2 * i + 1], sc[1][c])};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const uint2 b = qb(c, 2 * h + i, nt);
-          mma_f16(s[nt], a, b.x, b.y);
+          const uint2 b = qb(4 * c + 2 * hw + i, nt);
+          mma_f16(NT == 1 && i ? odd : s[nt], a, b.x, b.y);
         }
       }
     }
+  if constexpr (NT == 1) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[0][e] += odd[e];
   }
 }
 
-// One page's O^T += V^T P^T.  keep: bit s set iff key 4t + s holds valid
-// data (its scale counts as 0 otherwise).
+// One page's O^T += V^T P^T.  vp: the page's address plus this lane's offset
+// v_lane<D>(); sp: the same for its scale byte.  keep: bit s set iff key
+// 4t + s holds valid data (its scale counts as 0 otherwise).
+template <int D>
+__device__ __forceinline__ uint32_t v_lane(int g, int t) {
+  return 4 * t * fp4_row_bytes(D) + (D / 16) * g;
+}
+template <int D>
+__device__ __forceinline__ uint32_t v_lane_scale(int g, int t) {
+  return 4 * t * fp4_row_bytes(D) + D / 2 + (D / 8) * g / kFp4Group;
+}
 template <int D, int NT>
-__device__ __forceinline__ void page_values(const unsigned char *vp, int g,
-                                            int t, unsigned keep,
+__device__ __forceinline__ void page_values(uint32_t vp, uint32_t sp,
+                                            unsigned keep,
                                             const uint32_t (&pb)[NT][2],
                                             float (&o)[D / 16][NT][4]) {
-  constexpr int ROW = fp4_row_bytes(D);
-  constexpr int DPL = D / 8;  // dims of this lane: DPL g .. DPL g + DPL - 1
-  const unsigned char *r = vp + 4 * t * ROW;
-  uint32_t w[4][D / 64], sc[4];
+  constexpr int ROW = fp4_row_bytes(D), C = D / 64;
+  uint32_t w[4][C], sc[4];
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     if constexpr (D == 128) {
-      const uint2 x = *reinterpret_cast<const uint2 *>(r + s * ROW + 8 * g);
+      const uint2 x = lds64(vp + s * ROW);
       w[s][0] = x.x;
-      w[s][D / 64 - 1] = x.y;
+      w[s][C - 1] = x.y;
     } else {
-      w[s][0] = *reinterpret_cast<const uint32_t *>(r + s * ROW + 4 * g);
+      w[s][0] = lds32(vp + s * ROW);
     }
-    sc[s] = r[s * ROW + D / 2 + DPL * g / kFp4Group];
+    sc[s] = lds_u8(sp + s * ROW);
   }
   if (keep != 0xfu) {
 #pragma unroll
     for (int s = 0; s < 4; ++s)
       if (!((keep >> s) & 1u)) sc[s] = 0u;
   }
-  const uint32_t s01 = e4m3x2_f16x2(sc[0] | (sc[1] << 8));
-  const uint32_t s23 = e4m3x2_f16x2(sc[2] | (sc[3] << 8));
+  const uint32_t s01 = e4m3x2_f16x2(__byte_perm(sc[0], sc[1], 0x0040));
+  const uint32_t s23 = e4m3x2_f16x2(__byte_perm(sc[2], sc[3], 0x0040));
 #pragma unroll
-  for (int wi = 0; wi < D / 64; ++wi) {
+  for (int wi = 0; wi < C; ++wi) {
     // nibbles of two keys side by side: even dims, odd dims
     constexpr uint32_t M = 0x0f0f0f0fu;
     uint32_t e01[4], d01[4], e23[4], d23[4];
@@ -182,19 +249,15 @@ __device__ __forceinline__ void page_values(const unsigned char *vp, int g,
   }
 }
 
-// CTAs per SM the registers must allow.
-template <int NT>
-constexpr int min_ctas4() {
-  return NT == 1 ? 3 : 2;
-}
-
 template <int D, int NT, int MT>
-__global__ void __launch_bounds__(kThreads4, (min_ctas4<NT>()))
+__global__ void __launch_bounds__(Shape4<NT>::THREADS, Shape4<NT>::CTAS)
     paged_attention_fp4_kernel(const AttnParams p) {
   using S = Smem4<D, NT, MT>;
   constexpr int RW = S::RW, RB = S::RB;
+  constexpr int kWarps4 = S::kWarps4, kStages4 = S::kStages4;
   constexpr int NSTREAM = kWarps4 / MT;
   constexpr int KS = D / 16;
+  constexpr int PJ = NT <= 3 ? kStagePages : 1;  // pages scored together
   // as in attention.cu: a stage always belongs to the same stream
   static_assert(kStages4 % NSTREAM == 0, "ring depth: a multiple of the streams");
   extern __shared__ unsigned char smem_raw[];
@@ -230,7 +293,12 @@ __global__ void __launch_bounds__(kThreads4, (min_ctas4<NT>()))
     pdl_launch_dependents();       // the merge may be scheduled
   }
 
-  if (warp == kWarps4) {
+  if (Shape4<NT>::kWide && warp >= kWarps4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  }
+  if (warp > kWarps4) {
+    // the producer's idle neighbours
+  } else if (warp == kWarps4) {
     // ======================= producer warp =======================
     int *const seqlen = sm.prefix + p.batch + 1;
     const int total = build_prefix(p, sm.prefix, seqlen, groups_per_seq, lane,
@@ -264,6 +332,14 @@ __global__ void __launch_bounds__(kThreads4, (min_ctas4<NT>()))
         break;
       }
       const int n_pages = seg.n_pages;
+      // positions of the unit's first and last row: pages that end by the
+      // first (with a tree: before its nodes) and lie in the last one's
+      // window need no per-key test
+      const int base = seg.seq_len - p.q_len;
+      const int t_min =
+          p.tree_mask ? base - 1 : base + (seg.rg * RB) / p.group;
+      const int t_max =
+          base + (min(seg.rg * RB + RB, p.rows) - 1) / p.group;
       if (lane == 0) {
         sm.unit[slot] = seg;
         mbar_arrive(&sm.ufull[slot]);
@@ -320,6 +396,7 @@ __global__ void __launch_bounds__(kThreads4, (min_ctas4<NT>()))
           if (lane < n) {
             const int s = (c + lane) % kStages4;
             uint32_t bytes = 0;
+            bool all_vis = true;
 #pragma unroll
             for (int x = 0; x < kStagePages; ++x) {
               const int k = k0 + kk + kStagePages * lane + x;
@@ -333,7 +410,12 @@ __global__ void __launch_bounds__(kThreads4, (min_ctas4<NT>()))
                 }
               }
               sm.j0[s][x] = j0;
+              const int j1 = j0 + kBlockSize - 1;
+              all_vis = all_vis && j1 <= t_min &&
+                        (p.window == 0 || j1 < p.n_sink ||
+                         j0 > t_max - p.window);
             }
+            sm.checked[s] = !all_vis;
             if (bytes)
               mbar_arrive_expect_tx(&sm.full[s], bytes);
             else
@@ -370,6 +452,8 @@ __global__ void __launch_bounds__(kThreads4, (min_ctas4<NT>()))
     }
   } else {
     // ======================= consumer warps =======================
+    if (Shape4<NT>::kWide)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int g = lane >> 2, t = lane & 3;
     const int stream = warp / MT, mt = warp % MT;
     int c = 0, us = 0;
@@ -405,16 +489,14 @@ __global__ void __launch_bounds__(kThreads4, (min_ctas4<NT>()))
         uint32_t w[KS][2];
         uint32_t top = 0;
 #pragma unroll
-        for (int cc = 0; cc < D / 64; ++cc)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            uint4 v = __ldg(src + cc * 8 + t * 2 + x);
-            if (!valid) v = make_uint4(0, 0, 0, 0);
-            w[cc * 4 + 2 * x][0] = v.x;
-            w[cc * 4 + 2 * x][1] = v.y;
-            w[cc * 4 + 2 * x + 1][0] = v.z;
-            w[cc * 4 + 2 * x + 1][1] = v.w;
-          }
+        for (int x = 0; x < KS / 2; ++x) {  // q_dim: D/4 consecutive dims
+          uint4 v = __ldg(src + (KS / 2) * t + x);
+          if (!valid) v = make_uint4(0, 0, 0, 0);
+          w[2 * x][0] = v.x;
+          w[2 * x][1] = v.y;
+          w[2 * x + 1][0] = v.z;
+          w[2 * x + 1][1] = v.w;
+        }
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
@@ -440,11 +522,12 @@ __global__ void __launch_bounds__(kThreads4, (min_ctas4<NT>()))
         qs[nt][0] = __shfl_sync(kFull, sc, 8 * t);
         qs[nt][1] = __shfl_sync(kFull, sc, 8 * t + 4);
       }
-      auto qb = [&](int cc, int kk, int nt) -> uint2 {
+      const uint32_t q_addr = smem_u32(&sm.u.q[warp][0][lane]);
+      auto qb = [&](int ks, int nt) -> uint2 {
         if constexpr (S::kQSmem)
-          return sm.u.q[warp][nt * KS + cc * 4 + kk][lane];
+          return lds64(q_addr + (nt * KS + ks) * (32 * (int)sizeof(uint2)));
         else
-          return qf[nt][cc * 4 + kk];
+          return qf[nt][ks];
       };
 
       float o[D / 16][NT][4];
@@ -457,12 +540,9 @@ __global__ void __launch_bounds__(kThreads4, (min_ctas4<NT>()))
         for (int i = 0; i < D / 16; ++i)
           o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
       }
-      // positions of the unit's first and last row: pages that end by the
-      // first (with a tree: before its nodes) and lie in the last one's
-      // window need no per-key test
-      const int t_min = p.tree_mask ? t0 - 1 : t0 + (rg * RB) / p.group;
-      const int t_max = t0 + (min(rg * RB + RB, p.rows) - 1) / p.group;
-
+      const uint32_t kv0 = smem_u32(&sm.kv[0][0][0][0]);
+      const uint32_t k_off = k_lane<D>(g, t), v_off = v_lane<D>(g, t);
+      const uint32_t v_off_s = v_lane_scale<D>(g, t);
       const int n_stages = (ui.n_pages + kStagePages - 1) / kStagePages;
       const int first = ((stream - c) % NSTREAM + NSTREAM) % NSTREAM;
       for (int k = first; k < n_stages; k += NSTREAM) {
@@ -475,59 +555,54 @@ __global__ void __launch_bounds__(kThreads4, (min_ctas4<NT>()))
           aborted = true;
           break;
         }
+        const uint32_t st = kv0 + s * (kStagePages * 2 * S::PAGE);
+        const bool checked = sm.checked[s] != 0;  // warp-uniform
 #pragma unroll
-        for (int pg = 0; pg < kStagePages; ++pg) {
-          const int j0 = sm.j0[s][pg];
-          if (j0 == kNoPage) continue;  // warp-uniform
-          float x[NT][4];
+        for (int p0 = 0; p0 < kStagePages; p0 += PJ) {
+          float x[PJ][NT][4], y[PJ][NT][4];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
-          page_scores<D, NT>(sm.kv[s][pg][0], g, t, x, qb);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[nt][e] *= qs[nt][e & 1];
-          const int j1 = j0 + kBlockSize - 1;
-          const bool all_vis = j1 <= t_min &&
-                               (p.window == 0 || j1 < p.n_sink ||
-                                j0 > t_max - p.window);
-          unsigned keep = 0xfu;
-          if (!all_vis) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                const int gr = min(row0 + nt * 8 + 2 * t + r, p.rows - 1);
-                const int i = gr / p.group;
-                const uint32_t bits = row_tree_bits(p, b, i);
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                  if (!key_visible(j0 + fp4_key(g, h), t0 + i, bits, t0,
-                                   p.n_sink, p.window))
-                    x[nt][2 * h + r] = -INFINITY;
-              }
-#pragma unroll
-            for (int sx = 0; sx < 4; ++sx) {
-              const int j = j0 + 4 * t + sx;
-              if (!(j < L && (p.window == 0 || j < p.n_sink ||
-                              j > t0 - p.window)))
-                keep &= ~(1u << sx);
-            }
-          }
+          for (int j = 0; j < PJ; ++j)
+            page_scores<D, NT>(st + (p0 + j) * 2 * S::PAGE + k_off, t, x[j], qb);
           // ---- softmax with a lazy reference ----
           float far = -INFINITY;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int j = 0; j < PJ; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              far = fmaxf(far, x[nt][e] - ref[nt][e & 1]);
-          if (__any_sync(kFull, far > kRefSlack)) {
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                y[j][nt][e] = fmaf(x[j][nt][e], qs[nt][e & 1], -ref[nt][e & 1]);
+                far = fmaxf(far, y[j][nt][e]);
+              }
+          unsigned keep[PJ];
+#pragma unroll
+          for (int j = 0; j < PJ; ++j) keep[j] = 0xfu;
+          if (checked || __any_sync(kFull, far > kRefSlack)) {
+            // masked keys score -inf; a row whose scores reach beyond the
+            // slack gets a new reference
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
-                float mx = fmaxf(x[nt][r], x[nt][2 + r]);
+                uint32_t bits = ~0u;
+                int i = 0;
+                if (checked) {
+                  i = min(row0 + nt * 8 + 2 * t + r, p.rows - 1) / p.group;
+                  bits = row_tree_bits(p, b, i);
+                }
+                float mx = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < PJ; ++j)
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    float z = x[j][nt][2 * h + r] * qs[nt][r];
+                    if (checked &&
+                        !key_visible(sm.j0[s][p0 + j] + fp4_key(g, h), t0 + i,
+                                     bits, t0, p.n_sink, p.window))
+                      z = -INFINITY;
+                    x[j][nt][2 * h + r] = z;
+                    mx = fmaxf(mx, z);
+                  }
                 mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
                 mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
                 mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
@@ -536,24 +611,44 @@ __global__ void __launch_bounds__(kThreads4, (min_ctas4<NT>()))
                 ref[nt][r] = to;
                 l[nt][r] *= alpha;
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                  o[i][nt][r] *= alpha;
-                  o[i][nt][2 + r] *= alpha;
+                for (int d2 = 0; d2 < D / 16; ++d2) {
+                  o[d2][nt][r] *= alpha;
+                  o[d2][nt][2 + r] *= alpha;
                 }
+#pragma unroll
+                for (int j = 0; j < PJ; ++j)
+#pragma unroll
+                  for (int h = 0; h < 2; ++h)
+                    y[j][nt][2 * h + r] = x[j][nt][2 * h + r] - to;
               }
-          }
-          uint32_t pb[NT][2];
+            if (checked) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
+              for (int j = 0; j < PJ; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              x[nt][e] = ex2(x[nt][e] - ref[nt][e & 1]);
-              l[nt][e & 1] += x[nt][e];
+                for (int sx = 0; sx < 4; ++sx) {
+                  const int key = sm.j0[s][p0 + j] + 4 * t + sx;
+                  if (!(key < L && (p.window == 0 || key < p.n_sink ||
+                                    key > t0 - p.window)))
+                    keep[j] &= ~(1u << sx);
+                }
             }
-            pb[nt][0] = transpose8(pack_h2(x[nt][0], x[nt][1]));
-            pb[nt][1] = transpose8(pack_h2(x[nt][2], x[nt][3]));
           }
-          page_values<D, NT>(sm.kv[s][pg][1], g, t, keep, pb, o);
+#pragma unroll
+          for (int j = 0; j < PJ; ++j) {
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                y[j][nt][e] = ex2(y[j][nt][e]);
+                l[nt][e & 1] += y[j][nt][e];
+              }
+              pb[nt][0] = transpose8(pack_h2(y[j][nt][0], y[j][nt][1]));
+              pb[nt][1] = transpose8(pack_h2(y[j][nt][2], y[j][nt][3]));
+            }
+            const uint32_t vp = st + ((p0 + j) * 2 + 1) * S::PAGE;
+            page_values<D, NT>(vp + v_off, vp + v_off_s, keep[j], pb, o);
+          }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.empty[s]);
@@ -706,7 +801,7 @@ int prepare4(int batch) {
   int n = 0;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)smem) != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads4, smem) !=
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, Shape4<NT>::THREADS, smem) !=
           cudaSuccess)
     return -1;
   n = n > 0 ? n : 1;
@@ -741,7 +836,7 @@ template <int D, int NT, int MT>
 cudaError_t launch4(const AttnParams &p, int grid, cudaStream_t st) {
   if (prepare4<D, NT, MT>(p.batch) < 0) return cudaErrorInvalidValue;
   return launch_pdl(paged_attention_fp4_kernel<D, NT, MT>, (unsigned)grid,
-                    (unsigned)kThreads4, smem4<D, NT, MT>(p.batch), st, p);
+                    (unsigned)Shape4<NT>::THREADS, smem4<D, NT, MT>(p.batch), st, p);
 }
 
 }  // namespace
