@@ -151,7 +151,7 @@ int plan_attention(int batch, int num_q_heads, int num_kv_heads, int head_dim,
            : mma ? (rows <= 16 ? 16 : 32)
                  : rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : 8;
   const int n_rg = (rows + rb - 1) / rb;
-  const int ctas = fp4  ? attention_fp4_ctas_per_sm(head_dim, rb, batch)
+  const int ctas = fp4  ? 1
                    : tc ? attention_tc_ctas_per_sm(rb, batch)
                       : attention_ctas_per_sm(dtype, head_dim, rb, mma, batch);
   const long long groups = (long long)batch * num_kv_heads * n_rg;
@@ -168,15 +168,19 @@ int plan_attention(int batch, int num_q_heads, int num_kv_heads, int head_dim,
   plan->mma = mma;
   plan->tc = tc;
   plan->fp4 = fp4;
-  plan->batch_cap = tc ? tc_batch_cap() : kBatchPerLaunch;
+  plan->batch_cap = fp4 ? kBatchFp4 : tc ? tc_batch_cap() : kBatchPerLaunch;
   plan->min_pages = min_pages;
   plan->seg_items = fp4 ? kSegItemsFp4 : tc ? kSegItemsTc : kSegItemsCc;
   plan->grid = (int)grid;
   plan->ctas_per_sm = ctas;
   plan->ws_head = 256;
-  plan->ws_desc = align256((size_t)grid * 32);  // one SplitDesc per CTA
-  plan->ws_part_o = align256((size_t)2 * grid * rb * head_dim * 4);
-  plan->ws_part_lse = align256((size_t)2 * grid * rb * 4);
+  // one SplitDesc per CTA; 4-bit caches: the slices of every group, and a
+  // slice is a warp's
+  const size_t slices = (size_t)grid * (fp4 ? attention_fp4_warps(rb) : 1);
+  plan->ws_desc = align256(fp4 ? (size_t)groups * sizeof(int2)
+                               : (size_t)grid * 32);
+  plan->ws_part_o = align256(2 * slices * rb * head_dim * 4);
+  plan->ws_part_lse = align256(2 * slices * rb * 4);
   plan->ws_total =
       plan->ws_head + plan->ws_desc + plan->ws_part_o + plan->ws_part_lse;
   return SVP_OK;
@@ -207,7 +211,9 @@ static int plan_call(const svp_dims *d, int q_len, int n_sink, int window,
   const int path = select_path(d->dtype, d->head_dim, rows, d->kernel_path,
                                d->num_blocks, d->num_kv_heads);
   if (path < 0) return path;
-  const int cap = path == SVP_PATH_TCGEN05 ? tc_batch_cap() : kBatchPerLaunch;
+  const int cap = d->dtype == SVP_FP4_E2M1   ? kBatchFp4
+                  : path == SVP_PATH_TCGEN05 ? tc_batch_cap()
+                                             : kBatchPerLaunch;
   const int bl = batch_per_launch(d, q_len, n_sink, window, cap,
                                   d->dtype == SVP_FP4_E2M1   ? kSegItemsFp4
                                   : path == SVP_PATH_TCGEN05 ? kSegItemsTc
@@ -314,6 +320,7 @@ static int attention_call(const svp_dims *dims, const void *q,
     p.out = static_cast<char *>(out) + (size_t)b0 * q_len * row_elems * eb;
     p.lse = lse + (size_t)b0 * q_len * dims->num_q_heads;
     p.desc = reinterpret_cast<SplitDesc *>(wp + plan.ws_head);
+    p.split = reinterpret_cast<int2 *>(wp + plan.ws_head);
     p.part_o = reinterpret_cast<float *>(wp + plan.ws_head + plan.ws_desc);
     p.part_lse = reinterpret_cast<float *>(wp + plan.ws_head + plan.ws_desc +
                                            plan.ws_part_o);
@@ -330,7 +337,8 @@ static int attention_call(const svp_dims *dims, const void *q,
     p.rows = p.group * q_len;
     p.rb = plan.rb;
     p.n_rg = plan.n_rg;
-    // tcgen05: items are 8-page tiles, 4-bit caches: 2-page stages (a
+    p.merge_rows = std::min(plan.rb, p.rows);
+    // tcgen05: items are 8-page tiles, 4-bit caches: 4-page stages (a
     // slice's minimum in items)
     p.ppi = plan.fp4 ? kTilePagesFp4 : plan.tc ? kTilePagesTc : 1;
     p.min_pages = std::max(1, plan.min_pages / p.ppi);
@@ -358,8 +366,10 @@ static int attention_call(const svp_dims *dims, const void *q,
         : plan.tc ? launch_attention_tc(p, sub.grid, stream)
                 : launch_attention(p, dims->dtype, plan.mma, sub.grid, stream);
     if (e != cudaSuccess) return SVP_ERR_CUDA;
-    // groups split over several CTAs are finished by the merge kernel
-    if (launch_merge(p, dims->dtype, sub.grid, stream) != cudaSuccess)
+    // groups split over several CTAs are finished by the merge kernel (the
+    // 4-bit path launched its own)
+    if (!plan.fp4 &&
+        launch_merge(p, dims->dtype, sub.grid, stream) != cudaSuccess)
       return SVP_ERR_CUDA;
     launches += 2;
   }

@@ -1255,9 +1255,7 @@ cudaError_t launch_merge(const AttnParams &p, int dtype, int grid,
     SVP_MERGE_RB(4)
     SVP_MERGE_RB(8)
     SVP_MERGE_RB(16)
-    SVP_MERGE_RB(24)
     SVP_MERGE_RB(32)
-    SVP_MERGE_RB(48)
     SVP_MERGE_RB(64)
 #undef SVP_MERGE_RB
     default:

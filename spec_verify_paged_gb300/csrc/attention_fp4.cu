@@ -13,9 +13,9 @@
 // is done once per element for all rows, and the codes go from shared
 // memory to the matrix instruction through registers only.
 //
-//  * S^T = K Q^T, one 16-key page per m16 tile: lane (g, t) takes 16
-//    consecutive codes (one scale block) of keys g and g + 8 for four
-//    k-steps.  Q is fp16 with a power-of-two scale per row (fp4.cuh).
+//  * S^T = K Q^T, one 16-key page per m16 tile: lane (g, t) takes
+//    consecutive codes (whole scale blocks) of two keys.  Q is fp16 with a
+//    power-of-two scale per row (fp4.cuh).
 //  * Softmax on the accumulators in the log2 domain.  The running maximum is
 //    lazy: a row's reference moves only when a score exceeds it by 2^8, so
 //    the usual page costs one vote instead of shuffled maxima.  P is fp16 at
@@ -25,9 +25,15 @@
 //    (g, t) reads D/8 consecutive codes of four keys; the nibbles of two
 //    keys are interleaved before the conversion, so one cvt yields the pair
 //    of keys that the A operand wants for one dimension.
-//  * One producer warp, 1-D bulk copies (a head's page is one run of 9 D
-//    bytes), stages of two pages, mbarrier ring, stream-K slices and the
-//    split merge of attn_common.cuh.
+//  * Every warp is on its own: it takes one slice of the flattened page list
+//    (the stream-K order of attn_common.cuh, with a warp where that has a
+//    CTA), copies its pages itself (1-D bulk copies -- a head's page is one
+//    run of 9 D bytes -- four pages to a stage, two stages), keeps a
+//    segment's whole state in registers and writes the segment's result from
+//    there.  No barrier joins the warps, so a warp that ends a segment
+//    (normalise, write, next Q) costs the others nothing.
+//  * A group of pages cut by slice borders leaves one normalised partial per
+//    slice; merge_fp4_kernel joins them by log-sum-exp in slice order.
 //  * Rows whose memory holds no valid data take no part: masked keys score
 //    -inf whatever their bytes, and their V scale is replaced by 0.
 #include <cuda_fp16.h>
@@ -47,53 +53,53 @@ static __device__ unsigned int g_status_attn4;
 
 namespace {
 
-constexpr int kStagePages = 2;
+constexpr int kStagePages = kTilePagesFp4;    // 4
 constexpr int kNoPage = 0x7fffff00;           // j0 of a page that is not there
 constexpr float kRefOffset = 6.f;             // P = 2^6 at the reference
 constexpr float kRefSlack = 14.f;             // largest log2 P before a move
 constexpr float kNoRef = -3e38f;              // below any finite score
 
-// The CTA's shape for NT n8 tiles of query rows per warp.  Up to two tiles:
-// four consumer warps and the producer warp, several CTAs per SM.  From
-// three on a consumer holds 32 accumulators per tile: one CTA per SM, two
-// warpgroups of consumers and one whose first warp produces; 384 threads
-// launched with 168 registers each are split 224 / 56 (2 x 128 x 224 + 128 x
-// 56 = 384 x 168).
+// Warps of a CTA (one per SM) for NT n8 tiles of query rows: what the
+// registers allow (O alone takes 32 per tile), 170 per thread for twelve
+// warps, 255 for eight.
 template <int NT>
-struct Shape4 {
-  static constexpr bool kWide = NT > 2;
-  static constexpr int W = kWide ? 8 : 4;  // consumer warps
-  static constexpr int THREADS = kWide ? 384 : 160;
-  static constexpr int CTAS = NT == 1 ? 3 : kWide ? 1 : 2;  // per SM
-  static constexpr int STAGES = kWide ? 16 : 8;
+__host__ __device__ constexpr int warps4() {
+  return NT == 1 ? 12 : 8;
+}
+// Stages of a warp's ring: 9 D bytes x 8 each, as many as fit.
+template <int NT>
+__host__ __device__ constexpr int stages4() {
+  return NT == 1 ? 2 : 3;
+}
+constexpr int kSegRing4 = 8;  // decoded segments: read .. issued + 1
+
+// A run of pages of one group within a slice.
+struct Seg4 {
+  int b, g, rg, L;
+  int page0, n_pages, n_a, b_start;
+  int f, l;    // slices that hold the group's first and last page
+  int next;    // flat item after the run
+  int valid;
 };
 
-// MT warps share a stage.
-template <int D, int NT, int MT>
-struct Smem4 {
-  static constexpr int kWarps4 = Shape4<NT>::W, kStages4 = Shape4<NT>::STAGES;
+template <int D, int STAGES>
+struct Warp4 {
   static constexpr int PAGE = 9 * D;  // bytes of one head's 16 rows
-  static constexpr int RW = 8 * NT;
-  static constexpr int RB = RW * MT;
-  static constexpr bool kQSmem = NT > 2;
-  alignas(128) unsigned char kv[kStages4][kStagePages][2][PAGE];
-  union {
-    uint2 q[kWarps4][kQSmem ? NT * (D / 16) : 1][32];  // Q operand fragments
-    float o[kWarps4][RW][D + 4];                       // states, segment end
-  } u;
-  float red_m[kWarps4][RW];
-  float red_l[kWarps4][RW];
-  float wf[kWarps4][RB];
-  UnitInfo unit[kUnitRing];
-  int j0[kStages4][kStagePages];
-  int checked[kStages4];  // the stage's keys need the visibility test
-  uint64_t full[kStages4], empty[kStages4];
-  uint64_t ufull[kUnitRing], uempty[kUnitRing];
-  uint64_t epi;
-#ifdef SVP_TEST_STALL_AFTER
-  uint64_t stall;  // test builds: a barrier nothing arrives on
-#endif
-  int abort_flag;
+  alignas(128) unsigned char kv[STAGES][kStagePages][2][PAGE];
+};
+// what the issuing side leaves for the reading side
+template <int STAGES>
+struct Info4 {
+  uint64_t full[STAGES];
+  int j0[STAGES][kStagePages];
+  int checked[STAGES];  // the stage's keys need the visibility test
+  int pages[STAGES];
+  Seg4 seg[kSegRing4];
+};
+template <int D, int W, int STAGES>
+struct Smem4 {
+  Warp4<D, STAGES> warp[W];
+  Info4<STAGES> info[W];
   int prefix[1];  // [batch + 1] item prefix, then [batch] lengths: dynamic
 };
 
@@ -249,623 +255,571 @@ __device__ __forceinline__ void page_values(uint32_t vp, uint32_t sp,
   }
 }
 
-template <int D, int NT, int MT>
-__global__ void __launch_bounds__(Shape4<NT>::THREADS, Shape4<NT>::CTAS)
+// The first run of pages at or after flat item `pos` (as decode_segment of
+// attn_common.cuh, for slices instead of CTAs).
+__device__ __forceinline__ Seg4 next_segment(const AttnParams &p,
+                                             const int *prefix,
+                                             const int *seqlen, int per_seq,
+                                             int pos, int end, int total,
+                                             int n_slices) {
+  Seg4 s;
+  s.valid = 0;
+  if (pos >= end) return s;
+  int lo = 0, hi = p.batch;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid] <= pos) lo = mid; else hi = mid;
+  }
+  const int per = (prefix[lo + 1] - prefix[lo]) / per_seq;
+  const int nt = per - p.seg_items;
+  const int gi = (pos - prefix[lo]) / per;
+  const int off = pos - prefix[lo] - gi * per;
+  const int first = prefix[lo] + gi * per + p.seg_items;
+  const int t0 = off < p.seg_items ? 0 : off - p.seg_items;
+  int np;
+  s.b = lo;
+  s.L = seqlen[lo];
+  visible_pages(s.L, p.q_len, p.n_sink, p.window, s.n_a, s.b_start, np);
+  s.page0 = t0 * p.ppi;
+  s.g = gi / p.n_rg;
+  s.rg = gi - s.g * p.n_rg;
+  const int items = min(end - (first + t0), nt - t0);
+  s.n_pages = min(items * p.ppi, np - s.page0);
+  s.next = first + t0 + items;
+  s.f = div_u64((unsigned long long)(first + 1) * (unsigned)n_slices - 1u,
+                (unsigned)total);
+  s.l = div_u64((unsigned long long)(first + nt) * (unsigned)n_slices - 1u,
+                (unsigned)total);
+  s.valid = s.n_pages > 0;
+  return s;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * warps4<NT>(), 1)
     paged_attention_fp4_kernel(const AttnParams p) {
-  using S = Smem4<D, NT, MT>;
-  constexpr int RW = S::RW, RB = S::RB;
-  constexpr int kWarps4 = S::kWarps4, kStages4 = S::kStages4;
-  constexpr int NSTREAM = kWarps4 / MT;
-  constexpr int KS = D / 16;
-  constexpr int PJ = NT <= 3 ? kStagePages : 1;  // pages scored together
-  // as in attention.cu: a stage always belongs to the same stream
-  static_assert(kStages4 % NSTREAM == 0, "ring depth: a multiple of the streams");
+  constexpr int W = warps4<NT>(), RB = 8 * NT, KS = D / 16;
+  constexpr int PJ = 2;  // pages scored together
+  constexpr int kStages4 = stages4<NT>();
+  static_assert(kStages4 + 2 <= kSegRing4, "a stage holds at most one segment");
+  constexpr int PAGE = 9 * D;
   extern __shared__ unsigned char smem_raw[];
+  using S = Smem4<D, W, kStages4>;
   S &sm = *reinterpret_cast<S *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-
-  const int tid = threadIdx.x;
-  const int warp = tid >> 5;
-  const int lane = tid & 31;
-  const int groups_per_seq = p.num_kv_heads * p.n_rg;
-
-  if (tid == 0) {
-    for (int s = 0; s < kStages4; ++s) {
-      mbar_init(&sm.full[s], 1);
-      mbar_init(&sm.empty[s], MT);
-    }
-    for (int u = 0; u < kUnitRing; ++u) {
-      mbar_init(&sm.ufull[u], 1);
-      mbar_init(&sm.uempty[u], 1);
-    }
-    mbar_init(&sm.epi, kWarps4);
-#ifdef SVP_TEST_STALL_AFTER
-    mbar_init(&sm.stall, 1);
-#endif
-    sm.abort_flag = 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int per_seq = p.num_kv_heads * p.n_rg;
+  Info4<kStages4> &inf = sm.info[warp];
+  if (lane == 0) {
+    for (int s = 0; s < kStages4; ++s) mbar_init(&inf.full[s], 1);
     fence_mbar_init();
   }
-  __syncthreads();
+  __syncwarp();
   // launched early: see AttnParams::early
   if (!p.early) pdl_wait();
-  if (tid == 0) {
-    p.desc[blockIdx.x].valid = 0;  // until a split group starts
-    pdl_launch_dependents();       // the merge may be scheduled
-  }
+  pdl_launch_dependents();  // the merge may be scheduled
+  int *const seqlen = sm.prefix + p.batch + 1;
+  if (warp == 0) build_prefix(p, sm.prefix, seqlen, per_seq, lane, &g_status_attn4);
+  __syncthreads();  // the only one: the warps are on their own from here
+  const int total = sm.prefix[p.batch];
+  // slice s goes to warp s / gridDim.x of CTA s % gridDim.x: a small call
+  // spreads over the SMs
+  const int n_slices = min((long long)gridDim.x * W, max(1LL, (long long)total / p.min_pages));
+  const int slice = warp * gridDim.x + blockIdx.x;
+  if (slice >= n_slices) return;
+  const int end = slice_begin(slice + 1, total, n_slices);
 
-  if (Shape4<NT>::kWide && warp >= kWarps4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-  }
-  if (warp > kWarps4) {
-    // the producer's idle neighbours
-  } else if (warp == kWarps4) {
-    // ======================= producer warp =======================
-    int *const seqlen = sm.prefix + p.batch + 1;
-    const int total = build_prefix(p, sm.prefix, seqlen, groups_per_seq, lane,
-                                   &g_status_attn4);
-    const int n_ctas = working_ctas(total, p.min_pages);
-    const int range_begin = slice_begin(blockIdx.x, total, n_ctas);
-    const int range_end = blockIdx.x < n_ctas
-                              ? slice_begin(blockIdx.x + 1, total, n_ctas)
-                              : total;
-    int c = 0;   // stages issued so far
-    int us = 0;  // segments published so far
-    bool waited = !p.early;
-    bool ok = true;
-    int pos = range_begin;
-    while (true) {
-      const int slot = us % kUnitRing;
-      if (lane == 0)
-        ok = mbar_wait(&sm.uempty[slot], ((us / kUnitRing) & 1) ^ 1);
-      ok = __shfl_sync(kFull, ok, 0) && !sm.abort_flag;
-      if (!ok) break;
-      const UnitInfo seg =
-          pos < range_end
-              ? decode_segment(p, sm.prefix, seqlen, groups_per_seq, pos,
-                               us == 0, range_end, total, n_ctas)
-              : UnitInfo{};
-      if (!seg.valid) {
-        if (lane == 0) {
-          sm.unit[slot].valid = 0;
-          mbar_arrive(&sm.ufull[slot]);
-        }
-        break;
-      }
-      const int n_pages = seg.n_pages;
-      // positions of the unit's first and last row: pages that end by the
-      // first (with a tree: before its nodes) and lie in the last one's
-      // window need no per-key test
-      const int base = seg.seq_len - p.q_len;
-      const int t_min =
-          p.tree_mask ? base - 1 : base + (seg.rg * RB) / p.group;
-      const int t_max =
-          base + (min(seg.rg * RB + RB, p.rows) - 1) / p.group;
-      if (lane == 0) {
-        sm.unit[slot] = seg;
-        mbar_arrive(&sm.ufull[slot]);
-      }
-      // 32 block-table entries at a time (16 stages), the next 32 loaded
-      // while these go out
-      auto entry = [&](int k) {
-        return k < n_pages
-                   ? __ldg(p.block_table + (size_t)seg.b * p.max_blocks +
-                           logical_block(seg, seg.page0 + k))
-                   : -1;
-      };
-      int phys = entry(lane);
-      for (int k0 = 0; k0 < n_pages && ok; k0 += 32) {
-        const int next = entry(k0 + 32 + lane);
-        const int n_here = min(32, n_pages - k0);
-        // stages go out in batches, as in attention.cu: lane i arms stage
-        // c + i, lane 4 i + r issues copy r of its four
-        constexpr int MAXB = 8 < kStages4 ? 8 : kStages4;
-        for (int kk = 0; kk < n_here;) {
+  // ---- the issuing side: up to kStages4 stages ahead of the reading side.
+  // Segment `seg_i` is being issued, the one after it is decoded already and
+  // its first block-table entries are on their way. ----
+  bool waited = !p.early;  // the grid-dependency wait is behind us
+  int issued = 0, seg_i = 0, k = 0;
+  auto decode = [&](int i, int pos) {  // segment i of this slice, into the ring
+    const Seg4 s = next_segment(p, sm.prefix, seqlen, per_seq, pos, end, total,
+                                n_slices);
+    if (lane == 0) inf.seg[i % kSegRing4] = s;
+    __syncwarp();
+  };
+  auto entry = [&](int i, int page) {  // block-table entry of a page of segment i
+    const Seg4 &s = inf.seg[i % kSegRing4];
+    if (!s.valid || page >= s.n_pages) return -1;
+    const int pidx = s.page0 + page;
+    const int lb = pidx < s.n_a ? pidx : s.b_start + (pidx - s.n_a);
+    return __ldg(p.block_table + (size_t)s.b * p.max_blocks + lb);
+  };
+  decode(0, slice_begin(slice, total, n_slices));
+  // entries of pages k .. k + 31, of the 32 after them, and of the following
+  // segment's first 32
+  int phys = entry(0, lane), phys2 = entry(0, 32 + lane);
+  decode(1, inf.seg[0].valid ? inf.seg[0].next : end);
+  int phys_a = entry(1, lane);
+  auto issue = [&]() {
+    const Seg4 &cur = inf.seg[seg_i % kSegRing4];
+    if (!cur.valid) return;
+    const int st = issued % kStages4;
+    const int n_pages = cur.n_pages, page0 = cur.page0, n_a = cur.n_a;
+    const int skip = cur.b_start - n_a, kvh = cur.g, base = cur.L - p.q_len;
+    const int row0 = cur.rg * RB;
+    auto block = [&](int pidx) { return pidx < n_a ? pidx : pidx + skip; };
+    const int n = min(kStagePages, n_pages - k);
+    if (!waited && (block(page0 + k + n - 1) + 1) * kBlockSize > base) {
+      pdl_wait();  // a page may hold some of the appended positions
+      waited = true;
+    }
+    // lane 2 x + side: page x's copy of that side
+    const int x = lane >> 1, side = lane & 1;
+    const int ph = __shfl_sync(kFull, phys, ((k & 31) + x) & 31);
+    const bool here = lane < 2 * kStagePages && x < n;
+    const bool good = here && ph >= 0 && ph < p.num_blocks;
+    if (here && !good && side == 0) raise4(SVP_DEV_BAD_BLOCK_ID);
+    const int j0 = good ? block(page0 + k + x) * kBlockSize : kNoPage;
+    // pages that end by the unit's first position (with a tree: before its
+    // nodes) and lie in its last one's window need no per-key test
+    const int t_min = p.tree_mask ? base - 1 : base + row0 / p.group;
+    const int t_max = base + (min(row0 + RB, p.rows) - 1) / p.group;
+    const int j1 = j0 + kBlockSize - 1;
+    const bool clear = j1 <= t_min && (p.window == 0 || j1 < p.n_sink ||
+                                       j0 > t_max - p.window);
+    const unsigned copies = __ballot_sync(kFull, good);
+    const bool test = __any_sync(kFull, !clear && x < ((n + 1) & ~1));
+    if (lane < 2 * kStagePages && side == 0) inf.j0[st][x] = j0;
+    if (lane == 0) {
+      inf.checked[st] = test;
+      inf.pages[st] = n;
 #ifdef SVP_TEST_STALL_AFTER
-          if (c >= SVP_TEST_STALL_AFTER) {
-            if (lane == 0) ok = mbar_wait(&sm.stall, 0);
-            ok = __shfl_sync(kFull, ok, 0);
-            if (!ok) break;
-          }
+      // test builds only: later stages never arrive, so the waits run out
+      if (issued < SVP_TEST_STALL_AFTER)
 #endif
-          const int left = min((n_here - kk + 1) / kStagePages, MAXB);
-          if (!waited) {
-            const int lb = logical_block(
-                seg, seg.page0 + min(k0 + kk + left * kStagePages, n_pages) - 1);
-            if ((lb + 1) * kBlockSize > seg.seq_len - p.q_len) {
-              pdl_wait();  // it may hold some of the appended positions
-              waited = true;
-            }
-          }
-          bool ready = false;
-          if (lane == 0)
-            ready = mbar_wait(&sm.empty[c % kStages4], ((c / kStages4) & 1) ^ 1);
-          ok = __shfl_sync(kFull, ready, 0);
-          if (!ok) break;
-          if (lane > 0 && lane < left)
-            ready = mbar_ready(&sm.empty[(c + lane) % kStages4],
-                               (((c + lane) / kStages4) & 1) ^ 1);
-          const unsigned run = __ballot_sync(kFull, lane < left && ready);
-          const int n = __ffs(~run) - 1;  // stages c .. c + n - 1 are free
-          int ph[kStagePages];
-#pragma unroll
-          for (int x = 0; x < kStagePages; ++x)
-            ph[x] = __shfl_sync(kFull, phys, min(kk + kStagePages * lane + x, 31));
-          const int ci = lane >> 2, part = lane & 3;  // this lane's copy
-          const int ph_c = __shfl_sync(
-              kFull, phys, min(kk + kStagePages * ci + (part >> 1), 31));
-          if (lane < n) {
-            const int s = (c + lane) % kStages4;
-            uint32_t bytes = 0;
-            bool all_vis = true;
-#pragma unroll
-            for (int x = 0; x < kStagePages; ++x) {
-              const int k = k0 + kk + kStagePages * lane + x;
-              int j0 = kNoPage;
-              if (k < n_pages) {
-                if (ph[x] >= 0 && ph[x] < p.num_blocks) {
-                  j0 = logical_block(seg, seg.page0 + k) * kBlockSize;
-                  bytes += 2 * S::PAGE;
-                } else {
-                  raise4(SVP_DEV_BAD_BLOCK_ID);
-                }
-              }
-              sm.j0[s][x] = j0;
-              const int j1 = j0 + kBlockSize - 1;
-              all_vis = all_vis && j1 <= t_min &&
-                        (p.window == 0 || j1 < p.n_sink ||
-                         j0 > t_max - p.window);
-            }
-            sm.checked[s] = !all_vis;
-            if (bytes)
-              mbar_arrive_expect_tx(&sm.full[s], bytes);
-            else
-              mbar_arrive(&sm.full[s]);
-          }
-          __syncwarp();
-          if (ci < n && k0 + kk + kStagePages * ci + (part >> 1) < n_pages &&
-              ph_c >= 0 && ph_c < p.num_blocks) {
-            const int s = (c + ci) % kStages4;
-            const size_t off =
-                ((size_t)ph_c * p.num_kv_heads + seg.g) * (size_t)S::PAGE;
-            bulk_g2s(sm.kv[s][part >> 1][part & 1],
-                     static_cast<const unsigned char *>(part & 1 ? p.v_cache
-                                                                 : p.k_cache) +
-                         off,
-                     S::PAGE, &sm.full[s]);
-          }
-          c += n;
-          kk += n * kStagePages;
-        }
-        phys = next;
-      }
-      if (!ok) break;
-      pos = seg.item0 + (n_pages + p.ppi - 1) / p.ppi;
-      ++us;
-    }
-    if (!ok) {
-      if (lane == 0) {
-        raise4(SVP_DEV_TIMEOUT);
-        sm.abort_flag = 1;
-        for (int k = max(0, c - kStages4); k < c; ++k)
-          (void)mbar_wait_drain(&sm.full[k % kStages4], (k / kStages4) & 1);
-      }
-    }
-  } else {
-    // ======================= consumer warps =======================
-    if (Shape4<NT>::kWide)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    const int g = lane >> 2, t = lane & 3;
-    const int stream = warp / MT, mt = warp % MT;
-    int c = 0, us = 0;
-    uint32_t epi_phase = 0;
-    while (true) {
-      const int slot = us % kUnitRing;
-      const bool ok =
-          __all_sync(kFull, mbar_wait(&sm.ufull[slot], (us / kUnitRing) & 1));
-      if (!ok) {
-        if (lane == 0) { raise4(SVP_DEV_TIMEOUT); sm.abort_flag = 1; }
-        break;
-      }
-      const UnitInfo ui = sm.unit[slot];
-      if (!ui.valid || sm.abort_flag) break;
-      const int b = ui.b, kvh = ui.g, rg = ui.rg, L = ui.seq_len;
-      const int t0 = L - p.q_len;
-      const int row0 = rg * RB + mt * RW;  // this warp's first row
-      bool aborted = false;
-
-      // ---- Q fragments: row n = g of each n8 tile, fp16, scaled by row ----
-      uint2 qf[S::kQSmem ? 1 : NT][S::kQSmem ? 1 : KS];
-      float qs[NT][2];  // score scale of rows 2t, 2t + 1
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int gr = row0 + nt * 8 + g;
-        const bool valid = gr < p.rows;
-        const int grc = valid ? gr : rg * RB;
-        const int i = grc / p.group;
-        const int h = kvh * p.group + grc % p.group;
-        const uint4 *src = reinterpret_cast<const uint4 *>(
-            static_cast<const uint16_t *>(p.q) +
-            (((size_t)b * p.q_len + i) * p.num_q_heads + h) * D);
-        uint32_t w[KS][2];
-        uint32_t top = 0;
-#pragma unroll
-        for (int x = 0; x < KS / 2; ++x) {  // q_dim: D/4 consecutive dims
-          uint4 v = __ldg(src + (KS / 2) * t + x);
-          if (!valid) v = make_uint4(0, 0, 0, 0);
-          w[2 * x][0] = v.x;
-          w[2 * x][1] = v.y;
-          w[2 * x + 1][0] = v.z;
-          w[2 * x + 1][1] = v.w;
-        }
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            top = max(top, max(w[ks][x] & 0x7fffu, (w[ks][x] >> 16) & 0x7fffu));
-        top = max(top, __shfl_xor_sync(kFull, top, 1));
-        top = max(top, __shfl_xor_sync(kFull, top, 2));
-        const int e = q_exponent(__uint_as_float(top << 16));
-        const float f = pow2i(14 - e);
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          uint32_t hh[2];
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            hh[x] = pack_h2(__uint_as_float(w[ks][x] << 16) * f,
-                            __uint_as_float(w[ks][x] & 0xffff0000u) * f);
-          if constexpr (S::kQSmem)
-            sm.u.q[warp][nt * KS + ks][lane] = make_uint2(hh[0], hh[1]);
-          else
-            qf[nt][ks] = make_uint2(hh[0], hh[1]);
-        }
-        const float sc = p.qscale * pow2i(e - 14);
-        qs[nt][0] = __shfl_sync(kFull, sc, 8 * t);
-        qs[nt][1] = __shfl_sync(kFull, sc, 8 * t + 4);
-      }
-      const uint32_t q_addr = smem_u32(&sm.u.q[warp][0][lane]);
-      auto qb = [&](int ks, int nt) -> uint2 {
-        if constexpr (S::kQSmem)
-          return lds64(q_addr + (nt * KS + ks) * (32 * (int)sizeof(uint2)));
+      {
+        if (copies)
+          mbar_arrive_expect_tx(&inf.full[st], __popc(copies) * PAGE);
         else
-          return qf[nt][ks];
-      };
-
-      float o[D / 16][NT][4];
-      float ref[NT][2], l[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        ref[nt][0] = ref[nt][1] = kNoRef;
-        l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-          o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+          mbar_arrive(&inf.full[st]);
       }
-      const uint32_t kv0 = smem_u32(&sm.kv[0][0][0][0]);
-      const uint32_t k_off = k_lane<D>(g, t), v_off = v_lane<D>(g, t);
-      const uint32_t v_off_s = v_lane_scale<D>(g, t);
-      const int n_stages = (ui.n_pages + kStagePages - 1) / kStagePages;
-      const int first = ((stream - c) % NSTREAM + NSTREAM) % NSTREAM;
-      for (int k = first; k < n_stages; k += NSTREAM) {
-        const int cc = c + k;
-        const int s = cc % kStages4;
-        const bool got =
-            __all_sync(kFull, mbar_wait(&sm.full[s], (cc / kStages4) & 1));
-        if (!got) {
-          if (lane == 0) { raise4(SVP_DEV_TIMEOUT); sm.abort_flag = 1; }
-          aborted = true;
-          break;
+    }
+    __syncwarp();
+#ifdef SVP_TEST_STALL_AFTER
+    if (issued < SVP_TEST_STALL_AFTER)
+#endif
+    if (good) {
+      const size_t off = ((size_t)ph * p.num_kv_heads + kvh) * (size_t)PAGE;
+      bulk_g2s(sm.warp[warp].kv[st][x][side],
+               static_cast<const unsigned char *>(side ? p.v_cache : p.k_cache) + off,
+               PAGE, &inf.full[st]);
+    }
+    ++issued;
+    k += n;
+    if (k >= n_pages) {
+      k = 0;
+      ++seg_i;
+      phys = phys_a;
+      phys2 = entry(seg_i, 32 + lane);
+      const Seg4 &now = inf.seg[seg_i % kSegRing4];
+      decode(seg_i + 1, now.valid ? now.next : end);
+      phys_a = entry(seg_i + 1, lane);
+    } else if ((k & 31) == 0) {
+      phys = phys2;
+      phys2 = entry(seg_i, k + 32 + lane);
+    }
+  };
+  for (int s = 0; s < kStages4; ++s) issue();
+
+  // ---- the reading side ----
+  const uint32_t kv0 = smem_u32(&sm.warp[warp].kv[0][0][0][0]);
+  const uint32_t k_off = k_lane<D>(g, t), v_off = v_lane<D>(g, t);
+  const uint32_t v_off_s = v_lane_scale<D>(g, t);
+  int c = 0;  // stages read
+  for (int us = 0;; ++us) {
+    __syncwarp();
+    const Seg4 ui = inf.seg[us % kSegRing4];
+    if (!ui.valid) break;
+    const int L = ui.L, t0 = L - p.q_len;
+    const int row0 = ui.rg * RB;
+
+    // ---- Q fragments: row n = g of each n8 tile, fp16, scaled by row ----
+    uint2 qf[NT][KS];
+    float qs[NT][2];  // score scale of rows 2t, 2t + 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int gr = row0 + nt * 8 + g;
+      const bool valid = gr < p.rows;
+      const int grc = valid ? gr : row0;
+      const int i = grc / p.group;
+      const int h = ui.g * p.group + grc % p.group;
+      const uint4 *src = reinterpret_cast<const uint4 *>(
+          static_cast<const uint16_t *>(p.q) +
+          (((size_t)ui.b * p.q_len + i) * p.num_q_heads + h) * D);
+      uint32_t top = 0;
+#pragma unroll
+      for (int x = 0; x < KS / 2; ++x) {  // q_dim: D/4 consecutive dims
+        uint4 v = __ldg(src + (KS / 2) * t + x);
+        if (!valid) v = make_uint4(0, 0, 0, 0);
+        qf[nt][2 * x] = make_uint2(v.x, v.y);
+        qf[nt][2 * x + 1] = make_uint2(v.z, v.w);
+      }
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const uint2 v = qf[nt][ks];
+        top = max(top, max(max(v.x & 0x7fffu, (v.x >> 16) & 0x7fffu),
+                           max(v.y & 0x7fffu, (v.y >> 16) & 0x7fffu)));
+      }
+      top = max(top, __shfl_xor_sync(kFull, top, 1));
+      top = max(top, __shfl_xor_sync(kFull, top, 2));
+      const int e = q_exponent(__uint_as_float(top << 16));
+      const float f = pow2i(14 - e);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const uint2 v = qf[nt][ks];
+        qf[nt][ks] = make_uint2(pack_h2(__uint_as_float(v.x << 16) * f,
+                                        __uint_as_float(v.x & 0xffff0000u) * f),
+                                pack_h2(__uint_as_float(v.y << 16) * f,
+                                        __uint_as_float(v.y & 0xffff0000u) * f));
+      }
+      const float sc = p.qscale * pow2i(e - 14);
+      qs[nt][0] = __shfl_sync(kFull, sc, 8 * t);
+      qs[nt][1] = __shfl_sync(kFull, sc, 8 * t + 4);
+    }
+    auto qb = [&](int ks, int nt) { return qf[nt][ks]; };
+
+    float o[D / 16][NT][4];
+    float ref[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      ref[nt][0] = ref[nt][1] = kNoRef;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+        o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+    }
+
+    for (int k1 = 0; k1 < ui.n_pages; k1 += kStagePages, ++c) {
+      const int s = c % kStages4;
+      if (!__all_sync(kFull, mbar_wait(&inf.full[s], (c / kStages4) & 1))) {
+        // give up: flag it, wait (bounded) for the copies still in flight
+        if (lane == 0) {
+          raise4(SVP_DEV_TIMEOUT);
+          int armed = issued;
+#ifdef SVP_TEST_STALL_AFTER
+          armed = min(armed, SVP_TEST_STALL_AFTER);
+#endif
+          for (int q = c; q < armed; ++q)
+            (void)mbar_wait_drain(&inf.full[q % kStages4], (q / kStages4) & 1);
         }
-        const uint32_t st = kv0 + s * (kStagePages * 2 * S::PAGE);
-        const bool checked = sm.checked[s] != 0;  // warp-uniform
+        return;
+      }
+      const uint32_t st = kv0 + s * (kStagePages * 2 * PAGE);
+      const bool checked = inf.checked[s] != 0;  // warp-uniform
+      const int pages = inf.pages[s];
+#pragma unroll 1
+      for (int p0 = 0; p0 < pages; p0 += PJ) {
+        const uint32_t pair = st + p0 * (2 * PAGE);
+        float x[PJ][NT][4], y[PJ][NT][4];
 #pragma unroll
-        for (int p0 = 0; p0 < kStagePages; p0 += PJ) {
-          float x[PJ][NT][4], y[PJ][NT][4];
+        for (int j = 0; j < PJ; ++j)
+          page_scores<D, NT>(pair + j * 2 * PAGE + k_off, t, x[j], qb);
+        // ---- softmax with a lazy reference ----
+        float far = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < PJ; ++j)
-            page_scores<D, NT>(st + (p0 + j) * 2 * S::PAGE + k_off, t, x[j], qb);
-          // ---- softmax with a lazy reference ----
-          float far = -INFINITY;
+        for (int j = 0; j < PJ; ++j)
 #pragma unroll
-          for (int j = 0; j < PJ; ++j)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int e = 0; e < 4; ++e) {
+              y[j][nt][e] = fmaf(x[j][nt][e], qs[nt][e & 1], -ref[nt][e & 1]);
+              far = fmaxf(far, y[j][nt][e]);
+            }
+        unsigned keep[PJ];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                y[j][nt][e] = fmaf(x[j][nt][e], qs[nt][e & 1], -ref[nt][e & 1]);
-                far = fmaxf(far, y[j][nt][e]);
+        for (int j = 0; j < PJ; ++j) keep[j] = 0xfu;
+        if (checked || __any_sync(kFull, far > kRefSlack)) {
+          // masked keys score -inf; a row whose scores reach beyond the
+          // slack gets a new reference
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              uint32_t bits = ~0u;
+              int i = 0;
+              if (checked) {
+                i = min(row0 + nt * 8 + 2 * t + r, p.rows - 1) / p.group;
+                bits = row_tree_bits(p, ui.b, i);
               }
-          unsigned keep[PJ];
-#pragma unroll
-          for (int j = 0; j < PJ; ++j) keep[j] = 0xfu;
-          if (checked || __any_sync(kFull, far > kRefSlack)) {
-            // masked keys score -inf; a row whose scores reach beyond the
-            // slack gets a new reference
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                uint32_t bits = ~0u;
-                int i = 0;
-                if (checked) {
-                  i = min(row0 + nt * 8 + 2 * t + r, p.rows - 1) / p.group;
-                  bits = row_tree_bits(p, b, i);
-                }
-                float mx = -INFINITY;
-#pragma unroll
-                for (int j = 0; j < PJ; ++j)
-#pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    float z = x[j][nt][2 * h + r] * qs[nt][r];
-                    if (checked &&
-                        !key_visible(sm.j0[s][p0 + j] + fp4_key(g, h), t0 + i,
-                                     bits, t0, p.n_sink, p.window))
-                      z = -INFINITY;
-                    x[j][nt][2 * h + r] = z;
-                    mx = fmaxf(mx, z);
-                  }
-                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
-                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
-                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
-                const float to = fmaxf(ref[nt][r], mx - kRefOffset);
-                const float alpha = ex2(ref[nt][r] - to);
-                ref[nt][r] = to;
-                l[nt][r] *= alpha;
-#pragma unroll
-                for (int d2 = 0; d2 < D / 16; ++d2) {
-                  o[d2][nt][r] *= alpha;
-                  o[d2][nt][2 + r] *= alpha;
-                }
-#pragma unroll
-                for (int j = 0; j < PJ; ++j)
-#pragma unroll
-                  for (int h = 0; h < 2; ++h)
-                    y[j][nt][2 * h + r] = x[j][nt][2 * h + r] - to;
-              }
-            if (checked) {
+              float mx = -INFINITY;
 #pragma unroll
               for (int j = 0; j < PJ; ++j)
 #pragma unroll
-                for (int sx = 0; sx < 4; ++sx) {
-                  const int key = sm.j0[s][p0 + j] + 4 * t + sx;
-                  if (!(key < L && (p.window == 0 || key < p.n_sink ||
-                                    key > t0 - p.window)))
-                    keep[j] &= ~(1u << sx);
+                for (int h = 0; h < 2; ++h) {
+                  float z = x[j][nt][2 * h + r] * qs[nt][r];
+                  if (checked &&
+                      !key_visible(inf.j0[s][p0 + j] + fp4_key(g, h), t0 + i,
+                                   bits, t0, p.n_sink, p.window))
+                    z = -INFINITY;
+                  x[j][nt][2 * h + r] = z;
+                  mx = fmaxf(mx, z);
                 }
-            }
-          }
+              mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
+              const float to = fmaxf(ref[nt][r], mx - kRefOffset);
+              const float alpha = ex2(ref[nt][r] - to);
+              ref[nt][r] = to;
+              l[nt][r] *= alpha;
 #pragma unroll
-          for (int j = 0; j < PJ; ++j) {
-            uint32_t pb[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                y[j][nt][e] = ex2(y[j][nt][e]);
-                l[nt][e & 1] += y[j][nt][e];
+              for (int d2 = 0; d2 < D / 16; ++d2) {
+                o[d2][nt][r] *= alpha;
+                o[d2][nt][2 + r] *= alpha;
               }
-              pb[nt][0] = transpose8(pack_h2(y[j][nt][0], y[j][nt][1]));
-              pb[nt][1] = transpose8(pack_h2(y[j][nt][2], y[j][nt][3]));
+#pragma unroll
+              for (int j = 0; j < PJ; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  y[j][nt][2 * h + r] = x[j][nt][2 * h + r] - to;
             }
-            const uint32_t vp = st + ((p0 + j) * 2 + 1) * S::PAGE;
-            page_values<D, NT>(vp + v_off, vp + v_off_s, keep[j], pb, o);
+          if (checked) {
+#pragma unroll
+            for (int j = 0; j < PJ; ++j)
+#pragma unroll
+              for (int sx = 0; sx < 4; ++sx) {
+                const int key = inf.j0[s][p0 + j] + 4 * t + sx;
+                if (!(key < L && (p.window == 0 || key < p.n_sink ||
+                                  key > t0 - p.window)))
+                  keep[j] &= ~(1u << sx);
+              }
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.empty[s]);
-      }
-      c += n_stages;
-
-      // ---- this warp's states to shared memory ----
-      __syncwarp();  // its last reads of the Q fragments
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int j = 0; j < PJ; ++j) {
+          uint32_t pb[NT][2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float sum = l[nt][r];
-          sum += __shfl_xor_sync(kFull, sum, 4);
-          sum += __shfl_xor_sync(kFull, sum, 8);
-          sum += __shfl_xor_sync(kFull, sum, 16);
-          l[nt][r] = sum;
-        }
-      if constexpr (S::kQSmem) {
-        // the states overlie the Q fragments of every warp
-        if (!consumer_sync(&sm.epi, epi_phase, lane)) {
-          if (lane == 0) { raise4(SVP_DEV_TIMEOUT); sm.abort_flag = 1; }
-          break;
-        }
-      }
+          for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int row = nt * 8 + 2 * t + r;
-          if (g == 0) {
-            sm.red_m[warp][row] = l[nt][r] == 0.f ? -INFINITY : ref[nt][r];
-            sm.red_l[warp][row] = l[nt][r];
+            for (int e = 0; e < 4; ++e) {
+              y[j][nt][e] = ex2(y[j][nt][e]);
+              l[nt][e & 1] += y[j][nt][e];
+            }
+            pb[nt][0] = transpose8(pack_h2(y[j][nt][0], y[j][nt][1]));
+            pb[nt][1] = transpose8(pack_h2(y[j][nt][2], y[j][nt][3]));
           }
-          float *dst = &sm.u.o[warp][row][(D / 8) * g];
-#pragma unroll
-          for (int i = 0; i < D / 16; i += 2)
-            *reinterpret_cast<float4 *>(dst + 2 * i) =
-                make_float4(o[i][nt][r], o[i][nt][2 + r], o[i + 1][nt][r],
-                            o[i + 1][nt][2 + r]);
-        }
-
-      // ---- epilogue: merge the warps' states (as attention.cu) ----
-      if (p.early) pdl_wait();  // outputs are written from here on
-      if (!consumer_sync(&sm.epi, epi_phase, lane) || aborted) {
-        if (lane == 0) { raise4(SVP_DEV_TIMEOUT); sm.abort_flag = 1; }
-        break;
-      }
-      const bool single = ui.f == ui.l;
-      const size_t pslot = (size_t)(2 * blockIdx.x + ui.slot);
-      const int vrows = min(RB, p.rows - rg * RB);
-      if (tid < vrows) {
-        const int r = tid, w0 = r / RW, lr = r % RW;
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = w0; w < kWarps4; w += MT) M = fmaxf(M, sm.red_m[w][lr]);
-        float Lsum = 0.f;
-        float f[NSTREAM];
-#pragma unroll
-        for (int k = 0; k < NSTREAM; ++k) {
-          const float mw = sm.red_m[w0 + k * MT][lr];
-          f[k] = (mw == -INFINITY) ? 0.f : ex2(mw - M);
-          Lsum = fmaf(f[k], sm.red_l[w0 + k * MT][lr], Lsum);
-        }
-        const float inv = Lsum == 0.f ? 0.f : 1.f / Lsum;
-#pragma unroll
-        for (int k = 0; k < NSTREAM; ++k) sm.wf[w0 + k * MT][r] = f[k] * inv;
-        const float lse2 = Lsum == 0.f ? -INFINITY : M + log2f(Lsum);
-        const int gr = rg * RB + r;
-        if (single) {
-          const int i = gr / p.group;
-          const int h = kvh * p.group + gr % p.group;
-          p.lse[((size_t)b * p.q_len + i) * p.num_q_heads + h] = lse2 * kLn2;
-        } else {
-          p.part_lse[pslot * RB + r] = lse2;
+          const uint32_t vp = pair + (j * 2 + 1) * PAGE;
+          page_values<D, NT>(vp + v_off, vp + v_off_s, keep[j], pb, o);
         }
       }
-      if (!consumer_sync(&sm.epi, epi_phase, lane)) {
-        if (lane == 0) { raise4(SVP_DEV_TIMEOUT); sm.abort_flag = 1; }
-        break;
-      }
-      for (int e4 = tid; e4 < vrows * (D / 4); e4 += kWarps4 * 32) {
-        const int r = e4 / (D / 4), d = (e4 % (D / 4)) * 4;
-        const int w0 = r / RW, lr = r % RW;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < NSTREAM; ++k) {
-          const float f = sm.wf[w0 + k * MT][r];
-          const float4 v =
-              *reinterpret_cast<const float4 *>(&sm.u.o[w0 + k * MT][lr][d]);
-          a.x = fmaf(f, v.x, a.x);
-          a.y = fmaf(f, v.y, a.y);
-          a.z = fmaf(f, v.z, a.z);
-          a.w = fmaf(f, v.w, a.w);
-        }
-        a.x *= p.v_scale;
-        a.y *= p.v_scale;
-        a.z *= p.v_scale;
-        a.w *= p.v_scale;
-        if (single) {
-          const int gr = rg * RB + r;
-          const int i = gr / p.group;
-          const int h = kvh * p.group + gr % p.group;
-          uint16_t *dst = static_cast<uint16_t *>(p.out) +
-                          (((size_t)b * p.q_len + i) * p.num_q_heads + h) * D + d;
-          store_out(dst + 0, a.x);
-          store_out(dst + 1, a.y);
-          store_out(dst + 2, a.z);
-          store_out(dst + 3, a.w);
-        } else {
-          *reinterpret_cast<float4 *>(p.part_o + (pslot * RB + r) * D + d) = a;
-        }
-      }
-      if (!single && tid == 0) record_split(p, ui, blockIdx.x);
-      if (!consumer_sync(&sm.epi, epi_phase, lane)) {
-        if (lane == 0) { raise4(SVP_DEV_TIMEOUT); sm.abort_flag = 1; }
-        break;
-      }
-      if (tid == 0) mbar_arrive(&sm.uempty[slot]);
-      ++us;
+      __syncwarp();
+      issue();  // into the stage just read
     }
-  }
 
-  __syncthreads();  // no warp leaves while the others may use the barriers
+    // ---- the segment's result, from registers ----
+    if (p.early) pdl_wait();  // outputs are written from here on
+    const bool single = ui.f == ui.l;
+    if (slice == ui.f && lane == 0)
+      p.split[(ui.b * p.num_kv_heads + ui.g) * p.n_rg + ui.rg] =
+          make_int2(ui.f, ui.l);
+    const size_t part = (size_t)2 * slice + (slice == ui.f ? 1 : 0);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float sum = l[nt][r];
+        sum += __shfl_xor_sync(kFull, sum, 4);
+        sum += __shfl_xor_sync(kFull, sum, 8);
+        sum += __shfl_xor_sync(kFull, sum, 16);
+        const int lr = nt * 8 + 2 * t + r, gr = row0 + lr;
+        if (gr >= p.rows) continue;
+        const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
+        const float lse2 = sum == 0.f ? -INFINITY : ref[nt][r] + log2f(sum);
+        if (single) {
+          const int i = gr / p.group;
+          const int h = ui.g * p.group + gr % p.group;
+          const size_t row = ((size_t)ui.b * p.q_len + i) * p.num_q_heads + h;
+          if (g == 0) p.lse[row] = lse2 * kLn2;
+          uint4 *dst = reinterpret_cast<uint4 *>(
+              static_cast<uint16_t *>(p.out) + row * D + (D / 8) * g);
+#pragma unroll
+          for (int i4 = 0; i4 < D / 64; ++i4) {
+            uint32_t w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(
+                  o[4 * i4 + x][nt][r] * inv, o[4 * i4 + x][nt][2 + r] * inv);
+              w[x] = *reinterpret_cast<const uint32_t *>(&v);
+            }
+            dst[i4] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else {
+          if (g == 0) p.part_lse[part * RB + lr] = lse2;
+          float4 *dst = reinterpret_cast<float4 *>(
+              p.part_o + (part * RB + lr) * D + (D / 8) * g);
+#pragma unroll
+          for (int i4 = 0; i4 < D / 32; ++i4)
+            dst[i4] = make_float4(o[2 * i4][nt][r] * inv, o[2 * i4][nt][2 + r] * inv,
+                                  o[2 * i4 + 1][nt][r] * inv,
+                                  o[2 * i4 + 1][nt][2 + r] * inv);
+        }
+      }
+  }
+}
+
+// Joins the partials of the groups that slice borders cut: one CTA per group
+// and query row, its warps taking the group's slices in turn, eight loads in
+// flight each; the warps' states meet in shared memory in a fixed order.
+constexpr int kMergeWarps4 = 4;
+template <int D>
+__global__ void __launch_bounds__(32 * kMergeWarps4)
+    merge_fp4_kernel(const AttnParams p) {
+  constexpr int LPS = D / 4;       // lanes of a slice's row
+  constexpr int SPW = 32 / LPS;    // slices a warp takes at once
+  constexpr int STEP = kMergeWarps4 * SPW;
+  constexpr int UNROLL = 4;
+  __shared__ float sm_m[STEP], sm_w[STEP];
+  __shared__ float4 sm_o[STEP][LPS];
+  pdl_launch_dependents();
+  pdl_wait();  // launched early: the attention grid must have finished
+  const int group = blockIdx.x / p.merge_rows, lr = blockIdx.x % p.merge_rows;
+  const int rg = group % p.n_rg, g = (group / p.n_rg) % p.num_kv_heads;
+  const int b = group / (p.n_rg * p.num_kv_heads);
+  const int gr = rg * p.rb + lr;
+  const int L = p.seq_lens[b];
+  const int2 fl = p.split[group];
+  // nobody records a group of a sequence whose length is out of range, nor
+  // one whose slices gave up (a timeout): an unwritten record names anything,
+  // so it is followed only within the slots there are
+  if (gr >= p.rows || L < p.q_len || L > p.max_blocks * kBlockSize ||
+      fl.x < 0 || fl.y <= fl.x || fl.y >= p.slices)
+    return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int me = warp * SPW + lane / LPS, d4 = lane % LPS;
+  const int ns = fl.y - fl.x + 1;
+  float m = -INFINITY, w_sum = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = me; s0 < ns; s0 += STEP * UNROLL) {
+    float ls[UNROLL];
+    float4 v[UNROLL];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      const int s = s0 + u * STEP;
+      ls[u] = -INFINITY;
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s < ns) {
+        const size_t row =
+            ((size_t)2 * (fl.x + s) + (s == 0 ? 1 : 0)) * p.rb + lr;
+        ls[u] = p.part_lse[row];
+        v[u] = reinterpret_cast<const float4 *>(p.part_o)[row * LPS + d4];
+      }
+    }
+    float mn = m;
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) mn = fmaxf(mn, ls[u]);
+    if (mn == -INFINITY) continue;
+    const float sc = ex2(m - mn);
+    w_sum *= sc;
+    a.x *= sc; a.y *= sc; a.z *= sc; a.w *= sc;
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      const float w = ex2(ls[u] - mn);
+      w_sum += w;
+      a.x = fmaf(w, v[u].x, a.x);
+      a.y = fmaf(w, v[u].y, a.y);
+      a.z = fmaf(w, v[u].z, a.z);
+      a.w = fmaf(w, v[u].w, a.w);
+    }
+    m = mn;
+  }
+  sm_o[me][d4] = a;
+  if (d4 == 0) {
+    sm_m[me] = m;
+    sm_w[me] = w_sum;
+  }
+  __syncthreads();
+  if (threadIdx.x >= LPS) return;
+  float M = -INFINITY;
+#pragma unroll
+  for (int x = 0; x < STEP; ++x) M = fmaxf(M, sm_m[x]);
+  float total = 0.f;
+  a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int x = 0; x < STEP; ++x) {
+    const float w = sm_m[x] == -INFINITY ? 0.f : ex2(sm_m[x] - M);
+    const float4 v = sm_o[x][d4];
+    total = fmaf(w, sm_w[x], total);
+    a.x = fmaf(w, v.x, a.x);
+    a.y = fmaf(w, v.y, a.y);
+    a.z = fmaf(w, v.z, a.z);
+    a.w = fmaf(w, v.w, a.w);
+  }
+  const float inv = total == 0.f ? 0.f : 1.f / total;
+  const int i = gr / p.group, h = g * p.group + gr % p.group;
+  const size_t row = ((size_t)b * p.q_len + i) * p.num_q_heads + h;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * inv, a.y * inv);
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(a.z * inv, a.w * inv);
+  reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + row * D)[d4] =
+      make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
+                 *reinterpret_cast<const uint32_t *>(&hi));
+  if (d4 == 0)
+    p.lse[row] = total == 0.f ? -INFINITY : (M + log2f(total)) * kLn2;
 }
 
 // ---- host side ----
 
 std::mutex g_mu4;
-std::map<std::tuple<int, const void *, size_t>, int> g_occ4;
+std::map<std::tuple<int, const void *, size_t>, bool> g_ready4;
 
-template <int D, int NT, int MT>
+template <int D, int NT>
 size_t smem4(int batch) {
-  const size_t bucket = ((size_t)batch + 255) / 256 * 256;
-  return sizeof(Smem4<D, NT, MT>) + sizeof(int) * (2 * bucket + 1) + 128;
+  return sizeof(Smem4<D, warps4<NT>(), stages4<NT>()>) + sizeof(int) * 2 * (size_t)batch + 128;
 }
 
-// shared-memory attribute and occupancy, once per device and size; < 0 if
-// the runtime refuses
-template <int D, int NT, int MT>
-int prepare4(int batch) {
-  const size_t smem = smem4<D, NT, MT>(batch);
-  auto kern = paged_attention_fp4_kernel<D, NT, MT>;
+template <int D, int NT>
+cudaError_t launch4(AttnParams p, int grid, cudaStream_t st) {
+  p.slices = grid * warps4<NT>();
+  static_assert(sizeof(Smem4<D, warps4<NT>(), stages4<NT>()>) +
+                        sizeof(int) * 2 * kBatchFp4 + 128 <=
+                    232448,
+                "a CTA's shared memory");
+  auto kern = paged_attention_fp4_kernel<D, NT>;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
-  const auto key = std::make_tuple(dev, (const void *)kern, smem);
-  std::lock_guard<std::mutex> lk(g_mu4);
-  auto it = g_occ4.find(key);
-  if (it != g_occ4.end()) return it->second;
-  int n = 0;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem) != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, Shape4<NT>::THREADS, smem) !=
-          cudaSuccess)
-    return -1;
-  n = n > 0 ? n : 1;
-  g_occ4[key] = n;
-  return n;
-}
-
-#define SVP_DISPATCH4(CALL)                                   \
-  do {                                                        \
-    if (head_dim == 64) {                                     \
-      switch (rb) {                                           \
-        case 8: CALL(64, 1, 1); break;                        \
-        case 16: CALL(64, 2, 1); break;                       \
-        case 24: CALL(64, 3, 1); break;                       \
-        case 32: CALL(64, 4, 1); break;                       \
-        case 48: CALL(64, 3, 2); break;                       \
-        default: CALL(64, 4, 2); break;                       \
-      }                                                       \
-    } else {                                                  \
-      switch (rb) {                                           \
-        case 8: CALL(128, 1, 1); break;                       \
-        case 16: CALL(128, 2, 1); break;                      \
-        case 24: CALL(128, 3, 1); break;                      \
-        case 32: CALL(128, 4, 1); break;                      \
-        case 48: CALL(128, 3, 2); break;                      \
-        default: CALL(128, 4, 2); break;                      \
-      }                                                       \
-    }                                                         \
-  } while (0)
-
-template <int D, int NT, int MT>
-cudaError_t launch4(const AttnParams &p, int grid, cudaStream_t st) {
-  if (prepare4<D, NT, MT>(p.batch) < 0) return cudaErrorInvalidValue;
-  return launch_pdl(paged_attention_fp4_kernel<D, NT, MT>, (unsigned)grid,
-                    (unsigned)Shape4<NT>::THREADS, smem4<D, NT, MT>(p.batch), st, p);
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  // the largest request, once per device
+  const size_t most = smem4<D, NT>(kBatchFp4);
+  {
+    std::lock_guard<std::mutex> lk(g_mu4);
+    bool &ready = g_ready4[std::make_tuple(dev, (const void *)kern, most)];
+    if (!ready) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)most);
+      if (e != cudaSuccess) return e;
+      ready = true;
+    }
+  }
+  e = launch_pdl(kern, (unsigned)grid, 32u * warps4<NT>(), smem4<D, NT>(p.batch),
+                 st, p);
+  if (e != cudaSuccess) return e;
+  const long long blocks =
+      (long long)p.batch * p.num_kv_heads * p.n_rg * p.merge_rows;
+  return launch_pdl(merge_fp4_kernel<D>, (unsigned)blocks, 32u * kMergeWarps4, 0,
+                    st, p);
 }
 
 }  // namespace
 
+// Query rows of a unit: whole n8 tiles, at most three (24 rows); more rows
+// than that are dealt evenly to several units, each reading the pages again
+// (from L2: neighbouring units run close together).
 int attention_fp4_rows(int rows) {
-  for (int rb : {8, 16, 24, 32, 48, 64})
-    if (rows <= rb) return rb;
-  // several units per group, each reading the pages again: the fewest rows
-  // of padding, then the fewest units
-  const int r48 = (rows + 47) / 48 * 48, r64 = (rows + 63) / 64 * 64;
-  return r48 < r64 ? 48 : 64;
+  const int units = (rows + 23) / 24;
+  return ((rows + units - 1) / units + 7) / 8 * 8;
 }
 
-int attention_fp4_ctas_per_sm(int head_dim, int rb, int batch) {
-  int n = 1;
-#define SVP_CALL(D, NT, MT) n = prepare4<D, NT, MT>(batch)
-  SVP_DISPATCH4(SVP_CALL);
-#undef SVP_CALL
-  return n > 0 ? n : 1;
-}
+int attention_fp4_warps(int rb) { return rb <= 8 ? warps4<1>() : warps4<2>(); }
 
 cudaError_t launch_attention_fp4(const AttnParams &p, int grid,
                                  cudaStream_t stream) {
-  const int head_dim = p.head_dim, rb = p.rb;
-  cudaError_t e = cudaSuccess;
-#define SVP_CALL(D, NT, MT) e = launch4<D, NT, MT>(p, grid, stream)
-  SVP_DISPATCH4(SVP_CALL);
-#undef SVP_CALL
-  return e;
+  const bool d64 = p.head_dim == 64;
+  switch (p.rb) {
+    case 8: return d64 ? launch4<64, 1>(p, grid, stream) : launch4<128, 1>(p, grid, stream);
+    case 16: return d64 ? launch4<64, 2>(p, grid, stream) : launch4<128, 2>(p, grid, stream);
+    default: return d64 ? launch4<64, 3>(p, grid, stream) : launch4<128, 3>(p, grid, stream);
+  }
 }
 
 cudaError_t read_status_attention_fp4(cudaStream_t s, unsigned *flags) {

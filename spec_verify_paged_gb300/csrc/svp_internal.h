@@ -26,6 +26,9 @@ struct AttnParams {
   float *lse;
   // workspace pieces
   struct SplitDesc *desc;  // [grid] split group whose first page a CTA owns
+  int2 *split;         // 4-bit kernel: [groups] first and last slice
+  int merge_rows;      // 4-bit kernel: query rows the merge walks per group
+  int slices;          // 4-bit kernel: set by its launcher, the partials' bound
   float *part_o;       // [2 * grid][RB][D] normalised partials: each CTA's
                        // first- and last-segment slot
   float *part_lse;     // [2 * grid][RB] log2-domain LSE of the partials
@@ -87,10 +90,12 @@ constexpr int kSegItemsTc = 2;
 // counted as this many pages.
 constexpr int kSegItemsCc = 12;
 
-// The 4-bit kernel's items are the two pages of a stage; a segment's
-// epilogue counts as this many.
-constexpr int kTilePagesFp4 = 2;
-constexpr int kSegItemsFp4 = 8;
+// The 4-bit kernel's items are the four pages of a stage; a segment's fixed
+// cost (Q, the result) counts as one.  At most kBatchFp4 sequences per
+// launch: their prefix shares shared memory with the page ring.
+constexpr int kTilePagesFp4 = 4;
+constexpr int kSegItemsFp4 = 1;
+constexpr int kBatchFp4 = 512;
 
 // Query rows per kv head (GQA group x q_len) from which the automatic path
 // choice uses tensor cores (bf16 only): tcgen05 for head_dim 128, warp-level
@@ -119,11 +124,11 @@ int attention_tc_ctas_per_sm(int rb, int batch);
 cudaError_t launch_attention_tc(const AttnParams &p, int grid,
                                 cudaStream_t stream);
 
-// The 4-bit cache kernel (attention_fp4.cu): the unit's row count (8, 16,
-// 24, 32, 48 or 64) for this many query rows per kv head, its CTAs per SM
-// and its launch (at most 4096 sequences).
+// The 4-bit cache kernels (attention_fp4.cu): the unit's row count (8, 16
+// or 24) for this many query rows per kv head, the warps (slices) of a CTA,
+// of which an SM holds one, and the launch of attention and merge.
 int attention_fp4_rows(int rows);
-int attention_fp4_ctas_per_sm(int head_dim, int rb, int batch);
+int attention_fp4_warps(int rb);
 cudaError_t launch_attention_fp4(const AttnParams &p, int grid,
                                  cudaStream_t stream);
 
