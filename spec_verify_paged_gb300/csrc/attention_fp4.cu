@@ -71,6 +71,7 @@ template <int NT>
 __host__ __device__ constexpr int stages4() {
   return NT == 1 ? 2 : 3;
 }
+constexpr int kChecked = 256;
 constexpr int kSegRing4 = 8;  // decoded segments: read .. issued + 1
 
 // A run of pages of one group within a slice.
@@ -80,6 +81,10 @@ struct Seg4 {
   int f, l;    // slices that hold the group's first and last page
   int next;    // flat item after the run
   int valid;
+  // pages that end by t_min (the unit's first position; with a tree: before
+  // its nodes) and, under a window, lie in that of t_max (its last position)
+  // need no per-key test
+  int t_min, t_max;
 };
 
 template <int D, int STAGES>
@@ -92,8 +97,7 @@ template <int STAGES>
 struct Info4 {
   uint64_t full[STAGES];
   int j0[STAGES][kStagePages];
-  int checked[STAGES];  // the stage's keys need the visibility test
-  int pages[STAGES];
+  int meta[STAGES];  // pages; + kChecked: their keys need the visibility test
   Seg4 seg[kSegRing4];
 };
 template <int D, int W, int STAGES>
@@ -129,6 +133,45 @@ __device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
+}
+
+__device__ __forceinline__ void sts32(uint32_t a, int v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .b64 st;\n\t"
+      "mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_to(uint32_t dst, const void *src,
+                                        uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ bool mbar_try_at(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Waits (bounded) for the phase; the same answer in every lane.
+__device__ __forceinline__ bool mbar_wait_at(uint32_t bar, uint32_t parity) {
+  if (__all_sync(kFull, mbar_try_at(bar, parity))) return true;
+  const uint64_t start = globaltimer();
+  bool ok = false;
+  while (!(ok = mbar_try_at(bar, parity)) && globaltimer() - start <= SVP_WAIT_NS) {
+  }
+  return __all_sync(kFull, ok);
 }
 
 // Dims of k-step ks, lane t: four from q_dim on.  A lane's steps cover D/4
@@ -168,11 +211,7 @@ __device__ __forceinline__ void page_scores(uint32_t kp, int t,
       sc[h][0] = e4m3x2_f16x2(lds_u8(at) * 0x101u);
     }
   }
-  float odd[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+  float odd[4];
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -189,7 +228,11 @@ __device__ __forceinline__ void page_scores(uint32_t kp, int t,
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const uint2 b = qb(4 * c + 2 * hw + i, nt);
-          mma_f16(NT == 1 && i ? odd : s[nt], a, b.x, b.y);
+          float (&to)[4] = NT == 1 && i ? odd : s[nt];
+          if (c == 0 && hw == 0 && (NT == 1 || i == 0))
+            mma_f16_first(to, a, b.x, b.y);
+          else
+            mma_f16(to, a, b.x, b.y);
         }
       }
     }
@@ -261,7 +304,7 @@ __device__ __forceinline__ Seg4 next_segment(const AttnParams &p,
                                              const int *prefix,
                                              const int *seqlen, int per_seq,
                                              int pos, int end, int total,
-                                             int n_slices) {
+                                             int n_slices, int rb) {
   Seg4 s;
   s.valid = 0;
   if (pos >= end) return s;
@@ -291,6 +334,9 @@ __device__ __forceinline__ Seg4 next_segment(const AttnParams &p,
   s.l = div_u64((unsigned long long)(first + nt) * (unsigned)n_slices - 1u,
                 (unsigned)total);
   s.valid = s.n_pages > 0;
+  const int base = s.L - p.q_len;
+  s.t_min = p.tree_mask ? base - 1 : base + s.rg * rb / p.group;
+  s.t_max = base + (min(s.rg * rb + rb, p.rows) - 1) / p.group;
   return s;
 }
 
@@ -334,9 +380,12 @@ __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
   // its first block-table entries are on their way. ----
   bool waited = !p.early;  // the grid-dependency wait is behind us
   int issued = 0, seg_i = 0, k = 0;
+  // of the segment being issued: its pages, the flat page number from which
+  // sinks are skipped and by how much, its first page, head, limits
+  int n_pages = 0, page0 = 0, n_a = 0, skip = 0, kvh = 0, t_min = 0, t_max = 0;
   auto decode = [&](int i, int pos) {  // segment i of this slice, into the ring
     const Seg4 s = next_segment(p, sm.prefix, seqlen, per_seq, pos, end, total,
-                                n_slices);
+                                n_slices, RB);
     if (lane == 0) inf.seg[i % kSegRing4] = s;
     __syncwarp();
   };
@@ -347,85 +396,101 @@ __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
     const int lb = pidx < s.n_a ? pidx : s.b_start + (pidx - s.n_a);
     return __ldg(p.block_table + (size_t)s.b * p.max_blocks + lb);
   };
+  auto take_up = [&]() {  // the state of segment seg_i
+    const Seg4 &s = inf.seg[seg_i % kSegRing4];
+    n_pages = s.valid ? s.n_pages : 0;
+    page0 = s.page0;
+    n_a = s.n_a;
+    skip = s.b_start - n_a;
+    kvh = s.g;
+    t_min = s.t_min;
+    t_max = s.t_max;
+    k = 0;
+  };
+  // a block-table entry as the number of its head's page, -1 for a bad one
+  auto head_page = [&](int ph, int page) {
+    if (page >= n_pages) return -1;
+    if (ph >= 0 && ph < p.num_blocks) return ph * p.num_kv_heads + kvh;
+    raise4(SVP_DEV_BAD_BLOCK_ID);
+    return -1;
+  };
   decode(0, slice_begin(slice, total, n_slices));
-  // entries of pages k .. k + 31, of the 32 after them, and of the following
-  // segment's first 32
+  take_up();
+  // entries of pages k .. k + 31 (as head pages), of the 32 after them, and
+  // of the following segment's first 32
   int phys = entry(0, lane), phys2 = entry(0, 32 + lane);
-  decode(1, inf.seg[0].valid ? inf.seg[0].next : end);
+  decode(1, n_pages ? inf.seg[0].next : end);
   int phys_a = entry(1, lane);
+  phys = head_page(phys, lane);
+  const uint32_t bars = smem_u32(&inf.full[0]), metas = smem_u32(&inf.meta[0]);
+  const uint32_t j0s = smem_u32(&inf.j0[0][0]);
+  const uint32_t kv0 = smem_u32(&sm.warp[warp].kv[0][0][0][0]);
+  // lane 2 x + side issues page x's copy of that side
+  const unsigned char *const cache =
+      static_cast<const unsigned char *>(lane & 1 ? p.v_cache : p.k_cache);
   auto issue = [&]() {
-    const Seg4 &cur = inf.seg[seg_i % kSegRing4];
-    if (!cur.valid) return;
+    if (k >= n_pages) return;  // nothing left (uniform)
     const int st = issued % kStages4;
-    const int n_pages = cur.n_pages, page0 = cur.page0, n_a = cur.n_a;
-    const int skip = cur.b_start - n_a, kvh = cur.g, base = cur.L - p.q_len;
-    const int row0 = cur.rg * RB;
-    auto block = [&](int pidx) { return pidx < n_a ? pidx : pidx + skip; };
     const int n = min(kStagePages, n_pages - k);
-    if (!waited && (block(page0 + k + n - 1) + 1) * kBlockSize > base) {
-      pdl_wait();  // a page may hold some of the appended positions
-      waited = true;
+    const int last = page0 + k + ((n + 1) & ~1) - 1;  // of the last pair
+    if (!waited) {
+      const int pl = page0 + k + n - 1;
+      if (((pl < n_a ? pl : pl + skip) + 1) * kBlockSize >
+          inf.seg[seg_i % kSegRing4].L - p.q_len) {
+        pdl_wait();  // a page may hold some of the appended positions
+        waited = true;
+      }
     }
-    // lane 2 x + side: page x's copy of that side
-    const int x = lane >> 1, side = lane & 1;
-    const int ph = __shfl_sync(kFull, phys, ((k & 31) + x) & 31);
-    const bool here = lane < 2 * kStagePages && x < n;
-    const bool good = here && ph >= 0 && ph < p.num_blocks;
-    if (here && !good && side == 0) raise4(SVP_DEV_BAD_BLOCK_ID);
-    const int j0 = good ? block(page0 + k + x) * kBlockSize : kNoPage;
-    // pages that end by the unit's first position (with a tree: before its
-    // nodes) and lie in its last one's window need no per-key test
-    const int t_min = p.tree_mask ? base - 1 : base + row0 / p.group;
-    const int t_max = base + (min(row0 + RB, p.rows) - 1) / p.group;
-    const int j1 = j0 + kBlockSize - 1;
-    const bool clear = j1 <= t_min && (p.window == 0 || j1 < p.n_sink ||
-                                       j0 > t_max - p.window);
+    const int x = lane >> 1;
+    const int hp = __shfl_sync(kFull, phys, (k + x) & 31);
+    const bool good = lane < 2 * n && hp >= 0;
     const unsigned copies = __ballot_sync(kFull, good);
-    const bool test = __any_sync(kFull, !clear && x < ((n + 1) & ~1));
-    if (lane < 2 * kStagePages && side == 0) inf.j0[st][x] = j0;
+    const int pidx = page0 + k + x;
+    int j0 = (pidx < n_a ? pidx : pidx + skip) * kBlockSize;
+    if (!good) j0 = kNoPage;
+    bool test = __popc(copies) != 2 * n;
+    if (p.window == 0) {
+      test = test || last * kBlockSize + kBlockSize - 1 > t_min;
+    } else {
+      const int j1 = j0 + kBlockSize - 1;
+      const bool clear =
+          j1 <= t_min && (j1 < p.n_sink || j0 > t_max - p.window);
+      test = __any_sync(kFull, !clear && x < ((n + 1) & ~1));
+    }
+    if ((lane & 1) == 0 && lane < 2 * kStagePages)
+      sts32(j0s + (st * kStagePages + x) * 4, j0);
     if (lane == 0) {
-      inf.checked[st] = test;
-      inf.pages[st] = n;
+      sts32(metas + st * 4, n + (test ? kChecked : 0));
 #ifdef SVP_TEST_STALL_AFTER
       // test builds only: later stages never arrive, so the waits run out
       if (issued < SVP_TEST_STALL_AFTER)
 #endif
-      {
-        if (copies)
-          mbar_arrive_expect_tx(&inf.full[st], __popc(copies) * PAGE);
-        else
-          mbar_arrive(&inf.full[st]);
-      }
+        mbar_expect(bars + st * 8, __popc(copies) * PAGE);
     }
     __syncwarp();
 #ifdef SVP_TEST_STALL_AFTER
     if (issued < SVP_TEST_STALL_AFTER)
 #endif
-    if (good) {
-      const size_t off = ((size_t)ph * p.num_kv_heads + kvh) * (size_t)PAGE;
-      bulk_g2s(sm.warp[warp].kv[st][x][side],
-               static_cast<const unsigned char *>(side ? p.v_cache : p.k_cache) + off,
-               PAGE, &inf.full[st]);
-    }
+    if (good)
+      bulk_to(kv0 + (st * kStagePages * 2 + lane) * PAGE,
+              cache + (size_t)(unsigned)hp * PAGE, PAGE, bars + st * 8);
     ++issued;
     k += n;
     if (k >= n_pages) {
-      k = 0;
       ++seg_i;
-      phys = phys_a;
+      take_up();
+      phys = head_page(phys_a, lane);
       phys2 = entry(seg_i, 32 + lane);
-      const Seg4 &now = inf.seg[seg_i % kSegRing4];
-      decode(seg_i + 1, now.valid ? now.next : end);
+      decode(seg_i + 1, n_pages ? inf.seg[seg_i % kSegRing4].next : end);
       phys_a = entry(seg_i + 1, lane);
     } else if ((k & 31) == 0) {
-      phys = phys2;
+      phys = head_page(phys2, k + lane);
       phys2 = entry(seg_i, k + 32 + lane);
     }
   };
   for (int s = 0; s < kStages4; ++s) issue();
 
   // ---- the reading side ----
-  const uint32_t kv0 = smem_u32(&sm.warp[warp].kv[0][0][0][0]);
   const uint32_t k_off = k_lane<D>(g, t), v_off = v_lane<D>(g, t);
   const uint32_t v_off_s = v_lane_scale<D>(g, t);
   int c = 0;  // stages read
@@ -494,7 +559,7 @@ __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
 
     for (int k1 = 0; k1 < ui.n_pages; k1 += kStagePages, ++c) {
       const int s = c % kStages4;
-      if (!__all_sync(kFull, mbar_wait(&inf.full[s], (c / kStages4) & 1))) {
+      if (!mbar_wait_at(bars + s * 8, (c / kStages4) & 1)) {
         // give up: flag it, wait (bounded) for the copies still in flight
         if (lane == 0) {
           raise4(SVP_DEV_TIMEOUT);
@@ -508,8 +573,9 @@ __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
         return;
       }
       const uint32_t st = kv0 + s * (kStagePages * 2 * PAGE);
-      const bool checked = inf.checked[s] != 0;  // warp-uniform
-      const int pages = inf.pages[s];
+      const int meta = (int)lds32(metas + s * 4);  // warp-uniform
+      const bool checked = meta >= kChecked;
+      const int pages = meta & (kChecked - 1);
 #pragma unroll 1
       for (int p0 = 0; p0 < pages; p0 += PJ) {
         const uint32_t pair = st + p0 * (2 * PAGE);
@@ -551,7 +617,7 @@ __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
                 for (int h = 0; h < 2; ++h) {
                   float z = x[j][nt][2 * h + r] * qs[nt][r];
                   if (checked &&
-                      !key_visible(inf.j0[s][p0 + j] + fp4_key(g, h), t0 + i,
+                      !key_visible((int)lds32(j0s + (s * kStagePages + p0 + j) * 4) + fp4_key(g, h), t0 + i,
                                    bits, t0, p.n_sink, p.window))
                     z = -INFINITY;
                   x[j][nt][2 * h + r] = z;
@@ -580,7 +646,7 @@ __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
             for (int j = 0; j < PJ; ++j)
 #pragma unroll
               for (int sx = 0; sx < 4; ++sx) {
-                const int key = inf.j0[s][p0 + j] + 4 * t + sx;
+                const int key = (int)lds32(j0s + (s * kStagePages + p0 + j) * 4) + 4 * t + sx;
                 if (!(key < L && (p.window == 0 || key < p.n_sink ||
                                   key > t0 - p.window)))
                   keep[j] &= ~(1u << sx);
