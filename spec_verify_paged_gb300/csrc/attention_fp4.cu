@@ -868,13 +868,11 @@ cudaError_t launch4(AttnParams p, int grid, cudaStream_t st) {
 
 }  // namespace
 
-// Query rows of a unit: whole n8 tiles, at most three (24 rows); more rows
-// than that are dealt evenly to several units, each reading the pages again
-// (from L2: neighbouring units run close together).
-int attention_fp4_rows(int rows) {
-  const int units = (rows + 23) / 24;
-  return ((rows + units - 1) / units + 7) / 8 * 8;
-}
+// Query rows of a unit: one or two n8 tiles; more rows are dealt to several
+// units, each reading the pages again (from L2: neighbouring units run close
+// together).  A third tile per unit was slower (20 rows: 70 us against 68 on
+// 98 MB of cache; 60 rows: 143 against 122), its accumulators spill.
+int attention_fp4_rows(int rows) { return rows <= 8 ? 8 : 16; }
 
 int attention_fp4_warps(int rb) { return rb <= 8 ? warps4<1>() : warps4<2>(); }
 
@@ -883,8 +881,7 @@ cudaError_t launch_attention_fp4(const AttnParams &p, int grid,
   const bool d64 = p.head_dim == 64;
   switch (p.rb) {
     case 8: return d64 ? launch4<64, 1>(p, grid, stream) : launch4<128, 1>(p, grid, stream);
-    case 16: return d64 ? launch4<64, 2>(p, grid, stream) : launch4<128, 2>(p, grid, stream);
-    default: return d64 ? launch4<64, 3>(p, grid, stream) : launch4<128, 3>(p, grid, stream);
+    default: return d64 ? launch4<64, 2>(p, grid, stream) : launch4<128, 2>(p, grid, stream);
   }
 }
 

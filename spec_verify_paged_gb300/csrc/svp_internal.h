@@ -124,8 +124,8 @@ int attention_tc_ctas_per_sm(int rb, int batch);
 cudaError_t launch_attention_tc(const AttnParams &p, int grid,
                                 cudaStream_t stream);
 
-// The 4-bit cache kernels (attention_fp4.cu): the unit's row count (8, 16
-// or 24) for this many query rows per kv head, the warps (slices) of a CTA,
+// The 4-bit cache kernels (attention_fp4.cu): the unit's row count (8 or
+// 16) for this many query rows per kv head, the warps (slices) of a CTA,
 // of which an SM holds one, and the launch of attention and merge.
 int attention_fp4_rows(int rows);
 int attention_fp4_warps(int rb);
