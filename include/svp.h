@@ -280,7 +280,8 @@ int kv_append(const svp_dims *dims, const void *k_new, const void *v_new,
  * caches.  A sequence length outside [0, max_blocks_per_seq*16] gives zero
  * rows and SVP_DEV_BAD_SEQ_LEN, a bad block id a zero row and
  * SVP_DEV_BAD_BLOCK_ID.  Uses no workspace.
- * Errors as for kv_append, with n_rows in [0, 2^31). */
+ * Errors as for kv_append, with n_rows >= 0 and n_rows * num_kv_heads below
+ * 2^31 (else SVP_ERR_UNSUPPORTED). */
 int kv_gather(const svp_dims *dims, const void *k_cache, const void *v_cache,
               const int32_t *block_table, const int32_t *seq_lens,
               const int32_t *starts, int n_rows, void *k_out, void *v_out,
@@ -340,8 +341,8 @@ int paged_score_update(const svp_dims *dims, const void *q,
  * kept all -1 and SVP_DEV_BAD_SEQ_LEN; a row on a bad page id is not moved
  * (score read as -inf), with SVP_DEV_BAD_BLOCK_ID.  Two launches, no
  * workspace; deterministic.
- * Errors: SVP_ERR_INVALID_ARG for null pointers, misaligned caches (16
- * bytes) or scores (4), budget < 1, n_sink < 0, n_recent < 0, n_sink +
+ * Errors: SVP_ERR_INVALID_ARG for null pointers, caches or scores not
+ * 16-byte aligned, budget < 1, n_sink < 0, n_recent < 0, n_sink +
  * n_recent > budget, budget > 16 * the destination's blocks per sequence;
  * SVP_ERR_UNSUPPORTED as for kv_append and for max_blocks_per_seq >
  * 2^26. */

@@ -471,9 +471,8 @@ int kv_gather(const svp_dims *dims, const void *k_cache, const void *v_cache,
        reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) %
           16 != 0)
     return SVP_ERR_INVALID_ARG;
-  // the largest grid, in blocks of 256 lanes of 16 output bytes
-  const long long rows = (long long)dims->batch * n_rows;
-  if (rows > (1LL << 38) / ((long long)dims->num_kv_heads * dims->head_dim))
+  // rows of a sequence are counted in 32 bits
+  if ((long long)n_rows * dims->num_kv_heads >= (1LL << 31))
     return SVP_ERR_UNSUPPORTED;
   GatherParams p;
   p.k_cache = k_cache;
@@ -580,8 +579,8 @@ int kv_evict(const svp_dims *dims, void *k_cache, void *v_cache, float *scores,
       dst_block_table ? dst_max_blocks : dims->max_blocks_per_seq;
   if (budget > (long long)dst_blocks * kBlockSize) return SVP_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(k_cache) |
-       reinterpret_cast<uintptr_t>(v_cache)) % 16 != 0 ||
-      reinterpret_cast<uintptr_t>(scores) % 4 != 0)
+       reinterpret_cast<uintptr_t>(v_cache) |
+       reinterpret_cast<uintptr_t>(scores)) % 16 != 0)
     return SVP_ERR_INVALID_ARG;
   const int sms = device_sms();
   if (sms <= 0) return SVP_ERR_CUDA;

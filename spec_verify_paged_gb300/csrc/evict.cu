@@ -11,10 +11,9 @@
 //    CTA they are read again each pass).  The histograms are added across
 //    the cluster through distributed shared memory.  Bound by one read of
 //    the scores and, for short contexts, by the chain of passes.
-//  * compact_kernel: moves the kept rows of K, V and the scores.  Kept
-//    positions are increasing, so slot i never lies after its source: with
-//    all loads of a batch of rows before its stores, and batches in order,
-//    the move is safe in place.  Bound by the moved bytes, read and written.
+//  * compact_kernel: moves the kept rows of K, V and the scores, every warp
+//    a run of rows (in place: of columns) of one group by itself.  Bound by
+//    the moved bytes, read and written.
 #include <cooperative_groups.h>
 
 #include <cstdint>
@@ -36,7 +35,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048;
 
 struct SelShared {
-  unsigned hist[2][kBins];
+  alignas(16) unsigned hist[2][kBins];
   unsigned long long warp_sum[kSelThreads / 32];
   unsigned long long total;       // this CTA's kept-for-sure and tied counts
   unsigned bin, above;
@@ -94,37 +93,66 @@ __global__ void __launch_bounds__(kSelThreads)
       kept[i] = !bad && i < L ? i : -1;
     return;
   }
-  // this CTA's positions [lo, hi), thread's run of `run` of them: odd, so
-  // that a warp's runs start in different banks
-  const int per = (L + nc - 1) / nc;
+  // this CTA's positions [lo, hi): whole pages; a thread's run of `run` of
+  // them: odd, so that a warp's runs start in different banks
+  const int per = ((L + nc - 1) / nc + kBlockSize - 1) / kBlockSize * kBlockSize;
   const int lo = min(rank * per, L), hi = min(lo + per, L);
   const int run = ((per + kSelThreads - 1) / kSelThreads) | 1;
   const bool cached = per <= cache_cap;
   const int mid0 = p.n_sink, mid1 = L - p.n_recent;  // the candidates
   const int32_t *const table = p.block_table + (size_t)b * p.max_blocks;
-  auto load_key = [&](int j) {
+  // where position j's page keeps this head's scores, or null
+  auto page_scores = [&](int j) -> const float * {
     const int phys = __ldg(table + j / kBlockSize);
     if (phys < 0 || phys >= p.num_blocks) {
       atomicOr(&g_status_evict, (unsigned)SVP_DEV_BAD_BLOCK_ID);
-      return score_key(-INFINITY);
+      return nullptr;
     }
-    return score_key(p.scores[((size_t)phys * p.num_kv_heads + g) * kBlockSize +
-                              j % kBlockSize]);
+    return p.scores + ((size_t)phys * p.num_kv_heads + g) * kBlockSize;
   };
-  auto key_of = [&](int j) { return cached ? keys[j - lo] : load_key(j); };
+  auto key_of = [&](int j) {
+    if (cached) return keys[j - lo];
+    const float *at = page_scores(j);
+    return score_key(at ? at[j % kBlockSize] : -INFINITY);
+  };
 
   // ---- the k-th largest candidate ----
   const unsigned k = (unsigned)(p.budget - p.n_sink - p.n_recent);
   unsigned need = k;       // candidates still to take among those that match
   unsigned prefix = 0;     // the threshold's bits found so far
-  for (int i = tid; i < 2 * kBins; i += kSelThreads) (&sm.hist[0][0])[i] = 0;
+  for (int i = tid; i < 2 * kBins / 4; i += kSelThreads)
+    reinterpret_cast<uint4 *>(&sm.hist[0][0])[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
   if (cached) {
-#pragma unroll 4
-    for (int j = lo + tid; j < hi; j += kSelThreads) {
-      const unsigned key = load_key(j);
-      keys[j - lo] = key;
-      if (j >= mid0 && j < mid1) atomicAdd(&sm.hist[0][key >> 21], 1u);
+    // four positions of a page at a time, all loads of up to 16 in flight
+    constexpr int U = 4;
+    for (int q0 = lo / 4 + tid; q0 * 4 < hi; q0 += U * kSelThreads) {
+      const float *at[U];
+      float4 v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = (q0 + u * kSelThreads) * 4;
+        at[u] = j < hi ? page_scores(j) : nullptr;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = (q0 + u * kSelThreads) * 4;
+        v[u] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (at[u]) v[u] = *reinterpret_cast<const float4 *>(at[u] + j % kBlockSize);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = (q0 + u * kSelThreads) * 4;
+        if (j >= hi) continue;
+        const unsigned key[4] = {score_key(v[u].x), score_key(v[u].y),
+                                 score_key(v[u].z), score_key(v[u].w)};
+        *reinterpret_cast<uint4 *>(keys + (j - lo)) =
+            make_uint4(key[0], key[1], key[2], key[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (j + e >= mid0 && j + e < min(mid1, hi))
+            atomicAdd(&sm.hist[0][key[e] >> 21], 1u);
+      }
     }
   }
 #pragma unroll 1
@@ -141,16 +169,28 @@ __global__ void __launch_bounds__(kSelThreads)
     }
     if (nc > 1) cluster.sync(); else __syncthreads();
     // bins from the largest down, four per thread, summed over the cluster
-    unsigned c[4], mine = 0;
-    const int top = (1 << bits) - 1 - 4 * tid;  // this thread: top .. top - 3
+    // (one 16-byte read of every CTA, all in flight)
+    const int quad = (1 << bits) / 4 - 1 - tid;  // this thread's four bins
+    uint4 q4 = make_uint4(0, 0, 0, 0);
+    if (quad >= 0) {
+      uint4 part[kMaxCluster];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      c[i] = 0;
-      if (top - i >= 0)
-        for (int r = 0; r < nc; ++r)
-          c[i] += nc > 1 ? cluster.map_shared_rank(hist, r)[top - i] : hist[top - i];
-      mine += c[i];
+      for (int r = 0; r < kMaxCluster; ++r) {
+        part[r] = make_uint4(0, 0, 0, 0);
+        if (r < nc)
+          part[r] = reinterpret_cast<const uint4 *>(
+              nc > 1 ? cluster.map_shared_rank(hist, r) : hist)[quad];
+      }
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        q4.x += part[r].x;
+        q4.y += part[r].y;
+        q4.z += part[r].z;
+        q4.w += part[r].w;
+      }
     }
+    const unsigned c[4] = {q4.w, q4.z, q4.y, q4.x};
+    const unsigned mine = c[0] + c[1] + c[2] + c[3];
     unsigned all;
     unsigned above = block_scan<unsigned>(
         mine, reinterpret_cast<unsigned *>(sm.warp_sum), all);
@@ -158,7 +198,7 @@ __global__ void __launch_bounds__(kSelThreads)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (above < need && above + c[i] >= need) {
-          sm.bin = (unsigned)(top - i);
+          sm.bin = (unsigned)(4 * quad + 3 - i);
           sm.above = above;
           above = need;  // found
         } else {
@@ -170,15 +210,13 @@ __global__ void __launch_bounds__(kSelThreads)
       sm.bin = (1u << bits) - 1u;
       sm.above = 0;
     }
+    // the first histogram is free (its readers passed the barrier above) and
+    // serves the last pass
+    if (pass == 1)
+      reinterpret_cast<uint4 *>(sm.hist[0])[tid] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     prefix |= sm.bin << shift;
     need -= sm.above;
-    // the other histogram is free (its readers passed the barrier above)
-    // and is counted into after the next clearing
-    unsigned *const next = sm.hist[(pass & 1) ^ 1];
-    if (pass == 1)
-      for (int i = tid; i < kBins; i += kSelThreads) next[i] = 0;
-    __syncthreads();
   }
   // kept: keys above `prefix`, and the first `need` of those equal to it
 
@@ -214,104 +252,145 @@ __global__ void __launch_bounds__(kSelThreads)
 }
 
 // ---- the move ----
-constexpr int kMoveThreads = 256;
-constexpr int kMoveUnroll = 8;
+constexpr int kMoveWarps = 8;
+constexpr int kMoveRows = 128;  // rows whose addresses a warp works out at once
 
-// Rows of `units` vectors of type V.  Side 0: K, 1: V (blockIdx.y), in
-// `splits` parts; side 2: the scores, as rows of one 4-byte unit.
-template <typename V>
-__device__ __forceinline__ void move_rows(const EvictParams &p, char *data,
-                                          int units, int b, int g, int part,
-                                          int parts, long long *src_row,
-                                          long long *dst_row) {
-  const int tid = threadIdx.x;
-  const int group = b * p.num_kv_heads + g;
-  const int32_t *const kept = p.kept + (size_t)group * p.budget;
+// The kept rows slot0 .. slot1 - 1 of one (sequence, head): NU vectors of
+// type V each, from vector u0 of rows of `units` vectors.  One warp: it reads
+// 128 rows' positions and pages, then copies in batches of up to 18 vectors
+// per lane, every batch read before it is written.  Slot i's source is row i
+// or a later one, so no batch writes what a later one reads: safe in place.
+template <typename V, int NU>
+__device__ __forceinline__ void move_rows(const EvictParams &p, V *data,
+                                          int units, int u0, int b, int g,
+                                          int slot0, int slot1, long long *from,
+                                          long long *to) {
+  const int lane = threadIdx.x & 31;
+  const int32_t *const kept =
+      p.kept + (size_t)(b * p.num_kv_heads + g) * p.budget;
   const int32_t *const table = p.block_table + (size_t)b * p.max_blocks;
   const int32_t *const dtable = p.dst_table + (size_t)b * p.dst_blocks;
-  // a sequence is compacted in place iff its first destination page is its
-  // first source page; its parts then take columns instead of rows, so that
-  // no part writes what another has still to read
-  const bool in_place = dtable[0] == table[0];
-  int r0 = 0, r1 = p.budget, u0 = 0, u1 = units;
-  if (in_place) {
-    u0 = units * part / parts;
-    u1 = units * (part + 1) / parts;
-  } else {
-    r0 = (int)((long long)p.budget * part / parts);
-    r1 = (int)((long long)p.budget * (part + 1) / parts);
-  }
-  const int nu = u1 - u0;
-  if (nu <= 0) return;
-  for (int base = r0; base < r1; base += kMoveThreads) {
-    const int n = min(kMoveThreads, r1 - base);
-    // addresses of up to 256 rows, one row per thread
-    __syncthreads();  // the previous rows' addresses have been used
-    if (tid < n) {
+  constexpr int RPL = kMoveRows / 32;
+  constexpr int U = NU == 9 ? 18 : NU * RPL < 16 ? NU * RPL : 16;
+  static_assert(NU * RPL % U == 0, "whole batches");
+  for (int base = slot0; base < slot1; base += kMoveRows) {
+    int pos[RPL], ps[RPL], pd[RPL];
+#pragma unroll
+    for (int x = 0; x < RPL; ++x) {
+      const int slot = base + x * 32 + lane;
+      pos[x] = slot < slot1 ? kept[slot] : -1;
+    }
+#pragma unroll
+    for (int x = 0; x < RPL; ++x) {
+      ps[x] = pd[x] = -1;
+      if (pos[x] >= 0) {
+        ps[x] = table[pos[x] / kBlockSize];
+        pd[x] = dtable[(base + x * 32 + lane) / kBlockSize];
+      }
+    }
+    bool any = false;
+    __syncwarp();  // the addresses before have been used
+#pragma unroll
+    for (int x = 0; x < RPL; ++x) {
+      const int slot = base + x * 32 + lane;
       long long s = -1, d = -1;
-      const int slot = base + tid, from = kept[slot];
-      if (from >= 0) {
-        const int ps = table[from / kBlockSize], pd = dtable[slot / kBlockSize];
-        if (ps >= 0 && ps < p.num_blocks && pd >= 0 && pd < p.num_blocks) {
-          s = ((long long)ps * p.num_kv_heads + g) * kBlockSize + from % kBlockSize;
-          d = ((long long)pd * p.num_kv_heads + g) * kBlockSize + slot % kBlockSize;
+      if (pos[x] >= 0) {
+        if (ps[x] >= 0 && ps[x] < p.num_blocks && pd[x] >= 0 &&
+            pd[x] < p.num_blocks) {
+          s = ((long long)ps[x] * p.num_kv_heads + g) * kBlockSize +
+              pos[x] % kBlockSize;
+          d = ((long long)pd[x] * p.num_kv_heads + g) * kBlockSize +
+              slot % kBlockSize;
           if (s == d) s = -1;  // already there
         } else {
           atomicOr(&g_status_evict, (unsigned)SVP_DEV_BAD_BLOCK_ID);
         }
       }
-      src_row[tid] = s;
-      dst_row[tid] = d;
+      from[x * 32 + lane] = s < 0 ? -1 : s * units + u0;
+      to[x * 32 + lane] = d * units + u0;
+      any = any || s >= 0;
     }
-    const int some = __syncthreads_or(tid < n && src_row[tid] >= 0);
-    if (!some) continue;
-    const int total = n * nu;
-    for (int i0 = 0; i0 < total; i0 += kMoveThreads * kMoveUnroll) {
-      V v[kMoveUnroll];
-      long long to[kMoveUnroll];
+    if (!__any_sync(kFull, any)) continue;
+    __syncwarp();
+#pragma unroll 1
+    for (int i0 = 0; i0 < NU * RPL; i0 += U) {
+      V v[U];
 #pragma unroll
-      for (int x = 0; x < kMoveUnroll; ++x) {
-        const int i = i0 + x * kMoveThreads + tid;
-        to[x] = -1;
-        if (i < total) {
-          const int r = i / nu, u = u0 + i % nu;
-          if (src_row[r] >= 0) {
-            v[x] = reinterpret_cast<const V *>(data)[src_row[r] * units + u];
-            to[x] = dst_row[r] * units + u;
-          }
-        }
+      for (int x = 0; x < U; ++x) {
+        const int i = (i0 + x) * 32 + lane;
+        const long long at = from[i / NU];
+        if (at >= 0) v[x] = data[at + i % NU];
       }
-      if (in_place) __syncthreads();  // the batch is read before it is written
+      __syncwarp();  // the batch is read before it is written
 #pragma unroll
-      for (int x = 0; x < kMoveUnroll; ++x)
-        if (to[x] >= 0) reinterpret_cast<V *>(data)[to[x]] = v[x];
+      for (int x = 0; x < U; ++x) {
+        const int i = (i0 + x) * 32 + lane;
+        if (from[i / NU] >= 0) data[to[i / NU] + i % NU] = v[x];
+      }
     }
   }
 }
 
-template <typename V>
-__global__ void __launch_bounds__(kMoveThreads)
-    compact_kernel(const EvictParams p, int parts) {
-  __shared__ long long src_row[kMoveThreads], dst_row[kMoveThreads];
+// A warp per (group, part, side): side 0 K, 1 V, 2 the scores.  Parts are
+// runs of rows; where a sequence is compacted in place they are runs of
+// columns instead (UC vectors), so that no warp writes what another has still
+// to read.  In place means: the first destination page is the first source
+// page.
+template <typename V, int UNITS, int UC>
+__global__ void __launch_bounds__(32 * kMoveWarps)
+    compact_kernel(const EvictParams p, int parts, int warps) {
+  __shared__ long long from[kMoveWarps][kMoveRows], to[kMoveWarps][kMoveRows];
   pdl_wait();  // the selection
   pdl_launch_dependents();
-  const int part = blockIdx.x % parts, group = blockIdx.x / parts;
-  const int b = group / p.num_kv_heads, g = group % p.num_kv_heads;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long item = (long long)blockIdx.x * kMoveWarps + w;
+  const long long n_items = (long long)p.batch * p.num_kv_heads * warps;
   const int side = blockIdx.y;
-  if (side < 2) {
-    move_rows<V>(p, static_cast<char *>(side ? p.v_cache : p.k_cache),
-                 p.row_bytes / (int)sizeof(V), b, g, part, parts, src_row,
-                 dst_row);
-    return;
-  }
-  if (part != 0) return;
-  move_rows<uint32_t>(p, reinterpret_cast<char *>(p.scores), 1, b, g, 0, 1,
-                      src_row, dst_row);
-  if (g == 0 && threadIdx.x == 0) {
+  if (item >= n_items) return;
+  const int part = (int)(item % warps);
+  const int group = (int)(item / warps);
+  const int b = group / p.num_kv_heads, g = group % p.num_kv_heads;
+  if (side == 2 && group % p.num_kv_heads == 0 && part == 0 && lane == 0) {
     const int L = p.seq_lens[b];
     const bool bad = L < 0 || L > (long long)p.max_blocks * kBlockSize;
     p.new_lens[b] = bad ? -1 : min(L, p.budget);
   }
+  const bool in_place = p.dst_table[(size_t)b * p.dst_blocks] ==
+                        p.block_table[(size_t)b * p.max_blocks];
+  int slot0 = 0, slot1 = p.budget;
+  if (!in_place) {
+    if (part >= parts) return;
+    slot0 = (int)((long long)p.budget * part / parts);
+    slot1 = (int)((long long)p.budget * (part + 1) / parts);
+  }
+  if (side == 2) {
+    if (!in_place || part == 0)
+      move_rows<float, 1>(p, p.scores, 1, 0, b, g, slot0, slot1, from[w], to[w]);
+    return;
+  }
+  V *const data = static_cast<V *>(side ? p.v_cache : p.k_cache);
+  if (!in_place)
+    move_rows<V, UNITS>(p, data, UNITS, 0, b, g, slot0, slot1, from[w], to[w]);
+  else if (part < UNITS / UC)
+    move_rows<V, UC>(p, data, UNITS, part * UC, b, g, 0, p.budget, from[w], to[w]);
+}
+
+template <typename V, int UNITS, int UC>
+cudaError_t launch_compact(const EvictParams &p, int sms, cudaLaunchConfig_t cfg) {
+  const long long groups = (long long)p.batch * p.num_kv_heads;
+  // runs of at least 128 rows, enough of them for 32 warps on every SM
+  long long parts = ((long long)sms * 32 + 2 * groups - 1) / (2 * groups);
+  const long long most = (p.budget + kMoveRows - 1) / kMoveRows;
+  if (parts > most) parts = most;
+  const long long warps = parts > UNITS / UC ? parts : UNITS / UC;
+  const long long blocks = (groups * warps + kMoveWarps - 1) / kMoveWarps;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  cfg.gridDim = dim3((unsigned)blocks, 3);
+  cfg.blockDim = dim3(32 * kMoveWarps);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, compact_kernel<V, UNITS, UC>, p, (int)parts,
+                            (int)warps);
 }
 
 }  // namespace
@@ -323,7 +402,8 @@ cudaError_t launch_kv_evict(const EvictParams &p, int sms, cudaStream_t stream) 
   int nc = 1;
   while (nc < kMaxCluster && max_len > (long long)nc * kSelRun) nc *= 2;
   if (groups * nc > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const long long per = (max_len + nc - 1) / nc;
+  const long long per =
+      ((max_len + nc - 1) / nc + kBlockSize - 1) / kBlockSize * kBlockSize;
   const int cap = (int)(per < kSelCache ? per : kSelCache);
   const size_t smem = (size_t)cap * sizeof(unsigned);
   cudaError_t e = cudaSuccess;
@@ -350,24 +430,16 @@ cudaError_t launch_kv_evict(const EvictParams &p, int sms, cudaStream_t stream) 
   e = cudaLaunchKernelEx(&cfg, select_kernel, p, cap);
   if (e != cudaSuccess) return e;
 
-  // parts of a group's K or V: enough CTAs to fill the SMs, none with fewer
-  // than 128 rows
-  long long parts = ((long long)sms * 8 + 2 * groups - 1) / (2 * groups);
-  const long long most = (p.budget + 127) / 128;
-  if (parts > most) parts = most;
-  if (parts > 16) parts = 16;
-  if (groups * parts > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  cfg.gridDim = dim3((unsigned)(groups * parts), 3);
-  cfg.blockDim = dim3(kMoveThreads);
-  cfg.dynamicSmemBytes = 0;
-  cfg.numAttrs = 1;
-  // the widest vector that divides a row: 16 bytes, or 8 / 4 for the 72- and
-  // 36-byte rows of a 4-bit cache
-  if (p.row_bytes % 16 == 0)
-    return cudaLaunchKernelEx(&cfg, compact_kernel<uint4>, p, (int)parts);
-  if (p.row_bytes % 8 == 0)
-    return cudaLaunchKernelEx(&cfg, compact_kernel<uint2>, p, (int)parts);
-  return cudaLaunchKernelEx(&cfg, compact_kernel<uint32_t>, p, (int)parts);
+  // vectors of 16 bytes, or 8 / 4 for the 72- and 36-byte rows of a 4-bit
+  // cache; in place, columns of 64 bytes (24 and 12)
+  switch (p.row_bytes) {
+    case 36: return launch_compact<uint32_t, 9, 3>(p, sms, cfg);
+    case 72: return launch_compact<uint2, 9, 3>(p, sms, cfg);
+    case 64: return launch_compact<uint4, 4, 4>(p, sms, cfg);
+    case 128: return launch_compact<uint4, 8, 4>(p, sms, cfg);
+    case 256: return launch_compact<uint4, 16, 4>(p, sms, cfg);
+    default: return launch_compact<uint4, 32, 4>(p, sms, cfg);  // 512
+  }
 }
 
 cudaError_t read_status_evict(cudaStream_t s, unsigned *flags) {

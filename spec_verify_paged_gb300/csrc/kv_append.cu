@@ -113,28 +113,26 @@ __device__ __forceinline__ int page_of(const int32_t *table, int max_blocks,
 }
 
 // Rows into a 4-bit cache: one lane per block of 16 elements, the K and V
-// blocks of a row on neighbouring lanes.  Bound by the new rows' bytes (32
-// in, 9 out per block) or, for a decode step's few rows, by one round trip
-// through the block table.
+// blocks of a row on neighbouring lanes; a sequence's rows along x, the
+// sequences along y.  Bound by the new rows' bytes (32 in, 9 out per block)
+// or, for a decode step's few rows, by one round trip through the block
+// table.
+template <int NB>  // blocks of a row
 __global__ void __launch_bounds__(32 * kAppendWarps)
     kv_append_fp4_kernel(const AppendParams p) {
   pdl_launch_dependents();
-  const int nb = p.head_dim / kFp4Group;  // blocks of a row
-  const long long idx =
-      (long long)blockIdx.x * (32 * kAppendWarps) + threadIdx.x;
-  const long long n_rows = (long long)p.batch * p.n_new * p.num_kv_heads;
-  const long long row = idx / (2 * nb);
-  if (row >= n_rows) return;
-  const int r = (int)(idx % (2 * nb));
-  const bool is_v = r >= nb;
-  const int blk = is_v ? r - nb : r;
-  const int g = (int)(row % p.num_kv_heads);
-  const int k = (int)((row / p.num_kv_heads) % p.n_new);
-  const int b = (int)(row / ((long long)p.num_kv_heads * p.n_new));
+  const int b = blockIdx.y;
+  const unsigned idx = blockIdx.x * (32 * kAppendWarps) + threadIdx.x;
+  const unsigned row = idx / (2 * NB), r = idx % (2 * NB);  // row: (k, g)
+  if (row >= (unsigned)(p.n_new * p.num_kv_heads)) return;
+  const bool is_v = r >= NB;
+  const int blk = is_v ? r - NB : r;
+  const int k = row / p.num_kv_heads, g = row % p.num_kv_heads;
   // the new values do not depend on the table: load them first
   const uint4 *src = reinterpret_cast<const uint4 *>(
       static_cast<const uint16_t *>(is_v ? p.v_new : p.k_new) +
-      (size_t)row * p.head_dim + blk * kFp4Group);
+      ((size_t)b * p.n_new * p.num_kv_heads + row) * (NB * kFp4Group) +
+      blk * kFp4Group);
   const uint4 in[2] = {src[0], src[1]};
   const int L = p.seq_lens[b];
   if (L < p.n_new || L > (long long)p.max_blocks * kBlockSize) {
@@ -144,17 +142,22 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
   const int pos = L - p.n_new + k;
   const int phys = page_of(p.block_table, p.max_blocks, p.num_blocks, b, pos);
   if (phys < 0) return;
-  const float inv_of = is_v ? p.v_scale : p.k_scale;
+  const float factor = is_v ? p.v_scale : p.k_scale;
   float y[kFp4Group];
   const uint32_t w[8] = {in[0].x, in[0].y, in[0].z, in[0].w,
                          in[1].x, in[1].y, in[1].z, in[1].w};
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    y[2 * i] = __uint_as_float(w[i] << 16) / inv_of;
-    y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) / inv_of;
-    top = fmaxf(top, fmaxf(fabsf(y[2 * i]), fabsf(y[2 * i + 1])));
+    y[2 * i] = __uint_as_float(w[i] << 16);
+    y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
+  if (factor != 1.f) {
+#pragma unroll
+    for (int i = 0; i < kFp4Group; ++i) y[i] /= factor;
+  }
+#pragma unroll
+  for (int i = 0; i < kFp4Group; ++i) top = fmaxf(top, fabsf(y[i]));
   __nv_fp8_storage_t sc =
       __nv_cvt_float_to_fp8(top / 6.f, __NV_SATFINITE, __NV_E4M3);
   if (sc == 0) sc = 1;  // the smallest scale, 2^-9: finer than no scale
@@ -171,99 +174,141 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
   unsigned char *dst =
       static_cast<unsigned char *>(is_v ? p.v_cache : p.k_cache) +
       (((size_t)phys * p.num_kv_heads + g) * kBlockSize + pos % kBlockSize) *
-          (size_t)fp4_row_bytes(p.head_dim);
+          (size_t)fp4_row_bytes(NB * kFp4Group);
   uint32_t *d32 = reinterpret_cast<uint32_t *>(dst + 8 * blk);
   d32[0] = code[0];  // rows are 4-byte aligned (36 or 72 bytes)
   d32[1] = code[1];
-  dst[p.head_dim / 2 + blk] = sc;
+  dst[NB * 8 + blk] = sc;
 }
 
-// Rows back as values: one lane per 16 output bytes (8 bf16 or 4 fp32
-// elements) of a K or V row.  Bound by the output bytes.
+// Rows back as values: a lane writes 16 bytes (8 bf16 or 4 fp32 elements) of
+// a K row and of the V row beside it; a sequence's rows along x, the
+// sequences along y.  Bound by the output bytes.
+template <int DT, int D>
 __global__ void __launch_bounds__(32 * kAppendWarps)
     kv_gather_kernel(const GatherParams p) {
+  constexpr int PER = DT == SVP_F32 ? 4 : 8;  // elements of a lane
+  constexpr int NC = D / PER;                 // lanes of a row
+  constexpr int ROWB = DT == SVP_F32 ? 4 * D : DT == SVP_BF16 ? 2 * D
+                       : DT == SVP_FP8_E4M3 ? D : fp4_row_bytes(D);
   pdl_launch_dependents();
-  const int per = p.dtype == SVP_F32 ? 4 : 8;  // elements of a lane
-  const int nc = p.head_dim / per;             // lanes of a row
+  const int b = blockIdx.y;
   const long long idx =
       (long long)blockIdx.x * (32 * kAppendWarps) + threadIdx.x;
-  const long long n_rows = (long long)p.batch * p.n_rows * p.num_kv_heads;
-  const long long row = idx / (2 * nc);
-  if (row >= n_rows) return;
-  const int r = (int)(idx % (2 * nc));
-  const bool is_v = r >= nc;
-  const int c = is_v ? r - nc : r;
-  const int g = (int)(row % p.num_kv_heads);
-  const long long i = (row / p.num_kv_heads) % p.n_rows;
-  const int b = (int)(row / ((long long)p.num_kv_heads * p.n_rows));
+  const unsigned row = (unsigned)(idx / NC);  // (i, g)
+  const int c = threadIdx.x % NC;
+  if (row >= (unsigned)p.n_rows * (unsigned)p.num_kv_heads) return;
+  const unsigned i = row / p.num_kv_heads, g = row % p.num_kv_heads;
   const int L = p.seq_lens[b];
   int phys = -1;
   long long pos = 0;
   if (L < 0 || L > (long long)p.max_blocks * kBlockSize) {
-    if (r == 0) atomicOr(&g_status_append, (unsigned)SVP_DEV_BAD_SEQ_LEN);
+    if (c == 0) atomicOr(&g_status_append, (unsigned)SVP_DEV_BAD_SEQ_LEN);
   } else {
     pos = (p.starts ? (long long)p.starts[b] : (long long)L - p.n_rows) + i;
     if (pos >= 0 && pos < L)
       phys = page_of(p.block_table, p.max_blocks, p.num_blocks, b, (int)pos);
   }
-  uint4 out = make_uint4(0, 0, 0, 0);
+  uint4 out[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
   if (phys >= 0) {
-    const size_t at = ((size_t)phys * p.num_kv_heads + g) * kBlockSize +
-                      (size_t)(pos % kBlockSize);
-    const unsigned char *cache =
-        static_cast<const unsigned char *>(is_v ? p.v_cache : p.k_cache);
-    const float scale = is_v ? p.v_scale : p.k_scale;
-    uint32_t h[4];  // fp16 pairs of the 8 values before the scale factor
-    if (p.dtype == SVP_F32 || p.dtype == SVP_BF16) {
-      out = *reinterpret_cast<const uint4 *>(
-          cache + at * p.head_dim * (p.dtype == SVP_F32 ? 4 : 2) + 16 * c);
+    const size_t at = (((size_t)phys * p.num_kv_heads + g) * kBlockSize +
+                       (size_t)(pos % kBlockSize)) * ROWB;
+    const unsigned char *const src[2] = {
+        static_cast<const unsigned char *>(p.k_cache) + at,
+        static_cast<const unsigned char *>(p.v_cache) + at};
+    if constexpr (DT == SVP_F32 || DT == SVP_BF16) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        out[s] = __ldg(reinterpret_cast<const uint4 *>(src[s]) + c);
     } else {
-      if (p.dtype == SVP_FP8_E4M3) {
-        const uint2 w =
-            *reinterpret_cast<const uint2 *>(cache + at * p.head_dim + 8 * c);
-        h[0] = e4m3x2_f16x2(w.x);
-        h[1] = e4m3x2_f16x2(w.x >> 16);
-        h[2] = e4m3x2_f16x2(w.y);
-        h[3] = e4m3x2_f16x2(w.y >> 16);
+      uint32_t h[2][4];  // fp16 pairs of the 8 values before the factor
+      if constexpr (DT == SVP_FP8_E4M3) {
+        uint2 w[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          w[s] = __ldg(reinterpret_cast<const uint2 *>(src[s]) + c);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          h[s][0] = e4m3x2_f16x2(w[s].x);
+          h[s][1] = e4m3x2_f16x2(w[s].x >> 16);
+          h[s][2] = e4m3x2_f16x2(w[s].y);
+          h[s][3] = e4m3x2_f16x2(w[s].y >> 16);
+        }
       } else {
-        const unsigned char *src = cache + at * fp4_row_bytes(p.head_dim);
-        const uint32_t s =
-            e4m3x2_f16x2((uint32_t)src[p.head_dim / 2 + c / 2] * 0x101u);
-        e2m1x8_h2(*reinterpret_cast<const uint32_t *>(src + 4 * c), h);
+        uint32_t w[2], sc[2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = hmul2(h[j], s);
-      }
-      uint32_t o[4];
+        for (int s = 0; s < 2; ++s) {
+          w[s] = __ldg(reinterpret_cast<const uint32_t *>(src[s]) + c);
+          sc[s] = __ldg(src[s] + D / 2 + c / 2);
+        }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f =
-            __half22float2(*reinterpret_cast<const __half2 *>(&h[j]));
-        const __nv_bfloat162 v =
-            __floats2bfloat162_rn(f.x * scale, f.y * scale);
-        o[j] = *reinterpret_cast<const uint32_t *>(&v);
+        for (int s = 0; s < 2; ++s) {
+          const uint32_t s2 = e4m3x2_f16x2(sc[s] * 0x101u);
+          e2m1x8_h2(w[s], h[s]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) h[s][j] = hmul2(h[s][j], s2);
+        }
       }
-      out = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const float scale = s ? p.v_scale : p.k_scale;
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f =
+              __half22float2(*reinterpret_cast<const __half2 *>(&h[s][j]));
+          const __nv_bfloat162 v =
+              __floats2bfloat162_rn(f.x * scale, f.y * scale);
+          o[j] = *reinterpret_cast<const uint32_t *>(&v);
+        }
+        out[s] = make_uint4(o[0], o[1], o[2], o[3]);
+      }
     }
   }
-  reinterpret_cast<uint4 *>(is_v ? p.v_out : p.k_out)[(size_t)row * nc + c] = out;
+  const size_t to =
+      ((size_t)b * p.n_rows * p.num_kv_heads + row) * NC + c;
+  static_cast<uint4 *>(p.k_out)[to] = out[0];
+  static_cast<uint4 *>(p.v_out)[to] = out[1];
+}
+
+template <int DT, int D>
+static cudaError_t gather_t(const GatherParams &p, cudaStream_t stream) {
+  constexpr int T = 32 * kAppendWarps;
+  const long long lanes =
+      (long long)p.n_rows * p.num_kv_heads * (D / (DT == SVP_F32 ? 4 : 8));
+  kv_gather_kernel<DT, D><<<dim3((unsigned)((lanes + T - 1) / T),
+                                 (unsigned)p.batch), T, 0, stream>>>(p);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_kv_gather(const GatherParams &p, cudaStream_t stream) {
-  const long long lanes = (long long)p.batch * p.n_rows * p.num_kv_heads *
-                          (2 * p.head_dim / (p.dtype == SVP_F32 ? 4 : 8));
-  if (lanes == 0) return cudaSuccess;
-  constexpr int T = 32 * kAppendWarps;
-  kv_gather_kernel<<<(unsigned)((lanes + T - 1) / T), T, 0, stream>>>(p);
-  return cudaGetLastError();
+  const bool d64 = p.head_dim == 64;
+  switch (p.dtype) {
+    case SVP_F32:
+      return d64 ? gather_t<SVP_F32, 64>(p, stream) : gather_t<SVP_F32, 128>(p, stream);
+    case SVP_BF16:
+      return d64 ? gather_t<SVP_BF16, 64>(p, stream) : gather_t<SVP_BF16, 128>(p, stream);
+    case SVP_FP8_E4M3:
+      return d64 ? gather_t<SVP_FP8_E4M3, 64>(p, stream)
+                 : gather_t<SVP_FP8_E4M3, 128>(p, stream);
+    default:
+      return d64 ? gather_t<SVP_FP4_E2M1, 64>(p, stream)
+                 : gather_t<SVP_FP4_E2M1, 128>(p, stream);
+  }
 }
 
 cudaError_t launch_kv_append(const AppendParams &p, cudaStream_t stream) {
   const long long n_rows = (long long)p.batch * p.n_new * p.num_kv_heads;
   if (n_rows == 0) return cudaSuccess;
   if (p.fp4) {
-    const long long lanes = n_rows * (2 * p.head_dim / kFp4Group);
+    const int nb = p.head_dim / kFp4Group;
+    const long long lanes = (long long)p.n_new * p.num_kv_heads * 2 * nb;
     constexpr int T = 32 * kAppendWarps;
-    kv_append_fp4_kernel<<<(unsigned)((lanes + T - 1) / T), T, 0, stream>>>(p);
+    const dim3 grid((unsigned)((lanes + T - 1) / T), (unsigned)p.batch);
+    if (nb == 4)
+      kv_append_fp4_kernel<4><<<grid, T, 0, stream>>>(p);
+    else
+      kv_append_fp4_kernel<8><<<grid, T, 0, stream>>>(p);
     return cudaGetLastError();
   }
   const long long grid = (n_rows + kAppendWarps - 1) / kAppendWarps;
