@@ -426,6 +426,7 @@ def _paged_dims(batch, num_q_heads, cache, max_blocks, code, k_scale=1.0,
 _dims_kept: dict = {}   # dims by shape: read only, shared by all calls
 _plans: dict = {}       # (dims, workspace bytes) of 4-bit attention by shape
 _KEEP = 1024
+_WS_HEADER = 256
 
 
 def _dims_of(batch, num_q_heads, cache, max_blocks, code, k_scale=1.0,
@@ -481,13 +482,17 @@ def _attention_fp4(q, k_cache, v_cache, block_table, seq_lens, n_sink, window,
         need = lib.paged_decode_workspace_size(ctypes.byref(dims), ql,
                                                int(n_sink), int(window))
         plan = _plans[key] = (dims, int(need))
-    dims = SvpDims.from_buffer_copy(plan[0])
+    dims, need = plan
     if workspace is None:
-        if plan[1]:  # 0: an invalid request, which the call reports
-            workspace = torch.empty(plan[1], dtype=torch.uint8, device=dev)
+        # a header's size: the call uses none; 0: an invalid request, which
+        # the call reports
+        if need > _WS_HEADER:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            dims = SvpDims.from_buffer_copy(dims)
             dims.workspace = workspace.data_ptr()
-            dims.workspace_bytes = plan[1]
+            dims.workspace_bytes = need
     else:
+        dims = SvpDims.from_buffer_copy(dims)
         dims.workspace = workspace.data_ptr()
         dims.workspace_bytes = workspace.numel() * workspace.element_size()
     if out is None:

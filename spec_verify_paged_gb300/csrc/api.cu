@@ -163,6 +163,14 @@ int plan_attention(int batch, int num_q_heads, int num_kv_heads, int head_dim,
       groups * (long long)max_visible_pages(max_blocks, q_len, n_sink, window);
   if (grid > page_bound / min_pages) grid = page_bound / min_pages;
   if (grid < 1) grid = 1;
+  // a 4-bit call of short sequences: a warp to a group, as many CTAs as that
+  // takes (spread over the SMs when there are fewer groups)
+  plan->whole = fp4 && split_pages == 0 &&
+                max_visible_pages(max_blocks, q_len, n_sink, window) <= kWholePages;
+  if (plan->whole) {
+    const int w = attention_fp4_warps(rb);
+    grid = std::max((groups + w - 1) / w, std::min<long long>(groups, num_sms));
+  }
   plan->rb = rb;
   plan->n_rg = n_rg;
   plan->mma = mma;
@@ -181,6 +189,7 @@ int plan_attention(int batch, int num_q_heads, int num_kv_heads, int head_dim,
                                : (size_t)grid * 32);
   plan->ws_part_o = align256(2 * slices * rb * head_dim * 4);
   plan->ws_part_lse = align256(2 * slices * rb * 4);
+  if (plan->whole) plan->ws_desc = plan->ws_part_o = plan->ws_part_lse = 0;
   plan->ws_total =
       plan->ws_head + plan->ws_desc + plan->ws_part_o + plan->ws_part_lse;
   return SVP_OK;
@@ -298,7 +307,7 @@ static int attention_call(const svp_dims *dims, const void *q,
   void *ws = dims->workspace;
   if (ws) {
     if (dims->workspace_bytes < plan.ws_total) return SVP_ERR_WORKSPACE;
-  } else {
+  } else if (!plan.whole) {
     st = owned_workspace(plan.ws_total, stream, &ws);
     if (st != SVP_OK) return st;
   }
@@ -338,6 +347,7 @@ static int attention_call(const svp_dims *dims, const void *q,
     p.rb = plan.rb;
     p.n_rg = plan.n_rg;
     p.merge_rows = std::min(plan.rb, p.rows);
+    p.whole = plan.whole;
     // tcgen05: items are 8-page tiles, 4-bit caches: 4-page stages (a
     // slice's minimum in items)
     p.ppi = plan.fp4 ? kTilePagesFp4 : plan.tc ? kTilePagesTc : 1;
@@ -355,7 +365,8 @@ static int attention_call(const svp_dims *dims, const void *q,
     if (nb != bl) {
       plan_attention(nb, dims->num_q_heads, dims->num_kv_heads,
                      dims->head_dim, dims->dtype, dims->max_blocks_per_seq,
-                     q_len, n_sink, window, plan.min_pages,
+                     q_len, n_sink, window,
+                     plan.whole ? 0 : plan.min_pages,
                      plan.tc                 ? SVP_PATH_TCGEN05
                      : plan.mma || plan.fp4  ? SVP_PATH_TENSOR_CORES
                                              : SVP_PATH_CUDA_CORES,
@@ -371,7 +382,7 @@ static int attention_call(const svp_dims *dims, const void *q,
     if (!plan.fp4 &&
         launch_merge(p, dims->dtype, sub.grid, stream) != cudaSuccess)
       return SVP_ERR_CUDA;
-    launches += 2;
+    launches += plan.whole ? 1 : 2;
   }
   t_last_launches = launches;
   return SVP_OK;

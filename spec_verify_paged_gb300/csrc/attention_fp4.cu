@@ -32,6 +32,9 @@
 //    segment's whole state in registers and writes the segment's result from
 //    there.  No barrier joins the warps, so a warp that ends a segment
 //    (normalise, write, next Q) costs the others nothing.
+//  * Where no sequence can hold more than 32 pages a warp takes a group whole:
+//    no prefix of the lengths to build, no partials and no second launch
+//    (250 tokens of four heads: 19.5 us a call from the host against 24).
 //  * A group of pages cut by slice borders leaves one normalised partial per
 //    slice; merge_fp4_kernel joins them by log-sum-exp in slice order.
 //  * Rows whose memory holds no valid data take no part: masked keys score
@@ -340,6 +343,28 @@ __device__ __forceinline__ Seg4 next_segment(const AttnParams &p,
   return s;
 }
 
+// Group `slice` as one run of pages (AttnParams::whole).
+__device__ __forceinline__ Seg4 whole_segment(const AttnParams &p, int per_seq,
+                                              int slice, int rb, int lane) {
+  Seg4 s = {};
+  s.b = slice / per_seq;
+  const int gi = slice - s.b * per_seq;
+  s.g = gi / p.n_rg;
+  s.rg = gi - s.g * p.n_rg;
+  s.L = p.seq_lens[s.b];
+  if (s.L < p.q_len || s.L > p.max_blocks * kBlockSize) {
+    if (lane == 0 && gi == 0) raise4(SVP_DEV_BAD_SEQ_LEN);
+    return s;
+  }
+  visible_pages(s.L, p.q_len, p.n_sink, p.window, s.n_a, s.b_start, s.n_pages);
+  s.f = s.l = slice;
+  s.valid = 1;
+  const int base = s.L - p.q_len;
+  s.t_min = p.tree_mask ? base - 1 : base + s.rg * rb / p.group;
+  s.t_max = base + (min(s.rg * rb + rb, p.rows) - 1) / p.group;
+  return s;
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
     paged_attention_fp4_kernel(const AttnParams p) {
@@ -364,16 +389,21 @@ __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
   // launched early: see AttnParams::early
   if (!p.early) pdl_wait();
   pdl_launch_dependents();  // the merge may be scheduled
-  int *const seqlen = sm.prefix + p.batch + 1;
-  if (warp == 0) build_prefix(p, sm.prefix, seqlen, per_seq, lane, &g_status_attn4);
-  __syncthreads();  // the only one: the warps are on their own from here
-  const int total = sm.prefix[p.batch];
   // slice s goes to warp s / gridDim.x of CTA s % gridDim.x: a small call
   // spreads over the SMs
-  const int n_slices = min((long long)gridDim.x * W, max(1LL, (long long)total / p.min_pages));
   const int slice = warp * gridDim.x + blockIdx.x;
+  int *const seqlen = sm.prefix + p.batch + 1;
+  int total = 0, n_slices = p.batch * per_seq, end = 0;
+  if (!p.whole) {
+    if (warp == 0)
+      build_prefix(p, sm.prefix, seqlen, per_seq, lane, &g_status_attn4);
+    __syncthreads();  // the only one: the warps are on their own from here
+    total = sm.prefix[p.batch];
+    n_slices = (int)min((long long)gridDim.x * W,
+                        max(1LL, (long long)total / p.min_pages));
+  }
   if (slice >= n_slices) return;
-  const int end = slice_begin(slice + 1, total, n_slices);
+  if (!p.whole) end = slice_begin(slice + 1, total, n_slices);
 
   // ---- the issuing side: up to kStages4 stages ahead of the reading side.
   // Segment `seg_i` is being issued, the one after it is decoded already and
@@ -384,8 +414,10 @@ __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
   // sinks are skipped and by how much, its first page, head, limits
   int n_pages = 0, page0 = 0, n_a = 0, skip = 0, kvh = 0, t_min = 0, t_max = 0;
   auto decode = [&](int i, int pos) {  // segment i of this slice, into the ring
-    const Seg4 s = next_segment(p, sm.prefix, seqlen, per_seq, pos, end, total,
-                                n_slices, RB);
+    const Seg4 s = !p.whole ? next_segment(p, sm.prefix, seqlen, per_seq, pos, end,
+                                           total, n_slices, RB)
+                   : i == 0 ? whole_segment(p, per_seq, slice, RB, lane)
+                            : Seg4{};
     if (lane == 0) inf.seg[i % kSegRing4] = s;
     __syncwarp();
   };
@@ -414,7 +446,7 @@ __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
     raise4(SVP_DEV_BAD_BLOCK_ID);
     return -1;
   };
-  decode(0, slice_begin(slice, total, n_slices));
+  decode(0, p.whole ? 0 : slice_begin(slice, total, n_slices));
   take_up();
   // entries of pages k .. k + 31 (as head pages), of the 32 after them, and
   // of the following segment's first 32
@@ -677,7 +709,7 @@ __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
     // ---- the segment's result, from registers ----
     if (p.early) pdl_wait();  // outputs are written from here on
     const bool single = ui.f == ui.l;
-    if (slice == ui.f && lane == 0)
+    if (!p.whole && slice == ui.f && lane == 0)
       p.split[(ui.b * p.num_kv_heads + ui.g) * p.n_rg + ui.rg] =
           make_int2(ui.f, ui.l);
     const size_t part = (size_t)2 * slice + (slice == ui.f ? 1 : 0);
@@ -859,7 +891,7 @@ cudaError_t launch4(AttnParams p, int grid, cudaStream_t st) {
   }
   e = launch_pdl(kern, (unsigned)grid, 32u * warps4<NT>(), smem4<D, NT>(p.batch),
                  st, p);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.whole) return e;
   const long long blocks =
       (long long)p.batch * p.num_kv_heads * p.n_rg * p.merge_rows;
   return launch_pdl(merge_fp4_kernel<D>, (unsigned)blocks, 32u * kMergeWarps4, 0,

@@ -28,6 +28,7 @@ struct AttnParams {
   struct SplitDesc *desc;  // [grid] split group whose first page a CTA owns
   int2 *split;         // 4-bit kernel: [groups] first and last slice
   int merge_rows;      // 4-bit kernel: query rows the merge walks per group
+  int whole;           // 4-bit kernel: one slice per group, no merge
   int slices;          // 4-bit kernel: set by its launcher, the partials' bound
   float *part_o;       // [2 * grid][RB][D] normalised partials: each CTA's
                        // first- and last-segment slot
@@ -59,6 +60,7 @@ struct AttnPlan {
   bool mma;            // warp-level mma.sync path
   bool tc;             // tcgen05 path (tensor-memory accumulators)
   bool fp4;            // 4-bit cache kernel
+  bool whole;          // its slices are whole groups: no workspace, no merge
   int batch_cap;       // sequences per launch
   size_t ws_head, ws_desc, ws_part_o, ws_part_lse, ws_total;
 };
@@ -127,6 +129,8 @@ cudaError_t launch_attention_tc(const AttnParams &p, int grid,
 // The 4-bit cache kernels (attention_fp4.cu): the unit's row count (8 or
 // 16) for this many query rows per kv head, the warps (slices) of a CTA,
 // of which an SM holds one, and the launch of attention and merge.
+// Calls whose sequences span at most kWholePages pages take whole groups.
+constexpr int kWholePages = 32;
 int attention_fp4_rows(int rows);
 int attention_fp4_warps(int rb);
 cudaError_t launch_attention_fp4(const AttnParams &p, int grid,
