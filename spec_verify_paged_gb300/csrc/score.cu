@@ -39,16 +39,17 @@ constexpr int kScoreWarps = 4;
 constexpr int kScoreThreads = 32 * kScoreWarps;
 constexpr int kScoreMaxPages = 32 * kScoreWarps;  // of one CTA
 
-struct ScoreRow {
-  float qs;       // score scale (log2 domain)
-  float lse2;     // log2-domain LSE; +inf: the row adds nothing
-  int pos;        // query position within the new rows
-  uint32_t bits;  // ancestor bits (all ones without a tree)
+struct ScoreRows {
+  // score scale (log2 domain) and log2-domain LSE (+inf: the row adds
+  // nothing): two rows are one 16-byte read
+  alignas(16) float2 ql[kScoreRows];
+  int pos[kScoreRows];        // query position within the new rows
+  uint32_t bits[kScoreRows];  // ancestor bits (all ones without a tree)
 };
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4],
                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
       "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(kScoreThreads)
   constexpr int ROWB = DT == SVP_F32 ? 4 * D : DT == SVP_BF16 ? 2 * D
                        : DT == SVP_FP8_E4M3 ? D : fp4_row_bytes(D);
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  __shared__ ScoreRow rows[kScoreRows];
+  __shared__ ScoreRows rows;
   uint2 *const qf = reinterpret_cast<uint2 *>(smem_raw);   // [nt][KS][32]
   float *const qf32 = reinterpret_cast<float *>(smem_raw);  // [row][D]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -253,13 +254,11 @@ __global__ void __launch_bounds__(kScoreThreads)
       for (int ks = 0; ks < KS; ++ks) qf[(nt * KS + ks) * 32 + lane] = w[ks];
     }
     if (t == 0) {
-      ScoreRow sr;
-      sr.qs = qs;
       const float lse = valid ? __ldg(p.lse + qrow) : -INFINITY;
-      sr.lse2 = lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
-      sr.pos = i;
-      sr.bits = row_tree_bits(p.tree_mask, p.q_len, b, i);
-      rows[r] = sr;
+      rows.ql[r] = make_float2(
+          qs, lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f);
+      rows.pos[r] = i;
+      rows.bits[r] = row_tree_bits(p.tree_mask, p.q_len, b, i);
     }
   }
   __syncthreads();
@@ -305,7 +304,7 @@ __global__ void __launch_bounds__(kScoreThreads)
     float sum[2] = {0.f, 0.f};
     if constexpr (DT == SVP_F32) {
       for (int r = 0; r < p.rows; ++r) {
-        const ScoreRow sr = rows[r];
+        const float2 ql = rows.ql[r];
         const float4 *q4 = reinterpret_cast<const float4 *>(qf32) + r * (D / 4) + t;
         float d[2] = {0.f, 0.f};
 #pragma unroll
@@ -323,37 +322,56 @@ __global__ void __launch_bounds__(kScoreThreads)
         for (int h = 0; h < 2; ++h) {
           d[h] += __shfl_xor_sync(kFull, d[h], 1);
           d[h] += __shfl_xor_sync(kFull, d[h], 2);
-          const float w = ex2(fmaf(d[h], sr.qs, -sr.lse2));
-          if (all_vis || key_visible(j0 + g + 8 * h, t0 + sr.pos, sr.bits, t0,
-                                     p.n_sink, p.window))
+          const float w = ex2(fmaf(d[h], ql.x, -ql.y));
+          if (all_vis || key_visible(j0 + g + 8 * h, t0 + rows.pos[r],
+                                     rows.bits[r], t0, p.n_sink, p.window))
             sum[h] += w;
         }
       }
     } else {
-      for (int nt = 0; nt < n_tiles; ++nt) {
-        float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      uint32_t a[KS][4];  // converted once for all row tiles
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) now.operand(ks, t, a[ks]);
+      auto multiply = [&](int nt, float (&acc)[4]) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          uint32_t a[4];
-          now.operand(ks, t, a);
           const uint2 q = qf[(nt * KS + ks) * 32 + lane];
           if constexpr (DT == SVP_BF16)
-            mma_bf16(acc[ks & 1], a, q.x, q.y);
+            mma_bf16(acc, a[ks], q.x, q.y);
           else
-            mma_f16(acc[ks & 1], a, q.x, q.y);
+            mma_f16(acc, a[ks], q.x, q.y);
         }
+      };
+      auto weigh = [&](int nt, const float (&acc)[4]) {
+        const float4 ql =  // rows 2t and 2t + 1 of the tile
+            *reinterpret_cast<const float4 *>(&rows.ql[nt * 8 + 2 * t]);
+        float w[4] = {ex2(fmaf(acc[0], ql.x, -ql.y)), ex2(fmaf(acc[1], ql.z, -ql.w)),
+                      ex2(fmaf(acc[2], ql.x, -ql.y)), ex2(fmaf(acc[3], ql.z, -ql.w))};
+        if (!all_vis) {  // warp-uniform
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const ScoreRow sr = rows[nt * 8 + 2 * t + r];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float x = acc[0][2 * h + r] + acc[1][2 * h + r];
-            const float w = ex2(fmaf(x, sr.qs, -sr.lse2));
-            if (all_vis || key_visible(j0 + g + 8 * h, t0 + sr.pos, sr.bits,
-                                       t0, p.n_sink, p.window))
-              sum[h] += w;
+          for (int e = 0; e < 4; ++e) {
+            const int r = nt * 8 + 2 * t + (e & 1);
+            if (!key_visible(j0 + g + 8 * (e >> 1), t0 + rows.pos[r], rows.bits[r],
+                             t0, p.n_sink, p.window))
+              w[e] = 0.f;
           }
         }
+        sum[0] += w[0] + w[1];
+        sum[1] += w[2] + w[3];
+      };
+      // two row tiles at a time: two independent chains
+      int nt = 0;
+      for (; nt + 1 < n_tiles; nt += 2) {
+        float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+        multiply(nt, x);
+        multiply(nt + 1, y);
+        weigh(nt, x);
+        weigh(nt + 1, y);
+      }
+      if (nt < n_tiles) {
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        multiply(nt, x);
+        weigh(nt, x);
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
