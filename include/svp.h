@@ -111,8 +111,9 @@ typedef struct {
 /* Which attention kernel variant runs.  AUTO picks tensor cores (bf16 only)
  * when a kv head serves at least 3 query rows (GQA group x q_len): TCGEN05
  * for head_dim 128, TENSOR_CORES for head_dim 64; CUDA cores otherwise.
- * An SVP_FP4_E2M1 cache always takes warp-level mma.sync (fp16 operands
- * built from the codes in registers, fp32 accumulate).
+ * An SVP_FP4_E2M1 cache takes tensor cores for any number of rows, with fp16
+ * operands (code * scale is exact there) and fp32 accumulation: TCGEN05 for
+ * more than 8 rows at head_dim 128, TENSOR_CORES otherwise.
  * All compute the same quantity; forcing a path exists for testing and
  * tuning.
  *   CUDA_CORES    fp32 FMA dot products, any dtype.
@@ -122,8 +123,7 @@ typedef struct {
  *                 dimension (bf16, head_dim 128, 512 sequences per
  *                 kernel launch).
  * A forced path on data it cannot take (a tensor path on fp32 or FP8;
- * head_dim 64 for TCGEN05; anything but TENSOR_CORES on FP4) is
- * SVP_ERR_UNSUPPORTED. */
+ * head_dim 64 for TCGEN05; CUDA_CORES on FP4) is SVP_ERR_UNSUPPORTED. */
 typedef enum {
   SVP_PATH_AUTO = 0,
   SVP_PATH_CUDA_CORES = 1,

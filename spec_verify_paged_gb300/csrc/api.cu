@@ -109,10 +109,14 @@ static int select_path(int dtype, int head_dim, int rows, int kernel_path,
   // the tensor paths address the cache as a 2-D tensor with int32 rows
   const bool tma_ok = tensor_maps_available() &&
                       num_blocks * num_kv_heads * kBlockSize < (1LL << 31);
-  if (dtype == SVP_FP4_E2M1) {  // one kernel, on mma.sync
-    if (kernel_path != SVP_PATH_AUTO && kernel_path != SVP_PATH_TENSOR_CORES)
+  if (dtype == SVP_FP4_E2M1) {
+    if (kernel_path == SVP_PATH_CUDA_CORES ||
+        (kernel_path == SVP_PATH_TCGEN05 && head_dim != 128))
       return SVP_ERR_UNSUPPORTED;
-    return SVP_PATH_TENSOR_CORES;
+    if (kernel_path == SVP_PATH_AUTO)
+      return rows >= kFp4TcMinRows && head_dim == 128 ? SVP_PATH_TCGEN05
+                                                      : SVP_PATH_TENSOR_CORES;
+    return kernel_path;
   }
   switch (kernel_path) {
     case SVP_PATH_CUDA_CORES:
@@ -140,7 +144,7 @@ int plan_attention(int batch, int num_q_heads, int num_kv_heads, int head_dim,
   int path = select_path(dtype, head_dim, rows, kernel_path, num_blocks,
                          num_kv_heads);
   if (path < 0) return path;
-  const bool fp4 = dtype == SVP_FP4_E2M1;
+  const bool fp4 = dtype == SVP_FP4_E2M1 && path == SVP_PATH_TENSOR_CORES;
   const bool mma = path == SVP_PATH_TENSOR_CORES && !fp4;
   const bool tc = path == SVP_PATH_TCGEN05;
   // mma.sync: one m16 tile per warp, two warps share a page beyond 16 rows;
@@ -152,7 +156,9 @@ int plan_attention(int batch, int num_q_heads, int num_kv_heads, int head_dim,
                  : rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : 8;
   const int n_rg = (rows + rb - 1) / rb;
   const int ctas = fp4  ? 1
-                   : tc ? attention_tc_ctas_per_sm(rb, batch)
+                   : tc ? dtype == SVP_FP4_E2M1
+                              ? attention_fp4_tc_ctas_per_sm(rb, batch)
+                              : attention_tc_ctas_per_sm(rb, batch)
                       : attention_ctas_per_sm(dtype, head_dim, rb, mma, batch);
   const long long groups = (long long)batch * num_kv_heads * n_rg;
   // Every CTA of the persistent grid takes an equal slice of all pages;
@@ -220,12 +226,12 @@ static int plan_call(const svp_dims *d, int q_len, int n_sink, int window,
   const int path = select_path(d->dtype, d->head_dim, rows, d->kernel_path,
                                d->num_blocks, d->num_kv_heads);
   if (path < 0) return path;
-  const int cap = d->dtype == SVP_FP4_E2M1   ? kBatchFp4
-                  : path == SVP_PATH_TCGEN05 ? tc_batch_cap()
+  const int cap = path == SVP_PATH_TCGEN05   ? tc_batch_cap()
+                  : d->dtype == SVP_FP4_E2M1 ? kBatchFp4
                                              : kBatchPerLaunch;
   const int bl = batch_per_launch(d, q_len, n_sink, window, cap,
-                                  d->dtype == SVP_FP4_E2M1   ? kSegItemsFp4
-                                  : path == SVP_PATH_TCGEN05 ? kSegItemsTc
+                                  path == SVP_PATH_TCGEN05   ? kSegItemsTc
+                                  : d->dtype == SVP_FP4_E2M1 ? kSegItemsFp4
                                                              : kSegItemsCc);
   const int st = plan_attention(bl, d->num_q_heads, d->num_kv_heads,
                                 d->head_dim, d->dtype, d->max_blocks_per_seq,
@@ -316,7 +322,8 @@ static int attention_call(const svp_dims *dims, const void *q,
   char *wp = static_cast<char *>(ws);
   const size_t eb = dims->dtype == SVP_F32 ? 4 : 2;  // q / out (bf16 for FP8)
   const size_t row_elems = (size_t)dims->num_q_heads * dims->head_dim;
-  const bool scaled = dims->dtype == SVP_FP8_E4M3 || plan.fp4;
+  const bool scaled =
+      dims->dtype == SVP_FP8_E4M3 || dims->dtype == SVP_FP4_E2M1;
   int launches = 0;
   for (int b0 = 0; b0 < dims->batch; b0 += bl) {
     const int nb = dims->batch - b0 < bl ? dims->batch - b0 : bl;
@@ -373,7 +380,9 @@ static int attention_call(const svp_dims *dims, const void *q,
                      sms, dims->num_blocks, &sub);
     }
     cudaError_t e =
-        plan.fp4  ? launch_attention_fp4(p, sub.grid, stream)
+        plan.fp4 ? launch_attention_fp4(p, sub.grid, stream)
+        : plan.tc && dims->dtype == SVP_FP4_E2M1
+            ? launch_attention_fp4_tc(p, sub.grid, stream)
         : plan.tc ? launch_attention_tc(p, sub.grid, stream)
                 : launch_attention(p, dims->dtype, plan.mma, sub.grid, stream);
     if (e != cudaSuccess) return SVP_ERR_CUDA;
@@ -707,6 +716,8 @@ int svp_read_device_status(cudaStream_t stream, int *flags) {
   if (read_status_attention(stream, &f) != cudaSuccess) return SVP_ERR_CUDA;
   if (read_status_attention_tc(stream, &f) != cudaSuccess) return SVP_ERR_CUDA;
   if (read_status_attention_fp4(stream, &f) != cudaSuccess) return SVP_ERR_CUDA;
+  if (read_status_attention_fp4_tc(stream, &f) != cudaSuccess)
+    return SVP_ERR_CUDA;
   if (read_status_append(stream, &f) != cudaSuccess) return SVP_ERR_CUDA;
   if (read_status_score(stream, &f) != cudaSuccess) return SVP_ERR_CUDA;
   if (read_status_evict(stream, &f) != cudaSuccess) return SVP_ERR_CUDA;

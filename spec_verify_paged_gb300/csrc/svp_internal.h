@@ -104,6 +104,10 @@ constexpr int kBatchFp4 = 512;
 // mma.sync for head_dim 64.
 constexpr int kMmaMinRows = 3;
 
+// The same for 4-bit caches at head_dim 128: below, one or two row tiles of
+// the mma.sync kernel.
+constexpr int kFp4TcMinRows = 9;
+
 // Occupancy-derived CTAs per SM for the attention kernel of this shape
 // (queried once per device and shape, cached).
 int attention_ctas_per_sm(int dtype, int head_dim, int rb, bool mma,
@@ -135,6 +139,12 @@ int attention_fp4_rows(int rows);
 int attention_fp4_warps(int rb);
 cudaError_t launch_attention_fp4(const AttnParams &p, int grid,
                                  cudaStream_t stream);
+
+// The tcgen05 kernel over 4-bit caches (attention_fp4_tc.cu): head_dim 128,
+// units of 16, 32 or 64 rows; plan, batch cap and merge as attention_tc.cu.
+int attention_fp4_tc_ctas_per_sm(int rb, int batch);
+cudaError_t launch_attention_fp4_tc(const AttnParams &p, int grid,
+                                    cudaStream_t stream);
 
 struct AppendParams {
   const void *k_new;
@@ -235,6 +245,7 @@ cudaError_t launch_spec_accept_tree(const AcceptTreeParams &p,
 cudaError_t read_status_attention(cudaStream_t s, unsigned *flags);
 cudaError_t read_status_attention_tc(cudaStream_t s, unsigned *flags);
 cudaError_t read_status_attention_fp4(cudaStream_t s, unsigned *flags);
+cudaError_t read_status_attention_fp4_tc(cudaStream_t s, unsigned *flags);
 cudaError_t read_status_append(cudaStream_t s, unsigned *flags);
 cudaError_t read_status_score(cudaStream_t s, unsigned *flags);
 cudaError_t read_status_evict(cudaStream_t s, unsigned *flags);

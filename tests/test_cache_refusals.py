@@ -35,8 +35,8 @@ def test_fp4_scales_and_paths(lib):
         d = _dims(**kw)
         assert lib.kv_append(ctypes.byref(d), P, P, P, P, P, P, 1, None) == -1
         assert lib.paged_decode_workspace_size(ctypes.byref(d), 1, 0, 0) == 0
-    for path in (1, 3):
-        d = _dims(kernel_path=path)
+    for path, d in ((1, 128), (1, 64), (3, 64)):
+        d = _dims(kernel_path=path, head_dim=d)
         assert lib.paged_decode_attention(ctypes.byref(d), P, P, P, P, P, 1, 0, 0,
                                           0.1, P, P, None) in (-2, -3)
         assert lib.paged_decode_workspace_size(ctypes.byref(d), 1, 0, 0) == 0

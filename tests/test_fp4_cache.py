@@ -188,10 +188,16 @@ CASES = [
 ]
 
 
+PATHS = {0: "auto", 2: "mma", 3: "tcgen05"}
+
+
+@pytest.mark.parametrize("path", PATHS, ids=PATHS.values())
 @pytest.mark.parametrize("case", CASES, ids=[str(i) for i in range(len(CASES))])
-def test_attention(svp, case):
+def test_attention(svp, case, path):
     import torch
     d, hq, hkv, ql, lens, mask, split, ks = case
+    if path == 3 and d != 128:
+        pytest.skip("head_dim 128 only")
     vs = 0.75 * ks
     q, kc, vc, table, lens = _inputs(d + hq + ql, lens, hq, hkv, d, ql, ks, vs)
     scale = 1.0 / np.sqrt(d)
@@ -201,19 +207,22 @@ def test_attention(svp, case):
     if mask == "tree":
         tree = np.tile(R.binary_tree(ql), (len(lens), 1))
         out, lse = svp.paged_tree_attention(*g, R.to_gpu(tree), scale=scale,
-                                            split_pages=split, k_scale=ks, v_scale=vs)
+                                            split_pages=split, kernel_path=path,
+                                            k_scale=ks, v_scale=vs)
         mask = dict(tree=tree)
     else:
         out, lse = svp.paged_decode_attention(*g, scale=scale, split_pages=split,
-                                              k_scale=ks, v_scale=vs, **mask)
+                                              kernel_path=path, k_scale=ks,
+                                              v_scale=vs, **mask)
     assert svp.read_device_status() == 0
     ref = _reference(q, kc, vc, d, float(np.float32(scale)), lens, table, fks, fvs, **mask)
     _check(out, lse, ref, d)
 
 
+@pytest.mark.parametrize("path", [2, 3])
 @pytest.mark.parametrize("gain,scale", [(1e-30, 1e28), (200.0, 1.0), (1.0, 0.0),
                                         (1.0, -0.3), (3e4, 1e-3)])
-def test_query_ranges_and_scales(svp, gain, scale):
+def test_query_ranges_and_scales(svp, gain, scale, path):
     """Query rows far outside fp16's range, sharp softmaxes, a zero and a
     negative scale."""
     d = 128
@@ -221,12 +230,13 @@ def test_query_ranges_and_scales(svp, gain, scale):
     q = R.bf16(q * gain)
     out, lse = svp.paged_decode_attention(
         R.to_gpu(q, "bf16"), R.to_gpu(kc), R.to_gpu(vc), R.to_gpu(table),
-        R.to_gpu(lens), scale=scale)
+        R.to_gpu(lens), scale=scale, kernel_path=path)
     ref = _reference(q, kc, vc, d, float(np.float32(scale)), lens, table, 1.0, 1.0)
     _check(out, lse, ref, d)
 
 
-def test_rising_scores(svp):
+@pytest.mark.parametrize("path", [2, 3])
+def test_rising_scores(svp, path):
     """Scores that grow by more than the softmax's slack from page to page:
     the reference moves at every page."""
     d = 128
@@ -238,16 +248,17 @@ def test_rising_scores(svp):
         kc[table[0, j // 16], :, j % 16] = rows[j]
     out, lse = svp.paged_decode_attention(
         R.to_gpu(q, "bf16"), R.to_gpu(kc), R.to_gpu(vc), R.to_gpu(table),
-        R.to_gpu(lens), scale=1.0)
+        R.to_gpu(lens), scale=1.0, kernel_path=path)
     _check(out, lse, _reference(q, kc, vc, d, 1.0, lens, table, 1.0, 1.0), d)
 
 
-def test_many_splits_and_wide_table(svp):
+@pytest.mark.parametrize("ql", [1, 5])
+def test_many_splits_and_wide_table(svp, ql):
     """One long sequence over the whole grid (partials merged across many
     CTAs), a block table wider than any sequence, repeatable results."""
     import torch
     d = 128
-    q, kc, vc, table, lens = _inputs(11, [6000, 40], 8, 2, d, 1, width=900)
+    q, kc, vc, table, lens = _inputs(11, [6000, 40], 8, 2, d, ql, width=900)
     g = [R.to_gpu(q, "bf16"), R.to_gpu(kc), R.to_gpu(vc), R.to_gpu(table), R.to_gpu(lens)]
     out, lse = svp.paged_decode_attention(*g, scale=0.1)
     again, lse2 = svp.paged_decode_attention(*g, scale=0.1)
@@ -255,7 +266,8 @@ def test_many_splits_and_wide_table(svp):
     _check(out, lse, _reference(q, kc, vc, d, float(np.float32(0.1)), lens, table, 1.0, 1.0), d)
 
 
-def test_bad_pages_and_lengths_are_flagged(svp):
+@pytest.mark.parametrize("path", [2, 3])
+def test_bad_pages_and_lengths_are_flagged(svp, path):
     """A bad page is left out, a bad sequence is left as it was; the others
     are right."""
     import torch
@@ -269,7 +281,7 @@ def test_bad_pages_and_lengths_are_flagged(svp):
     out = torch.full((3, 1, 4, d), 7.0, dtype=torch.bfloat16, device="cuda")
     lse = torch.full((3, 1, 4), 7.0, device="cuda")
     svp.paged_decode_attention(*g, R.to_gpu(bad), R.to_gpu(bad_lens), scale=0.1,
-                               out=out, lse=lse)
+                               out=out, lse=lse, kernel_path=path)
     assert svp.read_device_status() == 3      # bad block id, bad length
     assert (out[2] == 7).all() and (lse[2] == 7).all()
     ref = _reference(q[1:2], kc, vc, d, float(np.float32(0.1)), lens[1:2], table[1:2], 1.0, 1.0)
@@ -377,7 +389,8 @@ def test_step_runner_over_a_4bit_cache(svp):
     assert svp.read_device_status() == 0
 
 
-def test_stalled_producer_times_out(svp):
+@pytest.mark.parametrize("path", [2, 3])
+def test_stalled_producer_times_out(svp, path):
     """A test build whose producers stop: every role's bounded wait runs out,
     the call returns with the flag set, and the next call is right."""
     import torch
@@ -389,7 +402,8 @@ def test_stalled_producer_times_out(svp):
     g = [R.to_gpu(q, "bf16"), R.to_gpu(kc), R.to_gpu(vc), R.to_gpu(table), R.to_gpu(lens)]
     out = torch.empty(q.shape, dtype=torch.bfloat16, device="cuda")
     lse = torch.empty(q.shape[:3], device="cuda")
-    dims = bd._paged_dims(2, 12, g[1], table.shape[1], bd.SVP_FP4_E2M1, split_pages=64)
+    dims = bd._paged_dims(2, 12, g[1], table.shape[1], bd.SVP_FP4_E2M1, split_pages=64,
+                          kernel_path=path)
     need = stall.paged_decode_workspace_size(ctypes.byref(dims), 4, 0, 0)
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
     dims.workspace, dims.workspace_bytes = ws.data_ptr(), need
@@ -402,6 +416,6 @@ def test_stalled_producer_times_out(svp):
     f = ctypes.c_int(0)
     assert stall.svp_read_device_status(stream, ctypes.byref(f)) == 0
     assert f.value & 8
-    out, lse = svp.paged_decode_attention(*g, scale=0.1)
+    out, lse = svp.paged_decode_attention(*g, scale=0.1, kernel_path=path)
     assert svp.read_device_status() == 0
     _check(out, lse, _reference(q, kc, vc, d, float(np.float32(0.1)), lens, table, 1.0, 1.0), d)
