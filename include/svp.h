@@ -113,7 +113,7 @@ typedef struct {
  * for head_dim 128, TENSOR_CORES for head_dim 64; CUDA cores otherwise.
  * An SVP_FP4_E2M1 cache takes tensor cores for any number of rows, with fp16
  * operands (code * scale is exact there) and fp32 accumulation: TCGEN05 for
- * more than 8 rows at head_dim 128, TENSOR_CORES otherwise.
+ * more than 32 rows at head_dim 128, TENSOR_CORES otherwise.
  * All compute the same quantity; forcing a path exists for testing and
  * tuning.
  *   CUDA_CORES    fp32 FMA dot products, any dtype.

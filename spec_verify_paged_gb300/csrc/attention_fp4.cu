@@ -589,121 +589,156 @@ __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
         o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
     }
 
-    for (int k1 = 0; k1 < ui.n_pages; k1 += kStagePages, ++c) {
-      const int s = c % kStages4;
-      if (!mbar_wait_at(bars + s * 8, (c / kStages4) & 1)) {
-        // give up: flag it, wait (bounded) for the copies still in flight
-        if (lane == 0) {
-          raise4(SVP_DEV_TIMEOUT);
-          int armed = issued;
+    // The pages of a segment go two by two.  A pair's scores are computed in
+    // the same straight run of code as the previous pair's P V: the two share
+    // no data, so the one's chains of conversions and MMAs fill the other's
+    // waits (long contexts: XX us against 126).
+    auto ready = [&](int cc) {
+      if (mbar_wait_at(bars + (cc % kStages4) * 8, (cc / kStages4) & 1)) return true;
+      // give up: flag it, wait (bounded) for the copies still in flight
+      if (lane == 0) {
+        raise4(SVP_DEV_TIMEOUT);
+        int armed = issued;
 #ifdef SVP_TEST_STALL_AFTER
-          armed = min(armed, SVP_TEST_STALL_AFTER);
+        armed = min(armed, SVP_TEST_STALL_AFTER);
 #endif
-          for (int q = c; q < armed; ++q)
-            (void)mbar_wait_drain(&inf.full[q % kStages4], (q / kStages4) & 1);
-        }
-        return;
+        for (int q = c; q < armed; ++q)
+          (void)mbar_wait_drain(&inf.full[q % kStages4], (q / kStages4) & 1);
       }
-      const uint32_t st = kv0 + s * (kStagePages * 2 * PAGE);
-      const int meta = (int)lds32(metas + s * 4);  // warp-uniform
+      return false;
+    };
+    if (!ready(c)) return;
+    int s = c % kStages4, p0 = 0, left = ui.n_pages;
+    int meta = (int)lds32(metas + s * 4);  // warp-uniform
+    uint32_t pair = kv0 + s * (kStagePages * 2 * PAGE);
+    float x[PJ][NT][4];
+#pragma unroll
+    for (int j = 0; j < PJ; ++j)
+      page_scores<D, NT>(pair + j * 2 * PAGE + k_off, t, x[j], qb);
+    while (true) {
       const bool checked = meta >= kChecked;
       const int pages = meta & (kChecked - 1);
-#pragma unroll 1
-      for (int p0 = 0; p0 < pages; p0 += PJ) {
-        const uint32_t pair = st + p0 * (2 * PAGE);
-        float x[PJ][NT][4], y[PJ][NT][4];
+      // ---- softmax with a lazy reference ----
+      float y[PJ][NT][4];
+      float far = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < PJ; ++j)
-          page_scores<D, NT>(pair + j * 2 * PAGE + k_off, t, x[j], qb);
-        // ---- softmax with a lazy reference ----
-        float far = -INFINITY;
+      for (int j = 0; j < PJ; ++j)
 #pragma unroll
-        for (int j = 0; j < PJ; ++j)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int e = 0; e < 4; ++e) {
+            y[j][nt][e] = fmaf(x[j][nt][e], qs[nt][e & 1], -ref[nt][e & 1]);
+            far = fmaxf(far, y[j][nt][e]);
+          }
+      unsigned keep[PJ];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              y[j][nt][e] = fmaf(x[j][nt][e], qs[nt][e & 1], -ref[nt][e & 1]);
-              far = fmaxf(far, y[j][nt][e]);
+      for (int j = 0; j < PJ; ++j) keep[j] = 0xfu;
+      if (checked || __any_sync(kFull, far > kRefSlack)) {
+        // masked keys score -inf; a row whose scores reach beyond the
+        // slack gets a new reference
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            uint32_t bits = ~0u;
+            int i = 0;
+            if (checked) {
+              i = min(row0 + nt * 8 + 2 * t + r, p.rows - 1) / p.group;
+              bits = row_tree_bits(p, ui.b, i);
             }
-        unsigned keep[PJ];
-#pragma unroll
-        for (int j = 0; j < PJ; ++j) keep[j] = 0xfu;
-        if (checked || __any_sync(kFull, far > kRefSlack)) {
-          // masked keys score -inf; a row whose scores reach beyond the
-          // slack gets a new reference
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              uint32_t bits = ~0u;
-              int i = 0;
-              if (checked) {
-                i = min(row0 + nt * 8 + 2 * t + r, p.rows - 1) / p.group;
-                bits = row_tree_bits(p, ui.b, i);
-              }
-              float mx = -INFINITY;
-#pragma unroll
-              for (int j = 0; j < PJ; ++j)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  float z = x[j][nt][2 * h + r] * qs[nt][r];
-                  if (checked &&
-                      !key_visible((int)lds32(j0s + (s * kStagePages + p0 + j) * 4) + fp4_key(g, h), t0 + i,
-                                   bits, t0, p.n_sink, p.window))
-                    z = -INFINITY;
-                  x[j][nt][2 * h + r] = z;
-                  mx = fmaxf(mx, z);
-                }
-              mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
-              mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
-              mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
-              const float to = fmaxf(ref[nt][r], mx - kRefOffset);
-              const float alpha = ex2(ref[nt][r] - to);
-              ref[nt][r] = to;
-              l[nt][r] *= alpha;
-#pragma unroll
-              for (int d2 = 0; d2 < D / 16; ++d2) {
-                o[d2][nt][r] *= alpha;
-                o[d2][nt][2 + r] *= alpha;
-              }
-#pragma unroll
-              for (int j = 0; j < PJ; ++j)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                  y[j][nt][2 * h + r] = x[j][nt][2 * h + r] - to;
-            }
-          if (checked) {
+            float mx = -INFINITY;
 #pragma unroll
             for (int j = 0; j < PJ; ++j)
 #pragma unroll
-              for (int sx = 0; sx < 4; ++sx) {
-                const int key = (int)lds32(j0s + (s * kStagePages + p0 + j) * 4) + 4 * t + sx;
-                if (!(key < L && (p.window == 0 || key < p.n_sink ||
-                                  key > t0 - p.window)))
-                  keep[j] &= ~(1u << sx);
+              for (int h = 0; h < 2; ++h) {
+                float z = x[j][nt][2 * h + r] * qs[nt][r];
+                if (checked &&
+                    !key_visible((int)lds32(j0s + (s * kStagePages + p0 + j) * 4) + fp4_key(g, h), t0 + i,
+                                 bits, t0, p.n_sink, p.window))
+                  z = -INFINITY;
+                x[j][nt][2 * h + r] = z;
+                mx = fmaxf(mx, z);
               }
-          }
-        }
+            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
+            const float to = fmaxf(ref[nt][r], mx - kRefOffset);
+            const float alpha = ex2(ref[nt][r] - to);
+            ref[nt][r] = to;
+            l[nt][r] *= alpha;
 #pragma unroll
-        for (int j = 0; j < PJ; ++j) {
-          uint32_t pb[NT][2];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              y[j][nt][e] = ex2(y[j][nt][e]);
-              l[nt][e & 1] += y[j][nt][e];
+            for (int d2 = 0; d2 < D / 16; ++d2) {
+              o[d2][nt][r] *= alpha;
+              o[d2][nt][2 + r] *= alpha;
             }
-            pb[nt][0] = transpose8(pack_h2(y[j][nt][0], y[j][nt][1]));
-            pb[nt][1] = transpose8(pack_h2(y[j][nt][2], y[j][nt][3]));
+#pragma unroll
+            for (int j = 0; j < PJ; ++j)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                y[j][nt][2 * h + r] = x[j][nt][2 * h + r] - to;
           }
-          const uint32_t vp = pair + (j * 2 + 1) * PAGE;
-          page_values<D, NT>(vp + v_off, vp + v_off_s, keep[j], pb, o);
+        if (checked) {
+#pragma unroll
+          for (int j = 0; j < PJ; ++j)
+#pragma unroll
+            for (int sx = 0; sx < 4; ++sx) {
+              const int key = (int)lds32(j0s + (s * kStagePages + p0 + j) * 4) + 4 * t + sx;
+              if (!(key < L && (p.window == 0 || key < p.n_sink ||
+                                key > t0 - p.window)))
+                keep[j] &= ~(1u << sx);
+            }
         }
       }
-      __syncwarp();
-      issue();  // into the stage just read
+#pragma unroll
+      for (int j = 0; j < PJ; ++j)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[j][nt][e] = ex2(y[j][nt][e]);
+            l[nt][e & 1] += y[j][nt][e];
+          }
+        }
+      uint32_t pb[PJ][NT][2];
+#pragma unroll
+      for (int j = 0; j < PJ; ++j)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          pb[j][nt][0] = transpose8(pack_h2(y[j][nt][0], y[j][nt][1]));
+          pb[j][nt][1] = transpose8(pack_h2(y[j][nt][2], y[j][nt][3]));
+        }
+      // the next pair: of this stage, of the next one, or none (this one's
+      // scores are then computed again and dropped)
+      const bool stage_end = p0 + PJ >= pages;
+      const bool more = !stage_end || left > kStagePages;
+      uint32_t next = pair;
+      int meta_n = meta;
+      if (!stage_end) {
+        next = pair + PJ * 2 * PAGE;
+      } else if (more) {
+        if (!ready(c + 1)) return;
+        const int sn = (c + 1) % kStages4;
+        next = kv0 + sn * (kStagePages * 2 * PAGE);
+        meta_n = (int)lds32(metas + sn * 4);
+      }
+#pragma unroll
+      for (int j = 0; j < PJ; ++j) {
+        const uint32_t vp = pair + (j * 2 + 1) * PAGE;
+        page_scores<D, NT>(next + j * 2 * PAGE + k_off, t, x[j], qb);
+        page_values<D, NT>(vp + v_off, vp + v_off_s, keep[j], pb[j], o);
+      }
+      pair = next;
+      meta = meta_n;
+      p0 += PJ;
+      if (stage_end) {
+        p0 = 0;
+        left -= kStagePages;
+        s = (c + 1) % kStages4;
+        __syncwarp();
+        issue();  // into the stage just read
+        ++c;
+        if (!more) break;
+      }
     }
 
     // ---- the segment's result, from registers ----

@@ -1,6 +1,6 @@
 // attention_fp4_tc.cu -- paged decode / speculative-verify attention over a
 // 4-bit cache on the fifth-generation tensor cores (tcgen05.mma, accumulators
-// in tensor memory): head_dim 128, more than 8 query rows per kv head.
+// in tensor memory): head_dim 128, many query rows per kv head.
 //
 // The pipeline is attention_tc.cu's -- keys as the MMA's M = 128 (a tile of 8
 // pages), query rows as N, S^T = K Q^T and O^T = V^T P^T, softmax groups,
@@ -371,37 +371,39 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr,
       : "memory");
 }
 
-// One block of 16 codes: row `n` (key) of the tile, block c of the row.
-// `raw`: shared address of the page's side, r the row in the page; `dst`: of
-// the tile.
-__device__ __forceinline__ void dequant_block(uint32_t raw, int r, uint32_t dst,
-                                              int n, int c) {
+// One block of 16 codes, in two steps so that a lane's reads of several
+// blocks are in flight together.
+struct Block4 {
   uint32_t w0, w1, sc;
+};
+// Block c of row r of a raw page (`raw`: its shared address).
+__device__ __forceinline__ Block4 read_block(uint32_t raw, int r, int c) {
+  Block4 b;
   const uint32_t row = raw + r * fp4_row_bytes(kD);
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-               : "=r"(w0), "=r"(w1)
+               : "=r"(b.w0), "=r"(b.w1)
                : "r"(row + 8 * c));
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sc) : "r"(row + kD / 2 + c));
-  const uint32_t s2 = e4m3x2_f16x2(sc * 0x101u);
-  uint32_t h[2][4];
-  e2m1x8_h2(w0, h[0]);
-  e2m1x8_h2(w1, h[1]);
-#pragma unroll
-  for (int x = 0; x < 2; ++x)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[x][i] = hmul2(h[x][i], s2);
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b.sc) : "r"(row + kD / 2 + c));
+  return b;
+}
+// The block as fp16 into row n (key) of the tile at `dst`.
+__device__ __forceinline__ void write_block(const Block4 &b, uint32_t dst,
+                                            int n, int c) {
+  const uint32_t s2 = e4m3x2_f16x2(b.sc * 0x101u);
   // the block's two 16-byte chunks, 2 c and 2 c + 1 of the row's sixteen:
   // lanes of the second half of a row write theirs in the other order, so
   // that eight lanes hit eight different bank groups
-  const uint32_t base = dst + (c >> 2) * kHalfBytes + n * 128;
   const int swap = c >> 2;
+  const uint32_t base = dst + swap * kHalfBytes + n * 128;
+  uint32_t h[2][4];
+  e2m1x8_h2(swap ? b.w1 : b.w0, h[0]);
+  e2m1x8_h2(swap ? b.w0 : b.w1, h[1]);
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    const int y = x ^ swap;
-    const uint32_t at = base + ((((2 * c + y) & 7) ^ (n & 7)) << 4);
+    const uint32_t at = base + ((((2 * c + (x ^ swap)) & 7) ^ (n & 7)) << 4);
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at),
-                 "r"(y ? h[1][0] : h[0][0]), "r"(y ? h[1][1] : h[0][1]),
-                 "r"(y ? h[1][2] : h[0][2]), "r"(y ? h[1][3] : h[0][3])
+                 "r"(hmul2(h[x][0], s2)), "r"(hmul2(h[x][1], s2)),
+                 "r"(hmul2(h[x][2], s2)), "r"(hmul2(h[x][3], s2))
                  : "memory");
   }
 }
@@ -576,12 +578,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const int pg = dw + 4 * half;
           if (!((mask >> pg) & 1)) continue;  // masked later
           const uint32_t src = raw + pg * (2 * kRawPage);
+          Block4 blk[8];
 #pragma unroll
-          for (int r0 = 0; r0 < 4; ++r0) {
-            const int r = r0 + r_off;
-            dequant_block(src, r, kt, pg * kBlockSize + r, c_blk);
-            dequant_block(src + kRawPage, r, vt, pg * kBlockSize + r, c_blk);
-          }
+          for (int x = 0; x < 8; ++x)
+            blk[x] = read_block(src + (x >> 2) * kRawPage, (x & 3) + r_off, c_blk);
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            write_block(blk[x], x < 4 ? kt : vt,
+                        pg * kBlockSize + (x & 3) + r_off, c_blk);
         }
         if (dw == 0 && lane == 0) sm.stage_mask[s] = mask;
         fence_proxy_async_smem();  // the tiles -> tensor core

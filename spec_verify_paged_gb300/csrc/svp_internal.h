@@ -104,9 +104,10 @@ constexpr int kBatchFp4 = 512;
 // mma.sync for head_dim 64.
 constexpr int kMmaMinRows = 3;
 
-// The same for 4-bit caches at head_dim 128: below, one or two row tiles of
-// the mma.sync kernel.
-constexpr int kFp4TcMinRows = 9;
+// The same for 4-bit caches at head_dim 128: below, units of 16 rows on the
+// mma.sync kernel (20 rows, 98 MB of cache: 67 us against 75; 60 rows: 120
+// against 89).
+constexpr int kFp4TcMinRows = 33;
 
 // Occupancy-derived CTAs per SM for the attention kernel of this shape
 // (queried once per device and shape, cached).
