@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
     // The pages of a segment go two by two.  A pair's scores are computed in
     // the same straight run of code as the previous pair's P V: the two share
     // no data, so the one's chains of conversions and MMAs fill the other's
-    // waits (long contexts: XX us against 126).
+    // waits (long contexts: 122 us against 126).
     auto ready = [&](int cc) {
       if (mbar_wait_at(bars + (cc % kStages4) * 8, (cc / kStages4) & 1)) return true;
       // give up: flag it, wait (bounded) for the copies still in flight
