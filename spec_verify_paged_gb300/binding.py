@@ -1,4 +1,6 @@
-"""Thin ctypes binding of libsvp.so (include/svp.h).
+"""Thin binding of libsvp.so (include/svp.h), by ctypes and, for the calls on
+4-bit caches and the gather, score and eviction calls, by a small extension
+module (csrc/calls.cpp).
 
 Argument marshalling only: shape/dtype/device checks, raw device pointers,
 the current CUDA stream, and a zero-filled workspace tensor kept per device.
@@ -273,9 +275,11 @@ def paged_decode_attention(q, k_cache, v_cache, block_table, seq_lens,
     fp4_row_bytes(D)) take bf16 q and their k_scale / v_scale."""
     if _is_fp4(k_cache):
         _need(q_len is None or q_len == q.shape[1], "q.shape[1] must equal q_len")
-        return _attention_fp4(q, k_cache, v_cache, block_table, seq_lens, n_sink,
-                              window, None, scale, out, lse, workspace,
-                              split_pages, kernel_path, stream, k_scale, v_scale)
+        r = (_calls or _load_calls()).attention_fp4(
+            q, k_cache, v_cache, block_table, seq_lens, n_sink, window, None,
+            scale, out, lse, workspace, split_pages, kernel_path, _raw(stream),
+            k_scale, v_scale)
+        return r if type(r) is tuple else _check("paged_decode_attention", r)
     return _attention(q, k_cache, v_cache, block_table, seq_lens, q_len,
                       n_sink, window, None, scale, out, lse, workspace,
                       split_pages, kernel_path, stream, k_scale, v_scale)
@@ -289,9 +293,12 @@ def paged_tree_attention(q, k_cache, v_cache, block_table, seq_lens,
     tree_mask: int32 (or uint32) [B, q_len] on the GPU, bit k of entry
     (b, i) set iff node k is an ancestor of node i or i itself."""
     if _is_fp4(k_cache):
-        return _attention_fp4(q, k_cache, v_cache, block_table, seq_lens, 0, 0,
-                              tree_mask, scale, out, lse, workspace, split_pages,
-                              kernel_path, stream, k_scale, v_scale)
+        _need(tree_mask is not None, "tree_mask must be int32/uint32 [B, q_len]")
+        r = (_calls or _load_calls()).attention_fp4(
+            q, k_cache, v_cache, block_table, seq_lens, 0, 0, tree_mask, scale,
+            out, lse, workspace, split_pages, kernel_path, _raw(stream), k_scale,
+            v_scale)
+        return r if type(r) is tuple else _check("paged_tree_attention", r)
     _cuda_contig(tree_mask, "tree_mask")
     _need(tree_mask.dtype in (torch.int32, getattr(torch, "uint32", torch.int32))
           and tuple(tree_mask.shape) == tuple(q.shape[:2]),
@@ -351,196 +358,31 @@ def _attention(q, k_cache, v_cache, block_table, seq_lens, q_len, n_sink,
     return out, lse
 
 
-# ---- the 4-bit cache, gather, score and eviction calls ----
-# A decode step makes these calls once per layer, so their host cost counts:
-# one pass over the tensors' attributes, dims and workspace sizes kept by
-# shape, the stream's handle without a Stream object.
-
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
+# ---- the 4-bit cache, gather, score and eviction calls: csrc/calls.cpp checks
+# their arguments, makes their outputs and calls the library ----
+CALLS_PATH = os.path.join(_HERE, "svp_calls.so")
+_calls = None
 
 
-def _handle(stream, device):
-    if stream is not None:
-        return stream.cuda_stream
-    if _raw_stream is not None:
-        return _raw_stream(device.index)
-    return torch.cuda.current_stream(device).cuda_stream
+def _load_calls():
+    """The marshalling module (raises if it has not been built)."""
+    global _calls
+    if _calls is None:
+        load_library()
+        if not os.path.exists(CALLS_PATH):
+            raise RuntimeError(
+                f"{CALLS_PATH} is missing: build it with "
+                "`python -c 'import __graft_entry__ as g; g.build()'`")
+        import importlib.util
+        spec = importlib.util.spec_from_file_location("svp_calls", CALLS_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _calls = module
+    return _calls
 
 
-def _elsewhere(device, stream):
-    """Whether the call needs another device or stream made current, so that
-    the library launches there and memory allocated on the way belongs to the
-    stream that uses it."""
-    return stream is not None or device.index != (
-        _current_device() if _current_device else torch.cuda.current_device())
-
-
-def _on(device, stream):
-    return torch.cuda.stream(torch.cuda.current_stream(device)
-                             if stream is None else stream)
-
-
-def _want(t, name, dev, dtype, shape):
-    """`t` is a contiguous tensor of that type and shape on CUDA device dev."""
-    if (t.dtype is dtype and t.shape == shape and t.device == dev and
-            t.is_contiguous() and dev.type == "cuda"):
-        return
-    raise ValueError(
-        f"{name} must be a contiguous {dtype} CUDA tensor {list(shape)} on {dev}, "
-        f"got {t.dtype} {list(t.shape)} on {t.device}")
-
-
-def _want_mask(t, dev, shape):
-    _need(t.element_size() == 4 and not t.is_floating_point(),
-          "tree_mask must be int32/uint32 [B, q_len]")
-    _want(t, "tree_mask", dev, t.dtype, shape)
-
-
-def _want_pages(k_cache, v_cache, block_table, seq_lens, batch):
-    """The paged arguments of a call for `batch` sequences; the caches'
-    device."""
-    dev = k_cache.device
-    _need(k_cache.dim() == 4, "caches must be [num_blocks, Hkv, block_size, row]")
-    _need(block_table.dim() == 2, "block_table must be int32 [B, max_blocks]")
-    shape = k_cache.shape
-    _want(k_cache, "k_cache", dev, k_cache.dtype, shape)
-    if v_cache is not None:
-        _want(v_cache, "v_cache", dev, k_cache.dtype, shape)
-    _want(block_table, "block_table", dev, torch.int32, (batch, block_table.shape[1]))
-    _want(seq_lens, "seq_lens", dev, torch.int32, (batch,))
-    return dev
-
-
-def _paged_dims(batch, num_q_heads, cache, max_blocks, code, k_scale=1.0,
-                v_scale=1.0, workspace=None, split_pages=0, kernel_path=0):
-    return SvpDims(batch, num_q_heads, cache.shape[1], _head_dim(cache),
-                   cache.shape[2], max_blocks, cache.shape[0], code,
-                   None if workspace is None else workspace.data_ptr(),
-                   0 if workspace is None else
-                   workspace.numel() * workspace.element_size(),
-                   int(split_pages), int(kernel_path), float(k_scale),
-                   float(v_scale))
-
-
-_dims_kept: dict = {}   # dims by shape: read only, shared by all calls
-_plans: dict = {}       # (dims, workspace bytes) of 4-bit attention by shape
-_KEEP = 1024
-_WS_HEADER = 256
-
-
-def _dims_of(batch, num_q_heads, cache, max_blocks, code, k_scale=1.0,
-             v_scale=1.0):
-    """dims without a workspace, made once per shape."""
-    key = (batch, num_q_heads, cache.shape, max_blocks, code, k_scale, v_scale)
-    dims = _dims_kept.get(key)
-    if dims is None:
-        if len(_dims_kept) >= _KEEP:
-            _dims_kept.clear()
-        dims = _paged_dims(batch, num_q_heads, cache, max_blocks, code, k_scale,
-                           v_scale)
-        _dims_kept[key] = dims
-    return dims
-
-
-def _attention_fp4(q, k_cache, v_cache, block_table, seq_lens, n_sink, window,
-                   tree_mask, scale, out, lse, workspace, split_pages,
-                   kernel_path, stream, k_scale, v_scale):
-    """Attention over a 4-bit cache.  Without a workspace of the caller's one
-    is allocated for this call alone, so calls on other streams and captured
-    graphs share nothing."""
-    lib = _lib or load_library()
-    _need(q.dim() == 4, "q must be [B, q_len, Hq, D]")
-    B, ql, Hq, D = shape = q.shape
-    dev = _want_pages(k_cache, v_cache, block_table, seq_lens, B)
-    _want(q, "q", dev, torch.bfloat16, shape)
-    if _FP4_DIMS[k_cache.shape[3]] != D:
-        raise ValueError(f"a 4-bit cache row for head_dim {D} has "
-                         f"{fp4_row_bytes(D)} bytes, got {k_cache.shape[3]}")
-    if tree_mask is not None:
-        _want_mask(tree_mask, dev, (B, ql))
-    if out is not None:
-        _want(out, "out", dev, torch.bfloat16, shape)
-    if lse is not None:
-        _want(lse, "lse", dev, torch.float32, (B, ql, Hq))
-    if workspace is not None:
-        _want(workspace, "workspace", dev, workspace.dtype, workspace.shape)
-    if _elsewhere(dev, stream):
-        with _on(dev, stream):
-            return _attention_fp4(q, k_cache, v_cache, block_table, seq_lens,
-                                  n_sink, window, tree_mask, scale, out, lse,
-                                  workspace, split_pages, kernel_path, None,
-                                  k_scale, v_scale)
-    key = (shape, k_cache.shape, block_table.shape[1], n_sink, window, k_scale,
-           v_scale, split_pages, kernel_path, dev.index)
-    plan = _plans.get(key)
-    if plan is None:
-        if len(_plans) >= _KEEP:
-            _plans.clear()
-        dims = _paged_dims(B, Hq, k_cache, block_table.shape[1], SVP_FP4_E2M1,
-                           k_scale, v_scale, None, split_pages, kernel_path)
-        need = lib.paged_decode_workspace_size(ctypes.byref(dims), ql,
-                                               int(n_sink), int(window))
-        plan = _plans[key] = (dims, int(need))
-    dims, need = plan
-    if workspace is None:
-        # a header's size: the call uses none; 0: an invalid request, which
-        # the call reports
-        if need > _WS_HEADER:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-            dims = SvpDims.from_buffer_copy(dims)
-            dims.workspace = workspace.data_ptr()
-            dims.workspace_bytes = need
-    else:
-        dims = SvpDims.from_buffer_copy(dims)
-        dims.workspace = workspace.data_ptr()
-        dims.workspace_bytes = workspace.numel() * workspace.element_size()
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((B, ql, Hq), dtype=torch.float32, device=dev)
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    if tree_mask is None:
-        st = lib.paged_decode_attention(
-            ctypes.byref(dims), q.data_ptr(), k_cache.data_ptr(),
-            v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), ql,
-            int(n_sink), int(window), scale, out.data_ptr(), lse.data_ptr(),
-            _handle(stream, dev))
-        if st:
-            _check("paged_decode_attention", st)
-    else:
-        st = lib.paged_tree_attention(
-            ctypes.byref(dims), q.data_ptr(), k_cache.data_ptr(),
-            v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), ql,
-            tree_mask.data_ptr(), scale, out.data_ptr(), lse.data_ptr(),
-            _handle(stream, dev))
-        if st:
-            _check("paged_tree_attention", st)
-    return out, lse
-
-
-def _append_fp4(k_new, v_new, k_cache, v_cache, block_table, seq_lens, stream,
-                k_scale, v_scale):
-    lib = _lib or load_library()
-    _need(k_new.dim() == 4, "k_new/v_new must be [B, n_new, Hkv, D]")
-    B, n_new, Hkv, _ = k_new.shape
-    dev = _want_pages(k_cache, v_cache, block_table, seq_lens, B)
-    shape = (B, n_new, k_cache.shape[1], _FP4_DIMS[k_cache.shape[3]])
-    _want(k_new, "k_new", dev, torch.bfloat16, shape)
-    _want(v_new, "v_new", dev, torch.bfloat16, shape)
-    if _elsewhere(dev, stream):
-        with _on(dev, stream):
-            return _append_fp4(k_new, v_new, k_cache, v_cache, block_table,
-                               seq_lens, None, k_scale, v_scale)
-    dims = _dims_of(B, Hkv, k_cache, block_table.shape[1], SVP_FP4_E2M1, k_scale,
-                    v_scale)
-    st = lib.kv_append(ctypes.byref(dims), k_new.data_ptr(), v_new.data_ptr(),
-                       k_cache.data_ptr(), v_cache.data_ptr(),
-                       block_table.data_ptr(), seq_lens.data_ptr(), n_new,
-                       _handle(stream, dev))
-    if st:
-        _check("kv_append", st)
+def _raw(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def kv_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens,
@@ -550,8 +392,10 @@ def kv_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens,
     Into FP8 and 4-bit caches the bf16 rows are quantised with k_scale /
     v_scale."""
     if _is_fp4(k_cache):
-        return _append_fp4(k_new, v_new, k_cache, v_cache, block_table, seq_lens,
-                           stream, k_scale, v_scale)
+        st = (_calls or _load_calls()).append_fp4(
+            k_new, v_new, k_cache, v_cache, block_table, seq_lens, _raw(stream),
+            k_scale, v_scale)
+        return None if st is None else _check("kv_append", st)
     lib = load_library()
     for t, n in ((k_new, "k_new"), (v_new, "v_new"), (k_cache, "k_cache"),
                  (v_cache, "v_cache"), (block_table, "block_table"),
@@ -582,39 +426,10 @@ def kv_gather(k_cache, v_cache, block_table, seq_lens, n_rows, starts=None,
     [B, n_rows, Hkv, D] (fp32 of an fp32 cache, else bf16), the values at
     logical positions starts[b] .. starts[b] + n_rows - 1 (int32 [B]; without
     it the newest n_rows); zeros outside the sequence."""
-    lib = _lib or load_library()
-    code = _any_cache_code(k_cache)
-    _need(seq_lens.dim() == 1, "seq_lens must be int32 [B]")
-    B = seq_lens.shape[0]
-    dev = _want_pages(k_cache, v_cache, block_table, seq_lens, B)
-    n_rows = int(n_rows)
-    _need(n_rows >= 0, "n_rows must not be negative")
-    shape = (B, n_rows, k_cache.shape[1], _head_dim(k_cache))
-    dtype = torch.float32 if code == SVP_F32 else torch.bfloat16
-    if starts is not None:
-        _want(starts, "starts", dev, torch.int32, (B,))
-    if k_out is not None:
-        _want(k_out, "k_out", dev, dtype, shape)
-    if v_out is not None:
-        _want(v_out, "v_out", dev, dtype, shape)
-    if _elsewhere(dev, stream):
-        with _on(dev, stream):
-            return kv_gather(k_cache, v_cache, block_table, seq_lens, n_rows,
-                             starts, k_out, v_out, None, k_scale, v_scale)
-    if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=dev)
-    if v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=dev)
-    dims = _dims_of(B, shape[2], k_cache, block_table.shape[1], code, k_scale,
-                    v_scale)
-    st = lib.kv_gather(
-        ctypes.byref(dims), k_cache.data_ptr(), v_cache.data_ptr(),
-        block_table.data_ptr(), seq_lens.data_ptr(),
-        None if starts is None else starts.data_ptr(), n_rows, k_out.data_ptr(),
-        v_out.data_ptr(), _handle(stream, dev))
-    if st:
-        _check("kv_gather", st)
-    return k_out, v_out
+    r = (_calls or _load_calls()).gather(
+        k_cache, v_cache, block_table, seq_lens, n_rows, starts, k_out, v_out,
+        _raw(stream), k_scale, v_scale)
+    return r if type(r) is tuple else _check("kv_gather", r)
 
 
 def paged_score_update(q, k_cache, lse, block_table, seq_lens, scores,
@@ -626,34 +441,10 @@ def paged_score_update(q, k_cache, lse, block_table, seq_lens, scores,
     the same arguments returned (include/svp.h: paged_score_update).  The
     newest n_fresh positions (default: q_len) start from zero.  Returns
     scores."""
-    lib = _lib or load_library()
-    _need(q.dim() == 4, "q must be [B, q_len, Hq, D]")
-    B, ql, Hq, D = shape = q.shape
-    dev = _want_pages(k_cache, None, block_table, seq_lens, B)
-    code = _cache_code(k_cache, q.dtype)
-    _need(_head_dim(k_cache) == D, "q and k_cache must share head_dim")
-    _want(q, "q", dev, q.dtype, shape)
-    _want(lse, "lse", dev, torch.float32, (B, ql, Hq))
-    _want(scores, "scores", dev, torch.float32, k_cache.shape[:3])
-    if tree_mask is not None:
-        _want_mask(tree_mask, dev, (B, ql))
-    if _elsewhere(dev, stream):
-        with _on(dev, stream):
-            return paged_score_update(q, k_cache, lse, block_table, seq_lens,
-                                      scores, n_fresh, n_sink, window, tree_mask,
-                                      scale, k_scale)
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    dims = _dims_of(B, Hq, k_cache, block_table.shape[1], code, k_scale)
-    st = lib.paged_score_update(
-        ctypes.byref(dims), q.data_ptr(), k_cache.data_ptr(), lse.data_ptr(),
-        block_table.data_ptr(), seq_lens.data_ptr(), ql, int(n_sink),
-        int(window), None if tree_mask is None else tree_mask.data_ptr(), scale,
-        ql if n_fresh is None else int(n_fresh), scores.data_ptr(),
-        _handle(stream, dev))
-    if st:
-        _check("paged_score_update", st)
-    return scores
+    st = (_calls or _load_calls()).score_update(
+        q, k_cache, lse, block_table, seq_lens, scores, n_fresh, n_sink, window,
+        tree_mask, scale, k_scale, _raw(stream))
+    return scores if st is None else _check("paged_score_update", st)
 
 
 def kv_evict(k_cache, v_cache, scores, block_table, seq_lens, budget, n_sink=0,
@@ -664,42 +455,10 @@ def kv_evict(k_cache, v_cache, scores, block_table, seq_lens, budget, n_sink=0,
     first rows of dst_block_table's pages (default: in place); scores move
     along (include/svp.h: kv_evict).  Returns (kept [B, Hkv, budget] int32
     positions, -1 padded, new_lens [B] int32)."""
-    lib = _lib or load_library()
-    code = _any_cache_code(k_cache)
-    _need(seq_lens.dim() == 1, "seq_lens must be int32 [B]")
-    B, budget = seq_lens.shape[0], int(budget)
-    dev = _want_pages(k_cache, v_cache, block_table, seq_lens, B)
-    _need(budget >= 1, "budget must be at least 1")
-    shape = (B, k_cache.shape[1], budget)
-    _want(scores, "scores", dev, torch.float32, k_cache.shape[:3])
-    dst, n_dst = None, 0
-    if dst_block_table is not None:
-        _need(dst_block_table.dim() == 2, "dst_block_table must be int32 [B, n]")
-        n_dst = dst_block_table.shape[1]
-        _want(dst_block_table, "dst_block_table", dev, torch.int32, (B, n_dst))
-        dst = dst_block_table.data_ptr()
-    if kept is not None:
-        _want(kept, "kept", dev, torch.int32, shape)
-    if new_lens is not None:
-        _want(new_lens, "new_lens", dev, torch.int32, (B,))
-    if _elsewhere(dev, stream):
-        with _on(dev, stream):
-            return kv_evict(k_cache, v_cache, scores, block_table, seq_lens,
-                            budget, n_sink, n_recent, dst_block_table, kept,
-                            new_lens)
-    if kept is None:
-        kept = torch.empty(shape, dtype=torch.int32, device=dev)
-    if new_lens is None:
-        new_lens = torch.empty(B, dtype=torch.int32, device=dev)
-    dims = _dims_of(B, shape[1], k_cache, block_table.shape[1], code)
-    st = lib.kv_evict(
-        ctypes.byref(dims), k_cache.data_ptr(), v_cache.data_ptr(),
-        scores.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), budget,
-        int(n_sink), int(n_recent), dst, n_dst, kept.data_ptr(),
-        new_lens.data_ptr(), _handle(stream, dev))
-    if st:
-        _check("kv_evict", st)
-    return kept, new_lens
+    r = (_calls or _load_calls()).evict(
+        k_cache, v_cache, scores, block_table, seq_lens, budget, n_sink,
+        n_recent, dst_block_table, kept, new_lens, _raw(stream))
+    return r if type(r) is tuple else _check("kv_evict", r)
 
 
 def spec_accept(target_logits, draft_logits, draft_tokens, uniforms,

@@ -21,6 +21,10 @@ HEADERS = [os.path.join(CSRC, h)
                      "fp4.cuh")] + [
     os.path.join(INCLUDE, "svp.h")]
 
+# the Python calls that marshal in C++ (linked to libsvp.so beside it)
+CALLS_SRC = os.path.join(CSRC, "calls.cpp")
+CALLS_LIB = os.path.join(PKG, "svp_calls.so")
+
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -46,21 +50,72 @@ def _compile(src: str, extra) -> str:
     return obj
 
 
+def _calls_stale() -> bool:
+    deps = (CALLS_SRC, os.path.join(INCLUDE, "svp.h"))
+    return (not os.path.exists(CALLS_LIB) or
+            any(os.path.getmtime(d) > os.path.getmtime(CALLS_LIB) for d in deps))
+
+
+def _compile_calls() -> str:
+    """Object file of the marshalling module, against torch's headers."""
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    obj = os.path.join(BUILD_DIR, "calls.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-c",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-isystem", inc, "-isystem",
+           os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem",
+           sysconfig.get_paths()["include"], "-isystem",
+           os.path.join(cuda, "include"), CALLS_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for calls.cpp:\n{r.stderr}")
+    return obj
+
+
+def _link_calls(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = CALLS_LIB + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libsvp.so", "-L", lib,
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+           "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stderr}")
+    os.replace(tmp, CALLS_LIB)
+
+
 def build(force: bool = False, ptxas_verbose: bool = False) -> str:
-    """Compile every CUDA source for sm_103a and link libsvp.so (in place)."""
-    if not force and not _stale():
+    """Compile every CUDA source for sm_103a and link libsvp.so, and the
+    Python calls' module beside it (in place)."""
+    kernels, calls = force or _stale(), force or _calls_stale()
+    if not kernels and not calls:
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
     extra = ["-Xptxas", "-v"] if ptxas_verbose else []
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(lambda s: _compile(s, extra), SOURCES))
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls_obj = ex.submit(_compile_calls) if calls else None
+        objs = (list(ex.map(lambda s: _compile(s, extra), SOURCES))
+                if kernels else None)
+        if objs:
+            _link(objs)
+        if calls_obj:
+            _link_calls(calls_obj.result())
+    return LIB
+
+
+def _link(objs) -> None:
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [NVCC] + ARCH + ["-shared", "-o", tmp] + objs
+    cmd = [NVCC] + ARCH + ["-shared", "-Xlinker", "-soname=libsvp.so", "-o",
+                           tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 def build_variant(name: str, defines, force: bool = False) -> str:

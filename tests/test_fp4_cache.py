@@ -53,6 +53,12 @@ def _inputs(seed, lens, hq, hkv, d, q_len, ks=1.0, vs=1.0, width=None):
     return q, kc, vc, table, lens
 
 
+def _dims(bd, batch, hq, cache, max_blocks, split_pages=0, kernel_path=0):
+    nb, hkv, page, row = cache.shape
+    return bd.SvpDims(batch, hq, hkv, row * 16 // 9, page, max_blocks, nb,
+                      bd.SVP_FP4_E2M1, None, 0, split_pages, kernel_path, 1.0, 1.0)
+
+
 def _reference(q, kc, vc, d, scale, lens, table, ks, vs, **mask):
     with np.errstate(invalid="ignore"):
         return R.attention(q, R.values(kc, "fp4", d, ks), R.values(vc, "fp4", d, vs),
@@ -340,7 +346,7 @@ def test_noalloc_and_caller_workspace(svp):
     o2, l2 = svp.paged_decode_attention(*g, scale=0.1, workspace=ws)
     assert torch.equal(out, o2) and torch.equal(lse, l2)
     lib = svp.load_library()
-    dims = bd._paged_dims(3, 6, g[1], table.shape[1], bd.SVP_FP4_E2M1)
+    dims = _dims(bd, 3, 6, g[1], table.shape[1])
     o3, l3 = torch.zeros_like(out), torch.zeros_like(lse)
     st = lib.paged_decode_attention_noalloc(
         ctypes.byref(dims), *(t.data_ptr() for t in g), 2, 0, 0,
@@ -402,8 +408,7 @@ def test_stalled_producer_times_out(svp, path):
     g = [R.to_gpu(q, "bf16"), R.to_gpu(kc), R.to_gpu(vc), R.to_gpu(table), R.to_gpu(lens)]
     out = torch.empty(q.shape, dtype=torch.bfloat16, device="cuda")
     lse = torch.empty(q.shape[:3], device="cuda")
-    dims = bd._paged_dims(2, 12, g[1], table.shape[1], bd.SVP_FP4_E2M1, split_pages=64,
-                          kernel_path=path)
+    dims = _dims(bd, 2, 12, g[1], table.shape[1], split_pages=64, kernel_path=path)
     need = stall.paged_decode_workspace_size(ctypes.byref(dims), 4, 0, 0)
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
     dims.workspace, dims.workspace_bytes = ws.data_ptr(), need
