@@ -256,13 +256,13 @@ constexpr int kMoveWarps = 8;
 constexpr int kMoveRows = 128;  // rows whose addresses a warp works out at once
 
 // The kept rows slot0 .. slot1 - 1 of one (sequence, head): NU vectors of
-// type V each, from vector u0 of rows of `units` vectors.  One warp: it reads
+// type V each, from vector u0 of rows of `row_units` vectors.  One warp: it reads
 // 128 rows' positions and pages, then copies in batches of up to 18 vectors
 // per lane, every batch read before it is written.  Slot i's source is row i
 // or a later one, so no batch writes what a later one reads: safe in place.
 template <typename V, int NU>
 __device__ __forceinline__ void move_rows(const EvictParams &p, V *data,
-                                          int units, int u0, int b, int g,
+                                          int row_units, int u0, int b, int g,
                                           int slot0, int slot1, long long *from,
                                           long long *to) {
   const int lane = threadIdx.x & 31;
@@ -306,14 +306,15 @@ __device__ __forceinline__ void move_rows(const EvictParams &p, V *data,
           atomicOr(&g_status_evict, (unsigned)SVP_DEV_BAD_BLOCK_ID);
         }
       }
-      from[x * 32 + lane] = s < 0 ? -1 : s * units + u0;
-      to[x * 32 + lane] = d * units + u0;
+      from[x * 32 + lane] = s < 0 ? -1 : s * row_units + u0;
+      to[x * 32 + lane] = d * row_units + u0;
       any = any || s >= 0;
     }
     if (!__any_sync(kFull, any)) continue;
     __syncwarp();
+    const int units = min(kMoveRows, slot1 - base) * NU;
 #pragma unroll 1
-    for (int i0 = 0; i0 < NU * RPL; i0 += U) {
+    for (int i0 = 0; i0 * 32 < units; i0 += U) {
       V v[U];
 #pragma unroll
       for (int x = 0; x < U; ++x) {
@@ -378,9 +379,9 @@ __global__ void __launch_bounds__(32 * kMoveWarps)
 template <typename V, int UNITS, int UC>
 cudaError_t launch_compact(const EvictParams &p, int sms, cudaLaunchConfig_t cfg) {
   const long long groups = (long long)p.batch * p.num_kv_heads;
-  // runs of at least 128 rows, enough of them for 32 warps on every SM
+  // enough runs for 32 warps on every SM, but of at least 32 rows
   long long parts = ((long long)sms * 32 + 2 * groups - 1) / (2 * groups);
-  const long long most = (p.budget + kMoveRows - 1) / kMoveRows;
+  const long long most = (p.budget + 31) / 32;
   if (parts > most) parts = most;
   const long long warps = parts > UNITS / UC ? parts : UNITS / UC;
   const long long blocks = (groups * warps + kMoveWarps - 1) / kMoveWarps;

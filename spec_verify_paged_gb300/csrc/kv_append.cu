@@ -143,33 +143,76 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
   const int phys = page_of(p.block_table, p.max_blocks, p.num_blocks, b, pos);
   if (phys < 0) return;
   const float factor = is_v ? p.v_scale : p.k_scale;
-  float y[kFp4Group];
+  float x[kFp4Group], top = 0.f;
   const uint32_t w[8] = {in[0].x, in[0].y, in[0].z, in[0].w,
                          in[1].x, in[1].y, in[1].z, in[1].w};
-  float top = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    y[2 * i] = __uint_as_float(w[i] << 16);
-    y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    top = fmaxf(top, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
   }
-  if (factor != 1.f) {
-#pragma unroll
-    for (int i = 0; i < kFp4Group; ++i) y[i] /= factor;
-  }
-#pragma unroll
-  for (int i = 0; i < kFp4Group; ++i) top = fmaxf(top, fabsf(y[i]));
+  top /= factor;  // division is monotonic: the largest |y|
   __nv_fp8_storage_t sc =
       __nv_cvt_float_to_fp8(top / 6.f, __NV_SATFINITE, __NV_E4M3);
   if (sc == 0) sc = 1;  // the smallest scale, 2^-9: finer than no scale
   const float s =
       __half2float(__half(__nv_cvt_fp8_to_halfraw(sc, __NV_E4M3)));
+  // The codes are those of r = (x / factor) / s, both quotients rounded to
+  // fp32.  Two divisions an element would be most of this kernel's time, so
+  // r is taken as x c, c = (1 / factor) (1 / s), which is within 2^-21 of it,
+  // and looked at where that could matter, next to E2M1's midpoints:
+  //  * factor a power of two: x / factor keeps x's 8 bits and s has 4, so a
+  //    quotient that is no midpoint is at least 2^-12 away from it, and
+  //    rounding x c to 16 bits (Veltkamp's splitting) restores every one
+  //    that is;
+  //  * else: if x c (1 - 2^-20) and x c (1 + 2^-20) have the same code, that
+  //    is r's; a block with one that has not (one in 10^4) divides.
+  // So do blocks whose largest value saturates the scale, and factors so far
+  // from 1 that c might leave fp32's range.
+  const float c = (1.f / factor) * (1.f / s);
   uint32_t code[2] = {0u, 0u};
+  bool sure = c > 0x1p-100f && c < 0x1p100f && top <= 8.f * s;
+  if (sure && (__float_as_uint(factor) & 0x7fffffu) == 0) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __nv_fp4x2_storage_t c = __nv_cvt_float2_to_fp4x2(
-        make_float2(y[2 * i] / s, y[2 * i + 1] / s), __NV_E2M1,
-        cudaRoundNearest);
-    code[i >> 2] |= (uint32_t)c << (8 * (i & 3));
+    for (int i = 0; i < 8; ++i) {
+      float r[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float q = x[2 * i + e] * c;
+        const float t = __fmul_rn(q, 257.f);
+        r[e] = __fsub_rn(t, __fsub_rn(t, q));
+      }
+      code[i >> 2] |= (uint32_t)__nv_cvt_float2_to_fp4x2(
+                          make_float2(r[0], r[1]), __NV_E2M1, cudaRoundNearest)
+                      << (8 * (i & 3));
+    }
+  } else if (sure) {
+    uint32_t high[2] = {0u, 0u};
+    const float c0 = c * (1.f - 0x1p-20f), c1 = c * (1.f + 0x1p-20f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 v = make_float2(x[2 * i], x[2 * i + 1]);
+      code[i >> 2] |=
+          (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(v.x * c0, v.y * c0),
+                                             __NV_E2M1, cudaRoundNearest)
+          << (8 * (i & 3));
+      high[i >> 2] |=
+          (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(v.x * c1, v.y * c1),
+                                             __NV_E2M1, cudaRoundNearest)
+          << (8 * (i & 3));
+    }
+    sure = code[0] == high[0] && code[1] == high[1];
+  }
+  if (!sure) {
+    code[0] = code[1] = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      code[i >> 2] |= (uint32_t)__nv_cvt_float2_to_fp4x2(
+                          make_float2(x[2 * i] / factor / s,
+                                      x[2 * i + 1] / factor / s),
+                          __NV_E2M1, cudaRoundNearest)
+                      << (8 * (i & 3));
   }
   unsigned char *dst =
       static_cast<unsigned char *>(is_v ? p.v_cache : p.k_cache) +
