@@ -280,8 +280,7 @@ int kv_append(const svp_dims *dims, const void *k_new, const void *v_new,
  * caches.  A sequence length outside [0, max_blocks_per_seq*16] gives zero
  * rows and SVP_DEV_BAD_SEQ_LEN, a bad block id a zero row and
  * SVP_DEV_BAD_BLOCK_ID.  Uses no workspace.
- * Errors as for kv_append, with n_rows >= 0 and n_rows * num_kv_heads below
- * 2^31 (else SVP_ERR_UNSUPPORTED). */
+ * Errors as for kv_append, with n_rows >= 0. */
 int kv_gather(const svp_dims *dims, const void *k_cache, const void *v_cache,
               const int32_t *block_table, const int32_t *seq_lens,
               const int32_t *starts, int n_rows, void *k_out, void *v_out,

@@ -491,9 +491,6 @@ int kv_gather(const svp_dims *dims, const void *k_cache, const void *v_cache,
        reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) %
           16 != 0)
     return SVP_ERR_INVALID_ARG;
-  // rows of a sequence are counted in 32 bits
-  if ((long long)n_rows * dims->num_kv_heads >= (1LL << 31))
-    return SVP_ERR_UNSUPPORTED;
   GatherParams p;
   p.k_cache = k_cache;
   p.v_cache = v_cache;

@@ -93,13 +93,12 @@ __global__ void __launch_bounds__(kSelThreads)
       kept[i] = !bad && i < L ? i : -1;
     return;
   }
-  // this CTA's positions [lo, hi): whole pages; a thread's run of `run` of
-  // them: odd, so that a warp's runs start in different banks
+  // this CTA's positions [lo, hi): whole pages
   const int per = ((L + nc - 1) / nc + kBlockSize - 1) / kBlockSize * kBlockSize;
   const int lo = min(rank * per, L), hi = min(lo + per, L);
-  const int run = ((per + kSelThreads - 1) / kSelThreads) | 1;
   const bool cached = per <= cache_cap;
   const int mid0 = p.n_sink, mid1 = L - p.n_recent;  // the candidates
+  const int c0 = max(lo, mid0), c1 = min(hi, mid1);  // this CTA's
   const int32_t *const table = p.block_table + (size_t)b * p.max_blocks;
   // where position j's page keeps this head's scores, or null
   auto page_scores = [&](int j) -> const float * {
@@ -148,9 +147,10 @@ __global__ void __launch_bounds__(kSelThreads)
                                  score_key(v[u].z), score_key(v[u].w)};
         *reinterpret_cast<uint4 *>(keys + (j - lo)) =
             make_uint4(key[0], key[1], key[2], key[3]);
+        const bool inside = j >= c0 && j + 4 <= c1;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (j + e >= mid0 && j + e < min(mid1, hi))
+          if (inside || (j + e >= c0 && j + e < c1))
             atomicAdd(&sm.hist[0][key[e] >> 21], 1u);
       }
     }
@@ -160,12 +160,15 @@ __global__ void __launch_bounds__(kSelThreads)
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const int bits = pass == 2 ? 10 : 11;
     unsigned *const hist = sm.hist[pass & 1];
+    // (shift + bits is 32 in the first pass: everything matches)
+    const int above_bits = pass == 0 ? 31 : shift + bits;
+    const unsigned match = pass == 0 ? 0u : prefix >> above_bits;
+    auto tally = [&](unsigned key) {
+      if (pass == 0 || (key >> above_bits) == match)
+        atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1u)], 1u);
+    };
     if (pass > 0 || !cached) {
-      for (int j = max(lo, mid0) + tid; j < min(hi, mid1); j += kSelThreads) {
-        const unsigned key = key_of(j);
-        if (pass == 0 || (key >> (shift + bits)) == (prefix >> (shift + bits)))
-          atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1u)], 1u);
-      }
+      for (int j = c0 + tid; j < c1; j += kSelThreads) tally(key_of(j));
     }
     if (nc > 1) cluster.sync(); else __syncthreads();
     // bins from the largest down, four per thread, summed over the cluster
@@ -221,17 +224,33 @@ __global__ void __launch_bounds__(kSelThreads)
   // kept: keys above `prefix`, and the first `need` of those equal to it
 
   // ---- number the kept positions ----
-  const int j_begin = min(lo + tid * run, hi), j_end = min(j_begin + run, hi);
+  // a warp numbers a run of them, 32 at a time: once to count, and once more,
+  // with the counts before it known, to write
+  constexpr int NW = kSelThreads / 32;
+  const int lane = tid & 31, warp = tid >> 5;
+  const int w_run = (per + 32 * NW - 1) / (32 * NW) * 32;
+  const int w0 = min(lo + warp * w_run, hi), w1 = min(w0 + w_run, hi);
+  auto look = [&](int j, bool &for_sure, bool &is_tied) {
+    for_sure = is_tied = false;
+    if (j < w1) {
+      const unsigned key = key_of(j);
+      const bool forced = j < mid0 || j >= mid1;
+      for_sure = forced || key > prefix;  // (k = 0: no key is above)
+      is_tied = !forced && key == prefix;
+    }
+  };
   unsigned sure = 0, tied = 0;
-  for (int j = j_begin; j < j_end; ++j) {
-    const unsigned key = key_of(j);
-    const bool forced = j < mid0 || j >= mid1;
-    sure += forced || (k > 0 && key > prefix);
-    tied += !forced && key == prefix;
+#pragma unroll 4
+  for (int j = w0; j < w1; j += 32) {
+    bool a, t;
+    look(j + lane, a, t);
+    sure += __popc(__ballot_sync(kFull, a));
+    tied += __popc(__ballot_sync(kFull, t));
   }
   unsigned long long sum;
-  const unsigned long long mine = ((unsigned long long)sure << 32) | tied;
-  unsigned long long before = block_scan<unsigned long long>(mine, sm.warp_sum, sum);
+  unsigned long long before = block_scan<unsigned long long>(
+      lane == 0 ? ((unsigned long long)sure << 32) | tied : 0, sm.warp_sum, sum);
+  before = __shfl_sync(kFull, before, 0);
   if (nc > 1) {
     if (tid == 0) sm.total = sum;
     cluster.sync();
@@ -239,14 +258,18 @@ __global__ void __launch_bounds__(kSelThreads)
       before += *cluster.map_shared_rank(&sm.total, r);
   }
   unsigned n_sure = (unsigned)(before >> 32), n_tied = (unsigned)before;
-  for (int j = j_begin; j < j_end; ++j) {
-    const unsigned key = key_of(j);
-    const bool forced = j < mid0 || j >= mid1;
-    const bool is_tied = !forced && key == prefix;
-    if (forced || (k > 0 && key > prefix) || (is_tied && n_tied < need))
-      kept[n_sure + min(n_tied, need)] = j;
-    n_sure += forced || (k > 0 && key > prefix);
-    n_tied += is_tied;
+  const unsigned lower = (1u << lane) - 1u;
+#pragma unroll 4
+  for (int j = w0; j < w1; j += 32) {
+    bool a, t;
+    look(j + lane, a, t);
+    const unsigned all_a = __ballot_sync(kFull, a);
+    const unsigned all_t = __ballot_sync(kFull, t);
+    const unsigned ties = n_tied + __popc(all_t & lower);
+    if (a || (t && ties < need))
+      kept[n_sure + __popc(all_a & lower) + min(ties, need)] = j + lane;
+    n_sure += __popc(all_a);
+    n_tied += __popc(all_t);
   }
   if (nc > 1) cluster.sync();  // no CTA leaves while its totals may be read
 }

@@ -224,103 +224,115 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
   dst[NB * 8 + blk] = sc;
 }
 
-// Rows back as values: a lane writes 16 bytes (8 bf16 or 4 fp32 elements) of
-// a K row and of the V row beside it; a sequence's rows along x, the
+// Rows back as values: a warp to a position (or to a share of its heads), so
+// that the page is looked up once; a lane writes 16 bytes (8 bf16 or 4 fp32
+// elements) of a K row and of the V row beside it.  Positions along x, the
 // sequences along y.  Bound by the output bytes.
 template <int DT, int D>
 __global__ void __launch_bounds__(32 * kAppendWarps)
-    kv_gather_kernel(const GatherParams p) {
+    kv_gather_kernel(const GatherParams p, int shares) {
   constexpr int PER = DT == SVP_F32 ? 4 : 8;  // elements of a lane
   constexpr int NC = D / PER;                 // lanes of a row
   constexpr int ROWB = DT == SVP_F32 ? 4 * D : DT == SVP_BF16 ? 2 * D
                        : DT == SVP_FP8_E4M3 ? D : fp4_row_bytes(D);
   pdl_launch_dependents();
   const int b = blockIdx.y;
-  const long long idx =
-      (long long)blockIdx.x * (32 * kAppendWarps) + threadIdx.x;
-  const unsigned row = (unsigned)(idx / NC);  // (i, g)
-  const int c = threadIdx.x % NC;
-  if (row >= (unsigned)p.n_rows * (unsigned)p.num_kv_heads) return;
-  const unsigned i = row / p.num_kv_heads, g = row % p.num_kv_heads;
+  const unsigned item = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+  const unsigned i = item / shares, share = item % shares;
+  if (i >= (unsigned)p.n_rows) return;
   const int L = p.seq_lens[b];
   int phys = -1;
   long long pos = 0;
   if (L < 0 || L > (long long)p.max_blocks * kBlockSize) {
-    if (c == 0) atomicOr(&g_status_append, (unsigned)SVP_DEV_BAD_SEQ_LEN);
+    if (threadIdx.x % 32 == 0)
+      atomicOr(&g_status_append, (unsigned)SVP_DEV_BAD_SEQ_LEN);
   } else {
     pos = (p.starts ? (long long)p.starts[b] : (long long)L - p.n_rows) + i;
     if (pos >= 0 && pos < L)
       phys = page_of(p.block_table, p.max_blocks, p.num_blocks, b, (int)pos);
   }
-  uint4 out[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-  if (phys >= 0) {
-    const size_t at = (((size_t)phys * p.num_kv_heads + g) * kBlockSize +
-                       (size_t)(pos % kBlockSize)) * ROWB;
-    const unsigned char *const src[2] = {
-        static_cast<const unsigned char *>(p.k_cache) + at,
-        static_cast<const unsigned char *>(p.v_cache) + at};
-    if constexpr (DT == SVP_F32 || DT == SVP_BF16) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        out[s] = __ldg(reinterpret_cast<const uint4 *>(src[s]) + c);
-    } else {
-      uint32_t h[2][4];  // fp16 pairs of the 8 values before the factor
-      if constexpr (DT == SVP_FP8_E4M3) {
-        uint2 w[2];
-#pragma unroll
+  // head g's row, 16 rows further on for the next head
+  const size_t first =
+      ((size_t)(phys < 0 ? 0 : phys) * p.num_kv_heads * kBlockSize +
+       (size_t)(pos & (kBlockSize - 1))) * ROWB;
+  const size_t to0 = ((size_t)b * p.n_rows + i) * p.num_kv_heads * NC;
+#pragma unroll 2
+  for (int j = share * 32 + threadIdx.x % 32; j < p.num_kv_heads * NC;
+       j += 32 * shares) {
+    const int g = j / NC, c = j % NC;
+    uint4 out[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (phys >= 0) {
+      const size_t at = first + (size_t)g * (kBlockSize * ROWB);
+      const unsigned char *const src[2] = {
+          static_cast<const unsigned char *>(p.k_cache) + at,
+          static_cast<const unsigned char *>(p.v_cache) + at};
+      if constexpr (DT == SVP_F32 || DT == SVP_BF16) {
+  #pragma unroll
         for (int s = 0; s < 2; ++s)
-          w[s] = __ldg(reinterpret_cast<const uint2 *>(src[s]) + c);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          h[s][0] = e4m3x2_f16x2(w[s].x);
-          h[s][1] = e4m3x2_f16x2(w[s].x >> 16);
-          h[s][2] = e4m3x2_f16x2(w[s].y);
-          h[s][3] = e4m3x2_f16x2(w[s].y >> 16);
-        }
+          out[s] = __ldg(reinterpret_cast<const uint4 *>(src[s]) + c);
       } else {
-        uint32_t w[2], sc[2];
-#pragma unroll
+        uint32_t h[2][4];  // fp16 pairs of the 8 values before the factor
+        if constexpr (DT == SVP_FP8_E4M3) {
+          uint2 w[2];
+  #pragma unroll
+          for (int s = 0; s < 2; ++s)
+            w[s] = __ldg(reinterpret_cast<const uint2 *>(src[s]) + c);
+  #pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            h[s][0] = e4m3x2_f16x2(w[s].x);
+            h[s][1] = e4m3x2_f16x2(w[s].x >> 16);
+            h[s][2] = e4m3x2_f16x2(w[s].y);
+            h[s][3] = e4m3x2_f16x2(w[s].y >> 16);
+          }
+        } else {
+          uint32_t w[2], sc[2];
+  #pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            w[s] = __ldg(reinterpret_cast<const uint32_t *>(src[s]) + c);
+            sc[s] = __ldg(src[s] + D / 2 + c / 2);
+          }
+  #pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const uint32_t s2 = e4m3x2_f16x2(sc[s] * 0x101u);
+            e2m1x8_h2(w[s], h[s]);
+  #pragma unroll
+            for (int x = 0; x < 4; ++x) h[s][x] = hmul2(h[s][x], s2);
+          }
+        }
+  #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          w[s] = __ldg(reinterpret_cast<const uint32_t *>(src[s]) + c);
-          sc[s] = __ldg(src[s] + D / 2 + c / 2);
+          const float scale = s ? p.v_scale : p.k_scale;
+          uint32_t o[4];
+  #pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float2 f =
+                __half22float2(*reinterpret_cast<const __half2 *>(&h[s][x]));
+            const __nv_bfloat162 v =
+                __floats2bfloat162_rn(f.x * scale, f.y * scale);
+            o[x] = *reinterpret_cast<const uint32_t *>(&v);
+          }
+          out[s] = make_uint4(o[0], o[1], o[2], o[3]);
         }
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const uint32_t s2 = e4m3x2_f16x2(sc[s] * 0x101u);
-          e2m1x8_h2(w[s], h[s]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) h[s][j] = hmul2(h[s][j], s2);
-        }
-      }
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const float scale = s ? p.v_scale : p.k_scale;
-        uint32_t o[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f =
-              __half22float2(*reinterpret_cast<const __half2 *>(&h[s][j]));
-          const __nv_bfloat162 v =
-              __floats2bfloat162_rn(f.x * scale, f.y * scale);
-          o[j] = *reinterpret_cast<const uint32_t *>(&v);
-        }
-        out[s] = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
+    static_cast<uint4 *>(p.k_out)[to0 + j] = out[0];
+    static_cast<uint4 *>(p.v_out)[to0 + j] = out[1];
   }
-  const size_t to =
-      ((size_t)b * p.n_rows * p.num_kv_heads + row) * NC + c;
-  static_cast<uint4 *>(p.k_out)[to] = out[0];
-  static_cast<uint4 *>(p.v_out)[to] = out[1];
 }
 
 template <int DT, int D>
 static cudaError_t gather_t(const GatherParams &p, cudaStream_t stream) {
-  constexpr int T = 32 * kAppendWarps;
-  const long long lanes =
-      (long long)p.n_rows * p.num_kv_heads * (D / (DT == SVP_F32 ? 4 : 8));
-  kv_gather_kernel<DT, D><<<dim3((unsigned)((lanes + T - 1) / T),
-                                 (unsigned)p.batch), T, 0, stream>>>(p);
+  // one warp to a position when there are many, else as many as its lanes
+  // fill (a decode step's few rows: the latency of one round of loads)
+  const int full = (p.num_kv_heads * (D / (DT == SVP_F32 ? 4 : 8)) + 31) / 32;
+  const long long positions = (long long)p.batch * p.n_rows;
+  const int shares = positions >= 4096 ? 1
+                     : (int)(4096 / positions < full ? 4096 / positions : full);
+  const long long blocks =
+      ((long long)p.n_rows * shares + kAppendWarps - 1) / kAppendWarps;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  kv_gather_kernel<DT, D><<<dim3((unsigned)blocks, (unsigned)p.batch),
+                            32 * kAppendWarps, 0, stream>>>(p, shares);
   return cudaGetLastError();
 }
 
