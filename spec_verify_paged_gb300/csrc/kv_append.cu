@@ -267,17 +267,17 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
           static_cast<const unsigned char *>(p.k_cache) + at,
           static_cast<const unsigned char *>(p.v_cache) + at};
       if constexpr (DT == SVP_F32 || DT == SVP_BF16) {
-  #pragma unroll
+#pragma unroll
         for (int s = 0; s < 2; ++s)
           out[s] = __ldg(reinterpret_cast<const uint4 *>(src[s]) + c);
       } else {
         uint32_t h[2][4];  // fp16 pairs of the 8 values before the factor
         if constexpr (DT == SVP_FP8_E4M3) {
           uint2 w[2];
-  #pragma unroll
+#pragma unroll
           for (int s = 0; s < 2; ++s)
             w[s] = __ldg(reinterpret_cast<const uint2 *>(src[s]) + c);
-  #pragma unroll
+#pragma unroll
           for (int s = 0; s < 2; ++s) {
             h[s][0] = e4m3x2_f16x2(w[s].x);
             h[s][1] = e4m3x2_f16x2(w[s].x >> 16);
@@ -286,24 +286,24 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
           }
         } else {
           uint32_t w[2], sc[2];
-  #pragma unroll
+#pragma unroll
           for (int s = 0; s < 2; ++s) {
             w[s] = __ldg(reinterpret_cast<const uint32_t *>(src[s]) + c);
             sc[s] = __ldg(src[s] + D / 2 + c / 2);
           }
-  #pragma unroll
+#pragma unroll
           for (int s = 0; s < 2; ++s) {
             const uint32_t s2 = e4m3x2_f16x2(sc[s] * 0x101u);
             e2m1x8_h2(w[s], h[s]);
-  #pragma unroll
+#pragma unroll
             for (int x = 0; x < 4; ++x) h[s][x] = hmul2(h[s][x], s2);
           }
         }
-  #pragma unroll
+#pragma unroll
         for (int s = 0; s < 2; ++s) {
           const float scale = s ? p.v_scale : p.k_scale;
           uint32_t o[4];
-  #pragma unroll
+#pragma unroll
           for (int x = 0; x < 4; ++x) {
             const float2 f =
                 __half22float2(*reinterpret_cast<const __half2 *>(&h[s][x]));

@@ -51,6 +51,8 @@ SCORES = [
     ("fp4", 128, 4, 4, 1, [1, 40, 300], dict(n_sink=20, window=1), 1.0),
     ("fp4", 128, 16, 4, 15, [15, 40, 300], "tree", 1.0),
     ("f32", 64, 2, 2, 6, [6, 40], "tree", 1.0),
+    ("fp4", 128, 32, 2, 16, [16, 150], "tree", 1.0),        # 256 rows: two launches
+    ("fp8", 128, 40, 2, 7, [7, 60], dict(n_sink=3, window=5), 1.0),  # 140 rows
 ]
 
 
@@ -129,6 +131,8 @@ EVICT = [
     ("f32", 128, 1, [128, 129], 128, 0, 128),
     ("bf16", 64, 2, [5000, 4097], 4000, 4, 64),            # two CTAs a group
     ("fp4", 128, 1, [33000], 1000, 4, 100),                # eight
+    ("bf16", 128, 2, [3000, 900, 2999], 2999, 0, 0),       # one row goes
+    ("fp8", 64, 3, [700, 0, 17], 16, 16, 0),
 ]
 
 
@@ -197,6 +201,43 @@ def test_evict_in_place_through_an_equal_table(svp):
     assert np.array_equal(gl.cpu().numpy(), ref_lens)
     for got, want in zip(g, _apply([kc, vc, s], ref, table, table)):
         assert np.array_equal(_raw(got), want)
+
+
+def test_two_evictions_at_once_and_replayed(svp):
+    """Two streams evict different sequences of one cache at the same time;
+    a captured eviction replayed on restored caches gives the same bytes."""
+    import torch
+    kc, vc, s, table, lens, dst = _evict_inputs("bf16", 128, 2, [1500, 1400, 900], 400)
+    first = [R.to_gpu(kc, "bf16"), R.to_gpu(vc, "bf16"), R.to_gpu(s)]
+    gt, gl = R.to_gpu(table), R.to_gpu(lens)
+    kept, new = svp.kv_evict(*first, gt, gl, 400, 4, 16)
+    g = [R.to_gpu(kc, "bf16"), R.to_gpu(vc, "bf16"), R.to_gpu(s)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    parts = []
+    for st, rows in zip(streams, (slice(0, 1), slice(1, 3))):
+        with torch.cuda.stream(st):
+            parts.append(svp.kv_evict(*g, gt[rows].contiguous(), gl[rows].contiguous(),
+                                      400, 4, 16))
+    torch.cuda.synchronize()
+    assert torch.equal(torch.cat([p[0] for p in parts]), kept)
+    for a, b in zip(g, first):
+        assert torch.equal(a, b)
+    start = [R.to_gpu(kc, "bf16"), R.to_gpu(vc, "bf16"), R.to_gpu(s)]
+    for t, x in zip(g, start):
+        t.copy_(x)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        k2, n2 = svp.kv_evict(*g, gt, gl, 400, 4, 16)
+    for _ in range(2):
+        for t, x in zip(g, start):
+            t.copy_(x)
+        k2.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(k2, kept) and torch.equal(n2, new)
+        for a, b in zip(g, first):
+            assert torch.equal(a, b)
 
 
 @pytest.mark.parametrize("kind", ["zero", "signs", "nan", "inf", "equal", "tiny"])

@@ -139,6 +139,88 @@ def test_append_extremes(svp):
     assert v[2, 40] == 6 * 0.25 and v[2, 41] == 1.5           # NaN: largest code
 
 
+@pytest.mark.parametrize("ks", [1.0, 0.5, 3.0, 0.1, 1e-3, 7.0, 1e-30, 3e37])
+def test_append_near_every_rounding_border(svp, ks):
+    """Byte for byte where a quotient lies on, or one bf16 step beside, a
+    border between codes or between block scales; and every bf16 mantissa as
+    a block's largest value."""
+    import torch
+    d, hkv = 128, 4
+    rng = np.random.default_rng(6)
+    f32 = np.float32
+    blocks = []
+    mant = (1 + np.arange(128) / 128.0)
+    tops = np.concatenate([mant * 2.0 ** e for e in (-12, -9, -3, 0, 4, 11, 12)])
+    # largest values whose sixth is a border between two E4M3 scales
+    mids = (R.E4M3[:126] + R.E4M3[1:127]) / 2 * 6
+    tops = np.concatenate([tops, mids])
+    for top in tops:
+        top = min(float(top) * float(f32(ks)), 3e38)
+        top = float(R.bf16(np.array([top]))[0])
+        y = float(f32(f32(top) / f32(ks)))
+        sc = R.E4M3[max(int(R.e4m3_code(np.array([float(f32(y) / f32(6))]))[0]), 1)]
+        near = []
+        for lo, hi in zip(R.E2M1[:-1], R.E2M1[1:]):
+            x = float(R.bf16(np.array([min((lo + hi) / 2 * sc * ks, 3e38)]))[0])
+            near += [x, np.nextafter(f32(x), f32(0)) if x else 0.0]
+        x = np.array([top] + near + [0.0] * 16)[:16]
+        x = np.minimum(np.abs(R.bf16(x)), top)
+        # a bf16 step up or down, and signs
+        u = x.astype(f32).view(np.uint32) + (rng.integers(-1, 2, 16) * 65536).astype(np.int64)
+        x = np.maximum(u, 0).astype(np.uint32).view(f32).astype(np.float64)
+        x = np.minimum(x, top)
+        x[0] = top
+        blocks.append(rng.permutation(x) * rng.choice([-1.0, 1.0], 16))
+    per = hkv * d // 16
+    n = -(-len(blocks) // per)
+    blocks += [np.zeros(16)] * (n * per - len(blocks))
+    x = R.bf16(np.stack(blocks).reshape(1, n, hkv, d))
+    t = R.to_gpu(x, "bf16")
+    width = -(-n // 16)
+    gk = torch.zeros((width, hkv, 16, svp.fp4_row_bytes(d)), dtype=torch.uint8, device="cuda")
+    gv = torch.zeros_like(gk)
+    gt = torch.arange(width, dtype=torch.int32, device="cuda").view(1, -1)
+    gl = torch.full((1,), n, dtype=torch.int32, device="cuda")
+    svp.kv_append(t, t, gk, gv, gt, gl, k_scale=ks, v_scale=ks)
+    got = gk.cpu().numpy().transpose(0, 2, 1, 3).reshape(width * 16, hkv, -1)[:n]
+    with np.errstate(over="ignore"):
+        want = R.quantise(x[0], ks)
+    # (a zero quotient keeps its sign here, not in the reference)
+    zero = np.zeros(x[0].shape, np.uint8)
+    zero[(x[0].astype(f32) / f32(ks) == 0) & np.signbit(x[0])] = 8
+    want[..., :d // 2] |= zero[..., 0::2] | (zero[..., 1::2] << 4)
+    assert np.array_equal(got, want)
+    assert torch.equal(gk, gv)
+
+
+def test_append_of_random_bit_patterns(svp):
+    """Finite bf16 patterns at random, against factors at random."""
+    import torch
+    rng = np.random.default_rng(9)
+    B, n, hkv, d = 8, 64, 2, 64
+    gt = torch.arange(B * n // 16, dtype=torch.int32, device="cuda").view(B, -1)
+    gl = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    for ks in np.exp(rng.uniform(-80, 80, 6)).astype(np.float32):
+        u = rng.integers(0, 65536, (B, n, hkv, d)).astype(np.uint32) << 16
+        with np.errstate(invalid="ignore"):
+            x = u.view(np.float32).astype(np.float64)
+        x = np.where(np.isfinite(x), x, 1.0)
+        # half of the rows within a factor of 64, where the codes vary
+        y = float(ks) * R.bf16(rng.standard_normal(x.shape) * np.exp(rng.uniform(-4, 4, x.shape)))
+        x = np.where(rng.random((B, n, hkv, 1)) < 0.5, R.bf16(np.clip(y, -3e38, 3e38)), x)
+        t = R.to_gpu(x, "bf16")
+        gk = torch.zeros((B * n // 16, hkv, 16, svp.fp4_row_bytes(d)), dtype=torch.uint8,
+                         device="cuda")
+        gv = torch.zeros_like(gk)
+        svp.kv_append(t, t, gk, gv, gt, gl, k_scale=float(ks), v_scale=float(ks))
+        got = gk.cpu().numpy().transpose(0, 2, 1, 3).reshape(B, n, hkv, -1)
+        with np.errstate(over="ignore"):
+            want = R.quantise(x, ks)
+        # (values: a zero's sign does not count)
+        assert np.array_equal(got[..., d // 2:], want[..., d // 2:])
+        assert np.array_equal(R.values(got, "fp4", d), R.values(want, "fp4", d))
+
+
 @pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 128), ("fp8", 64),
                                      ("fp8", 128), ("fp4", 64), ("fp4", 128)])
 def test_gather_positions(svp, dtype, d):
@@ -270,6 +352,156 @@ def test_many_splits_and_wide_table(svp, ql):
     again, lse2 = svp.paged_decode_attention(*g, scale=0.1)
     assert torch.equal(out, again) and torch.equal(lse, lse2)
     _check(out, lse, _reference(q, kc, vc, d, float(np.float32(0.1)), lens, table, 1.0, 1.0), d)
+
+
+@pytest.mark.parametrize("width", [4, 40])
+def test_more_sequences_than_a_launch_takes(svp, width):
+    """1100 sequences, in several launches; 4 pages a sequence at most (a
+    warp takes one whole) and a wide table (slices)."""
+    rng = np.random.default_rng(width)
+    lens = rng.integers(1, 65, 1100)
+    q, kc, vc, table, lens = _inputs(5, lens, 2, 1, 64, 1, width=width)
+    out, lse = svp.paged_decode_attention(
+        R.to_gpu(q, "bf16"), R.to_gpu(kc), R.to_gpu(vc), R.to_gpu(table),
+        R.to_gpu(lens), scale=0.125)
+    assert svp.read_device_status() == 0
+    _check(out, lse, _reference(q, kc, vc, 64, 0.125, lens, table, 1.0, 1.0), 64)
+
+
+@pytest.mark.parametrize("path", [2, 3])
+def test_rows_that_see_nothing(svp, path):
+    """A tree mask without any bit over a sequence of the new rows only: zero
+    output and lse -inf; the other sequence is as without them."""
+    import torch
+    d, ql = 128, 5
+    q, kc, vc, table, lens = _inputs(13, [ql, 77], 8, 2, d, ql)
+    tree = np.stack([np.zeros(ql, np.int32), R.binary_tree(ql)])
+    tree[0, 3] = 0b1000                       # one row of it sees itself
+    g = [R.to_gpu(q, "bf16"), R.to_gpu(kc), R.to_gpu(vc), R.to_gpu(table), R.to_gpu(lens)]
+    mask = R.to_gpu(tree)
+    out, lse = svp.paged_tree_attention(*g, mask, scale=0.1, kernel_path=path)
+    none = [0, 1, 2, 4]
+    assert (out[0, none] == 0).all() and (lse[0, none] == -float("inf")).all()
+    s = float(np.float32(0.1))
+    k3 = R.values(kc, "fp4", d)[table[0, 0], :, 3]
+    v3 = R.values(vc, "fp4", d)[table[0, 0], :, 3]
+    for h in range(8):
+        x = float(k3[h // 4] @ q[0, 3, h]) * s
+        assert abs(float(lse[0, 3, h]) - x) <= 2.0 ** -16 * (1 + np.abs(k3[h // 4]) @ np.abs(q[0, 3, h]))
+        got = out[0, 3, h].double().cpu().numpy()
+        assert (np.abs(got - v3[h // 4]) <= (2.0 ** -8 + 2.0 ** -9) * np.abs(v3[h // 4])).all()
+    ref = _reference(q[1:], kc, vc, d, s, lens[1:], table[1:], 1.0, 1.0, tree=tree[1:])
+    _check(out[1:], lse[1:], ref, d)
+    # the score update of the same rows: rows that see nothing add nothing
+    scores = torch.zeros((kc.shape[0], 2, 16), device="cuda")
+    svp.paged_score_update(g[0], g[1], lse, g[3], g[4], scores, scale=0.1, tree_mask=mask)
+    first = scores[int(table[0, 0])].cpu().numpy()
+    assert (first[:, [0, 1, 2] + list(range(4, 16))] == 0).all()
+    # four rows of weight exp(0): the score and the lse each round
+    assert np.abs(first[:, 3] - 4).max() < 1e-3
+    if hasattr(torch, "uint32"):
+        o2, l2 = svp.paged_tree_attention(*g, mask.view(torch.uint32), scale=0.1,
+                                          kernel_path=path)
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+def test_offsets_beyond_32_bits(svp):
+    """Pages on both sides of 4 GB of cache: append, attention, gather, score
+    update and eviction give what they give on a small cache."""
+    import torch
+    d, hkv, hq = 128, 8, 16
+    total = 5 * 10 ** 9 // (hkv * 16 * 72)
+    free, _ = torch.cuda.mem_get_info()
+    if free < 14 * 10 ** 9:
+        pytest.skip("not enough device memory")
+    rng = np.random.default_rng(12)
+    lens = np.array([200, 64], np.int32)
+    small = rng.permutation(26).astype(np.int32).reshape(2, 13)
+    far = np.sort(rng.choice(np.r_[0:40, total - 60:total], 26, replace=False))
+    far = rng.permutation(far).astype(np.int32)
+    x = [torch.randn((2, 64, hkv, d), device="cuda").to(torch.bfloat16) for _ in range(2)]
+    q = torch.randn((2, 1, hq, d), device="cuda").to(torch.bfloat16)
+    results = []
+    for n, ids in ((26, np.arange(26)), (total, far)):
+        kc = torch.zeros((n, hkv, 16, 72), dtype=torch.uint8, device="cuda")
+        vc = torch.zeros_like(kc)
+        s = torch.zeros((n, hkv, 16), device="cuda")
+        gt = R.to_gpu(ids[small].astype(np.int32))
+        for L in (64, 128, 192, 200):          # sequence 0 grows
+            svp.kv_append(*x, kc, vc, gt, R.to_gpu(np.array([L, 64], np.int32)))
+        gl = R.to_gpu(lens)
+        out, lse = svp.paged_decode_attention(q, kc, vc, gt, gl)
+        svp.paged_score_update(q, kc, lse, gt, gl, s)
+        rows = svp.kv_gather(kc, vc, gt, gl, 200)
+        kept, new = svp.kv_evict(kc, vc, s, gt, gl, 48, 4, 8)
+        after = svp.kv_gather(kc, vc, gt, new, 48)
+        at = R.to_gpu(ids.astype(np.int64))
+        results.append([out, lse, *rows, kept, new, *after, s[at], kc[at], vc[at]])
+        assert svp.read_device_status() == 0
+        del kc, vc, s
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
+def test_calls_on_a_stream_of_their_own(svp):
+    """The whole step on a side stream while the current one is busy, outputs
+    made by the call: as on the current stream."""
+    import torch
+    d, hkv, hq = 128, 2, 8
+    q, kc, vc, table, lens = _inputs(41, [300, 90], hq, hkv, d, 1)
+    rng = np.random.default_rng(1)
+    new = [R.to_gpu(R.bf16(rng.standard_normal((2, 1, hkv, d))), "bf16") for _ in range(2)]
+    gq, gt, gl = R.to_gpu(q, "bf16"), R.to_gpu(table), R.to_gpu(lens)
+    side = torch.cuda.Stream()
+    results = []
+    for stream in (None, side):
+        k, v = R.to_gpu(kc), R.to_gpu(vc)
+        s = torch.zeros((kc.shape[0], hkv, 16), device="cuda")
+        torch.cuda.synchronize()
+        if stream is not None:     # the current stream lags behind
+            busy = torch.randn((4096, 4096), device="cuda")
+            for _ in range(20):
+                busy = busy @ busy * 1e-3
+        svp.kv_append(*new, k, v, gt, gl, stream=stream)
+        out, lse = svp.paged_decode_attention(gq, k, v, gt, gl, stream=stream)
+        svp.paged_score_update(gq, k, lse, gt, gl, s, stream=stream)
+        kept, n = svp.kv_evict(k, v, s, gt, gl, 80, 4, 8, stream=stream)
+        rows = svp.kv_gather(k, v, gt, n, 80, stream=stream)
+        torch.cuda.synchronize()
+        results.append([out, lse, s, kept, n, *rows, k, v])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
+def test_empty_calls_and_layouts(svp):
+    """No rows, no sequences; a transposed cache, a sliced query and a wrong
+    device are refused."""
+    import torch
+    q, kc, vc, table, lens = _inputs(43, [30, 9], 4, 2, 64, 1)
+    g = [R.to_gpu(q, "bf16"), R.to_gpu(kc), R.to_gpu(vc), R.to_gpu(table), R.to_gpu(lens)]
+    k, v = svp.kv_gather(*g[1:], 0)
+    assert tuple(k.shape) == (2, 0, 2, 64) == tuple(v.shape)
+    none = [g[0][:0], *g[1:3], g[3][:0], g[4][:0]]
+    out, lse = svp.paged_decode_attention(*none)
+    assert out.shape[0] == 0 and lse.shape[0] == 0
+    s = torch.ones((kc.shape[0], 2, 16), device="cuda")
+    svp.paged_score_update(none[0], none[1], lse, *none[3:], s)
+    kept, n = svp.kv_evict(*none[1:3], s, *none[3:], 8)
+    assert kept.shape[0] == 0 and n.shape[0] == 0 and (s == 1).all()
+    wide = torch.zeros((2, 1, 8, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        svp.paged_decode_attention(wide[:, :, ::2], *g[1:])
+    with pytest.raises(ValueError):
+        svp.kv_gather(g[1].transpose(0, 1), g[2].transpose(0, 1), *g[3:], 1)
+    with pytest.raises(ValueError):
+        svp.kv_gather(*g[1:4], g[4].cpu(), 1)
+    with pytest.raises(ValueError):
+        svp.paged_decode_attention(*g[:4], g[4].long())
+    with pytest.raises(ValueError):
+        svp.kv_evict(*g[1:3], s.double(), *g[3:], 8)
+    with pytest.raises(TypeError):
+        svp.kv_gather(g[1], None, *g[3:], 1)
+    assert svp.read_device_status() == 0
 
 
 @pytest.mark.parametrize("path", [2, 3])
