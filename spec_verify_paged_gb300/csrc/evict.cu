@@ -9,11 +9,22 @@
 //    each with a run of positions; scores are read from memory once and
 //    their ordered keys kept in shared memory (beyond 16,384 positions per
 //    CTA they are read again each pass).  The histograms are added across
-//    the cluster through distributed shared memory.  Bound by one read of
-//    the scores and, for short contexts, by the chain of passes.
-//  * compact_kernel: moves the kept rows of K, V and the scores, every warp
-//    a run of rows (in place: of columns) of one group by itself.  Bound by
-//    the moved bytes, read and written.
+//    the cluster through distributed shared memory.  Bound by latency, not
+//    by the scores' bytes: a load of page id and scores, three rounds of
+//    histogram, cluster barrier and scan, and the numbering (131,072
+//    positions on eight CTAs: 12-16, 10, 10, 5 and 14 thousand cycles, 27 us;
+//    the 17 MB of scores of 32 such groups are 2.5 us).  Sixteen CTAs per
+//    cluster were slower (four sequences of 131,072: 214 us in all against
+//    164: such clusters find room on few GPCs at a time), and so were four
+//    keys to a read in the later passes on short contexts.
+//  * compact_kernel: moves the kept rows of K, V and the scores, a cluster to
+//    a group and side.  Bound by the moved bytes, read and written, and by
+//    the partly used sectors at both ends of a row.
+// Measured (both kernels): 32 sequences of 32 heads, 2200 to 4096 positions,
+// 2048 kept, bf16 rows of 256 bytes, to other pages: 360 us, 0.90 of the
+// bytes' time at the copy rate; one sequence of 8 heads, 1024 of 1087: 10 us.
+// 4096 of 4200 positions of one sequence: 21 us in place or not (by columns
+// of 64 bytes, a warp to a column, in place took 77).
 #include <cooperative_groups.h>
 
 #include <cstdint>
@@ -278,44 +289,61 @@ __global__ void __launch_bounds__(kSelThreads)
 constexpr int kMoveWarps = 8;
 constexpr int kMoveRows = 128;  // rows whose addresses a warp works out at once
 
-// The kept rows slot0 .. slot1 - 1 of one (sequence, head): NU vectors of
-// type V each, from vector u0 of rows of `row_units` vectors.  One warp: it reads
-// 128 rows' positions and pages, then copies in batches of up to 18 vectors
-// per lane, every batch read before it is written.  Slot i's source is row i
-// or a later one, so no batch writes what a later one reads: safe in place.
+// Vectors a lane has in flight, of rows of NU vectors, and the rows they make
+// for a warp: about 16 vectors (with 8, evictions in place took 4-12% longer).
+template <int NU>
+__host__ __device__ constexpr int move_vectors() {
+  return NU == 9 ? 18 : NU * (kMoveRows / 32) < 16 ? NU * (kMoveRows / 32) : 16;
+}
+template <int NU>
+__host__ __device__ constexpr int move_step() {
+  return move_vectors<NU>() * 32 / NU;
+}
+
+// The kept rows of one (sequence, head) on one side, by a cluster: rows of NU
+// vectors of type V.  A step is R consecutive slots for each of the cluster's
+// warps; a warp works out the addresses of 128 of its rows at once, then takes
+// them step by step, all of a step's vectors (up to 18 per lane) in flight.
+// In place, every warp's reads of a step come before any warp's writes of it
+// (one barrier): slot i's source is row i or a later one, so no step writes
+// what a later step reads.  Pages of the call's own need no barrier.
 template <typename V, int NU>
-__device__ __forceinline__ void move_rows(const EvictParams &p, V *data,
-                                          int row_units, int u0, int b, int g,
-                                          int slot0, int slot1, long long *from,
-                                          long long *to) {
+__device__ __forceinline__ void move_rows(const EvictParams &p, V *data, int b,
+                                          int g, bool in_place, int nc, int rank,
+                                          long long *from, long long *to) {
+  constexpr int RPL = kMoveRows / 32;
+  constexpr int U = move_vectors<NU>(), R = move_step<NU>();
+  static_assert(U * 32 % NU == 0 && kMoveRows % R == 0, "whole rows and steps");
   const int lane = threadIdx.x & 31;
+  const int me = rank * kMoveWarps + (threadIdx.x >> 5);
+  const unsigned stride = nc * kMoveWarps * R;  // slots of a step
+  const unsigned budget = p.budget;
   const int32_t *const kept =
       p.kept + (size_t)(b * p.num_kv_heads + g) * p.budget;
   const int32_t *const table = p.block_table + (size_t)b * p.max_blocks;
   const int32_t *const dtable = p.dst_table + (size_t)b * p.dst_blocks;
-  constexpr int RPL = kMoveRows / 32;
-  constexpr int U = NU == 9 ? 18 : NU * RPL < 16 ? NU * RPL : 16;
-  static_assert(NU * RPL % U == 0, "whole batches");
-  for (int base = slot0; base < slot1; base += kMoveRows) {
+  for (unsigned base = 0; base < budget; base += stride * (kMoveRows / R)) {
+    // this warp's row i: step i / R, row i % R of its R
+    auto slot_of = [&](int i) {
+      return base + (unsigned)(i / R) * stride + me * R + i % R;
+    };
     int pos[RPL], ps[RPL], pd[RPL];
 #pragma unroll
     for (int x = 0; x < RPL; ++x) {
-      const int slot = base + x * 32 + lane;
-      pos[x] = slot < slot1 ? kept[slot] : -1;
+      const unsigned slot = slot_of(x * 32 + lane);
+      pos[x] = slot < budget ? kept[slot] : -1;
     }
 #pragma unroll
     for (int x = 0; x < RPL; ++x) {
       ps[x] = pd[x] = -1;
       if (pos[x] >= 0) {
         ps[x] = table[pos[x] / kBlockSize];
-        pd[x] = dtable[(base + x * 32 + lane) / kBlockSize];
+        pd[x] = dtable[slot_of(x * 32 + lane) / kBlockSize];
       }
     }
-    bool any = false;
     __syncwarp();  // the addresses before have been used
 #pragma unroll
     for (int x = 0; x < RPL; ++x) {
-      const int slot = base + x * 32 + lane;
       long long s = -1, d = -1;
       if (pos[x] >= 0) {
         if (ps[x] >= 0 && ps[x] < p.num_blocks && pd[x] >= 0 &&
@@ -323,98 +351,81 @@ __device__ __forceinline__ void move_rows(const EvictParams &p, V *data,
           s = ((long long)ps[x] * p.num_kv_heads + g) * kBlockSize +
               pos[x] % kBlockSize;
           d = ((long long)pd[x] * p.num_kv_heads + g) * kBlockSize +
-              slot % kBlockSize;
+              slot_of(x * 32 + lane) % kBlockSize;
           if (s == d) s = -1;  // already there
         } else {
           atomicOr(&g_status_evict, (unsigned)SVP_DEV_BAD_BLOCK_ID);
         }
       }
-      from[x * 32 + lane] = s < 0 ? -1 : s * row_units + u0;
-      to[x * 32 + lane] = d * row_units + u0;
-      any = any || s >= 0;
+      from[x * 32 + lane] = s < 0 ? -1 : s * NU;
+      to[x * 32 + lane] = d * NU;
     }
-    if (!__any_sync(kFull, any)) continue;
     __syncwarp();
-    const int units = min(kMoveRows, slot1 - base) * NU;
 #pragma unroll 1
-    for (int i0 = 0; i0 * 32 < units; i0 += U) {
+    for (int k = 0; k < kMoveRows / R; ++k) {
+      if (base + k * stride >= budget) break;  // the same for all
       V v[U];
 #pragma unroll
       for (int x = 0; x < U; ++x) {
-        const int i = (i0 + x) * 32 + lane;
-        const long long at = from[i / NU];
+        const int i = x * 32 + lane;
+        const long long at = from[k * R + i / NU];
         if (at >= 0) v[x] = data[at + i % NU];
       }
-      __syncwarp();  // the batch is read before it is written
+      if (in_place) {
+        if (nc > 1) cg::this_cluster().sync(); else __syncthreads();
+      }
 #pragma unroll
       for (int x = 0; x < U; ++x) {
-        const int i = (i0 + x) * 32 + lane;
-        if (from[i / NU] >= 0) data[to[i / NU] + i % NU] = v[x];
+        const int i = x * 32 + lane;
+        if (from[k * R + i / NU] >= 0) data[to[k * R + i / NU] + i % NU] = v[x];
       }
     }
   }
 }
 
-// A warp per (group, part, side): side 0 K, 1 V, 2 the scores.  Parts are
-// runs of rows; where a sequence is compacted in place they are runs of
-// columns instead (UC vectors), so that no warp writes what another has still
-// to read.  In place means: the first destination page is the first source
-// page.
-template <typename V, int UNITS, int UC>
+// A cluster per group and side: side 0 K, 1 V, 2 the scores.  In place means:
+// the first destination page is the first source page.
+template <typename V, int UNITS>
 __global__ void __launch_bounds__(32 * kMoveWarps)
-    compact_kernel(const EvictParams p, int parts, int warps) {
+    compact_kernel(const EvictParams p) {
   __shared__ long long from[kMoveWarps][kMoveRows], to[kMoveWarps][kMoveRows];
+  const int nc = (int)cg::this_cluster().num_blocks();
+  const int rank = (int)cg::this_cluster().block_rank();
   pdl_wait();  // the selection
   pdl_launch_dependents();
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long item = (long long)blockIdx.x * kMoveWarps + w;
-  const long long n_items = (long long)p.batch * p.num_kv_heads * warps;
+  const int w = threadIdx.x >> 5;
   const int side = blockIdx.y;
-  if (item >= n_items) return;
-  const int part = (int)(item % warps);
-  const int group = (int)(item / warps);
+  const int group = blockIdx.x / nc;
   const int b = group / p.num_kv_heads, g = group % p.num_kv_heads;
-  if (side == 2 && group % p.num_kv_heads == 0 && part == 0 && lane == 0) {
+  if (side == 2 && g == 0 && rank == 0 && threadIdx.x == 0) {
     const int L = p.seq_lens[b];
     const bool bad = L < 0 || L > (long long)p.max_blocks * kBlockSize;
     p.new_lens[b] = bad ? -1 : min(L, p.budget);
   }
   const bool in_place = p.dst_table[(size_t)b * p.dst_blocks] ==
                         p.block_table[(size_t)b * p.max_blocks];
-  int slot0 = 0, slot1 = p.budget;
-  if (!in_place) {
-    if (part >= parts) return;
-    slot0 = (int)((long long)p.budget * part / parts);
-    slot1 = (int)((long long)p.budget * (part + 1) / parts);
-  }
-  if (side == 2) {
-    if (!in_place || part == 0)
-      move_rows<float, 1>(p, p.scores, 1, 0, b, g, slot0, slot1, from[w], to[w]);
-    return;
-  }
-  V *const data = static_cast<V *>(side ? p.v_cache : p.k_cache);
-  if (!in_place)
-    move_rows<V, UNITS>(p, data, UNITS, 0, b, g, slot0, slot1, from[w], to[w]);
-  else if (part < UNITS / UC)
-    move_rows<V, UC>(p, data, UNITS, part * UC, b, g, 0, p.budget, from[w], to[w]);
+  if (side == 2)
+    move_rows<float, 1>(p, p.scores, b, g, in_place, nc, rank, from[w], to[w]);
+  else
+    move_rows<V, UNITS>(p, static_cast<V *>(side ? p.v_cache : p.k_cache), b, g,
+                        in_place, nc, rank, from[w], to[w]);
 }
 
-template <typename V, int UNITS, int UC>
+template <typename V, int UNITS>
 cudaError_t launch_compact(const EvictParams &p, int sms, cudaLaunchConfig_t cfg) {
   const long long groups = (long long)p.batch * p.num_kv_heads;
-  // enough runs for 32 warps on every SM, but of at least 32 rows
-  long long parts = ((long long)sms * 32 + 2 * groups - 1) / (2 * groups);
-  const long long most = (p.budget + 31) / 32;
-  if (parts > most) parts = most;
-  const long long warps = parts > UNITS / UC ? parts : UNITS / UC;
-  const long long blocks = (groups * warps + kMoveWarps - 1) / kMoveWarps;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  cfg.gridDim = dim3((unsigned)blocks, 3);
+  // enough CTAs for 32 warps on every SM, but no more than one step's rows
+  int nc = 1;
+  while (nc < kMaxCluster && 2 * groups * nc < 4LL * sms &&
+         nc * kMoveWarps * move_step<UNITS>() < p.budget)
+    nc *= 2;
+  if (groups * nc > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  cfg.gridDim = dim3((unsigned)(groups * nc), 3);
   cfg.blockDim = dim3(32 * kMoveWarps);
   cfg.dynamicSmemBytes = 0;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, compact_kernel<V, UNITS, UC>, p, (int)parts,
-                            (int)warps);
+  cfg.attrs[1].val.clusterDim.x = (unsigned)nc;
+  cfg.numAttrs = nc > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, compact_kernel<V, UNITS>, p);
 }
 
 }  // namespace
@@ -455,14 +466,14 @@ cudaError_t launch_kv_evict(const EvictParams &p, int sms, cudaStream_t stream) 
   if (e != cudaSuccess) return e;
 
   // vectors of 16 bytes, or 8 / 4 for the 72- and 36-byte rows of a 4-bit
-  // cache; in place, columns of 64 bytes (24 and 12)
+  // cache
   switch (p.row_bytes) {
-    case 36: return launch_compact<uint32_t, 9, 3>(p, sms, cfg);
-    case 72: return launch_compact<uint2, 9, 3>(p, sms, cfg);
-    case 64: return launch_compact<uint4, 4, 4>(p, sms, cfg);
-    case 128: return launch_compact<uint4, 8, 4>(p, sms, cfg);
-    case 256: return launch_compact<uint4, 16, 4>(p, sms, cfg);
-    default: return launch_compact<uint4, 32, 4>(p, sms, cfg);  // 512
+    case 36: return launch_compact<uint32_t, 9>(p, sms, cfg);
+    case 72: return launch_compact<uint2, 9>(p, sms, cfg);
+    case 64: return launch_compact<uint4, 4>(p, sms, cfg);
+    case 128: return launch_compact<uint4, 8>(p, sms, cfg);
+    case 256: return launch_compact<uint4, 16>(p, sms, cfg);
+    default: return launch_compact<uint4, 32>(p, sms, cfg);  // 512
   }
 }
 
