@@ -150,7 +150,8 @@ int plan_attention(int batch, int num_q_heads, int num_kv_heads, int head_dim,
   // mma.sync: one m16 tile per warp, two warps share a page beyond 16 rows;
   // tcgen05: the rows are the MMA's N (16 or 32), or two 32-row groups
   // sharing each K/V tile beyond 32 rows
-  int rb = fp4   ? attention_fp4_rows(rows)
+  const long long visible = max_visible_pages(max_blocks, q_len, n_sink, window);
+  int rb = fp4   ? attention_fp4_rows(rows, visible * batch * num_kv_heads, num_sms)
            : tc  ? (rows <= 16 ? 16 : rows <= 32 ? 32 : 64)
            : mma ? (rows <= 16 ? 16 : 32)
                  : rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : 8;
@@ -165,14 +166,12 @@ int plan_attention(int batch, int num_q_heads, int num_kv_heads, int head_dim,
   // a slice holds at least min_pages pages (fewer CTAs for small calls).
   int min_pages = split_pages > 0 ? split_pages : 8;
   long long grid = (long long)num_sms * ctas;
-  const long long page_bound =
-      groups * (long long)max_visible_pages(max_blocks, q_len, n_sink, window);
+  const long long page_bound = groups * visible;
   if (grid > page_bound / min_pages) grid = page_bound / min_pages;
   if (grid < 1) grid = 1;
   // a 4-bit call of short sequences: a warp to a group, as many CTAs as that
   // takes (spread over the SMs when there are fewer groups)
-  plan->whole = fp4 && split_pages == 0 &&
-                max_visible_pages(max_blocks, q_len, n_sink, window) <= kWholePages;
+  plan->whole = fp4 && split_pages == 0 && visible <= kWholePages;
   if (plan->whole) {
     const int w = attention_fp4_warps(rb);
     grid = std::max((groups + w - 1) / w, std::min<long long>(groups, num_sms));

@@ -63,8 +63,9 @@ constexpr float kRefSlack = 14.f;             // largest log2 P before a move
 constexpr float kNoRef = -3e38f;              // below any finite score
 
 // Warps of a CTA (one per SM) for NT n8 tiles of query rows: what the
-// registers allow (O alone takes 32 per tile), 170 per thread for twelve
-// warps, 255 for eight.
+// registers allow (O alone takes 32 per tile), 168 per thread for twelve
+// warps, 255 for eight (twelve warps for two tiles spill: 56 us against 46
+// for 16 rows on 98 MB of cache).
 template <int NT>
 __host__ __device__ constexpr int warps4() {
   return NT == 1 ? 12 : 8;
@@ -72,7 +73,14 @@ __host__ __device__ constexpr int warps4() {
 // Stages of a warp's ring: 9 D bytes x 8 each, as many as fit.
 template <int NT>
 __host__ __device__ constexpr int stages4() {
-  return NT == 1 ? 2 : 3;
+  return NT == 2 ? 3 : 2;
+}
+// Three tiles leave no registers for the Q fragments: they wait in shared
+// memory, read back by the lane that wrote them, and the pages go one by one
+// (in pairs, with spills: 63 us against 59 for 20 rows on 98 MB).
+template <int NT>
+__host__ __device__ constexpr bool q_in_smem() {
+  return NT == 3;
 }
 constexpr int kChecked = 256;
 constexpr int kSegRing4 = 8;  // decoded segments: read .. issued + 1
@@ -103,9 +111,10 @@ struct Info4 {
   int meta[STAGES];  // pages; + kChecked: their keys need the visibility test
   Seg4 seg[kSegRing4];
 };
-template <int D, int W, int STAGES>
+template <int D, int NT, int W, int STAGES>
 struct Smem4 {
   Warp4<D, STAGES> warp[W];
+  uint2 q[q_in_smem<NT>() ? W * NT * (D / 16) * 32 : 1];
   Info4<STAGES> info[W];
   int prefix[1];  // [batch + 1] item prefix, then [batch] lengths: dynamic
 };
@@ -369,12 +378,13 @@ template <int D, int NT>
 __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
     paged_attention_fp4_kernel(const AttnParams p) {
   constexpr int W = warps4<NT>(), RB = 8 * NT, KS = D / 16;
-  constexpr int PJ = 2;  // pages scored together
+  constexpr int PJ = NT == 3 ? 1 : 2;  // pages scored together
+  static_assert(warps4<2>() == warps4<3>(), "a launch's rest may plan for either");
   constexpr int kStages4 = stages4<NT>();
   static_assert(kStages4 + 2 <= kSegRing4, "a stage holds at most one segment");
   constexpr int PAGE = 9 * D;
   extern __shared__ unsigned char smem_raw[];
-  using S = Smem4<D, W, kStages4>;
+  using S = Smem4<D, NT, W, kStages4>;
   S &sm = *reinterpret_cast<S *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -576,7 +586,18 @@ __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
       qs[nt][0] = __shfl_sync(kFull, sc, 8 * t);
       qs[nt][1] = __shfl_sync(kFull, sc, 8 * t + 4);
     }
-    auto qb = [&](int ks, int nt) { return qf[nt][ks]; };
+    const uint32_t qa = smem_u32(&sm.q[0]) + (warp * NT * KS * 32 + lane) * 8;
+    if constexpr (q_in_smem<NT>()) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+          sm.q[((warp * NT + nt) * KS + ks) * 32 + lane] = qf[nt][ks];
+      __syncwarp();
+    }
+    auto qb = [&](int ks, int nt) {
+      return q_in_smem<NT>() ? lds64(qa + (nt * KS + ks) * 256) : qf[nt][ks];
+    };
 
     float o[D / 16][NT][4];
     float ref[NT][2], l[NT][2];
@@ -898,13 +919,13 @@ std::map<std::tuple<int, const void *, size_t>, bool> g_ready4;
 
 template <int D, int NT>
 size_t smem4(int batch) {
-  return sizeof(Smem4<D, warps4<NT>(), stages4<NT>()>) + sizeof(int) * 2 * (size_t)batch + 128;
+  return sizeof(Smem4<D, NT, warps4<NT>(), stages4<NT>()>) + sizeof(int) * 2 * (size_t)batch + 128;
 }
 
 template <int D, int NT>
 cudaError_t launch4(AttnParams p, int grid, cudaStream_t st) {
   p.slices = grid * warps4<NT>();
-  static_assert(sizeof(Smem4<D, warps4<NT>(), stages4<NT>()>) +
+  static_assert(sizeof(Smem4<D, NT, warps4<NT>(), stages4<NT>()>) +
                         sizeof(int) * 2 * kBatchFp4 + 128 <=
                     232448,
                 "a CTA's shared memory");
@@ -935,11 +956,19 @@ cudaError_t launch4(AttnParams p, int grid, cudaStream_t st) {
 
 }  // namespace
 
-// Query rows of a unit: one or two n8 tiles; more rows are dealt to several
-// units, each reading the pages again (from L2: neighbouring units run close
-// together).  A third tile per unit was slower (20 rows: 70 us against 68 on
-// 98 MB of cache; 60 rows: 143 against 122), its accumulators spill.
-int attention_fp4_rows(int rows) { return rows <= 8 ? 8 : 16; }
+// Query rows of a unit: one or two n8 tiles, three for 17 to 24 rows; more
+// rows are dealt to several units, each reading the pages again (from L2:
+// neighbouring units run close together).  Three tiles convert the cache
+// once where two units convert it twice, but a warp goes through its pages
+// more slowly and the longer code takes longer to fetch, so it needs work:
+// 20 rows, 8 heads, up to 8192 positions: batch 1 30 us against 22, 6 43
+// against 43 (20 pages a warp), 16 59 against 68, 64 202 against 300.
+constexpr int kMinPages3 = 20;
+int attention_fp4_rows(int rows, long long pages, int sms) {
+  if (rows <= 8) return 8;
+  return rows > 16 && rows <= 24 && pages >= (long long)kMinPages3 * warps4<3>() * sms
+             ? 24 : 16;
+}
 
 int attention_fp4_warps(int rb) { return rb <= 8 ? warps4<1>() : warps4<2>(); }
 
@@ -948,6 +977,7 @@ cudaError_t launch_attention_fp4(const AttnParams &p, int grid,
   const bool d64 = p.head_dim == 64;
   switch (p.rb) {
     case 8: return d64 ? launch4<64, 1>(p, grid, stream) : launch4<128, 1>(p, grid, stream);
+    case 24: return d64 ? launch4<64, 3>(p, grid, stream) : launch4<128, 3>(p, grid, stream);
     default: return d64 ? launch4<64, 2>(p, grid, stream) : launch4<128, 2>(p, grid, stream);
   }
 }

@@ -104,8 +104,8 @@ constexpr int kBatchFp4 = 512;
 // mma.sync for head_dim 64.
 constexpr int kMmaMinRows = 3;
 
-// The same for 4-bit caches at head_dim 128: below, units of 16 rows on the
-// mma.sync kernel (20 rows, 98 MB of cache: 67 us against 75; 60 rows: 120
+// The same for 4-bit caches at head_dim 128: below, the mma.sync kernel (98 MB
+// of cache: 20 rows 59 us against 75, 32 rows 73 against 75; 60 rows: 120
 // against 89).
 constexpr int kFp4TcMinRows = 33;
 
@@ -131,12 +131,13 @@ int attention_tc_ctas_per_sm(int rb, int batch);
 cudaError_t launch_attention_tc(const AttnParams &p, int grid,
                                 cudaStream_t stream);
 
-// The 4-bit cache kernels (attention_fp4.cu): the unit's row count (8 or
-// 16) for this many query rows per kv head, the warps (slices) of a CTA,
-// of which an SM holds one, and the launch of attention and merge.
+// The 4-bit cache kernels (attention_fp4.cu): the unit's row count (8, 16 or
+// 24) for this many query rows per kv head and pages of the launch, the warps
+// (slices) of a CTA, of which an SM holds one, and the launch of attention
+// and merge.
 // Calls whose sequences span at most kWholePages pages take whole groups.
 constexpr int kWholePages = 32;
-int attention_fp4_rows(int rows);
+int attention_fp4_rows(int rows, long long pages, int sms);
 int attention_fp4_warps(int rb);
 cudaError_t launch_attention_fp4(const AttnParams &p, int grid,
                                  cudaStream_t stream);

@@ -368,6 +368,36 @@ def test_more_sequences_than_a_launch_takes(svp, width):
     _check(out, lse, _reference(q, kc, vc, 64, 0.125, lens, table, 1.0, 1.0), 64)
 
 
+@pytest.mark.parametrize("d,batch,hkv,width,mask", [
+    (128, 600, 1, 50, {}),       # in slices, and a launch for the 88 left
+    (64, 600, 2, 31, {}),        # whole groups
+    (128, 512, 12, 50, dict(n_sink=5, window=40)),
+    (128, 520, 1, 50, "tree"),
+], ids=["slices", "whole", "window", "tree"])
+def test_wide_units(svp, d, batch, hkv, width, mask):
+    """24 query rows and enough pages for the widest unit."""
+    import torch
+    rng = np.random.default_rng(width)
+    ql, hq = 6, 4 * hkv
+    lens = rng.integers(ql, 90, batch)
+    lens[:3] = (ql, 31 * 16, 200)
+    q, kc, vc, table, lens = _inputs(7, lens, hq, hkv, d, ql, 0.4, 0.3, width=width)
+    g = [R.to_gpu(q, "bf16"), R.to_gpu(kc), R.to_gpu(vc), R.to_gpu(table), R.to_gpu(lens)]
+    kw = dict(scale=0.125, k_scale=0.4, v_scale=0.3)
+    if mask == "tree":
+        mask = dict(tree=np.tile(R.binary_tree(ql), (batch, 1)))
+        call = lambda: svp.paged_tree_attention(*g, R.to_gpu(mask["tree"]), **kw)
+    else:
+        call = lambda: svp.paged_decode_attention(*g, **kw, **mask)
+    out, lse = call()
+    assert svp.read_device_status() == 0
+    ref = _reference(q, kc, vc, d, 0.125, lens, table, float(np.float32(0.4)),
+                     float(np.float32(0.3)), **mask)
+    _check(out, lse, ref, d)
+    again, _ = call()
+    assert torch.equal(out, again)
+
+
 @pytest.mark.parametrize("path", [2, 3])
 def test_rows_that_see_nothing(svp, path):
     """A tree mask without any bit over a sequence of the new rows only: zero
