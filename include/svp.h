@@ -6,7 +6,10 @@
  * the GPU's memory: store the new tokens' K/V in the paged cache
  * (kv_append), let the new query rows attend to their sequence's cached
  * rows (paged_decode_attention), and accept or resample the draft tokens
- * (spec_accept).
+ * (spec_accept).  Caches are fp32, bf16, FP8 or 4-bit (svp_dtype).  Beside
+ * the step: rows back out of a cache (kv_gather), and eviction by
+ * accumulated attention weight (paged_score_update after each attention
+ * call, kv_evict when a sequence has outgrown its budget).
  *
  * Conventions shared by every entry point
  *  - Every tensor argument is a caller-owned DEVICE pointer, row-major and
@@ -117,11 +120,12 @@ typedef struct {
  * All compute the same quantity; forcing a path exists for testing and
  * tuning.
  *   CUDA_CORES    fp32 FMA dot products, any dtype.
- *   TENSOR_CORES  warp-level mma.sync (bf16 in, fp32 accumulate).
+ *   TENSOR_CORES  warp-level mma.sync (bf16 in, or fp16 over a 4-bit cache;
+ *                 fp32 accumulate).
  *   TCGEN05       fifth-generation tensor cores: tcgen05.mma with fp32
  *                 accumulators in tensor memory, keys as the 128-row M
- *                 dimension (bf16, head_dim 128, 512 sequences per
- *                 kernel launch).
+ *                 dimension (bf16 or a 4-bit cache, head_dim 128, 512
+ *                 sequences per kernel launch).
  * A forced path on data it cannot take (a tensor path on fp32 or FP8;
  * head_dim 64 for TCGEN05; CUDA_CORES on FP4) is SVP_ERR_UNSUPPORTED. */
 typedef enum {
@@ -159,7 +163,11 @@ typedef enum {
  * no initialisation: each CTA rewrites the split record it owns in every
  * launch, and the merge kernel reads partials only where a record of the
  * same launch points.  Two kernel launches (attention, merge) per 4096
- * sequences (512 on the TCGEN05 path).  With
+ * sequences (512 on the TCGEN05 path and over 4-bit caches).  A 4-bit call
+ * on the TENSOR_CORES path with split_pages == 0 whose sequences cannot see
+ * more than 32 pages takes every group whole: one launch, no workspace used.
+ * Over 4-bit caches on that path a slice is a warp's, in steps of 4 pages.
+ * With
  * dims->workspace == NULL the library uses a buffer of its own per device,
  * (re)allocated inside the call when it is too small -- that first call is
  * then not capturable in a CUDA graph.  Calls that share a workspace must
@@ -277,7 +285,7 @@ int kv_append(const svp_dims *dims, const void *k_new, const void *v_new,
  * (the newest rows).  Positions outside [0, seq_lens[b]) give zero rows.
  * FP8 and FP4 values are code (* scale) * k_scale rounded once to bf16.
  * For dense kernels over a cached prefix, and for moving rows between
- * caches.  A sequence length outside [0, max_blocks_per_seq*16] gives zero
+ * caches.  k_out and v_out overlap neither each other nor the caches.  A sequence length outside [0, max_blocks_per_seq*16] gives zero
  * rows and SVP_DEV_BAD_SEQ_LEN, a bad block id a zero row and
  * SVP_DEV_BAD_BLOCK_ID.  Uses no workspace.
  * Errors as for kv_append, with n_rows >= 0. */

@@ -5,8 +5,12 @@
 // V = code * scale * v_scale.  k_scale is folded into the score scale,
 // v_scale multiplies the outputs, code * scale is exact in fp16.
 //
-// What bounds it: a cached element is 9/16 byte, so at the copy rate an SM
-// has to turn 80 elements a nanosecond into products.  On the CUDA cores
+// What bounds it: the issue slots.  A cached element is 9/16 byte, so at the
+// copy rate an SM has to turn 80 elements a nanosecond into products: a page
+// of K and V (2304 bytes, D = 128) may take 99 cycles, and its conversion,
+// products and softmax, about 250 warp instructions for up to 8 rows, take
+// 111 with twelve warps (without the copies; the copies alone: 100 us of
+// the 122 of four 131,072-token sequences).  On the CUDA cores
 // that is an FMA per element and query row on top of the conversion; here
 // even a single query row goes through mma.sync (keys as M, query rows as
 // N = 8): the conversion (one cvt and one fp16 multiply per two elements)
@@ -20,7 +24,9 @@
 //    lazy: a row's reference moves only when a score exceeds it by 2^8, so
 //    the usual page costs one vote instead of shuffled maxima.  P is fp16 at
 //    2^6 times its softmax weight relative to the reference (at most 2^14),
-//    which keeps weights down to 2^-20 normal; the row sums are fp32.
+//    which keeps weights down to 2^-20 normal: rounding P costs each weight
+//    half an fp16 step, 2^-11, as bf16 P costs 2^-8; the row sums are fp32
+//    and of the weights before that rounding.
 //  * O^T = V^T P^T: P's fp16 pairs become the B operand by movmatrix.  Lane
 //    (g, t) reads D/8 consecutive codes of four keys; the nibbles of two
 //    keys are interleaved before the conversion, so one cvt yields the pair
@@ -28,17 +34,25 @@
 //  * Every warp is on its own: it takes one slice of the flattened page list
 //    (the stream-K order of attn_common.cuh, with a warp where that has a
 //    CTA), copies its pages itself (1-D bulk copies -- a head's page is one
-//    run of 9 D bytes -- four pages to a stage, two stages), keeps a
+//    run of 9 D bytes -- four pages to a stage, two or three stages), keeps a
 //    segment's whole state in registers and writes the segment's result from
 //    there.  No barrier joins the warps, so a warp that ends a segment
 //    (normalise, write, next Q) costs the others nothing.
 //  * Where no sequence can hold more than 32 pages a warp takes a group whole:
 //    no prefix of the lengths to build, no partials and no second launch
-//    (250 tokens of four heads: 19.5 us a call from the host against 24).
+//    (250 tokens of four heads: 11.6 us a call).
 //  * A group of pages cut by slice borders leaves one normalised partial per
 //    slice; merge_fp4_kernel joins them by log-sum-exp in slice order.
 //  * Rows whose memory holds no valid data take no part: masked keys score
 //    -inf whatever their bytes, and their V scale is replaced by 0.
+//
+// Measured (attention and merge, D = 128; of the cache's bytes at the copy
+// rate): 32 sequences of 32 heads, up to 4096 tokens, one row each: 77.5 us,
+// 0.65; four sequences of 131,072 tokens, 8 rows: 122 us, 0.73; 16 sequences
+// of 8 heads, up to 8192 tokens, 20 rows: 58.5 us, 0.24 -- there an SM's
+// eight warps issue 0.27 instructions a cycle and scheduler, waiting on the
+// fixed latencies of conversion, MMA and exponential chains (1.8 of 5.6
+// cycles an instruction) and on code (0.8).
 #include <cuda_fp16.h>
 
 #include <cmath>

@@ -18,14 +18,21 @@
 //    power-of-two scale per row (fp4.cuh), whose inverse the softmax applies
 //    with the score scale.
 //  * P is fp16 at 2^14 times its weight relative to the running maximum, so
-//    weights down to 2^-28 stay normal; the row sums carry the same factor.
+//    weights down to 2^-28 stay normal (each is rounded by at most 2^-11);
+//    the row sums, of the fp32 weights, carry the same factor.
 //
-// What bounds it: shared-memory traffic.  A tile's K and V are written (64
-// KB) and read by the MMAs (64 KB) at 128 bytes a cycle and SM, about 1000
-// cycles, against 790 for its 18 KB at the copy rate.  The conversion itself
-// (1700 warp instructions a tile) and the MMAs fit beside that.  Against the
-// mma.sync kernel the conversion is done once for all rows of a unit (up to
-// 64), not once per 16.
+// What bounds it: the tile pipeline.  A tile takes 2860 cycles at 60 rows
+// where its 18 KB would take 790 at the copy rate: its 16 MMAs (M = 128, 87
+// cycles each whatever the rows) are 1400, the softmax of 128 keys x 64 rows
+// runs beside them, and its K and V tiles are written and read through shared
+// memory (128 KB, about 1000).  Without the conversion the same calls take
+// 59 us for 75 (20 rows) and 71 for 89 (60 rows): the dequantising warps are
+// a quarter of it.  Against the mma.sync kernel the conversion is done once
+// for all rows of a unit (up to 64), not once per 16 or 24.
+//
+// Measured (16 sequences of 8 heads, up to 8192 tokens: 98 MB of cache; call
+// times): 60 rows 89 us against 120 of the mma.sync kernel, 32 rows 75
+// against 73, 20 rows 75 against 59.
 #include <cstring>
 #include <map>
 #include <mutex>
@@ -46,7 +53,7 @@ constexpr int kD = 128;
 constexpr int kTilePages = 8;
 constexpr int kTileKeys = kTilePages * kBlockSize;  // the MMA's M
 static_assert(kTilePages == kTilePagesTc, "stream-K items are the kernel's tiles");
-constexpr int kHalfBytes = kTileKeys * 128;  // 64 columns x 128 keys, bf16
+constexpr int kHalfBytes = kTileKeys * 128;  // 64 columns x 128 keys, fp16
 constexpr int kTileBytes = 2 * kHalfBytes;   // one K (or V) tile: 32 KB
 constexpr int kStages = 2;     // fp16 tiles
 constexpr int kRawStages = 3;  // raw tiles
@@ -76,7 +83,7 @@ constexpr int kTcBatchCap = 512;  // sequences per launch (prefix in smem)
 template <int N, bool DUAL = false>
 struct Tc4Smem {
   static constexpr int ST = kStages;
-  static constexpr int PB = N * kTileKeys * 2;  // one group's P tile (bf16)
+  static constexpr int PB = N * kTileKeys * 2;  // one group's P tile (fp16)
   alignas(1024) unsigned char k[ST][kTileBytes];
   alignas(1024) unsigned char v[ST][kTileBytes];
   alignas(128) unsigned char raw[kRawStages][kTilePages][2][kRawPage];
@@ -286,7 +293,7 @@ __device__ __forceinline__ void tc_wait_st() {
 }
 
 // Byte offset of element (row n, column k) of an [N rows x 128 columns]
-// bf16 operand in the K-major 128-byte-swizzled layout: two 64-column
+// fp16 operand in the K-major 128-byte-swizzled layout: two 64-column
 // halves, each [N][128 B], 16-byte chunks XOR-ed with the row mod 8.
 template <int N>
 __device__ __forceinline__ uint32_t kmajor_off(int n, int k) {
@@ -359,7 +366,7 @@ __device__ __forceinline__ int row_of(int lane) {
   return 8 * (v >> 1) + 2 * (lane & 3) + (v & 1);
 }
 
-// Four 8x8 bf16 blocks, stored transposed: this thread's fragment r[i]
+// Four 8x8 16-bit blocks, stored transposed: this thread's fragment r[i]
 // (rows 2 (t % 4) and 2 (t % 4) + 1 of key t / 4) lands in block i, whose
 // row t % 8 starts at `addr` of lane 8 i + t % 8.
 __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr,
@@ -1163,7 +1170,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // group 1 writes P again once the TMA engine has read it
         if (!DUAL && gi == 1 && prev < 0 && us > 0)
           ok = __all_sync(kFull, mbar_wait(&sm.stg_free, (us - 1) & 1)) && ok;
-        // P as bf16, K-major and swizzled: per 8-row block, four 8x8 blocks
+        // P as fp16, K-major and swizzled: per 8-row block, four 8x8 blocks
         // (keys gw 32 + 8 i ..) stored transposed.  DUAL: rows gi N .. of
         // the 2N-row operand in the stage's K tile, which the tile's S MMAs
         // have read

@@ -2,10 +2,9 @@
 // calls (binding.py wraps these functions).  Argument marshalling only: type,
 // shape and device checks, output allocation, raw pointers for libsvp.so.
 //
-// A decode step makes these calls once per layer and head group, and the
-// smallest of them run 5 us on the GPU: checking seven tensors and making
-// two in Python takes 13-17 us a call, here 1-2.  Nothing is kept between
-// calls.
+// A decode step makes these calls once per layer, and the smallest of them
+// run 4 us on the GPU: marshalled in Python a call takes 10-17 us of host
+// time, here 4-6, launch included.  Nothing is kept between calls.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

@@ -7,9 +7,14 @@
 // warp that reads it -- no split merge, no atomics, no shared state between
 // CTAs -- and K is read once, V not at all.
 //
-// What bounds it: K's bytes (for one query row per kv head, 2 D bytes of
-// bf16 per 2 D products) and, from about 16 rows on a 4-bit cache, the
-// mma.sync rate.  Design:
+// What bounds it: K's bytes for few rows -- 32 sequences of 32 heads, up to
+// 4096 tokens, one row, bf16: 102 us, 0.90 of the copy rate.  With many rows
+// over a 4-bit cache the start of the CTAs (lengths, page ids, query rows:
+// 3-4 us each, five resident per SM) and the conversion and exponentials of
+// a page (about 200 warp instructions at 20 rows): 16 sequences of 8 heads,
+// up to 8192 tokens, 20 rows: 27.6 us where the bytes take 7.9.  Fewer, longer
+// CTAs with pages fetched three ahead left SMs idle at ragged lengths (53
+// pages a CTA: 40 us).  Design:
 //  * K goes from global memory to registers as matrix operands: keys are M,
 //    query rows N (m16n8k16, one page per tile), and the k positions are
 //    dealt to the dimensions so that a lane's operands are consecutive
@@ -19,7 +24,8 @@
 //    multiplied.
 //  * The query rows wait in shared memory as B operands (bf16 as they are;
 //    fp16 with a power-of-two scale per row against FP8 and FP4 keys, whose
-//    values are exact in fp16), one copy for the CTA's four warps.
+//    values are exact in fp16), one copy for the CTA's four warps.  Sums,
+//    weights and scores are fp32.
 //  * fp32 caches use fp32 FMAs in the same lane layout.
 #include <cuda_fp16.h>
 
