@@ -165,7 +165,8 @@ typedef enum {
  * same launch points.  Two kernel launches (attention, merge) per 4096
  * sequences (512 on the TCGEN05 path and over 4-bit caches).  A 4-bit call
  * on the TENSOR_CORES path with split_pages == 0 whose sequences cannot see
- * more than 32 pages takes every group whole: one launch, no workspace used.
+ * more than 32 pages (64 for few groups) takes every group whole: one launch,
+ * no workspace used.
  * Over 4-bit caches on that path a slice is a warp's, in steps of 4 pages.
  * With
  * dims->workspace == NULL the library uses a buffer of its own per device,

@@ -169,12 +169,23 @@ int plan_attention(int batch, int num_q_heads, int num_kv_heads, int head_dim,
   const long long page_bound = groups * visible;
   if (grid > page_bound / min_pages) grid = page_bound / min_pages;
   if (grid < 1) grid = 1;
-  // a 4-bit call of short sequences: a warp to a group, as many CTAs as that
-  // takes (spread over the SMs when there are fewer groups)
+  // a 4-bit call of short sequences: whole groups, a warp to each or, where
+  // warps would idle, several (at least a pair of pages each)
   plan->whole = fp4 && split_pages == 0 && visible <= kWholePages;
+  plan->parts = 1;
   if (plan->whole) {
     const int w = attention_fp4_warps(rb);
-    grid = std::max((groups + w - 1) / w, std::min<long long>(groups, num_sms));
+    int &parts = plan->parts;
+    while (parts < kMaxParts && groups <= (long long)num_sms * (w / (2 * parts)) &&
+           4 * parts <= visible)
+      parts *= 2;
+    plan->whole = visible <= (long long)kPartPages * parts;
+    const int teams = w / parts;
+    if (plan->whole)
+      grid = std::max((groups + teams - 1) / teams,
+                      std::min<long long>(groups, num_sms));
+    else
+      parts = 1;
   }
   plan->rb = rb;
   plan->n_rg = n_rg;
@@ -354,6 +365,7 @@ static int attention_call(const svp_dims *dims, const void *q,
     p.n_rg = plan.n_rg;
     p.merge_rows = std::min(plan.rb, p.rows);
     p.whole = plan.whole;
+    p.parts = plan.parts;
     // tcgen05: items are 8-page tiles, 4-bit caches: 4-page stages (a
     // slice's minimum in items)
     p.ppi = plan.fp4 ? kTilePagesFp4 : plan.tc ? kTilePagesTc : 1;
@@ -368,11 +380,10 @@ static int attention_call(const svp_dims *dims, const void *q,
     // previous launch's merge, which reads the workspace it would reset
     p.early = early && b0 == 0;
     AttnPlan sub = plan;
-    if (nb != bl) {
+    if (nb != bl && !plan.whole) {
       plan_attention(nb, dims->num_q_heads, dims->num_kv_heads,
                      dims->head_dim, dims->dtype, dims->max_blocks_per_seq,
-                     q_len, n_sink, window,
-                     plan.whole ? 0 : plan.min_pages,
+                     q_len, n_sink, window, plan.min_pages,
                      plan.tc                 ? SVP_PATH_TCGEN05
                      : plan.mma || plan.fp4  ? SVP_PATH_TENSOR_CORES
                                              : SVP_PATH_CUDA_CORES,

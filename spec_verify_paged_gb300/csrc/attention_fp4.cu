@@ -38,9 +38,10 @@
 //    segment's whole state in registers and writes the segment's result from
 //    there.  No barrier joins the warps, so a warp that ends a segment
 //    (normalise, write, next Q) costs the others nothing.
-//  * Where no sequence can hold more than 32 pages a warp takes a group whole:
-//    no prefix of the lengths to build, no partials and no second launch
-//    (250 tokens of four heads: 11.6 us a call).
+//  * Short sequences (kWholePages) are taken whole, a group by one warp or by
+//    a team of neighbours whose results meet in shared memory: no prefix of
+//    the lengths to build, no partials in memory and no second launch (250
+//    tokens of four heads: 7.5 us a call, 11.5 by single warps).
 //  * A group of pages cut by slice borders leaves one normalised partial per
 //    slice; merge_fp4_kernel joins them by log-sum-exp in slice order.
 //  * Rows whose memory holds no valid data take no part: masked keys score
@@ -49,7 +50,7 @@
 // Measured (attention and merge, D = 128; of the cache's bytes at the copy
 // rate): 32 sequences of 32 heads, up to 4096 tokens, one row each: 77.5 us,
 // 0.65; four sequences of 131,072 tokens, 8 rows: 122 us, 0.73; 16 sequences
-// of 8 heads, up to 8192 tokens, 20 rows: 58.5 us, 0.24 -- there an SM's
+// of 8 heads, up to 8192 tokens, 20 rows: 59.5 us, 0.24 -- there an SM's
 // eight warps issue 0.27 instructions a cycle and scheduler, waiting on the
 // fixed latencies of conversion, MMA and exponential chains (1.8 of 5.6
 // cycles an instruction) and on code (0.8).
@@ -366,9 +367,10 @@ __device__ __forceinline__ Seg4 next_segment(const AttnParams &p,
   return s;
 }
 
-// Group `slice` as one run of pages (AttnParams::whole).
+// Part `part` of group `slice` (AttnParams::whole, ::parts), in pairs of pages.
 __device__ __forceinline__ Seg4 whole_segment(const AttnParams &p, int per_seq,
-                                              int slice, int rb, int lane) {
+                                              int slice, int part, int rb,
+                                              int lane) {
   Seg4 s = {};
   s.b = slice / per_seq;
   const int gi = slice - s.b * per_seq;
@@ -379,9 +381,13 @@ __device__ __forceinline__ Seg4 whole_segment(const AttnParams &p, int per_seq,
     if (lane == 0 && gi == 0) raise4(SVP_DEV_BAD_SEQ_LEN);
     return s;
   }
-  visible_pages(s.L, p.q_len, p.n_sink, p.window, s.n_a, s.b_start, s.n_pages);
+  int np;
+  visible_pages(s.L, p.q_len, p.n_sink, p.window, s.n_a, s.b_start, np);
+  const int pairs = (np + 1) / 2;
+  s.page0 = 2 * (pairs * part / p.parts);
+  s.n_pages = min(2 * (pairs * (part + 1) / p.parts), np) - s.page0;
   s.f = s.l = slice;
-  s.valid = 1;
+  s.valid = s.n_pages > 0;
   const int base = s.L - p.q_len;
   s.t_min = p.tree_mask ? base - 1 : base + s.rg * rb / p.group;
   s.t_max = base + (min(s.rg * rb + rb, p.rows) - 1) / p.group;
@@ -414,11 +420,15 @@ __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
   if (!p.early) pdl_wait();
   pdl_launch_dependents();  // the merge may be scheduled
   // slice s goes to warp s / gridDim.x of CTA s % gridDim.x: a small call
-  // spreads over the SMs
-  const int slice = warp * gridDim.x + blockIdx.x;
+  // spreads over the SMs (parts of a group: to neighbouring warps)
+  const int part = p.whole ? warp % p.parts : 0;
+  const int team = p.whole ? warp / p.parts : warp;
+  const int slice = team * gridDim.x + blockIdx.x;
   int *const seqlen = sm.prefix + p.batch + 1;
   int total = 0, n_slices = p.batch * per_seq, end = 0;
-  if (!p.whole) {
+  if (p.whole) {
+    if ((team + 1) * p.parts > W) return;  // warps of no whole team
+  } else {
     if (warp == 0)
       build_prefix(p, sm.prefix, seqlen, per_seq, lane, &g_status_attn4);
     __syncthreads();  // the only one: the warps are on their own from here
@@ -440,7 +450,7 @@ __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
   auto decode = [&](int i, int pos) {  // segment i of this slice, into the ring
     const Seg4 s = !p.whole ? next_segment(p, sm.prefix, seqlen, per_seq, pos, end,
                                            total, n_slices, RB)
-                   : i == 0 ? whole_segment(p, per_seq, slice, RB, lane)
+                   : i == 0 ? whole_segment(p, per_seq, slice, part, RB, lane)
                             : Seg4{};
     if (lane == 0) inf.seg[i % kSegRing4] = s;
     __syncwarp();
@@ -550,6 +560,10 @@ __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
   const uint32_t k_off = k_lane<D>(g, t), v_off = v_lane<D>(g, t);
   const uint32_t v_off_s = v_lane_scale<D>(g, t);
   int c = 0;  // stages read
+  bool gave_up = false;
+  // a part's result, where its pages were: rows, their LSEs, whether it gave up
+  float *const part_s = reinterpret_cast<float *>(&sm.warp[warp].kv[0][0][0][0]);
+  static_assert((RB * D + RB + 1) * 4 <= sizeof(Warp4<D, kStages4>), "a part's result");
   for (int us = 0;; ++us) {
     __syncwarp();
     const Seg4 ui = inf.seg[us % kSegRing4];
@@ -642,7 +656,10 @@ __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
       }
       return false;
     };
-    if (!ready(c)) return;
+    if (!ready(c)) {
+      gave_up = true;
+      break;
+    }
     int s = c % kStages4, p0 = 0, left = ui.n_pages;
     int meta = (int)lds32(metas + s * 4);  // warp-uniform
     uint32_t pair = kv0 + s * (kStagePages * 2 * PAGE);
@@ -751,7 +768,10 @@ __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
       if (!stage_end) {
         next = pair + PJ * 2 * PAGE;
       } else if (more) {
-        if (!ready(c + 1)) return;
+        if (!ready(c + 1)) {
+          gave_up = true;
+          break;
+        }
         const int sn = (c + 1) % kStages4;
         next = kv0 + sn * (kStagePages * 2 * PAGE);
         meta_n = (int)lds32(metas + sn * 4);
@@ -776,13 +796,14 @@ __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
       }
     }
 
+    if (gave_up) break;
     // ---- the segment's result, from registers ----
     if (p.early) pdl_wait();  // outputs are written from here on
-    const bool single = ui.f == ui.l;
+    const bool single = p.whole ? p.parts == 1 : ui.f == ui.l;
     if (!p.whole && slice == ui.f && lane == 0)
       p.split[(ui.b * p.num_kv_heads + ui.g) * p.n_rg + ui.rg] =
           make_int2(ui.f, ui.l);
-    const size_t part = (size_t)2 * slice + (slice == ui.f ? 1 : 0);
+    const size_t slot = (size_t)2 * slice + (slice == ui.f ? 1 : 0);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -814,9 +835,9 @@ __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
             dst[i4] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else {
-          if (g == 0) p.part_lse[part * RB + lr] = lse2;
-          float4 *dst = reinterpret_cast<float4 *>(
-              p.part_o + (part * RB + lr) * D + (D / 8) * g);
+          float *const to = p.whole ? part_s : p.part_o + slot * RB * D;
+          if (g == 0) (p.whole ? part_s + RB * D : p.part_lse + slot * RB)[lr] = lse2;
+          float4 *dst = reinterpret_cast<float4 *>(to + lr * D + (D / 8) * g);
 #pragma unroll
           for (int i4 = 0; i4 < D / 32; ++i4)
             dst[i4] = make_float4(o[2 * i4][nt][r] * inv, o[2 * i4][nt][2 + r] * inv,
@@ -824,6 +845,54 @@ __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
                                   o[2 * i4 + 1][nt][2 + r] * inv);
         }
       }
+  }
+
+  // ---- the parts of a whole group meet: every warp of the team comes here
+  // (their limits run out on their own), then takes some of the rows ----
+  if (!p.whole || p.parts == 1) return;
+  const Seg4 u0 = inf.seg[0];
+  __syncwarp();
+  if (lane == 0) part_s[RB * D + RB] = gave_up ? 1.f : 0.f;
+  if (!u0.valid && lane < RB) part_s[RB * D + lane] = -INFINITY;
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * p.parts) : "memory");
+  if (u0.L < p.q_len || u0.L > (long long)p.max_blocks * kBlockSize) return;
+  if (p.early) pdl_wait();
+  constexpr int STRIDE = sizeof(Warp4<D, kStages4>) / 4;  // to the next part
+  const float *const first = part_s - part * STRIDE;
+  for (int x = 0; x < p.parts; ++x)
+    if (first[x * STRIDE + RB * D + RB] != 0.f) return;
+  for (int lr = part; lr < RB; lr += p.parts) {
+    const int gr = u0.rg * RB + lr;
+    if (gr >= p.rows) break;
+    float m = -INFINITY;
+    for (int x = 0; x < p.parts; ++x) m = fmaxf(m, first[x * STRIDE + RB * D + lr]);
+    float sum = 0.f, a[D / 32] = {};
+    for (int x = 0; x < p.parts; ++x) {
+      const float lx = first[x * STRIDE + RB * D + lr];
+      if (lx == -INFINITY) continue;  // (its rows may not be written)
+      const float w = ex2(lx - m);
+      sum += w;
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d)
+        a[d] = fmaf(w, first[x * STRIDE + lr * D + (D / 32) * lane + d], a[d]);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int i = gr / p.group, h = u0.g * p.group + gr % p.group;
+    const size_t row = ((size_t)u0.b * p.q_len + i) * p.num_q_heads + h;
+    uint32_t w[D / 64];
+#pragma unroll
+    for (int d = 0; d < D / 64; ++d) {
+      const __nv_bfloat162 v =
+          __floats2bfloat162_rn(a[2 * d] * inv, a[2 * d + 1] * inv);
+      w[d] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    uint32_t *const dst = reinterpret_cast<uint32_t *>(
+        static_cast<uint16_t *>(p.out) + row * D) + (D / 64) * lane;
+    if constexpr (D == 128)
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[D / 64 - 1]);
+    else
+      dst[0] = w[0];
+    if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
   }
 }
 

@@ -100,8 +100,9 @@ __global__ void __launch_bounds__(kSelThreads)
   if (bad || L <= p.budget) {  // nothing to choose (uniform over the cluster)
     if (bad && tid == 0 && rank == 0)
       atomicOr(&g_status_evict, (unsigned)SVP_DEV_BAD_SEQ_LEN);
-    for (int i = rank * kSelThreads + tid; i < p.budget; i += nc * kSelThreads)
-      kept[i] = !bad && i < L ? i : -1;
+    for (unsigned i = rank * kSelThreads + tid; i < (unsigned)p.budget;
+         i += nc * kSelThreads)
+      kept[i] = !bad && (int)i < L ? (int)i : -1;
     return;
   }
   // this CTA's positions [lo, hi): whole pages

@@ -29,6 +29,7 @@ struct AttnParams {
   int2 *split;         // 4-bit kernel: [groups] first and last slice
   int merge_rows;      // 4-bit kernel: query rows the merge walks per group
   int whole;           // 4-bit kernel: one slice per group, no merge
+  int parts;           // ... by this many warps of a CTA (1 unless whole)
   int slices;          // 4-bit kernel: set by its launcher, the partials' bound
   float *part_o;       // [2 * grid][RB][D] normalised partials: each CTA's
                        // first- and last-segment slot
@@ -61,6 +62,7 @@ struct AttnPlan {
   bool tc;             // tcgen05 path (tensor-memory accumulators)
   bool fp4;            // 4-bit cache kernel
   bool whole;          // its slices are whole groups: no workspace, no merge
+  int parts;           // and this many warps take one
   int batch_cap;       // sequences per launch
   size_t ws_head, ws_desc, ws_part_o, ws_part_lse, ws_total;
 };
@@ -135,8 +137,15 @@ cudaError_t launch_attention_tc(const AttnParams &p, int grid,
 // 24) for this many query rows per kv head and pages of the launch, the warps
 // (slices) of a CTA, of which an SM holds one, and the launch of attention
 // and merge.
-// Calls whose sequences span at most kWholePages pages take whole groups.
-constexpr int kWholePages = 32;
+// Calls whose sequences span at most kWholePages pages take whole groups,
+// shared by up to kMaxParts warps, if a warp then has kPartPages at most (one
+// query row, 8 heads, 63 pages: 1 sequence 12.6 us against 13.3 in slices, 32
+// 17.2 against 17.9, but 128, a warp to a group, 41 against 37; 125 pages: 16.9
+// against 12.1.  31 pages: 1 sequence 10 us, by one warp 21; 128 25 against 27;
+// 300, where warps take turns, 58 against 55).
+constexpr int kWholePages = 64;
+constexpr int kPartPages = 32;
+constexpr int kMaxParts = 8;
 int attention_fp4_rows(int rows, long long pages, int sms);
 int attention_fp4_warps(int rb);
 cudaError_t launch_attention_fp4(const AttnParams &p, int grid,

@@ -398,6 +398,77 @@ def test_wide_units(svp, d, batch, hkv, width, mask):
     assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("d,batch,hq,hkv,ql,width,mask", [
+    (64, 1, 4, 4, 1, 16, {}),
+    (128, 1, 8, 1, 1, 3, {}),
+    (128, 3, 16, 2, 2, 64, {}),                # 63 pages over eight warps
+    (128, 40, 16, 8, 1, 31, {}),               # four warps a group
+    (128, 90, 8, 8, 1, 20, {}),                # two
+    (64, 200, 8, 8, 1, 12, {}),                # one, and CTAs of twelve groups
+    (128, 30, 16, 4, 5, 30, {}),
+    (128, 8, 24, 4, 4, 40, dict(n_sink=3, window=100)),
+    (128, 5, 16, 4, 4, 8, "tree"),
+], ids=lambda x: None)
+def test_whole_groups(svp, d, batch, hq, hkv, ql, width, mask):
+    """Short sequences, the warps of a team with full, single and no pages;
+    one sequence's length is out of range and another's page is bad."""
+    import torch
+    rng = np.random.default_rng(width * batch)
+    lens = rng.integers(ql, 16 * width, batch)
+    lens[0] = 16 * width - 5
+    if batch > 2:
+        lens[1:3] = (ql, min(17, 16 * width))
+    q, kc, vc, table, lens = _inputs(8, lens, hq, hkv, d, ql, width=width)
+    g = [R.to_gpu(q, "bf16"), R.to_gpu(kc), R.to_gpu(vc), R.to_gpu(table), R.to_gpu(lens)]
+    if mask == "tree":
+        mask = dict(tree=np.tile(R.binary_tree(ql), (batch, 1)))
+        call = lambda *a: svp.paged_tree_attention(*a, R.to_gpu(mask["tree"]), scale=0.1)
+    else:
+        call = lambda *a: svp.paged_decode_attention(*a, scale=0.1, **mask)
+    out, lse = call(*g)
+    assert svp.read_device_status() == 0 and svp.last_launch_count() == 1
+    ref = _reference(q, kc, vc, d, float(np.float32(0.1)), lens, table, 1.0, 1.0, **mask)
+    _check(out, lse, ref, d)
+    if batch > 4:
+        bad_lens, bad = lens.copy(), table.copy()
+        bad_lens[3], bad[0, 0] = 10 ** 6, -7
+        o2, l2 = call(*g[:3], R.to_gpu(bad), R.to_gpu(bad_lens))
+        assert svp.read_device_status() == 3
+        rest = [b for b in range(batch) if b not in (0, 3)]
+        assert torch.equal(o2[rest], out[rest]) and torch.equal(l2[rest], lse[rest])
+        assert torch.isfinite(o2[0].float()).all()
+
+
+def test_stalled_whole_groups_time_out(svp):
+    """The same test build over short sequences, four warps to a group: those
+    with more than the two stages that arrive give up, the team meets and
+    leaves the output alone; a short sequence's team is right."""
+    import torch
+    from spec_verify_paged_gb300 import binding as bd, build
+    from test_bounded_wait import STALL_DEFINES
+    stall = bd.load_library(build.build_variant("stalltest", STALL_DEFINES))
+    d, batch = 128, 20
+    lens = [1000] * (batch - 1) + [100]
+    q, kc, vc, table, lens = _inputs(42, lens, 8, 8, d, 1)
+    g = [R.to_gpu(q, "bf16"), R.to_gpu(kc), R.to_gpu(vc), R.to_gpu(table), R.to_gpu(lens)]
+    out = torch.full(q.shape, 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full(q.shape[:3], 3.0, device="cuda")
+    dims = _dims(bd, batch, 8, g[1], table.shape[1])
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert stall.paged_decode_attention(
+        ctypes.byref(dims), *(t.data_ptr() for t in g), 1, 0, 0, float(np.float32(0.1)),
+        out.data_ptr(), lse.data_ptr(), stream) == 0
+    assert stall.svp_last_launch_count() == 1
+    torch.cuda.synchronize()
+    f = ctypes.c_int(0)
+    assert stall.svp_read_device_status(stream, ctypes.byref(f)) == 0
+    assert f.value & 8
+    assert (out[:-1] == 3).all() and (lse[:-1] == 3).all()
+    ref = svp.paged_decode_attention(*g, scale=0.1)
+    assert torch.equal(out[-1], ref[0][-1]) and torch.equal(lse[-1], ref[1][-1])
+    assert svp.read_device_status() == 0
+
+
 @pytest.mark.parametrize("path", [2, 3])
 def test_rows_that_see_nothing(svp, path):
     """A tree mask without any bit over a sequence of the new rows only: zero
