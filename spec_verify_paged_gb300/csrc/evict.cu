@@ -16,13 +16,15 @@
 //    the 17 MB of scores of 32 such groups are 2.5 us).  Sixteen CTAs per
 //    cluster were slower (four sequences of 131,072: 214 us in all against
 //    164: such clusters find room on few GPCs at a time), and so were four
-//    keys to a read in the later passes on short contexts.
+//    keys to a read in the later passes on short contexts, and eight warps
+//    for groups of one CTA (32 x 32 heads of up to 4096: 414 us in all
+//    against 351).
 //  * compact_kernel: moves the kept rows of K, V and the scores, a cluster to
-//    a group and side.  Bound by the moved bytes, read and written, and by
-//    the partly used sectors at both ends of a row.
+//    a group and side.  Bound by the moved bytes, read and written; scattered
+//    72-byte rows read 2.3 times their bytes (partial sectors and bursts).
 // Measured (both kernels): 32 sequences of 32 heads, 2200 to 4096 positions,
-// 2048 kept, bf16 rows of 256 bytes, to other pages: 360 us, 0.90 of the
-// bytes' time at the copy rate; one sequence of 8 heads, 1024 of 1087: 10 us.
+// 2048 kept, bf16 rows of 256 bytes, to other pages: 351 us, 0.92 of the
+// bytes' time at the copy rate; one sequence of 8 heads, 1024 of 1087: 9.3 us.
 // 4096 of 4200 positions of one sequence: 21 us in place or not (by columns
 // of 64 bytes, a warp to a column, in place took 77).
 #include <cooperative_groups.h>
@@ -72,15 +74,18 @@ __device__ __forceinline__ T block_scan(T v, T *warp_sum, T &sum) {
   __syncthreads();  // warp_sum may still be read from an earlier scan
   if (lane == 31) warp_sum[warp] = incl;
   __syncthreads();
-  T before = 0;
-  sum = 0;
+  // every warp scans the warps' sums
+  constexpr int NW = kSelThreads / 32;
+  static_assert(NW == 16, "four steps");
+  const T x = lane < NW ? warp_sum[lane] : T(0);
+  T y = x;
 #pragma unroll
-  for (int w = 0; w < kSelThreads / 32; ++w) {
-    const T x = warp_sum[w];
-    if (w < warp) before += x;
-    sum += x;
+  for (int off = 1; off < NW; off <<= 1) {
+    const T z = __shfl_up_sync(kFull, y, off);
+    if (lane >= off) y += z;
   }
-  return before + incl - v;
+  sum = __shfl_sync(kFull, y, NW - 1);
+  return __shfl_sync(kFull, y - x, warp) + incl - v;
 }
 
 __global__ void __launch_bounds__(kSelThreads)
@@ -187,14 +192,16 @@ __global__ void __launch_bounds__(kSelThreads)
     // (one 16-byte read of every CTA, all in flight)
     const int quad = (1 << bits) / 4 - 1 - tid;  // this thread's four bins
     uint4 q4 = make_uint4(0, 0, 0, 0);
-    if (quad >= 0) {
+    if (quad >= 0 && nc == 1) {
+      q4 = reinterpret_cast<const uint4 *>(hist)[quad];
+    } else if (quad >= 0) {
       uint4 part[kMaxCluster];
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r) {
         part[r] = make_uint4(0, 0, 0, 0);
         if (r < nc)
           part[r] = reinterpret_cast<const uint4 *>(
-              nc > 1 ? cluster.map_shared_rank(hist, r) : hist)[quad];
+              cluster.map_shared_rank(hist, r))[quad];
       }
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r) {
