@@ -203,6 +203,21 @@ def test_evict_in_place_through_an_equal_table(svp):
         assert np.array_equal(_raw(got), want)
 
 
+def test_evict_leaves_shared_prefixes_intact(svp):
+    """Three sequences share pages; their kept rows go to pages of their own
+    and nothing else changes."""
+    kc, vc, s, table, lens, dst = _evict_inputs("fp4", 128, 2, [300, 260, 90], 60)
+    table[1, :10] = table[0, :10]
+    table[2, :5] = table[0, :5]
+    g = [R.to_gpu(kc), R.to_gpu(vc), R.to_gpu(s)]
+    kept, new = svp.kv_evict(*g, R.to_gpu(table), R.to_gpu(lens), 60, 2, 10, R.to_gpu(dst))
+    ref, ref_lens = R.evict(s, lens, table, 60, 2, 10, 2)
+    assert np.array_equal(kept.cpu().numpy(), ref)
+    assert np.array_equal(new.cpu().numpy(), ref_lens)
+    for got, want in zip(g, _apply([kc, vc, s], ref, table, dst)):
+        assert np.array_equal(_raw(got), want)
+
+
 def test_two_evictions_at_once_and_replayed(svp):
     """Two streams evict different sequences of one cache at the same time;
     a captured eviction replayed on restored caches gives the same bytes."""
