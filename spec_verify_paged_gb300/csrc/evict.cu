@@ -140,9 +140,12 @@ __global__ void __launch_bounds__(kSelThreads)
     reinterpret_cast<uint4 *>(&sm.hist[0][0])[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
   if (cached) {
-    // four positions of a page at a time, all loads of up to 16 in flight
+    // four positions of a page at a time, all loads of up to 16 in flight.  lo
+    // is a page's start, or L where the sequence ends before this CTA's run (a
+    // short sequence in a wide table): rounded up, so that no thread of such a
+    // CTA takes the last, partial four of another's
     constexpr int U = 4;
-    for (int q0 = lo / 4 + tid; q0 * 4 < hi; q0 += U * kSelThreads) {
+    for (int q0 = (lo + 3) / 4 + tid; q0 * 4 < hi; q0 += U * kSelThreads) {
       const float *at[U];
       float4 v[U];
 #pragma unroll
