@@ -388,6 +388,10 @@ static int attention_call(const svp_dims *dims, const void *q,
                      : plan.mma || plan.fp4  ? SVP_PATH_TENSOR_CORES
                                              : SVP_PATH_CUDA_CORES,
                      sms, dims->num_blocks, &sub);
+      // the workspace was laid out for plan.grid.  A smaller batch can plan
+      // more CTAs than that: its shorter prefix lets an SM hold one more, and
+      // narrower units (attention_fp4_rows) count its pages twice
+      sub.grid = std::min(sub.grid, plan.grid);
     }
     cudaError_t e =
         plan.fp4 ? launch_attention_fp4(p, sub.grid, stream)

@@ -57,3 +57,87 @@ def test_evict_short_sequences_in_a_wide_table(svp, width, lens, budget, n_sink,
                 slot = np.arange(len(pos))
                 want[dst[b, slot // 16], h, slot % 16] = old[table[b, pos // 16], h, pos % 16]
         assert np.array_equal(got.cpu().numpy(), want)
+
+
+# ------------------------------------- the last launch of a call of several
+
+def _guarded(svp, q, kc, table, split_pages=0):
+    """A workspace of exactly the size the call asks for, and the bytes behind
+    it (0xa5)."""
+    import ctypes
+    import torch
+    from spec_verify_paged_gb300 import binding as bd
+    d = q.shape[-1]
+    code = bd._cache_code(kc, q.dtype)
+    dims = bd.SvpDims(q.shape[0], q.shape[2], kc.shape[1], d, 16, table.shape[1],
+                      kc.shape[0], code, None, 0, split_pages, 0, 1.0, 1.0)
+    need = svp.load_library().paged_decode_workspace_size(ctypes.byref(dims), q.shape[1], 0, 0)
+    whole = torch.full((need + (64 << 20),), 0xa5, dtype=torch.uint8, device="cuda")
+    return whole[:need], whole[need:]
+
+
+def _torch_attention(q, k, v, scale):
+    """q [.., H, D], k and v [.., n, H, D] of one row each, fp64."""
+    x = (k.double() * q.double()[:, None]).sum(-1) * scale
+    p = x.softmax(1)
+    return (p[..., None] * v.double()).sum(1), x.logsumexp(1)
+
+
+def test_last_launch_stays_in_the_workspace_bf16(svp):
+    """4100 sequences on the CUDA cores: 4096 short ones, then a launch of
+    four long ones, whose CTAs an SM holds more of."""
+    import torch
+    B, hkv, d, width = 4100, 2, 128, 600
+    g = torch.Generator(device="cuda").manual_seed(3)
+    pages = 1 + 4 * width
+    kc, vc = (torch.randn((pages, hkv, 16, d), device="cuda", generator=g).bfloat16()
+              for _ in range(2))
+    q = torch.randn((B, 1, hkv, d), device="cuda", generator=g).bfloat16()
+    table = torch.zeros((B, width), dtype=torch.int32, device="cuda")
+    table[4096:] = torch.arange(1, pages, dtype=torch.int32, device="cuda").view(4, width)
+    lens = torch.ones(B, dtype=torch.int32, device="cuda")
+    lens[4096:] = 16 * width - torch.arange(4, dtype=torch.int32, device="cuda")
+    ws, guard = _guarded(svp, q, kc, table)
+    out, lse = svp.paged_decode_attention(q, kc, vc, table, lens, scale=0.1, workspace=ws)
+    assert svp.read_device_status() == 0
+    assert (guard == 0xa5).all()
+    # rows of one key: the value itself and its score (128 products in fp32)
+    assert torch.equal(out[:4096, 0], vc[0, :, 0].expand(4096, -1, -1))
+    for b in range(4096, B):
+        n = int(lens[b])
+        k, v = (c[table[b].long()].transpose(1, 2).flatten(0, 1)[None, :n] for c in (kc, vc))
+        o, l = _torch_attention(q[b], k, v, 0.1)
+        # bf16 output, half a step, and fp32 sums of 9600 weights
+        assert (out[b].double() - o).abs().max() <= 2.0 ** -8 * o.abs().max() + 1e-4
+        assert (lse[b].double() - l).abs().max() <= 1e-4
+
+
+def test_last_launch_stays_in_the_workspace_4bit(svp):
+    """1018 sequences of a page each, 20 rows: the first launch takes units of
+    24 rows, the last has fewer pages than those want, and slices of a size
+    that one CTA's warps are the whole workspace."""
+    import torch
+    B, hkv, group, d, split = 1018, 48, 20, 64, 12289
+    g = torch.Generator(device="cuda").manual_seed(4)
+    q = torch.randn((B, 1, hkv * group, d), device="cuda", generator=g).bfloat16()
+    x = torch.randn((1, 16, hkv, d), device="cuda", generator=g).bfloat16()
+    kc = torch.zeros((1, hkv, 16, svp.fp4_row_bytes(d)), dtype=torch.uint8, device="cuda")
+    vc = torch.zeros_like(kc)
+    table = torch.zeros((B, 1), dtype=torch.int32, device="cuda")
+    lens = torch.full((B,), 16, dtype=torch.int32, device="cuda")
+    svp.kv_append(x, x, kc, vc, table[:1], lens[:1])
+    k, v = svp.kv_gather(kc, vc, table[:1], lens[:1], 16)
+    ws, guard = _guarded(svp, q, kc, table, split)
+    out, lse = svp.paged_decode_attention(q, kc, vc, table, lens, scale=0.1, workspace=ws,
+                                          split_pages=split)
+    assert svp.read_device_status() == 0
+    assert (guard == 0xa5).all()
+    qs = q[:, 0].unflatten(1, (hkv, group))
+    for h in range(0, hkv, 7):
+        s = torch.einsum("bgd,nd->bgn", qs[:, h].double(), k[0, :, h].double()) * 0.1
+        o = torch.einsum("bgn,nd->bgd", s.softmax(-1), v[0, :, h].double())
+        at = slice(h * group, (h + 1) * group)
+        # fp16 weights (2^-11) of values up to max|v|, bf16 output
+        tol = 2.0 ** -10 * v[0, :, h].abs().max() + 2.0 ** -8 * o.abs()
+        assert ((out[:, 0, at].double() - o).abs() <= tol).all()
+        assert (lse[:, 0, at].double() - s.logsumexp(-1)).abs().max() <= 1e-4
