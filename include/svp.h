@@ -103,7 +103,8 @@ typedef struct {
   int max_blocks_per_seq;
   int num_blocks;
   int dtype;              /* svp_dtype of q, out and both caches           */
-  void *workspace;        /* device scratch for split partials, or NULL    */
+  void *workspace;        /* device scratch for split partials (16-byte
+                             aligned), or NULL                            */
   size_t workspace_bytes; /* size of `workspace`                           */
   int split_pages;        /* fewest pages per CTA slice; 0 = automatic (8) */
   int kernel_path;        /* svp_kernel_path; SVP_PATH_AUTO by default     */
@@ -173,7 +174,7 @@ typedef enum {
  * (re)allocated inside the call when it is too small -- that first call is
  * then not capturable in a CUDA graph.  Calls that share a workspace must
  * not overlap on the GPU.
- * q, k_cache, v_cache and out must be 16-byte aligned.
+ * q, k_cache, v_cache, out and dims->workspace must be 16-byte aligned.
  * Errors: SVP_ERR_INVALID_ARG for null or misaligned pointers, sizes < 0,
  * num_q_heads not a multiple of num_kv_heads, q_len < 1, n_sink < 0,
  * window < 0, a non-finite scale or an unknown kernel_path;

@@ -308,10 +308,10 @@ static int attention_call(const svp_dims *dims, const void *q,
     return SVP_ERR_INVALID_ARG;
   if (dims->num_blocks == 0 || dims->max_blocks_per_seq == 0)
     return SVP_ERR_INVALID_ARG;
-  // pages, q and out move with 16-byte bulk copies
+  // pages, q, out and split partials move with 16-byte vectors and bulk copies
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_cache) |
-       reinterpret_cast<uintptr_t>(v_cache) | reinterpret_cast<uintptr_t>(out)) %
-          16 != 0)
+       reinterpret_cast<uintptr_t>(v_cache) | reinterpret_cast<uintptr_t>(out) |
+       reinterpret_cast<uintptr_t>(dims->workspace)) % 16 != 0)
     return SVP_ERR_INVALID_ARG;
   const int sms = device_sms();
   if (sms <= 0) return SVP_ERR_CUDA;
