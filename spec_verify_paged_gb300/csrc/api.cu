@@ -93,7 +93,7 @@ static int check_dims(const svp_dims *d) {
 static int max_visible_pages(int max_blocks, int q_len, int n_sink,
                              int window) {
   if (window == 0) return max_blocks;
-  const long long sink_pages = (n_sink + kBlockSize - 1) / kBlockSize;
+  const long long sink_pages = ((long long)n_sink + kBlockSize - 1) / kBlockSize;
   const long long win_pages =
       ((long long)window + q_len - 1 + kBlockSize - 1) / kBlockSize + 1;
   const long long b = sink_pages + win_pages;

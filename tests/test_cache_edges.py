@@ -141,3 +141,31 @@ def test_last_launch_stays_in_the_workspace_4bit(svp):
         tol = 2.0 ** -10 * v[0, :, h].abs().max() + 2.0 ** -8 * o.abs()
         assert ((out[:, 0, at].double() - o).abs() <= tol).all()
         assert (lse[:, 0, at].double() - s.logsumexp(-1)).abs().max() <= 1e-4
+
+
+# ------------------------------------------------------- masks at their ends
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp4"])
+def test_all_keys_are_sinks(svp, dtype):
+    """n_sink up to INT_MAX beside a window: every key is visible, to attention
+    and to the score update, as without a window."""
+    import torch
+    rng = np.random.default_rng(4)
+    lens = np.array([1500, 3], np.int32)
+    table, total, _ = R.pages(rng, lens, width=200)
+    cache = [R.to_gpu(R.make_cache(rng, dtype, total, 2, 64), "bf16" if dtype == "bf16" else None)
+             for _ in range(2)]
+    q = R.to_gpu(R.bf16(rng.standard_normal((2, 2, 4, 64))), "bf16")
+    pg = [R.to_gpu(table), R.to_gpu(lens)]
+    want = svp.paged_decode_attention(q, *cache, *pg)
+    for n_sink in (2 ** 31 - 16, 2 ** 31 - 1):
+        for window in (1, 2 ** 31 - 1):
+            m = dict(n_sink=n_sink, window=window)
+            out, lse = svp.paged_decode_attention(q, *cache, *pg, **m)
+            # the same slices of the same pages
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+            s = [torch.zeros((total, 2, 16), device="cuda") for _ in range(2)]
+            svp.paged_score_update(q, cache[0], lse, *pg, s[0])
+            svp.paged_score_update(q, cache[0], lse, *pg, s[1], **m)
+            assert torch.equal(*s) and float(s[0].sum()) > 0
+    assert svp.read_device_status() == 0

@@ -37,3 +37,16 @@ def test_workspace_alignment(lib, dtype, off):
     assert lib.paged_tree_attention(ctypes.byref(d), P, P, P, P, P, 2, P, 0.1, P, P,
                                     None) == -1
     assert lib.svp_last_launch_count() == 0
+
+
+@pytest.mark.parametrize("dtype", [1, 3])
+@pytest.mark.parametrize("n_sink", [2 ** 31 - 16, 2 ** 31 - 15, 2 ** 31 - 1])
+def test_any_number_of_sinks_plans_the_whole_table(lib, dtype, n_sink):
+    """Sinks beyond any length: the visible pages are the table's, as without
+    a window."""
+    d = _dims(dtype=dtype, batch=8, max_blocks_per_seq=4096, num_blocks=4096)
+    all_pages = lib.paged_decode_workspace_size(ctypes.byref(d), 1, 0, 0)
+    assert all_pages > 256
+    for window in (1, 16, 2 ** 31 - 1):
+        assert lib.paged_decode_workspace_size(ctypes.byref(d), 1, n_sink,
+                                               window) == all_pages
