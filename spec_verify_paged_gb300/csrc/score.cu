@@ -47,7 +47,8 @@ constexpr int kScoreMaxPages = 32 * kScoreWarps;  // of one CTA
 
 struct ScoreRows {
   // score scale (log2 domain) and log2-domain LSE (+inf: the row adds
-  // nothing): two rows are one 16-byte read
+  // nothing, whatever its products -- a padding row's zeros make NaN of an
+  // infinite key): two rows are one 16-byte read
   alignas(16) float2 ql[kScoreRows];
   int pos[kScoreRows];        // query position within the new rows
   uint32_t bits[kScoreRows];  // ancestor bits (all ones without a tree)
@@ -329,6 +330,7 @@ __global__ void __launch_bounds__(kScoreThreads)
           d[h] += __shfl_xor_sync(kFull, d[h], 1);
           d[h] += __shfl_xor_sync(kFull, d[h], 2);
           const float w = ex2(fmaf(d[h], ql.x, -ql.y));
+          if (ql.y == INFINITY) continue;
           if (all_vis || key_visible(j0 + g + 8 * h, t0 + rows.pos[r],
                                      rows.bits[r], t0, p.n_sink, p.window))
             sum[h] += w;
@@ -353,6 +355,8 @@ __global__ void __launch_bounds__(kScoreThreads)
             *reinterpret_cast<const float4 *>(&rows.ql[nt * 8 + 2 * t]);
         float w[4] = {ex2(fmaf(acc[0], ql.x, -ql.y)), ex2(fmaf(acc[1], ql.z, -ql.w)),
                       ex2(fmaf(acc[2], ql.x, -ql.y)), ex2(fmaf(acc[3], ql.z, -ql.w))};
+        if (ql.y == INFINITY) w[0] = w[2] = 0.f;
+        if (ql.w == INFINITY) w[1] = w[3] = 0.f;
         if (!all_vis) {  // warp-uniform
 #pragma unroll
           for (int e = 0; e < 4; ++e) {

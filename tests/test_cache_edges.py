@@ -169,3 +169,80 @@ def test_all_keys_are_sinks(svp, dtype):
             svp.paged_score_update(q, cache[0], lse, *pg, s[1], **m)
             assert torch.equal(*s) and float(s[0].sum()) > 0
     assert svp.read_device_status() == 0
+
+
+# -------------------------------------------- scores over infinite keys
+
+@pytest.mark.parametrize("dtype,d,hq,hkv,ql", [
+    ("bf16", 128, 2, 2, 1), ("bf16", 64, 6, 2, 1), ("bf16", 128, 6, 2, 3),
+    ("bf16", 64, 8, 1, 1), ("bf16", 128, 32, 2, 9), ("f32", 64, 2, 2, 1),
+])
+def test_score_update_over_infinite_keys(svp, dtype, d, hq, hkv, ql):
+    """A visible key with an infinite element: its score is -inf for every
+    row, its weight 0, and its old score stays; the number of rows makes no
+    difference."""
+    import torch
+    rng = np.random.default_rng(hq)
+    lens = np.array([60], np.int32)
+    table, total, _ = R.pages(rng, lens)
+    io = "bf16" if dtype == "bf16" else None
+    kc = R.make_cache(rng, dtype, total, hkv, d)
+    q = R.bf16(rng.standard_normal((1, ql, hq, d)))
+    q[..., 7] = -np.abs(q[..., 7]) - 1
+    q = R.bf16(q)       # (what the call is given)
+    for j in (3, 20, 47):
+        kc[table[0, j // 16], :, j % 16, 7] = np.inf
+    scale = float(np.float32(0.1))
+    with np.errstate(invalid="ignore"):
+        k = kc.astype(np.float64)
+        _, lse, _, _ = R.attention(q, k, np.zeros_like(k), scale, lens, table)
+    assert np.isfinite(lse).all()
+    lse = lse.astype(np.float32)
+    old = rng.random((total, hkv, 16)).astype(np.float32)
+    scores = R.to_gpu(old)
+    gq = R.to_gpu(q.astype(np.float32), io)
+    svp.paged_score_update(gq, R.to_gpu(kc, io), R.to_gpu(lse), R.to_gpu(table),
+                           R.to_gpu(lens), scores, scale=scale)
+    ref, _ = R.score_update(q, k, lse.astype(np.float64), scale, lens, table, old, ql)
+    assert np.isfinite(ref).all()
+    got = scores.double().cpu().numpy()
+    # a weight is off by a factor 1 + 2 (2 D + 8) u sum|q||k| scale at most (the
+    # sum is about 10 at D = 128: 3e-4 if every rounding of the products' sum
+    # fell the same way; 1e-4 is asked for)
+    assert (np.abs(got - ref) <= 1e-4 * np.abs(ref)).all()
+    for j in (3, 20, 47):
+        at = table[0, j // 16], slice(None), j % 16
+        assert np.array_equal(got[at], old[at].astype(np.float64))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_left_out_by_their_lse(svp, dtype):
+    """A row whose lse is -inf adds nothing, not even over a key whose score
+    for it is +inf or NaN."""
+    import torch
+    rng = np.random.default_rng(2)
+    d, hq, hkv, ql = 64, 4, 2, 2
+    lens = np.array([40], np.int32)
+    table, total, _ = R.pages(rng, lens)
+    io = "bf16" if dtype == "bf16" else None
+    kc = R.make_cache(rng, dtype, total, hkv, d)
+    q = R.bf16(rng.standard_normal((1, ql, hq, d)))
+    q[0, 0, 1, 7], q[0, 0, 3, 7] = 1.0, 0.0           # +inf and NaN scores
+    q[0, 0, [0, 2], 7] = -1.0
+    q[0, 1, :, 7] = -1.0
+    kc[table[0, 0], :, 5, 7] = np.inf
+    lse = rng.standard_normal((1, ql, hq)).astype(np.float32) + 4
+    lse[0, 0, [1, 3]] = -np.inf
+    old = rng.random((total, hkv, 16)).astype(np.float32)
+    scores = R.to_gpu(old)
+    scale = float(np.float32(0.125))
+    svp.paged_score_update(R.to_gpu(q.astype(np.float32), io), R.to_gpu(kc, io),
+                           R.to_gpu(lse), R.to_gpu(table), R.to_gpu(lens), scores,
+                           scale=scale)
+    ref, _ = R.score_update(q, kc.astype(np.float64), lse.astype(np.float64), scale,
+                            lens, table, old, ql)
+    assert np.isfinite(ref).all()
+    got = scores.double().cpu().numpy()
+    assert (np.abs(got - ref) <= 1e-4 * np.abs(ref)).all()
+    at = table[0, 0], slice(None), 5
+    assert np.array_equal(got[at], old[at].astype(np.float64))
