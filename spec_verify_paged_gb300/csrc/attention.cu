@@ -1138,9 +1138,7 @@ static int prepare_t(int batch) {
     auto it = g_occ.find(key);
     if (it != g_occ.end()) return it->second;
   }
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem) != cudaSuccess)
-    return -1;
+  if (allow_smem((const void *)kern, smem) != cudaSuccess) return -1;
   int n = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, smem) !=
       cudaSuccess)

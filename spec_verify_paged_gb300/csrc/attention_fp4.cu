@@ -58,9 +58,6 @@
 
 #include <cmath>
 #include <cstdint>
-#include <map>
-#include <mutex>
-#include <tuple>
 
 #include "attn_common.cuh"
 #include "fp4.cuh"
@@ -997,9 +994,6 @@ __global__ void __launch_bounds__(32 * kMergeWarps4)
 
 // ---- host side ----
 
-std::mutex g_mu4;
-std::map<std::tuple<int, const void *, size_t>, bool> g_ready4;
-
 template <int D, int NT>
 size_t smem4(int batch) {
   return sizeof(Smem4<D, NT, warps4<NT>(), stages4<NT>()>) + sizeof(int) * 2 * (size_t)batch + 128;
@@ -1013,21 +1007,8 @@ cudaError_t launch4(AttnParams p, int grid, cudaStream_t st) {
                     232448,
                 "a CTA's shared memory");
   auto kern = paged_attention_fp4_kernel<D, NT>;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  cudaError_t e = allow_smem((const void *)kern, smem4<D, NT>(p.batch));
   if (e != cudaSuccess) return e;
-  // the largest request, once per device
-  const size_t most = smem4<D, NT>(kBatchFp4);
-  {
-    std::lock_guard<std::mutex> lk(g_mu4);
-    bool &ready = g_ready4[std::make_tuple(dev, (const void *)kern, most)];
-    if (!ready) {
-      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)most);
-      if (e != cudaSuccess) return e;
-      ready = true;
-    }
-  }
   e = launch_pdl(kern, (unsigned)grid, 32u * warps4<NT>(), smem4<D, NT>(p.batch),
                  st, p);
   if (e != cudaSuccess || p.whole) return e;

@@ -1408,9 +1408,7 @@ static int prepare_tc(int batch) {
     auto it = g_tc4_occ.find(key);
     if (it != g_tc4_occ.end()) return it->second;
   }
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem) != cudaSuccess)
-    return -1;
+  if (allow_smem((const void *)kern, smem) != cudaSuccess) return -1;
   int n = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kTcThreads,
                                                     smem) != cudaSuccess)

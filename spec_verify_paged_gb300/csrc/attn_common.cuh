@@ -24,7 +24,9 @@
 
 #include <cmath>
 #include <cstdint>
+#include <map>
 #include <mutex>
+#include <utility>
 
 #include "ptx.cuh"
 #include "svp.h"
@@ -414,6 +416,24 @@ __global__ void __launch_bounds__(kMergeThreads)
 }
 
 // ---- host side ----
+
+// Lets `kern` take `bytes` of dynamic shared memory on the current device.
+// The limit is one value per kernel, and launches of different batch sizes
+// ask for different amounts: it is only ever raised.
+inline cudaError_t allow_smem(const void *kern, size_t bytes) {
+  static std::mutex mu;
+  static std::map<std::pair<int, const void *>, size_t> limits;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(mu);
+  size_t &limit = limits[std::make_pair(dev, kern)];
+  if (bytes <= limit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)bytes);
+  if (e == cudaSuccess) limit = bytes;
+  return e;
+}
 
 // cuTensorMapEncodeTiled, fetched once through the runtime (no -lcuda).
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t,

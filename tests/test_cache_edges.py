@@ -246,3 +246,47 @@ def test_rows_left_out_by_their_lse(svp, dtype):
     assert (np.abs(got - ref) <= 1e-4 * np.abs(ref)).all()
     at = table[0, 0], slice(None), 5
     assert np.array_equal(got[at], old[at].astype(np.float64))
+
+
+# -------------------------------------- calls of different sizes, one process
+
+SIZES = '''
+import sys
+import torch
+import spec_verify_paged_gb300 as svp
+kind, sizes = sys.argv[1], [int(x) for x in sys.argv[2].split(",")]
+d, group = dict(tc4=(128, 40), tc=(128, 4), cores=(128, 1), mma=(64, 4))[kind]
+most = max(sizes)
+x = torch.randn((most, 1, 1, d), device="cuda").bfloat16()
+q = torch.randn((most, 1, group, d), device="cuda").bfloat16()
+row = svp.fp4_row_bytes(d) if kind == "tc4" else d
+k = torch.zeros((most, 1, 16, row), device="cuda",
+                dtype=torch.uint8 if kind == "tc4" else torch.bfloat16)
+v = torch.zeros_like(k)
+table = torch.arange(most, dtype=torch.int32, device="cuda").view(-1, 1)
+lens = torch.ones(most, dtype=torch.int32, device="cuda")
+svp.kv_append(x, x, k, v, table, lens)
+want, _ = svp.kv_gather(k, v, table, lens, 1)
+for n in sizes:
+    out, lse = svp.paged_decode_attention(q[:n], k, v, table[:n], lens[:n])
+    torch.cuda.synchronize()
+    # one key a sequence: every row is its value
+    assert torch.equal(out, want[:n].expand(-1, -1, group, -1)), n
+    assert torch.isfinite(lse).all(), n
+assert svp.read_device_status() == 0
+print("done")
+'''
+
+
+@pytest.mark.parametrize("kind", ["tc4", "tc", "cores", "mma"])
+@pytest.mark.parametrize("sizes", ["600,600", "300,10,300,600"])
+def test_calls_of_changing_batch_sizes(svp, kind, sizes):
+    """In a process of its own: a smaller launch leaves the next larger one
+    its shared memory."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", SIZES, kind, sizes], cwd=root,
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "done" in r.stdout, r.stderr[-2000:]
