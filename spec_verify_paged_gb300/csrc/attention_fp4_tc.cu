@@ -556,8 +556,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                          __uint_as_float(w[k] & 0xffff0000u) * f);
         // a score is S times this; a scale of zero or less is applied to S
         // itself, so that the maximum is always taken with a positive factor
+        // (at least 2^-126: a product that underflowed to zero would make NaN
+        // of a masked key's -inf; |S| < 2^34, so a score is nothing either way)
         if (c_blk == 0)
-          sm.qsc[slot][r] = (p.qscale > 0.f ? p.qscale : 1.f) * pow2i(e - 14);
+          sm.qsc[slot][r] = fmaxf(
+              (p.qscale > 0.f ? p.qscale : 1.f) * pow2i(e - 14), 0x1p-126f);
         unsigned char *dst = sm.q + (c_blk >> 2) * (UR * 128) + r * 128;
 #pragma unroll
         for (int k = 0; k < 2; ++k)

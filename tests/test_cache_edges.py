@@ -171,6 +171,37 @@ def test_all_keys_are_sinks(svp, dtype):
     assert svp.read_device_status() == 0
 
 
+@pytest.mark.parametrize("path", [2, 3])
+@pytest.mark.parametrize("hq", [2, 20, 30, 48])
+def test_zero_query_rows_and_tiny_factors(svp, path, hq):
+    """A query row of zeros weighs every visible key the same, however small
+    scale * k_scale is."""
+    import torch
+    rng = np.random.default_rng(hq)
+    d, ql, lens = 128, 2, np.array([2, 37, 130, 700], np.int32)
+    table, total, _ = R.pages(rng, lens)
+    kc = R.make_cache(rng, "fp4", total, 2, d, 1.0, lens, table)
+    vc = R.make_cache(rng, "fp4", total, 2, d, 1.0, lens, table)
+    q = R.bf16(rng.standard_normal((len(lens), ql, hq, d)))
+    q[:, :, ::2] = 0
+    out, lse = svp.paged_decode_attention(
+        R.to_gpu(q, "bf16"), R.to_gpu(kc), R.to_gpu(vc), R.to_gpu(table),
+        R.to_gpu(lens), scale=1.0, k_scale=1e-30, kernel_path=path)
+    with np.errstate(invalid="ignore"):
+        v = R.values(vc, "fp4", d)
+    for b, L in enumerate(lens):
+        for i in range(ql):
+            n = L - ql + i + 1
+            for h in range(hq):    # a score is below 1e-25: no weight differs
+                vv = R.logical(v, table[b], h // (hq // 2), L)[:n]
+                # fp16 weights, 2^-11; bf16 output, 2^-8
+                tol = 2.0 ** -10 * np.abs(vv).max() + 2.0 ** -8 * np.abs(vv.mean(0))
+                got = out[b, i, h].double().cpu().numpy()
+                assert (np.abs(got - vv.mean(0)) <= tol).all()
+                assert abs(float(lse[b, i, h]) - np.log(n)) <= 1e-5
+    assert svp.read_device_status() == 0
+
+
 # -------------------------------------------- scores over infinite keys
 
 @pytest.mark.parametrize("dtype,d,hq,hkv,ql", [
