@@ -833,7 +833,11 @@ __global__ void __launch_bounds__(32 * warps4<NT>(), 1)
           }
         } else {
           float *const to = p.whole ? part_s : p.part_o + slot * RB * D;
-          if (g == 0) (p.whole ? part_s + RB * D : p.part_lse + slot * RB)[lr] = lse2;
+          // (+inf, not NaN, of a row that is NaN: maxima keep it and the
+          // weight it gives is NaN again)
+          if (g == 0)
+            (p.whole ? part_s + RB * D : p.part_lse + slot * RB)[lr] =
+                lse2 == lse2 ? lse2 : INFINITY;
           float4 *dst = reinterpret_cast<float4 *>(to + lr * D + (D / 8) * g);
 #pragma unroll
           for (int i4 = 0; i4 < D / 32; ++i4)

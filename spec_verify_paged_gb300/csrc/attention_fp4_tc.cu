@@ -1222,8 +1222,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         float *fw = gi == 0 ? sm.f0 : sm.f1;
         if (gt < N) {
           fw[gt] = l_run > 0.f ? p.v_scale / l_run : 0.f;
-          const float lse2 =
-              l_run > 0.f ? m_run + (log2f(l_run) - kPShift) : -INFINITY;
+          const float lse2 =  // (NaN of a row that is NaN)
+              l_run == 0.f ? -INFINITY : m_run + (log2f(l_run) - kPShift);
           if (single) {
             if (gt < vrows) {
               const int gr = row0 + gt;
@@ -1231,7 +1231,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               p.lse[((size_t)b * p.q_len + i) * p.num_q_heads + h] = lse2 * kLn2;
             }
           } else {
-            sm.lse_st[gi][gt] = lse2;
+            // (+inf for NaN: the merge's maxima keep it and the weight it
+            // gives is NaN again)
+            sm.lse_st[gi][gt] = lse2 == lse2 ? lse2 : INFINITY;
           }
         }
         named_bar(gbar, kGroupThreads);
@@ -1310,7 +1312,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           sm.f0[gt] = w0 * inv;
           sm.f1[gt] = w1 * inv;
           const float lse2 =
-              lt > 0.f ? mr + (log2f(lt) - kPShift) : -INFINITY;
+              lt == 0.f ? -INFINITY : mr + (log2f(lt) - kPShift);
           if (single) {
             if (gt < vrows) {
               const int gr = row0 + gt;
@@ -1318,7 +1320,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               p.lse[((size_t)b * p.q_len + i) * p.num_q_heads + h] = lse2 * kLn2;
             }
           } else {
-            sm.lse_st[0][gt] = lse2;
+            sm.lse_st[0][gt] = lse2 == lse2 ? lse2 : INFINITY;
           }
         }
         // group 1's state is read: its slot may be reused

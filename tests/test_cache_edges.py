@@ -202,6 +202,35 @@ def test_zero_query_rows_and_tiny_factors(svp, path, hq):
     assert svp.read_device_status() == 0
 
 
+@pytest.mark.parametrize("path", [2, 3])
+@pytest.mark.parametrize("hq", [2, 20, 48])
+@pytest.mark.parametrize("split", [0, 1])
+def test_nan_query_rows_give_nan(svp, path, hq, split):
+    """A row with a NaN is NaN, output and lse, in short sequences and in
+    groups that many slices share; the other rows are as without it."""
+    import torch
+    rng = np.random.default_rng(hq)
+    d, lens = 128, np.array([1, 90, 5000], np.int32)
+    table, total, _ = R.pages(rng, lens)
+    cache = [R.to_gpu(R.make_cache(rng, "fp4", total, 2, d, 1.0, lens, table))
+             for _ in range(2)]
+    q = R.to_gpu(R.bf16(rng.standard_normal((3, 1, hq, d))), "bf16")
+    call = lambda x: svp.paged_decode_attention(
+        x, *cache, R.to_gpu(table), R.to_gpu(lens), scale=0.1, kernel_path=path,
+        split_pages=split)
+    out, lse = call(q)
+    bad = q.clone()
+    row = hq // 2
+    bad[:, 0, row, 5] = float("nan")
+    o2, l2 = call(bad)
+    assert torch.isnan(o2[:, 0, row]).all() and torch.isnan(l2[:, 0, row]).all()
+    rest = [h for h in range(hq) if h != row]
+    # (rows of a tile share the moves of its softmax reference: rounding)
+    assert (o2[:, 0, rest].float() - out[:, 0, rest].float()).abs().max() <= 2.0 ** -6
+    assert (l2[:, 0, rest] - lse[:, 0, rest]).abs().max() <= 1e-4
+    assert svp.read_device_status() == 0
+
+
 # -------------------------------------------- scores over infinite keys
 
 @pytest.mark.parametrize("dtype,d,hq,hkv,ql", [
