@@ -50,10 +50,31 @@ def _compile(src: str, extra) -> str:
     return obj
 
 
+def _calls_tag() -> str:
+    """What the module's object code is bound to beside its source: torch's
+    C++ headers and library folder, and Python's."""
+    import importlib.metadata
+    import importlib.util
+    import sysconfig
+    try:
+        where = importlib.util.find_spec("torch").origin
+        torch = f"{importlib.metadata.version('torch')} {where}"
+    except (AttributeError, importlib.metadata.PackageNotFoundError):
+        torch = "none"
+    return f"torch {torch}\npython {sysconfig.get_config_var('SOABI')}\n"
+
+
+def _calls_tag_file() -> str:
+    return os.path.join(BUILD_DIR, "svp_calls.tag")
+
+
 def _calls_stale() -> bool:
     deps = (CALLS_SRC, os.path.join(INCLUDE, "svp.h"))
-    return (not os.path.exists(CALLS_LIB) or
-            any(os.path.getmtime(d) > os.path.getmtime(CALLS_LIB) for d in deps))
+    if (not os.path.exists(CALLS_LIB) or not os.path.exists(_calls_tag_file()) or
+            any(os.path.getmtime(d) > os.path.getmtime(CALLS_LIB) for d in deps)):
+        return True
+    with open(_calls_tag_file()) as f:
+        return f.read() != _calls_tag()
 
 
 def _compile_calls() -> str:
@@ -66,6 +87,7 @@ def _compile_calls() -> str:
     obj = os.path.join(BUILD_DIR, "calls.o")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-c",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DSVP_TORCH="{torch.__version__}"',
            "-I", INCLUDE, "-isystem", inc, "-isystem",
            os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem",
            sysconfig.get_paths()["include"], "-isystem",
@@ -104,7 +126,15 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
         if objs:
             _link(objs)
         if calls_obj:
-            _link_calls(calls_obj.result())
+            try:
+                _link_calls(calls_obj.result())
+            except Exception as e:
+                raise RuntimeError(
+                    "svp_calls.so did not build, so the 4-bit cache, gather, "
+                    "score and eviction calls will raise (libsvp.so is in "
+                    f"place): {e}") from e
+            with open(_calls_tag_file(), "w") as f:
+                f.write(_calls_tag())
     return LIB
 
 

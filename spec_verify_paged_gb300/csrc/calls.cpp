@@ -446,4 +446,12 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "svp_calls", nullptr, -1, kMethods
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit_svp_calls(void) { return PyModule_Create(&kModule); }
+PyMODINIT_FUNC PyInit_svp_calls(void) {
+  PyObject *m = PyModule_Create(&kModule);
+  // the torch whose headers this was compiled against
+  if (m && PyModule_AddStringConstant(m, "torch_version", SVP_TORCH) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
