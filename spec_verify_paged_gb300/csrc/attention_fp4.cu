@@ -374,7 +374,7 @@ __device__ __forceinline__ Seg4 whole_segment(const AttnParams &p, int per_seq,
   s.g = gi / p.n_rg;
   s.rg = gi - s.g * p.n_rg;
   s.L = p.seq_lens[s.b];
-  if (s.L < p.q_len || s.L > p.max_blocks * kBlockSize) {
+  if (s.L < p.q_len || s.L > (long long)p.max_blocks * kBlockSize) {
     if (lane == 0 && gi == 0) raise4(SVP_DEV_BAD_SEQ_LEN);
     return s;
   }
@@ -921,7 +921,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps4)
   // nobody records a group of a sequence whose length is out of range, nor
   // one whose slices gave up (a timeout): an unwritten record names anything,
   // so it is followed only within the slots there are
-  if (gr >= p.rows || L < p.q_len || L > p.max_blocks * kBlockSize ||
+  if (gr >= p.rows || L < p.q_len || L > (long long)p.max_blocks * kBlockSize ||
       fl.x < 0 || fl.y <= fl.x || fl.y >= p.slices)
     return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

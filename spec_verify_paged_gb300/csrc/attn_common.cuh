@@ -179,7 +179,7 @@ __device__ __forceinline__ int build_prefix(const AttnParams &p, int *prefix,
     if (b < p.batch) {
       const int L = p.seq_lens[b];
       seqlen[b] = L;
-      if (L < p.q_len || L > p.max_blocks * kBlockSize) {
+      if (L < p.q_len || L > (long long)p.max_blocks * kBlockSize) {
         if (blockIdx.x == 0) atomicOr(status, (unsigned)SVP_DEV_BAD_SEQ_LEN);
       } else {
         int na, bs, np;

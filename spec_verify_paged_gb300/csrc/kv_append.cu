@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
   const int k = (int)((row / p.num_kv_heads) % p.n_new);
   const int b = (int)(row / ((long long)p.num_kv_heads * p.n_new));
   const int L = p.seq_lens[b];
-  if (L < p.n_new || L > p.max_blocks * kBlockSize) {
+  if (L < p.n_new || L > (long long)p.max_blocks * kBlockSize) {
     if (lane == 0) atomicOr(&g_status_append, (unsigned)SVP_DEV_BAD_SEQ_LEN);
     return;
   }

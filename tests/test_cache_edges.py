@@ -231,6 +231,37 @@ def test_nan_query_rows_give_nan(svp, path, hq, split):
     assert svp.read_device_status() == 0
 
 
+@pytest.mark.parametrize("dtype,paths", [("fp4", (2, 3)), ("bf16", (1, 3))])
+def test_tables_of_2_to_the_27_pages(svp, dtype, paths):
+    """A table whose width in tokens passes 32 bits: the same as a narrow one."""
+    import torch
+    rng = np.random.default_rng(6)
+    d, lens = 128, np.array([50], np.int32)
+    table, total, _ = R.pages(rng, lens)
+    io = "bf16" if dtype == "bf16" else None
+    wide = torch.full((1, 2 ** 27), -1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = R.to_gpu(table)
+    x = R.to_gpu(R.bf16(rng.standard_normal((1, 2, 1, d))), "bf16")
+    q = R.to_gpu(R.bf16(rng.standard_normal((1, 2, 4, d))), "bf16")
+    gl = R.to_gpu(lens)
+    start = R.make_cache(rng, dtype, total, 1, d)
+    got = []
+    for t in (R.to_gpu(table), wide):
+        k, v = R.to_gpu(start, io), R.to_gpu(start, io)
+        svp.kv_append(x, x, k, v, t, gl)
+        res = [k, v, *svp.kv_gather(k, v, t, gl, 50)]
+        for path in paths:
+            out, lse = svp.paged_decode_attention(q, k, v, t, gl, kernel_path=path)
+            res += [out, lse]
+        s = torch.zeros((total, 1, 16), device="cuda")
+        svp.paged_score_update(q, k, lse, t, gl, s)
+        got.append(res + [s])
+        assert svp.read_device_status() == 0
+    # (slices differ with the width: partial sums in another order, bf16 out)
+    for a, b in zip(*got):
+        assert (a.float() - b.float()).abs().max() <= 2.0 ** -7
+
+
 # -------------------------------------------- scores over infinite keys
 
 @pytest.mark.parametrize("dtype,d,hq,hkv,ql", [
