@@ -287,9 +287,10 @@ int kv_append(const svp_dims *dims, const void *k_new, const void *v_new,
  * (the newest rows).  Positions outside [0, seq_lens[b]) give zero rows.
  * FP8 and FP4 values are code (* scale) * k_scale rounded once to bf16.
  * For dense kernels over a cached prefix, and for moving rows between
- * caches.  k_out and v_out overlap neither each other nor the caches.  A sequence length outside [0, max_blocks_per_seq*16] gives zero
- * rows and SVP_DEV_BAD_SEQ_LEN, a bad block id a zero row and
- * SVP_DEV_BAD_BLOCK_ID.  Uses no workspace.
+ * caches.  k_out and v_out overlap neither each other nor the caches.  A
+ * sequence length outside [0, max_blocks_per_seq*16] gives zero rows and
+ * SVP_DEV_BAD_SEQ_LEN, a bad block id a zero row and SVP_DEV_BAD_BLOCK_ID.
+ * Uses no workspace.
  * Errors as for kv_append, with n_rows >= 0. */
 int kv_gather(const svp_dims *dims, const void *k_cache, const void *v_cache,
               const int32_t *block_table, const int32_t *seq_lens,
@@ -310,11 +311,14 @@ int kv_gather(const svp_dims *dims, const void *k_cache, const void *v_cache,
  * lengths and mask (n_sink and window, or tree_mask if not NULL, as there).
  * The newest n_fresh positions (0 <= n_fresh <= q_len; q_len for the rows
  * just appended) start from zero: their old score is not read.  Other keys'
- * scores stay as they are.  Rows with lse = -inf add nothing.  Reads K
- * only; one launch for each 128 query rows of a kv head (group * q_len); no
- * workspace, no atomics: the result does not depend on the order of the
- * CTAs.  No page may appear twice in the call's visible
- * block-table entries (a page's scores belong to one sequence).
+ * scores stay as they are.  Rows with lse = -inf add nothing, whatever
+ * their products.  Reads K only; one launch for each 128 query rows of a
+ * kv head (group * q_len); no workspace, no atomics: the result does not
+ * depend on the order of the CTAs.  No page may appear twice in the call's
+ * visible block-table entries: its scores are read and written back once for
+ * each, so one update would be lost.  Sequences that share pages are updated
+ * in calls of their own, in stream order; a shared page's scores then hold
+ * what all of them gave it.
  * Errors: those of paged_decode_attention (tree_mask: of
  * paged_tree_attention), SVP_ERR_INVALID_ARG for n_fresh outside [0, q_len]
  * or lse / scores not 4-byte aligned.  dims->workspace, split_pages,

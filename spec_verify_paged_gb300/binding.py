@@ -445,7 +445,12 @@ def paged_score_update(q, k_cache, lse, block_table, seq_lens, scores,
     [B, q_len, Hq, D], lse [B, q_len, Hq] being what the attention call with
     the same arguments returned (include/svp.h: paged_score_update).  The
     newest n_fresh positions (default: q_len) start from zero.  Returns
-    scores."""
+    scores.
+
+    No page may stand twice among the sequences of one call: its scores are
+    read and written back once for each, and one update would be lost.
+    Sequences that share pages (a common prefix) are updated in calls of their
+    own, one after another; a shared page's scores then count them all."""
     st = (_calls or _load_calls()).score_update(
         q, k_cache, lse, block_table, seq_lens, scores, n_fresh, n_sink, window,
         tree_mask, scale, k_scale, _raw(stream))
@@ -459,7 +464,11 @@ def kv_evict(k_cache, v_cache, scores, block_table, seq_lens, budget, n_sink=0,
     rows, its newest n_recent and the best-scored others, in order, as the
     first rows of dst_block_table's pages (default: in place); scores move
     along (include/svp.h: kv_evict).  Returns (kept [B, Hkv, budget] int32
-    positions, -1 padded, new_lens [B] int32)."""
+    positions, -1 padded, new_lens [B] int32).
+
+    In place, a sequence's pages are its own and its block table has room for
+    the budget.  Sequences that share pages go to pages of their own: the
+    source pages, scores included, are then only read."""
     r = (_calls or _load_calls()).evict(
         k_cache, v_cache, scores, block_table, seq_lens, budget, n_sink,
         n_recent, dst_block_table, kept, new_lens, _raw(stream))

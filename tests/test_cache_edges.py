@@ -381,3 +381,52 @@ def test_calls_of_changing_batch_sizes(svp, kind, sizes):
     r = subprocess.run([sys.executable, "-c", SIZES, kind, sizes], cwd=root,
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "done" in r.stdout, r.stderr[-2000:]
+
+
+# ------------------------------------------------------ flows of the README
+
+def _score_inputs(seed, lens, hq, hkv, d, ql, table=None, total=None):
+    rng = np.random.default_rng(seed)
+    lens = np.asarray(lens, np.int32)
+    if table is None:
+        table, total, _ = R.pages(rng, lens)
+    kc = R.make_cache(rng, "fp4", total, hkv, d)
+    q = R.bf16(rng.standard_normal((len(lens), ql, hq, d)))
+    old = rng.random((total, hkv, 16)).astype(np.float32)
+    return q, kc, lens, table, old
+
+
+def test_scores_of_shared_pages_one_call_a_sequence(svp):
+    """Sequences that share pages are updated one after another: a shared
+    page's scores hold what all of them gave it, and each evicts by that into
+    pages of its own."""
+    import torch
+    rng = np.random.default_rng(21)
+    lens = np.array([300, 260, 90], np.int32)
+    hq, hkv, d, budget = 8, 2, 128, 60
+    table, total, spare = R.pages(rng, lens, spare=3 * 4)
+    table[1, :10] = table[0, :10]
+    table[2, :5] = table[0, :5]
+    q, kc, lens, table, old = _score_inputs(22, lens, hq, hkv, d, 1, table, total)
+    scale = float(np.float32(0.1))
+    g = [R.to_gpu(q, "bf16"), R.to_gpu(kc), R.to_gpu(table), R.to_gpu(lens)]
+    scores = R.to_gpu(old)
+    _, lse = svp.paged_decode_attention(g[0], g[1], g[1], g[2], g[3], scale=scale)
+    for b in range(3):
+        at = slice(b, b + 1)
+        svp.paged_score_update(g[0][at], g[1], lse[at], g[2][at], g[3][at], scores,
+                               scale=scale)
+    k = R.values(kc, "fp4", d)
+    l64 = lse.double().cpu().numpy()
+    ref = old
+    for b in range(3):
+        at = slice(b, b + 1)
+        ref, _ = R.score_update(q[at], k, l64[at], scale, lens[at], table[at], ref, 1)
+    got = scores.double().cpu().numpy()
+    # weights within 2 (2 D + 8) 2^-24 sum|q||k| scale, which is below 13
+    assert (np.abs(got - ref) <= 4e-4 * np.abs(ref)).all()
+    dst = spare.reshape(3, 4)
+    kept, new = svp.kv_evict(g[1], g[1].clone(), scores, g[2], g[3], budget, 2, 10,
+                             R.to_gpu(dst))
+    want, _ = R.evict(got.astype(np.float32), lens, table, budget, 2, 10, hkv)
+    assert np.array_equal(kept.cpu().numpy(), want)
