@@ -312,7 +312,9 @@ int kv_gather(const svp_dims *dims, const void *k_cache, const void *v_cache,
  * The newest n_fresh positions (0 <= n_fresh <= q_len; q_len for the rows
  * just appended) start from zero: their old score is not read.  Other keys'
  * scores stay as they are.  Rows with lse = -inf add nothing, whatever
- * their products.  Reads K only; one launch for each 128 query rows of a
+ * their products: after a verification a caller leaves the rejected drafts'
+ * rows out by overwriting their lse (the next step's rows start from zero
+ * where those stood).  Reads K only; one launch for each 128 query rows of a
  * kv head (group * q_len); no workspace, no atomics: the result does not
  * depend on the order of the CTAs.  No page may appear twice in the call's
  * visible block-table entries: its scores are read and written back once for

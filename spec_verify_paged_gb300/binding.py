@@ -450,7 +450,12 @@ def paged_score_update(q, k_cache, lse, block_table, seq_lens, scores,
     No page may stand twice among the sequences of one call: its scores are
     read and written back once for each, and one update would be lost.
     Sequences that share pages (a common prefix) are updated in calls of their
-    own, one after another; a shared page's scores then count them all."""
+    own, one after another; a shared page's scores then count them all.
+
+    Rows whose lse is -inf add nothing.  After a verification,
+    lse.masked_fill_((arange(q_len) > n_accepted[:, None])[..., None], -inf)
+    leaves the rejected drafts' rows out; the next step's rows then start from
+    zero where those stood."""
     st = (_calls or _load_calls()).score_update(
         q, k_cache, lse, block_table, seq_lens, scores, n_fresh, n_sink, window,
         tree_mask, scale, k_scale, _raw(stream))

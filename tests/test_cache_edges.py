@@ -430,3 +430,41 @@ def test_scores_of_shared_pages_one_call_a_sequence(svp):
                              R.to_gpu(dst))
     want, _ = R.evict(got.astype(np.float32), lens, table, budget, 2, 10, hkv)
     assert np.array_equal(kept.cpu().numpy(), want)
+
+
+def test_scores_of_a_verification_leave_rejected_drafts_out(svp):
+    """After a verification the rows of rejected drafts take an lse of -inf
+    before the score update: the scores are those of the accepted rows alone,
+    and the next step's rows start from zero where rejected ones stood."""
+    import torch
+    hq, hkv, d, ql = 8, 2, 128, 4
+    q, kc, lens, table, old = _score_inputs(23, [64, 45, 90], hq, hkv, d, ql)
+    scale = float(np.float32(0.1))
+    g = [R.to_gpu(q, "bf16"), R.to_gpu(kc), R.to_gpu(table), R.to_gpu(lens)]
+    scores = R.to_gpu(old)
+    _, lse = svp.paged_decode_attention(g[0], g[1], g[1], g[2], g[3], scale=scale)
+    n_accepted = torch.tensor([0, 3, 1], dtype=torch.int32, device="cuda")
+    rejected = torch.arange(ql, device="cuda") > n_accepted[:, None]
+    lse.masked_fill_(rejected[..., None], -float("inf"))
+    svp.paged_score_update(g[0], g[1], lse, g[2], g[3], scores, scale=scale)
+    l64 = lse.double().cpu().numpy()
+    k = R.values(kc, "fp4", d)
+    ref = old
+    for b, n in enumerate(n_accepted.tolist()):
+        # the definition over the accepted rows of the shorter sequence
+        at = slice(b, b + 1)
+        short = lens[at] - ql + n + 1
+        ref, _ = R.score_update(q[at, :n + 1], k, l64[at, :n + 1], scale, short,
+                                table[at], ref, n + 1)
+        for j in range(short[0], lens[b]):      # rejected: nobody sees them
+            ref[table[b, j // 16], :, j % 16] = 0.0
+    got = scores.double().cpu().numpy()
+    assert (np.abs(got - ref) <= 4e-4 * np.abs(ref)).all()
+    # the next step appends where the rejected rows were
+    lens2 = lens - ql + n_accepted.cpu().numpy() + 1 + ql
+    lens2 = np.minimum(lens2, 16 * np.array([(t >= 0).sum() for t in table])).astype(np.int32)
+    gl = R.to_gpu(lens2)
+    _, lse = svp.paged_decode_attention(g[0], g[1], g[1], g[2], gl, scale=scale)
+    svp.paged_score_update(g[0], g[1], lse, g[2], gl, scores, scale=scale)
+    ref, _ = R.score_update(q, k, lse.double().cpu().numpy(), scale, lens2, table, got, ql)
+    assert (np.abs(scores.double().cpu().numpy() - ref) <= 4e-4 * np.abs(ref)).all()
