@@ -468,3 +468,107 @@ def test_scores_of_a_verification_leave_rejected_drafts_out(svp):
     svp.paged_score_update(g[0], g[1], lse, g[2], gl, scores, scale=scale)
     ref, _ = R.score_update(q, k, lse.double().cpu().numpy(), scale, lens2, table, got, ql)
     assert (np.abs(scores.double().cpu().numpy() - ref) <= 4e-4 * np.abs(ref)).all()
+
+
+# ---------------------------------------- the captured step over 4-bit caches
+
+@pytest.mark.parametrize("hq,hkv,ql,lens,path,split,mask", [
+    (8, 8, 1, [40, 900, 2100], 0, 0, {}),                   # slices
+    (8, 2, 3, [3, 70, 1500], 2, 1, {}),                     # many slices
+    (16, 2, 5, [17, 700, 1300], 2, 4, {}),                  # 40 rows, mma.sync
+    (8, 2, 4, [300, 2000], 0, 2, dict(n_sink=5, window=300)),
+    (16, 2, 5, [17, 700, 1300], 0, 0, {}),                  # 40 rows, tcgen05
+    (8, 2, 3, [35, 500, 3000], 3, 0, {}),                   # 16-row units
+    (32, 2, 2, [2, 33, 1100], 3, 8, {}),                    # 32-row units
+    (32, 2, 4, [16, 129, 1100], 3, 0, dict(n_sink=3, window=200)),  # 64
+    (8, 2, 16, [16, 33, 1600], 0, 0, "tree"),               # 64 rows
+    (8, 2, 7, [7, 150, 1000], 2, 1, "tree"),
+])
+def test_step_runner_in_slices_and_on_tcgen05(svp, hq, hkv, ql, lens, path, split, mask):
+    """The captured step, whose attention reads the prefix pages while the
+    append runs, gives bit for bit what the single calls give, over groups
+    that slices cut and over the tcgen05 kernel."""
+    import torch
+    rng = np.random.default_rng(hq + ql)
+    d, vocab, B = 128, 64, len(lens)
+    lens = np.asarray(lens, np.int32)
+    steps = 4
+    top = lens + steps * ql
+    table, total, _ = R.pages(rng, top)
+    start = [R.make_cache(rng, "fp4", total, hkv, d) for _ in range(2)]
+    runs = [[R.to_gpu(x) for x in start] for _ in range(2)]
+    kw = dict(split_pages=split, kernel_path=path, k_scale=0.4, v_scale=0.3)
+    tree = mask == "tree"
+    m = {} if tree else mask
+    run = svp.StepRunner(*runs[0], B, hq, ql, table.shape[1], vocab=vocab if tree else 0,
+                         tree_nodes=ql if tree else 0, **kw, **m)
+    bits = np.tile(R.binary_tree(ql), (B, 1))
+    gt = R.to_gpu(table)
+    try:
+        for step in range(steps):
+            n = lens + step * ql
+            t = [R.to_gpu(rng.standard_normal((B, ql, h, d)), "bf16") for h in (hq, hkv, hkv)]
+            slot = step % 2
+            for name, x in zip(("q", "k_new", "v_new"), t):
+                run.host(slot, name)[:] = x.view(torch.int16).cpu().numpy().view(np.uint16)
+            run.host(slot, "block_table")[:] = table
+            run.host(slot, "seq_lens")[:] = n
+            if tree:
+                run.host(slot, "tree_mask")[:] = bits.view(np.uint32)
+                run.host(slot, "parents")[:] = [(i - 1) // 2 if i else -1 for i in range(ql)]
+                run.host(slot, "node_tokens")[:] = 1
+                run.host(slot, "target_logits")[:] = 0
+                run.host(slot, "draft_logits")[:] = 0
+                run.host(slot, "uniforms")[:] = 0.5
+            run.launch(slot)
+            run.wait(slot)
+            gl = R.to_gpu(n)
+            svp.kv_append(t[1], t[2], *runs[1], gt, gl, k_scale=0.4, v_scale=0.3)
+            if tree:
+                out, lse = svp.paged_tree_attention(t[0], *runs[1], gt, gl, R.to_gpu(bits), **kw)
+            else:
+                out, lse = svp.paged_decode_attention(t[0], *runs[1], gt, gl, **kw, **m)
+            got = torch.from_numpy(run.host(slot, "out").view(np.int16).copy())
+            assert torch.equal(got, out.view(torch.int16).cpu())
+            assert np.array_equal(run.host(slot, "lse"), lse.cpu().numpy())
+            assert torch.isfinite(out.float()).all()
+        for a, b in zip(*runs):
+            assert torch.equal(a, b)
+    finally:
+        run.close()
+    assert svp.read_device_status() == 0
+
+
+@pytest.mark.parametrize("ql,mask", [(1, {}), (3, dict(n_sink=3, window=20)), (12, "tree")])
+def test_more_sequences_than_a_tcgen05_launch_takes(svp, ql, mask):
+    """600 sequences of 36 query rows on the automatic path: 512 and the rest,
+    twice."""
+    import torch
+    rng = np.random.default_rng(ql)
+    B, d, hq = 600, 128, 36 // ql
+    lens = rng.integers(ql, 70, B).astype(np.int32)
+    lens[[0, 511, 512, 599]] = (300, ql, 400, 17)
+    table, total, _ = R.pages(rng, lens)
+    kc = R.make_cache(rng, "fp4", total, 1, d, 1.0, lens, table)
+    vc = R.make_cache(rng, "fp4", total, 1, d, 1.0, lens, table)
+    q = R.bf16(rng.standard_normal((B, ql, hq, d)))
+    g = [R.to_gpu(q, "bf16"), R.to_gpu(kc), R.to_gpu(vc), R.to_gpu(table), R.to_gpu(lens)]
+    if mask == "tree":
+        mask = dict(tree=np.tile(R.binary_tree(ql), (B, 1)))
+        call = lambda: svp.paged_tree_attention(*g, R.to_gpu(mask["tree"]), scale=0.1)
+    else:
+        call = lambda: svp.paged_decode_attention(*g, scale=0.1, **mask)
+    out, lse = call()
+    assert svp.read_device_status() == 0 and svp.last_launch_count() == 4
+    again = call()
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    with np.errstate(invalid="ignore"):
+        k, v = (R.values(x, "fp4", d) for x in (kc, vc))
+    o_ref, l_ref, mag, vmax = R.attention(q, k, v, float(np.float32(0.1)), lens, table, **mask)
+    # as test_fp4_cache.py: fp32 sums of D products, fp16 weights, bf16 output
+    u = 2.0 ** -24
+    delta = 2 * d * u * mag + 8 * u * (mag + np.abs(l_ref))
+    tol = ((2 * delta + 2.0 ** -11 + 2.0 ** -16) * vmax)[..., None] + 2.0 ** -8 * np.abs(o_ref)
+    assert (np.abs(out.double().cpu().numpy() - o_ref) <= tol).all()
+    err = np.abs(lse.double().cpu().numpy() - l_ref)
+    assert (err <= 2 * delta + 2.0 ** -18 + 4 * u * np.abs(l_ref)).all()
