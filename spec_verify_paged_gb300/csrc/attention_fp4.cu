@@ -5,17 +5,18 @@
 // V = code * scale * v_scale.  k_scale is folded into the score scale,
 // v_scale multiplies the outputs, code * scale is exact in fp16.
 //
-// What bounds it: the issue slots.  A cached element is 9/16 byte, so at the
-// copy rate an SM has to turn 80 elements a nanosecond into products: a page
-// of K and V (2304 bytes, D = 128) may take 99 cycles, and its conversion,
-// products and softmax, about 250 warp instructions for up to 8 rows, take
-// 111 with twelve warps (without the copies; the copies alone: 100 us of
-// the 122 of four 131,072-token sequences).  On the CUDA cores
-// that is an FMA per element and query row on top of the conversion; here
-// even a single query row goes through mma.sync (keys as M, query rows as
-// N = 8): the conversion (one cvt and one fp16 multiply per two elements)
-// is done once per element for all rows, and the codes go from shared
-// memory to the matrix instruction through registers only.
+// What bounds it: latency.  A cached element is 9/16 byte, so at the copy
+// rate an SM has to turn 80 elements a nanosecond into products: a page of K
+// and V (2304 bytes, D = 128) may take 99 cycles.  Its conversion, products
+// and softmax are about 250 warp instructions for up to 8 rows, 63 issue
+// cycles of the SM's four schedulers, but take 111 with the three warps a
+// scheduler that registers leave (without the copies; issue active 50%, and
+// 1.6 of the stalls an instruction are fixed latencies).  Hence as few
+// instructions an element as there are: even a single query row goes through
+// mma.sync (keys as M, query rows as N = 8), so the conversion (one cvt and
+// one fp16 multiply per two elements) is done once per element for all rows,
+// and the codes go from shared memory to the matrix instruction through
+// registers only.
 //
 //  * S^T = K Q^T, one 16-key page per m16 tile: lane (g, t) takes
 //    consecutive codes (whole scale blocks) of two keys.  Q is fp16 with a
@@ -41,19 +42,19 @@
 //  * Short sequences (kWholePages) are taken whole, a group by one warp or by
 //    a team of neighbours whose results meet in shared memory: no prefix of
 //    the lengths to build, no partials in memory and no second launch (250
-//    tokens of four heads: 7.5 us a call, 11.5 by single warps).
+//    tokens of four heads: 7.4 us a call).
 //  * A group of pages cut by slice borders leaves one normalised partial per
 //    slice; merge_fp4_kernel joins them by log-sum-exp in slice order.
 //  * Rows whose memory holds no valid data take no part: masked keys score
 //    -inf whatever their bytes, and their V scale is replaced by 0.
 //
-// Measured (attention and merge, D = 128; of the cache's bytes at the copy
-// rate): 32 sequences of 32 heads, up to 4096 tokens, one row each: 77.5 us,
-// 0.65; four sequences of 131,072 tokens, 8 rows: 122 us, 0.73; 16 sequences
-// of 8 heads, up to 8192 tokens, 20 rows: 59.5 us, 0.24 -- there an SM's
-// eight warps issue 0.27 instructions a cycle and scheduler, waiting on the
-// fixed latencies of conversion, MMA and exponential chains (1.8 of 5.6
-// cycles an instruction) and on code (0.8).
+// Measured (call times, D = 128; of the cache's bytes at the copy rate): 32
+// sequences of 32 heads, up to 4096 tokens, one row each: 78.5 us, 0.64 (a
+// bf16 cache: 242 us); four sequences of 131,072 tokens, 8 rows: 123 us, 0.73
+// (326); 16 sequences of 8 heads, up to 8192 tokens, 20 rows: 60 us, 0.24
+// (68) -- there an SM's eight warps issue 0.34 instructions a cycle and
+// scheduler, waiting on the fixed latencies of conversion, MMA and
+// exponential chains (1.9 stalls an instruction) and on code (0.7).
 #include <cuda_fp16.h>
 
 #include <cmath>
@@ -1029,8 +1030,8 @@ cudaError_t launch4(AttnParams p, int grid, cudaStream_t st) {
 // neighbouring units run close together).  Three tiles convert the cache
 // once where two units convert it twice, but a warp goes through its pages
 // more slowly and the longer code takes longer to fetch, so it needs work:
-// 20 rows, 8 heads, up to 8192 positions: batch 1 30 us against 22, 6 43
-// against 43 (20 pages a warp), 16 59 against 68, 64 202 against 300.
+// 20 rows, 8 heads, 2048 to 8192 positions: batch 1 31 us against 23, 6 41.5
+// against 39 (20 pages a warp), 16 60 against 72, 64 165 against 229.
 constexpr int kMinPages3 = 20;
 int attention_fp4_rows(int rows, long long pages, int sms) {
   if (rows <= 8) return 8;

@@ -21,18 +21,21 @@
 //    weights down to 2^-28 stay normal (each is rounded by at most 2^-11);
 //    the row sums, of the fp32 weights, carry the same factor.
 //
-// What bounds it: the tile pipeline.  A tile takes 2860 cycles at 60 rows
-// where its 18 KB would take 790 at the copy rate: its 16 MMAs (M = 128, 87
-// cycles each whatever the rows) are 1400, the softmax of 128 keys x 64 rows
-// runs beside them, and its K and V tiles are written and read through shared
-// memory (128 KB, about 1000).  Without the conversion the same calls take
-// 59 us for 75 (20 rows) and 71 for 89 (60 rows): the dequantising warps are
-// a quarter of it.  Against the mma.sync kernel the conversion is done once
-// for all rows of a unit (up to 64), not once per 16 or 24.
+// What bounds it: the chain of a tile.  A tile takes 2860 cycles at 60 rows
+// where its 18 KB would take 790 at the copy rate, and neither the tensor
+// pipe (9% active) nor issue (33%) is near its limit: conversion, S, the
+// maximum over four warps, P through shared memory, P V and the fold of O
+// follow one another with barriers between, and two tiles in flight do not
+// cover it (4.7 stalls an instruction on loads, 2.3 on barriers).  Without
+// the conversion the calls took 59 us for 75 (20 rows) and 71 for 89 (60
+// rows): the dequantising warps are a quarter of it.  Against the mma.sync
+// kernel the conversion is done once for all rows of a unit (up to 64), not
+// once per 16 or 24.
 //
-// Measured (16 sequences of 8 heads, up to 8192 tokens: 98 MB of cache; call
-// times): 60 rows 89 us against 120 of the mma.sync kernel, 32 rows 75
-// against 73, 20 rows 75 against 59.
+// Measured (16 sequences of 8 heads, 2048 to 8192 tokens: 98 MB of cache;
+// call times against the mma.sync kernel's, and a bf16 cache's): 20 rows 76
+// us against 60 and 69, 32 rows 76 against 74 and 69, 36 rows 89 against 97
+// and 75, 60 rows 90 against 126 and 75.
 #include <cstring>
 #include <map>
 #include <mutex>

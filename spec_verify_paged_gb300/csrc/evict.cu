@@ -14,19 +14,18 @@
 //    histogram, cluster barrier and scan, and the numbering (131,072
 //    positions on eight CTAs: 12-16, 10, 10, 5 and 14 thousand cycles, 27 us;
 //    the 17 MB of scores of 32 such groups are 2.5 us).  Sixteen CTAs per
-//    cluster were slower (four sequences of 131,072: 214 us in all against
-//    164: such clusters find room on few GPCs at a time), and so were four
-//    keys to a read in the later passes on short contexts, and eight warps
-//    for groups of one CTA (32 x 32 heads of up to 4096: 414 us in all
-//    against 351).
+//    cluster were slower (four sequences of 131,072: 1.3 times the whole call:
+//    such clusters find room on few GPCs at a time), and so were four keys to
+//    a read in the later passes on short contexts, and eight warps for groups
+//    of one CTA (32 x 32 heads of up to 4096: 1.18 times the whole call).
 //  * compact_kernel: moves the kept rows of K, V and the scores, a cluster to
 //    a group and side.  Bound by the moved bytes, read and written; scattered
 //    72-byte rows read 2.3 times their bytes (partial sectors and bursts).
-// Measured (both kernels): 32 sequences of 32 heads, 2200 to 4096 positions,
-// 2048 kept, bf16 rows of 256 bytes, to other pages: 351 us, 0.92 of the
-// bytes' time at the copy rate; one sequence of 8 heads, 1024 of 1087: 9.3 us.
-// 4096 of 4200 positions of one sequence: 21 us in place or not (by columns
-// of 64 bytes, a warp to a column, in place took 77).
+// Measured (both kernels, call times): 32 sequences of 32 heads, 2200 to 4096
+// positions, 2048 kept, bf16 rows of 256 bytes: 352 us to other pages, 0.92 of
+// the bytes' time at the copy rate, and 356 in place; one sequence of 8 heads,
+// 1024 of 1087: 9.1 us; 4096 of 4200: 24 and 21; 16,384 of 131,072 4-bit rows,
+// one sequence 45 and 48, four 89 and 94.
 #include <cooperative_groups.h>
 
 #include <cstdint>

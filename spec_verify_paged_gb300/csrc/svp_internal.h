@@ -106,9 +106,10 @@ constexpr int kBatchFp4 = 512;
 // mma.sync for head_dim 64.
 constexpr int kMmaMinRows = 3;
 
-// The same for 4-bit caches at head_dim 128: below, the mma.sync kernel (98 MB
-// of cache: 20 rows 59 us against 75, 32 rows 73 against 75; 60 rows: 120
-// against 89).
+// The same for 4-bit caches at head_dim 128: below, the mma.sync kernel, whose
+// units convert the cache once per 16 or 24 rows (98 MB of cache, 8 heads: 4
+// rows 35 us against 66 on tcgen05, 16 47 against 66, 24 61 against 76, 32 74
+// against 76; 36 97 against 89, 48 99 against 90, 60 126 against 90).
 constexpr int kFp4TcMinRows = 33;
 
 // Occupancy-derived CTAs per SM for the attention kernel of this shape
@@ -138,11 +139,11 @@ cudaError_t launch_attention_tc(const AttnParams &p, int grid,
 // (slices) of a CTA, of which an SM holds one, and the launch of attention
 // and merge.
 // Calls whose sequences span at most kWholePages pages take whole groups,
-// shared by up to kMaxParts warps, if a warp then has kPartPages at most (one
-// query row, 8 heads, 63 pages: 1 sequence 12.6 us against 13.3 in slices, 32
-// 17.2 against 17.9, but 128, a warp to a group, 41 against 37; 125 pages: 16.9
-// against 12.1.  31 pages: 1 sequence 10 us, by one warp 21; 128 25 against 27;
-// 300, where warps take turns, 58 against 55).
+// shared by up to kMaxParts warps, if a warp then has kPartPages at most (call
+// times, one query row, 8 heads, 31 pages: 1 sequence 10.1 us against 14.1 in
+// slices, 32 13.5 against 16.8, 128 27.6 against 33.2; 300, where warps take
+// turns, 64.6 against 59.9.  63 pages: 1 sequence 12.7 against 14.0, 32 19.5
+// against 23.1).
 constexpr int kWholePages = 64;
 constexpr int kPartPages = 32;
 constexpr int kMaxParts = 8;
