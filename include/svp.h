@@ -285,7 +285,8 @@ int kv_append(const svp_dims *dims, const void *k_new, const void *v_new,
  * cache, else bf16) is the value the caches hold at logical position
  * start + i, start = starts[b] or, with starts == NULL, seq_lens[b] - n_rows
  * (the newest rows).  Positions outside [0, seq_lens[b]) give zero rows.
- * FP8 and FP4 values are code (* scale) * k_scale rounded once to bf16.
+ * FP8 and FP4 values are code (* scale) * k_scale, the last product in fp32,
+ * then rounded to bf16.
  * For dense kernels over a cached prefix, and for moving rows between
  * caches.  k_out and v_out overlap neither each other nor the caches.  A
  * sequence length outside [0, max_blocks_per_seq*16] gives zero rows and

@@ -377,9 +377,10 @@ def _load_calls():
         spec = importlib.util.spec_from_file_location("svp_calls", CALLS_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
-        if module.torch_version != torch.__version__:
+        built = getattr(module, "torch_version", "of another version")
+        if built != torch.__version__:
             raise RuntimeError(
-                f"{CALLS_PATH} was built for torch {module.torch_version}, this is "
+                f"{CALLS_PATH} was built for torch {built}, this is "
                 f"{torch.__version__}: build it again with "
                 "`python -c 'import __graft_entry__ as g; g.build()'`")
         _calls = module

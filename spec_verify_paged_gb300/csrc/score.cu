@@ -8,13 +8,13 @@
 // CTAs -- and K is read once, V not at all.
 //
 // What bounds it: K's bytes for few rows -- 32 sequences of 32 heads, up to
-// 4096 tokens, one row: bf16 101 us, 0.91 of the copy rate, fp32 181, FP8 74.  With many rows
-// over a 4-bit cache the start of the CTAs (lengths, page ids, query rows:
-// 3-4 us each, five resident per SM) and the conversion and exponentials of
-// a page (about 200 warp instructions at 20 rows): 16 sequences of 8 heads,
-// up to 8192 tokens, 20 rows: 28.6 us where the bytes take 7.9.  Fewer, longer
-// CTAs with pages fetched three ahead left SMs idle at ragged lengths (53
-// pages a CTA: 40 us).  Design:
+// 4096 tokens, one row: bf16 101 us, 0.91 of the copy rate, fp32 181, FP8 74.
+// With many rows over a 4-bit cache the start of the CTAs (lengths, page ids,
+// query rows: 3-4 us each, five resident per SM) and the conversion and
+// exponentials of a page (about 200 warp instructions at 20 rows): 16
+// sequences of 8 heads, up to 8192 tokens, 20 rows: 28.4 us where the bytes
+// take 7.9.  Fewer, longer CTAs with pages fetched three ahead left SMs idle
+// at ragged lengths (53 pages a CTA: 40 us).  Design:
 //  * K goes from global memory to registers as matrix operands: keys are M,
 //    query rows N (m16n8k16, one page per tile), and the k positions are
 //    dealt to the dimensions so that a lane's operands are consecutive
