@@ -7,9 +7,13 @@
  * (kv_append), let the new query rows attend to their sequence's cached
  * rows (paged_decode_attention), and accept or resample the draft tokens
  * (spec_accept).  Caches are fp32, bf16, FP8 or 4-bit (svp_dtype).  Beside
- * the step: rows back out of a cache (kv_gather), and eviction by
+ * the step: rows back out of a cache (kv_gather), eviction by
  * accumulated attention weight (paged_score_update after each attention
- * call, kv_evict when a sequence has outgrown its budget).
+ * call, kv_evict when a sequence has outgrown its budget), attention over
+ * selected pages only (kv_page_bounds, paged_page_scores,
+ * paged_select_pages, paged_sparse_attention), pages for sequences that grow
+ * and shrink (kv_assign_pages, kv_append_slots) and the emitted tokens' log
+ * probabilities (token_logprobs).
  *
  * Conventions shared by every entry point
  *  - Every tensor argument is a caller-owned DEVICE pointer, row-major and
@@ -75,7 +79,8 @@ enum {
   SVP_DEV_BAD_BLOCK_ID = 1,  /* a visible page maps outside [0,num_blocks) */
   SVP_DEV_BAD_SEQ_LEN = 2,   /* seq_len < q_len or > max_blocks_per_seq*16 */
   SVP_DEV_BAD_TOKEN = 4,     /* a draft token outside [0, vocab)           */
-  SVP_DEV_TIMEOUT = 8        /* a bounded device-side wait gave up         */
+  SVP_DEV_TIMEOUT = 8,       /* a bounded device-side wait gave up         */
+  SVP_DEV_NO_PAGES = 16      /* kv_assign_pages: pages or slots ran out    */
 };
 
 /* Shapes shared by kv_append and paged_decode_attention.
@@ -368,6 +373,139 @@ int kv_evict(const svp_dims *dims, void *k_cache, void *v_cache, float *scores,
              int dst_max_blocks, int32_t *kept, int32_t *new_lens,
              cudaStream_t stream);
 
+/* ---- attention over selected pages -------------------------------------
+ * Over a long context a query's weight lies on few keys.  These calls let it
+ * read the pages that may hold them and no others: bounds of every page's
+ * keys (kept up to date with each append), a score from the bounds, the
+ * choice of the best pages, and attention over those. */
+
+/* Page bounds: for every page that holds one of the newest n_new positions of
+ * a sequence (n_new >= the longest length: every page), and every kv head,
+ *   bounds[page, g, 0, d] = min over the page's rows j < seq_lens[b] of K[j][d]
+ *   bounds[page, g, 1, d] = max ...
+ * bounds [num_blocks, num_kv_heads, 2, head_dim] bf16 (DEVICE, 16-byte
+ * aligned); K without dims->k_scale.  Values of a bf16, FP8 or FP4 cache are
+ * exact in bf16; an fp32 minimum is rounded down, a maximum up, so both stay
+ * bounds.  A NaN key makes its dimension's bounds NaN.  Other pages' bounds
+ * stay as they are.  A page that several sequences of a call hold is full in
+ * all of them, or in each to the same row.  After rows were taken back
+ * (rejected drafts) the bounds may be wider than the keys until the page is
+ * appended to again: still bounds.  A length outside [0,
+ * max_blocks_per_seq*16] updates nothing and sets SVP_DEV_BAD_SEQ_LEN, a bad
+ * block id sets SVP_DEV_BAD_BLOCK_ID.  One launch, no workspace.
+ * Errors as for kv_append (n_new >= 0, no upper limit); SVP_ERR_UNSUPPORTED
+ * where the touched pages of a sequence times heads reach 2^31. */
+int kv_page_bounds(const svp_dims *dims, const void *k_cache,
+                   const int32_t *block_table, const int32_t *seq_lens,
+                   int n_new, void *bounds, cudaStream_t stream);
+
+/* Page scores: for every page p of sequence b that holds positions,
+ *   scores[b, g, p] = max over the rows (i, h) of kv head g of
+ *       |scale| * sum_d max(q'_d, 0) * hi_d + min(q'_d, 0) * lo_d,
+ *       q' = q[b, i, h] (scale >= 0) or -q[b, i, h],
+ * which no product scale * <q, K_j> of a row with a key of the page exceeds
+ * (up to fp32 rounding); -inf for the entries past the sequence's pages.
+ * scores [batch, num_kv_heads, max_blocks_per_seq] fp32, every entry is
+ * written.  q [batch, q_len, num_q_heads, head_dim], fp32 where dims->dtype
+ * is SVP_F32, else bf16.  `scale` takes in the cache's k_scale (dims->k_scale
+ * is not used).  Products of 0 and an infinity are NaN, and a page with a NaN
+ * product scores NaN.  A length outside [0, max_blocks_per_seq*16] gives
+ * -inf and SVP_DEV_BAD_SEQ_LEN, a bad block id -inf and SVP_DEV_BAD_BLOCK_ID.
+ * One launch for each 128 query rows of a kv head (64 of fp32); no workspace,
+ * no atomics.
+ * Errors: those of paged_decode_attention; q and bounds are 16-byte aligned. */
+int paged_page_scores(const svp_dims *dims, const void *q, const void *bounds,
+                      const int32_t *block_table, const int32_t *seq_lens,
+                      int q_len, float scale, float *scores,
+                      cudaStream_t stream);
+
+/* Page selection: with n = ceil(seq_lens[b] / 16), pages[b, h] are the first
+ * n_sink of the pages 0 .. n-1, the newest n_recent and, of those between,
+ * the n_select - n_sink - n_recent with the largest scores (ties: the lower
+ * page; NaN ranks above everything), in increasing order, then -1.  A sequence
+ * of at most n_select pages keeps all of them.  scores [batch, heads,
+ * max_blocks] fp32, pages [batch, heads, n_select] int32; scores of forced
+ * pages and past n are not read.  A length outside [0, max_blocks*16] gives
+ * all -1 and SVP_DEV_BAD_SEQ_LEN.  One launch, no workspace; deterministic.
+ * Errors: SVP_ERR_INVALID_ARG for null or misaligned pointers, batch < 0,
+ * heads < 1, max_blocks < 0, n_select < 1, n_sink < 0, n_recent < 0 or
+ * n_sink + n_recent > n_select; SVP_ERR_UNSUPPORTED for batch > 65535 or
+ * max_blocks > 2^26. */
+int paged_select_pages(int batch, int heads, int max_blocks,
+                       const float *scores, const int32_t *seq_lens,
+                       int n_select, int n_sink, int n_recent, int32_t *pages,
+                       cudaStream_t stream);
+
+/* paged_decode_attention (tree_mask not NULL: paged_tree_attention) over the
+ * listed pages only: row (i, h) of sequence b attends to the keys it would
+ * see there (without sinks and window) that lie in a page of
+ * pages[b, h / group], [batch, num_kv_heads, n_select] int32 logical page
+ * numbers.  Negative entries are holes; the order does not matter; a page
+ * listed twice counts twice.  The last page is cut at seq_lens[b].  A row that
+ * sees no key (or whose every product is -inf) gets zeros and lse = -inf.
+ * Any cache type; a NaN or infinity in the V row of a position below
+ * seq_lens[b] may reach every row of the kv head, also those that do not see
+ * the position.
+ * An entry past the sequence's pages is skipped with SVP_DEV_BAD_BLOCK_ID, as
+ * is a bad block id; a length below q_len or above max_blocks_per_seq*16 sets
+ * SVP_DEV_BAD_SEQ_LEN and leaves the sequence's rows as they were.
+ * One launch, no workspace (dims->workspace is not used); dims->split_pages:
+ * fewest list entries of a CTA (0: automatic).
+ * Errors: those of paged_decode_attention, SVP_ERR_INVALID_ARG for
+ * n_select < 1, SVP_ERR_UNSUPPORTED for a kernel_path other than AUTO. */
+int paged_sparse_attention(const svp_dims *dims, const void *q,
+                           const void *k_cache, const void *v_cache,
+                           const int32_t *block_table, const int32_t *seq_lens,
+                           int q_len, const int32_t *pages, int n_select,
+                           const uint32_t *tree_mask, float scale, void *out,
+                           float *lse, cudaStream_t stream);
+
+/* ---- pages for growing and shrinking sequences -------------------------- */
+
+/* Page assignment: block_table [batch, max_blocks], seq_lens [batch] and the
+ * stack of free pages, free_pages [capacity] with *free_count entries (all
+ * DEVICE, updated in place), go from seq_lens to new_lens [batch].  In order:
+ *   1. every page past ceil(new_lens[b] / 16) goes back: for b, then the page,
+ *      in increasing order, the table's entry is pushed and becomes -1;
+ *   2. every missing page is taken: for b, then the page, in increasing
+ *      order, the stack's top is popped into the table;
+ *   3. seq_lens[b] = new_lens[b].
+ * Stack entries at and above the new count stay as the pushes left them.
+ * slots [n_slots] int64 (or NULL with n_slots 0): the slots of the new
+ * positions seq_lens[b] .. new_lens[b] - 1 of all sequences, packed in order,
+ * slot = page * 16 + position % 16; -1 past the last.  offsets [batch + 1]
+ * int32 (or NULL): where each sequence's begin (at most 2^31 - 1).
+ * Pages (or, with slots, entries of slots) may run out: from the first
+ * sequence whose new pages (new positions) no longer fit, no sequence that
+ * needs any is served: its table and length stay as they were, its slots are
+ * -1, and SVP_DEV_NO_PAGES is set.
+ * A length outside [0, max_blocks*16] (old or new) leaves the sequence as it
+ * is and sets SVP_DEV_BAD_SEQ_LEN.  A page id outside [0, num_blocks) is
+ * pushed or taken as it stands, gets slot -1 and sets SVP_DEV_BAD_BLOCK_ID.  A
+ * count outside [0, capacity], or pages coming back that would pass
+ * capacity, change nothing (slots -1, offsets 0) and set SVP_DEV_NO_PAGES.
+ * Pages are not counted by reference: a sequence that shares pages shrinks no
+ * further than to those.  One launch, no workspace; deterministic.
+ * new_lens may be seq_lens (nothing happens); the other arrays do not overlap.
+ * Errors: SVP_ERR_INVALID_ARG for null pointers (where the sizes ask for
+ * them), negative sizes, pointers off 4 bytes (slots: 8);
+ * SVP_ERR_UNSUPPORTED for batch > 65535. */
+int kv_assign_pages(int batch, int max_blocks, int num_blocks,
+                    int32_t *block_table, int32_t *seq_lens,
+                    const int32_t *new_lens, int32_t *free_pages,
+                    int32_t *free_count, int capacity, int64_t *slots,
+                    int n_slots, int32_t *offsets, cudaStream_t stream);
+
+/* kv_append of packed rows: row i of k_new / v_new [n_rows, num_kv_heads,
+ * head_dim] goes to slot slots[i] (int64, page * 16 + row), stored as
+ * kv_append stores it.  A negative slot stores nothing; one past the cache
+ * sets SVP_DEV_BAD_BLOCK_ID.  Slots of one call are distinct.  Of dims, batch
+ * and max_blocks_per_seq are not used.  Errors as for kv_append
+ * (n_rows >= 0, no upper limit; slots 8-byte aligned). */
+int kv_append_slots(const svp_dims *dims, const void *k_new, const void *v_new,
+                    void *k_cache, void *v_cache, const int64_t *slots,
+                    int n_rows, cudaStream_t stream);
+
 /* Speculative acceptance (pages: "How speculative decoding doubles LLM
  * speed", step 3 (sampling) and section "Absolute mathematical exactness";
  * "Speculative decoding: how AI models get faster without getting bigger").
@@ -474,6 +612,36 @@ int spec_accept_tree(int batch, int num_nodes, int vocab,
                      const float *uniforms, int32_t *out_tokens,
                      int32_t *out_nodes, int32_t *n_accepted,
                      cudaStream_t stream);
+
+/* Log probabilities of given tokens.  For row r of logits [rows, vocab]
+ * (SVP_F32 or SVP_BF16), with p = softmax(logits / temperature) over the
+ * tokens that `allowed` (NULL, or [rows, (vocab+31)/32] uint32 as in
+ * svp_accept_opts) lets take part:
+ *   logprobs[r]      ln p(tokens[r]); -inf for a token of probability 0 (not
+ *                    allowed, or a logit of -inf)
+ *   entropy[r]       -sum p ln p (or NULL)
+ *   ranks[r]         tokens ahead of tokens[r], by logit and, among equals, by
+ *                    index: 0 for the most likely one; -1 for a token of
+ *                    probability 0 (or NULL)
+ *   top_tokens, top_logprobs [rows, n_top]: the most likely tokens in that
+ *                    order and their ln p; -1 and -inf where fewer have any
+ * tokens [rows] int32: spec_accept's out_tokens with target_logits (rows =
+ * batch * (num_draft+1)), for instance.  A negative token is padding: the row
+ * is not read, its results are 0, 0, -1 and no alternatives; one >= vocab
+ * gives the same and sets SVP_DEV_BAD_TOKEN.  A row that allows nothing has
+ * logprob -inf and entropy 0.  A NaN or +inf among a row's allowed logits
+ * makes its log probabilities and entropy NaN; NaN ranks above +inf.
+ * Logits are read once; sums are fp32.  One launch, no workspace;
+ * deterministic.
+ * Errors: SVP_ERR_INVALID_ARG for null or misaligned pointers (logits to their
+ * elements), rows < 0, vocab < 2, n_top < 0, another dtype, temperature <= 0
+ * or not finite; SVP_ERR_UNSUPPORTED for vocab > 320000, n_top > 64 or
+ * rows > 2^27. */
+int token_logprobs(int rows, int vocab, int dtype, const void *logits,
+                   const int32_t *tokens, int n_top, float temperature,
+                   const uint32_t *allowed, float *logprobs, float *entropy,
+                   int32_t *ranks, float *top_logprobs, int32_t *top_tokens,
+                   cudaStream_t stream);
 
 /* ---- the graph-captured decode step ----------------------------------
  * (page: "How Moondream cut VLM inference latency by 35% via pipelined

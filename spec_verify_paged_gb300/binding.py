@@ -1,6 +1,7 @@
 """Thin binding of libsvp.so (include/svp.h), by ctypes and, for the calls on
-4-bit caches and the gather, score and eviction calls, by a small extension
-module (csrc/calls.cpp).
+4-bit caches, the gather, score and eviction calls, those on selected pages,
+page assignment and log probabilities, by a small extension module
+(csrc/calls.cpp).
 
 Argument marshalling only: shape/dtype/device checks, raw device pointers,
 the current CUDA stream, and a zero-filled workspace tensor kept per device.
@@ -27,10 +28,14 @@ SVP_OK, SVP_ERR_INVALID_ARG, SVP_ERR_UNSUPPORTED, SVP_ERR_CUDA, SVP_ERR_WORKSPAC
 SVP_F32, SVP_BF16, SVP_FP8_E4M3, SVP_FP4_E2M1 = 0, 1, 2, 3
 PATH_AUTO, PATH_CUDA_CORES, PATH_TENSOR_CORES, PATH_TCGEN05 = 0, 1, 2, 3
 DEV_BAD_BLOCK_ID, DEV_BAD_SEQ_LEN, DEV_BAD_TOKEN, DEV_TIMEOUT = 1, 2, 4, 8
+DEV_NO_PAGES = 16
 EXPORTED = ("paged_decode_attention", "paged_decode_attention_noalloc",
             "paged_tree_attention",
             "paged_decode_workspace_size",
             "kv_append", "kv_gather", "paged_score_update", "kv_evict",
+            "kv_page_bounds", "paged_page_scores", "paged_select_pages",
+            "paged_sparse_attention", "kv_assign_pages", "kv_append_slots",
+            "token_logprobs",
             "spec_accept", "spec_accept_ex", "spec_accept_tree",
             "svp_read_device_status",
             "svp_step_create", "svp_step_host_buffer", "svp_step_launch",
@@ -125,6 +130,20 @@ def load_library(path: str = LIB_PATH):
         lib.kv_evict.argtypes = [dims_p, vp, vp, vp, vp, vp, i32, i32, i32, vp,
                                  i32, vp, vp, vp]
         lib.kv_evict.restype = i32
+        lib.kv_page_bounds.argtypes = [dims_p, vp, vp, vp, i32, vp, vp]
+        lib.paged_page_scores.argtypes = [dims_p, vp, vp, vp, vp, i32, f32, vp, vp]
+        lib.paged_select_pages.argtypes = [i32, i32, i32, vp, vp, i32, i32, i32,
+                                           vp, vp]
+        lib.paged_sparse_attention.argtypes = [dims_p, vp, vp, vp, vp, vp, i32,
+                                               vp, i32, vp, f32, vp, vp, vp]
+        lib.kv_assign_pages.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp, i32,
+                                        vp, i32, vp, vp]
+        lib.kv_append_slots.argtypes = [dims_p, vp, vp, vp, vp, vp, i32, vp]
+        lib.token_logprobs.argtypes = [i32, i32, i32, vp, vp, i32, f32, vp, vp,
+                                       vp, vp, vp, vp, vp]
+        for name in EXPORTED[EXPORTED.index("kv_page_bounds"):
+                             EXPORTED.index("token_logprobs") + 1]:
+            getattr(lib, name).restype = i32
         lib.spec_accept.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp, vp, vp]
         lib.spec_accept.restype = i32
         lib.spec_accept_ex.argtypes = ([i32, i32, i32] + [vp] * 4 +
@@ -391,12 +410,25 @@ def _raw(stream):
     return None if stream is None else stream.cuda_stream
 
 
-def kv_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens,
-              stream=None, k_scale=1.0, v_scale=1.0):
+def kv_append(k_new, v_new, k_cache, v_cache, block_table=None, seq_lens=None,
+              stream=None, k_scale=1.0, v_scale=1.0, slots=None):
     """Scatter k_new/v_new [B, n_new, Hkv, D] into the paged caches in place
     (include/svp.h: kv_append).  seq_lens are the lengths after the append.
     Into FP8 and 4-bit caches the bf16 rows are quantised with k_scale /
-    v_scale."""
+    v_scale.
+
+    With slots (int64 [n_rows], as kv_assign_pages makes them, instead of
+    block_table and seq_lens) the rows are packed, [n_rows, Hkv, D], and row i
+    goes to slot slots[i]; a negative slot stores nothing (include/svp.h:
+    kv_append_slots)."""
+    if slots is not None:
+        _need(block_table is None and seq_lens is None,
+              "kv_append takes either slots or block_table and seq_lens")
+        st = (_calls or _load_calls()).append_slots(
+            k_new, v_new, k_cache, v_cache, slots, _raw(stream), k_scale, v_scale)
+        return None if st is None else _check("kv_append_slots", st)
+    _need(block_table is not None and seq_lens is not None,
+          "kv_append takes block_table and seq_lens, or slots")
     if _is_fp4(k_cache):
         st = (_calls or _load_calls()).append_fp4(
             k_new, v_new, k_cache, v_cache, block_table, seq_lens, _raw(stream),
@@ -479,6 +511,90 @@ def kv_evict(k_cache, v_cache, scores, block_table, seq_lens, budget, n_sink=0,
         k_cache, v_cache, scores, block_table, seq_lens, budget, n_sink,
         n_recent, dst_block_table, kept, new_lens, _raw(stream))
     return r if type(r) is tuple else _check("kv_evict", r)
+
+
+def kv_page_bounds(k_cache, block_table, seq_lens, bounds, n_new=None,
+                   stream=None):
+    """Elementwise smallest and largest K of every page that holds one of the
+    newest n_new positions of a sequence (default: of every page), per kv head,
+    into bounds [num_blocks, Hkv, 2, D] bf16, in place (include/svp.h:
+    kv_page_bounds).  Called after each append with its n_new, before
+    paged_page_scores.  Returns bounds."""
+    st = (_calls or _load_calls()).page_bounds(
+        k_cache, block_table, seq_lens, bounds, n_new, _raw(stream))
+    return bounds if st is None else _check("kv_page_bounds", st)
+
+
+def paged_page_scores(q, bounds, block_table, seq_lens, scale=None, k_scale=1.0,
+                      scores=None, stream=None):
+    """scores [B, Hkv, max_blocks] fp32: what scale * k_scale * <q, K> can be at
+    most for a key of the page, the largest over the kv head's query rows
+    (include/svp.h: paged_page_scores); -inf past a sequence's pages."""
+    r = (_calls or _load_calls()).page_scores(
+        q, bounds, block_table, seq_lens, scale, k_scale, scores, _raw(stream))
+    return r if type(r) is not int else _check("paged_page_scores", r)
+
+
+def paged_select_pages(scores, seq_lens, n_select, n_sink=0, n_recent=1,
+                       pages=None, stream=None):
+    """pages [B, Hkv, n_select] int32: per sequence and kv head the first n_sink
+    pages, the newest n_recent and the best-scored others, in increasing order,
+    -1 padded (include/svp.h: paged_select_pages).  For a query to see its own
+    key (and the drafts before it) n_recent covers the pages of the newest
+    q_len positions: (q_len + 30) // 16."""
+    r = (_calls or _load_calls()).select_pages(
+        scores, seq_lens, n_select, n_sink, n_recent, pages, _raw(stream))
+    return r if type(r) is not int else _check("paged_select_pages", r)
+
+
+def paged_sparse_attention(q, k_cache, v_cache, block_table, seq_lens, pages,
+                           tree_mask=None, scale=None, out=None, lse=None,
+                           split_pages=0, stream=None, k_scale=1.0, v_scale=1.0):
+    """out [B, q_len, Hq, D] and lse [B, q_len, Hq] of attention over the pages
+    listed in pages [B, Hkv, n_select] int32 only (include/svp.h:
+    paged_sparse_attention), causal within the newest q_len positions or, with
+    tree_mask, along the draft tree.  Negative entries are holes.  A row that
+    sees no listed key gets zeros and -inf."""
+    r = (_calls or _load_calls()).sparse_attention(
+        q, k_cache, v_cache, block_table, seq_lens, pages, tree_mask, scale, out,
+        lse, split_pages, _raw(stream), k_scale, v_scale)
+    return r if type(r) is tuple else _check("paged_sparse_attention", r)
+
+
+def kv_assign_pages(block_table, seq_lens, new_lens, free_pages, free_count,
+                    n_slots=None, slots=None, offsets=None, num_blocks=None,
+                    stream=None):
+    """Takes the sequences from seq_lens to new_lens (int32 [B]), in place:
+    pages past the new lengths go back onto the stack free_pages (int32
+    [capacity], free_count int32 [1] entries), missing ones are taken from it
+    (include/svp.h: kv_assign_pages).  Returns (slots, offsets): with n_slots
+    (or slots, int64 [n_slots]) the slots of the new positions, packed in the
+    order of the sequences and -1 padded, for kv_append(slots=...), else None;
+    offsets int32 [B + 1] say where each sequence's begin.  Ids outside
+    [0, num_blocks) get no slot.
+
+    Where pages or slots run out, the sequences from the first that does not
+    fit keep their length and table, and read_device_status() has
+    DEV_NO_PAGES."""
+    r = (_calls or _load_calls()).assign_pages(
+        block_table, seq_lens, new_lens, free_pages, free_count, n_slots, slots,
+        offsets, num_blocks, _raw(stream))
+    return r if type(r) is tuple else _check("kv_assign_pages", r)
+
+
+def token_logprobs(logits, tokens, n_top=0, temperature=1.0, allowed=None,
+                   logprobs=None, entropy=None, ranks=None, top_logprobs=None,
+                   top_tokens=None, stream=None):
+    """(logprobs, entropy, ranks, top_logprobs, top_tokens) of int32 tokens
+    [...] under softmax(logits / temperature), logits [..., V] fp32 or bf16,
+    over the tokens that the mask `allowed` (int32/uint32 [..., ceil(V/32)], as
+    spec_accept takes it) lets take part; top_* [..., n_top] are the most likely
+    tokens (include/svp.h: token_logprobs).  Negative tokens are padding, so
+    spec_accept's out_tokens go with its target_logits as they are."""
+    r = (_calls or _load_calls()).logprobs(
+        logits, tokens, n_top, temperature, allowed, logprobs, entropy, ranks,
+        top_logprobs, top_tokens, _raw(stream))
+    return r if type(r) is tuple else _check("token_logprobs", r)
 
 
 def spec_accept(target_logits, draft_logits, draft_tokens, uniforms,

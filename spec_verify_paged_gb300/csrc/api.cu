@@ -722,6 +722,299 @@ int spec_accept_tree(int batch, int num_nodes, int vocab,
   return SVP_OK;
 }
 
+int kv_append_slots(const svp_dims *dims, const void *k_new, const void *v_new,
+                    void *k_cache, void *v_cache, const int64_t *slots,
+                    int n_rows, cudaStream_t stream) {
+  t_last_launches = 0;
+  const int st = check_dims(dims);
+  if (st != SVP_OK) return st;
+  if (n_rows < 0) return SVP_ERR_INVALID_ARG;
+  if (n_rows == 0) return SVP_OK;
+  if (!k_new || !v_new || !k_cache || !v_cache || !slots)
+    return SVP_ERR_INVALID_ARG;
+  if (dims->num_blocks == 0) return SVP_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new) |
+       reinterpret_cast<uintptr_t>(k_cache) |
+       reinterpret_cast<uintptr_t>(v_cache)) % 16 != 0 ||
+      reinterpret_cast<uintptr_t>(slots) % 8 != 0)
+    return SVP_ERR_INVALID_ARG;
+  AppendSlotsParams p;
+  p.k_new = k_new;
+  p.v_new = v_new;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.slots = reinterpret_cast<const long long *>(slots);
+  p.n_rows = n_rows;
+  p.num_kv_heads = dims->num_kv_heads;
+  p.head_dim = dims->head_dim;
+  p.num_blocks = dims->num_blocks;
+  p.dtype = dims->dtype;
+  const bool scaled =
+      dims->dtype == SVP_FP8_E4M3 || dims->dtype == SVP_FP4_E2M1;
+  p.k_scale = scaled ? dims->k_scale : 1.0f;
+  p.v_scale = scaled ? dims->v_scale : 1.0f;
+  if (launch_append_slots(p, stream) != cudaSuccess) return SVP_ERR_CUDA;
+  t_last_launches = 1;
+  return SVP_OK;
+}
+
+int kv_assign_pages(int batch, int max_blocks, int num_blocks,
+                    int32_t *block_table, int32_t *seq_lens,
+                    const int32_t *new_lens, int32_t *free_pages,
+                    int32_t *free_count, int capacity, int64_t *slots,
+                    int n_slots, int32_t *offsets, cudaStream_t stream) {
+  t_last_launches = 0;
+  if (batch < 0 || max_blocks < 0 || num_blocks < 0 || capacity < 0 ||
+      n_slots < 0)
+    return SVP_ERR_INVALID_ARG;
+  if (batch > kMaxBatch) return SVP_ERR_UNSUPPORTED;
+  if (batch == 0 && n_slots == 0 && !offsets) return SVP_OK;
+  if ((batch > 0 && (!seq_lens || !new_lens)) || !free_count ||
+      (batch > 0 && max_blocks > 0 && !block_table) ||
+      (capacity > 0 && !free_pages) || (n_slots > 0 && !slots))
+    return SVP_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(block_table) |
+       reinterpret_cast<uintptr_t>(seq_lens) |
+       reinterpret_cast<uintptr_t>(new_lens) |
+       reinterpret_cast<uintptr_t>(free_pages) |
+       reinterpret_cast<uintptr_t>(free_count) |
+       reinterpret_cast<uintptr_t>(offsets)) % 4 != 0 ||
+      reinterpret_cast<uintptr_t>(slots) % 8 != 0)
+    return SVP_ERR_INVALID_ARG;
+  AssignParams p;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.new_lens = new_lens;
+  p.free_pages = free_pages;
+  p.free_count = free_count;
+  p.slots = reinterpret_cast<long long *>(slots);
+  p.offsets = offsets;
+  p.batch = batch;
+  p.max_blocks = max_blocks;
+  p.num_blocks = num_blocks;
+  p.capacity = capacity;
+  p.n_slots = n_slots;
+  if (launch_assign_pages(p, stream) != cudaSuccess) return SVP_ERR_CUDA;
+  t_last_launches = 1;
+  return SVP_OK;
+}
+
+int kv_page_bounds(const svp_dims *dims, const void *k_cache,
+                   const int32_t *block_table, const int32_t *seq_lens,
+                   int n_new, void *bounds, cudaStream_t stream) {
+  t_last_launches = 0;
+  const int st = check_dims(dims);
+  if (st != SVP_OK) return st;
+  if (n_new < 0) return SVP_ERR_INVALID_ARG;
+  if (dims->batch == 0 || n_new == 0 || dims->max_blocks_per_seq == 0)
+    return SVP_OK;
+  if (!k_cache || !block_table || !seq_lens || !bounds)
+    return SVP_ERR_INVALID_ARG;
+  if (dims->num_blocks == 0) return SVP_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(k_cache) |
+       reinterpret_cast<uintptr_t>(bounds)) % 16 != 0)
+    return SVP_ERR_INVALID_ARG;
+  BoundsParams p;
+  p.k_cache = k_cache;
+  p.bounds = bounds;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.batch = dims->batch;
+  p.num_kv_heads = dims->num_kv_heads;
+  p.head_dim = dims->head_dim;
+  p.n_new = n_new;
+  p.max_blocks = dims->max_blocks_per_seq;
+  p.num_blocks = dims->num_blocks;
+  // n_new positions that start anywhere in a page
+  p.max_pages = std::min(p.max_blocks, (n_new - 1) / kBlockSize + 2);
+  p.dtype = dims->dtype;
+  if ((long long)p.max_pages * p.num_kv_heads > (1LL << 31) - 64)
+    return SVP_ERR_UNSUPPORTED;
+  if (launch_page_bounds(p, stream) != cudaSuccess) return SVP_ERR_CUDA;
+  t_last_launches = 1;
+  return SVP_OK;
+}
+
+int paged_page_scores(const svp_dims *dims, const void *q, const void *bounds,
+                      const int32_t *block_table, const int32_t *seq_lens,
+                      int q_len, float scale, float *scores,
+                      cudaStream_t stream) {
+  t_last_launches = 0;
+  const int st = check_attention_args(dims, q_len, 0, 0, scale);
+  if (st != SVP_OK) return st;
+  if (dims->batch == 0 || dims->max_blocks_per_seq == 0) return SVP_OK;
+  if (!q || !bounds || !block_table || !seq_lens || !scores)
+    return SVP_ERR_INVALID_ARG;
+  if (dims->num_blocks == 0) return SVP_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(bounds)) %
+              16 != 0 ||
+      reinterpret_cast<uintptr_t>(scores) % 4 != 0)
+    return SVP_ERR_INVALID_ARG;
+  const int sms = device_sms();
+  if (sms <= 0) return SVP_ERR_CUDA;
+  PageScoreParams p = {};
+  p.q = q;
+  p.bounds = bounds;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.scores = scores;
+  p.batch = dims->batch;
+  p.num_q_heads = dims->num_q_heads;
+  p.num_kv_heads = dims->num_kv_heads;
+  p.head_dim = dims->head_dim;
+  p.group = dims->num_q_heads / dims->num_kv_heads;
+  p.q_len = q_len;
+  p.max_blocks = dims->max_blocks_per_seq;
+  p.num_blocks = dims->num_blocks;
+  p.f32 = dims->dtype == SVP_F32;
+  p.negate = scale < 0.f;
+  p.scale = std::fabs(scale);
+  const long long rows = (long long)p.group * q_len;
+  const int per = p.f32 ? kPageScoreRowsF32 : kPageScoreRows;
+  int launches = 0;
+  for (long long r0 = 0; r0 < rows; r0 += per, ++launches) {
+    p.row0 = (int)r0;
+    p.rows = (int)std::min<long long>(per, rows - r0);
+    p.more = r0 > 0;
+    if (launch_page_scores(p, sms, stream) != cudaSuccess) return SVP_ERR_CUDA;
+  }
+  t_last_launches = launches;
+  return SVP_OK;
+}
+
+int paged_select_pages(int batch, int heads, int max_blocks,
+                       const float *scores, const int32_t *seq_lens,
+                       int n_select, int n_sink, int n_recent, int32_t *pages,
+                       cudaStream_t stream) {
+  t_last_launches = 0;
+  if (batch < 0 || heads < 1 || max_blocks < 0 || n_select < 1 || n_sink < 0 ||
+      n_recent < 0 || (long long)n_sink + n_recent > n_select)
+    return SVP_ERR_INVALID_ARG;
+  if (batch > kMaxBatch || max_blocks > (1 << 26)) return SVP_ERR_UNSUPPORTED;
+  if (batch == 0) return SVP_OK;
+  if ((max_blocks > 0 && !scores) || !seq_lens || !pages)
+    return SVP_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(scores) |
+       reinterpret_cast<uintptr_t>(pages)) % 4 != 0)
+    return SVP_ERR_INVALID_ARG;
+  PickParams p;
+  p.scores = scores;
+  p.seq_lens = seq_lens;
+  p.pages = pages;
+  p.batch = batch;
+  p.heads = heads;
+  p.max_blocks = max_blocks;
+  p.n_select = n_select;
+  p.n_sink = n_sink;
+  p.n_recent = n_recent;
+  if (launch_pick_pages(p, stream) != cudaSuccess) return SVP_ERR_CUDA;
+  t_last_launches = 1;
+  return SVP_OK;
+}
+
+int paged_sparse_attention(const svp_dims *dims, const void *q,
+                           const void *k_cache, const void *v_cache,
+                           const int32_t *block_table, const int32_t *seq_lens,
+                           int q_len, const int32_t *pages, int n_select,
+                           const uint32_t *tree_mask, float scale, void *out,
+                           float *lse, cudaStream_t stream) {
+  t_last_launches = 0;
+  const int st = check_attention_args(dims, q_len, 0, 0, scale);
+  if (st != SVP_OK) return st;
+  if (n_select < 1) return SVP_ERR_INVALID_ARG;
+  if (dims->kernel_path != SVP_PATH_AUTO) return SVP_ERR_UNSUPPORTED;
+  if (dims->batch == 0) return SVP_OK;
+  if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !pages ||
+      !out || !lse)
+    return SVP_ERR_INVALID_ARG;
+  if (dims->num_blocks == 0 || dims->max_blocks_per_seq == 0)
+    return SVP_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_cache) |
+       reinterpret_cast<uintptr_t>(v_cache) | reinterpret_cast<uintptr_t>(out)) %
+              16 != 0 ||
+      (reinterpret_cast<uintptr_t>(pages) | reinterpret_cast<uintptr_t>(lse) |
+       reinterpret_cast<uintptr_t>(tree_mask)) % 4 != 0)
+    return SVP_ERR_INVALID_ARG;
+  const int sms = device_sms();
+  if (sms <= 0) return SVP_ERR_CUDA;
+  const bool scaled =
+      dims->dtype == SVP_FP8_E4M3 || dims->dtype == SVP_FP4_E2M1;
+  SparseParams p = {};
+  p.q = q;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.pages = pages;
+  p.tree_mask = tree_mask;
+  p.out = out;
+  p.lse = lse;
+  p.batch = dims->batch;
+  p.num_q_heads = dims->num_q_heads;
+  p.num_kv_heads = dims->num_kv_heads;
+  p.head_dim = dims->head_dim;
+  p.group = dims->num_q_heads / dims->num_kv_heads;
+  p.q_len = q_len;
+  p.n_select = n_select;
+  p.max_blocks = dims->max_blocks_per_seq;
+  p.num_blocks = dims->num_blocks;
+  p.rows = p.group * q_len;
+  p.split_pages = dims->split_pages;
+  p.qscale = scale * 1.4426950408889634f * (scaled ? dims->k_scale : 1.0f);
+  p.v_scale = scaled ? dims->v_scale : 1.0f;
+  if (launch_sparse_attention(p, dims->dtype, sms, stream) != cudaSuccess)
+    return SVP_ERR_CUDA;
+  t_last_launches = 1;
+  return SVP_OK;
+}
+
+int token_logprobs(int rows, int vocab, int dtype, const void *logits,
+                   const int32_t *tokens, int n_top, float temperature,
+                   const uint32_t *allowed, float *logprobs, float *entropy,
+                   int32_t *ranks, float *top_logprobs, int32_t *top_tokens,
+                   cudaStream_t stream) {
+  t_last_launches = 0;
+  if (rows < 0 || vocab < 2 || n_top < 0 ||
+      (dtype != SVP_F32 && dtype != SVP_BF16) ||
+      !(std::isfinite(temperature) && temperature > 0.f))
+    return SVP_ERR_INVALID_ARG;
+  if (vocab > kMaxVocab || n_top > kMaxTop || rows > (1 << 27))
+    return SVP_ERR_UNSUPPORTED;
+  if (rows == 0) return SVP_OK;
+  if (!logits || !tokens || !logprobs || (n_top > 0 && (!top_logprobs || !top_tokens)))
+    return SVP_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(logits) % (dtype == SVP_F32 ? 4 : 2) != 0 ||
+      (reinterpret_cast<uintptr_t>(tokens) | reinterpret_cast<uintptr_t>(allowed) |
+       reinterpret_cast<uintptr_t>(logprobs) | reinterpret_cast<uintptr_t>(entropy) |
+       reinterpret_cast<uintptr_t>(ranks) |
+       reinterpret_cast<uintptr_t>(top_logprobs) |
+       reinterpret_cast<uintptr_t>(top_tokens)) % 4 != 0)
+    return SVP_ERR_INVALID_ARG;
+  const int sms = device_sms();
+  if (sms <= 0) return SVP_ERR_CUDA;
+  LogprobParams p;
+  p.logits = logits;
+  p.tokens = tokens;
+  p.allowed = allowed;
+  p.logprobs = logprobs;
+  p.entropy = entropy;
+  p.ranks = ranks;
+  p.top_logprobs = top_logprobs;
+  p.top_tokens = top_tokens;
+  p.rows = rows;
+  p.vocab = vocab;
+  p.words = (vocab + 31) / 32;
+  p.n_top = n_top;
+  // kept finite at the smallest temperatures: the largest logit's own distance
+  // is 0 and stays so
+  p.inv_t = std::min(1.0f / temperature, 3e38f);
+  p.sc = std::min(1.4426950408889634f / temperature, 3e38f);
+  if (launch_token_logprobs(p, dtype, sms, stream) != cudaSuccess)
+    return SVP_ERR_CUDA;
+  t_last_launches = 1;
+  return SVP_OK;
+}
+
 int svp_read_device_status(cudaStream_t stream, int *flags) {
   unsigned f = 0;
   if (read_status_attention(stream, &f) != cudaSuccess) return SVP_ERR_CUDA;
@@ -733,6 +1026,10 @@ int svp_read_device_status(cudaStream_t stream, int *flags) {
   if (read_status_score(stream, &f) != cudaSuccess) return SVP_ERR_CUDA;
   if (read_status_evict(stream, &f) != cudaSuccess) return SVP_ERR_CUDA;
   if (read_status_accept(stream, &f) != cudaSuccess) return SVP_ERR_CUDA;
+  if (read_status_pages(stream, &f) != cudaSuccess) return SVP_ERR_CUDA;
+  if (read_status_sparse(stream, &f) != cudaSuccess) return SVP_ERR_CUDA;
+  if (read_status_assign(stream, &f) != cudaSuccess) return SVP_ERR_CUDA;
+  if (read_status_logprobs(stream, &f) != cudaSuccess) return SVP_ERR_CUDA;
   if (flags) *flags = (int)f;
   return SVP_OK;
 }

@@ -28,6 +28,26 @@ static __device__ unsigned int g_status_append;
 
 constexpr int kAppendWarps = 8;
 
+// 8 bf16 values -> E4M3 codes of x / s.
+__device__ __forceinline__ uint2 quant_fp8(uint4 w, float s) {
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  uint32_t out[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t packed = 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const uint32_t u = in[2 * h + t];
+      const float2 f = make_float2(__uint_as_float(u << 16) / s,
+                                   __uint_as_float(u & 0xffff0000u) / s);
+      packed |= (uint32_t)__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3)
+                << (16 * t);
+    }
+    out[h] = packed;
+  }
+  return make_uint2(out[0], out[1]);
+}
+
 __global__ void __launch_bounds__(32 * kAppendWarps)
     kv_append_kernel(const AppendParams p) {
   // the attention kernel that usually follows may set itself up meanwhile;
@@ -61,29 +81,10 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
           static_cast<const char *>(p.k_new) + src)[c];
       const uint4 vv = reinterpret_cast<const uint4 *>(
           static_cast<const char *>(p.v_new) + src)[c];
-      auto quant = [](uint4 w, float s) {
-        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-        uint32_t out[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t packed = 0;
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const uint32_t u = in[2 * h + t];
-            const float2 f = make_float2(__uint_as_float(u << 16) / s,
-                                         __uint_as_float(u & 0xffff0000u) / s);
-            packed |= (uint32_t)__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE,
-                                                         __NV_E4M3)
-                      << (16 * t);
-          }
-          out[h] = packed;
-        }
-        return make_uint2(out[0], out[1]);
-      };
       reinterpret_cast<uint2 *>(static_cast<char *>(p.k_cache) + dst)[c] =
-          quant(kv, p.k_scale);
+          quant_fp8(kv, p.k_scale);
       reinterpret_cast<uint2 *>(static_cast<char *>(p.v_cache) + dst)[c] =
-          quant(vv, p.v_scale);
+          quant_fp8(vv, p.v_scale);
     }
     return;
   }
@@ -112,38 +113,11 @@ __device__ __forceinline__ int page_of(const int32_t *table, int max_blocks,
   return -1;
 }
 
-// Rows into a 4-bit cache: one lane per block of 16 elements, the K and V
-// blocks of a row on neighbouring lanes; a sequence's rows along x, the
-// sequences along y.  Bound by one chain of loads -- row, length, page id,
-// then the stores -- and the launch.  64 rows of 64 sequences, 8 heads (22 MB):
-// 6.3 us as a graph node, 0.5 of the copy rate, 8.4 as a call; a decode step's
-// 32 rows of 32 heads: 2.0 and 4.1.
-template <int NB>  // blocks of a row
-__global__ void __launch_bounds__(32 * kAppendWarps)
-    kv_append_fp4_kernel(const AppendParams p) {
-  pdl_launch_dependents();
-  const int b = blockIdx.y;
-  const unsigned idx = blockIdx.x * (32 * kAppendWarps) + threadIdx.x;
-  const unsigned row = idx / (2 * NB), r = idx % (2 * NB);  // row: (k, g)
-  if (row >= (unsigned)(p.n_new * p.num_kv_heads)) return;
-  const bool is_v = r >= NB;
-  const int blk = is_v ? r - NB : r;
-  const int k = row / p.num_kv_heads, g = row % p.num_kv_heads;
-  // the new values do not depend on the table: load them first
-  const uint4 *src = reinterpret_cast<const uint4 *>(
-      static_cast<const uint16_t *>(is_v ? p.v_new : p.k_new) +
-      ((size_t)b * p.n_new * p.num_kv_heads + row) * (NB * kFp4Group) +
-      blk * kFp4Group);
-  const uint4 in[2] = {src[0], src[1]};
-  const int L = p.seq_lens[b];
-  if (L < p.n_new || L > (long long)p.max_blocks * kBlockSize) {
-    if (r == 0) atomicOr(&g_status_append, (unsigned)SVP_DEV_BAD_SEQ_LEN);
-    return;
-  }
-  const int pos = L - p.n_new + k;
-  const int phys = page_of(p.block_table, p.max_blocks, p.num_blocks, b, pos);
-  if (phys < 0) return;
-  const float factor = is_v ? p.v_scale : p.k_scale;
+// 16 bf16 values as a block of a 4-bit row: E2M1 codes and, returned, their
+// E4M3 scale.
+__device__ __forceinline__ __nv_fp8_storage_t quant_fp4(const uint4 (&in)[2],
+                                                        float factor,
+                                                        uint32_t (&code)[2]) {
   float x[kFp4Group], top = 0.f;
   const uint32_t w[8] = {in[0].x, in[0].y, in[0].z, in[0].w,
                          in[1].x, in[1].y, in[1].z, in[1].w};
@@ -172,7 +146,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
   // So do blocks whose largest value saturates the scale, and factors so far
   // from 1 that c might leave fp32's range.
   const float c = (1.f / factor) * (1.f / s);
-  uint32_t code[2] = {0u, 0u};
+  code[0] = code[1] = 0u;
   bool sure = c > 0x1p-100f && c < 0x1p100f && top <= 8.f * s;
   if (sure && (__float_as_uint(factor) & 0x7fffffu) == 0) {
 #pragma unroll
@@ -215,6 +189,43 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
                           __NV_E2M1, cudaRoundNearest)
                       << (8 * (i & 3));
   }
+  return sc;
+}
+
+// Rows into a 4-bit cache: one lane per block of 16 elements, the K and V
+// blocks of a row on neighbouring lanes; a sequence's rows along x, the
+// sequences along y.  Bound by one chain of loads -- row, length, page id,
+// then the stores -- and the launch.  64 rows of 64 sequences, 8 heads (22 MB):
+// 6.3 us as a graph node, 0.5 of the copy rate, 8.4 as a call; a decode step's
+// 32 rows of 32 heads: 2.0 and 4.1.
+template <int NB>  // blocks of a row
+__global__ void __launch_bounds__(32 * kAppendWarps)
+    kv_append_fp4_kernel(const AppendParams p) {
+  pdl_launch_dependents();
+  const int b = blockIdx.y;
+  const unsigned idx = blockIdx.x * (32 * kAppendWarps) + threadIdx.x;
+  const unsigned row = idx / (2 * NB), r = idx % (2 * NB);  // row: (k, g)
+  if (row >= (unsigned)(p.n_new * p.num_kv_heads)) return;
+  const bool is_v = r >= NB;
+  const int blk = is_v ? r - NB : r;
+  const int k = row / p.num_kv_heads, g = row % p.num_kv_heads;
+  // the new values do not depend on the table: load them first
+  const uint4 *src = reinterpret_cast<const uint4 *>(
+      static_cast<const uint16_t *>(is_v ? p.v_new : p.k_new) +
+      ((size_t)b * p.n_new * p.num_kv_heads + row) * (NB * kFp4Group) +
+      blk * kFp4Group);
+  const uint4 in[2] = {src[0], src[1]};
+  const int L = p.seq_lens[b];
+  if (L < p.n_new || L > (long long)p.max_blocks * kBlockSize) {
+    if (r == 0) atomicOr(&g_status_append, (unsigned)SVP_DEV_BAD_SEQ_LEN);
+    return;
+  }
+  const int pos = L - p.n_new + k;
+  const int phys = page_of(p.block_table, p.max_blocks, p.num_blocks, b, pos);
+  if (phys < 0) return;
+  const float factor = is_v ? p.v_scale : p.k_scale;
+  uint32_t code[2];
+  const __nv_fp8_storage_t sc = quant_fp4(in, factor, code);
   unsigned char *dst =
       static_cast<unsigned char *>(is_v ? p.v_cache : p.k_cache) +
       (((size_t)phys * p.num_kv_heads + g) * kBlockSize + pos % kBlockSize) *
@@ -223,6 +234,100 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
   d32[0] = code[0];  // rows are 4-byte aligned (36 or 72 bytes)
   d32[1] = code[1];
   dst[NB * 8 + blk] = sc;
+}
+
+// Packed rows to their slots.  A thread takes U items of K and the same of V,
+// 16 bytes of new values each (a block of 32 bytes for a 4-bit cache), all in
+// flight; a slot is looked up once for its item.  Bound by the rows' bytes.
+template <int DT, int D>
+__global__ void __launch_bounds__(256) kv_append_slots_kernel(const AppendSlotsParams p) {
+  constexpr bool FP4 = DT == SVP_FP4_E2M1;
+  constexpr int U = FP4 ? 1 : 2;
+  constexpr int PIECES = FP4 ? D / kFp4Group : DT == SVP_F32 ? D / 4 : D / 8;
+  constexpr int ROWB = DT == SVP_F32 ? 4 * D : DT == SVP_BF16 ? 2 * D
+                       : DT == SVP_FP8_E4M3 ? D : fp4_row_bytes(D);
+  pdl_wait();
+  pdl_launch_dependents();
+  // items: (token, head, piece); the block's first in 64 bits, the rest from it
+  const unsigned per = (unsigned)p.num_kv_heads * PIECES;
+  const unsigned long long first = (unsigned long long)blockIdx.x * (256 * U);
+  const unsigned long long token0 = first / per;
+  const unsigned rest = (unsigned)(first - token0 * per);
+  uint4 in[U][2][FP4 ? 2 : 1];
+  long long slot[U];
+  unsigned at[U];  // piece of the token
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const unsigned x = rest + u * 256 + threadIdx.x;
+    const unsigned long long token = token0 + x / per;
+    at[u] = x % per;
+    slot[u] = -1;
+    if (token >= (unsigned long long)p.n_rows) continue;
+    const size_t from = ((size_t)token * per + at[u]) * (FP4 ? 2 : 1);
+#pragma unroll
+    for (int side = 0; side < 2; ++side)
+#pragma unroll
+      for (int h = 0; h < (FP4 ? 2 : 1); ++h)
+        in[u][side][h] =
+            __ldg(static_cast<const uint4 *>(side ? p.v_new : p.k_new) + from + h);
+    slot[u] = __ldg(p.slots + token);
+    if (slot[u] >= (long long)p.num_blocks * kBlockSize) {
+      atomicOr(&g_status_append, (unsigned)SVP_DEV_BAD_BLOCK_ID);
+      slot[u] = -1;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (slot[u] < 0) continue;
+    const unsigned g = at[u] / PIECES, c = at[u] % PIECES;
+    const size_t to = (((size_t)(slot[u] / kBlockSize) * p.num_kv_heads + g) *
+                           kBlockSize + (size_t)(slot[u] % kBlockSize)) * ROWB;
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      unsigned char *const row =
+          static_cast<unsigned char *>(side ? p.v_cache : p.k_cache) + to;
+      const float factor = side ? p.v_scale : p.k_scale;
+      if constexpr (FP4) {
+        uint32_t code[2];
+        const __nv_fp8_storage_t sc = quant_fp4(in[u][side], factor, code);
+        uint32_t *const d32 = reinterpret_cast<uint32_t *>(row + 8 * c);
+        d32[0] = code[0];
+        d32[1] = code[1];
+        row[D / 2 + c] = sc;
+      } else if constexpr (DT == SVP_FP8_E4M3) {
+        reinterpret_cast<uint2 *>(row)[c] = quant_fp8(in[u][side][0], factor);
+      } else {
+        reinterpret_cast<uint4 *>(row)[c] = in[u][side][0];
+      }
+    }
+  }
+}
+
+template <int DT, int D>
+static cudaError_t slots_t(const AppendSlotsParams &p, cudaStream_t stream) {
+  constexpr int U = DT == SVP_FP4_E2M1 ? 1 : 2;
+  constexpr int PIECES = DT == SVP_FP4_E2M1 ? D / kFp4Group
+                         : DT == SVP_F32    ? D / 4 : D / 8;
+  const long long items = p.n_rows * p.num_kv_heads * PIECES;
+  const long long grid = (items + 256 * U - 1) / (256 * U);
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  return launch_pdl(kv_append_slots_kernel<DT, D>, (unsigned)grid, 256, 0, stream, p);
+}
+
+cudaError_t launch_append_slots(const AppendSlotsParams &p, cudaStream_t stream) {
+  const bool d64 = p.head_dim == 64;
+  switch (p.dtype) {
+    case SVP_F32:
+      return d64 ? slots_t<SVP_F32, 64>(p, stream) : slots_t<SVP_F32, 128>(p, stream);
+    case SVP_BF16:
+      return d64 ? slots_t<SVP_BF16, 64>(p, stream) : slots_t<SVP_BF16, 128>(p, stream);
+    case SVP_FP8_E4M3:
+      return d64 ? slots_t<SVP_FP8_E4M3, 64>(p, stream)
+                 : slots_t<SVP_FP8_E4M3, 128>(p, stream);
+    default:
+      return d64 ? slots_t<SVP_FP4_E2M1, 64>(p, stream)
+                 : slots_t<SVP_FP4_E2M1, 128>(p, stream);
+  }
 }
 
 // Rows back as values: a warp to a position (or to a share of its heads), so

@@ -1,0 +1,618 @@
+// page_select.cu -- which pages of a long context attention needs to read:
+// bounds of the keys of every page (kv_page_bounds), what a query's products
+// with a page's keys can be at most (paged_page_scores) and the choice of
+// pages by such a score (paged_select_pages).  include/svp.h has the calls.
+//
+// For a page with keys K_j and a query row q, every product is
+//   <q, K_j> = sum_d q_d K_j,d <= sum_d max(q_d, 0) hi_d + min(q_d, 0) lo_d
+// with lo and hi the elementwise smallest and largest key: 4 D bytes of
+// bounds (bf16) stand for 16 keys, an eighth of what bf16 keys take.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "attn_common.cuh"
+#include "fp4.cuh"
+
+namespace svp {
+
+static __device__ unsigned int g_status_pages;
+
+namespace {
+
+__device__ __forceinline__ void raise_pages(unsigned f) {
+  atomicOr(&g_status_pages, f);
+}
+
+// ---- bounds ----
+// A warp takes one head's page: a lane holds V consecutive elements (16 bytes
+// of a row; 8 bytes of codes of a 4-bit row), so one access of the warp covers
+// 32 V / D rows and all rows are in flight at once.  The lanes that hold the
+// same elements of other rows are then joined by shuffles.
+// Bound by the keys' bytes.
+constexpr int kBoundWarps = 8;
+
+template <int DT>
+struct BoundType;
+// packed pairs with their NaN-propagating extremes; ident: nothing seen yet
+struct PairBf16 {
+  static __device__ __forceinline__ uint32_t lo(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ uint32_t hi(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static constexpr uint32_t kPosInf = 0x7f807f80u, kNegInf = 0xff80ff80u;
+  // as a bf16 pair
+  static __device__ __forceinline__ uint32_t out(uint32_t a, bool) { return a; }
+};
+struct PairF16 {
+  static __device__ __forceinline__ uint32_t lo(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ uint32_t hi(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static constexpr uint32_t kPosInf = 0x7c007c00u, kNegInf = 0xfc00fc00u;
+  // codes and code * scale have at most 6 significant bits: exact in bf16
+  static __device__ __forceinline__ uint32_t out(uint32_t a, bool) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&a));
+    const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+};
+struct OneF32 {
+  static __device__ __forceinline__ uint32_t lo(uint32_t a, uint32_t b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;"
+        : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+    return __float_as_uint(r);
+  }
+  static __device__ __forceinline__ uint32_t hi(uint32_t a, uint32_t b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;"
+        : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+    return __float_as_uint(r);
+  }
+  static constexpr uint32_t kPosInf = 0x7f800000u, kNegInf = 0xff800000u;
+};
+template <> struct BoundType<SVP_BF16> { using P = PairBf16; };
+template <> struct BoundType<SVP_FP8_E4M3> { using P = PairF16; };
+template <> struct BoundType<SVP_FP4_E2M1> { using P = PairF16; };
+template <> struct BoundType<SVP_F32> { using P = OneF32; };
+
+// fp32 -> bf16 bits, away from zero where `out` says so (a lower bound is
+// rounded down, an upper bound up), NaN as the quiet NaN.
+__device__ __forceinline__ uint32_t bf16_outward(float x, bool up) {
+  const uint32_t u = __float_as_uint(x);
+  if (x != x) return 0x7fffu;
+  const bool away = (u & 0xffffu) != 0 && ((u >> 31) == 0) == up;
+  return (u >> 16) + (away ? 1u : 0u);
+}
+
+template <int DT, int D>
+__global__ void __launch_bounds__(32 * kBoundWarps)
+    page_bounds_kernel(const BoundsParams p) {
+  using P = typename BoundType<DT>::P;
+  constexpr int V = DT == SVP_F32 ? 4 : DT == SVP_BF16 ? 8 : 16;
+  constexpr int LPR = D / V;         // lanes of a row
+  constexpr int RPA = 32 / LPR;      // rows of an access
+  constexpr int NA = kBlockSize / RPA;  // accesses
+  constexpr int NR = DT == SVP_F32 ? 4 : V / 2;  // registers of V elements
+  constexpr int ROWB = DT == SVP_F32 ? 4 * D : DT == SVP_BF16 ? 2 * D
+                       : DT == SVP_FP8_E4M3 ? D : fp4_row_bytes(D);
+  pdl_wait();
+  pdl_launch_dependents();
+  const int b = blockIdx.y;
+  const int lane = threadIdx.x & 31;
+  const unsigned item = blockIdx.x * kBoundWarps + (threadIdx.x >> 5);
+  const unsigned i = item / (unsigned)p.num_kv_heads;
+  const int g = (int)(item - i * (unsigned)p.num_kv_heads);
+  const int L = p.seq_lens[b];
+  if (L < 0 || L > (long long)p.max_blocks * kBlockSize) {
+    if (threadIdx.x == 0) raise_pages(SVP_DEV_BAD_SEQ_LEN);
+    return;
+  }
+  const int first = max(L - p.n_new, 0) / kBlockSize;
+  const int page = first + (int)i;
+  if (i >= (unsigned)p.max_pages || (long long)page * kBlockSize >= L) return;
+  const int phys = p.block_table[(size_t)b * p.max_blocks + page];
+  if (phys < 0 || phys >= p.num_blocks) {
+    if (lane == 0) raise_pages(SVP_DEV_BAD_BLOCK_ID);
+    return;
+  }
+  const int rows = min(L - page * kBlockSize, kBlockSize);
+  const int r0 = lane / LPR, c = lane % LPR;
+  const unsigned char *src =
+      static_cast<const unsigned char *>(p.k_cache) +
+      ((size_t)phys * p.num_kv_heads + g) * (size_t)(kBlockSize * ROWB);
+  uint32_t lo[NR], hi[NR];
+#pragma unroll
+  for (int e = 0; e < NR; ++e) {
+    lo[e] = P::kPosInf;
+    hi[e] = P::kNegInf;
+  }
+  auto take = [&](const uint32_t (&w)[NR]) {
+#pragma unroll
+    for (int e = 0; e < NR; ++e) {
+      lo[e] = P::lo(lo[e], w[e]);
+      hi[e] = P::hi(hi[e], w[e]);
+    }
+  };
+  if constexpr (DT == SVP_FP4_E2M1) {
+    uint32_t w[NA][2], sc[NA];
+#pragma unroll
+    for (int a = 0; a < NA; ++a) {
+      const int r = min(a * RPA + r0, rows - 1);  // rows past the end: the last
+      const uint32_t *row = reinterpret_cast<const uint32_t *>(src + r * ROWB);
+      w[a][0] = __ldg(row + 2 * c);
+      w[a][1] = __ldg(row + 2 * c + 1);
+      sc[a] = __ldg(src + r * ROWB + D / 2 + c);
+    }
+#pragma unroll
+    for (int a = 0; a < NA; ++a) {
+      uint32_t v[NR], h[4];
+      const uint32_t s2 = e4m3x2_f16x2(sc[a] * 0x101u);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        e2m1x8_h2(w[a][x], h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * x + e] = hmul2(h[e], s2);
+      }
+      take(v);
+    }
+  } else {
+    uint4 w[NA];
+#pragma unroll
+    for (int a = 0; a < NA; ++a) {
+      const int r = min(a * RPA + r0, rows - 1);
+      w[a] = __ldg(reinterpret_cast<const uint4 *>(src + r * ROWB) + c);
+    }
+#pragma unroll
+    for (int a = 0; a < NA; ++a) {
+      const uint32_t x[4] = {w[a].x, w[a].y, w[a].z, w[a].w};
+      if constexpr (DT == SVP_FP8_E4M3) {
+        uint32_t v[NR];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[2 * e] = e4m3x2_f16x2(x[e]);
+          v[2 * e + 1] = e4m3x2_f16x2(x[e] >> 16);
+        }
+        take(v);
+      } else {
+        take(x);
+      }
+    }
+  }
+#pragma unroll
+  for (int off = LPR; off < 32; off <<= 1) {
+#pragma unroll
+    for (int e = 0; e < NR; ++e) {
+      lo[e] = P::lo(lo[e], __shfl_xor_sync(kFull, lo[e], off));
+      hi[e] = P::hi(hi[e], __shfl_xor_sync(kFull, hi[e], off));
+    }
+  }
+  if (r0 > 0) return;
+  unsigned char *dst = static_cast<unsigned char *>(p.bounds) +
+                       ((size_t)phys * p.num_kv_heads + g) * (4 * D) + c * (2 * V);
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    uint32_t o[V / 2];
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) {
+      if constexpr (DT == SVP_F32) {
+        const uint32_t *from = side ? hi : lo;
+        o[e] = bf16_outward(__uint_as_float(from[2 * e]), side) |
+               (bf16_outward(__uint_as_float(from[2 * e + 1]), side) << 16);
+      } else {
+        o[e] = P::out(side ? hi[e] : lo[e], side);
+      }
+    }
+    unsigned char *to = dst + side * (2 * D);
+    if constexpr (V == 4) {
+      *reinterpret_cast<uint2 *>(to) = make_uint2(o[0], o[1]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V / 2; e += 4)
+        reinterpret_cast<uint4 *>(to)[e / 4] =
+            make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+    }
+  }
+}
+
+// ---- scores ----
+// The bound is a matrix product: pages as M, query rows as N, and 2 D terms,
+// hi with the positive parts of q and lo with the negative ones.  mma.sync
+// m16n8k16 takes 16 pages; the order of the terms does not matter, so they
+// are dealt such that lane (g, t) reads 16 consecutive bytes of pages g and
+// g + 8 for two steps: the bounds go from memory to the matrix instruction
+// through registers only, the query rows' parts wait in shared memory.
+// bf16 products are exact in fp32, the sums are fp32; an fp32 q is taken as
+// three bf16 terms of 8 bits each.
+// Bound by the bounds' bytes.
+constexpr int kPScoreWarps = 4;
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1,
+                                         uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+template <int D, int S>  // S: bf16 terms of a q value
+__host__ __device__ constexpr int pscore_row() {
+  return 2 * S * 2 * D + 16;  // positive and negative parts; no bank conflicts
+}
+
+template <int D, int S>
+__global__ void __launch_bounds__(32 * kPScoreWarps)
+    page_scores_kernel(const PageScoreParams p) {
+  constexpr int NC = D / 32;  // 16-byte chunks of a lane on one side
+  constexpr int ROW = pscore_row<D, S>();
+  extern __shared__ __align__(16) unsigned char sq[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const unsigned unit = blockIdx.x / (unsigned)p.chunks;
+  const int chunk = (int)(blockIdx.x - unit * (unsigned)p.chunks);
+  const int b = (int)(unit / (unsigned)p.num_kv_heads);
+  const int head = (int)(unit - (unsigned)b * (unsigned)p.num_kv_heads);
+  pdl_wait();
+  pdl_launch_dependents();
+  const int L = p.seq_lens[b];
+  int n = (int)(((long long)L + kBlockSize - 1) / kBlockSize);
+  if (L < 0 || L > (long long)p.max_blocks * kBlockSize) {
+    if (threadIdx.x == 0 && chunk == 0) raise_pages(SVP_DEV_BAD_SEQ_LEN);
+    n = 0;
+  }
+  const int tiles = (p.max_blocks + 15) / 16;
+  const int first = chunk * p.tiles_per_cta;
+  const int last = min(first + p.tiles_per_cta, tiles);
+  float *const out = p.scores + (size_t)unit * p.max_blocks;
+  if (first * 16 < n) {
+    // the query rows' parts: row r of this launch is (position, head of the
+    // group) r0 + r
+    const int padded = (p.rows + 7) / 8 * 8;
+    for (int i = threadIdx.x; i < padded * (D / 2); i += 32 * kPScoreWarps) {
+      const int r = i / (D / 2), pair = i - r * (D / 2);
+      const int row = p.row0 + r;
+      uint32_t pos[S], neg[S];
+      float x[2] = {0.f, 0.f};
+      if (r < p.rows) {
+        const size_t at =
+            (((size_t)b * p.q_len + row / p.group) * p.num_q_heads +
+             (size_t)head * p.group + row % p.group) * D + 2 * pair;
+        if constexpr (S == 1) {
+          const uint32_t w = *reinterpret_cast<const uint32_t *>(
+              static_cast<const uint16_t *>(p.q) + at);
+          x[0] = __uint_as_float(w << 16);
+          x[1] = __uint_as_float(w & 0xffff0000u);
+        } else {
+          const float2 w = *reinterpret_cast<const float2 *>(
+              static_cast<const float *>(p.q) + at);
+          x[0] = w.x;
+          x[1] = w.y;
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < S; ++s) pos[s] = neg[s] = 0u;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float v = p.negate ? -x[e] : x[e];
+        const bool up = v > 0.f, nan = v != v;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          const __nv_bfloat16 h = __float2bfloat16_rn(v);
+          const uint32_t bits = (uint32_t)__bfloat16_as_ushort(h) << (16 * e);
+          if (up || nan) pos[s] |= bits;
+          if (!up) neg[s] |= bits;
+          // what is left; nothing of an infinity or a NaN
+          v = isfinite(__bfloat162float(h)) ? v - __bfloat162float(h) : 0.f;
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        // side 0 (negative parts, with lo), then side 1
+        *reinterpret_cast<uint32_t *>(sq + r * ROW + s * 2 * D + 4 * pair) = neg[s];
+        *reinterpret_cast<uint32_t *>(sq + r * ROW + (S + s) * 2 * D + 4 * pair) =
+            pos[s];
+      }
+    }
+    __syncthreads();
+  }
+  const int n_nt = (p.rows + 7) / 8;
+  const int32_t *const table = p.block_table + (size_t)b * p.max_blocks;
+  for (int tile = first + warp; tile < last; tile += kPScoreWarps) {
+    const int page0 = tile * 16;
+    if (page0 >= n) {  // nothing here: -inf, so that a score is always there
+      if (lane < 16 && page0 + lane < p.max_blocks && !p.more)
+        out[page0 + lane] = -INFINITY;
+      continue;
+    }
+    int id = -1;
+    if (lane < 16 && page0 + lane < n) {
+      id = table[page0 + lane];
+      if (id < 0 || id >= p.num_blocks) {
+        raise_pages(SVP_DEV_BAD_BLOCK_ID);
+        id = -1;
+      }
+    }
+    uint4 w[2][2][NC];  // [page g, g + 8][lo, hi]
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int page = __shfl_sync(kFull, id, g + 8 * h);
+      const uint4 *src = reinterpret_cast<const uint4 *>(
+          static_cast<const unsigned char *>(p.bounds) +
+          ((size_t)(page < 0 ? 0 : page) * p.num_kv_heads + head) * (4 * D));
+#pragma unroll
+      for (int side = 0; side < 2; ++side)
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          w[h][side][c] = page < 0 ? make_uint4(0, 0, 0, 0)
+                                   : __ldg(src + side * (D / 8) + 4 * c + t);
+    }
+    float best[2] = {-INFINITY, -INFINITY};
+    for (int nt = 0; nt < n_nt; ++nt) {
+      float acc[2][4] = {};
+      const unsigned char *qr = sq + (nt * 8 + g) * ROW + 16 * t;
+#pragma unroll
+      for (int side = 0; side < 2; ++side)
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(
+                qr + (side * S + s) * 2 * D + 64 * c);
+            const uint4 &a = w[0][side][c], &e = w[1][side][c];
+            mma_bf16(acc[0], a.x, e.x, a.y, e.y, q.x, q.y);
+            mma_bf16(acc[1], a.z, e.z, a.w, e.w, q.z, q.w);
+          }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (nt * 8 + 2 * t + (e & 1) < p.rows)
+          best[e >> 1] = max_nan(best[e >> 1], acc[0][e] + acc[1][e]);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      best[h] = max_nan(best[h], __shfl_xor_sync(kFull, best[h], 1));
+      best[h] = max_nan(best[h], __shfl_xor_sync(kFull, best[h], 2));
+      const int at = page0 + g + 8 * h;
+      const bool there = __shfl_sync(kFull, id, g + 8 * h) >= 0;
+      if (t == 0 && at < p.max_blocks) {
+        float v = there ? best[h] * p.scale : -INFINITY;
+        if (p.more && there) v = max_nan(v, out[at]);
+        out[at] = v;
+      }
+    }
+  }
+}
+
+// ---- selection ----
+// The k-th largest of a list's scores, found bit by bit: the largest key T
+// such that at least k keys are not below it, each bit one count over the
+// CTA's registers and one barrier.  Then the kept pages are numbered in order.
+// Bound by that chain of barriers; histograms of digits would be fewer
+// passes, but scores share their leading bits and so their bins.
+constexpr int kPickKeys = 16;  // keys of a thread held in registers
+constexpr int kPickMax = 1024;
+
+// Ascending unsigned order; NaN above everything, -0 as +0.  Never 0.
+__device__ __forceinline__ unsigned pick_key(float x) {
+  if (x != x) return 0xffffffffu;
+  const unsigned u = __float_as_uint(x + 0.f);
+  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+
+// Sum of v over the block, for every thread; buf: two rows of 32, used in turn.
+__device__ __forceinline__ unsigned block_sum(unsigned v, unsigned (*buf)[32],
+                                              int round) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  v = __reduce_add_sync(kFull, v);
+  unsigned *const row = buf[round & 1];
+  if (lane == 0) row[warp] = v;
+  __syncthreads();
+  const unsigned x = lane < (int)(blockDim.x >> 5) ? row[lane] : 0u;
+  return __reduce_add_sync(kFull, x);
+}
+
+template <bool REGS>
+__global__ void __launch_bounds__(kPickMax)
+    pick_pages_kernel(const PickParams p) {
+  __shared__ unsigned sums[2][32];
+  __shared__ unsigned cells[2][32];
+  const int tid = threadIdx.x, T = blockDim.x;
+  const int warp = tid >> 5, lane = tid & 31, n_warps = T >> 5;
+  const unsigned unit = blockIdx.x;
+  const int b = (int)(unit / (unsigned)p.heads);
+  pdl_wait();
+  pdl_launch_dependents();
+  int32_t *const pages = p.pages + (size_t)unit * p.n_select;
+  const int L = p.seq_lens[b];
+  int n = (int)(((long long)L + kBlockSize - 1) / kBlockSize);
+  if (L < 0 || n > p.max_blocks) {
+    if (tid == 0) raise_pages(SVP_DEV_BAD_SEQ_LEN);
+    n = 0;
+  }
+  if (n <= p.n_select) {
+    for (int i = tid; i < p.n_select; i += T) pages[i] = i < n ? i : -1;
+    return;
+  }
+  // candidates [c0, c1) compete for k places
+  const int c0 = p.n_sink, c1 = n - p.n_recent;
+  const unsigned k = (unsigned)(p.n_select - p.n_sink - p.n_recent);
+  const float *const scores = p.scores + (size_t)unit * p.max_blocks;
+  unsigned key[REGS ? kPickKeys : 1];
+  if constexpr (REGS) {
+#pragma unroll
+    for (int i = 0; i < kPickKeys; ++i) {
+      const int j = i * T + tid;
+      key[i] = j >= c0 && j < c1 ? pick_key(scores[j]) : 0u;
+    }
+  }
+  // keys not below `at` (at > 0)
+  auto count = [&](unsigned at) {
+    unsigned c = 0;
+    if constexpr (REGS) {
+#pragma unroll
+      for (int i = 0; i < kPickKeys; ++i) c += key[i] >= at ? 1u : 0u;
+    } else {
+      for (int j = c0 + tid; j < c1; j += T) c += pick_key(scores[j]) >= at ? 1u : 0u;
+    }
+    return c;
+  };
+  unsigned edge = 0xffffffffu, ties = 0;  // k == 0: nothing is kept by score
+  bool any = k > 0;
+  if (any) {
+    edge = 0;
+    for (int bit = 31; bit >= 0; --bit) {
+      const unsigned at = edge | (1u << bit);
+      if (block_sum(count(at), sums, bit) >= k) edge = at;
+    }
+    // kept: all above the edge, and the first `ties` of those at it
+    const unsigned above =
+        edge == 0xffffffffu ? 0u : block_sum(count(edge + 1), sums, 1);
+    ties = k - above;
+  }
+  // number the kept pages, T positions at a time, warp after warp
+  unsigned n_sure = 0, n_tied = 0;
+  const unsigned lower = (1u << lane) - 1u;
+  for (int i = 0, j0 = 0; j0 < n; ++i, j0 += T) {
+    const int j = j0 + tid;
+    const bool forced = j < c0 || (j >= c1 && j < n);
+    unsigned x = 0;
+    if (any && j >= c0 && j < c1) {
+      if constexpr (REGS) {
+#pragma unroll
+        for (int u = 0; u < kPickKeys; ++u)
+          if (u == i) x = key[u];
+      } else {
+        x = pick_key(scores[j]);
+      }
+    }
+    const bool sure = forced || x > edge, tied = x != 0 && x == edge;
+    const unsigned s = __ballot_sync(kFull, sure), e = __ballot_sync(kFull, tied);
+    unsigned *const row = cells[i & 1];
+    if (lane == 0) row[warp] = (__popc(s) << 16) | __popc(e);
+    __syncthreads();
+    const unsigned mine = lane < n_warps ? row[lane] : 0u;
+    unsigned before = lane < warp ? mine : 0u;
+    before = __reduce_add_sync(kFull, before);
+    const unsigned all = __reduce_add_sync(kFull, mine);
+    const unsigned t0 = n_tied + (before & 0xffffu) + __popc(e & lower);
+    const unsigned s0 = n_sure + (before >> 16) + __popc(s & lower);
+    if (sure || (tied && t0 < ties)) pages[s0 + min(t0, ties)] = j;
+    n_sure += all >> 16;
+    n_tied += all & 0xffffu;
+  }
+}
+
+template <int DT>
+cudaError_t bounds_t(const BoundsParams &p, dim3 grid, cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(32 * kBoundWarps);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return p.head_dim == 64 ? cudaLaunchKernelEx(&cfg, page_bounds_kernel<DT, 64>, p)
+                          : cudaLaunchKernelEx(&cfg, page_bounds_kernel<DT, 128>, p);
+}
+
+template <int D, int S>
+cudaError_t scores_t(const PageScoreParams &p, unsigned grid, cudaStream_t stream) {
+  constexpr int kRows = S == 1 ? kPageScoreRows : kPageScoreRowsF32;
+  static_assert(kRows * pscore_row<D, S>() <= 227 * 1024, "shared memory");
+  const size_t smem = (size_t)((p.rows + 7) / 8 * 8) * pscore_row<D, S>();
+  if (smem > 48 * 1024) {
+    // always the most that any launch takes: launches in other host threads
+    // may need more than this one
+    const cudaError_t e = cudaFuncSetAttribute(
+        page_scores_kernel<D, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        kRows * pscore_row<D, S>());
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(page_scores_kernel<D, S>, grid, 32 * kPScoreWarps, smem, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_page_bounds(const BoundsParams &p, cudaStream_t stream) {
+  const long long items = (long long)p.max_pages * p.num_kv_heads;
+  const long long blocks = (items + kBoundWarps - 1) / kBoundWarps;
+  if (blocks > 0x7fffffffLL / kBoundWarps) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)blocks, (unsigned)p.batch);
+  switch (p.dtype) {
+    case SVP_F32: return bounds_t<SVP_F32>(p, grid, stream);
+    case SVP_BF16: return bounds_t<SVP_BF16>(p, grid, stream);
+    case SVP_FP8_E4M3: return bounds_t<SVP_FP8_E4M3>(p, grid, stream);
+    default: return bounds_t<SVP_FP4_E2M1>(p, grid, stream);
+  }
+}
+
+cudaError_t launch_page_scores(PageScoreParams p, int sms, cudaStream_t stream) {
+  const long long tiles = ((long long)p.max_blocks + 15) / 16;
+  const long long units = (long long)p.batch * p.num_kv_heads;
+  // a warp's tiles one after another, so that the query rows are laid out
+  // once for several: but at least eight CTAs to an SM while there are tiles
+  long long per = tiles * units / ((long long)sms * 8 * kPScoreWarps);
+  per = per < 1 ? 1 : per > 8 ? 8 : per;
+  per *= kPScoreWarps;
+  const long long chunks = (tiles + per - 1) / per;
+  if (chunks * units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  p.tiles_per_cta = (int)per;
+  p.chunks = (int)chunks;
+  const unsigned grid = (unsigned)(chunks * units);
+  if (p.f32)
+    return p.head_dim == 64 ? scores_t<64, 3>(p, grid, stream)
+                            : scores_t<128, 3>(p, grid, stream);
+  return p.head_dim == 64 ? scores_t<64, 1>(p, grid, stream)
+                          : scores_t<128, 1>(p, grid, stream);
+}
+
+cudaError_t launch_pick_pages(const PickParams &p, cudaStream_t stream) {
+  const long long units = (long long)p.batch * p.heads;
+  if (units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  // enough threads for the longest list's keys, at least a warp per 4 keys
+  int threads = 128;
+  while (threads < kPickMax && threads * 8 < p.max_blocks) threads *= 2;
+  if (p.max_blocks <= kPickMax * kPickKeys && p.max_blocks <= threads * kPickKeys)
+    return launch_pdl(pick_pages_kernel<true>, (unsigned)units, threads, 0, stream, p);
+  return launch_pdl(pick_pages_kernel<false>, (unsigned)units, threads, 0, stream, p);
+}
+
+cudaError_t read_status_pages(cudaStream_t s, unsigned *flags) {
+  unsigned v = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_status_pages, sizeof v, 0,
+                                            cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return e;
+  const unsigned zero = 0;
+  e = cudaMemcpyToSymbolAsync(g_status_pages, &zero, sizeof zero, 0,
+                              cudaMemcpyHostToDevice, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  *flags |= v;
+  return e;
+}
+
+}  // namespace svp

@@ -209,6 +209,112 @@ constexpr int kScoreRows = 128;  // query rows of one launch
 cudaError_t launch_score_update(const ScoreParams &p, int sms,
                                 cudaStream_t stream);
 
+// kv_append of packed rows: row i of k_new / v_new [n_rows, Hkv, D] to slot
+// slots[i] (page * 16 + row; negative: nowhere).
+struct AppendSlotsParams {
+  const void *k_new;
+  const void *v_new;
+  void *k_cache;
+  void *v_cache;
+  const long long *slots;
+  long long n_rows;
+  int num_kv_heads, head_dim, num_blocks;
+  int dtype;                 // svp_dtype of the caches
+  float k_scale, v_scale;
+};
+cudaError_t launch_append_slots(const AppendSlotsParams &p, cudaStream_t stream);
+
+// Page bounds, scores and selection (page_select.cu).
+struct BoundsParams {
+  const void *k_cache;
+  void *bounds;               // bf16 [num_blocks, Hkv, 2, D]
+  const int32_t *block_table;
+  const int32_t *seq_lens;
+  int batch, num_kv_heads, head_dim, n_new, max_blocks, num_blocks;
+  int max_pages;              // bound of the pages that n_new positions touch
+  int dtype;
+};
+cudaError_t launch_page_bounds(const BoundsParams &p, cudaStream_t stream);
+
+struct PageScoreParams {
+  const void *q;
+  const void *bounds;
+  const int32_t *block_table;
+  const int32_t *seq_lens;
+  float *scores;              // [batch, Hkv, max_blocks]
+  int batch, num_q_heads, num_kv_heads, head_dim, group, q_len;
+  int max_blocks, num_blocks;
+  int row0, rows;             // query rows of this launch
+  int more;                   // not the first launch: add to what is there
+  int f32;                    // q is fp32
+  int negate;                 // the scale is negative
+  float scale;                // its magnitude
+  int tiles_per_cta, chunks;  // set by the launcher
+};
+constexpr int kPageScoreRows = 128;  // query rows of one launch
+constexpr int kPageScoreRowsF32 = 64;
+cudaError_t launch_page_scores(PageScoreParams p, int sms, cudaStream_t stream);
+
+struct PickParams {
+  const float *scores;        // [batch, heads, max_blocks]
+  const int32_t *seq_lens;
+  int32_t *pages;             // [batch, heads, n_select]
+  int batch, heads, max_blocks, n_select, n_sink, n_recent;
+};
+cudaError_t launch_pick_pages(const PickParams &p, cudaStream_t stream);
+
+// One paged_sparse_attention call (attention_sparse.cu).
+struct SparseParams {
+  const void *q;
+  const void *k_cache;
+  const void *v_cache;
+  const int32_t *block_table;
+  const int32_t *seq_lens;
+  const int32_t *pages;       // [batch, Hkv, n_select]
+  const uint32_t *tree_mask;  // [batch, q_len] ancestor bits, or null
+  void *out;
+  float *lse;
+  int batch, num_q_heads, num_kv_heads, head_dim, group, q_len;
+  int n_select, max_blocks, num_blocks;
+  int rows;                   // group * q_len
+  int n_rb;                   // set by the launcher: units of these rows
+  int split_pages;            // fewest list entries of a CTA, 0 = automatic
+  float qscale;               // scale * log2(e) (* k_scale)
+  float v_scale;
+};
+cudaError_t launch_sparse_attention(const SparseParams &p, int dtype, int sms,
+                                    cudaStream_t stream);
+
+struct AssignParams {
+  int32_t *block_table;
+  int32_t *seq_lens;
+  const int32_t *new_lens;
+  int32_t *free_pages;        // [capacity] stack
+  int32_t *free_count;
+  long long *slots;           // [n_slots] or null
+  int32_t *offsets;           // [batch + 1] or null
+  int batch, max_blocks, num_blocks, capacity, n_slots;
+};
+cudaError_t launch_assign_pages(const AssignParams &p, cudaStream_t stream);
+
+struct LogprobParams {
+  const void *logits;         // [rows, vocab]
+  const int32_t *tokens;
+  const uint32_t *allowed;    // [rows, words] or null
+  float *logprobs;
+  float *entropy;             // or null
+  int32_t *ranks;             // or null
+  float *top_logprobs;        // [rows, n_top]
+  int32_t *top_tokens;
+  int rows, vocab, words, n_top;
+  float inv_t;                // 1 / temperature
+  float sc;                   // log2(e) / temperature
+};
+constexpr int kMaxTop = 64;
+constexpr int kMaxVocab = 320000;
+cudaError_t launch_token_logprobs(const LogprobParams &p, int dtype, int sms,
+                                  cudaStream_t stream);
+
 struct EvictParams {
   void *k_cache;
   void *v_cache;
@@ -262,6 +368,10 @@ cudaError_t read_status_append(cudaStream_t s, unsigned *flags);
 cudaError_t read_status_score(cudaStream_t s, unsigned *flags);
 cudaError_t read_status_evict(cudaStream_t s, unsigned *flags);
 cudaError_t read_status_accept(cudaStream_t s, unsigned *flags);
+cudaError_t read_status_pages(cudaStream_t s, unsigned *flags);
+cudaError_t read_status_sparse(cudaStream_t s, unsigned *flags);
+cudaError_t read_status_assign(cudaStream_t s, unsigned *flags);
+cudaError_t read_status_logprobs(cudaStream_t s, unsigned *flags);
 
 #ifdef __CUDACC__
 // A launch that may start while the previous kernel on the stream is still
