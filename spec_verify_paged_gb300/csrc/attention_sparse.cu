@@ -16,7 +16,7 @@
 //
 //  * bf16: S = Q K^T and O = P V by mma.sync m16n8k16 with the query rows as
 //    M: S's accumulators are, packed, the A operand of P V.  P is bf16: a
-//    weight is off by half a bf16 step, 2^-9, as the output is; row sums are
+//    weight is off by half a bf16 step, 2^-8, as the output is; row sums are
 //    fp32 and of the weights before that rounding.
 //  * FP8 and 4-bit rows become fp16 operands between shared memory and the
 //    matrix instruction (exact); P is fp16 at 2^6 times its weight, which
