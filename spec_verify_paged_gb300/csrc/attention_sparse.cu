@@ -47,6 +47,7 @@ constexpr int kSpWarps = 4;
 constexpr int kSpThreads = 32 * kSpWarps;
 constexpr int kTilePages = 4;
 constexpr int kListCap = 512;      // list entries a CTA looks up at once
+constexpr int kNoPage = 0x7ffffff0; // first position of a page that is not there
 constexpr float kSpNoRef = -3e38f; // below any score
 
 __device__ __forceinline__ void raise_sparse(unsigned f) {
@@ -84,41 +85,40 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// Shared-memory reads by 32-bit address.  volatile keeps them behind the
+// barriers, and nothing else in order.
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(a)
-               : "memory");
+               : "r"(a));
 }
 __device__ __forceinline__ void ldsm4_t(uint32_t a, uint32_t (&r)[4]) {
   asm volatile(
       "ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-      : "r"(a)
-      : "memory");
+      : "r"(a));
 }
 __device__ __forceinline__ uint4 ls128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a)
-               : "memory");
+               : "r"(a));
   return v;
 }
 __device__ __forceinline__ uint2 ls64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
-               : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+               : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
 __device__ __forceinline__ uint32_t ls32(uint32_t a) {
   uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
 __device__ __forceinline__ uint32_t ls8(uint32_t a) {
   uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
 __device__ __forceinline__ float4 as_f4(uint4 v) {
@@ -175,7 +175,7 @@ __device__ __forceinline__ void load_tile(const SparseParams &p, uint32_t stage,
     if (ALL % kSpThreads != 0 && x >= ALL) break;
     const int page = x / (2 * PIECES), side = x / PIECES % 2, y = x % PIECES;
     const int at = tile * kTilePages + page;
-    const int2 e = at < count ? list[at] : make_int2(0, 0x7ffffff0);
+    const int2 e = at < count ? list[at] : make_int2(0, kNoPage);
     const char *src = static_cast<const char *>(side ? p.v_cache : p.k_cache) +
                       ((size_t)e.x * p.num_kv_heads + head) * S::PAGE + y * 16;
     uint32_t dst = stage + (page * 2 + side) * S::PAGE;
@@ -297,12 +297,15 @@ struct WarpMma {
     return DT == SVP_FP4_E2M1 ? fp4_key(n, j) : 8 * j + n;
   }
 
-  __device__ __forceinline__ void page(const SparseParams &, uint32_t kp,
-                                       uint32_t vp, int j0, unsigned char *,
-                                       int lane) {
+  // S of a page: lane (g, t) gets rows g and g + 8, columns 2 t and 2 t + 1 of
+  // two tiles of eight keys.
+  __device__ __forceinline__ void scores(uint32_t kp, float (&s)[2][4], int lane) {
     const int g = lane >> 2, t = lane & 3;
     constexpr int ROWB = SpShape<DT, D>::ROWB;
-    float s[2][4] = {};
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
     if constexpr (DT == SVP_BF16) {
       const int r = (lane >> 4) * 8 + (lane & 7), c = (lane >> 3) & 1;
 #pragma unroll
@@ -355,51 +358,13 @@ struct WarpMma {
         }
       }
     }
-    // scores in the log2 domain, masked; value e of tile j: row g + 8 (e / 2),
-    // column 2 t + e % 2
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[j][e] *= factor[e >> 1];
-    if (j0 + kBlockSize - 1 > t_all) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (!mask[e >> 1].sees(j0 + key(j, 2 * t + (e & 1)))) s[j][e] = -INFINITY;
-    }
-    float top[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      top[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]),
-                     fmaxf(s[1][2 * h], s[1][2 * h + 1]));
-    if (__any_sync(kFull, top[0] > ref[0] + (kSlack - kOff) ||
-                              top[1] > ref[1] + (kSlack - kOff))) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 1));
-        top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 2));
-        if (top[h] > ref[h]) {
-          const float f = ex2(ref[h] - top[h]);
-          ref[h] = top[h];
-          sum[h] *= f;
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            o[n][2 * h] *= f;
-            o[n][2 * h + 1] *= f;
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[j][e] = ex2(s[j][e] - ref[e >> 1] + kOff);
-        sum[e >> 1] += s[j][e];
-      }
-    const uint32_t pa[4] = {pack2<DT>(s[0][0], s[0][1]), pack2<DT>(s[0][2], s[0][3]),
-                            pack2<DT>(s[1][0], s[1][1]), pack2<DT>(s[1][2], s[1][3])};
+  }
+
+  // O += P V of a page.
+  __device__ __forceinline__ void values(uint32_t vp, const uint32_t (&pa)[4],
+                                         int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    constexpr int ROWB = SpShape<DT, D>::ROWB;
     if constexpr (DT == SVP_BF16) {
       const int r = ((lane >> 3) & 1) * 8 + (lane & 7), c = lane >> 4;
 #pragma unroll
@@ -458,6 +423,74 @@ struct WarpMma {
           mma16<DT>(o[8 * x + 2 * i + 1], pa, hmul2(d01[i], s01), hmul2(d23[i], s23));
         }
       }
+    }
+  }
+
+  // NP pages at `stage` (K, V, K, V, ..), their first positions j0; the products
+  // of several pages are independent chains, and one vote serves them all.  A
+  // page at kNoPage has no visible key.
+  template <int NP>
+  __device__ __forceinline__ void pages(const SparseParams &, uint32_t stage,
+                                        const int (&j0)[NP], unsigned char *,
+                                        int lane) {
+    const int t = lane & 3;
+    constexpr int PAGE = SpShape<DT, D>::PAGE;
+    float s[NP][2][4];
+#pragma unroll
+    for (int n = 0; n < NP; ++n) scores(stage + 2 * n * PAGE, s[n], lane);
+    // in the log2 domain, masked; value e of tile j: row g + 8 (e / 2), column
+    // 2 t + e % 2
+    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][j][e] *= factor[e >> 1];
+      if (j0[n] + kBlockSize - 1 > t_all) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!mask[e >> 1].sees(j0[n] + key(j, 2 * t + (e & 1))))
+              s[n][j][e] = -INFINITY;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        top[h] = fmaxf(top[h], fmaxf(fmaxf(s[n][0][2 * h], s[n][0][2 * h + 1]),
+                                     fmaxf(s[n][1][2 * h], s[n][1][2 * h + 1])));
+    }
+    if (__any_sync(kFull, top[0] > ref[0] + (kSlack - kOff) ||
+                              top[1] > ref[1] + (kSlack - kOff))) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 1));
+        top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 2));
+        if (top[h] > ref[h]) {
+          const float f = ex2(ref[h] - top[h]);
+          ref[h] = top[h];
+          sum[h] *= f;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            o[n][2 * h] *= f;
+            o[n][2 * h + 1] *= f;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[n][j][e] = ex2(s[n][j][e] - ref[e >> 1] + kOff);
+          sum[e >> 1] += s[n][j][e];
+        }
+      const uint32_t pa[4] = {
+          pack2<DT>(s[n][0][0], s[n][0][1]), pack2<DT>(s[n][0][2], s[n][0][3]),
+          pack2<DT>(s[n][1][0], s[n][1][1]), pack2<DT>(s[n][1][2], s[n][1][3])};
+      values(stage + (2 * n + 1) * PAGE, pa, lane);
     }
   }
 
@@ -529,6 +562,17 @@ struct WarpF32 {
     __syncwarp();
     const int base = L - p.q_len;
     t_all = p.tree_mask ? base - 1 : base + min(row0, p.rows - 1) / p.group;
+  }
+
+  template <int NP>
+  __device__ __forceinline__ void pages(const SparseParams &p, uint32_t stage,
+                                        const int (&first)[NP], unsigned char *own,
+                                        int lane) {
+    constexpr int PAGE = SpShape<SVP_F32, D>::PAGE;
+#pragma unroll 1
+    for (int n = 0; n < NP; ++n)
+      if (first[n] < kNoPage)
+        page(p, stage + 2 * n * PAGE, stage + (2 * n + 1) * PAGE, first[n], own, lane);
   }
 
   __device__ __forceinline__ void page(const SparseParams &p, uint32_t kp,
@@ -734,12 +778,16 @@ __global__ void __launch_bounds__(kSpThreads)
                          head, L);
       cp_commit();
       const uint32_t stage = ring + tile % S::STAGES * S::STAGE;
+      // a warp's pages of the tile lie side by side
+      constexpr int MINE = kTilePages / KG, NP = MINE < 2 ? MINE : 2;
 #pragma unroll 1
-      for (int x = kg; x < kTilePages; x += KG) {
+      for (int x = kg * MINE; x < (kg + 1) * MINE; x += NP) {
         const int e = tile * kTilePages + x;
         if (e >= count || idle) break;
-        st.page(p, stage + (2 * x) * S::PAGE, stage + (2 * x + 1) * S::PAGE,
-                list[e].y, own, lane);
+        int j0[NP];
+#pragma unroll
+        for (int n = 0; n < NP; ++n) j0[n] = e + n < count ? list[e + n].y : kNoPage;
+        st.template pages<NP>(p, stage + 2 * x * S::PAGE, j0, own, lane);
       }
     }
     cp_wait<0>();

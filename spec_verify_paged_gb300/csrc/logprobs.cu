@@ -8,12 +8,19 @@
 // so one maximum and one pass of exponentials give everything but the order.
 //
 // A cluster of 1 to 8 CTAs takes a row; every thread keeps its part of the row
-// in registers, so the logits are read once.  The alternatives: the k-th
-// largest of the threads' own largest values bounds the k-th largest of all
-// from below, and few elements reach that bound; they are gathered and ranked
-// by counting.  Where many do (equal logits), the k-th largest is found bit by
-// bit instead.  Equal logits are ordered by token, so no result depends on
-// the order of atomics.
+// in registers (what is not allowed as -inf), so the logits are read once.
+// What bounds it for long rows is instructions: about nine an element with the
+// exponential, so what can be done on pairs of bf16 is (the maximum, the count
+// of the tokens ahead), and nothing is done for an element that one test of
+// its vector or thread can rule out.  Each CTA's sums are relative to its own
+// maximum; they meet in the first CTA's shared memory at the end, by one
+// cluster barrier.
+//
+// The alternatives: the k-th largest of the threads' own largest values bounds
+// the k-th largest of all from below, and few elements reach that bound; they
+// are gathered and ranked by counting.  Where many do (equal logits), the k-th
+// largest is found bit by bit instead.  Equal logits are ordered by token, so
+// no result depends on the order of atomics.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -30,24 +37,37 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kLpThreads = 512;
-constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpCluster = 8;
 constexpr int kLpFound = 512;  // candidates ranked by counting
+constexpr int kLpSlack = 8;    // threads more than k that may reach the bound
+
+// The two halves of a cluster barrier: what comes before the arrival is visible
+// after the wait.
+__device__ __forceinline__ void lp_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void lp_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 struct Found {
   unsigned key;
   int token;
 };
+struct LpPart {            // one CTA's share of the row's results
+  float top, sum, sum_z;   // its largest logit, sums relative to that
+  unsigned ahead, n_best, key;
+};
+template <int W>
 struct LpShared {
   Found found[kLpFound];
-  Found best[kMaxTop];     // this CTA's alternatives, in order
-  Found all[kLpCluster * kMaxTop];
-  float warp_f[kLpWarps][2];
-  unsigned warp_u[2][kLpWarps];
-  float top;               // this CTA's largest logit
-  float sum, sum_z;        // relative to the row's
-  unsigned ahead, n_found, n_best;
+  Found best[kLpCluster][kMaxTop];  // in the first CTA: every CTA's, in order
+  LpPart part[kLpCluster];          // in the first CTA
+  float warp_f[W][2];
+  unsigned warp_u[2][W];
+  unsigned n_found;
 };
 
 // Ascending order of logits; NaN above everything, -0 as +0.  0: no logit
@@ -62,22 +82,114 @@ __device__ __forceinline__ float key_logit(unsigned k) {
   if (k == 0xffffffffu) return NAN;
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
+constexpr unsigned kLowestKey = 0x00800000u;  // of the lowest finite logit
 
-__device__ __forceinline__ unsigned lp_sum(unsigned v, LpShared &sm, int round) {
+template <int W>
+__device__ __forceinline__ unsigned lp_sum(unsigned v, LpShared<W> &sm, int round) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   v = __reduce_add_sync(kFull, v);
   unsigned *const row = sm.warp_u[round & 1];
   if (lane == 0) row[warp] = v;
   __syncthreads();
-  return __reduce_add_sync(kFull, lane < kLpWarps ? row[lane] : 0u);
+  return __reduce_add_sync(kFull, lane < W ? row[lane] : 0u);
 }
 
-template <int DT, int NV>  // NV: 16-byte vectors of a thread
-__global__ void __launch_bounds__(kLpThreads)
-    token_logprobs_kernel(const LogprobParams p) {
-  constexpr int VEC = DT == SVP_F32 ? 4 : 8;
-  constexpr int SIZE = 16 / VEC;
-  __shared__ LpShared sm;
+__device__ __forceinline__ float max_nan_f(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_nan_2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) {
+  return __uint_as_float(w & 0xffff0000u);
+}
+
+// The bytes of y that the four digits of `sel` name; a digit of 8 and more
+// spreads the sign of the byte it names (less 8).
+__device__ __forceinline__ uint32_t spread(uint32_t y, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(y), "r"(sel));
+  return r;
+}
+
+// A 16-byte vector of logits.
+template <int DT>
+struct Vec {
+  static constexpr int N = DT == SVP_F32 ? 4 : 8;
+  static constexpr uint32_t kNone = DT == SVP_F32 ? 0xff800000u : 0xff80ff80u;
+  static __device__ __forceinline__ uint4 none() {
+    return make_uint4(kNone, kNone, kNone, kNone);
+  }
+  static __device__ __forceinline__ float value(const uint4 &v, int e) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (DT == SVP_F32) return __uint_as_float(w[e]);
+    else return e % 2 ? hi_f(w[e / 2]) : lo_f(w[e / 2]);
+  }
+  // the largest element, NaN if there is one
+  static __device__ __forceinline__ float top(const uint4 &v) {
+    if constexpr (DT == SVP_F32) {
+      return max_nan_f(max_nan_f(__uint_as_float(v.x), __uint_as_float(v.y)),
+                       max_nan_f(__uint_as_float(v.z), __uint_as_float(v.w)));
+    } else {
+      const uint32_t m = max_nan_2(max_nan_2(v.x, v.y), max_nan_2(v.z, v.w));
+      return max_nan_f(lo_f(m), hi_f(m));
+    }
+  }
+  // v where bit e of `bits` is set, -inf elsewhere.  Four bits become the sign
+  // bits of four bytes, which the byte permutation spreads.
+  static __device__ __forceinline__ uint4 masked(const uint4 &v, uint32_t bits) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (DT == SVP_F32) {
+      const uint32_t y = (bits & 15u) * 0x10204080u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t m = spread(y, 0x8888 + 0x1111 * e);
+        w[e] = (w[e] & m) | (kNone & ~m);
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t y = ((bits >> (4 * h)) & 15u) * 0x10204080u;
+        const uint32_t m0 = spread(y, 0x9988);
+        const uint32_t m1 = spread(y, 0xbbaa);
+        w[2 * h] = (w[2 * h] & m0) | (kNone & ~m0);
+        w[2 * h + 1] = (w[2 * h + 1] & m1) | (kNone & ~m1);
+      }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// What is worked out from v after this is worked out anew: nothing of it stays
+// in registers from one pass over the row to the next.
+__device__ __forceinline__ void anew(uint4 &v) {
+  asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w));
+}
+
+// The next value above x (x below +inf), as the type has it.
+template <int DT>
+__device__ __forceinline__ float next_up(float x) {
+  constexpr uint32_t ulp = DT == SVP_F32 ? 1u : 0x10000u;
+  if (x == 0.f) return __uint_as_float(ulp);
+  const uint32_t u = __float_as_uint(x);
+  return __uint_as_float((u >> 31) ? u - ulp : u + ulp);
+}
+
+// CTAs that an SM is to hold, with 4 NV registers of a thread for the row.
+constexpr int lp_ctas(int nv, int t) {
+  return t > 256 ? 1 : nv <= 4 ? 4 : nv <= 8 ? 3 : 2;
+}
+
+template <int DT, int NV, int T>  // NV: vectors of a thread
+__global__ void __launch_bounds__(T, lp_ctas(NV, T)) token_logprobs_kernel(const LogprobParams p) {
+  using V = Vec<DT>;
+  constexpr int VEC = V::N, SIZE = 16 / VEC, W = T / 32;
+  __shared__ LpShared<W> sm;
   cg::cluster_group cluster = cg::this_cluster();
   const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -93,121 +205,174 @@ __global__ void __launch_bounds__(kLpThreads)
         if (p.entropy) p.entropy[row] = 0.f;
         if (p.ranks) p.ranks[row] = -1;
       }
-      for (int i = tid; i < p.n_top; i += kLpThreads) {
+      for (int i = tid; i < p.n_top; i += T) {
         p.top_logprobs[row * p.n_top + i] = -INFINITY;
         p.top_tokens[row * p.n_top + i] = -1;
       }
     }
     return;  // the whole cluster
   }
+  if (nc > 1) lp_arrive();  // the first CTA's shared memory is there
 
   // ---- the row into registers ----
-  // Rows start anywhere: vectors are aligned ones that cover the row, the
-  // first and the last may hold less than VEC of its elements.
+  // Rows start anywhere.  The whole aligned vectors are dealt out; what is left
+  // before and after them is one extra vector of the first CTA's thread 0 and
+  // its second warp's first.
   const char *const base = static_cast<const char *>(p.logits) +
                            row * (size_t)p.vocab * SIZE;
   const int shift = (int)(reinterpret_cast<uintptr_t>(base) & 15u) / SIZE;
-  const char *const aligned = base - shift * SIZE;
-  const int n_vec = (shift + p.vocab + VEC - 1) / VEC;
+  const uint4 *const aligned = reinterpret_cast<const uint4 *>(base - shift * SIZE);
+  const int f0 = shift ? 1 : 0, f1 = max((shift + p.vocab) / VEC, f0);
   const uint32_t *const allowed =
       p.allowed ? p.allowed + row * (size_t)p.words : nullptr;
-  uint4 raw[NV];
-  uint32_t bits[NV];  // which elements take part
-  auto vec_of = [&](int i) { return (i * nc + rank) * kLpThreads + tid; };
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = vec_of(i);
-    raw[i] = make_uint4(0, 0, 0, 0);
-    bits[i] = 0u;
-    if (v < n_vec) {
-      const int t0 = v * VEC - shift;  // token of the vector's first element
-      if (t0 >= 0 && t0 + VEC <= p.vocab) {
-        raw[i] = __ldg(reinterpret_cast<const uint4 *>(aligned) + v);
-        bits[i] = (1u << VEC) - 1u;
-      } else {
-        uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          if (t0 + e < 0 || t0 + e >= p.vocab) continue;
-          bits[i] |= 1u << e;
-          if constexpr (DT == SVP_F32)
-            w[e] = __ldg(reinterpret_cast<const uint32_t *>(base) + t0 + e);
-          else
-            w[e / 2] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(base) +
-                                        t0 + e) << (16 * (e % 2));
-        }
-        raw[i] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    }
-  }
-  if (allowed) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (bits[i] == 0u) continue;
-      // VEC bits from bit t0 on (from bit 0 where the row's first vector
-      // starts before it), out of one or two words
-      const int t0 = vec_of(i) * VEC - shift;
-      const int from = t0 < 0 ? 0 : t0;
-      const int w = from >> 5;
-      const uint32_t w0 = __ldg(allowed + w);
-      const uint32_t w1 = w + 1 < p.words ? __ldg(allowed + w + 1) : 0u;
-      const uint32_t m = __funnelshift_r(w0, w1, from & 31);
-      bits[i] &= m << (from - t0);
-    }
-  }
-  auto value = [&](int i, int e) {
-    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-    if constexpr (DT == SVP_F32) return __uint_as_float(w[e]);
+  auto element = [&](int t) {  // logit of token t
+    if constexpr (DT == SVP_F32) return reinterpret_cast<const float *>(base)[t];
     else
-      return __uint_as_float(e % 2 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+      return __uint_as_float(
+          (uint32_t)reinterpret_cast<const uint16_t *>(base)[t] << 16);
   };
-  // the order key of element e of vector i: 0 where it takes no part
-  auto key = [&](int i, int e) {
-    return (bits[i] >> e) & 1u ? logit_key(value(i, e)) : 0u;
+  auto may = [&](int t) {
+    return !allowed || ((__ldg(allowed + (t >> 5)) >> (t & 31)) & 1u);
   };
-
-  // ---- the largest logit ----
-  unsigned mine = 0;  // this thread's largest key
+  uint4 raw[NV], extra = V::none();
+  auto vec_of = [&](int i) { return f0 + (i * nc + rank) * T + tid; };
+  auto token_of = [&](int i) { return vec_of(i) * VEC - shift; };
 #pragma unroll
   for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) mine = max(mine, key(i, e));
-  {
-    const unsigned m = __reduce_max_sync(kFull, mine);
-    if (lane == 0) sm.warp_u[0][warp] = m;
-    __syncthreads();
-    const unsigned x =
-        __reduce_max_sync(kFull, lane < kLpWarps ? sm.warp_u[0][lane] : 0u);
-    if (tid == 0) sm.top = __uint_as_float(x);  // the key's bits
-  }
-  if (nc > 1) cluster.sync(); else __syncthreads();
-  unsigned top_key = 0;
-  for (int r = 0; r < nc; ++r)
-    top_key = max(top_key, __float_as_uint(nc > 1 ? *cluster.map_shared_rank(&sm.top, r)
-                                                  : sm.top));
-  const float top = top_key ? key_logit(top_key) : 0.f;
-
-  // ---- sums, and how many are ahead of the token ----
-  const bool in_mask = !allowed || ((allowed[token >> 5] >> (token & 31)) & 1u);
-  float xt;
-  if constexpr (DT == SVP_F32) xt = reinterpret_cast<const float *>(base)[token];
-  else
-    xt = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(base)[token] << 16);
-  const unsigned kt = in_mask ? logit_key(xt) : 0u;
-  float s = 0.f, sz = 0.f;
-  unsigned ahead = 0;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int t0 = vec_of(i) * VEC - shift;
+    raw[i] = vec_of(i) < f1 ? __ldg(aligned + vec_of(i)) : V::none();
+  const float xt = element(token);
+  const unsigned kt = may(token) ? logit_key(xt) : 0u;
+  const bool has_extra = rank == 0 && warp < 2;  // (the warp)
+  const int extra0 = warp == 0 ? 0 : f1 * VEC - shift;  // its tokens
+  const int extra1 = warp == 0 ? min(f0 * VEC - shift, p.vocab) : p.vocab;
+  if (has_extra && lane == 0) {
+    uint32_t w[4] = {V::kNone, V::kNone, V::kNone, V::kNone};
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      const unsigned k = key(i, e);
-      if (k == 0u) continue;
-      const float d = (value(i, e) - top) * p.sc;  // in units of log 2
+      if (extra0 + e >= extra1 || !may(extra0 + e)) continue;
+      const uint32_t u = __float_as_uint(element(extra0 + e));
+      if constexpr (DT == SVP_F32) w[e] = u;
+      else
+        w[e / 2] = e % 2 ? (w[e / 2] & 0xffffu) | u : (w[e / 2] & 0xffff0000u) | (u >> 16);
+    }
+    extra = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (allowed) {
+    uint32_t bits[NV];
+    if (shift == 0) {  // a vector's bits lie in one byte
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int v = vec_of(i);
+        bits[i] = 0;
+        if (v < f1) {
+          const uint32_t y =
+              __ldg(reinterpret_cast<const unsigned char *>(allowed) + v * VEC / 8);
+          bits[i] = VEC == 8 ? y : y >> (4 * (v & 1));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int t0 = token_of(i);
+        bits[i] = 0;
+        if (vec_of(i) < f1) {
+          const int w = t0 >> 5;
+          const uint32_t w0 = __ldg(allowed + w);
+          const uint32_t w1 = (t0 & 31) + VEC > 32 ? __ldg(allowed + w + 1) : 0u;
+          bits[i] = __funnelshift_r(w0, w1, t0 & 31);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) raw[i] = V::masked(raw[i], bits[i]);
+  }
+
+  // ---- the largest logit ----
+  float big = V::top(raw[0]);
+#pragma unroll
+  for (int i = 1; i < NV; ++i) big = max_nan_f(big, V::top(raw[i]));
+  if (has_extra) big = max_nan_f(big, V::top(extra));
+  const unsigned mine = logit_key(big);  // this thread's largest key
+  if (tid == 0) sm.n_found = 0;
+  const unsigned wm = __reduce_max_sync(kFull, mine);
+  if (lane == 0) sm.warp_u[0][warp] = wm;
+  __syncthreads();
+  const unsigned top_key =
+      __reduce_max_sync(kFull, lane < W ? sm.warp_u[0][lane] : 0u);
+  const float top = top_key ? key_logit(top_key) : 0.f;
+  const bool odd = !(top < INFINITY);  // NaN or +inf: no probabilities
+
+  // f(key, token) of every logit of this CTA, out of memory again: for the rare
+  // rows that need more passes than the registers are laid out for
+  auto each = [&](auto f) {
+    for (int v = rank * T + tid; v < f1 - f0; v += nc * T) {
+      const uint4 x = __ldg(aligned + f0 + v);
+      const int t0 = (f0 + v) * VEC - shift;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (may(t0 + e)) f(logit_key(V::value(x, e)), t0 + e);
+    }
+    if (has_extra && lane == 0)
+      for (int t = extra0; t < extra1; ++t)
+        if (may(t)) f(logit_key(element(t)), t);
+  };
+
+  // ---- sums, and how many are ahead of the token ----
+  // Tokens before it are ahead with a logit that is not smaller, those after
+  // it with a larger one: not below one of two bounds.  The vector that holds
+  // the token counts as after; thread 0 of the cluster adds the equals in it.
+  float s = 0.f, sz = 0.f;
+  unsigned ahead = 0;
+  auto sums = [&](uint4 v) {
+    anew(v);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      // in units of log 2; far below what counts, and finite
+      const float d = fmaxf((V::value(v, e) - top) * p.sc, -1e4f);
       const float w = ex2(d);
       s += w;
-      sz = fmaf(w, d > -200.f ? d : 0.f, sz);
-      ahead += k > kt || (k == kt && t0 + e < token) ? 1u : 0u;
+      sz = fmaf(w, d, sz);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < NV; ++i) sums(raw[i]);
+  if (has_extra) sums(extra);
+  if (p.ranks && kt != 0u) {
+    if (xt < INFINITY) {
+      const float up = next_up<DT>(xt);
+      uint32_t n2 = 0u;
+      auto count = [&](const uint4 &v, int t0) {
+        const float at = t0 + VEC <= token ? xt : up;
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        if constexpr (DT == SVP_F32) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            ahead += !(__uint_as_float(w[e]) < at) ? 1u : 0u;
+        } else {
+          // counts of at most 4 (NV + 1) in each half: exact in bf16
+          const uint32_t u = __float_as_uint(at);
+          const uint32_t at2 = (u & 0xffff0000u) | (u >> 16);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t r;
+            asm("set.geu.bf16x2.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w[e]), "r"(at2));
+            asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(n2) : "r"(r));
+          }
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < NV; ++i) count(raw[i], token_of(i));
+      if (has_extra) count(extra, warp == 0 ? -shift : extra0);
+      if constexpr (DT != SVP_F32) ahead += (unsigned)(lo_f(n2) + hi_f(n2));
+      if (rank == 0 && tid == 0) {
+        const int from = (token + shift) / VEC * VEC - shift;
+        for (int t = max(from, 0); t < token; ++t)
+          if (may(t) && element(t) == xt) ++ahead;
+      }
+    } else {  // +inf or NaN: by key
+      each([&](unsigned x, int t) {
+        ahead += x > kt || (x == kt && t < token) ? 1u : 0u;
+      });
     }
   }
 #pragma unroll
@@ -220,151 +385,184 @@ __global__ void __launch_bounds__(kLpThreads)
     sm.warp_f[warp][1] = sz;
   }
   const unsigned n_ahead = lp_sum(ahead, sm, 1);  // its barrier serves both
-  if (tid == 0) {
-    float a = 0.f, c = 0.f;
-    for (int w = 0; w < kLpWarps; ++w) {
-      a += sm.warp_f[w][0];
-      c += sm.warp_f[w][1];
-    }
-    sm.sum = a;
-    sm.sum_z = c;
-    sm.ahead = n_ahead;
-    sm.n_found = 0;
-  }
-  __syncthreads();
 
   // ---- this CTA's alternatives ----
-  if (p.n_top > 0) {
+  unsigned keep = 0;
+  if (p.n_top > 0 && top_key > 0u) {
     const unsigned k = (unsigned)p.n_top;
-    // the largest bound that k threads reach: with fewer threads that hold
-    // anything, every element
-    unsigned edge = 0;
-    for (int bit = 31; bit >= 0; --bit) {
-      const unsigned at = edge | (1u << bit);
-      if ((unsigned)__syncthreads_count(mine >= at) >= k) edge = at;
+    // a bound that at least k threads reach, and few more: first two octaves
+    // below the largest, else from the lowest logit on (with fewer threads
+    // that hold any, every element)
+    unsigned edge = kLowestKey, hi = top_key == 0xffffffffu ? top_key : top_key + 1u;
+    {
+      const unsigned guess = top_key - (2u << 23);
+      if (top_key > kLowestKey + (2u << 23)) {
+        const unsigned c = (unsigned)__syncthreads_count(mine >= guess);
+        if (c >= k) edge = guess; else hi = guess;
+        if (c >= k && c <= k + kLpSlack) hi = edge;
+      }
+      while (hi > edge + 1u) {
+        const unsigned mid = edge + (hi - edge) / 2u;
+        const unsigned c = (unsigned)__syncthreads_count(mine >= mid);
+        if (c >= k) {
+          edge = mid;
+          if (c <= k + kLpSlack) break;
+        } else {
+          hi = mid;
+        }
+      }
     }
-    if (edge == 0) edge = 1;
-    unsigned reach = 0;
+    auto add = [&](unsigned x, int t) {
+      const unsigned at = atomicAdd(&sm.n_found, 1u);
+      if (at < kLpFound) {
+        sm.found[at].key = x;
+        sm.found[at].token = t;
+      }
+    };
+    if (mine >= edge) {
+      auto some = [&](uint4 v, int t0) {
+        anew(v);
+        if (logit_key(V::top(v)) < edge) return;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+        for (int e = 0; e < VEC; ++e) {
+          const unsigned x = logit_key(V::value(v, e));
+          if (x >= edge) add(x, t0 + e);
+        }
+      };
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) reach += key(i, e) >= edge ? 1u : 0u;
-    unsigned n = lp_sum(reach, sm, 0);
-    int last = 0x7fffffff;  // the last token that counts among those at the edge
+      for (int i = 0; i < NV; ++i) some(raw[i], token_of(i));
+      if (has_extra) some(extra, extra0);
+    }
+    __syncthreads();
+    unsigned n = sm.n_found;
     if (n > kLpFound) {
       // the k-th largest of all, then the token up to which its equals count
       edge = 0;
       for (int bit = 31; bit >= 0; --bit) {
         const unsigned at = edge | (1u << bit);
         unsigned c = 0;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) c += key(i, e) >= at ? 1u : 0u;
+        each([&](unsigned x, int) { c += x >= at ? 1u : 0u; });
         if (lp_sum(c, sm, bit) >= k) edge = at;
       }
-      last = 0;
+      int last = 0;
       for (int bit = 30; bit >= 0; --bit) {
         // do fewer than k come before token `at`?
         const int at = last | (1 << bit);
         unsigned c = 0;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const unsigned x = key(i, e);
-            c += x > edge || (x == edge && vec_of(i) * VEC - shift + e < at) ? 1u : 0u;
-          }
+        each([&](unsigned x, int t) {
+          c += x > edge || (x == edge && t < at) ? 1u : 0u;
+        });
         if (lp_sum(c, sm, bit + 1) < k) last = at;  // (+ 1: in turn with the above)
       }
+      if (tid == 0) sm.n_found = 0;
+      __syncthreads();
+      each([&](unsigned x, int t) {
+        if (x > edge || (x == edge && t <= last)) add(x, t);
+      });
+      __syncthreads();
       n = k;
     }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const unsigned x = key(i, e);
-        const int t = vec_of(i) * VEC - shift + e;
-        if (x > edge || (x == edge && t <= last)) {
-          const unsigned at = atomicAdd(&sm.n_found, 1u);
-          sm.found[at].key = x;
-          sm.found[at].token = t;
-        }
-      }
-    __syncthreads();
-    const unsigned keep = min(n, k);
-    for (unsigned c = tid; c < n; c += kLpThreads) {
+    keep = min(n, k);
+    if (nc > 1) lp_wait();
+    Found *const best =
+        nc > 1 ? cluster.map_shared_rank(&sm.best[rank][0], 0) : &sm.best[0][0];
+    for (unsigned c = tid; c < n; c += T) {
       const Found f = sm.found[c];
       unsigned r = 0;
       for (unsigned o = 0; o < n; ++o) {
         const Found h = sm.found[o];
         r += h.key > f.key || (h.key == f.key && h.token < f.token) ? 1u : 0u;
       }
-      if (r < keep) sm.best[r] = f;
+      if (r < keep) best[r] = f;
     }
-    if (tid == 0) sm.n_best = keep;
+  } else if (nc > 1) {
+    lp_wait();
   }
-  if (nc > 1) cluster.sync(); else __syncthreads();
+  if (tid == 0) {
+    LpPart part;
+    part.top = top;
+    part.key = top_key;
+    part.sum = part.sum_z = 0.f;
+    for (int w = 0; w < W; ++w) {
+      part.sum += sm.warp_f[w][0];
+      part.sum_z += sm.warp_f[w][1];
+    }
+    if (odd) part.sum = NAN;
+    if (top_key == 0u) part.sum = part.sum_z = 0.f;
+    part.ahead = n_ahead;
+    part.n_best = keep;
+    LpPart *const to =
+        nc > 1 ? cluster.map_shared_rank(&sm.part[rank], 0) : &sm.part[0];
+    *to = part;
+  }
+  // the others' results are in the first CTA, which alone goes on
+  if (nc > 1) {
+    lp_arrive();
+    if (rank != 0) return;
+    lp_wait();
+  } else {
+    __syncthreads();
+  }
 
   // ---- the row's results ----
-  if (rank == 0) {
-    float total = 0.f, total_z = 0.f;
-    unsigned n_before = 0;
-    for (int r = 0; r < nc; ++r) {
-      const LpShared *o = nc > 1 ? cluster.map_shared_rank(&sm, r) : &sm;
-      total += o->sum;
-      total_z += o->sum_z;
-      n_before += o->ahead;
-    }
-    const float ln = logf(total);
-    if (tid == 0) {
-      // a row that allows nothing has no probabilities: -inf, entropy 0
-      p.logprobs[row] = total != total ? NAN
-                        : kt == 0u     ? -INFINITY
-                                       : (xt - top) * p.inv_t - ln;
-      if (p.entropy)
-        p.entropy[row] = top_key == 0u ? 0.f : ln - total_z / total * kLn2;
-      if (p.ranks) p.ranks[row] = kt == 0u ? -1 : (int)n_before;
-    }
-    if (p.n_top > 0) {
-      unsigned n = 0, from[kLpCluster + 1];
-#pragma unroll
-      for (int r = 0; r < kLpCluster; ++r) {
-        from[r] = n;
-        if (r < nc) n += nc > 1 ? cluster.map_shared_rank(&sm, r)->n_best : sm.n_best;
-      }
-      from[kLpCluster] = n;
-#pragma unroll
-      for (int r = 0; r < kLpCluster; ++r) {
-        const unsigned c = from[r + 1] - from[r];
-        if (r < nc)
-          for (unsigned i = tid; i < c; i += kLpThreads)
-            sm.all[from[r] + i] =
-                nc > 1 ? cluster.map_shared_rank(&sm, r)->best[i] : sm.best[i];
-      }
-      __syncthreads();
-      for (unsigned c = tid; c < n; c += kLpThreads) {
-        const Found f = sm.all[c];
-        unsigned r = 0;
-        for (unsigned o = 0; o < n; ++o) {
-          const Found h = sm.all[o];
-          r += h.key > f.key || (h.key == f.key && h.token < f.token) ? 1u : 0u;
+  unsigned row_key = 0, n_before = 0;
+  for (int r = 0; r < nc; ++r) {
+    row_key = max(row_key, sm.part[r].key);
+    n_before += sm.part[r].ahead;
+  }
+  const float peak = row_key ? key_logit(row_key) : 0.f;
+  float total = 0.f, total_z = 0.f;
+  for (int r = 0; r < nc; ++r) {
+    if (sm.part[r].key == 0u) continue;  // nothing there
+    // this CTA's distance from the row's maximum, in units of log 2
+    const float d = fmaxf((sm.part[r].top - peak) * p.sc, -1e4f);
+    const float f = ex2(d);
+    total = fmaf(sm.part[r].sum, f, total);
+    total_z = fmaf(fmaf(sm.part[r].sum, d, sm.part[r].sum_z), f, total_z);
+  }
+  const float ln = logf(total);
+  if (tid == 0) {
+    // a row that allows nothing has no probabilities: -inf, entropy 0
+    p.logprobs[row] = total != total ? NAN
+                      : kt == 0u     ? -INFINITY
+                                     : (xt - peak) * p.inv_t - ln;
+    if (p.entropy)
+      p.entropy[row] = row_key == 0u ? 0.f : ln - total_z / total * kLn2;
+    if (p.ranks) p.ranks[row] = kt == 0u ? -1 : (int)n_before;
+  }
+  if (p.n_top > 0) {
+    unsigned n = 0;
+    for (int r = 0; r < nc; ++r) n += sm.part[r].n_best;
+    for (int x = tid; x < nc * kMaxTop; x += T) {
+      const int c = x / kMaxTop, i = x % kMaxTop;
+      if (i >= (int)sm.part[c].n_best) continue;
+      const Found f = sm.best[c][i];
+      // its place: the larger ones before it in its own list, and in the others'
+      unsigned r = (unsigned)i;
+      for (int o = 0; o < nc; ++o) {
+        if (o == c) continue;
+        unsigned lo = 0, hi = sm.part[o].n_best;  // first that is not ahead
+        while (lo < hi) {
+          const unsigned mid = (lo + hi) / 2u;
+          const Found h = sm.best[o][mid];
+          if (h.key > f.key || (h.key == f.key && h.token < f.token)) lo = mid + 1u;
+          else hi = mid;
         }
-        if (r < (unsigned)p.n_top) {
-          p.top_logprobs[row * p.n_top + r] = (key_logit(f.key) - top) * p.inv_t - ln;
-          p.top_tokens[row * p.n_top + r] = f.token;
-        }
+        r += lo;
       }
-      for (unsigned i = n + tid; i < (unsigned)p.n_top; i += kLpThreads) {
-        p.top_logprobs[row * p.n_top + i] = -INFINITY;
-        p.top_tokens[row * p.n_top + i] = -1;
+      if (r < (unsigned)p.n_top) {
+        p.top_logprobs[row * p.n_top + r] = (key_logit(f.key) - peak) * p.inv_t - ln;
+        p.top_tokens[row * p.n_top + r] = f.token;
       }
+    }
+    for (unsigned i = n + tid; i < (unsigned)p.n_top; i += T) {
+      p.top_logprobs[row * p.n_top + i] = -INFINITY;
+      p.top_tokens[row * p.n_top + i] = -1;
     }
   }
-  if (nc > 1) cluster.sync();  // results may still be read
 }
 
-template <int DT, int NV>
+template <int DT, int NV, int T>
 cudaError_t logprobs_t(const LogprobParams &p, int nc, cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -374,33 +572,32 @@ cudaError_t logprobs_t(const LogprobParams &p, int nc, cudaStream_t stream) {
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.rows * nc));
-  cfg.blockDim = dim3(kLpThreads);
+  cfg.gridDim = dim3((unsigned)p.rows * (unsigned)nc);
+  cfg.blockDim = dim3(T);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<DT, NV>, p);
+  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<DT, NV, T>, p);
 }
 
 template <int DT>
 cudaError_t logprobs_dt(const LogprobParams &p, int sms, cudaStream_t stream) {
-  constexpr int VEC = DT == SVP_F32 ? 4 : 8;
-  // vectors of a row, one more where it starts off a 16-byte boundary
-  const int vecs = (p.vocab + 2 * VEC - 2) / VEC;
-  const int per_cta = (vecs + kLpThreads - 1) / kLpThreads;  // of a thread, nc = 1
-  // few rows: more CTAs to a row; long rows: as many as keep a thread's part
-  // in 8 vectors
+  constexpr int T = 256;
+  const int vecs = p.vocab / Vec<DT>::N;
+  // CTAs of a row: as many as keep a thread's part in 16 vectors; more for few
+  // rows, while a thread has a vector
   int nc = 1;
-  while (nc < kLpCluster && per_cta > nc &&
-         (per_cta > 8 * nc || (long long)p.rows * nc < 2LL * sms))
+  while (nc < kLpCluster &&
+         (vecs > 16 * T * nc || ((long long)p.rows * nc < 4LL * sms && vecs > T * nc)))
     nc *= 2;
-  const int nv = (per_cta + nc - 1) / nc;
-  if (nv <= 1) return logprobs_t<DT, 1>(p, nc, stream);
-  if (nv <= 2) return logprobs_t<DT, 2>(p, nc, stream);
-  if (nv <= 4) return logprobs_t<DT, 4>(p, nc, stream);
-  if (nv <= 8) return logprobs_t<DT, 8>(p, nc, stream);
-  if (nv <= 20) return logprobs_t<DT, 20>(p, nc, stream);
-  return cudaErrorInvalidConfiguration;  // more than kMaxVocab
+  const int nv = (vecs + T * nc - 1) / (T * nc);
+  if (nv <= 1) return logprobs_t<DT, 1, T>(p, nc, stream);
+  if (nv <= 2) return logprobs_t<DT, 2, T>(p, nc, stream);
+  if (nv <= 4) return logprobs_t<DT, 4, T>(p, nc, stream);
+  if (nv <= 8) return logprobs_t<DT, 8, T>(p, nc, stream);
+  if (nv <= 16) return logprobs_t<DT, 16, T>(p, nc, stream);
+  static_assert(20 * 512 * kLpCluster >= kMaxVocab / 4, "the longest row");
+  return logprobs_t<DT, 20, 512>(p, nc, stream);
 }
 
 }  // namespace

@@ -262,6 +262,59 @@ __host__ __device__ constexpr int pscore_row() {
   return 2 * S * 2 * D + 16;  // positive and negative parts; no bank conflicts
 }
 
+// The parts of eight elements of a query row, from dimension 8 c on.
+template <int D, int S>
+__device__ __forceinline__ void stage_query(const PageScoreParams &p, unsigned char *to,
+                                            size_t at, int c, bool there) {
+  // the negative parts (for lo), then the positive ones
+  if constexpr (S == 1) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (there)
+      v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + at) + c);
+    const uint32_t flip = p.negate ? 0x80008000u : 0u;
+    const uint32_t w[4] = {v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip};
+    uint32_t neg[4], pos[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      neg[e] = PairBf16::lo(w[e], 0u);
+      pos[e] = PairBf16::hi(w[e], 0u);
+    }
+    *reinterpret_cast<uint4 *>(to + 16 * c) = make_uint4(neg[0], neg[1], neg[2], neg[3]);
+    *reinterpret_cast<uint4 *>(to + 2 * D + 16 * c) =
+        make_uint4(pos[0], pos[1], pos[2], pos[3]);
+  } else {
+    float x[8] = {};
+    if (there) {
+      const float4 *from =
+          reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + at) + 2 * c;
+      const float4 u = __ldg(from), v = __ldg(from + 1);
+      x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+      x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+    }
+    uint32_t neg[S][4] = {}, pos[S][4] = {};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float v = p.negate ? -x[e] : x[e];
+      const bool up = v > 0.f, nan = v != v;
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        const float h = __bfloat162float(__float2bfloat16_rn(v));
+        const uint32_t bits = __float_as_uint(h) >> 16 << (16 * (e & 1));
+        if (up || nan) pos[s][e / 2] |= bits;
+        if (!up) neg[s][e / 2] |= bits;
+        v = isfinite(h) ? v - h : 0.f;  // what is left; nothing of an infinity
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      *reinterpret_cast<uint4 *>(to + s * 2 * D + 16 * c) =
+          make_uint4(neg[s][0], neg[s][1], neg[s][2], neg[s][3]);
+      *reinterpret_cast<uint4 *>(to + (S + s) * 2 * D + 16 * c) =
+          make_uint4(pos[s][0], pos[s][1], pos[s][2], pos[s][3]);
+    }
+  }
+}
+
 template <int D, int S>
 __global__ void __launch_bounds__(32 * kPScoreWarps)
     page_scores_kernel(const PageScoreParams p) {
@@ -286,75 +339,22 @@ __global__ void __launch_bounds__(32 * kPScoreWarps)
   const int first = chunk * p.tiles_per_cta;
   const int last = min(first + p.tiles_per_cta, tiles);
   float *const out = p.scores + (size_t)unit * p.max_blocks;
-  if (first * 16 < n) {
-    // the query rows' parts: row r of this launch is (position, head of the
-    // group) r0 + r
-    const int padded = (p.rows + 7) / 8 * 8;
-    for (int i = threadIdx.x; i < padded * (D / 2); i += 32 * kPScoreWarps) {
-      const int r = i / (D / 2), pair = i - r * (D / 2);
-      const int row = p.row0 + r;
-      uint32_t pos[S], neg[S];
-      float x[2] = {0.f, 0.f};
-      if (r < p.rows) {
-        const size_t at =
-            (((size_t)b * p.q_len + row / p.group) * p.num_q_heads +
-             (size_t)head * p.group + row % p.group) * D + 2 * pair;
-        if constexpr (S == 1) {
-          const uint32_t w = *reinterpret_cast<const uint32_t *>(
-              static_cast<const uint16_t *>(p.q) + at);
-          x[0] = __uint_as_float(w << 16);
-          x[1] = __uint_as_float(w & 0xffff0000u);
-        } else {
-          const float2 w = *reinterpret_cast<const float2 *>(
-              static_cast<const float *>(p.q) + at);
-          x[0] = w.x;
-          x[1] = w.y;
-        }
-      }
-#pragma unroll
-      for (int s = 0; s < S; ++s) pos[s] = neg[s] = 0u;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float v = p.negate ? -x[e] : x[e];
-        const bool up = v > 0.f, nan = v != v;
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-          const __nv_bfloat16 h = __float2bfloat16_rn(v);
-          const uint32_t bits = (uint32_t)__bfloat16_as_ushort(h) << (16 * e);
-          if (up || nan) pos[s] |= bits;
-          if (!up) neg[s] |= bits;
-          // what is left; nothing of an infinity or a NaN
-          v = isfinite(__bfloat162float(h)) ? v - __bfloat162float(h) : 0.f;
-        }
-      }
-#pragma unroll
-      for (int s = 0; s < S; ++s) {
-        // side 0 (negative parts, with lo), then side 1
-        *reinterpret_cast<uint32_t *>(sq + r * ROW + s * 2 * D + 4 * pair) = neg[s];
-        *reinterpret_cast<uint32_t *>(sq + r * ROW + (S + s) * 2 * D + 4 * pair) =
-            pos[s];
-      }
-    }
-    __syncthreads();
-  }
-  const int n_nt = (p.rows + 7) / 8;
   const int32_t *const table = p.block_table + (size_t)b * p.max_blocks;
-  for (int tile = first + warp; tile < last; tile += kPScoreWarps) {
-    const int page0 = tile * 16;
-    if (page0 >= n) {  // nothing here: -inf, so that a score is always there
-      if (lane < 16 && page0 + lane < p.max_blocks && !p.more)
-        out[page0 + lane] = -INFINITY;
-      continue;
-    }
+  // lane r < 16: the physical page of page r of a tile, or -1
+  auto page_ids = [&](int tile) {
+    const int at = tile * 16 + lane;
     int id = -1;
-    if (lane < 16 && page0 + lane < n) {
-      id = table[page0 + lane];
+    if (lane < 16 && tile < last && at < n) {
+      id = table[at];
       if (id < 0 || id >= p.num_blocks) {
         raise_pages(SVP_DEV_BAD_BLOCK_ID);
         id = -1;
       }
     }
-    uint4 w[2][2][NC];  // [page g, g + 8][lo, hi]
+    return id;
+  };
+  uint4 w[2][2][NC];  // [page g, g + 8][lo, hi]
+  auto load = [&](int id) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int page = __shfl_sync(kFull, id, g + 8 * h);
@@ -368,34 +368,65 @@ __global__ void __launch_bounds__(32 * kPScoreWarps)
           w[h][side][c] = page < 0 ? make_uint4(0, 0, 0, 0)
                                    : __ldg(src + side * (D / 8) + 4 * c + t);
     }
+  };
+  // the first tile's bounds are on their way while the query rows are laid out
+  int id = page_ids(first + warp);
+  if (first * 16 < n) {
+    load(id);
+    // row r of this launch is (position, head of the group) row0 + r
+    const int padded = (p.rows + 7) / 8 * 8;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < padded * (D / 8); i += 32 * kPScoreWarps) {
+      const int r = i / (D / 8), c = i % (D / 8);
+      const int row = p.row0 + min(r, p.rows - 1);
+      const size_t at = (((size_t)b * p.q_len + row / p.group) * p.num_q_heads +
+                         (size_t)head * p.group + row % p.group) * D;
+      stage_query<D, S>(p, sq + r * ROW, at, c, r < p.rows);
+    }
+    __syncthreads();
+  }
+  const int n_nt = (p.rows + 7) / 8;
+  for (int tile = first + warp; tile < last; tile += kPScoreWarps) {
+    const int page0 = tile * 16;
+    if (page0 >= n) {  // nothing here: -inf, so that a score is always there
+      if (lane < 16 && page0 + lane < p.max_blocks && !p.more)
+        out[page0 + lane] = -INFINITY;
+      continue;
+    }
+    const int next = page_ids(tile + kPScoreWarps);
     float best[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
     for (int nt = 0; nt < n_nt; ++nt) {
-      float acc[2][4] = {};
+      float acc[2][2][4] = {};  // four chains of products
       const unsigned char *qr = sq + (nt * 8 + g) * ROW + 16 * t;
 #pragma unroll
-      for (int side = 0; side < 2; ++side)
+      for (int s = 0; s < S; ++s)
 #pragma unroll
-        for (int s = 0; s < S; ++s)
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
+          for (int side = 0; side < 2; ++side) {
             const uint4 q = *reinterpret_cast<const uint4 *>(
                 qr + (side * S + s) * 2 * D + 64 * c);
             const uint4 &a = w[0][side][c], &e = w[1][side][c];
-            mma_bf16(acc[0], a.x, e.x, a.y, e.y, q.x, q.y);
-            mma_bf16(acc[1], a.z, e.z, a.w, e.w, q.z, q.w);
+            mma_bf16(acc[side][0], a.x, e.x, a.y, e.y, q.x, q.y);
+            mma_bf16(acc[side][1], a.z, e.z, a.w, e.w, q.z, q.w);
           }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (nt * 8 + 2 * t + (e & 1) < p.rows)
-          best[e >> 1] = max_nan(best[e >> 1], acc[0][e] + acc[1][e]);
+          best[e >> 1] = max_nan(best[e >> 1], (acc[0][0][e] + acc[0][1][e]) +
+                                                   (acc[1][0][e] + acc[1][1][e]));
       }
     }
+    const int now = id;
+    id = next;
+    load(id);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       best[h] = max_nan(best[h], __shfl_xor_sync(kFull, best[h], 1));
       best[h] = max_nan(best[h], __shfl_xor_sync(kFull, best[h], 2));
       const int at = page0 + g + 8 * h;
-      const bool there = __shfl_sync(kFull, id, g + 8 * h) >= 0;
+      const bool there = __shfl_sync(kFull, now, g + 8 * h) >= 0;
       if (t == 0 && at < p.max_blocks) {
         float v = there ? best[h] * p.scale : -INFINITY;
         if (p.more && there) v = max_nan(v, out[at]);
@@ -406,13 +437,24 @@ __global__ void __launch_bounds__(32 * kPScoreWarps)
 }
 
 // ---- selection ----
-// The k-th largest of a list's scores, found bit by bit: the largest key T
-// such that at least k keys are not below it, each bit one count over the
-// CTA's registers and one barrier.  Then the kept pages are numbered in order.
-// Bound by that chain of barriers; histograms of digits would be fewer
-// passes, but scores share their leading bits and so their bins.
-constexpr int kPickKeys = 16;  // keys of a thread held in registers
-constexpr int kPickMax = 1024;
+// The k-th largest of a list's scores: a histogram of 1024 equal parts of the
+// keys' range tells which part holds it, and how many it is from that part's
+// top; of a part with few keys those are ranked by counting, one with many
+// is cut into 1024 again (three times at most: keys have 32 bits).  Then the
+// kept pages are numbered in order.  Bound by that chain of about ten
+// barriers.
+constexpr int kPickMax = 1024;   // threads
+constexpr int kPickKeys = 16;    // keys of a thread held in registers
+constexpr int kPickBins = 1024;
+constexpr int kPickFew = 256;    // keys ranked by counting
+
+struct PickShared {
+  uint4 hist4[kPickBins / 4];
+  unsigned few[kPickFew];
+  unsigned warp_a[32], warp_b[32];
+  unsigned cells[kPickMax * kPickKeys / 32];
+  unsigned bin, above, in_bin, n_few, edge, ties;
+};
 
 // Ascending unsigned order; NaN above everything, -0 as +0.  Never 0.
 __device__ __forceinline__ unsigned pick_key(float x) {
@@ -421,23 +463,25 @@ __device__ __forceinline__ unsigned pick_key(float x) {
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-// Sum of v over the block, for every thread; buf: two rows of 32, used in turn.
-__device__ __forceinline__ unsigned block_sum(unsigned v, unsigned (*buf)[32],
-                                              int round) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  v = __reduce_add_sync(kFull, v);
-  unsigned *const row = buf[round & 1];
-  if (lane == 0) row[warp] = v;
+// Exclusive prefix sum over the block; buf holds one value per warp.
+__device__ __forceinline__ unsigned pick_scan(unsigned v, unsigned *buf) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned incl = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const unsigned y = __shfl_up_sync(kFull, incl, off);
+    if (lane >= off) incl += y;
+  }
+  if (lane == 31) buf[warp] = incl;
   __syncthreads();
-  const unsigned x = lane < (int)(blockDim.x >> 5) ? row[lane] : 0u;
-  return __reduce_add_sync(kFull, x);
+  return __reduce_add_sync(kFull, lane < warp ? buf[lane] : 0u) + incl - v;
 }
 
-template <bool REGS>
+template <int KEYS>  // keys of a thread in registers; 0: read again each time
 __global__ void __launch_bounds__(kPickMax)
     pick_pages_kernel(const PickParams p) {
-  __shared__ unsigned sums[2][32];
-  __shared__ unsigned cells[2][32];
+  __shared__ PickShared sm;
+  unsigned *const hist = reinterpret_cast<unsigned *>(sm.hist4);
   const int tid = threadIdx.x, T = blockDim.x;
   const int warp = tid >> 5, lane = tid & 31, n_warps = T >> 5;
   const unsigned unit = blockIdx.x;
@@ -445,7 +489,14 @@ __global__ void __launch_bounds__(kPickMax)
   pdl_wait();
   pdl_launch_dependents();
   int32_t *const pages = p.pages + (size_t)unit * p.n_select;
+  const float *const scores = p.scores + (size_t)unit * p.max_blocks;
   const int L = p.seq_lens[b];
+  float x[KEYS ? KEYS : 1];
+  if constexpr (KEYS > 0) {
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i)
+      x[i] = i * T + tid < p.max_blocks ? __ldg(scores + i * T + tid) : 0.f;
+  }
   int n = (int)(((long long)L + kBlockSize - 1) / kBlockSize);
   if (L < 0 || n > p.max_blocks) {
     if (tid == 0) raise_pages(SVP_DEV_BAD_SEQ_LEN);
@@ -458,69 +509,155 @@ __global__ void __launch_bounds__(kPickMax)
   // candidates [c0, c1) compete for k places
   const int c0 = p.n_sink, c1 = n - p.n_recent;
   const unsigned k = (unsigned)(p.n_select - p.n_sink - p.n_recent);
-  const float *const scores = p.scores + (size_t)unit * p.max_blocks;
-  unsigned key[REGS ? kPickKeys : 1];
-  if constexpr (REGS) {
+  unsigned key[KEYS ? KEYS : 1];
+  if constexpr (KEYS > 0) {
 #pragma unroll
-    for (int i = 0; i < kPickKeys; ++i) {
+    for (int i = 0; i < KEYS; ++i) {
       const int j = i * T + tid;
-      key[i] = j >= c0 && j < c1 ? pick_key(scores[j]) : 0u;
+      key[i] = j >= c0 && j < c1 ? pick_key(x[i]) : 0u;
     }
   }
-  // keys not below `at` (at > 0)
-  auto count = [&](unsigned at) {
-    unsigned c = 0;
-    if constexpr (REGS) {
+  auto each = [&](auto f) {  // f(key) of every candidate
+    if constexpr (KEYS > 0) {
 #pragma unroll
-      for (int i = 0; i < kPickKeys; ++i) c += key[i] >= at ? 1u : 0u;
+      for (int i = 0; i < KEYS; ++i)
+        if (key[i] != 0u) f(key[i]);
     } else {
-      for (int j = c0 + tid; j < c1; j += T) c += pick_key(scores[j]) >= at ? 1u : 0u;
+      for (int j = c0 + tid; j < c1; j += T) f(pick_key(__ldg(scores + j)));
     }
-    return c;
   };
-  unsigned edge = 0xffffffffu, ties = 0;  // k == 0: nothing is kept by score
-  bool any = k > 0;
-  if (any) {
-    edge = 0;
-    for (int bit = 31; bit >= 0; --bit) {
-      const unsigned at = edge | (1u << bit);
-      if (block_sum(count(at), sums, bit) >= k) edge = at;
+  unsigned edge = 0xffffffffu, ties = 0;  // kept: above the edge, and ties at it
+  if (k > 0) {
+    unsigned lo = 0xffffffffu, hi = 0u;
+    each([&](unsigned y) {
+      lo = min(lo, y);
+      hi = max(hi, y);
+    });
+    lo = __reduce_min_sync(kFull, lo);
+    hi = __reduce_max_sync(kFull, hi);
+    if (lane == 0) {
+      sm.warp_a[warp] = lo;
+      sm.warp_b[warp] = hi;
     }
-    // kept: all above the edge, and the first `ties` of those at it
-    const unsigned above =
-        edge == 0xffffffffu ? 0u : block_sum(count(edge + 1), sums, 1);
-    ties = k - above;
-  }
-  // number the kept pages, T positions at a time, warp after warp
-  unsigned n_sure = 0, n_tied = 0;
-  const unsigned lower = (1u << lane) - 1u;
-  for (int i = 0, j0 = 0; j0 < n; ++i, j0 += T) {
-    const int j = j0 + tid;
-    const bool forced = j < c0 || (j >= c1 && j < n);
-    unsigned x = 0;
-    if (any && j >= c0 && j < c1) {
-      if constexpr (REGS) {
-#pragma unroll
-        for (int u = 0; u < kPickKeys; ++u)
-          if (u == i) x = key[u];
-      } else {
-        x = pick_key(scores[j]);
-      }
-    }
-    const bool sure = forced || x > edge, tied = x != 0 && x == edge;
-    const unsigned s = __ballot_sync(kFull, sure), e = __ballot_sync(kFull, tied);
-    unsigned *const row = cells[i & 1];
-    if (lane == 0) row[warp] = (__popc(s) << 16) | __popc(e);
+    for (int i = tid; i < kPickBins / 4; i += T) sm.hist4[i] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) sm.n_few = 0;
     __syncthreads();
-    const unsigned mine = lane < n_warps ? row[lane] : 0u;
-    unsigned before = lane < warp ? mine : 0u;
-    before = __reduce_add_sync(kFull, before);
-    const unsigned all = __reduce_add_sync(kFull, mine);
-    const unsigned t0 = n_tied + (before & 0xffffu) + __popc(e & lower);
-    const unsigned s0 = n_sure + (before >> 16) + __popc(s & lower);
-    if (sure || (tied && t0 < ties)) pages[s0 + min(t0, ties)] = j;
-    n_sure += all >> 16;
-    n_tied += all & 0xffffu;
+    lo = __reduce_min_sync(kFull, lane < n_warps ? sm.warp_a[lane] : 0xffffffffu);
+    hi = __reduce_max_sync(kFull, lane < n_warps ? sm.warp_b[lane] : 0u);
+    unsigned need = k;
+    while (true) {
+      // keys in [lo, hi], `need` of them wanted
+      const unsigned range = hi - lo;
+      const int shift = range < kPickBins ? 0 : 22 - __clz(range);
+      each([&](unsigned y) {
+        if (y >= lo && y <= hi) atomicAdd(&hist[(y - lo) >> shift], 1u);
+      });
+      __syncthreads();
+      // from the top: a thread takes kPickBins / T bins, at most 8
+      const int per = kPickBins / T;
+      unsigned mine = 0;
+      for (int i = 0; i < per; ++i) mine += hist[kPickBins - 1 - (tid * per + i)];
+      unsigned before = pick_scan(mine, sm.warp_a);
+      if (before < need && before + mine >= need) {  // exactly one thread
+        for (int i = 0; i < per; ++i) {
+          const int bin = kPickBins - 1 - (tid * per + i);
+          if (before + hist[bin] >= need) {
+            sm.bin = (unsigned)bin;
+            sm.above = before;
+            sm.in_bin = hist[bin];
+            break;
+          }
+          before += hist[bin];
+        }
+      }
+      __syncthreads();
+      const unsigned in_bin = sm.in_bin;
+      need -= sm.above;
+      lo += sm.bin << shift;
+      hi = lo + min(hi - lo, (1u << shift) - 1u);
+      if (shift == 0 || need == in_bin) {
+        // equal keys, or all of the part's
+        edge = shift == 0 ? lo : lo - 1u;
+        ties = shift == 0 ? need : 0u;
+        break;
+      }
+      if (in_bin <= kPickFew) {
+        each([&](unsigned y) {
+          if (y >= lo && y <= hi) sm.few[atomicAdd(&sm.n_few, 1u)] = y;
+        });
+        __syncthreads();
+        for (unsigned c = tid; c < in_bin; c += T) {
+          const unsigned y = sm.few[c];
+          unsigned above = 0, same = 0;
+          for (unsigned o = 0; o < in_bin; ++o) {
+            above += sm.few[o] > y ? 1u : 0u;
+            same += sm.few[o] == y ? 1u : 0u;
+          }
+          if (above < need && above + same >= need) {  // (equal keys agree)
+            sm.edge = y;
+            sm.ties = need - above;
+          }
+        }
+        __syncthreads();
+        edge = sm.edge;
+        ties = sm.ties;
+        break;
+      }
+      for (int i = tid; i < kPickBins / 4; i += T) sm.hist4[i] = make_uint4(0, 0, 0, 0);
+      __syncthreads();
+    }
+  }
+  // number the kept pages: T positions a row, warp after warp
+  const unsigned lower = (1u << lane) - 1u;
+  auto look = [&](int j, unsigned y, unsigned &sure, unsigned &tied) {
+    const bool forced = j < c0 || (j >= c1 && j < n);
+    sure = __ballot_sync(kFull, forced || y > edge);
+    tied = __ballot_sync(kFull, y != 0u && y == edge);
+  };
+  auto put = [&](int j, unsigned sure, unsigned tied, unsigned s0, unsigned t0) {
+    const bool a = (sure >> lane) & 1u, t = (tied >> lane) & 1u;
+    t0 += __popc(tied & lower);
+    if (a || (t && t0 < ties)) pages[s0 + __popc(sure & lower) + min(t0, ties)] = j;
+  };
+  if constexpr (KEYS > 0) {
+    if (k == 0) {
+#pragma unroll
+      for (int i = 0; i < KEYS; ++i) key[i] = 0u;
+    }
+    unsigned sure[KEYS], tied[KEYS];
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i) {
+      look(i * T + tid, key[i], sure[i], tied[i]);
+      if (lane == 0)
+        sm.cells[i * n_warps + warp] = (__popc(sure[i]) << 16) | __popc(tied[i]);
+    }
+    __syncthreads();
+    // at most T cells: both counts' prefix sums at once
+    const unsigned c = tid < KEYS * n_warps ? sm.cells[tid] : 0u;
+    const unsigned before = pick_scan(c, sm.warp_b);
+    if (tid < KEYS * n_warps) sm.cells[tid] = before;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i) {
+      const unsigned y = sm.cells[i * n_warps + warp];
+      put(i * T + tid, sure[i], tied[i], y >> 16, y & 0xffffu);
+    }
+  } else {
+    unsigned n_sure = 0, n_tied = 0;
+    for (int i = 0, j0 = 0; j0 < n; ++i, j0 += T) {
+      const int j = j0 + tid;
+      unsigned sure, tied;
+      look(j, k > 0 && j >= c0 && j < c1 ? pick_key(__ldg(scores + j)) : 0u, sure, tied);
+      unsigned *const row = sm.cells + 32 * (i & 1);
+      if (lane == 0) row[warp] = (__popc(sure) << 16) | __popc(tied);
+      __syncthreads();
+      const unsigned all = lane < n_warps ? row[lane] : 0u;
+      const unsigned y = __reduce_add_sync(kFull, lane < warp ? all : 0u);
+      put(j, sure, tied, n_sure + (y >> 16), n_tied + (y & 0xffffu));
+      const unsigned sum = __reduce_add_sync(kFull, all);
+      n_sure += sum >> 16;
+      n_tied += sum & 0xffffu;
+    }
   }
 }
 
@@ -575,7 +712,7 @@ cudaError_t launch_page_scores(PageScoreParams p, int sms, cudaStream_t stream) 
   const long long units = (long long)p.batch * p.num_kv_heads;
   // a warp's tiles one after another, so that the query rows are laid out
   // once for several: but at least eight CTAs to an SM while there are tiles
-  long long per = tiles * units / ((long long)sms * 8 * kPScoreWarps);
+  long long per = tiles * units / ((long long)sms * 6 * kPScoreWarps);
   per = per < 1 ? 1 : per > 8 ? 8 : per;
   per *= kPScoreWarps;
   const long long chunks = (tiles + per - 1) / per;
@@ -593,12 +730,14 @@ cudaError_t launch_page_scores(PageScoreParams p, int sms, cudaStream_t stream) 
 cudaError_t launch_pick_pages(const PickParams &p, cudaStream_t stream) {
   const long long units = (long long)p.batch * p.heads;
   if (units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  // enough threads for the longest list's keys, at least a warp per 4 keys
-  int threads = 128;
-  while (threads < kPickMax && threads * 8 < p.max_blocks) threads *= 2;
-  if (p.max_blocks <= kPickMax * kPickKeys && p.max_blocks <= threads * kPickKeys)
-    return launch_pdl(pick_pages_kernel<true>, (unsigned)units, threads, 0, stream, p);
-  return launch_pdl(pick_pages_kernel<false>, (unsigned)units, threads, 0, stream, p);
+  // eight keys to a thread, sixteen where that takes more threads than there are
+  const int most = p.max_blocks;
+  const int threads = most <= 1024 ? 128 : most <= 2048 ? 256 : most <= 4096 ? 512 : kPickMax;
+  if (most <= 8 * threads)
+    return launch_pdl(pick_pages_kernel<8>, (unsigned)units, threads, 0, stream, p);
+  if (most <= kPickKeys * threads)
+    return launch_pdl(pick_pages_kernel<kPickKeys>, (unsigned)units, threads, 0, stream, p);
+  return launch_pdl(pick_pages_kernel<0>, (unsigned)units, threads, 0, stream, p);
 }
 
 cudaError_t read_status_pages(cudaStream_t s, unsigned *flags) {
