@@ -18,10 +18,12 @@
 //    M: S's accumulators are, packed, the A operand of P V.  P is bf16: a
 //    weight is off by half a bf16 step, 2^-8, as the output is; row sums are
 //    fp32 and of the weights before that rounding.
-//  * FP8 and 4-bit rows become fp16 operands between shared memory and the
-//    matrix instruction (exact); P is fp16 at 2^6 times its weight, which
-//    keeps weights down to 2^-20 normal.  q takes a power-of-two scale per row
-//    (fp4.cuh).
+//  * FP8 and 4-bit rows become fp16 operands (exact); P is fp16 at 2^6 times
+//    its weight, which keeps weights down to 2^-20 normal.  q takes a
+//    power-of-two scale per row (fp4.cuh).  With one row group that happens
+//    between shared memory and the matrix instruction, in registers; with
+//    several the four warps first expand a tile in shared memory, once for all
+//    of them.
 //  * fp32: CUDA cores, fp32 throughout.
 //  * Softmax in the log2 domain with a lazy reference: it moves only when a
 //    score exceeds it by 2^8, so the usual page costs one vote.
@@ -46,6 +48,7 @@ namespace cg = cooperative_groups;
 constexpr int kSpWarps = 4;
 constexpr int kSpThreads = 32 * kSpWarps;
 constexpr int kTilePages = 4;
+static_assert(kTilePages == kSpWarps, "a warp expands a page");
 constexpr int kListCap = 512;      // list entries a CTA looks up at once
 constexpr int kNoPage = 0x7ffffff0; // first position of a page that is not there
 constexpr float kSpNoRef = -3e38f; // below any score
@@ -69,9 +72,19 @@ struct SpShape {
   static constexpr int RES = kSpWarps * RPW * (RES_ROW + 8);
   static constexpr int RING = STAGES * STAGE > RES ? STAGES * STAGE : RES;
   static constexpr int SMEM =
-      RING + LIST + 64 +
+      RING + LIST + 128 +
       (DT == SVP_F32 ? kSpWarps * RPW * (QROW + kBlockSize * 4) : 0);
 };
+
+// Whether a tile is expanded to fp16 in shared memory, behind everything else
+// there: with several row groups, which would each convert it.
+__host__ __device__ constexpr bool sp_expand(int dt, int rg) {
+  return rg > 1 && (dt == SVP_FP8_E4M3 || dt == SVP_FP4_E2M1);
+}
+template <int DT, int D, int RG>
+__host__ __device__ constexpr int sp_smem() {
+  return SpShape<DT, D>::SMEM + (sp_expand(DT, RG) ? SpShape<SVP_BF16, D>::STAGE : 0);
+}
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -216,7 +229,7 @@ __device__ __forceinline__ RowMask row_mask(const SparseParams &p, int b, int L,
 }
 
 // A warp's state over 16-bit operands: lane (g, t) holds rows g and g + 8.
-template <int DT, int D>
+template <int DT, int D, bool WIDE>  // WIDE: 16-bit elements in shared memory
 struct WarpMma {
   static constexpr int KS = D / 16, NT = D / 8;
   static constexpr float kOff = DT == SVP_BF16 ? 0.f : 6.f;
@@ -248,7 +261,7 @@ struct WarpMma {
       const uint16_t *src = static_cast<const uint16_t *>(p.q) + at;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        if constexpr (DT == SVP_BF16) {
+        if constexpr (WIDE) {
           w[h][ks][0] = *reinterpret_cast<const uint32_t *>(src + 16 * ks + 2 * t);
           w[h][ks][1] = *reinterpret_cast<const uint32_t *>(src + 16 * ks + 2 * t + 8);
         } else {
@@ -294,7 +307,7 @@ struct WarpMma {
 
   // Key of column n (0..7) of S tile j.
   static __device__ __forceinline__ int key(int j, int n) {
-    return DT == SVP_FP4_E2M1 ? fp4_key(n, j) : 8 * j + n;
+    return !WIDE && DT == SVP_FP4_E2M1 ? fp4_key(n, j) : 8 * j + n;
   }
 
   // S of a page: lane (g, t) gets rows g and g + 8, columns 2 t and 2 t + 1 of
@@ -306,12 +319,12 @@ struct WarpMma {
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
-    if constexpr (DT == SVP_BF16) {
+    if constexpr (WIDE) {
       const int r = (lane >> 4) * 8 + (lane & 7), c = (lane >> 3) & 1;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         uint32_t k[4];
-        ldsm4(kp + piece<DT, D>(r, 2 * ks + c), k);
+        ldsm4(kp + piece<SVP_BF16, D>(r, 2 * ks + c), k);
         mma16<DT>(s[0], q[ks], k[0], k[1]);
         mma16<DT>(s[1], q[ks], k[2], k[3]);
       }
@@ -365,12 +378,12 @@ struct WarpMma {
                                          int lane) {
     const int g = lane >> 2, t = lane & 3;
     constexpr int ROWB = SpShape<DT, D>::ROWB;
-    if constexpr (DT == SVP_BF16) {
+    if constexpr (WIDE) {
       const int r = ((lane >> 3) & 1) * 8 + (lane & 7), c = lane >> 4;
 #pragma unroll
       for (int i = 0; i < NT / 2; ++i) {
         uint32_t v[4];
-        ldsm4_t(vp + piece<DT, D>(r, 2 * i + c), v);
+        ldsm4_t(vp + piece<SVP_BF16, D>(r, 2 * i + c), v);
         mma16<DT>(o[2 * i], pa, v[0], v[1]);
         mma16<DT>(o[2 * i + 1], pa, v[2], v[3]);
       }
@@ -434,7 +447,7 @@ struct WarpMma {
                                         const int (&j0)[NP], unsigned char *,
                                         int lane) {
     const int t = lane & 3;
-    constexpr int PAGE = SpShape<DT, D>::PAGE;
+    constexpr int PAGE = SpShape<WIDE ? SVP_BF16 : DT, D>::PAGE;
     float s[NP][2][4];
 #pragma unroll
     for (int n = 0; n < NP; ++n) scores(stage + 2 * n * PAGE, s[n], lane);
@@ -496,7 +509,7 @@ struct WarpMma {
 
   // Dimension of column n of O tile i.
   static __device__ __forceinline__ int dim(int i, int n) {
-    return DT == SVP_BF16       ? 8 * i + n
+    return WIDE                 ? 8 * i + n
            : DT == SVP_FP8_E4M3 ? 16 * (i >> 1) + 2 * n + (i & 1)
                                 : (D / 8) * n + i;
   }
@@ -676,20 +689,67 @@ struct WarpF32 {
   }
 };
 
-template <int DT, int D>
+template <int DT, int D, bool WIDE>
 struct WarpOf {
-  using T = WarpMma<DT, D>;
+  using T = WarpMma<DT, D, WIDE>;
 };
 template <int D>
-struct WarpOf<SVP_F32, D> {
+struct WarpOf<SVP_F32, D, false> {
   using T = WarpF32<D>;
 };
+
+// A page's side of FP8 or 4-bit rows as fp16, by a warp.
+template <int DT, int D>
+__device__ __forceinline__ void expand_side(uint32_t from, uint32_t to, int lane) {
+  constexpr int BLOCKS = D / 16;  // of 16 elements, of a row
+#pragma unroll
+  for (int i = 0; i < kBlockSize * BLOCKS / 32; ++i) {
+    const int y = i * 32 + lane, r = y / BLOCKS, c = y % BLOCKS;
+    uint32_t h[8];
+    if constexpr (DT == SVP_FP8_E4M3) {
+      const uint4 w = ls128(from + piece<DT, D>(r, c));
+      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        h[2 * e] = e4m3x2_f16x2(x[e]);
+        h[2 * e + 1] = e4m3x2_f16x2(x[e] >> 16);
+      }
+    } else {
+      const uint32_t row = from + r * fp4_row_bytes(D);
+      uint32_t w[2], v[4];
+      if constexpr (D == 128) {
+        const uint2 u = ls64(row + 8 * c);
+        w[0] = u.x;
+        w[1] = u.y;
+      } else {
+        w[0] = ls32(row + 8 * c);
+        w[1] = ls32(row + 8 * c + 4);
+      }
+      const uint32_t sc = e4m3x2_f16x2(ls8(row + D / 2 + c) * 0x101u);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        e2m1x8_h2(w[x], v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[4 * x + e] = hmul2(v[e], sc);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                       to + piece<SVP_BF16, D>(r, 2 * c + x)),
+                   "r"(h[4 * x]), "r"(h[4 * x + 1]), "r"(h[4 * x + 2]),
+                   "r"(h[4 * x + 3])
+                   : "memory");
+  }
+}
 
 template <int DT, int D, int RG>
 __global__ void __launch_bounds__(kSpThreads)
     sparse_attention_kernel(const SparseParams p) {
   using S = SpShape<DT, D>;
   constexpr int KG = kSpWarps / RG, RPW = S::RPW, RB = RG * RPW;
+  constexpr bool EXPAND = sp_expand(DT, RG);
+  using W16 = SpShape<SVP_BF16, D>;
   extern __shared__ __align__(128) unsigned char smem[];
   int2 *const list = reinterpret_cast<int2 *>(smem + S::RING);
   int *const counts = reinterpret_cast<int *>(smem + S::RING + S::LIST);
@@ -717,7 +777,7 @@ __global__ void __launch_bounds__(kSpThreads)
   const int hi = (int)((long long)p.n_select * (rank + 1) / nc);
   const int n_pages = (int)(((long long)L + kBlockSize - 1) / kBlockSize);
 
-  typename WarpOf<DT, D>::T st;
+  typename WarpOf<DT, D, EXPAND || DT == SVP_BF16>::T st;
   st.start(p, b, head, L, rb * RB + rg * RPW, own, lane);
   const bool idle = rb * RB + rg * RPW >= p.rows;  // a row group without rows
 
@@ -777,7 +837,17 @@ __global__ void __launch_bounds__(kSpThreads)
         load_tile<DT, D>(p, ring + ahead % S::STAGES * S::STAGE, list, ahead, count,
                          head, L);
       cp_commit();
-      const uint32_t stage = ring + tile % S::STAGES * S::STAGE;
+      uint32_t stage = ring + tile % S::STAGES * S::STAGE;
+      if constexpr (EXPAND) {
+        const uint32_t wide = ring + S::SMEM;
+#pragma unroll
+        for (int side = 0; side < 2; ++side)
+          expand_side<DT, D>(stage + (2 * warp + side) * S::PAGE,
+                             wide + (2 * warp + side) * W16::PAGE, lane);
+        __syncthreads();
+        stage = wide;
+      }
+      constexpr int PAGE = EXPAND ? W16::PAGE : S::PAGE;
       // a warp's pages of the tile lie side by side
       constexpr int MINE = kTilePages / KG, NP = MINE < 2 ? MINE : 2;
 #pragma unroll 1
@@ -787,7 +857,7 @@ __global__ void __launch_bounds__(kSpThreads)
         int j0[NP];
 #pragma unroll
         for (int n = 0; n < NP; ++n) j0[n] = e + n < count ? list[e + n].y : kNoPage;
-        st.template pages<NP>(p, stage + 2 * x * S::PAGE, j0, own, lane);
+        st.template pages<NP>(p, stage + 2 * x * PAGE, j0, own, lane);
       }
     }
     cp_wait<0>();
@@ -858,7 +928,7 @@ cudaError_t sparse_t(SparseParams p, int splits, cudaStream_t stream) {
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   auto kern = sparse_attention_kernel<DT, D, RG>;
   cudaError_t e = cudaFuncSetAttribute(
-      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, sp_smem<DT, D, RG>());
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -870,7 +940,7 @@ cudaError_t sparse_t(SparseParams p, int splits, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kSpThreads);
-  cfg.dynamicSmemBytes = S::SMEM;
+  cfg.dynamicSmemBytes = sp_smem<DT, D, RG>();
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;

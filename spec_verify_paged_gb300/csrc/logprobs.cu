@@ -7,12 +7,15 @@
 //   entropy   = ln S - (1 / S) sum ((x - m) / T) exp((x - m) / T)
 // so one maximum and one pass of exponentials give everything but the order.
 //
-// A cluster of 1 to 8 CTAs takes a row; every thread keeps its part of the row
-// in registers (what is not allowed as -inf), so the logits are read once.
-// What bounds it for long rows is instructions: about nine an element with the
-// exponential, so what can be done on pairs of bf16 is (the maximum, the count
-// of the tokens ahead), and nothing is done for an element that one test of
-// its vector or thread can rule out.  Each CTA's sums are relative to its own
+// A cluster of 1 to 8 CTAs takes a row, each a part of it that it copies into
+// shared memory (what is not allowed becomes -inf there), so the logits are
+// read once; a thread reads only what it copied, so no barrier is needed in
+// between.  What bounds it for long rows is instructions: about eight an
+// element with the exponential.  So what can be done on pairs of bf16 is (the
+// maximum, the count of the tokens ahead), and one test of a thread's or a
+// vector's maximum rules out most of them as alternatives.  Loops are short:
+// the row in registers, with everything unrolled, waited for instructions (512
+// rows of 131,072 bf16: 148 us).  Each CTA's sums are relative to its own
 // maximum; they meet in the first CTA's shared memory at the end, by one
 // cluster barrier.
 //
@@ -37,6 +40,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
+constexpr int kLpThreads = 256;
 constexpr int kLpCluster = 8;
 constexpr int kLpFound = 512;  // candidates ranked by counting
 constexpr int kLpSlack = 8;    // threads more than k that may reach the bound
@@ -57,8 +61,9 @@ struct Found {
   int token;
 };
 struct LpPart {            // one CTA's share of the row's results
-  float top, sum, sum_z;   // its largest logit, sums relative to that
-  unsigned ahead, n_best, key;
+  float top, c;            // its largest logit, and what sums are relative to:
+  float sum, sum_z;        // c in units of log 2, or (huge) the logit itself
+  unsigned ahead, n_best, key, huge;
 };
 template <int W>
 struct LpShared {
@@ -165,12 +170,6 @@ struct Vec {
   }
 };
 
-// What is worked out from v after this is worked out anew: nothing of it stays
-// in registers from one pass over the row to the next.
-__device__ __forceinline__ void anew(uint4 &v) {
-  asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w));
-}
-
 // The next value above x (x below +inf), as the type has it.
 template <int DT>
 __device__ __forceinline__ float next_up(float x) {
@@ -180,15 +179,12 @@ __device__ __forceinline__ float next_up(float x) {
   return __uint_as_float((u >> 31) ? u - ulp : u + ulp);
 }
 
-// CTAs that an SM is to hold, with 4 NV registers of a thread for the row.
-constexpr int lp_ctas(int nv, int t) {
-  return t > 256 ? 1 : nv <= 4 ? 4 : nv <= 8 ? 3 : 2;
-}
-
-template <int DT, int NV, int T>  // NV: vectors of a thread
-__global__ void __launch_bounds__(T, lp_ctas(NV, T)) token_logprobs_kernel(const LogprobParams p) {
+template <int DT>
+__global__ void __launch_bounds__(kLpThreads)
+    token_logprobs_kernel(const LogprobParams p, int part) {  // vectors of a CTA
   using V = Vec<DT>;
-  constexpr int VEC = V::N, SIZE = 16 / VEC, W = T / 32;
+  constexpr int T = kLpThreads, VEC = V::N, SIZE = 16 / VEC, W = T / 32;
+  extern __shared__ uint4 held[];  // thread tid's are tid, tid + T, ..
   __shared__ LpShared<W> sm;
   cg::cluster_group cluster = cg::this_cluster();
   const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -214,15 +210,23 @@ __global__ void __launch_bounds__(T, lp_ctas(NV, T)) token_logprobs_kernel(const
   }
   if (nc > 1) lp_arrive();  // the first CTA's shared memory is there
 
-  // ---- the row into registers ----
+  // ---- the row into shared memory ----
   // Rows start anywhere.  The whole aligned vectors are dealt out; what is left
   // before and after them is one extra vector of the first CTA's thread 0 and
   // its second warp's first.
   const char *const base = static_cast<const char *>(p.logits) +
                            row * (size_t)p.vocab * SIZE;
   const int shift = (int)(reinterpret_cast<uintptr_t>(base) & 15u) / SIZE;
-  const uint4 *const aligned = reinterpret_cast<const uint4 *>(base - shift * SIZE);
   const int f0 = shift ? 1 : 0, f1 = max((shift + p.vocab) / VEC, f0);
+  const int v0 = min(f0 + rank * part, f1);  // this CTA's
+  const int n_vec = min(part, f1 - v0);
+  const uint4 *const aligned = reinterpret_cast<const uint4 *>(base - shift * SIZE) + v0;
+  const int t00 = v0 * VEC - shift;          // the first one's first token
+  for (int i = tid; i < n_vec; i += T) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(held + i)),
+                 "l"(aligned + i) : "memory");
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
   const uint32_t *const allowed =
       p.allowed ? p.allowed + row * (size_t)p.words : nullptr;
   auto element = [&](int t) {  // logit of token t
@@ -234,14 +238,9 @@ __global__ void __launch_bounds__(T, lp_ctas(NV, T)) token_logprobs_kernel(const
   auto may = [&](int t) {
     return !allowed || ((__ldg(allowed + (t >> 5)) >> (t & 31)) & 1u);
   };
-  uint4 raw[NV], extra = V::none();
-  auto vec_of = [&](int i) { return f0 + (i * nc + rank) * T + tid; };
-  auto token_of = [&](int i) { return vec_of(i) * VEC - shift; };
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-    raw[i] = vec_of(i) < f1 ? __ldg(aligned + vec_of(i)) : V::none();
   const float xt = element(token);
   const unsigned kt = may(token) ? logit_key(xt) : 0u;
+  uint4 extra = V::none();
   const bool has_extra = rank == 0 && warp < 2;  // (the warp)
   const int extra0 = warp == 0 ? 0 : f1 * VEC - shift;  // its tokens
   const int extra1 = warp == 0 ? min(f0 * VEC - shift, p.vocab) : p.vocab;
@@ -257,41 +256,33 @@ __global__ void __launch_bounds__(T, lp_ctas(NV, T)) token_logprobs_kernel(const
     }
     extra = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  if (allowed) {
-    uint32_t bits[NV];
-    if (shift == 0) {  // a vector's bits lie in one byte
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int v = vec_of(i);
-        bits[i] = 0;
-        if (v < f1) {
-          const uint32_t y =
-              __ldg(reinterpret_cast<const unsigned char *>(allowed) + v * VEC / 8);
-          bits[i] = VEC == 8 ? y : y >> (4 * (v & 1));
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int t0 = token_of(i);
-        bits[i] = 0;
-        if (vec_of(i) < f1) {
-          const int w = t0 >> 5;
-          const uint32_t w0 = __ldg(allowed + w);
-          const uint32_t w1 = (t0 & 31) + VEC > 32 ? __ldg(allowed + w + 1) : 0u;
-          bits[i] = __funnelshift_r(w0, w1, t0 & 31);
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) raw[i] = V::masked(raw[i], bits[i]);
-  }
 
   // ---- the largest logit ----
-  float big = V::top(raw[0]);
-#pragma unroll
-  for (int i = 1; i < NV; ++i) big = max_nan_f(big, V::top(raw[i]));
-  if (has_extra) big = max_nan_f(big, V::top(extra));
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  float big = V::top(extra);
+  if (!allowed) {
+#pragma unroll 4
+    for (int i = tid; i < n_vec; i += T) big = max_nan_f(big, V::top(held[i]));
+  } else if (shift == 0) {  // a vector's bits lie in one byte
+    const unsigned char *const bytes = reinterpret_cast<const unsigned char *>(allowed);
+#pragma unroll 4
+    for (int i = tid; i < n_vec; i += T) {
+      const uint32_t y = __ldg(bytes + (v0 + i) * VEC / 8);
+      const uint4 v = V::masked(held[i], VEC == 8 ? y : y >> (4 * ((v0 + i) & 1)));
+      held[i] = v;
+      big = max_nan_f(big, V::top(v));
+    }
+  } else {
+#pragma unroll 4
+    for (int i = tid; i < n_vec; i += T) {
+      const int t0 = t00 + i * VEC, w = t0 >> 5;
+      const uint32_t w0 = __ldg(allowed + w);
+      const uint32_t w1 = (t0 & 31) + VEC > 32 ? __ldg(allowed + w + 1) : 0u;
+      const uint4 v = V::masked(held[i], __funnelshift_r(w0, w1, t0 & 31));
+      held[i] = v;
+      big = max_nan_f(big, V::top(v));
+    }
+  }
   const unsigned mine = logit_key(big);  // this thread's largest key
   if (tid == 0) sm.n_found = 0;
   const unsigned wm = __reduce_max_sync(kFull, mine);
@@ -302,79 +293,107 @@ __global__ void __launch_bounds__(T, lp_ctas(NV, T)) token_logprobs_kernel(const
   const float top = top_key ? key_logit(top_key) : 0.f;
   const bool odd = !(top < INFINITY);  // NaN or +inf: no probabilities
 
-  // f(key, token) of every logit of this CTA, out of memory again: for the rare
-  // rows that need more passes than the registers are laid out for
+  // f(key, token) of every logit of this thread, for rare rows
   auto each = [&](auto f) {
-    for (int v = rank * T + tid; v < f1 - f0; v += nc * T) {
-      const uint4 x = __ldg(aligned + f0 + v);
-      const int t0 = (f0 + v) * VEC - shift;
+#pragma unroll 1
+    for (int i = tid; i < n_vec; i += T) {
+      const uint4 v = held[i];
 #pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        if (may(t0 + e)) f(logit_key(V::value(x, e)), t0 + e);
+      for (int e = 0; e < VEC; ++e) f(logit_key(V::value(v, e)), t00 + i * VEC + e);
     }
-    if (has_extra && lane == 0)
-      for (int t = extra0; t < extra1; ++t)
-        if (may(t)) f(logit_key(element(t)), t);
+    if (has_extra) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) f(logit_key(V::value(extra, e)), extra0 + e);
+    }
   };
 
   // ---- sums, and how many are ahead of the token ----
   // Tokens before it are ahead with a logit that is not smaller, those after
   // it with a larger one: not below one of two bounds.  The vector that holds
   // the token counts as after; thread 0 of the cluster adds the equals in it.
+  // The distance to the maximum in units of log 2 is x sc - c, c = top sc: one
+  // instruction, exact but for c's rounding, which shifts all distances alike
+  // and so cancels as long as c is used throughout.  With huge logits c is no
+  // longer fine enough (or infinite): there it is (x - top) sc, as at
+  // temperatures beyond 1e30.
+  const bool huge = !(fabsf(top * p.sc) < 0x1p20f) || p.sc < 1e-30f;
+  const float c = huge ? 0.f : top * p.sc;
+  // far below what counts, and finite
+  const float low = top - 400.f / p.sc;
   float s = 0.f, sz = 0.f;
   unsigned ahead = 0;
-  auto sums = [&](uint4 v) {
-    anew(v);
+  auto distance = [&](float x) { return huge ? (x - top) * p.sc : fmaf(x, p.sc, -c); };
+  auto add_up = [&](float d) {
+    const float w = ex2(d);
+    s += w;
+    sz = fmaf(w, d, sz);
+  };
+  const bool ranked = p.ranks && kt != 0u;
+  const bool plain_rank = ranked && xt < INFINITY;
+  const float up = next_up<DT>(xt);
+  uint32_t n2 = 0u;  // counts of two halves: exact in bf16 up to 256
+  auto count = [&](const uint4 &v, int t0) {
+    const float at = t0 + VEC <= token ? xt : up;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (DT == SVP_F32) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      // in units of log 2; far below what counts, and finite
-      const float d = fmaxf((V::value(v, e) - top) * p.sc, -1e4f);
-      const float w = ex2(d);
-      s += w;
-      sz = fmaf(w, d, sz);
+      for (int e = 0; e < 4; ++e) ahead += !(__uint_as_float(w[e]) < at) ? 1u : 0u;
+    } else {
+      const uint32_t u = __float_as_uint(at);
+      const uint32_t at2 = (u & 0xffff0000u) | (u >> 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t r;
+        asm("set.geu.bf16x2.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w[e]), "r"(at2));
+        asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(n2) : "r"(r));
+      }
     }
   };
+  auto pour = [&] {  // the halves' counts, before they pass 256
+    if constexpr (DT != SVP_F32) {
+      ahead += (unsigned)(lo_f(n2) + hi_f(n2));
+      n2 = 0u;
+    }
+  };
+  if (!huge) {
+#pragma unroll 1
+    for (int i0 = tid; i0 < n_vec; i0 += 32 * T) {  // at most 128 in a half
+#pragma unroll 2
+      for (int i = i0; i < min(n_vec, i0 + 32 * T); i += T) {
+        const uint4 v = held[i];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) sums(raw[i]);
-  if (has_extra) sums(extra);
-  if (p.ranks && kt != 0u) {
-    if (xt < INFINITY) {
-      const float up = next_up<DT>(xt);
-      uint32_t n2 = 0u;
-      auto count = [&](const uint4 &v, int t0) {
-        const float at = t0 + VEC <= token ? xt : up;
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        if constexpr (DT == SVP_F32) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            ahead += !(__uint_as_float(w[e]) < at) ? 1u : 0u;
-        } else {
-          // counts of at most 4 (NV + 1) in each half: exact in bf16
-          const uint32_t u = __float_as_uint(at);
-          const uint32_t at2 = (u & 0xffff0000u) | (u >> 16);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t r;
-            asm("set.geu.bf16x2.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w[e]), "r"(at2));
-            asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(n2) : "r"(r));
-          }
-        }
-      };
-#pragma unroll
-      for (int i = 0; i < NV; ++i) count(raw[i], token_of(i));
-      if (has_extra) count(extra, warp == 0 ? -shift : extra0);
-      if constexpr (DT != SVP_F32) ahead += (unsigned)(lo_f(n2) + hi_f(n2));
-      if (rank == 0 && tid == 0) {
-        const int from = (token + shift) / VEC * VEC - shift;
-        for (int t = max(from, 0); t < token; ++t)
-          if (may(t) && element(t) == xt) ++ahead;
+        for (int e = 0; e < VEC; ++e)
+          add_up(fmaf(fmaxf(V::value(v, e), low), p.sc, -c));
+        if (plain_rank) count(v, t00 + i * VEC);
       }
-    } else {  // +inf or NaN: by key
-      each([&](unsigned x, int t) {
-        ahead += x > kt || (x == kt && t < token) ? 1u : 0u;
-      });
+      pour();
+    }
+  } else {
+#pragma unroll 1
+    for (int i = tid; i < n_vec; i += T) {
+      const uint4 v = held[i];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        add_up(fmaxf((V::value(v, e) - top) * p.sc, -1e4f));
+      if (plain_rank) count(v, t00 + i * VEC);
+      pour();
     }
   }
+  if (has_extra) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) add_up(fmaxf(distance(V::value(extra, e)), -1e4f));
+    if (plain_rank) count(extra, warp == 0 ? -shift : extra0);
+    pour();
+  }
+  if (plain_rank && rank == 0 && tid == 0) {
+    const int from = (token + shift) / VEC * VEC - shift;
+    for (int t = max(from, 0); t < token; ++t)
+      if (may(t) && element(t) == xt) ++ahead;
+  }
+  if (ranked && !plain_rank)  // +inf or NaN: by key
+    each([&](unsigned x, int t) {
+      ahead += x > kt || (x == kt && t < token) ? 1u : 0u;
+    });
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
     s += __shfl_xor_sync(kFull, s, off);
@@ -420,8 +439,7 @@ __global__ void __launch_bounds__(T, lp_ctas(NV, T)) token_logprobs_kernel(const
       }
     };
     if (mine >= edge) {
-      auto some = [&](uint4 v, int t0) {
-        anew(v);
+      auto some = [&](const uint4 &v, int t0) {
         if (logit_key(V::top(v)) < edge) return;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
@@ -429,8 +447,8 @@ __global__ void __launch_bounds__(T, lp_ctas(NV, T)) token_logprobs_kernel(const
           if (x >= edge) add(x, t0 + e);
         }
       };
-#pragma unroll
-      for (int i = 0; i < NV; ++i) some(raw[i], token_of(i));
+#pragma unroll 1
+      for (int i = tid; i < n_vec; i += T) some(held[i], t00 + i * VEC);
       if (has_extra) some(extra, extra0);
     }
     __syncthreads();
@@ -481,6 +499,8 @@ __global__ void __launch_bounds__(T, lp_ctas(NV, T)) token_logprobs_kernel(const
   if (tid == 0) {
     LpPart part;
     part.top = top;
+    part.c = c;
+    part.huge = huge;
     part.key = top_key;
     part.sum = part.sum_z = 0.f;
     for (int w = 0; w < W; ++w) {
@@ -506,26 +526,38 @@ __global__ void __launch_bounds__(T, lp_ctas(NV, T)) token_logprobs_kernel(const
 
   // ---- the row's results ----
   unsigned row_key = 0, n_before = 0;
+  int best_part = 0;
   for (int r = 0; r < nc; ++r) {
-    row_key = max(row_key, sm.part[r].key);
+    if (sm.part[r].key > row_key) {
+      row_key = sm.part[r].key;
+      best_part = r;
+    }
     n_before += sm.part[r].ahead;
   }
-  const float peak = row_key ? key_logit(row_key) : 0.f;
+  // everything relative to what the part with the largest logit is
+  const float peak = row_key ? sm.part[best_part].top : 0.f;
+  const bool far = sm.part[best_part].huge;
+  const float origin = sm.part[best_part].c;
   float total = 0.f, total_z = 0.f;
   for (int r = 0; r < nc; ++r) {
-    if (sm.part[r].key == 0u) continue;  // nothing there
-    // this CTA's distance from the row's maximum, in units of log 2
-    const float d = fmaxf((sm.part[r].top - peak) * p.sc, -1e4f);
-    const float f = ex2(d);
-    total = fmaf(sm.part[r].sum, f, total);
-    total_z = fmaf(fmaf(sm.part[r].sum, d, sm.part[r].sum_z), f, total_z);
+    const LpPart &o = sm.part[r];
+    if (o.key == 0u) continue;  // nothing there
+    // from what its sums are relative to, to that, in units of log 2
+    const float d = far      ? (o.top - peak) * p.sc - (o.huge ? 0.f : o.top * p.sc - o.c)
+                    : o.huge ? fmaf(o.top, p.sc, -origin)
+                             : o.c - origin;
+    const float near = fmaxf(d, -1e4f);
+    const float f = ex2(near);
+    total = fmaf(o.sum, f, total);
+    total_z = fmaf(fmaf(o.sum, near, o.sum_z), f, total_z);
   }
   const float ln = logf(total);
+  auto log_p = [&](float x) {
+    return (far ? (x - peak) * p.inv_t : fmaf(x, p.sc, -origin) * kLn2) - ln;
+  };
   if (tid == 0) {
     // a row that allows nothing has no probabilities: -inf, entropy 0
-    p.logprobs[row] = total != total ? NAN
-                      : kt == 0u     ? -INFINITY
-                                     : (xt - peak) * p.inv_t - ln;
+    p.logprobs[row] = total != total ? NAN : kt == 0u ? -INFINITY : log_p(xt);
     if (p.entropy)
       p.entropy[row] = row_key == 0u ? 0.f : ln - total_z / total * kLn2;
     if (p.ranks) p.ranks[row] = kt == 0u ? -1 : (int)n_before;
@@ -551,7 +583,7 @@ __global__ void __launch_bounds__(T, lp_ctas(NV, T)) token_logprobs_kernel(const
         r += lo;
       }
       if (r < (unsigned)p.n_top) {
-        p.top_logprobs[row * p.n_top + r] = (key_logit(f.key) - peak) * p.inv_t - ln;
+        p.top_logprobs[row * p.n_top + r] = log_p(key_logit(f.key));
         p.top_tokens[row * p.n_top + r] = f.token;
       }
     }
@@ -562,8 +594,25 @@ __global__ void __launch_bounds__(T, lp_ctas(NV, T)) token_logprobs_kernel(const
   }
 }
 
-template <int DT, int NV, int T>
-cudaError_t logprobs_t(const LogprobParams &p, int nc, cudaStream_t stream) {
+template <int DT>
+cudaError_t logprobs_dt(const LogprobParams &p, int sms, cudaStream_t stream) {
+  constexpr int T = kLpThreads;
+  const int vecs = p.vocab / Vec<DT>::N;
+  // CTAs of a row: as many as keep a part within 64 KB, so that an SM holds
+  // three; more for few rows, while a thread has a vector
+  int nc = 1;
+  while (nc < kLpCluster &&
+         (vecs > 16 * T * nc || ((long long)p.rows * nc < 4LL * sms && vecs > T * nc)))
+    nc *= 2;
+  const int part = (vecs + nc - 1) / nc;
+  constexpr int kMost = kMaxVocab / Vec<DT>::N / kLpCluster * 16;  // 160 KB at most
+  const int smem = part * 16;
+  if (smem > kMost) return cudaErrorInvalidConfiguration;
+  if (smem > 32 * 1024) {  // (the static part counts as well)
+    const cudaError_t e = cudaFuncSetAttribute(
+        token_logprobs_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -574,30 +623,11 @@ cudaError_t logprobs_t(const LogprobParams &p, int nc, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.rows * (unsigned)nc);
   cfg.blockDim = dim3(T);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<DT, NV, T>, p);
-}
-
-template <int DT>
-cudaError_t logprobs_dt(const LogprobParams &p, int sms, cudaStream_t stream) {
-  constexpr int T = 256;
-  const int vecs = p.vocab / Vec<DT>::N;
-  // CTAs of a row: as many as keep a thread's part in 16 vectors; more for few
-  // rows, while a thread has a vector
-  int nc = 1;
-  while (nc < kLpCluster &&
-         (vecs > 16 * T * nc || ((long long)p.rows * nc < 4LL * sms && vecs > T * nc)))
-    nc *= 2;
-  const int nv = (vecs + T * nc - 1) / (T * nc);
-  if (nv <= 1) return logprobs_t<DT, 1, T>(p, nc, stream);
-  if (nv <= 2) return logprobs_t<DT, 2, T>(p, nc, stream);
-  if (nv <= 4) return logprobs_t<DT, 4, T>(p, nc, stream);
-  if (nv <= 8) return logprobs_t<DT, 8, T>(p, nc, stream);
-  if (nv <= 16) return logprobs_t<DT, 16, T>(p, nc, stream);
-  static_assert(20 * 512 * kLpCluster >= kMaxVocab / 4, "the longest row");
-  return logprobs_t<DT, 20, 512>(p, nc, stream);
+  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<DT>, p, part);
 }
 
 }  // namespace

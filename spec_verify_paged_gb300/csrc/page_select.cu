@@ -194,38 +194,56 @@ __global__ void __launch_bounds__(32 * kBoundWarps)
       }
     }
   }
+  // Lanes that hold the same elements of other rows: in each step a lane hands
+  // half of its registers to its partner and keeps the other half, so at the
+  // end it has the bounds of NR / RPA (of one if there are fewer) registers.
+  int base = 0;  // the first register's place among the row's
 #pragma unroll
-  for (int off = LPR; off < 32; off <<= 1) {
+  for (int off = 16, left = NR; off >= LPR; off >>= 1) {
+    const bool up = (lane & off) != 0;
+    if (left > 1) {
+      left /= 2;
 #pragma unroll
-    for (int e = 0; e < NR; ++e) {
-      lo[e] = P::lo(lo[e], __shfl_xor_sync(kFull, lo[e], off));
-      hi[e] = P::hi(hi[e], __shfl_xor_sync(kFull, hi[e], off));
+      for (int e = 0; e < NR / 2; ++e) {
+        if (e >= left) break;
+        const uint32_t l = up ? lo[e] : lo[e + left], h = up ? hi[e] : hi[e + left];
+        const uint32_t ml = up ? lo[e + left] : lo[e], mh = up ? hi[e + left] : hi[e];
+        lo[e] = P::lo(ml, __shfl_xor_sync(kFull, l, off));
+        hi[e] = P::hi(mh, __shfl_xor_sync(kFull, h, off));
+      }
+      base += up ? left : 0;
+    } else {
+      lo[0] = P::lo(lo[0], __shfl_xor_sync(kFull, lo[0], off));
+      hi[0] = P::hi(hi[0], __shfl_xor_sync(kFull, hi[0], off));
     }
   }
-  if (r0 > 0) return;
+  constexpr int LEFT = NR / RPA > 1 ? NR / RPA : 1;
   unsigned char *dst = static_cast<unsigned char *>(p.bounds) +
                        ((size_t)phys * p.num_kv_heads + g) * (4 * D) + c * (2 * V);
 #pragma unroll
   for (int side = 0; side < 2; ++side) {
-    uint32_t o[V / 2];
-#pragma unroll
-    for (int e = 0; e < V / 2; ++e) {
-      if constexpr (DT == SVP_F32) {
-        const uint32_t *from = side ? hi : lo;
-        o[e] = bf16_outward(__uint_as_float(from[2 * e]), side) |
-               (bf16_outward(__uint_as_float(from[2 * e + 1]), side) << 16);
-      } else {
-        o[e] = P::out(side ? hi[e] : lo[e], side);
-      }
-    }
+    const uint32_t *from = side ? hi : lo;
     unsigned char *to = dst + side * (2 * D);
-    if constexpr (V == 4) {
-      *reinterpret_cast<uint2 *>(to) = make_uint2(o[0], o[1]);
+    if constexpr (DT == SVP_F32) {
+      uint16_t *const t16 = reinterpret_cast<uint16_t *>(to) + base;
+      if constexpr (LEFT == 4)
+        *reinterpret_cast<uint2 *>(t16) = make_uint2(
+            bf16_outward(__uint_as_float(from[0]), side) |
+                (bf16_outward(__uint_as_float(from[1]), side) << 16),
+            bf16_outward(__uint_as_float(from[2]), side) |
+                (bf16_outward(__uint_as_float(from[3]), side) << 16));
+      else
+        *reinterpret_cast<uint32_t *>(t16) =
+            bf16_outward(__uint_as_float(from[0]), side) |
+            (bf16_outward(__uint_as_float(from[1]), side) << 16);
     } else {
-#pragma unroll
-      for (int e = 0; e < V / 2; e += 4)
-        reinterpret_cast<uint4 *>(to)[e / 4] =
-            make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      uint32_t *const t32 = reinterpret_cast<uint32_t *>(to) + base;
+      if constexpr (LEFT >= 2)
+        *reinterpret_cast<uint2 *>(t32) =
+            make_uint2(P::out(from[0], side), P::out(from[1], side));
+      else
+        *t32 = P::out(from[0], side);
+      static_assert(LEFT <= 2, "pairs at most");
     }
   }
 }
@@ -234,9 +252,11 @@ __global__ void __launch_bounds__(32 * kBoundWarps)
 // The bound is a matrix product: pages as M, query rows as N, and 2 D terms,
 // hi with the positive parts of q and lo with the negative ones.  mma.sync
 // m16n8k16 takes 16 pages; the order of the terms does not matter, so they
-// are dealt such that lane (g, t) reads 16 consecutive bytes of pages g and
-// g + 8 for two steps: the bounds go from memory to the matrix instruction
-// through registers only, the query rows' parts wait in shared memory.
+// are dealt such that lane (g, t) takes 16 consecutive bytes of pages g and
+// g + 8 for two steps.  A lane copies its own pieces through a ring of two
+// tiles of 16 pages in shared memory, so both are on their way while a third
+// is multiplied, and no warp waits for another; the query rows' parts are in
+// shared memory as well.
 // bf16 products are exact in fp32, the sums are fp32; an fp32 q is taken as
 // three bf16 terms of 8 bits each.
 // Bound by the bounds' bytes.
@@ -353,8 +373,11 @@ __global__ void __launch_bounds__(32 * kPScoreWarps)
     }
     return id;
   };
-  uint4 w[2][2][NC];  // [page g, g + 8][lo, hi]
-  auto load = [&](int id) {
+  // this lane's pieces of a tile, [page g, g + 8][lo, hi][NC], in a ring of two
+  constexpr int PIECES = 4 * NC;
+  const uint32_t ring = smem_u32(sq) + (unsigned)((p.rows + 7) / 8 * 8) * ROW +
+                        (warp * 2 * PIECES * 32 + lane) * 16;
+  auto load = [&](int id, int stage) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int page = __shfl_sync(kFull, id, g + 8 * h);
@@ -362,17 +385,23 @@ __global__ void __launch_bounds__(32 * kPScoreWarps)
           static_cast<const unsigned char *>(p.bounds) +
           ((size_t)(page < 0 ? 0 : page) * p.num_kv_heads + head) * (4 * D));
 #pragma unroll
-      for (int side = 0; side < 2; ++side)
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-          w[h][side][c] = page < 0 ? make_uint4(0, 0, 0, 0)
-                                   : __ldg(src + side * (D / 8) + 4 * c + t);
+      for (int x = 0; x < 2 * NC; ++x)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         ring + (stage * PIECES + h * 2 * NC + x) * 512),
+                     "l"(src + x / NC * (D / 8) + 4 * (x % NC) + t),
+                     "r"(page < 0 ? 0 : 16)  // (a page that is not there: zeros)
+                     : "memory");
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  // the first tile's bounds are on their way while the query rows are laid out
-  int id = page_ids(first + warp);
+  // the first tiles' bounds are on their way while the query rows are laid out
+  constexpr int W = kPScoreWarps;
+  int id[3];  // of this warp's next tiles
+#pragma unroll
+  for (int i = 0; i < 3; ++i) id[i] = page_ids(first + warp + i * W);
   if (first * 16 < n) {
-    load(id);
+    load(id[0], 0);
+    load(id[1], 1);
     // row r of this launch is (position, head of the group) row0 + r
     const int padded = (p.rows + 7) / 8 * 8;
 #pragma unroll 4
@@ -386,14 +415,30 @@ __global__ void __launch_bounds__(32 * kPScoreWarps)
     __syncthreads();
   }
   const int n_nt = (p.rows + 7) / 8;
-  for (int tile = first + warp; tile < last; tile += kPScoreWarps) {
+  for (int tile = first + warp, stage = 0; tile < last; tile += W, stage ^= 1) {
     const int page0 = tile * 16;
     if (page0 >= n) {  // nothing here: -inf, so that a score is always there
       if (lane < 16 && page0 + lane < p.max_blocks && !p.more)
         out[page0 + lane] = -INFINITY;
       continue;
     }
-    const int next = page_ids(tile + kPScoreWarps);
+    const int next = page_ids(tile + 3 * W);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    uint4 w[2][2][NC];
+#pragma unroll
+    for (int x = 0; x < PIECES; ++x)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[x / (2 * NC)][x / NC % 2][x % NC].x),
+                     "=r"(w[x / (2 * NC)][x / NC % 2][x % NC].y),
+                     "=r"(w[x / (2 * NC)][x / NC % 2][x % NC].z),
+                     "=r"(w[x / (2 * NC)][x / NC % 2][x % NC].w)
+                   : "r"(ring + (stage * PIECES + x) * 512)
+                   : "memory");
+    const int now = id[0];
+    id[0] = id[1];
+    id[1] = id[2];
+    id[2] = next;
+    load(id[1], stage);  // the tile after the next one
     float best[2] = {-INFINITY, -INFINITY};
 #pragma unroll 1
     for (int nt = 0; nt < n_nt; ++nt) {
@@ -418,9 +463,6 @@ __global__ void __launch_bounds__(32 * kPScoreWarps)
                                                    (acc[1][0][e] + acc[1][1][e]));
       }
     }
-    const int now = id;
-    id = next;
-    load(id);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       best[h] = max_nan(best[h], __shfl_xor_sync(kFull, best[h], 1));
@@ -446,11 +488,11 @@ __global__ void __launch_bounds__(32 * kPScoreWarps)
 constexpr int kPickMax = 1024;   // threads
 constexpr int kPickKeys = 16;    // keys of a thread held in registers
 constexpr int kPickBins = 1024;
-constexpr int kPickFew = 256;    // keys ranked by counting
+constexpr int kPickFew = 128;    // keys ranked by counting
 
 struct PickShared {
   uint4 hist4[kPickBins / 4];
-  unsigned few[kPickFew];
+  alignas(16) unsigned few[kPickFew + 4];
   unsigned warp_a[32], warp_b[32];
   unsigned cells[kPickMax * kPickKeys / 32];
   unsigned bin, above, in_bin, n_few, edge, ties;
@@ -550,34 +592,51 @@ __global__ void __launch_bounds__(kPickMax)
       const unsigned range = hi - lo;
       const int shift = range < kPickBins ? 0 : 22 - __clz(range);
       each([&](unsigned y) {
-        if (y >= lo && y <= hi) atomicAdd(&hist[(y - lo) >> shift], 1u);
+        if (y >= lo && y <= hi) atomicAdd(&hist[(hi - y) >> shift], 1u);
       });
       __syncthreads();
-      // from the top: a thread takes kPickBins / T bins, at most 8
+      // from the top: a thread takes kPickBins / T bins, one to eight
       const int per = kPickBins / T;
+      unsigned c[8];
+      if (per >= 4) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 q = 4 * i < per ? sm.hist4[tid * (per / 4) + i]
+                                      : make_uint4(0, 0, 0, 0);
+          c[4 * i] = q.x;
+          c[4 * i + 1] = q.y;
+          c[4 * i + 2] = q.z;
+          c[4 * i + 3] = q.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = i < per ? hist[tid * per + i] : 0u;
+      }
       unsigned mine = 0;
-      for (int i = 0; i < per; ++i) mine += hist[kPickBins - 1 - (tid * per + i)];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mine += c[i];
       unsigned before = pick_scan(mine, sm.warp_a);
       if (before < need && before + mine >= need) {  // exactly one thread
-        for (int i = 0; i < per; ++i) {
-          const int bin = kPickBins - 1 - (tid * per + i);
-          if (before + hist[bin] >= need) {
-            sm.bin = (unsigned)bin;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (before < need && before + c[i] >= need) {
+            sm.bin = (unsigned)(tid * per + i);
             sm.above = before;
-            sm.in_bin = hist[bin];
-            break;
+            sm.in_bin = c[i];
+            before = need;  // found
+          } else {
+            before += c[i];
           }
-          before += hist[bin];
         }
       }
       __syncthreads();
       const unsigned in_bin = sm.in_bin;
       need -= sm.above;
-      lo += sm.bin << shift;
-      hi = lo + min(hi - lo, (1u << shift) - 1u);
+      hi -= sm.bin << shift;
+      lo = hi - min(hi - lo, (1u << shift) - 1u);
       if (shift == 0 || need == in_bin) {
         // equal keys, or all of the part's
-        edge = shift == 0 ? lo : lo - 1u;
+        edge = shift == 0 ? hi : lo - 1u;
         ties = shift == 0 ? need : 0u;
         break;
       }
@@ -585,13 +644,15 @@ __global__ void __launch_bounds__(kPickMax)
         each([&](unsigned y) {
           if (y >= lo && y <= hi) sm.few[atomicAdd(&sm.n_few, 1u)] = y;
         });
+        if (tid < 4) sm.few[in_bin + tid] = 0u;  // below every key
         __syncthreads();
         for (unsigned c = tid; c < in_bin; c += T) {
           const unsigned y = sm.few[c];
           unsigned above = 0, same = 0;
-          for (unsigned o = 0; o < in_bin; ++o) {
-            above += sm.few[o] > y ? 1u : 0u;
-            same += sm.few[o] == y ? 1u : 0u;
+          for (unsigned o = 0; o < in_bin; o += 4) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(sm.few + o);
+            above += (q.x > y) + (q.y > y) + (q.z > y) + (q.w > y);
+            same += (q.x == y) + (q.y == y) + (q.z == y) + (q.w == y);
           }
           if (above < need && above + same >= need) {  // (equal keys agree)
             sm.edge = y;
@@ -678,15 +739,16 @@ cudaError_t bounds_t(const BoundsParams &p, dim3 grid, cudaStream_t stream) {
 
 template <int D, int S>
 cudaError_t scores_t(const PageScoreParams &p, unsigned grid, cudaStream_t stream) {
+  constexpr int kRing = kPScoreWarps * 2 * 16 * 4 * D;
   constexpr int kRows = S == 1 ? kPageScoreRows : kPageScoreRowsF32;
-  static_assert(kRows * pscore_row<D, S>() <= 227 * 1024, "shared memory");
-  const size_t smem = (size_t)((p.rows + 7) / 8 * 8) * pscore_row<D, S>();
+  static_assert(kRows * pscore_row<D, S>() + kRing <= 227 * 1024, "shared memory");
+  const size_t smem = (size_t)((p.rows + 7) / 8 * 8) * pscore_row<D, S>() + kRing;
   if (smem > 48 * 1024) {
     // always the most that any launch takes: launches in other host threads
     // may need more than this one
     const cudaError_t e = cudaFuncSetAttribute(
         page_scores_kernel<D, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-        kRows * pscore_row<D, S>());
+        kRows * pscore_row<D, S>() + kRing);
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(page_scores_kernel<D, S>, grid, 32 * kPScoreWarps, smem, stream, p);
