@@ -13,7 +13,9 @@
 // sequence by a binary search in the prefix sums); a cluster barrier separates
 // the releases from the takes, which may take what was just released, and the
 // reads of the old lengths from the writes of the new ones.
-// Bound by that chain: launch, lengths, scans, barriers.
+// Up to 1024 sequences are read and scanned once, by one scan for the three
+// sums; more go chunk by chunk.
+// Bound by that chain: launch, lengths, scan, table or stack, barriers.
 #include <cooperative_groups.h>
 
 #include <cstdint>
@@ -90,13 +92,154 @@ __device__ __forceinline__ Ask ask_of(const AssignParams &p, int b) {
   return a;
 }
 
-// The sequence (of a chunk) that holds entry i: the last with before <= i.
-__device__ __forceinline__ int holder(const u64 *before, u64 i) {
+// The sequence (of a chunk) that holds entry i: the last with before <= i;
+// span: a power of two, at least the chunk's sequences.
+__device__ __forceinline__ int holder(const u64 *before, u64 i, int span) {
   int lo = 0;
-#pragma unroll
-  for (int step = kAssignThreads / 2; step > 0; step >>= 1)
+  for (int step = span / 2; step > 0; step >>= 1)
     if (before[lo + step] <= i) lo += step;
   return lo;
+}
+
+// No stack of this size, or one that its pages do not fit: nothing changes.
+__device__ __forceinline__ void refuse(const AssignParams &p, u64 me, u64 all) {
+  if (me == 0) raise_assign(SVP_DEV_NO_PAGES);
+  for (u64 i = me; i < (u64)p.n_slots; i += all) p.slots[i] = -1;
+  if (p.offsets)
+    for (u64 i = me; i <= (u64)p.batch; i += all) p.offsets[i] = 0;
+}
+
+__device__ __forceinline__ int saturated(u64 x) {
+  return x > 0x7fffffffull ? 0x7fffffff : (int)x;
+}
+
+// The slot of a sequence's new position: its page is one it had, or take
+// `first` on and counting.
+__device__ __forceinline__ long long slot_of(const AssignParams &p, int b, int old_len,
+                                             int nth, u64 first, u64 top) {
+  const int pos = old_len + nth;
+  const int have = (int)(((long long)old_len + kBlockSize - 1) / kBlockSize);
+  const int k = pos / kBlockSize;
+  const int page = k < have ? p.block_table[(size_t)b * p.max_blocks + k]
+                            : p.free_pages[top - 1 - (first + (u64)(k - have))];
+  if (page >= 0 && page < p.num_blocks)
+    return (long long)page * kBlockSize + pos % kBlockSize;
+  raise_assign(SVP_DEV_BAD_BLOCK_ID);
+  return -1;
+}
+
+// Up to kAssignThreads sequences.
+struct AssignOne {
+  u64 sums[3][32];
+  u64 give[kAssignThreads], need[kAssignThreads], rows[kAssignThreads];
+  int old_len[kAssignThreads], want[kAssignThreads];
+  u64 given;
+  unsigned char served[kAssignThreads];
+};
+
+__global__ void __launch_bounds__(kAssignThreads)
+    assign_one_kernel(const AssignParams p, int span) {
+  __shared__ AssignOne sm;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const u64 me = (u64)rank * kAssignThreads + tid;
+  const u64 all = (u64)nc * kAssignThreads;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int F = *p.free_count;
+  const Ask a = ask_of(p, tid);
+  if (a.bad && rank == 0) raise_assign(SVP_DEV_BAD_SEQ_LEN);
+  // pages that come back, pages that are missing, new positions
+  u64 v[3] = {a.have > a.want ? (u64)(a.have - a.want) : 0,
+              a.want > a.have ? (u64)(a.want - a.have) : 0,
+              a.new_len > a.old_len ? (u64)(a.new_len - a.old_len) : 0};
+  const u64 mine[3] = {v[0], v[1], v[2]};
+  u64 sum[3];
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1)
+#pragma unroll
+    for (int x = 0; x < 3; ++x) {
+      const u64 y = __shfl_up_sync(0xffffffffu, v[x], off);
+      if (lane >= off) v[x] += y;
+    }
+  if (lane == 31) {
+#pragma unroll
+    for (int x = 0; x < 3; ++x) sm.sums[x][warp] = v[x];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int x = 0; x < 3; ++x) {
+    u64 y = sm.sums[x][lane];
+    const u64 own = y;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const u64 z = __shfl_up_sync(0xffffffffu, y, off);
+      if (lane >= off) y += z;
+    }
+    sum[x] = __shfl_sync(0xffffffffu, y, 31);
+    v[x] += __shfl_sync(0xffffffffu, y - own, warp) - mine[x];
+  }
+  const u64 R = sum[0], top = (u64)F + R;
+  if (F < 0 || (long long)top > p.capacity) {
+    refuse(p, me, all);  // (the whole cluster)
+    return;
+  }
+  // Sequences are served in order: from the first whose pages or slots run
+  // out, no sequence that needs any is.
+  const bool fits = (mine[1] == 0 || v[1] + mine[1] <= top) &&
+                    (mine[2] == 0 || !p.slots || v[2] + mine[2] <= (u64)p.n_slots);
+  sm.give[tid] = v[0];
+  sm.need[tid] = v[1];
+  sm.rows[tid] = v[2];
+  sm.old_len[tid] = a.old_len;
+  sm.want[tid] = a.want;
+  sm.served[tid] = fits;
+  if (tid == 0) sm.given = sum[1];
+  __syncthreads();
+  if (!fits && mine[1] > 0) atomicMin(&sm.given, v[1]);
+  if (!fits && rank == 0) raise_assign(SVP_DEV_NO_PAGES);
+  for (u64 i = me; i < R; i += all) {
+    const int s = holder(sm.give, i, span);
+    int32_t *const entry = p.block_table + (size_t)s * p.max_blocks + sm.want[s] +
+                           (i - sm.give[s]);
+    const int page = *entry;
+    if (page < 0 || page >= p.num_blocks) raise_assign(SVP_DEV_BAD_BLOCK_ID);
+    p.free_pages[(u64)F + i] = page;
+    *entry = -1;
+  }
+  // what was released may be taken, and every CTA has read the lengths
+  if (nc > 1) cluster.sync(); else __syncthreads();
+  const u64 given = sm.given;  // pages of the sequences served
+  for (u64 i = me; i < given; i += all) {
+    const int s = holder(sm.need, i, span);
+    const int have =
+        (int)(((long long)sm.old_len[s] + kBlockSize - 1) / kBlockSize);
+    const int page = p.free_pages[top - 1 - i];
+    if (page < 0 || page >= p.num_blocks) raise_assign(SVP_DEV_BAD_BLOCK_ID);
+    p.block_table[(size_t)s * p.max_blocks + have + (i - sm.need[s])] = page;
+  }
+  if (p.slots) {
+#pragma unroll 4
+    for (u64 i = me; i < (u64)p.n_slots; i += all) {
+      long long slot = -1;
+      if (i < sum[2]) {
+        const int s = holder(sm.rows, i, span);
+        if (sm.served[s])
+          slot = slot_of(p, s, sm.old_len[s], (int)(i - sm.rows[s]), sm.need[s], top);
+      }
+      p.slots[i] = slot;
+    }
+  }
+  if (rank != 0) return;
+  if (tid < p.batch) {
+    if (fits && !a.bad) p.seq_lens[tid] = a.new_len;
+    if (p.offsets) p.offsets[tid] = saturated(v[2]);
+  }
+  if (tid == 0) {
+    *p.free_count = (int)(top - given);
+    if (p.offsets) p.offsets[p.batch] = saturated(sum[2]);
+  }
 }
 
 __global__ void __launch_bounds__(kAssignThreads)
@@ -121,12 +264,7 @@ __global__ void __launch_bounds__(kAssignThreads)
     if (a.bad && leader) raise_assign(SVP_DEV_BAD_SEQ_LEN);
   }
   if (F < 0 || (long long)F + (long long)R > p.capacity) {
-    // no stack of this size, or one that its pages do not fit: do nothing
-    // (uniform over the cluster)
-    if (leader && tid == 0) raise_assign(SVP_DEV_NO_PAGES);
-    for (u64 i = me; i < (u64)p.n_slots; i += all) p.slots[i] = -1;
-    if (p.offsets)
-      for (u64 i = me; i <= (u64)p.batch; i += all) p.offsets[i] = 0;
+    refuse(p, me, all);  // (the whole cluster)
     return;
   }
   u64 done = 0;
@@ -139,7 +277,7 @@ __global__ void __launch_bounds__(kAssignThreads)
       sm.from[tid] = a.want;
       __syncthreads();
       for (u64 i = me; i < sum; i += all) {
-        const int s = holder(sm.before, i);
+        const int s = holder(sm.before, i, kAssignThreads);
         int32_t *const entry = p.block_table + (size_t)(b0 + s) * p.max_blocks +
                                sm.from[s] + (i - sm.before[s]);
         const int page = *entry;
@@ -170,17 +308,15 @@ __global__ void __launch_bounds__(kAssignThreads)
         (need == 0 || taken + n0 + need <= top) &&
         (rows == 0 || !p.slots || tokens + r0 + rows <= (u64)p.n_slots);
     const u64 g0 = scan(fits ? need : 0, sm.warp_sum[0], all_given);
-    if (leader && p.offsets && b0 + tid < p.batch) {
-      const u64 at = tokens + r0;
-      p.offsets[b0 + tid] = at > 0x7fffffffull ? 0x7fffffff : (int)at;
-    }
+    if (leader && p.offsets && b0 + tid < p.batch)
+      p.offsets[b0 + tid] = saturated(tokens + r0);
     if (leader && !fits) raise_assign(SVP_DEV_NO_PAGES);
     if (all_given > 0) {
       sm.before[tid] = g0;
       sm.from[tid] = a.have;
       __syncthreads();
       for (u64 i = me; i < all_given; i += all) {
-        const int s = holder(sm.before, i);
+        const int s = holder(sm.before, i, kAssignThreads);
         const int page = p.free_pages[top - 1 - (given + i)];
         if (page < 0 || page >= p.num_blocks) raise_assign(SVP_DEV_BAD_BLOCK_ID);
         p.block_table[(size_t)(b0 + s) * p.max_blocks + sm.from[s] +
@@ -196,22 +332,11 @@ __global__ void __launch_bounds__(kAssignThreads)
       __syncthreads();
       for (u64 i = me; i < all_rows; i += all) {
         if (tokens + i >= (u64)p.n_slots) break;
-        const int s = holder(sm.before, i);
-        long long slot = -1;
-        if (sm.served[s]) {
-          const int old = sm.from[s];
-          const int pos = old + (int)(i - sm.before[s]);
-          const int have = (int)(((long long)old + kBlockSize - 1) / kBlockSize);
-          const int k = pos / kBlockSize;
-          const int page =
-              k < have ? p.block_table[(size_t)(b0 + s) * p.max_blocks + k]
-                       : p.free_pages[top - 1 - (sm.first[s] + (k - have))];
-          if (page >= 0 && page < p.num_blocks)
-            slot = (long long)page * kBlockSize + pos % kBlockSize;
-          else
-            raise_assign(SVP_DEV_BAD_BLOCK_ID);
-        }
-        p.slots[tokens + i] = slot;
+        const int s = holder(sm.before, i, kAssignThreads);
+        p.slots[tokens + i] =
+            sm.served[s] ? slot_of(p, b0 + s, sm.from[s], (int)(i - sm.before[s]),
+                                   sm.first[s], top)
+                         : -1;
       }
       __syncthreads();
     }
@@ -227,8 +352,7 @@ __global__ void __launch_bounds__(kAssignThreads)
   if (!leader) return;
   if (tid == 0) {
     *p.free_count = (int)(top - given);
-    if (p.offsets)
-      p.offsets[p.batch] = tokens > 0x7fffffffull ? 0x7fffffff : (int)tokens;
+    if (p.offsets) p.offsets[p.batch] = saturated(tokens);
   }
   taken = tokens = 0;
   for (int b0 = 0; b0 < p.batch; b0 += kAssignThreads) {
@@ -250,8 +374,10 @@ __global__ void __launch_bounds__(kAssignThreads)
 }  // namespace
 
 cudaError_t launch_assign_pages(const AssignParams &p, cudaStream_t stream) {
-  // one CTA for a decode step's few entries, eight for prompts
-  const int nc = p.n_slots > 8 * kAssignThreads ? 8 : 1;
+  // one CTA for a decode step's few entries, eight where there may be many
+  const bool many = p.n_slots > 4 * kAssignThreads ||
+                    (!p.slots && (long long)p.batch * p.max_blocks > 64 * kAssignThreads);
+  const int nc = many ? 8 : 1;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -265,7 +391,10 @@ cudaError_t launch_assign_pages(const AssignParams &p, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, assign_pages_kernel, p);
+  if (p.batch > kAssignThreads) return cudaLaunchKernelEx(&cfg, assign_pages_kernel, p);
+  int span = 1;
+  while (span < p.batch) span *= 2;
+  return cudaLaunchKernelEx(&cfg, assign_one_kernel, p, span);
 }
 
 cudaError_t read_status_assign(cudaStream_t s, unsigned *flags) {

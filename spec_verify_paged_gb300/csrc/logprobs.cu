@@ -1,23 +1,22 @@
 // logprobs.cu -- log probabilities of given tokens, their ranks, the rows'
 // entropies and most likely alternatives (token_logprobs, include/svp.h).
 //
-// With z = x / T over the allowed tokens of a row, m = max x and
-// S = sum exp((x - m) / T):
-//   log p(t)  = (x_t - m) / T - ln S
-//   entropy   = ln S - (1 / S) sum ((x - m) / T) exp((x - m) / T)
-// so one maximum and one pass of exponentials give everything but the order.
+// With z = x / T over the allowed tokens of a row, r any logit near the largest
+// and S = sum exp((x - r) / T):
+//   log p(t)  = (x_t - r) / T - ln S
+//   entropy   = ln S - (1 / S) sum ((x - r) / T) exp((x - r) / T)
+// A thread moves its r only when a logit exceeds it by a factor 2^8 of
+// probability, so one pass of exponentials gives everything but the order.
 //
 // A cluster of 1 to 8 CTAs takes a row, each a part of it that it copies into
-// shared memory (what is not allowed becomes -inf there), so the logits are
-// read once; a thread reads only what it copied, so no barrier is needed in
-// between.  What bounds it for long rows is instructions: about eight an
-// element with the exponential.  So what can be done on pairs of bf16 is (the
-// maximum, the count of the tokens ahead), and one test of a thread's or a
-// vector's maximum rules out most of them as alternatives.  Loops are short:
-// the row in registers, with everything unrolled, waited for instructions (512
-// rows of 131,072 bf16: 148 us).  Each CTA's sums are relative to its own
-// maximum; they meet in the first CTA's shared memory at the end, by one
-// cluster barrier.
+// shared memory, so the logits are read once; a thread reads only what it
+// copied, so no barrier is needed in between.  What bounds it for long rows is
+// instructions, about nine an element (with a mask eleven): what can be done
+// on pairs of bf16 is (the maximum, the count of the tokens ahead), and few
+// vectors are looked at again for the alternatives.  Loops are short: the row
+// in registers, with everything unrolled, waited for instructions (512 rows of
+// 131,072 bf16: 148 us; two passes out of shared memory, 97).  The CTAs' sums
+// meet in the first CTA's shared memory at the end, by one cluster barrier.
 //
 // The alternatives: the k-th largest of the threads' own largest values bounds
 // the k-th largest of all from below, and few elements reach that bound; they
@@ -60,19 +59,23 @@ struct Found {
   unsigned key;
   int token;
 };
+// Sums of weights w = 2^d and of w d, d = (x - r) / T in units of log 2.
+struct LpSums {
+  float r, s, sz;
+};
 struct LpPart {            // one CTA's share of the row's results
-  float top, c;            // its largest logit, and what sums are relative to:
-  float sum, sum_z;        // c in units of log 2, or (huge) the logit itself
-  unsigned ahead, n_best, key, huge;
+  LpSums sums;
+  unsigned ahead, n_best, key;
 };
 template <int W>
 struct LpShared {
   Found found[kLpFound];
   Found best[kLpCluster][kMaxTop];  // in the first CTA: every CTA's, in order
   LpPart part[kLpCluster];          // in the first CTA
-  float warp_f[W][2];
+  LpSums warp_f[W];
   unsigned warp_u[2][W];
-  unsigned n_found;
+  unsigned n_found, n_high;
+  unsigned short high[32 * W];      // threads that reach the bound
 };
 
 // Ascending order of logits; NaN above everything, -0 as +0.  0: no logit
@@ -127,6 +130,7 @@ template <int DT>
 struct Vec {
   static constexpr int N = DT == SVP_F32 ? 4 : 8;
   static constexpr uint32_t kNone = DT == SVP_F32 ? 0xff800000u : 0xff80ff80u;
+  static constexpr uint32_t kLowest = DT == SVP_F32 ? 0xff7fffffu : 0xff7f0000u;
   static __device__ __forceinline__ uint4 none() {
     return make_uint4(kNone, kNone, kNone, kNone);
   }
@@ -169,6 +173,17 @@ struct Vec {
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
+
+// Two parts' sums, relative to the larger reference.
+__device__ __forceinline__ LpSums join(const LpSums &a, const LpSums &b, float sc) {
+  LpSums o;
+  o.r = fmaxf(a.r, b.r);
+  const float da = fmaxf((a.r - o.r) * sc, -1e4f), db = fmaxf((b.r - o.r) * sc, -1e4f);
+  const float fa = ex2(da), fb = ex2(db);
+  o.s = fmaf(a.s, fa, b.s * fb);
+  o.sz = fmaf(a.sz, fa, a.s * (da * fa)) + fmaf(b.sz, fb, b.s * (db * fb));
+  return o;
+}
 
 // The next value above x (x below +inf), as the type has it.
 template <int DT>
@@ -257,47 +272,26 @@ __global__ void __launch_bounds__(kLpThreads)
     extra = make_uint4(w[0], w[1], w[2], w[3]);
   }
 
-  // ---- the largest logit ----
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-  float big = V::top(extra);
-  if (!allowed) {
-#pragma unroll 4
-    for (int i = tid; i < n_vec; i += T) big = max_nan_f(big, V::top(held[i]));
-  } else if (shift == 0) {  // a vector's bits lie in one byte
-    const unsigned char *const bytes = reinterpret_cast<const unsigned char *>(allowed);
-#pragma unroll 4
-    for (int i = tid; i < n_vec; i += T) {
-      const uint32_t y = __ldg(bytes + (v0 + i) * VEC / 8);
-      const uint4 v = V::masked(held[i], VEC == 8 ? y : y >> (4 * ((v0 + i) & 1)));
-      held[i] = v;
-      big = max_nan_f(big, V::top(v));
+  // this thread's vector i as it counts: with -inf for what is not allowed
+  auto fetch = [&](int i) {
+    const uint4 v = held[i];
+    if (!allowed) return v;
+    if (shift == 0) {  // a vector's bits lie in one byte
+      const uint32_t y = __ldg(reinterpret_cast<const unsigned char *>(allowed) +
+                               (v0 + i) * VEC / 8);
+      return V::masked(v, VEC == 8 ? y : y >> (4 * ((v0 + i) & 1)));
     }
-  } else {
-#pragma unroll 4
-    for (int i = tid; i < n_vec; i += T) {
-      const int t0 = t00 + i * VEC, w = t0 >> 5;
-      const uint32_t w0 = __ldg(allowed + w);
-      const uint32_t w1 = (t0 & 31) + VEC > 32 ? __ldg(allowed + w + 1) : 0u;
-      const uint4 v = V::masked(held[i], __funnelshift_r(w0, w1, t0 & 31));
-      held[i] = v;
-      big = max_nan_f(big, V::top(v));
-    }
-  }
-  const unsigned mine = logit_key(big);  // this thread's largest key
-  if (tid == 0) sm.n_found = 0;
-  const unsigned wm = __reduce_max_sync(kFull, mine);
-  if (lane == 0) sm.warp_u[0][warp] = wm;
-  __syncthreads();
-  const unsigned top_key =
-      __reduce_max_sync(kFull, lane < W ? sm.warp_u[0][lane] : 0u);
-  const float top = top_key ? key_logit(top_key) : 0.f;
-  const bool odd = !(top < INFINITY);  // NaN or +inf: no probabilities
+    const int t0 = t00 + i * VEC, w = t0 >> 5;
+    const uint32_t w0 = __ldg(allowed + w);
+    const uint32_t w1 = (t0 & 31) + VEC > 32 ? __ldg(allowed + w + 1) : 0u;
+    return V::masked(v, __funnelshift_r(w0, w1, t0 & 31));
+  };
 
   // f(key, token) of every logit of this thread, for rare rows
   auto each = [&](auto f) {
 #pragma unroll 1
     for (int i = tid; i < n_vec; i += T) {
-      const uint4 v = held[i];
+      const uint4 v = fetch(i);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) f(logit_key(V::value(v, e)), t00 + i * VEC + e);
     }
@@ -307,32 +301,37 @@ __global__ void __launch_bounds__(kLpThreads)
     }
   };
 
-  // ---- sums, and how many are ahead of the token ----
+  // ---- sums, the largest logit, and how many are ahead of the token ----
   // Tokens before it are ahead with a logit that is not smaller, those after
   // it with a larger one: not below one of two bounds.  The vector that holds
   // the token counts as after; thread 0 of the cluster adds the equals in it.
-  // The distance to the maximum in units of log 2 is x sc - c, c = top sc: one
-  // instruction, exact but for c's rounding, which shifts all distances alike
-  // and so cancels as long as c is used throughout.  With huge logits c is no
-  // longer fine enough (or infinite): there it is (x - top) sc, as at
-  // temperatures beyond 1e30.
-  const bool huge = !(fabsf(top * p.sc) < 0x1p20f) || p.sc < 1e-30f;
-  const float c = huge ? 0.f : top * p.sc;
-  // far below what counts, and finite
-  const float low = top - 400.f / p.sc;
-  float s = 0.f, sz = 0.f;
-  unsigned ahead = 0;
-  auto distance = [&](float x) { return huge ? (x - top) * p.sc : fmaf(x, p.sc, -c); };
-  auto add_up = [&](float d) {
-    const float w = ex2(d);
-    s += w;
-    sz = fmaf(w, d, sz);
-  };
   const bool ranked = p.ranks && kt != 0u;
   const bool plain_rank = ranked && xt < INFINITY;
   const float up = next_up<DT>(xt);
+  unsigned ahead = 0;
   uint32_t n2 = 0u;  // counts of two halves: exact in bf16 up to 256
-  auto count = [&](const uint4 &v, int t0) {
+  float big = -INFINITY;
+  LpSums a = {__uint_as_float(V::kLowest), 0.f, 0.f};
+  const float margin = fminf(8.f / p.sc, 1e30f);
+  auto take = [&](const uint4 &v, int t0) {
+    const float top = V::top(v);
+    big = max_nan_f(big, top);
+    if (top > a.r + margin) {
+      const float d = fmaxf((a.r - top) * p.sc, -1e4f), f = ex2(d);
+      a.sz = fmaf(a.s, d, a.sz) * f;
+      a.s *= f;
+      a.r = top;
+    }
+    if (top == -INFINITY) return;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      // (far below what counts it stays finite)
+      const float d = fmaxf((V::value(v, e) - a.r) * p.sc, -1e4f);
+      const float w = ex2(d);
+      a.s += w;
+      a.sz = fmaf(w, d, a.sz);
+    }
+    if (!plain_rank) return;
     const float at = t0 + VEC <= token ? xt : up;
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     if constexpr (DT == SVP_F32) {
@@ -355,36 +354,19 @@ __global__ void __launch_bounds__(kLpThreads)
       n2 = 0u;
     }
   };
-  if (!huge) {
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll 1
-    for (int i0 = tid; i0 < n_vec; i0 += 32 * T) {  // at most 128 in a half
+  for (int i0 = tid; i0 < n_vec; i0 += 32 * T) {  // at most 128 in a half
+    const int end = min(n_vec, i0 + 32 * T);
 #pragma unroll 2
-      for (int i = i0; i < min(n_vec, i0 + 32 * T); i += T) {
-        const uint4 v = held[i];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          add_up(fmaf(fmaxf(V::value(v, e), low), p.sc, -c));
-        if (plain_rank) count(v, t00 + i * VEC);
-      }
-      pour();
-    }
-  } else {
-#pragma unroll 1
-    for (int i = tid; i < n_vec; i += T) {
-      const uint4 v = held[i];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        add_up(fmaxf((V::value(v, e) - top) * p.sc, -1e4f));
-      if (plain_rank) count(v, t00 + i * VEC);
-      pour();
-    }
-  }
-  if (has_extra) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) add_up(fmaxf(distance(V::value(extra, e)), -1e4f));
-    if (plain_rank) count(extra, warp == 0 ? -shift : extra0);
+    for (int i = i0; i < end; i += T) take(fetch(i), t00 + i * VEC);
     pour();
   }
+  if (has_extra) {
+    take(extra, warp == 0 ? -shift : extra0);
+    pour();
+  }
+  const unsigned mine = logit_key(big);  // this thread's largest key
   if (plain_rank && rank == 0 && tid == 0) {
     const int from = (token + shift) / VEC * VEC - shift;
     for (int t = max(from, 0); t < token; ++t)
@@ -396,14 +378,19 @@ __global__ void __launch_bounds__(kLpThreads)
     });
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
-    s += __shfl_xor_sync(kFull, s, off);
-    sz += __shfl_xor_sync(kFull, sz, off);
+    const LpSums o = {__shfl_xor_sync(kFull, a.r, off), __shfl_xor_sync(kFull, a.s, off),
+                      __shfl_xor_sync(kFull, a.sz, off)};
+    a = join(a, o, p.sc);
   }
+  const unsigned wm = __reduce_max_sync(kFull, mine);
   if (lane == 0) {
-    sm.warp_f[warp][0] = s;
-    sm.warp_f[warp][1] = sz;
+    sm.warp_f[warp] = a;
+    sm.warp_u[0][warp] = wm;
   }
-  const unsigned n_ahead = lp_sum(ahead, sm, 1);  // its barrier serves both
+  if (tid == 0) sm.n_found = sm.n_high = 0;
+  const unsigned n_ahead = lp_sum(ahead, sm, 1);  // its barrier serves all
+  const unsigned top_key =
+      __reduce_max_sync(kFull, lane < W ? sm.warp_u[0][lane] : 0u);
 
   // ---- this CTA's alternatives ----
   unsigned keep = 0;
@@ -438,19 +425,22 @@ __global__ void __launch_bounds__(kLpThreads)
         sm.found[at].token = t;
       }
     };
-    if (mine >= edge) {
-      auto some = [&](const uint4 &v, int t0) {
-        if (logit_key(V::top(v)) < edge) return;
+    auto some = [&](const uint4 &v, int t0) {
+      if (logit_key(V::top(v)) < edge) return;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const unsigned x = logit_key(V::value(v, e));
-          if (x >= edge) add(x, t0 + e);
-        }
-      };
-#pragma unroll 1
-      for (int i = tid; i < n_vec; i += T) some(held[i], t00 + i * VEC);
-      if (has_extra) some(extra, extra0);
-    }
+      for (int e = 0; e < VEC; ++e) {
+        const unsigned x = logit_key(V::value(v, e));
+        if (x >= edge) add(x, t0 + e);
+      }
+    };
+    // the vectors of the threads that reach it, a warp to a thread
+    if (mine >= edge) sm.high[atomicAdd(&sm.n_high, 1u)] = (unsigned short)tid;
+    __syncthreads();
+    const unsigned n_high = sm.n_high;
+    for (unsigned x = warp; x < n_high; x += W)
+      for (int i = sm.high[x] + lane * T; i < n_vec; i += 32 * T)
+        some(fetch(i), t00 + i * VEC);
+    if (has_extra && mine >= edge) some(extra, extra0);
     __syncthreads();
     unsigned n = sm.n_found;
     if (n > kLpFound) {
@@ -498,17 +488,10 @@ __global__ void __launch_bounds__(kLpThreads)
   }
   if (tid == 0) {
     LpPart part;
-    part.top = top;
-    part.c = c;
-    part.huge = huge;
     part.key = top_key;
-    part.sum = part.sum_z = 0.f;
-    for (int w = 0; w < W; ++w) {
-      part.sum += sm.warp_f[w][0];
-      part.sum_z += sm.warp_f[w][1];
-    }
-    if (odd) part.sum = NAN;
-    if (top_key == 0u) part.sum = part.sum_z = 0.f;
+    part.sums = sm.warp_f[0];
+    for (int w = 1; w < W; ++w) part.sums = join(part.sums, sm.warp_f[w], p.sc);
+    if (top_key > logit_key(3.402823466e38f)) part.sums.s = NAN;  // +inf or NaN
     part.ahead = n_ahead;
     part.n_best = keep;
     LpPart *const to =
@@ -526,40 +509,19 @@ __global__ void __launch_bounds__(kLpThreads)
 
   // ---- the row's results ----
   unsigned row_key = 0, n_before = 0;
-  int best_part = 0;
+  LpSums all = sm.part[0].sums;
   for (int r = 0; r < nc; ++r) {
-    if (sm.part[r].key > row_key) {
-      row_key = sm.part[r].key;
-      best_part = r;
-    }
+    row_key = max(row_key, sm.part[r].key);
     n_before += sm.part[r].ahead;
+    if (r > 0) all = join(all, sm.part[r].sums, p.sc);
   }
-  // everything relative to what the part with the largest logit is
-  const float peak = row_key ? sm.part[best_part].top : 0.f;
-  const bool far = sm.part[best_part].huge;
-  const float origin = sm.part[best_part].c;
-  float total = 0.f, total_z = 0.f;
-  for (int r = 0; r < nc; ++r) {
-    const LpPart &o = sm.part[r];
-    if (o.key == 0u) continue;  // nothing there
-    // from what its sums are relative to, to that, in units of log 2
-    const float d = far      ? (o.top - peak) * p.sc - (o.huge ? 0.f : o.top * p.sc - o.c)
-                    : o.huge ? fmaf(o.top, p.sc, -origin)
-                             : o.c - origin;
-    const float near = fmaxf(d, -1e4f);
-    const float f = ex2(near);
-    total = fmaf(o.sum, f, total);
-    total_z = fmaf(fmaf(o.sum, near, o.sum_z), f, total_z);
-  }
-  const float ln = logf(total);
-  auto log_p = [&](float x) {
-    return (far ? (x - peak) * p.inv_t : fmaf(x, p.sc, -origin) * kLn2) - ln;
-  };
+  const float ln = logf(all.s);
+  auto log_p = [&](float x) { return (x - all.r) * p.inv_t - ln; };
   if (tid == 0) {
     // a row that allows nothing has no probabilities: -inf, entropy 0
-    p.logprobs[row] = total != total ? NAN : kt == 0u ? -INFINITY : log_p(xt);
+    p.logprobs[row] = all.s != all.s ? NAN : kt == 0u ? -INFINITY : log_p(xt);
     if (p.entropy)
-      p.entropy[row] = row_key == 0u ? 0.f : ln - total_z / total * kLn2;
+      p.entropy[row] = row_key == 0u ? 0.f : ln - all.sz / all.s * kLn2;
     if (p.ranks) p.ranks[row] = kt == 0u ? -1 : (int)n_before;
   }
   if (p.n_top > 0) {

@@ -343,10 +343,12 @@ __global__ void __launch_bounds__(32 * kPScoreWarps)
   extern __shared__ __align__(16) unsigned char sq[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const unsigned unit = blockIdx.x / (unsigned)p.chunks;
-  const int chunk = (int)(blockIdx.x - unit * (unsigned)p.chunks);
-  const int b = (int)(unit / (unsigned)p.num_kv_heads);
-  const int head = (int)(unit - (unsigned)b * (unsigned)p.num_kv_heads);
+  // heads side by side: their bounds of a page lie next to one another
+  const unsigned bc = blockIdx.x / (unsigned)p.num_kv_heads;
+  const int head = (int)(blockIdx.x - bc * (unsigned)p.num_kv_heads);
+  const int b = (int)(bc / (unsigned)p.chunks);
+  const int chunk = (int)(bc - (unsigned)b * (unsigned)p.chunks);
+  const size_t unit = (size_t)b * p.num_kv_heads + head;
   pdl_wait();
   pdl_launch_dependents();
   const int L = p.seq_lens[b];
@@ -358,7 +360,7 @@ __global__ void __launch_bounds__(32 * kPScoreWarps)
   const int tiles = (p.max_blocks + 15) / 16;
   const int first = chunk * p.tiles_per_cta;
   const int last = min(first + p.tiles_per_cta, tiles);
-  float *const out = p.scores + (size_t)unit * p.max_blocks;
+  float *const out = p.scores + unit * p.max_blocks;
   const int32_t *const table = p.block_table + (size_t)b * p.max_blocks;
   // lane r < 16: the physical page of page r of a tile, or -1
   auto page_ids = [&](int tile) {
@@ -774,7 +776,7 @@ cudaError_t launch_page_scores(PageScoreParams p, int sms, cudaStream_t stream) 
   const long long units = (long long)p.batch * p.num_kv_heads;
   // a warp's tiles one after another, so that the query rows are laid out
   // once for several: but at least eight CTAs to an SM while there are tiles
-  long long per = tiles * units / ((long long)sms * 6 * kPScoreWarps);
+  long long per = tiles * units / ((long long)sms * 3 * kPScoreWarps);
   per = per < 1 ? 1 : per > 8 ? 8 : per;
   per *= kPScoreWarps;
   const long long chunks = (tiles + per - 1) / per;
