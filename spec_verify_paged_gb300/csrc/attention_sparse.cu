@@ -76,9 +76,9 @@ struct SpShape {
   static constexpr bool Q_SHARED = DT != SVP_F32 && NT > 2;
   static constexpr int QROW = 4 * D + 32;
   static constexpr int Q = DT == SVP_F32 ? ROWS * QROW + kSpWarps * ROWS * kBlockSize * 4
-                           : Q_SHARED    ? NT * (D / 16) * 32 * 8
+                           : Q_SHARED    ? NT * ((D / 16) * 256 + 32)
                                          : 0;
-  static constexpr int SMEM = RING + LIST + 64 + Q;
+  static constexpr int SMEM = RING + LIST + 64 + (Q > ROWS * 8 ? Q : ROWS * 8);
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes) {
@@ -243,75 +243,97 @@ struct WarpMma {
                                 : (D / 8) * g + 2 * i + h;
   }
 
-  // shared: the unit's query fragments (a barrier follows)
-  __device__ __forceinline__ void start(const SparseParams &p, int b, int head, int L,
-                                        int row0, unsigned char *shared, int warp,
-                                        int lane) {
+  // The B fragments of tile n and their rows' factor: lane (g, t) holds row
+  // 8 n + g.
+  __device__ __forceinline__ float fragments(const SparseParams &p, int b, int head,
+                                             int row0, int n, uint2 (&w)[KS], int lane) {
     const int g = lane >> 2, t = lane & 3;
+    const int row = row0 + 8 * n + g;
+    const bool there = row < p.rows;
+    const int r = there ? row : 0;
+    const uint16_t *src = static_cast<const uint16_t *>(p.q) +
+                          (((size_t)b * p.q_len + r / p.group) * p.num_q_heads +
+                           (size_t)head * p.group + r % p.group) * D;
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int ks = 0; ks < KS; ++ks) {
+      if constexpr (DT == SVP_BF16) {
+        w[ks].x = *reinterpret_cast<const uint32_t *>(src + 16 * ks + 2 * t);
+        w[ks].y = *reinterpret_cast<const uint32_t *>(src + 16 * ks + 2 * t + 8);
+      } else {
+        w[ks] = *reinterpret_cast<const uint2 *>(src + (D / 4) * t + 4 * ks);
+      }
+    }
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+    for (int ks = 0; ks < KS; ++ks)
+      if (!there) w[ks] = make_uint2(0u, 0u);
+    float f = p.qscale;
+    if constexpr (DT != SVP_BF16) {
+      float top = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const uint32_t x[2] = {w[ks].x, w[ks].y};
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[y] << 16)),
+                                 fabsf(__uint_as_float(x[y] & 0xffff0000u))));
+      }
+      top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+      const int e = q_exponent(top);
+      const float up = pow2i(14 - e);
+      f *= pow2i(e - 14);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+        w[ks] = make_uint2(pack_h2(__uint_as_float(w[ks].x << 16) * up,
+                                   __uint_as_float(w[ks].x & 0xffff0000u) * up),
+                           pack_h2(__uint_as_float(w[ks].y << 16) * up,
+                                   __uint_as_float(w[ks].y & 0xffff0000u) * up));
+    }
+    return f;
+  }
+
+  // Before a barrier: the unit's query fragments, where they are shared a tile
+  // to a warp, and their rows' factors behind them.
+  __device__ __forceinline__ void load_query(const SparseParams &p, int b, int head,
+                                             int row0, unsigned char *shared, int warp,
+                                             int lane) {
+    if constexpr (Q_SHARED) {
+      for (int n = warp; n < NT; n += kSpWarps) {
+        uint2 w[KS];
+        const float f = fragments(p, b, head, row0, n, w, lane);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+          reinterpret_cast<uint2 *>(shared)[(n * KS + ks) * 32 + lane] = w[ks];
+        if (lane % 4 == 0)
+          reinterpret_cast<float *>(shared + NT * KS * 256)[8 * n + lane / 4] = f;
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float f = fragments(p, b, head, row0, n, q[n], lane);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)  // this lane's rows of S^T: 2 t + e
+          factor[n][e] = __shfl_sync(kFull, f, 4 * (2 * (lane & 3) + e));
+      }
+    }
+  }
+
+  // After it.
+  __device__ __forceinline__ void start(const SparseParams &p, int L, int row0,
+                                        const unsigned char *shared, int lane) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][n][e] = 0.f;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      // B fragments: lane (g, t) holds row 8 n + g
-      const int row = row0 + 8 * n + g;
-      const bool there = row < p.rows;
-      const int r = there ? row : 0;
-      const uint16_t *src = static_cast<const uint16_t *>(p.q) +
-                            (((size_t)b * p.q_len + r / p.group) * p.num_q_heads +
-                             (size_t)head * p.group + r % p.group) * D;
-      uint2 w[KS];
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        if constexpr (DT == SVP_BF16) {
-          w[ks].x = *reinterpret_cast<const uint32_t *>(src + 16 * ks + 2 * t);
-          w[ks].y = *reinterpret_cast<const uint32_t *>(src + 16 * ks + 2 * t + 8);
-        } else {
-          w[ks] = *reinterpret_cast<const uint2 *>(src + (D / 4) * t + 4 * ks);
-        }
-        if (!there) w[ks] = make_uint2(0u, 0u);
-      }
-      float f = p.qscale;
-      if constexpr (DT != SVP_BF16) {
-        float top = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const uint32_t x[2] = {w[ks].x, w[ks].y};
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[y] << 16)),
-                                   fabsf(__uint_as_float(x[y] & 0xffff0000u))));
-        }
-        top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
-        const int e = q_exponent(top);
-        const float up = pow2i(14 - e);
-        f *= pow2i(e - 14);
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-          w[ks] = make_uint2(pack_h2(__uint_as_float(w[ks].x << 16) * up,
-                                     __uint_as_float(w[ks].x & 0xffff0000u) * up),
-                             pack_h2(__uint_as_float(w[ks].y << 16) * up,
-                                     __uint_as_float(w[ks].y & 0xffff0000u) * up));
-      }
-#pragma unroll
       for (int e = 0; e < 2; ++e) {
-        // the factor of this lane's rows of S^T: 2 t + e, held by lanes g = that
-        factor[n][e] = __shfl_sync(kFull, f, 4 * (2 * t + e));
+        if constexpr (Q_SHARED)
+          factor[n][e] = reinterpret_cast<const float *>(
+              shared + NT * KS * 256)[8 * n + 2 * (lane & 3) + e];
         ref[n][e] = kSpNoRef;
         sum[n][e] = 0.f;
-      }
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        if constexpr (Q_SHARED) {
-          if (n % kSpWarps == warp)
-            reinterpret_cast<uint2 *>(shared)[(n * KS + ks) * 32 + lane] = w[ks];
-        } else {
-          q[n][ks] = w[ks];
-        }
       }
     }
     const int base = L - p.q_len;
@@ -581,17 +603,10 @@ struct WarpF32 {
     return 16 * c + (c >= D / 8 ? 16 : 0);
   }
 
-  // shared: the unit's query rows (a barrier follows), then the warps' weights
-  __device__ __forceinline__ void start(const SparseParams &p, int b, int head, int L,
-                                        int row0, unsigned char *shared, int warp,
-                                        int lane) {
-    factor = p.qscale;
-#pragma unroll
-    for (int r = 0; r < RPW; ++r) {
-      o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-      ref[r] = kSpNoRef;
-      sum[r] = 0.f;
-    }
+  // Before a barrier: the unit's query rows; behind them the warps' weights.
+  __device__ __forceinline__ void load_query(const SparseParams &p, int b, int head,
+                                             int row0, unsigned char *shared, int warp,
+                                             int lane) {
     for (int x = warp * 32 + lane; x < RPW * (D / 4); x += kSpThreads) {
       const int r = x / (D / 4), c = x % (D / 4), row = row0 + r;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -601,6 +616,17 @@ struct WarpF32 {
             (((size_t)b * p.q_len + row / p.group) * p.num_q_heads +
              (size_t)head * p.group + row % p.group) * D)[c];
       *reinterpret_cast<float4 *>(shared + r * QROW + q_at(c)) = v;
+    }
+  }
+
+  __device__ __forceinline__ void start(const SparseParams &p, int L, int row0,
+                                        const unsigned char *, int) {
+    factor = p.qscale;
+#pragma unroll
+    for (int r = 0; r < RPW; ++r) {
+      o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+      ref[r] = kSpNoRef;
+      sum[r] = 0.f;
     }
     const int base = L - p.q_len;
     t_all = p.tree_mask ? base - 1 : base + min(row0, p.rows - 1) / p.group;
@@ -736,51 +762,56 @@ __global__ void __launch_bounds__(kSpThreads)
   const int head = (int)(bh - (unsigned)b * (unsigned)p.num_kv_heads);
   pdl_wait();
   pdl_launch_dependents();
-  const int L = p.seq_lens[b];
-  if (L < p.q_len || L > (long long)p.max_blocks * kBlockSize) {
-    if (tid == 0) raise_sparse(SVP_DEV_BAD_SEQ_LEN);
-    return;  // the whole cluster
-  }
   const int32_t *const entries = p.pages + (size_t)bh * p.n_select;
   const int32_t *const table = p.block_table + (size_t)b * p.max_blocks;
   const int lo = (int)((long long)p.n_select * rank / nc);
   const int hi = (int)((long long)p.n_select * (rank + 1) / nc);
-  const int n_pages = (int)(((long long)L + kBlockSize - 1) / kBlockSize);
-
-  typename WarpOf<DT, D, NT>::T st;
-  const int row0 = rb * RB;
-  st.start(p, b, head, L, row0, shared, warp, lane);
-  const uint32_t ring = smem_u32(smem) + warp * S::WARP;
-
-  for (int at = lo; at < hi; at += kListCap) {
-    // the listed pages of this round, holes left out
-    constexpr int PER = kListCap / kSpThreads;
-    int page[PER], phys[PER];
+  // entries of the list that this thread looks up in a round
+  constexpr int PER = kListCap / kSpThreads;
+  int page[PER];
+  auto look = [&](int at) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int x = at + i * kSpThreads + tid;
       page[i] = x < hi ? entries[x] : -1;
     }
+  };
+  look(lo);
+  const int L = p.seq_lens[b];
+  if (L < p.q_len || L > (long long)p.max_blocks * kBlockSize) {
+    if (tid == 0) raise_sparse(SVP_DEV_BAD_SEQ_LEN);
+    return;  // the whole cluster
+  }
+  const int n_pages = (int)(((long long)L + kBlockSize - 1) / kBlockSize);
+
+  typename WarpOf<DT, D, NT>::T st;
+  const int row0 = rb * RB;
+  const uint32_t ring = smem_u32(smem) + warp * S::WARP;
+
+  for (int at = lo; at < hi || at == lo; at += kListCap) {
+    // the listed pages of this round, holes left out
+    int phys[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       phys[i] = -1;
       if (page[i] >= n_pages) raise_sparse(SVP_DEV_BAD_BLOCK_ID);
-      if (page[i] >= 0 && page[i] < n_pages) {
-        phys[i] = table[page[i]];
-        if (phys[i] < 0 || phys[i] >= p.num_blocks) {
-          raise_sparse(SVP_DEV_BAD_BLOCK_ID);
-          phys[i] = -1;
-        }
-      }
+      if (page[i] >= 0 && page[i] < n_pages) phys[i] = table[page[i]];
     }
-    int count = 0;
-    __syncthreads();  // the list of the round before is read
+    if (at == lo) st.load_query(p, b, head, row0, shared, warp, lane);
+    else __syncthreads();  // the list of the round before is read
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
+      const bool listed = page[i] >= 0 && page[i] < n_pages;
+      if (listed && (phys[i] < 0 || phys[i] >= p.num_blocks)) {
+        raise_sparse(SVP_DEV_BAD_BLOCK_ID);
+        phys[i] = -1;
+      }
       const unsigned m = __ballot_sync(kFull, phys[i] >= 0);
       if (lane == 0) counts[i * kSpWarps + warp] = __popc(m);
     }
     __syncthreads();
+    if (at == lo) st.start(p, L, row0, shared, lane);
+    int count = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const unsigned m = __ballot_sync(kFull, phys[i] >= 0);
@@ -792,6 +823,7 @@ __global__ void __launch_bounds__(kSpThreads)
         count += counts[i * kSpWarps + w];
       }
     }
+    if (at + kListCap < hi) look(at + kListCap);
     __syncthreads();
     // this warp's pages: every fourth
     const int n_mine = (count - warp + kSpWarps - 1) / kSpWarps;
@@ -817,43 +849,19 @@ __global__ void __launch_bounds__(kSpThreads)
     cp_wait<0>();
   }
 
-  // ---- the warps' results meet ----
+  // ---- the warps' results meet, then the CTAs' ----
   __syncthreads();  // the rings are free
   constexpr int RR = S::RES_ROW / 4;
   float *const res = reinterpret_cast<float *>(smem);
   float2 *const stat = reinterpret_cast<float2 *>(res + kSpWarps * RB * RR);
+  float2 *const both = reinterpret_cast<float2 *>(shared);  // (the queries are used)
   st.finish(res + warp * RB * RR, stat + warp * RB, lane);
-  if (nc > 1) cluster.sync(); else __syncthreads();
-  const int rows = min(RB, p.rows - rb * RB);
-  for (int x = rank * kSpThreads + tid; x < rows * (D / 4); x += nc * kSpThreads) {
-    const int r = x / (D / 4), c = x % (D / 4);
-    float top = kSpNoRef;
-    for (int k = 0; k < nc; ++k) {
-      const float2 *from = nc > 1 ? cluster.map_shared_rank(stat, k) : stat;
-#pragma unroll
-      for (int w = 0; w < kSpWarps; ++w) top = fmaxf(top, from[w * RB + r].x);
-    }
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    float total = 0.f;
-    for (int k = 0; k < nc; ++k) {
-      const float2 *from = nc > 1 ? cluster.map_shared_rank(stat, k) : stat;
-      const float *val = nc > 1 ? cluster.map_shared_rank(res, k) : res;
-#pragma unroll
-      for (int w = 0; w < kSpWarps; ++w) {
-        const float2 f = from[w * RB + r];
-        const float s = ex2(f.x - top);
-        const float4 y =
-            *reinterpret_cast<const float4 *>(val + (w * RB + r) * RR + 4 * c);
-        total = fmaf(f.y, s, total);
-        v.x = fmaf(y.x, s, v.x);
-        v.y = fmaf(y.y, s, v.y);
-        v.z = fmaf(y.z, s, v.z);
-        v.w = fmaf(y.w, s, v.w);
-      }
-    }
+  __syncthreads();
+  const int rows = min(RB, p.rows - row0);
+  auto put = [&](int r, int c, float4 v, float top, float total) {
     // a row that sees nothing: zeros, and a log-sum-exp of -inf
     const float inv = total == 0.f ? 0.f : p.v_scale / total;
-    const int row = rb * RB + r;
+    const int row = row0 + r;
     const size_t to = ((size_t)b * p.q_len + row / p.group) * p.num_q_heads +
                       (size_t)head * p.group + row % p.group;
     if constexpr (DT == SVP_F32) {
@@ -868,8 +876,66 @@ __global__ void __launch_bounds__(kSpThreads)
       constexpr float off = DT == SVP_F32 || DT == SVP_BF16 ? 0.f : 6.f;
       p.lse[to] = total == 0.f ? -INFINITY : (top - off + log2f(total)) * kLn2;
     }
+  };
+  for (int x = tid; x < rows * (D / 4); x += kSpThreads) {
+    const int r = x / (D / 4), c = x % (D / 4);
+    float2 f[kSpWarps];
+    float top = kSpNoRef, total = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSpWarps; ++w) {
+      f[w] = stat[w * RB + r];
+      top = fmaxf(top, f[w].x);
+    }
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kSpWarps; ++w) {
+      const float s = ex2(f[w].x - top);
+      const float4 y = *reinterpret_cast<const float4 *>(res + (w * RB + r) * RR + 4 * c);
+      total = fmaf(f[w].y, s, total);
+      v.x = fmaf(y.x, s, v.x);
+      v.y = fmaf(y.y, s, v.y);
+      v.z = fmaf(y.z, s, v.z);
+      v.w = fmaf(y.w, s, v.w);
+    }
+    if (nc == 1) {
+      put(r, c, v, top, total);
+    } else {  // in the place of the first warp's, which no one else reads
+      *reinterpret_cast<float4 *>(res + r * RR + 4 * c) = v;
+      if (c == 0) both[r] = make_float2(top, total);
+    }
   }
-  if (nc > 1) cluster.sync();  // results may still be read
+  if (nc == 1) return;
+  cluster.sync();
+  for (int x = rank * kSpThreads + tid; x < rows * (D / 4); x += nc * kSpThreads) {
+    const int r = x / (D / 4), c = x % (D / 4);
+    float2 f[8];
+    float4 y[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      f[k] = make_float2(kSpNoRef, 0.f);
+      y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k < nc) {
+        f[k] = cluster.map_shared_rank(both, k)[r];
+        y[k] = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(res, k) +
+                                                 r * RR + 4 * c);
+      }
+    }
+    float top = f[0].x, total = 0.f;
+#pragma unroll
+    for (int k = 1; k < 8; ++k) top = fmaxf(top, f[k].x);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float s = ex2(f[k].x - top);
+      total = fmaf(f[k].y, s, total);
+      v.x = fmaf(y[k].x, s, v.x);
+      v.y = fmaf(y[k].y, s, v.y);
+      v.z = fmaf(y[k].z, s, v.z);
+      v.w = fmaf(y[k].w, s, v.w);
+    }
+    put(r, c, v, top, total);
+  }
+  cluster.sync();  // results may still be read
 }
 
 template <int DT, int D, int NT>
