@@ -6,7 +6,7 @@
 // What bounds it: the listed K and V rows' bytes, each read once, while a kv
 // head has few query rows; the chain of a page's products and softmax beyond.
 //
-// A cluster of 1 to 8 CTAs takes a unit: a (sequence, kv head) and up to 40 of
+// A cluster of 1 to 8 CTAs takes a unit: a (sequence, kv head) and up to 24 of
 // its query rows (8 over an fp32 cache).  Its CTAs split the list and their
 // warps deal out the pages; the results meet in distributed shared memory, so
 // a call is one launch, without partials in memory.  Every warp copies its own
@@ -48,9 +48,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSpWarps = 4;
-constexpr int kSpThreads = 32 * kSpWarps;
-constexpr int kSpTiles = 5;         // most n8 tiles of query rows of a unit
+constexpr int kSpTiles = 4;         // most n8 tiles of query rows of a unit
 constexpr int kListCap = 512;       // list entries a CTA looks up at once
 constexpr float kSpNoRef = -3e38f;  // below any score
 
@@ -63,19 +61,23 @@ struct SpShape {
   static constexpr int ROWB = DT == SVP_F32 ? 4 * D : DT == SVP_BF16 ? 2 * D
                               : DT == SVP_FP8_E4M3 ? D : fp4_row_bytes(D);
   static constexpr int PAGE = kBlockSize * ROWB;  // one side
-  static constexpr int STAGES = PAGE >= 4096 ? 3 : 4;
+  // warps of a CTA, of which an SM holds two: eight over small pages, whose
+  // rings leave the room, while 128 registers are enough
+  static constexpr int WARPS = PAGE < 4096 && DT != SVP_F32 && NT == 1 ? 8 : 4;
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int STAGES = PAGE * WARPS >= 16384 ? 3 : 4;
   static constexpr int ROWS = 8 * NT;             // of a unit
   static constexpr int WARP = STAGES * 2 * PAGE;  // a warp's ring
   // the warps' results take the rings' place at the end
   static constexpr int RES_ROW = 4 * D + 16;
-  static constexpr int RES = kSpWarps * ROWS * (RES_ROW + 8);
-  static constexpr int RING = kSpWarps * WARP > RES ? kSpWarps * WARP : RES;
+  static constexpr int RES = WARPS * ROWS * (RES_ROW + 8);
+  static constexpr int RING = WARPS * WARP > RES ? WARPS * WARP : RES;
   static constexpr int LIST = kListCap * 8;
   // query rows: with many tiles, as fragments for all warps; fp32 rows, and
   // each warp's weights
   static constexpr bool Q_SHARED = DT != SVP_F32 && NT > 2;
   static constexpr int QROW = 4 * D + 32;
-  static constexpr int Q = DT == SVP_F32 ? ROWS * QROW + kSpWarps * ROWS * kBlockSize * 4
+  static constexpr int Q = DT == SVP_F32 ? ROWS * QROW + WARPS * ROWS * kBlockSize * 4
                            : Q_SHARED    ? NT * ((D / 16) * 256 + 32)
                                          : 0;
   static constexpr int SMEM = RING + LIST + 64 + (Q > ROWS * 8 ? Q : ROWS * 8);
@@ -298,7 +300,7 @@ struct WarpMma {
                                              int row0, unsigned char *shared, int warp,
                                              int lane) {
     if constexpr (Q_SHARED) {
-      for (int n = warp; n < NT; n += kSpWarps) {
+      for (int n = warp; n < NT; n += S::WARPS) {
         uint2 w[KS];
         const float f = fragments(p, b, head, row0, n, w, lane);
 #pragma unroll
@@ -607,7 +609,7 @@ struct WarpF32 {
   __device__ __forceinline__ void load_query(const SparseParams &p, int b, int head,
                                              int row0, unsigned char *shared, int warp,
                                              int lane) {
-    for (int x = warp * 32 + lane; x < RPW * (D / 4); x += kSpThreads) {
+    for (int x = warp * 32 + lane; x < RPW * (D / 4); x += S::THREADS) {
       const int r = x / (D / 4), c = x % (D / 4), row = row0 + r;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (row < p.rows)
@@ -744,10 +746,10 @@ struct WarpOf<SVP_F32, D, NT> {
 };
 
 template <int DT, int D, int NT>
-__global__ void __launch_bounds__(kSpThreads)
+__global__ void __launch_bounds__(SpShape<DT, D, NT>::THREADS, 2)
     sparse_attention_kernel(const SparseParams p) {
   using S = SpShape<DT, D, NT>;
-  constexpr int RB = S::ROWS, STAGES = S::STAGES;
+  constexpr int RB = S::ROWS, STAGES = S::STAGES, W = S::WARPS, T = S::THREADS;
   extern __shared__ __align__(128) unsigned char smem[];
   int2 *const list = reinterpret_cast<int2 *>(smem + S::RING);
   int *const counts = reinterpret_cast<int *>(smem + S::RING + S::LIST);
@@ -767,12 +769,12 @@ __global__ void __launch_bounds__(kSpThreads)
   const int lo = (int)((long long)p.n_select * rank / nc);
   const int hi = (int)((long long)p.n_select * (rank + 1) / nc);
   // entries of the list that this thread looks up in a round
-  constexpr int PER = kListCap / kSpThreads;
+  constexpr int PER = kListCap / T;
   int page[PER];
   auto look = [&](int at) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int x = at + i * kSpThreads + tid;
+      const int x = at + i * T + tid;
       page[i] = x < hi ? entries[x] : -1;
     }
   };
@@ -807,7 +809,7 @@ __global__ void __launch_bounds__(kSpThreads)
         phys[i] = -1;
       }
       const unsigned m = __ballot_sync(kFull, phys[i] >= 0);
-      if (lane == 0) counts[i * kSpWarps + warp] = __popc(m);
+      if (lane == 0) counts[i * W + warp] = __popc(m);
     }
     __syncthreads();
     if (at == lo) st.start(p, L, row0, shared, lane);
@@ -816,21 +818,21 @@ __global__ void __launch_bounds__(kSpThreads)
     for (int i = 0; i < PER; ++i) {
       const unsigned m = __ballot_sync(kFull, phys[i] >= 0);
 #pragma unroll
-      for (int w = 0; w < kSpWarps; ++w) {
+      for (int w = 0; w < W; ++w) {
         if (w == warp && phys[i] >= 0)
           list[count + __popc(m & ((1u << lane) - 1u))] =
               make_int2(phys[i], page[i] * kBlockSize);
-        count += counts[i * kSpWarps + w];
+        count += counts[i * W + w];
       }
     }
     if (at + kListCap < hi) look(at + kListCap);
     __syncthreads();
     // this warp's pages: every fourth
-    const int n_mine = (count - warp + kSpWarps - 1) / kSpWarps;
+    const int n_mine = (count - warp + W - 1) / W;
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i) {
       if (i < n_mine)
-        load_page<DT, D>(p, ring + i * 2 * S::PAGE, list[warp + i * kSpWarps], head, L,
+        load_page<DT, D>(p, ring + i * 2 * S::PAGE, list[warp + i * W], head, L,
                          lane);
       cp_commit();
     }
@@ -840,9 +842,9 @@ __global__ void __launch_bounds__(kSpThreads)
       const int ahead = i + STAGES - 1;
       if (ahead < n_mine)
         load_page<DT, D>(p, ring + (stage == 0 ? STAGES - 1 : stage - 1) * 2 * S::PAGE,
-                         list[warp + ahead * kSpWarps], head, L, lane);
+                         list[warp + ahead * W], head, L, lane);
       cp_commit();
-      st.page(p, ring + stage * 2 * S::PAGE, list[warp + i * kSpWarps].y, b, L, row0,
+      st.page(p, ring + stage * 2 * S::PAGE, list[warp + i * W].y, b, L, row0,
               shared, warp, lane);
       stage = stage == STAGES - 1 ? 0 : stage + 1;
     }
@@ -853,7 +855,7 @@ __global__ void __launch_bounds__(kSpThreads)
   __syncthreads();  // the rings are free
   constexpr int RR = S::RES_ROW / 4;
   float *const res = reinterpret_cast<float *>(smem);
-  float2 *const stat = reinterpret_cast<float2 *>(res + kSpWarps * RB * RR);
+  float2 *const stat = reinterpret_cast<float2 *>(res + W * RB * RR);
   float2 *const both = reinterpret_cast<float2 *>(shared);  // (the queries are used)
   st.finish(res + warp * RB * RR, stat + warp * RB, lane);
   __syncthreads();
@@ -877,18 +879,18 @@ __global__ void __launch_bounds__(kSpThreads)
       p.lse[to] = total == 0.f ? -INFINITY : (top - off + log2f(total)) * kLn2;
     }
   };
-  for (int x = tid; x < rows * (D / 4); x += kSpThreads) {
+  for (int x = tid; x < rows * (D / 4); x += T) {
     const int r = x / (D / 4), c = x % (D / 4);
-    float2 f[kSpWarps];
+    float2 f[W];
     float top = kSpNoRef, total = 0.f;
 #pragma unroll
-    for (int w = 0; w < kSpWarps; ++w) {
+    for (int w = 0; w < W; ++w) {
       f[w] = stat[w * RB + r];
       top = fmaxf(top, f[w].x);
     }
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < kSpWarps; ++w) {
+    for (int w = 0; w < W; ++w) {
       const float s = ex2(f[w].x - top);
       const float4 y = *reinterpret_cast<const float4 *>(res + (w * RB + r) * RR + 4 * c);
       total = fmaf(f[w].y, s, total);
@@ -906,7 +908,7 @@ __global__ void __launch_bounds__(kSpThreads)
   }
   if (nc == 1) return;
   cluster.sync();
-  for (int x = rank * kSpThreads + tid; x < rows * (D / 4); x += nc * kSpThreads) {
+  for (int x = rank * T + tid; x < rows * (D / 4); x += nc * T) {
     const int r = x / (D / 4), c = x % (D / 4);
     float2 f[8];
     float4 y[8];
@@ -958,7 +960,7 @@ cudaError_t sparse_t(SparseParams p, int splits, cudaStream_t stream) {
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kSpThreads);
+  cfg.blockDim = dim3(S::THREADS);
   cfg.dynamicSmemBytes = S::SMEM;
   cfg.stream = stream;
   cfg.attrs = attr;
@@ -974,22 +976,19 @@ cudaError_t sparse_rows(SparseParams p, int sms, cudaStream_t stream) {
   const int nt = ((p.rows + p.n_rb - 1) / p.n_rb + 7) / 8;
   p.n_rb = (p.rows + 8 * nt - 1) / (8 * nt);
   const long long units = (long long)p.batch * p.num_kv_heads * p.n_rb;
-  // split a list while the CTAs all find room and a warp keeps two pages, or to
-  // the caller's pages per CTA
-  const long long least = p.split_pages > 0 ? p.split_pages : 2 * kSpWarps;
+  // split a list while the CTAs all find room and keep eight pages, or to the
+  // caller's pages per CTA
+  const long long least = p.split_pages > 0 ? p.split_pages : 8;
   int splits = 1;
   while (splits < 8 && 2LL * splits * least <= p.n_select &&
          (p.split_pages > 0 || units * splits * 2 <= 2LL * sms))
     splits *= 2;
   if constexpr (DT == SVP_F32) return sparse_t<DT, D, 1>(p, splits, stream);
   else
-    switch (nt) {
-      case 1: return sparse_t<DT, D, 1>(p, splits, stream);
-      case 2: return sparse_t<DT, D, 2>(p, splits, stream);
-      case 3: return sparse_t<DT, D, 3>(p, splits, stream);
-      case 4: return sparse_t<DT, D, 4>(p, splits, stream);
-      default: return sparse_t<DT, D, 5>(p, splits, stream);
-    }
+    return nt == 1   ? sparse_t<DT, D, 1>(p, splits, stream)
+           : nt == 2 ? sparse_t<DT, D, 2>(p, splits, stream)
+           : nt == 3 ? sparse_t<DT, D, 3>(p, splits, stream)
+                     : sparse_t<DT, D, 4>(p, splits, stream);
 }
 
 }  // namespace
