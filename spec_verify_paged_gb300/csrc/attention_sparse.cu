@@ -50,6 +50,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kSpTiles = 4;         // most n8 tiles of query rows of a unit
 constexpr int kListCap = 512;       // list entries a CTA looks up at once
+constexpr int kNoPage = 0x7ffffff0; // first position of a page that is not there
 constexpr float kSpNoRef = -3e38f;  // below any score
 
 __device__ __forceinline__ void raise_sparse(unsigned f) {
@@ -66,6 +67,9 @@ struct SpShape {
   static constexpr int WARPS = PAGE < 4096 && DT != SVP_F32 && NT == 1 ? 8 : 4;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int STAGES = PAGE * WARPS >= 16384 ? 3 : 4;
+  // pages that a warp takes at once: two where latency counts more than room
+  // and registers (their products are independent chains, one vote serves both)
+  static constexpr int AT_ONCE = PAGE < 4096 && DT != SVP_F32 && NT > 1 ? 2 : 1;
   static constexpr int ROWS = 8 * NT;             // of a unit
   static constexpr int WARP = STAGES * 2 * PAGE;  // a warp's ring
   // the warps' results take the rings' place at the end
@@ -177,7 +181,7 @@ __device__ __forceinline__ void load_page(const SparseParams &p, uint32_t stage,
   using S = SpShape<DT, D, 1>;
   constexpr int PIECES = S::PAGE / 16;  // of a side
   const size_t at = ((size_t)e.x * p.num_kv_heads + head) * S::PAGE;
-  const int rows = min(L - e.y, kBlockSize);
+  const int rows = max(min(L - e.y, kBlockSize), 0);
 #pragma unroll
   for (int i = 0; i < (2 * PIECES + 31) / 32; ++i) {
     const int x = i * 32 + lane;
@@ -501,46 +505,58 @@ struct WarpMma {
     }
   }
 
-  __device__ __forceinline__ void page(const SparseParams &p, uint32_t kp, int j0,
-                                       int b, int L, int row0, unsigned char *shared,
-                                       int, int lane) {
+  // The pages that stand at `at` in the ring (K, then V), first positions j0; one
+  // at kNoPage has no visible key.
+  template <int NP>
+  __device__ __forceinline__ void pages(const SparseParams &p, const uint32_t (&at)[NP],
+                                        const int (&j0)[NP], int b, int L, int row0,
+                                        unsigned char *shared, int, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    float s[NT][4];
-    scores(kp, s, shared, lane);
+    float s[NP][NT][4];
+#pragma unroll
+    for (int x = 0; x < NP; ++x) scores(at[x], s[x], shared, lane);
     // in the log2 domain, masked; value 2 h + e: key of half h, row 2 t + e
-    bool over = false;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[n][e] *= factor[n][e & 1];
-    if (j0 + kBlockSize - 1 > t_all) {
+    for (int x = 0; x < NP; ++x) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const RowMask m = row_mask(p, b, L, row0 + 8 * n + 2 * t + e);
+        for (int e = 0; e < 4; ++e) s[x][n][e] *= factor[n][e & 1];
+      if (j0[x] + kBlockSize - 1 > t_all) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (!m.sees(j0 + key(g, h))) s[n][2 * h + e] = -INFINITY;
-        }
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const RowMask m = row_mask(p, b, L, row0 + 8 * n + 2 * t + e);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (!m.sees(j0[x] + key(g, h))) s[x][n][2 * h + e] = -INFINITY;
+          }
+      }
     }
+    bool over = false;
+    float top[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        over |= fmaxf(s[n][e], s[n][2 + e]) > ref[n][e] + (kSlack - kOff);
+      for (int e = 0; e < 2; ++e) {
+        top[n][e] = fmaxf(s[0][n][e], s[0][n][2 + e]);
+#pragma unroll
+        for (int x = 1; x < NP; ++x)
+          top[n][e] = fmaxf(top[n][e], fmaxf(s[x][n][e], s[x][n][2 + e]));
+        over |= top[n][e] > ref[n][e] + (kSlack - kOff);
+      }
     if (__any_sync(kFull, over)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float top = fmaxf(s[n][e], s[n][2 + e]);
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1)
-            top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
-          if (top > ref[n][e]) {
-            const float f = ex2(ref[n][e] - top);
-            ref[n][e] = top;
+            top[n][e] = fmaxf(top[n][e], __shfl_xor_sync(kFull, top[n][e], off));
+          if (top[n][e] > ref[n][e]) {
+            const float f = ex2(ref[n][e] - top[n][e]);
+            ref[n][e] = top[n][e];
             sum[n][e] *= f;
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
@@ -550,19 +566,22 @@ struct WarpMma {
           }
         }
     }
-    uint32_t pb[NT][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int x = 0; x < NP; ++x) {
+      uint32_t pb[NT][2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[n][e] = ex2(s[n][e] - ref[n][e & 1] + kOff);
-        sum[n][e & 1] += s[n][e];
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[x][n][e] = ex2(s[x][n][e] - ref[n][e & 1] + kOff);
+          sum[n][e & 1] += s[x][n][e];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          pb[n][h] = transpose8(pack2<DT>(s[x][n][2 * h], s[x][n][2 * h + 1]));
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        pb[n][h] = transpose8(pack2<DT>(s[n][2 * h], s[n][2 * h + 1]));
+      values(at[x] + S::PAGE, pb, lane);
     }
-    values(kp + S::PAGE, pb, lane);
   }
 
   // The warp's rows to shared memory: values, then reference and sum.
@@ -634,10 +653,13 @@ struct WarpF32 {
     t_all = p.tree_mask ? base - 1 : base + min(row0, p.rows - 1) / p.group;
   }
 
-  __device__ __forceinline__ void page(const SparseParams &p, uint32_t kp, int j0,
-                                       int b, int L, int row0, unsigned char *shared,
-                                       int warp, int lane) {
-    const uint32_t qs = smem_u32(shared), vp = kp + S::PAGE;
+  template <int NP>
+  __device__ __forceinline__ void pages(const SparseParams &p, const uint32_t (&at)[NP],
+                                        const int (&first)[NP], int b, int L, int row0,
+                                        unsigned char *shared, int warp, int lane) {
+    static_assert(NP == 1, "");
+    const int j0 = first[0];
+    const uint32_t qs = smem_u32(shared), kp = at[0], vp = kp + S::PAGE;
     float *const ps = reinterpret_cast<float *>(shared + RPW * QROW) +
                       warp * RPW * kBlockSize;
     const int k = lane & 15, half = lane >> 4;
@@ -829,24 +851,33 @@ __global__ void __launch_bounds__(SpShape<DT, D, NT>::THREADS, 2)
     __syncthreads();
     // this warp's pages: every fourth
     const int n_mine = (count - warp + W - 1) / W;
+    constexpr int NP = S::AT_ONCE, AHEAD = STAGES - NP;  // on their way at a time
+    static_assert(STAGES % NP == 0, "a step's stages lie side by side");
+    auto load = [&](int i) {  // pages i .. i + NP - 1; zeros for one that is not there
+      if (i < n_mine) {
 #pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) {
-      if (i < n_mine)
-        load_page<DT, D>(p, ring + i * 2 * S::PAGE, list[warp + i * W], head, L,
-                         lane);
+        for (int x = 0; x < NP; ++x)
+          load_page<DT, D>(p, ring + (i + x) % STAGES * 2 * S::PAGE,
+                           i + x < n_mine ? list[warp + (i + x) * W]
+                                          : make_int2(0, kNoPage),
+                           head, L, lane);
+      }
       cp_commit();
-    }
-    for (int i = 0, stage = 0; i < n_mine; ++i) {
-      cp_wait<STAGES - 2>();
-      __syncwarp();  // the page is there, and the one before has been read
-      const int ahead = i + STAGES - 1;
-      if (ahead < n_mine)
-        load_page<DT, D>(p, ring + (stage == 0 ? STAGES - 1 : stage - 1) * 2 * S::PAGE,
-                         list[warp + ahead * W], head, L, lane);
-      cp_commit();
-      st.page(p, ring + stage * 2 * S::PAGE, list[warp + i * W].y, b, L, row0,
-              shared, warp, lane);
-      stage = stage == STAGES - 1 ? 0 : stage + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; i += NP) load(i);
+    for (int i = 0; i < n_mine; i += NP) {
+      cp_wait<AHEAD / NP - 1>();
+      __syncwarp();  // the pages are there, and the step before has been read
+      load(i + AHEAD);
+      uint32_t where[NP];
+      int j0[NP];
+#pragma unroll
+      for (int x = 0; x < NP; ++x) {
+        where[x] = ring + (i + x) % STAGES * 2 * S::PAGE;
+        j0[x] = i + x < n_mine ? list[warp + (i + x) * W].y : kNoPage;
+      }
+      st.template pages<NP>(p, where, j0, b, L, row0, shared, warp, lane);
     }
     cp_wait<0>();
   }
