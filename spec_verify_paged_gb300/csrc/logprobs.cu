@@ -43,6 +43,7 @@ constexpr int kLpThreads = 256;
 constexpr int kLpCluster = 8;
 constexpr int kLpFound = 512;  // candidates ranked by counting
 constexpr int kLpSlack = 8;    // threads more than k that may reach the bound
+constexpr int kLpBins = 256;   // over the two octaves below the largest logit
 
 // The two halves of a cluster barrier: what comes before the arrival is visible
 // after the wait.
@@ -69,11 +70,14 @@ struct LpPart {            // one CTA's share of the row's results
 };
 template <int W>
 struct LpShared {
-  Found found[kLpFound];
-  Found best[kLpCluster][kMaxTop];  // in the first CTA: every CTA's, in order
+  alignas(16) Found found[kLpFound + 1];
+  // in the first CTA: the others' best too, n_top of each, keys of 0 where a CTA
+  // has fewer
+  alignas(16) Found best[kLpCluster * kMaxTop + 1];
   LpPart part[kLpCluster];          // in the first CTA
   LpSums warp_f[W];
   unsigned warp_u[2][W];
+  alignas(16) unsigned hist[kLpBins];           // of the threads' largest keys
   unsigned n_found, n_high;
   unsigned short high[32 * W];      // threads that reach the bound
 };
@@ -199,7 +203,8 @@ __global__ void __launch_bounds__(kLpThreads)
     token_logprobs_kernel(const LogprobParams p, int part) {  // vectors of a CTA
   using V = Vec<DT>;
   constexpr int T = kLpThreads, VEC = V::N, SIZE = 16 / VEC, W = T / 32;
-  extern __shared__ uint4 held[];  // thread tid's are tid, tid + T, ..
+  extern __shared__ uint4 held[];  // [part], thread tid's are tid, tid + T, ..
+  const uint32_t *const mask = reinterpret_cast<const uint32_t *>(held + part);
   __shared__ LpShared<W> sm;
   cg::cluster_group cluster = cg::this_cluster();
   const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -241,9 +246,16 @@ __global__ void __launch_bounds__(kLpThreads)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(held + i)),
                  "l"(aligned + i) : "memory");
   }
-  asm volatile("cp.async.commit_group;" ::: "memory");
   const uint32_t *const allowed =
       p.allowed ? p.allowed + row * (size_t)p.words : nullptr;
+  const int word0 = max(t00, 0) >> 5;  // the mask's words of these tokens
+  if (allowed && n_vec > 0) {
+    const int n_words = ((t00 + n_vec * VEC - 1) >> 5) - word0 + 1;
+    for (int i = tid; i < n_words; i += T)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(mask + i)),
+                   "l"(allowed + word0 + i) : "memory");
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
   auto element = [&](int t) {  // logit of token t
     if constexpr (DT == SVP_F32) return reinterpret_cast<const float *>(base)[t];
     else
@@ -276,15 +288,14 @@ __global__ void __launch_bounds__(kLpThreads)
   auto fetch = [&](int i) {
     const uint4 v = held[i];
     if (!allowed) return v;
+    const int t0 = t00 + i * VEC;
     if (shift == 0) {  // a vector's bits lie in one byte
-      const uint32_t y = __ldg(reinterpret_cast<const unsigned char *>(allowed) +
-                               (v0 + i) * VEC / 8);
-      return V::masked(v, VEC == 8 ? y : y >> (4 * ((v0 + i) & 1)));
+      const uint32_t y = reinterpret_cast<const unsigned char *>(mask)[t0 / 8 - 4 * word0];
+      return V::masked(v, VEC == 8 ? y : y >> (t0 & 4));
     }
-    const int t0 = t00 + i * VEC, w = t0 >> 5;
-    const uint32_t w0 = __ldg(allowed + w);
-    const uint32_t w1 = (t0 & 31) + VEC > 32 ? __ldg(allowed + w + 1) : 0u;
-    return V::masked(v, __funnelshift_r(w0, w1, t0 & 31));
+    const int w = (t0 >> 5) - word0;
+    const uint32_t w1 = (t0 & 31) + VEC > 32 ? mask[w + 1] : 0u;
+    return V::masked(v, __funnelshift_r(mask[w], w1, t0 & 31));
   };
 
   // f(key, token) of every logit of this thread, for rare rows
@@ -300,6 +311,9 @@ __global__ void __launch_bounds__(kLpThreads)
       for (int e = 0; e < VEC; ++e) f(logit_key(V::value(extra, e)), extra0 + e);
     }
   };
+
+  if (tid == 0) sm.n_found = sm.n_high = 0;
+  for (int i = tid; i < kLpBins; i += T) sm.hist[i] = 0u;
 
   // ---- sums, the largest logit, and how many are ahead of the token ----
   // Tokens before it are ahead with a logit that is not smaller, those after
@@ -355,6 +369,7 @@ __global__ void __launch_bounds__(kLpThreads)
     }
   };
   asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (allowed) __syncthreads();  // (the mask's words are every thread's)
 #pragma unroll 1
   for (int i0 = tid; i0 < n_vec; i0 += 32 * T) {  // at most 128 in a half
     const int end = min(n_vec, i0 + 32 * T);
@@ -387,7 +402,6 @@ __global__ void __launch_bounds__(kLpThreads)
     sm.warp_f[warp] = a;
     sm.warp_u[0][warp] = wm;
   }
-  if (tid == 0) sm.n_found = sm.n_high = 0;
   const unsigned n_ahead = lp_sum(ahead, sm, 1);  // its barrier serves all
   const unsigned top_key =
       __reduce_max_sync(kFull, lane < W ? sm.warp_u[0][lane] : 0u);
@@ -396,17 +410,48 @@ __global__ void __launch_bounds__(kLpThreads)
   unsigned keep = 0;
   if (p.n_top > 0 && top_key > 0u) {
     const unsigned k = (unsigned)p.n_top;
-    // a bound that at least k threads reach, and few more: first two octaves
-    // below the largest, else from the lowest logit on (with fewer threads
-    // that hold any, every element)
-    unsigned edge = kLowestKey, hi = top_key == 0xffffffffu ? top_key : top_key + 1u;
-    {
-      const unsigned guess = top_key - (2u << 23);
-      if (top_key > kLowestKey + (2u << 23)) {
-        const unsigned c = (unsigned)__syncthreads_count(mine >= guess);
-        if (c >= k) edge = guess; else hi = guess;
-        if (c >= k && c <= k + kLpSlack) hi = edge;
+    // A bound that at least k threads reach, and few more: the lower end of the
+    // part of the two octaves below the largest that holds the k-th.
+    unsigned edge = kLowestKey;
+    const unsigned low = top_key - (2u << 23);
+    unsigned in_range = 0;
+    if (top_key > kLowestKey + (2u << 23)) {
+      if (mine > low)
+        atomicAdd(&sm.hist[(top_key - mine) >> 16], 1u);  // from the largest down
+      __syncthreads();
+      constexpr int PER = kLpBins / 32;
+      unsigned c[PER], before = 0;
+#pragma unroll
+      for (int i = 0; i < PER; i += 4) {
+        const uint4 y = *reinterpret_cast<const uint4 *>(sm.hist + lane * PER + i);
+        c[i] = y.x;
+        c[i + 1] = y.y;
+        c[i + 2] = y.z;
+        c[i + 3] = y.w;
       }
+#pragma unroll
+      for (int i = 0; i < PER; ++i) before += c[i];
+      const unsigned own = before;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const unsigned y = __shfl_up_sync(kFull, before, off);
+        if (lane >= off) before += y;
+      }
+      in_range = __shfl_sync(kFull, before, 31);
+      before -= own;
+      unsigned at = 0xffffffffu;  // the first bin by whose end there are k
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        before += c[i];
+        if (before >= k) at = min(at, (unsigned)(lane * PER + i));
+      }
+      at = __reduce_min_sync(kFull, at);
+      if (in_range >= k) edge = top_key - (at << 16) - 0xffffu;
+    }
+    if (in_range < k) {
+      // bit by bit, from the lowest logit on (with fewer threads that hold any,
+      // every element)
+      unsigned hi = top_key == 0xffffffffu ? top_key : top_key + 1u;
       while (hi > edge + 1u) {
         const unsigned mid = edge + (hi - edge) / 2u;
         const unsigned c = (unsigned)__syncthreads_count(mine >= mid);
@@ -433,12 +478,15 @@ __global__ void __launch_bounds__(kLpThreads)
         if (x >= edge) add(x, t0 + e);
       }
     };
-    // the vectors of the threads that reach it, a warp to a thread
+    // the vectors of the threads that reach it, as many at once as a warp takes
     if (mine >= edge) sm.high[atomicAdd(&sm.n_high, 1u)] = (unsigned short)tid;
     __syncthreads();
-    const unsigned n_high = sm.n_high;
-    for (unsigned x = warp; x < n_high; x += W)
-      for (int i = sm.high[x] + lane * T; i < n_vec; i += 32 * T)
+    const int n_high = (int)sm.n_high;
+    int lanes = 1;  // for a thread's vectors
+    while (lanes < 32 && lanes * T < n_vec) lanes *= 2;
+    const int per = 32 / lanes;
+    for (int x = warp * per + lane / lanes; x < n_high; x += W * per)
+      for (int i = sm.high[x] + lane % lanes * T; i < n_vec; i += lanes * T)
         some(fetch(i), t00 + i * VEC);
     if (has_extra && mine >= edge) some(extra, extra0);
     __syncthreads();
@@ -471,21 +519,31 @@ __global__ void __launch_bounds__(kLpThreads)
       n = k;
     }
     keep = min(n, k);
+    if (tid == 0) sm.found[n].key = 0u;  // (n <= kLpFound)
+    __syncthreads();
     if (nc > 1) lp_wait();
     Found *const best =
-        nc > 1 ? cluster.map_shared_rank(&sm.best[rank][0], 0) : &sm.best[0][0];
+        (nc > 1 ? cluster.map_shared_rank(sm.best, 0) : sm.best) + rank * p.n_top;
+    for (unsigned r = keep + tid; r < k; r += T) best[r] = Found{0u, 0};
     for (unsigned c = tid; c < n; c += T) {
       const Found f = sm.found[c];
       unsigned r = 0;
-      for (unsigned o = 0; o < n; ++o) {
-        const Found h = sm.found[o];
-        r += h.key > f.key || (h.key == f.key && h.token < f.token) ? 1u : 0u;
+#pragma unroll 4
+      for (unsigned o = 0; o < n; o += 2) {  // (one more is there: nothing)
+        const uint4 h = *reinterpret_cast<const uint4 *>(sm.found + o);
+        r += h.x > f.key || (h.x == f.key && (int)h.y < f.token) ? 1u : 0u;
+        r += h.z > f.key || (h.z == f.key && (int)h.w < f.token) ? 1u : 0u;
       }
       if (r < keep) best[r] = f;
     }
-  } else if (nc > 1) {
-    lp_wait();
+  } else {
+    if (nc > 1) lp_wait();
+    Found *const best =
+        (nc > 1 ? cluster.map_shared_rank(sm.best, 0) : sm.best) + rank * p.n_top;
+    for (int r = tid; r < p.n_top; r += T) best[r] = Found{0u, 0};
   }
+  // (the counting takes them in pairs)
+  if (rank == 0 && tid == 0) sm.best[nc * p.n_top] = Found{0u, 0};
   if (tid == 0) {
     LpPart part;
     part.key = top_key;
@@ -525,24 +583,18 @@ __global__ void __launch_bounds__(kLpThreads)
     if (p.ranks) p.ranks[row] = kt == 0u ? -1 : (int)n_before;
   }
   if (p.n_top > 0) {
+    const int n_all = nc * p.n_top;
     unsigned n = 0;
     for (int r = 0; r < nc; ++r) n += sm.part[r].n_best;
-    for (int x = tid; x < nc * kMaxTop; x += T) {
-      const int c = x / kMaxTop, i = x % kMaxTop;
-      if (i >= (int)sm.part[c].n_best) continue;
-      const Found f = sm.best[c][i];
-      // its place: the larger ones before it in its own list, and in the others'
-      unsigned r = (unsigned)i;
-      for (int o = 0; o < nc; ++o) {
-        if (o == c) continue;
-        unsigned lo = 0, hi = sm.part[o].n_best;  // first that is not ahead
-        while (lo < hi) {
-          const unsigned mid = (lo + hi) / 2u;
-          const Found h = sm.best[o][mid];
-          if (h.key > f.key || (h.key == f.key && h.token < f.token)) lo = mid + 1u;
-          else hi = mid;
-        }
-        r += lo;
+    for (int x = tid; x < n_all; x += T) {
+      const Found f = sm.best[x];
+      if (f.key == 0u) continue;
+      unsigned r = 0;  // how many are before it
+#pragma unroll 4
+      for (int o = 0; o < n_all; o += 2) {
+        const uint4 h = *reinterpret_cast<const uint4 *>(sm.best + o);
+        r += h.x > f.key || (h.x == f.key && (int)h.y < f.token) ? 1u : 0u;
+        r += h.z > f.key || (h.z == f.key && (int)h.w < f.token) ? 1u : 0u;
       }
       if (r < (unsigned)p.n_top) {
         p.top_logprobs[row * p.n_top + r] = log_p(key_logit(f.key));
@@ -564,11 +616,13 @@ cudaError_t logprobs_dt(const LogprobParams &p, int sms, cudaStream_t stream) {
   // three; more for few rows, while a thread has a vector
   int nc = 1;
   while (nc < kLpCluster &&
-         (vecs > 16 * T * nc || ((long long)p.rows * nc < 4LL * sms && vecs > T * nc)))
+         (vecs > 8 * T * nc || ((long long)p.rows * nc < 4LL * sms && vecs > T * nc)))
     nc *= 2;
   const int part = (vecs + nc - 1) / nc;
-  constexpr int kMost = kMaxVocab / Vec<DT>::N / kLpCluster * 16;  // 160 KB at most
-  const int smem = part * 16;
+  constexpr int kMost =  // 165 KB at most
+      kMaxVocab / kLpCluster * (16 / Vec<DT>::N) + kMaxVocab / kLpCluster / 8 + 16;
+  // the mask's words, and one more where a row does not start with a word
+  const int smem = part * 16 + (p.allowed ? (part * Vec<DT>::N / 32 + 2) * 4 : 0);
   if (smem > kMost) return cudaErrorInvalidConfiguration;
   if (smem > 32 * 1024) {  // (the static part counts as well)
     const cudaError_t e = cudaFuncSetAttribute(
