@@ -8,15 +8,16 @@
 // A thread moves its r only when a logit exceeds it by a factor 2^8 of
 // probability, so one pass of exponentials gives everything but the order.
 //
-// A cluster of 1 to 8 CTAs takes a row, each a part of it that it copies into
-// shared memory, so the logits are read once; a thread reads only what it
-// copied, so no barrier is needed in between.  What bounds it for long rows is
-// instructions, about nine an element (with a mask eleven): what can be done
-// on pairs of bf16 is (the maximum, the count of the tokens ahead), and few
-// vectors are looked at again for the alternatives.  Loops are short: the row
-// in registers, with everything unrolled, waited for instructions (512 rows of
-// 131,072 bf16: 148 us; two passes out of shared memory, 97).  The CTAs' sums
-// meet in the first CTA's shared memory at the end, by one cluster barrier.
+// A cluster of 1 to 8 CTAs takes a row; a thread's vectors lie a CTA's width
+// apart.  What bounds it for long rows is instructions, about eleven an element
+// (with a mask fourteen), and what a CTA does once: so a row takes as few CTAs as
+// fill the GPU, two fp32 values are multiplied and added at once, what can be
+// done on pairs of bf16 is (the maximum, the count of the tokens ahead), and few
+// vectors are looked at again, out of L2, for the alternatives.  Tried on 512
+// masked rows of 131,072 bf16: the row in registers, with everything unrolled,
+// 148 us (waiting for instructions); in shared memory, four CTAs a row, 98.  The
+// CTAs' sums meet in the first one's shared memory at the end, by one cluster
+// barrier.
 //
 // The alternatives: the k-th largest of the threads' own largest values bounds
 // the k-th largest of all from below, and few elements reach that bound; they
@@ -41,7 +42,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kLpThreads = 256;
 constexpr int kLpCluster = 8;
-constexpr int kLpFound = 512;  // candidates ranked by counting
+constexpr int kLpFound = 256;  // candidates ranked by counting
 constexpr int kLpSlack = 8;    // threads more than k that may reach the bound
 constexpr int kLpBins = 256;   // over the two octaves below the largest logit
 
@@ -60,9 +61,9 @@ struct Found {
   unsigned key;
   int token;
 };
-// Sums of weights w = 2^d and of w d, d = (x - r) / T in units of log 2.
+// Sums of weights w = 2^d and of w d, d = (x - r) / T + e in units of log 2.
 struct LpSums {
-  float r, s, sz;
+  float r, e, s, sz;
 };
 struct LpPart {            // one CTA's share of the row's results
   LpSums sums;
@@ -129,6 +130,26 @@ __device__ __forceinline__ uint32_t spread(uint32_t y, uint32_t sel) {
   return r;
 }
 
+// Two fp32 values at once.
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void parts(uint64_t x, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // A 16-byte vector of logits.
 template <int DT>
 struct Vec {
@@ -152,6 +173,17 @@ struct Vec {
       const uint32_t m = max_nan_2(max_nan_2(v.x, v.y), max_nan_2(v.z, v.w));
       return max_nan_f(lo_f(m), hi_f(m));
     }
+  }
+  // elements 2 i and 2 i + 1, nothing as a finite value far below every logit
+  // that counts
+  static __device__ __forceinline__ uint64_t pair(const uint4 &v, int i) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (DT == SVP_F32)
+      return two(fmaxf(__uint_as_float(w[2 * i]), -1e30f),
+                 fmaxf(__uint_as_float(w[2 * i + 1]), -1e30f));
+    uint32_t c;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(w[i]), "r"(0xf14af14au));  // -1e30
+    return two(lo_f(c), hi_f(c));
   }
   // v where bit e of `bits` is set, -inf elsewhere.  Four bits become the sign
   // bits of four bytes, which the byte permutation spreads.
@@ -180,13 +212,12 @@ struct Vec {
 
 // Two parts' sums, relative to the larger reference.
 __device__ __forceinline__ LpSums join(const LpSums &a, const LpSums &b, float sc) {
-  LpSums o;
-  o.r = fmaxf(a.r, b.r);
-  const float da = fmaxf((a.r - o.r) * sc, -1e4f), db = fmaxf((b.r - o.r) * sc, -1e4f);
+  const LpSums &o = a.r >= b.r ? a : b;
+  const float da = fmaxf((a.r - o.r) * sc - a.e + o.e, -1e4f);
+  const float db = fmaxf((b.r - o.r) * sc - b.e + o.e, -1e4f);
   const float fa = ex2(da), fb = ex2(db);
-  o.s = fmaf(a.s, fa, b.s * fb);
-  o.sz = fmaf(a.sz, fa, a.s * (da * fa)) + fmaf(b.sz, fb, b.s * (db * fb));
-  return o;
+  return {o.r, o.e, fmaf(a.s, fa, b.s * fb),
+          fmaf(a.sz, fa, a.s * (da * fa)) + fmaf(b.sz, fb, b.s * (db * fb))};
 }
 
 // The next value above x (x below +inf), as the type has it.
@@ -200,11 +231,9 @@ __device__ __forceinline__ float next_up(float x) {
 
 template <int DT>
 __global__ void __launch_bounds__(kLpThreads)
-    token_logprobs_kernel(const LogprobParams p, int part) {  // vectors of a CTA
+    token_logprobs_kernel(const LogprobParams p) {
   using V = Vec<DT>;
   constexpr int T = kLpThreads, VEC = V::N, SIZE = 16 / VEC, W = T / 32;
-  extern __shared__ uint4 held[];  // [part], thread tid's are tid, tid + T, ..
-  const uint32_t *const mask = reinterpret_cast<const uint32_t *>(held + part);
   __shared__ LpShared<W> sm;
   cg::cluster_group cluster = cg::this_cluster();
   const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -230,7 +259,7 @@ __global__ void __launch_bounds__(kLpThreads)
   }
   if (nc > 1) lp_arrive();  // the first CTA's shared memory is there
 
-  // ---- the row into shared memory ----
+  // ---- the row ----
   // Rows start anywhere.  The whole aligned vectors are dealt out; what is left
   // before and after them is one extra vector of the first CTA's thread 0 and
   // its second warp's first.
@@ -238,24 +267,13 @@ __global__ void __launch_bounds__(kLpThreads)
                            row * (size_t)p.vocab * SIZE;
   const int shift = (int)(reinterpret_cast<uintptr_t>(base) & 15u) / SIZE;
   const int f0 = shift ? 1 : 0, f1 = max((shift + p.vocab) / VEC, f0);
+  const int part = (f1 - f0 + nc - 1) / nc;
   const int v0 = min(f0 + rank * part, f1);  // this CTA's
   const int n_vec = min(part, f1 - v0);
   const uint4 *const aligned = reinterpret_cast<const uint4 *>(base - shift * SIZE) + v0;
   const int t00 = v0 * VEC - shift;          // the first one's first token
-  for (int i = tid; i < n_vec; i += T) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(held + i)),
-                 "l"(aligned + i) : "memory");
-  }
   const uint32_t *const allowed =
       p.allowed ? p.allowed + row * (size_t)p.words : nullptr;
-  const int word0 = max(t00, 0) >> 5;  // the mask's words of these tokens
-  if (allowed && n_vec > 0) {
-    const int n_words = ((t00 + n_vec * VEC - 1) >> 5) - word0 + 1;
-    for (int i = tid; i < n_words; i += T)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(mask + i)),
-                   "l"(allowed + word0 + i) : "memory");
-  }
-  asm volatile("cp.async.commit_group;" ::: "memory");
   auto element = [&](int t) {  // logit of token t
     if constexpr (DT == SVP_F32) return reinterpret_cast<const float *>(base)[t];
     else
@@ -284,18 +302,21 @@ __global__ void __launch_bounds__(kLpThreads)
     extra = make_uint4(w[0], w[1], w[2], w[3]);
   }
 
-  // this thread's vector i as it counts: with -inf for what is not allowed
-  auto fetch = [&](int i) {
-    const uint4 v = held[i];
-    if (!allowed) return v;
+  // the bits of vector i: VEC of them, out of one word or two
+  auto bits_of = [&](int i) {
     const int t0 = t00 + i * VEC;
-    if (shift == 0) {  // a vector's bits lie in one byte
-      const uint32_t y = reinterpret_cast<const unsigned char *>(mask)[t0 / 8 - 4 * word0];
-      return V::masked(v, VEC == 8 ? y : y >> (t0 & 4));
+    if (shift == 0) {  // they lie in one byte
+      const uint32_t y = __ldg(reinterpret_cast<const unsigned char *>(allowed) + t0 / 8);
+      return VEC == 8 ? y : y >> (t0 & 4);
     }
-    const int w = (t0 >> 5) - word0;
-    const uint32_t w1 = (t0 & 31) + VEC > 32 ? mask[w + 1] : 0u;
-    return V::masked(v, __funnelshift_r(mask[w], w1, t0 & 31));
+    const uint32_t w0 = __ldg(allowed + (t0 >> 5));
+    const uint32_t w1 = (t0 & 31) + VEC > 32 ? __ldg(allowed + (t0 >> 5) + 1) : 0u;
+    return __funnelshift_r(w0, w1, t0 & 31);
+  };
+  // vector i as it counts: with -inf for what is not allowed
+  auto fetch = [&](int i) {
+    const uint4 v = __ldg(aligned + i);
+    return allowed ? V::masked(v, bits_of(i)) : v;
   };
 
   // f(key, token) of every logit of this thread, for rare rows
@@ -325,25 +346,55 @@ __global__ void __launch_bounds__(kLpThreads)
   unsigned ahead = 0;
   uint32_t n2 = 0u;  // counts of two halves: exact in bf16 up to 256
   float big = -INFINITY;
-  LpSums a = {__uint_as_float(V::kLowest), 0.f, 0.f};
-  const float margin = fminf(8.f / p.sc, 1e30f);
+  float r = __uint_as_float(V::kLowest);  // the reference, and
+  float margin = fminf(8.f / p.sc, 1e30f);  // how far a logit may exceed it
+  // The distance to it in units of log 2 is x sc - c, c = r sc: one
+  // instruction, exact but for c's rounding, which is kept (LpSums::e).  Where c
+  // would not be fine enough (huge logits, extreme temperatures), (x - r) sc.
+  const bool mild = p.sc > 1e-20f && p.sc < 1e8f;
+  bool fine = false;
+  uint64_t minus_c = 0, sums = two(0.f, 0.f), sums_z = two(0.f, 0.f);
+  const uint64_t sc2 = two(p.sc, p.sc);
   auto take = [&](const uint4 &v, int t0) {
     const float top = V::top(v);
     big = max_nan_f(big, top);
-    if (top > a.r + margin) {
-      const float d = fmaxf((a.r - top) * p.sc, -1e4f), f = ex2(d);
-      a.sz = fmaf(a.s, d, a.sz) * f;
-      a.s *= f;
-      a.r = top;
+    if (top > r + margin) {
+      const bool was_fine = fine;
+      float c0, c1;
+      parts(minus_c, c0, c1);
+      const float e0 = was_fine ? fmaf(r, p.sc, c0) : 0.f;
+      fine = mild && fabsf(top * p.sc) < 0x1p20f;
+      const float c = -(top * p.sc);
+      minus_c = two(c, c);
+      const float e1 = fine ? fmaf(top, p.sc, c) : 0.f;
+      const float d = fmaxf((r - top) * p.sc - e0 + e1, -1e4f), f = ex2(d);
+      sums_z = fma2(sums, two(d, d), sums_z);
+      sums_z = fma2(sums_z, two(f, f), 0ull);
+      sums = fma2(sums, two(f, f), 0ull);
+      r = top;
     }
     if (top == -INFINITY) return;
+    if (fine) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      // (far below what counts it stays finite)
-      const float d = fmaxf((V::value(v, e) - a.r) * p.sc, -1e4f);
-      const float w = ex2(d);
-      a.s += w;
-      a.sz = fmaf(w, d, a.sz);
+      for (int i = 0; i < VEC / 2; ++i) {
+        const uint64_t d = fma2(V::pair(v, i), sc2, minus_c);
+        float d0, d1;
+        parts(d, d0, d1);
+        const uint64_t w = two(ex2(d0), ex2(d1));
+        sums = add2(sums, w);
+        sums_z = fma2(w, d, sums_z);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; i += 2) {
+        const uint64_t d = two(fmaxf((V::value(v, i) - r) * p.sc, -1e4f),
+                               fmaxf((V::value(v, i + 1) - r) * p.sc, -1e4f));
+        float d0, d1;
+        parts(d, d0, d1);
+        const uint64_t w = two(ex2(d0), ex2(d1));
+        sums = add2(sums, w);
+        sums_z = fma2(w, d, sums_z);
+      }
     }
     if (!plain_rank) return;
     const float at = t0 + VEC <= token ? xt : up;
@@ -368,18 +419,41 @@ __global__ void __launch_bounds__(kLpThreads)
       n2 = 0u;
     }
   };
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-  if (allowed) __syncthreads();  // (the mask's words are every thread's)
+  constexpr int U = 4;  // vectors on their way at a time
 #pragma unroll 1
   for (int i0 = tid; i0 < n_vec; i0 += 32 * T) {  // at most 128 in a half
-    const int end = min(n_vec, i0 + 32 * T);
-#pragma unroll 2
-    for (int i = i0; i < end; i += T) take(fetch(i), t00 + i * VEC);
+#pragma unroll 1
+    for (int i = i0; i < min(n_vec, i0 + 32 * T); i += U * T) {
+      uint4 v[U];
+      uint32_t bits[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        v[u] = i + u * T < n_vec ? __ldg(aligned + i + u * T) : V::none();
+      if (allowed) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) bits[u] = i + u * T < n_vec ? bits_of(i + u * T) : 0u;
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = V::masked(v[u], bits[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) take(v[u], t00 + (i + u * T) * VEC);
+    }
     pour();
   }
   if (has_extra) {
     take(extra, warp == 0 ? -shift : extra0);
     pour();
+  }
+  LpSums a;
+  {
+    float c0, c1, x0, x1;
+    parts(minus_c, c0, c1);
+    a.r = r;
+    a.e = fine ? fmaf(r, p.sc, c0) : 0.f;
+    parts(sums, x0, x1);
+    a.s = x0 + x1;
+    parts(sums_z, x0, x1);
+    a.sz = x0 + x1;
   }
   const unsigned mine = logit_key(big);  // this thread's largest key
   if (plain_rank && rank == 0 && tid == 0) {
@@ -393,8 +467,8 @@ __global__ void __launch_bounds__(kLpThreads)
     });
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
-    const LpSums o = {__shfl_xor_sync(kFull, a.r, off), __shfl_xor_sync(kFull, a.s, off),
-                      __shfl_xor_sync(kFull, a.sz, off)};
+    const LpSums o = {__shfl_xor_sync(kFull, a.r, off), __shfl_xor_sync(kFull, a.e, off),
+                      __shfl_xor_sync(kFull, a.s, off), __shfl_xor_sync(kFull, a.sz, off)};
     a = join(a, o, p.sc);
   }
   const unsigned wm = __reduce_max_sync(kFull, mine);
@@ -574,7 +648,9 @@ __global__ void __launch_bounds__(kLpThreads)
     if (r > 0) all = join(all, sm.part[r].sums, p.sc);
   }
   const float ln = logf(all.s);
-  auto log_p = [&](float x) { return (x - all.r) * p.inv_t - ln; };
+  auto log_p = [&](float x) {
+    return fmaf(x - all.r, p.inv_t, all.e * kLn2) - ln;
+  };
   if (tid == 0) {
     // a row that allows nothing has no probabilities: -inf, entropy 0
     p.logprobs[row] = all.s != all.s ? NAN : kt == 0u ? -INFINITY : log_p(xt);
@@ -612,23 +688,11 @@ template <int DT>
 cudaError_t logprobs_dt(const LogprobParams &p, int sms, cudaStream_t stream) {
   constexpr int T = kLpThreads;
   const int vecs = p.vocab / Vec<DT>::N;
-  // CTAs of a row: as many as keep a part within 64 KB, so that an SM holds
-  // three; more for few rows, while a thread has a vector
+  // more CTAs to a row while there are few of them and a thread has a vector:
+  // 80 rows of 32,000 fp32 take 11.0 us with four, 14.1 with eight; 512 of 131,072
+  // bf16 44 with one, 47 with two, 61 with four
   int nc = 1;
-  while (nc < kLpCluster &&
-         (vecs > 8 * T * nc || ((long long)p.rows * nc < 4LL * sms && vecs > T * nc)))
-    nc *= 2;
-  const int part = (vecs + nc - 1) / nc;
-  constexpr int kMost =  // 165 KB at most
-      kMaxVocab / kLpCluster * (16 / Vec<DT>::N) + kMaxVocab / kLpCluster / 8 + 16;
-  // the mask's words, and one more where a row does not start with a word
-  const int smem = part * 16 + (p.allowed ? (part * Vec<DT>::N / 32 + 2) * 4 : 0);
-  if (smem > kMost) return cudaErrorInvalidConfiguration;
-  if (smem > 32 * 1024) {  // (the static part counts as well)
-    const cudaError_t e = cudaFuncSetAttribute(
-        token_logprobs_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-    if (e != cudaSuccess) return e;
-  }
+  while (nc < kLpCluster && (long long)p.rows * nc < 2LL * sms && vecs > T * nc) nc *= 2;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -639,11 +703,10 @@ cudaError_t logprobs_dt(const LogprobParams &p, int sms, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.rows * (unsigned)nc);
   cfg.blockDim = dim3(T);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<DT>, p, part);
+  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<DT>, p);
 }
 
 }  // namespace
