@@ -10,6 +10,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -253,9 +254,9 @@ __global__ void __launch_bounds__(32 * kBoundWarps)
 // hi with the positive parts of q and lo with the negative ones.  mma.sync
 // m16n8k16 takes 16 pages; the order of the terms does not matter, so they
 // are dealt such that lane (g, t) takes 16 consecutive bytes of pages g and
-// g + 8 for two steps.  A lane copies its own pieces through a ring of two
-// tiles of 16 pages in shared memory, so both are on their way while a third
-// is multiplied, and no warp waits for another; the query rows' parts are in
+// g + 8 for two steps.  A lane copies its own pieces of a tile of 16 pages
+// through shared memory, so the next tile is on its way while one is
+// multiplied, and no warp waits for another; the query rows' parts are in
 // shared memory as well.
 // bf16 products are exact in fp32, the sums are fp32; an fp32 q is taken as
 // three bf16 terms of 8 bits each.
@@ -375,11 +376,11 @@ __global__ void __launch_bounds__(32 * kPScoreWarps)
     }
     return id;
   };
-  // this lane's pieces of a tile, [page g, g + 8][lo, hi][NC], in a ring of two
+  // this lane's pieces of a tile, [page g, g + 8][lo, hi][NC]
   constexpr int PIECES = 4 * NC;
   const uint32_t ring = smem_u32(sq) + (unsigned)((p.rows + 7) / 8 * 8) * ROW +
-                        (warp * 2 * PIECES * 32 + lane) * 16;
-  auto load = [&](int id, int stage) {
+                        (warp * PIECES * 32 + lane) * 16;
+  auto load = [&](int id) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int page = __shfl_sync(kFull, id, g + 8 * h);
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(32 * kPScoreWarps)
 #pragma unroll
       for (int x = 0; x < 2 * NC; ++x)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                         ring + (stage * PIECES + h * 2 * NC + x) * 512),
+                         ring + (h * 2 * NC + x) * 512),
                      "l"(src + x / NC * (D / 8) + 4 * (x % NC) + t),
                      "r"(page < 0 ? 0 : 16)  // (a page that is not there: zeros)
                      : "memory");
@@ -398,12 +399,11 @@ __global__ void __launch_bounds__(32 * kPScoreWarps)
   };
   // the first tiles' bounds are on their way while the query rows are laid out
   constexpr int W = kPScoreWarps;
-  int id[3];  // of this warp's next tiles
+  int id[2];  // of this warp's next tiles
 #pragma unroll
-  for (int i = 0; i < 3; ++i) id[i] = page_ids(first + warp + i * W);
+  for (int i = 0; i < 2; ++i) id[i] = page_ids(first + warp + i * W);
   if (first * 16 < n) {
-    load(id[0], 0);
-    load(id[1], 1);
+    load(id[0]);
     // row r of this launch is (position, head of the group) row0 + r
     const int padded = (p.rows + 7) / 8 * 8;
 #pragma unroll 4
@@ -417,15 +417,15 @@ __global__ void __launch_bounds__(32 * kPScoreWarps)
     __syncthreads();
   }
   const int n_nt = (p.rows + 7) / 8;
-  for (int tile = first + warp, stage = 0; tile < last; tile += W, stage ^= 1) {
+  for (int tile = first + warp; tile < last; tile += W) {
     const int page0 = tile * 16;
     if (page0 >= n) {  // nothing here: -inf, so that a score is always there
       if (lane < 16 && page0 + lane < p.max_blocks && !p.more)
         out[page0 + lane] = -INFINITY;
       continue;
     }
-    const int next = page_ids(tile + 3 * W);
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    const int next = page_ids(tile + 2 * W);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     uint4 w[2][2][NC];
 #pragma unroll
     for (int x = 0; x < PIECES; ++x)
@@ -434,13 +434,12 @@ __global__ void __launch_bounds__(32 * kPScoreWarps)
                      "=r"(w[x / (2 * NC)][x / NC % 2][x % NC].y),
                      "=r"(w[x / (2 * NC)][x / NC % 2][x % NC].z),
                      "=r"(w[x / (2 * NC)][x / NC % 2][x % NC].w)
-                   : "r"(ring + (stage * PIECES + x) * 512)
+                   : "r"(ring + x * 512)
                    : "memory");
     const int now = id[0];
     id[0] = id[1];
-    id[1] = id[2];
-    id[2] = next;
-    load(id[1], stage);  // the tile after the next one
+    id[1] = next;
+    load(id[0]);
     float best[2] = {-INFINITY, -INFINITY};
 #pragma unroll 1
     for (int nt = 0; nt < n_nt; ++nt) {
@@ -741,7 +740,7 @@ cudaError_t bounds_t(const BoundsParams &p, dim3 grid, cudaStream_t stream) {
 
 template <int D, int S>
 cudaError_t scores_t(const PageScoreParams &p, unsigned grid, cudaStream_t stream) {
-  constexpr int kRing = kPScoreWarps * 2 * 16 * 4 * D;
+  constexpr int kRing = kPScoreWarps * 16 * 4 * D;
   constexpr int kRows = S == 1 ? kPageScoreRows : kPageScoreRowsF32;
   static_assert(kRows * pscore_row<D, S>() + kRing <= 227 * 1024, "shared memory");
   const size_t smem = (size_t)((p.rows + 7) / 8 * 8) * pscore_row<D, S>() + kRing;
@@ -774,11 +773,20 @@ cudaError_t launch_page_bounds(const BoundsParams &p, cudaStream_t stream) {
 cudaError_t launch_page_scores(PageScoreParams p, int sms, cudaStream_t stream) {
   const long long tiles = ((long long)p.max_blocks + 15) / 16;
   const long long units = (long long)p.batch * p.num_kv_heads;
-  // a warp's tiles one after another, so that the query rows are laid out
-  // once for several: but at least eight CTAs to an SM while there are tiles
-  long long per = tiles * units / ((long long)sms * 3 * kPScoreWarps);
-  per = per < 1 ? 1 : per > 8 ? 8 : per;
-  per *= kPScoreWarps;
+  // One wave of CTAs (four to an SM, or what its shared memory holds) if that is
+  // at most 12 tiles to a warp: the
+  // query rows are laid out once in each.  Else shorter parts, which even out
+  // ragged lengths (5 tiles to a warp 33 us where 16 take 38: 32 sequences of 8
+  // heads, up to 32,768 positions), not as short with many rows (40 rows over
+  // 131,072 positions of 8 sequences: 8 tiles 72 us, 3 tiles 79).
+  constexpr int W = kPScoreWarps;
+  const int splits = p.f32 ? 3 : 1;
+  const long long smem = (p.rows + 7) / 8 * 8LL * (4 * splits * p.head_dim + 16) +
+                         64LL * W * p.head_dim + 1024;
+  const long long fit = std::max(1LL, std::min(4LL, (228 << 10) / smem));
+  long long per = std::max(1LL, fit * sms / units);
+  per = std::max<long long>((tiles + per - 1) / per, W);
+  if (per > 12 * W) per = (p.rows > 32 ? 8 : 5) * W;
   const long long chunks = (tiles + per - 1) / per;
   if (chunks * units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   p.tiles_per_cta = (int)per;
