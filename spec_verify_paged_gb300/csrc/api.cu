@@ -830,7 +830,9 @@ int kv_page_bounds(const svp_dims *dims, const void *k_cache,
   p.dtype = dims->dtype;
   if ((long long)p.max_pages * p.num_kv_heads > (1LL << 31) - 64)
     return SVP_ERR_UNSUPPORTED;
-  if (launch_page_bounds(p, stream) != cudaSuccess) return SVP_ERR_CUDA;
+  const int sms = device_sms();
+  if (sms <= 0) return SVP_ERR_CUDA;
+  if (launch_page_bounds(p, sms, stream) != cudaSuccess) return SVP_ERR_CUDA;
   t_last_launches = 1;
   return SVP_OK;
 }

@@ -72,6 +72,43 @@ struct PairF16 {
     return *reinterpret_cast<const uint32_t *>(&v);
   }
 };
+// E4M3 codes as unsigned numbers of the same order (the sign bit flipped, all
+// bits of a negative code), each in the high byte of a 16-bit half, where the
+// byte below it only breaks ties.  So a word of four codes makes two registers
+// by three instructions and no conversion, and three-operand minima and maxima
+// take two rows at a time.  A NaN is the largest or the smallest.
+struct PairE4m3 {
+  static __device__ __forceinline__ uint32_t lo(uint32_t a, uint32_t b) {
+    return __vminu2(a, b);
+  }
+  static __device__ __forceinline__ uint32_t hi(uint32_t a, uint32_t b) {
+    return __vmaxu2(a, b);
+  }
+  static constexpr uint32_t kPosInf = 0xffffffffu, kNegInf = 0u;
+  // codes 0 and 2 of a word, codes 1 and 3
+  static __device__ __forceinline__ void split(uint32_t w, uint32_t &even,
+                                               uint32_t &odd) {
+    uint32_t sign;  // of each byte, in all of its bits
+    asm("prmt.b32 %0, %1, 0, 0xba98;" : "=r"(sign) : "r"(w));
+    odd = w ^ (sign | 0x80808080u);
+    even = odd << 8;
+  }
+  // the bounds' codes in the high bytes as bf16, low half and high half
+  static __device__ __forceinline__ uint32_t out(uint32_t l, uint32_t h, bool upper) {
+    const uint32_t x = upper ? h : l;
+    uint32_t sign;
+    asm("prmt.b32 %0, %1, 0, 0xba98;" : "=r"(sign) : "r"(x));
+    const uint32_t code = x ^ (~sign | 0x80808080u);
+    const uint32_t two = e4m3x2_f16x2(__byte_perm(code, 0, 0x4431));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&two));
+    __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
+    uint32_t r = *reinterpret_cast<const uint32_t *>(&v);
+    // a NaN among them
+    if ((h & 0xff00u) == 0xff00u || (l & 0xff00u) == 0u) r |= 0x7fffu;
+    if (h >= 0xff000000u || l < 0x01000000u) r |= 0x7fff0000u;
+    return r;
+  }
+};
 struct OneF32 {
   static __device__ __forceinline__ uint32_t lo(uint32_t a, uint32_t b) {
     float r;
@@ -88,7 +125,7 @@ struct OneF32 {
   static constexpr uint32_t kPosInf = 0x7f800000u, kNegInf = 0xff800000u;
 };
 template <> struct BoundType<SVP_BF16> { using P = PairBf16; };
-template <> struct BoundType<SVP_FP8_E4M3> { using P = PairF16; };
+template <> struct BoundType<SVP_FP8_E4M3> { using P = PairE4m3; };
 template <> struct BoundType<SVP_FP4_E2M1> { using P = PairF16; };
 template <> struct BoundType<SVP_F32> { using P = OneF32; };
 
@@ -117,8 +154,11 @@ __global__ void __launch_bounds__(32 * kBoundWarps)
   const int b = blockIdx.y;
   const int lane = threadIdx.x & 31;
   const unsigned item = blockIdx.x * kBoundWarps + (threadIdx.x >> 5);
-  const unsigned i = item / (unsigned)p.num_kv_heads;
-  const int g = (int)(item - i * (unsigned)p.num_kv_heads);
+  const unsigned shares = (unsigned)(p.num_kv_heads + p.heads - 1) / (unsigned)p.heads;
+  const unsigned i = item / shares;
+  const int g0 = (int)(item - i * shares) * p.heads;  // this warp's heads
+  // (rows of 256 bytes and more: one, and no loop)
+  const int g1 = ROWB >= 256 ? g0 + 1 : min(g0 + p.heads, p.num_kv_heads);
   const int L = p.seq_lens[b];
   if (L < 0 || L > (long long)p.max_blocks * kBlockSize) {
     if (threadIdx.x == 0) raise_pages(SVP_DEV_BAD_SEQ_LEN);
@@ -134,117 +174,141 @@ __global__ void __launch_bounds__(32 * kBoundWarps)
   }
   const int rows = min(L - page * kBlockSize, kBlockSize);
   const int r0 = lane / LPR, c = lane % LPR;
-  const unsigned char *src =
-      static_cast<const unsigned char *>(p.k_cache) +
-      ((size_t)phys * p.num_kv_heads + g) * (size_t)(kBlockSize * ROWB);
-  uint32_t lo[NR], hi[NR];
-#pragma unroll
-  for (int e = 0; e < NR; ++e) {
-    lo[e] = P::kPosInf;
-    hi[e] = P::kNegInf;
-  }
-  auto take = [&](const uint32_t (&w)[NR]) {
+#pragma unroll 1
+  for (int g = g0; g < g1; ++g) {
+    const unsigned char *src =
+        static_cast<const unsigned char *>(p.k_cache) +
+        ((size_t)phys * p.num_kv_heads + g) * (size_t)(kBlockSize * ROWB);
+    uint32_t lo[NR], hi[NR];
 #pragma unroll
     for (int e = 0; e < NR; ++e) {
-      lo[e] = P::lo(lo[e], w[e]);
-      hi[e] = P::hi(hi[e], w[e]);
+      lo[e] = P::kPosInf;
+      hi[e] = P::kNegInf;
     }
-  };
-  if constexpr (DT == SVP_FP4_E2M1) {
-    uint32_t w[NA][2], sc[NA];
+    auto take = [&](const uint32_t (&w)[NR]) {
 #pragma unroll
-    for (int a = 0; a < NA; ++a) {
-      const int r = min(a * RPA + r0, rows - 1);  // rows past the end: the last
-      const uint32_t *row = reinterpret_cast<const uint32_t *>(src + r * ROWB);
-      w[a][0] = __ldg(row + 2 * c);
-      w[a][1] = __ldg(row + 2 * c + 1);
-      sc[a] = __ldg(src + r * ROWB + D / 2 + c);
-    }
-#pragma unroll
-    for (int a = 0; a < NA; ++a) {
-      uint32_t v[NR], h[4];
-      const uint32_t s2 = e4m3x2_f16x2(sc[a] * 0x101u);
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        e2m1x8_h2(w[a][x], h);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * x + e] = hmul2(h[e], s2);
+      for (int e = 0; e < NR; ++e) {
+        lo[e] = P::lo(lo[e], w[e]);
+        hi[e] = P::hi(hi[e], w[e]);
       }
-      take(v);
-    }
-  } else {
-    uint4 w[NA];
+    };
+    if constexpr (DT == SVP_FP4_E2M1) {
+      uint32_t w[NA][2], sc[NA];
 #pragma unroll
-    for (int a = 0; a < NA; ++a) {
-      const int r = min(a * RPA + r0, rows - 1);
-      w[a] = __ldg(reinterpret_cast<const uint4 *>(src + r * ROWB) + c);
-    }
+      for (int a = 0; a < NA; ++a) {
+        const int r = min(a * RPA + r0, rows - 1);  // rows past the end: the last
+        const uint32_t *row = reinterpret_cast<const uint32_t *>(src + r * ROWB);
+        w[a][0] = __ldg(row + 2 * c);
+        w[a][1] = __ldg(row + 2 * c + 1);
+        sc[a] = __ldg(src + r * ROWB + D / 2 + c);
+      }
 #pragma unroll
-    for (int a = 0; a < NA; ++a) {
-      const uint32_t x[4] = {w[a].x, w[a].y, w[a].z, w[a].w};
-      if constexpr (DT == SVP_FP8_E4M3) {
-        uint32_t v[NR];
+      for (int a = 0; a < NA; ++a) {
+        uint32_t v[NR], h[4];
+        const uint32_t s2 = e4m3x2_f16x2(sc[a] * 0x101u);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[2 * e] = e4m3x2_f16x2(x[e]);
-          v[2 * e + 1] = e4m3x2_f16x2(x[e] >> 16);
+        for (int x = 0; x < 2; ++x) {
+          e2m1x8_h2(w[a][x], h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[4 * x + e] = hmul2(h[e], s2);
         }
         take(v);
+      }
+    } else {
+      uint4 w[NA];
+#pragma unroll
+      for (int a = 0; a < NA; ++a) {
+        const int r = min(a * RPA + r0, rows - 1);
+        w[a] = __ldg(reinterpret_cast<const uint4 *>(src + r * ROWB) + c);
+      }
+      if constexpr (DT == SVP_FP8_E4M3) {
+#pragma unroll
+        for (int a = 0; a < NA; a += 2) {
+          const uint32_t x[4] = {w[a].x, w[a].y, w[a].z, w[a].w};
+          const uint32_t y[4] = {w[a + 1].x, w[a + 1].y, w[a + 1].z, w[a + 1].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t u[2], v[2];
+            P::split(x[e], u[0], u[1]);
+            P::split(y[e], v[0], v[1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              lo[2 * e + h] = __vimin3_u16x2(lo[2 * e + h], u[h], v[h]);
+              hi[2 * e + h] = __vimax3_u16x2(hi[2 * e + h], u[h], v[h]);
+            }
+          }
+        }
       } else {
-        take(x);
+#pragma unroll
+        for (int a = 0; a < NA; ++a) {
+          const uint32_t x[4] = {w[a].x, w[a].y, w[a].z, w[a].w};
+          take(x);
+        }
       }
     }
-  }
-  // Lanes that hold the same elements of other rows: in each step a lane hands
-  // half of its registers to its partner and keeps the other half, so at the
-  // end it has the bounds of NR / RPA (of one if there are fewer) registers.
-  int base = 0;  // the first register's place among the row's
+    // Lanes that hold the same elements of other rows: in each step a lane hands
+    // half of its registers to its partner and keeps the other half, so at the
+    // end it has the bounds of NR / RPA (of one if there are fewer) registers.
+    int base = 0;  // the first register's place among the row's
 #pragma unroll
-  for (int off = 16, left = NR; off >= LPR; off >>= 1) {
-    const bool up = (lane & off) != 0;
-    if (left > 1) {
-      left /= 2;
+    for (int off = 16, left = NR; off >= LPR; off >>= 1) {
+      const bool up = (lane & off) != 0;
+      if (left > 1) {
+        left /= 2;
 #pragma unroll
-      for (int e = 0; e < NR / 2; ++e) {
-        if (e >= left) break;
-        const uint32_t l = up ? lo[e] : lo[e + left], h = up ? hi[e] : hi[e + left];
-        const uint32_t ml = up ? lo[e + left] : lo[e], mh = up ? hi[e + left] : hi[e];
-        lo[e] = P::lo(ml, __shfl_xor_sync(kFull, l, off));
-        hi[e] = P::hi(mh, __shfl_xor_sync(kFull, h, off));
+        for (int e = 0; e < NR / 2; ++e) {
+          if (e >= left) break;
+          const uint32_t l = up ? lo[e] : lo[e + left], h = up ? hi[e] : hi[e + left];
+          const uint32_t ml = up ? lo[e + left] : lo[e], mh = up ? hi[e + left] : hi[e];
+          lo[e] = P::lo(ml, __shfl_xor_sync(kFull, l, off));
+          hi[e] = P::hi(mh, __shfl_xor_sync(kFull, h, off));
+        }
+        base += up ? left : 0;
+      } else {
+        lo[0] = P::lo(lo[0], __shfl_xor_sync(kFull, lo[0], off));
+        hi[0] = P::hi(hi[0], __shfl_xor_sync(kFull, hi[0], off));
       }
-      base += up ? left : 0;
-    } else {
-      lo[0] = P::lo(lo[0], __shfl_xor_sync(kFull, lo[0], off));
-      hi[0] = P::hi(hi[0], __shfl_xor_sync(kFull, hi[0], off));
     }
-  }
-  constexpr int LEFT = NR / RPA > 1 ? NR / RPA : 1;
-  unsigned char *dst = static_cast<unsigned char *>(p.bounds) +
-                       ((size_t)phys * p.num_kv_heads + g) * (4 * D) + c * (2 * V);
+    constexpr int LEFT = NR / RPA > 1 ? NR / RPA : 1;
+    unsigned char *dst = static_cast<unsigned char *>(p.bounds) +
+                         ((size_t)phys * p.num_kv_heads + g) * (4 * D) + c * (2 * V);
 #pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    const uint32_t *from = side ? hi : lo;
-    unsigned char *to = dst + side * (2 * D);
-    if constexpr (DT == SVP_F32) {
-      uint16_t *const t16 = reinterpret_cast<uint16_t *>(to) + base;
-      if constexpr (LEFT == 4)
-        *reinterpret_cast<uint2 *>(t16) = make_uint2(
-            bf16_outward(__uint_as_float(from[0]), side) |
-                (bf16_outward(__uint_as_float(from[1]), side) << 16),
-            bf16_outward(__uint_as_float(from[2]), side) |
-                (bf16_outward(__uint_as_float(from[3]), side) << 16));
-      else
-        *reinterpret_cast<uint32_t *>(t16) =
-            bf16_outward(__uint_as_float(from[0]), side) |
-            (bf16_outward(__uint_as_float(from[1]), side) << 16);
-    } else {
-      uint32_t *const t32 = reinterpret_cast<uint32_t *>(to) + base;
-      if constexpr (LEFT >= 2)
-        *reinterpret_cast<uint2 *>(t32) =
-            make_uint2(P::out(from[0], side), P::out(from[1], side));
-      else
-        *t32 = P::out(from[0], side);
-      static_assert(LEFT <= 2, "pairs at most");
+    for (int side = 0; side < 2; ++side) {
+      const uint32_t *from = side ? hi : lo;
+      unsigned char *to = dst + side * (2 * D);
+      if constexpr (DT == SVP_F32) {
+        uint16_t *const t16 = reinterpret_cast<uint16_t *>(to) + base;
+        if constexpr (LEFT == 4)
+          *reinterpret_cast<uint2 *>(t16) = make_uint2(
+              bf16_outward(__uint_as_float(from[0]), side) |
+                  (bf16_outward(__uint_as_float(from[1]), side) << 16),
+              bf16_outward(__uint_as_float(from[2]), side) |
+                  (bf16_outward(__uint_as_float(from[3]), side) << 16));
+        else
+          *reinterpret_cast<uint32_t *>(t16) =
+              bf16_outward(__uint_as_float(from[0]), side) |
+              (bf16_outward(__uint_as_float(from[1]), side) << 16);
+      } else if constexpr (DT == SVP_FP8_E4M3) {
+        // registers come in pairs: elements 0 and 2, elements 1 and 3 of a word
+        uint16_t *const t16 = reinterpret_cast<uint16_t *>(to) + base / 2 * 4;
+        if constexpr (LEFT == 2) {
+          const uint32_t even = P::out(lo[0], hi[0], side), odd = P::out(lo[1], hi[1], side);
+          *reinterpret_cast<uint2 *>(t16) = make_uint2(__byte_perm(even, odd, 0x5410),
+                                                       __byte_perm(even, odd, 0x7632));
+        } else {
+          const uint32_t v = P::out(lo[0], hi[0], side);
+          t16[base & 1] = (uint16_t)v;
+          t16[(base & 1) + 2] = (uint16_t)(v >> 16);
+        }
+      } else {
+        uint32_t *const t32 = reinterpret_cast<uint32_t *>(to) + base;
+        if constexpr (LEFT >= 2)
+          *reinterpret_cast<uint2 *>(t32) =
+              make_uint2(P::out(from[0], side), P::out(from[1], side));
+        else
+          *t32 = P::out(from[0], side);
+        static_assert(LEFT <= 2, "pairs at most");
+      }
     }
   }
 }
@@ -757,8 +821,17 @@ cudaError_t scores_t(const PageScoreParams &p, unsigned grid, cudaStream_t strea
 
 }  // namespace
 
-cudaError_t launch_page_bounds(const BoundsParams &p, cudaStream_t stream) {
-  const long long items = (long long)p.max_pages * p.num_kv_heads;
+cudaError_t launch_page_bounds(BoundsParams p, int sms, cudaStream_t stream) {
+  // a warp takes heads of a page of 4 KB in all, so that its look-ups serve more
+  // than 1 KB, once there are enough warps all the same
+  const int row = p.dtype == SVP_F32        ? 4 * p.head_dim
+                  : p.dtype == SVP_BF16     ? 2 * p.head_dim
+                  : p.dtype == SVP_FP8_E4M3 ? p.head_dim
+                                            : fp4_row_bytes(p.head_dim);
+  p.heads = std::max(1, 256 / row);
+  if ((long long)p.batch * p.max_pages * p.num_kv_heads < 256LL * sms) p.heads = 1;
+  const long long items =
+      (long long)p.max_pages * ((p.num_kv_heads + p.heads - 1) / p.heads);
   const long long blocks = (items + kBoundWarps - 1) / kBoundWarps;
   if (blocks > 0x7fffffffLL / kBoundWarps) return cudaErrorInvalidConfiguration;
   const dim3 grid((unsigned)blocks, (unsigned)p.batch);

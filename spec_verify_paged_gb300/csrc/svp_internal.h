@@ -233,8 +233,9 @@ struct BoundsParams {
   int batch, num_kv_heads, head_dim, n_new, max_blocks, num_blocks;
   int max_pages;              // bound of the pages that n_new positions touch
   int dtype;
+  int heads;                  // set by the launcher: heads that a warp takes
 };
-cudaError_t launch_page_bounds(const BoundsParams &p, cudaStream_t stream);
+cudaError_t launch_page_bounds(BoundsParams p, int sms, cudaStream_t stream);
 
 struct PageScoreParams {
   const void *q;
