@@ -390,7 +390,8 @@ int kv_evict(const svp_dims *dims, void *k_cache, void *v_cache, float *scores,
  * stay as they are.  A page that several sequences of a call hold is full in
  * all of them, or in each to the same row.  After rows were taken back
  * (rejected drafts) the bounds may be wider than the keys until the page is
- * appended to again: still bounds.  A length outside [0,
+ * appended to again: still bounds.  Rows that kv_evict has moved need their
+ * pages' bounds anew (n_new of the whole sequence).  A length outside [0,
  * max_blocks_per_seq*16] updates nothing and sets SVP_DEV_BAD_SEQ_LEN, a bad
  * block id sets SVP_DEV_BAD_BLOCK_ID.  One launch, no workspace.
  * Errors as for kv_append (n_new >= 0, no upper limit); SVP_ERR_UNSUPPORTED
@@ -429,8 +430,8 @@ int paged_page_scores(const svp_dims *dims, const void *q, const void *bounds,
  * all -1 and SVP_DEV_BAD_SEQ_LEN.  One launch, no workspace; deterministic.
  * Errors: SVP_ERR_INVALID_ARG for null or misaligned pointers, batch < 0,
  * heads < 1, max_blocks < 0, n_select < 1, n_sink < 0, n_recent < 0 or
- * n_sink + n_recent > n_select; SVP_ERR_UNSUPPORTED for batch > 65535 or
- * max_blocks > 2^26. */
+ * n_sink + n_recent > n_select; SVP_ERR_UNSUPPORTED for batch > 65535,
+ * max_blocks > 2^26 or n_select > 2^26. */
 int paged_select_pages(int batch, int heads, int max_blocks,
                        const float *scores, const int32_t *seq_lens,
                        int n_select, int n_sink, int n_recent, int32_t *pages,
@@ -452,7 +453,8 @@ int paged_select_pages(int batch, int heads, int max_blocks,
  * One launch, no workspace (dims->workspace is not used); dims->split_pages:
  * fewest list entries of a CTA (0: automatic).
  * Errors: those of paged_decode_attention, SVP_ERR_INVALID_ARG for
- * n_select < 1, SVP_ERR_UNSUPPORTED for a kernel_path other than AUTO. */
+ * n_select < 1, SVP_ERR_UNSUPPORTED for n_select > 2^26 or a kernel_path other
+ * than AUTO. */
 int paged_sparse_attention(const svp_dims *dims, const void *q,
                            const void *k_cache, const void *v_cache,
                            const int32_t *block_table, const int32_t *seq_lens,

@@ -892,7 +892,8 @@ int paged_select_pages(int batch, int heads, int max_blocks,
   if (batch < 0 || heads < 1 || max_blocks < 0 || n_select < 1 || n_sink < 0 ||
       n_recent < 0 || (long long)n_sink + n_recent > n_select)
     return SVP_ERR_INVALID_ARG;
-  if (batch > kMaxBatch || max_blocks > (1 << 26)) return SVP_ERR_UNSUPPORTED;
+  if (batch > kMaxBatch || max_blocks > kMaxPages || n_select > kMaxPages)
+    return SVP_ERR_UNSUPPORTED;
   if (batch == 0) return SVP_OK;
   if ((max_blocks > 0 && !scores) || !seq_lens || !pages)
     return SVP_ERR_INVALID_ARG;
@@ -924,7 +925,8 @@ int paged_sparse_attention(const svp_dims *dims, const void *q,
   const int st = check_attention_args(dims, q_len, 0, 0, scale);
   if (st != SVP_OK) return st;
   if (n_select < 1) return SVP_ERR_INVALID_ARG;
-  if (dims->kernel_path != SVP_PATH_AUTO) return SVP_ERR_UNSUPPORTED;
+  if (dims->kernel_path != SVP_PATH_AUTO || n_select > kMaxPages)
+    return SVP_ERR_UNSUPPORTED;
   if (dims->batch == 0) return SVP_OK;
   if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !pages ||
       !out || !lse)

@@ -145,8 +145,9 @@ __global__ void __launch_bounds__(kAssignThreads)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const u64 me = (u64)rank * kAssignThreads + tid;
   const u64 all = (u64)nc * kAssignThreads;
+  // (nothing may start early after this one: the next kernel's block table
+  // and lengths are what it writes)
   pdl_wait();
-  pdl_launch_dependents();
   const int F = *p.free_count;
   const Ask a = ask_of(p, tid);
   if (a.bad && rank == 0) raise_assign(SVP_DEV_BAD_SEQ_LEN);
@@ -250,8 +251,9 @@ __global__ void __launch_bounds__(kAssignThreads)
   const int tid = threadIdx.x;
   const u64 me = (u64)rank * kAssignThreads + tid;
   const u64 all = (u64)nc * kAssignThreads;
+  // (nothing may start early after this one: the next kernel's block table
+  // and lengths are what it writes)
   pdl_wait();
-  pdl_launch_dependents();
   const bool leader = rank == 0;
   const int F = *p.free_count;
 

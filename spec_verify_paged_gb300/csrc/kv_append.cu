@@ -269,8 +269,8 @@ __global__ void __launch_bounds__(256) kv_append_slots_kernel(const AppendSlotsP
 #pragma unroll
       for (int h = 0; h < (FP4 ? 2 : 1); ++h)
         in[u][side][h] =
-            __ldg(static_cast<const uint4 *>(side ? p.v_new : p.k_new) + from + h);
-    slot[u] = __ldg(p.slots + token);
+            static_cast<const uint4 *>(side ? p.v_new : p.k_new)[from + h];
+    slot[u] = p.slots[token];
     if (slot[u] >= (long long)p.num_blocks * kBlockSize) {
       atomicOr(&g_status_append, (unsigned)SVP_DEV_BAD_BLOCK_ID);
       slot[u] = -1;

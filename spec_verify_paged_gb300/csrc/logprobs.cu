@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kLpThreads)
           (uint32_t)reinterpret_cast<const uint16_t *>(base)[t] << 16);
   };
   auto may = [&](int t) {
-    return !allowed || ((__ldg(allowed + (t >> 5)) >> (t & 31)) & 1u);
+    return !allowed || ((allowed[t >> 5] >> (t & 31)) & 1u);
   };
   const float xt = element(token);
   const unsigned kt = may(token) ? logit_key(xt) : 0u;
@@ -306,16 +306,16 @@ __global__ void __launch_bounds__(kLpThreads)
   auto bits_of = [&](int i) {
     const int t0 = t00 + i * VEC;
     if (shift == 0) {  // they lie in one byte
-      const uint32_t y = __ldg(reinterpret_cast<const unsigned char *>(allowed) + t0 / 8);
+      const uint32_t y = *(reinterpret_cast<const unsigned char *>(allowed) + t0 / 8);
       return VEC == 8 ? y : y >> (t0 & 4);
     }
-    const uint32_t w0 = __ldg(allowed + (t0 >> 5));
-    const uint32_t w1 = (t0 & 31) + VEC > 32 ? __ldg(allowed + (t0 >> 5) + 1) : 0u;
+    const uint32_t w0 = allowed[t0 >> 5];
+    const uint32_t w1 = (t0 & 31) + VEC > 32 ? allowed[(t0 >> 5) + 1] : 0u;
     return __funnelshift_r(w0, w1, t0 & 31);
   };
   // vector i as it counts: with -inf for what is not allowed
   auto fetch = [&](int i) {
-    const uint4 v = __ldg(aligned + i);
+    const uint4 v = aligned[i];
     return allowed ? V::masked(v, bits_of(i)) : v;
   };
 
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kLpThreads)
       uint32_t bits[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        v[u] = i + u * T < n_vec ? __ldg(aligned + i + u * T) : V::none();
+        v[u] = i + u * T < n_vec ? aligned[i + u * T] : V::none();
       if (allowed) {
 #pragma unroll
         for (int u = 0; u < U; ++u) bits[u] = i + u * T < n_vec ? bits_of(i + u * T) : 0u;

@@ -198,9 +198,9 @@ __global__ void __launch_bounds__(32 * kBoundWarps)
       for (int a = 0; a < NA; ++a) {
         const int r = min(a * RPA + r0, rows - 1);  // rows past the end: the last
         const uint32_t *row = reinterpret_cast<const uint32_t *>(src + r * ROWB);
-        w[a][0] = __ldg(row + 2 * c);
-        w[a][1] = __ldg(row + 2 * c + 1);
-        sc[a] = __ldg(src + r * ROWB + D / 2 + c);
+        w[a][0] = row[2 * c];
+        w[a][1] = row[2 * c + 1];
+        sc[a] = src[r * ROWB + D / 2 + c];
       }
 #pragma unroll
       for (int a = 0; a < NA; ++a) {
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(32 * kBoundWarps)
 #pragma unroll
       for (int a = 0; a < NA; ++a) {
         const int r = min(a * RPA + r0, rows - 1);
-        w[a] = __ldg(reinterpret_cast<const uint4 *>(src + r * ROWB) + c);
+        w[a] = *(reinterpret_cast<const uint4 *>(src + r * ROWB) + c);
       }
       if constexpr (DT == SVP_FP8_E4M3) {
 #pragma unroll
@@ -355,7 +355,7 @@ __device__ __forceinline__ void stage_query(const PageScoreParams &p, unsigned c
   if constexpr (S == 1) {
     uint4 v = make_uint4(0, 0, 0, 0);
     if (there)
-      v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + at) + c);
+      v = *(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + at) + c);
     const uint32_t flip = p.negate ? 0x80008000u : 0u;
     const uint32_t w[4] = {v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip};
     uint32_t neg[4], pos[4];
@@ -372,7 +372,7 @@ __device__ __forceinline__ void stage_query(const PageScoreParams &p, unsigned c
     if (there) {
       const float4 *from =
           reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + at) + 2 * c;
-      const float4 u = __ldg(from), v = __ldg(from + 1);
+      const float4 u = from[0], v = from[1];
       x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
       x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
     }
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(kPickMax)
   if constexpr (KEYS > 0) {
 #pragma unroll
     for (int i = 0; i < KEYS; ++i)
-      x[i] = i * T + tid < p.max_blocks ? __ldg(scores + i * T + tid) : 0.f;
+      x[i] = i * T + tid < p.max_blocks ? scores[i * T + tid] : 0.f;
   }
   int n = (int)(((long long)L + kBlockSize - 1) / kBlockSize);
   if (L < 0 || n > p.max_blocks) {
@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(kPickMax)
       for (int i = 0; i < KEYS; ++i)
         if (key[i] != 0u) f(key[i]);
     } else {
-      for (int j = c0 + tid; j < c1; j += T) f(pick_key(__ldg(scores + j)));
+      for (int j = c0 + tid; j < c1; j += T) f(pick_key(scores[j]));
     }
   };
   unsigned edge = 0xffffffffu, ties = 0;  // kept: above the edge, and ties at it
@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(kPickMax)
     for (int i = 0, j0 = 0; j0 < n; ++i, j0 += T) {
       const int j = j0 + tid;
       unsigned sure, tied;
-      look(j, k > 0 && j >= c0 && j < c1 ? pick_key(__ldg(scores + j)) : 0u, sure, tied);
+      look(j, k > 0 && j >= c0 && j < c1 ? pick_key(scores[j]) : 0u, sure, tied);
       unsigned *const row = sm.cells + 32 * (i & 1);
       if (lane == 0) row[warp] = (__popc(sure) << 16) | __popc(tied);
       __syncthreads();

@@ -13,6 +13,7 @@ constexpr int kBlockSize = 16;     // tokens per KV page
 constexpr int kMaxQLen = 16;
 constexpr int kMaxBatch = 65535;
 constexpr int kMaxDraft = 15;
+constexpr int kMaxPages = 1 << 26; // listed pages, pages to choose from
 constexpr int kMaxNodes = 16;    // draft-tree nodes (= the verify rows)
 
 // One paged_decode_attention launch.

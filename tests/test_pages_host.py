@@ -85,6 +85,7 @@ def test_select_arguments(lib):
         assert call(**bad) == -1, bad
     assert call(batch=65536) == -2
     assert call(blocks=2 ** 26 + 1) == -2
+    assert call(n=2 ** 26 + 1) == -2
     assert call(batch=0, ptrs=(None, None), out=None) == 0
     assert lib.svp_last_launch_count() == 0
 
@@ -106,6 +107,7 @@ def test_sparse_attention_arguments(lib):
     assert call(_dims(head_dim=80)) == -2
     for path in (1, 2, 3):
         assert call(_dims(kernel_path=path)) == -2
+    assert call(_dims(), n=2 ** 26 + 1) == -2
     assert call(_dims(dtype=3, v_scale=0.0)) == -1
     assert call(_dims(split_pages=-1)) == -1
     assert call(_dims(max_blocks_per_seq=0)) == -1
