@@ -70,7 +70,7 @@ struct SpShape {
   // pages that a warp takes at once: two where latency counts more than room
   // and registers (their products are independent chains, one vote serves both)
   static constexpr int AT_ONCE = PAGE < 4096 && DT != SVP_F32 && NT > 1 ? 2 : 1;
-  static constexpr int ROWS = 8 * NT;             // of a unit
+  static constexpr int ROWS = NT == 0 ? 4 : 8 * NT;  // of a unit
   static constexpr int WARP = STAGES * 2 * PAGE;  // a warp's ring
   // the warps' results take the rings' place at the end
   static constexpr int RES_ROW = 4 * D + 16;
@@ -606,12 +606,12 @@ struct WarpMma {
   }
 };
 
-// A warp's state over an fp32 cache: 8 rows.  Scores: lane = key + 16 half of
+// A warp's state over an fp32 cache: R rows.  Scores: lane = key + 16 half of
 // the dimensions; values: a lane owns 4 dimensions (of half the keys for D 64).
-template <int D>
+template <int D, int R>
 struct WarpF32 {
-  static constexpr int RPW = 8;
-  using S = SpShape<SVP_F32, D, 1>;
+  static constexpr int RPW = R;
+  using S = SpShape<SVP_F32, D, R == 4 ? 0 : 1>;
   static constexpr int QROW = S::QROW, ROWB = S::ROWB;
   float4 o[RPW];
   float ref[RPW], sum[RPW];
@@ -764,7 +764,7 @@ struct WarpOf {
 };
 template <int D, int NT>
 struct WarpOf<SVP_F32, D, NT> {
-  using T = WarpF32<D>;
+  using T = WarpF32<D, NT == 0 ? 4 : 8>;
 };
 
 template <int DT, int D, int NT>
@@ -1005,7 +1005,8 @@ cudaError_t sparse_rows(SparseParams p, int sms, cudaStream_t stream) {
   constexpr int MOST = DT == SVP_F32 ? 8 : 8 * kSpTiles;
   p.n_rb = (p.rows + MOST - 1) / MOST;
   const int nt = ((p.rows + p.n_rb - 1) / p.n_rb + 7) / 8;
-  p.n_rb = (p.rows + 8 * nt - 1) / (8 * nt);
+  const bool few = DT == SVP_F32 && p.rows <= 4;
+  p.n_rb = few ? 1 : (p.rows + 8 * nt - 1) / (8 * nt);
   const long long units = (long long)p.batch * p.num_kv_heads * p.n_rb;
   // split a list while the CTAs all find room and keep eight pages, or to the
   // caller's pages per CTA
@@ -1014,7 +1015,9 @@ cudaError_t sparse_rows(SparseParams p, int sms, cudaStream_t stream) {
   while (splits < 8 && 2LL * splits * least <= p.n_select &&
          (p.split_pages > 0 || units * splits * 2 <= 2LL * sms))
     splits *= 2;
-  if constexpr (DT == SVP_F32) return sparse_t<DT, D, 1>(p, splits, stream);
+  if constexpr (DT == SVP_F32)
+    return few ? sparse_t<DT, D, 0>(p, splits, stream)
+               : sparse_t<DT, D, 1>(p, splits, stream);
   else
     return nt == 1   ? sparse_t<DT, D, 1>(p, splits, stream)
            : nt == 2 ? sparse_t<DT, D, 2>(p, splits, stream)
