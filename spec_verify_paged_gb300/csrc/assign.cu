@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kAssignThreads)
 cudaError_t launch_assign_pages(const AssignParams &p, cudaStream_t stream) {
   // one CTA for a decode step's few entries, eight where there may be many
   const bool many = p.n_slots > 4 * kAssignThreads ||
-                    (!p.slots && (long long)p.batch * p.max_blocks > 64 * kAssignThreads);
+                    (!p.slots && (long long)p.batch * p.max_blocks > 4 * kAssignThreads);
   const int nc = many ? 8 : 1;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
