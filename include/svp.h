@@ -633,8 +633,8 @@ int spec_accept_tree(int batch, int num_nodes, int vocab,
  * gives the same and sets SVP_DEV_BAD_TOKEN.  A row that allows nothing has
  * logprob -inf and entropy 0.  A NaN or +inf among a row's allowed logits
  * makes its log probabilities and entropy NaN; NaN ranks above +inf.
- * Logits are read once; sums are fp32.  One launch, no workspace;
- * deterministic.
+ * Logits are read once, few of them again for the alternatives; sums are
+ * fp32.  One launch, no workspace; deterministic.
  * Errors: SVP_ERR_INVALID_ARG for null or misaligned pointers (logits to their
  * elements), rows < 0, vocab < 2, n_top < 0, another dtype, temperature <= 0
  * or not finite; SVP_ERR_UNSUPPORTED for vocab > 320000, n_top > 64 or

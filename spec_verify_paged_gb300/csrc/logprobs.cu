@@ -9,8 +9,8 @@
 // probability, so one pass of exponentials gives everything but the order.
 //
 // A cluster of 1 to 8 CTAs takes a row; a thread's vectors lie a CTA's width
-// apart.  What bounds it for long rows is instructions, about eleven an element
-// (with a mask fourteen), and what a CTA does once: so a row takes as few CTAs as
+// apart.  What bounds it for long rows is instructions, about twelve an element
+// (nineteen with a mask and alternatives), and what a CTA does once: so a row takes as few CTAs as
 // fill the GPU, two fp32 values are multiplied and added at once, what can be
 // done on pairs of bf16 is (the maximum, the count of the tokens ahead), and few
 // vectors are looked at again, out of L2, for the alternatives.  Tried on 512
@@ -24,6 +24,11 @@
 // are gathered and ranked by counting.  Where many do (equal logits), the k-th
 // largest is found bit by bit instead.  Equal logits are ordered by token, so
 // no result depends on the order of atomics.
+//
+// Measured: 512 rows of 131,072 bf16: 36 us, 44 with 20 alternatives, 52 with
+// those and a mask (0.54, 0.45 and 0.40 of the copy rate; issue active 61 %);
+// fp32 54 and 70 (0.73, 0.57).  80 rows of 32,000 fp32, 5 alternatives: 9 us with
+// 40 % of them padding, 10.7 with none.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
