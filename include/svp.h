@@ -426,7 +426,7 @@ int paged_page_scores(const svp_dims *dims, const void *q, const void *bounds,
  * page; NaN ranks above everything), in increasing order, then -1.  A sequence
  * of at most n_select pages keeps all of them.  scores [batch, heads,
  * max_blocks] fp32, pages [batch, heads, n_select] int32; scores of forced
- * pages and past n are not read.  A length outside [0, max_blocks*16] gives
+ * pages and past n may hold anything.  A length outside [0, max_blocks*16] gives
  * all -1 and SVP_DEV_BAD_SEQ_LEN.  One launch, no workspace; deterministic.
  * Errors: SVP_ERR_INVALID_ARG for null or misaligned pointers, batch < 0,
  * heads < 1, max_blocks < 0, n_select < 1, n_sink < 0, n_recent < 0 or

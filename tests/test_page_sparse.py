@@ -329,6 +329,9 @@ def _check(dtype, d, out, lse, ref):
     (128, 1, 8, 8, 12, 4),     # 64 rows
     (128, 2, 5, 13, 12, 0),    # 65 rows: two units
     (64, 1, 33, 4, 5, 1),      # 132 rows
+    (64, 2, 4, 3, 13, 0),      # 12 rows
+    (128, 2, 8, 2, 13, 1),     # 16 rows, clusters
+    (64, 1, 8, 3, 11, 2),      # 24 rows
 ])
 def test_sparse(svp, dtype, d, hkv, group, ql, n_select, split):
     rng = np.random.default_rng(d + group + ql + n_select)
@@ -356,10 +359,12 @@ def test_sparse_long_lists(svp, dtype):
     lens = [300, 17]
     lists = rng.integers(-3, 19, (2, 2, 1500)).astype(np.int32)
     lists[1] = np.minimum(lists[1], 1)
-    for split in (1500, 0):
-        out, lse, ref = _sparse(svp, rng, dtype, 64, 2, 2, 1, lens, 1500, split, lists=lists)
+    for split, d, group, ql in ((1500, 64, 2, 1), (0, 64, 2, 1), (1500, 128, 4, 3),
+                                (0, 64, 7, 3)):
+        out, lse, ref = _sparse(svp, rng, dtype, d, 2, group, ql, lens, 1500, split,
+                                lists=lists)
         assert svp.read_device_status() == 0
-        _check(dtype, 64, out, lse, ref)
+        _check(dtype, d, out, lse, ref)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
