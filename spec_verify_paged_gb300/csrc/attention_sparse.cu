@@ -858,7 +858,7 @@ __global__ void __launch_bounds__(SpShape<DT, D, NT>::THREADS, 2)
     }
     if (at + kListCap < hi) look(at + kListCap);
     __syncthreads();
-    // this warp's pages: every fourth
+    // this warp's pages: every W-th
     const int n_mine = (count - warp + W - 1) / W;
     constexpr int NP = S::AT_ONCE, AHEAD = STAGES - NP;  // on their way at a time
     static_assert(STAGES % NP == 0, "a step's stages lie side by side");
