@@ -10,10 +10,11 @@
 //
 // A cluster of 1 to 8 CTAs takes a row; a thread's vectors lie a CTA's width
 // apart.  What bounds it for long rows is instructions, about twelve an element
-// (nineteen with a mask and alternatives), and what a CTA does once: so a row takes as few CTAs as
-// fill the GPU, two fp32 values are multiplied and added at once, what can be
-// done on pairs of bf16 is (the maximum, the count of the tokens ahead), and few
-// vectors are looked at again, out of L2, for the alternatives.  Tried on 512
+// (nineteen with a mask and alternatives), and what a CTA does once: so a row
+// takes as few CTAs as fill the GPU, two fp32 values are multiplied and added at
+// once, what can be done on pairs of bf16 is (the maximum, the count of the
+// tokens ahead), and few vectors are looked at again, out of L2, for the
+// alternatives.  Tried on 512
 // masked rows of 131,072 bf16: the row in registers, with everything unrolled,
 // 148 us (waiting for instructions); in shared memory, four CTAs a row, 98.  The
 // CTAs' sums meet in the first one's shared memory at the end, by one cluster
