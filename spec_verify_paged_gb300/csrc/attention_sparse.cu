@@ -6,14 +6,14 @@
 // What bounds it: the listed K and V rows' bytes, each read once, while a kv
 // head has few query rows; the chain of a page's products and softmax beyond.
 //
-// A cluster of 1 to 8 CTAs takes a unit: a (sequence, kv head) and up to 32 of
+// A cluster of 1 to 16 CTAs takes a unit: a (sequence, kv head) and up to 32 of
 // its query rows (8 over an fp32 cache).  Its CTAs split the list and their
 // warps deal out the pages; the results meet in distributed shared memory, so
 // a call is one launch, without partials in memory.  Every warp copies its own
 // pages (cp.async, a ring of three or four, in steps of one page or two), so
-// no barrier joins the warps in between.  The 16-byte pieces are swizzled on the way so that the matrix
-// operands are read without bank conflicts.  Rows of a page past the
-// sequence's end are filled with zeros instead of being read.
+// no barrier joins the warps in between.  The 16-byte pieces are swizzled on
+// the way so that the matrix operands are read without bank conflicts.  Rows of
+// a page past the sequence's end are filled with zeros instead of being read.
 //
 //  * Keys are the M of mma.sync m16n8k16, query rows the N: S^T = K Q^T,
 //    O^T = V^T P^T, so a page's operands are made once for all rows of the
@@ -58,6 +58,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kSpTiles = 4;         // most n8 tiles of query rows of a unit
+constexpr int kSpCluster = 16;      // most CTAs of a unit; above 8 by leave
 constexpr int kListCap = 512;       // list entries a CTA looks up at once
 constexpr int kNoPage = 0x7ffffff0; // first position of a page that is not there
 constexpr float kSpNoRef = -3e38f;  // below any score
@@ -950,30 +951,38 @@ __global__ void __launch_bounds__(SpShape<DT, D, NT>::THREADS, 2)
   cluster.sync();
   for (int x = rank * T + tid; x < rows * (D / 4); x += nc * T) {
     const int r = x / (D / 4), c = x % (D / 4);
-    float2 f[8];
-    float4 y[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      f[k] = make_float2(kSpNoRef, 0.f);
-      y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (k < nc) {
-        f[k] = cluster.map_shared_rank(both, k)[r];
-        y[k] = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(res, k) +
-                                                 r * RR + 4 * c);
-      }
-    }
-    float top = f[0].x, total = 0.f;
-#pragma unroll
-    for (int k = 1; k < 8; ++k) top = fmaxf(top, f[k].x);
+    float top = kSpNoRef, total = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int k0 = 0; k0 < nc; k0 += 8) {
+      float2 f[8];
+      float4 y[8];
+      float high = top;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float s = ex2(f[k].x - top);
-      total = fmaf(f[k].y, s, total);
-      v.x = fmaf(y[k].x, s, v.x);
-      v.y = fmaf(y[k].y, s, v.y);
-      v.z = fmaf(y[k].z, s, v.z);
-      v.w = fmaf(y[k].w, s, v.w);
+      for (int k = 0; k < 8; ++k) {
+        f[k] = make_float2(kSpNoRef, 0.f);
+        y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k0 + k < nc) {
+          f[k] = cluster.map_shared_rank(both, k0 + k)[r];
+          y[k] = *reinterpret_cast<const float4 *>(
+              cluster.map_shared_rank(res, k0 + k) + r * RR + 4 * c);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) high = fmaxf(high, f[k].x);
+      const float was = ex2(top - high);
+      total *= was;
+      v = make_float4(v.x * was, v.y * was, v.z * was, v.w * was);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float s = ex2(f[k].x - high);
+        total = fmaf(f[k].y, s, total);
+        v.x = fmaf(y[k].x, s, v.x);
+        v.y = fmaf(y[k].y, s, v.y);
+        v.z = fmaf(y[k].z, s, v.z);
+        v.w = fmaf(y[k].w, s, v.w);
+      }
+      top = high;
     }
     put(r, c, v, top, total);
   }
@@ -990,6 +999,8 @@ cudaError_t sparse_t(SparseParams p, int splits, cudaStream_t stream) {
   auto kern = sparse_attention_kernel<DT, D, NT>;
   cudaError_t e = cudaFuncSetAttribute(
       kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+  if (e == cudaSuccess && splits > 8)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1026,6 +1037,13 @@ cudaError_t sparse_rows(SparseParams p, int sms, cudaStream_t stream) {
   while (splits < 8 && 2LL * splits * least <= p.n_select &&
          (p.split_pages > 0 || units * splits * 2 <= 2LL * sms))
     splits *= 2;
+  // Sixteen where the CTAs leave room to spare, as larger clusters are placed
+  // less evenly, which fp32's bytes feel first.  2048 pages of one sequence, one
+  // row, eighths and sixteenths: 2 heads bf16 27 us and 17, fp32 76 and 42; 8
+  // heads bf16 34 and 27, FP8 30 and 30, fp32 77 and 83 (six units: 122 and 65)
+  if (splits == 8 && 2LL * splits * least <= p.n_select &&
+      units * kSpCluster <= (DT == SVP_F32 ? sms * 2 / 3 : sms))
+    splits = kSpCluster;
   if constexpr (DT == SVP_F32)
     return few ? sparse_t<DT, D, 0>(p, splits, stream)
                : sparse_t<DT, D, 1>(p, splits, stream);

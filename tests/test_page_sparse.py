@@ -368,6 +368,25 @@ def test_sparse_long_lists(svp, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d,hkv,group,ql,n_select,split", [
+    (64, 2, 3, 2, 16, 1),     # an entry to a CTA
+    (128, 1, 4, 5, 257, 0),   # 20 rows
+    (128, 2, 7, 5, 300, 0),   # 35 rows
+    (64, 1, 8, 1, 255, 0),    # one entry too few: clusters of eight
+])
+def test_sparse_clusters_of_sixteen(svp, dtype, d, hkv, group, ql, n_select, split):
+    """Also with shares that list nothing, but one, and none at all."""
+    rng = np.random.default_rng(d + ql + n_select)
+    for kept in (slice(0, n_select), slice(n_select - 1, None), slice(3, 6), slice(0, 0)):
+        lists = np.full((1, hkv, n_select), -1, np.int32)
+        lists[..., kept] = rng.integers(0, 25, lists[..., kept].shape)
+        out, lse, ref = _sparse(svp, rng, dtype, d, hkv, group, ql, [397], n_select, split,
+                                lists=lists)
+        assert svp.read_device_status() == 0
+        _check(dtype, d, out, lse, ref)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_sparse_rows_that_see_nothing(svp, dtype):
     """Empty lists, and lists whose keys lie after a row's position."""
     rng = np.random.default_rng(22)
