@@ -21,8 +21,12 @@
 //    accumulators to the B operand by movmatrix.  (With the rows as M, each
 //    row group of 16 to a warp converted every page for itself: 40 rows over
 //    FP8 pages 30 us, against 22.7.)
-//  * bf16: P is bf16, so a weight is off by half a bf16 step, 2^-8, as the
-//    output is; row sums are fp32 and of the weights before that rounding.
+//  * bf16: a weight is two bf16 terms, off by 2^-16 of itself, so that the
+//    output's own rounding is what an output is off by (0.0017 of its norm
+//    over random values, 0.0022 with one term of 2^-8).  The second product
+//    costs 1 % where bytes bound the call and up to a fifth where the chain
+//    does (32 x 8 lists of 128 pages, 4 rows 43.9 -> 44.3 us, 32 rows 50.7 ->
+//    52.7; 4 x 8 of 256, 40 rows 20.7 -> 23.7).  Row sums are fp32.
 //  * FP8 and 4-bit rows become fp16 operands between shared memory and the
 //    matrix instruction (exact); P is fp16 at 2^6 times its weight, which
 //    keeps weights down to 2^-20 normal.  q takes a power-of-two scale per row
@@ -32,9 +36,9 @@
 //    score exceeds it by 2^8, so the usual page costs one vote.
 //
 // Measured (D = 128; of the listed rows' bytes at the copy rate): 32 sequences
-// of 8 heads, 128 pages each, 4 query rows: bf16 44.2 us, 0.90; fp32 89, 0.90;
-// FP8 28.7, 0.70; 4-bit 23.3, 0.48 (the conversion).  20 rows over bf16 47, 32
-// rows 51.  4 sequences of 8 heads, 256 FP8 pages, 40 rows: 22.7 us where the
+// of 8 heads, 128 pages each, 4 query rows: bf16 44.3 us, 0.90; fp32 89, 0.90;
+// FP8 28.7, 0.70; 4-bit 23.3, 0.48 (the conversion).  16 rows over bf16 48, 32
+// rows 53.  4 sequences of 8 heads, 256 FP8 pages, 40 rows: 22.7 us where the
 // bytes take 5.1: about 7 us of start, look-ups and joining, and 16 pages a
 // warp at 1.7 warps to a scheduler (issue active 40 %, tensor pipe 27 %, an
 // instruction every 2.5 cycles of a warp); one unit of 40 rows spills (23),
@@ -242,6 +246,7 @@ struct WarpMma {
   static constexpr int KS = D / 16, MT = D / 16, ROWB = S::ROWB;
   static constexpr float kOff = DT == SVP_BF16 ? 0.f : 6.f;
   static constexpr float kSlack = DT == SVP_BF16 ? 8.f : 14.f;
+  static constexpr int kTerms = DT == SVP_BF16 ? 2 : 1;  // of a weight
   static constexpr bool Q_SHARED = S::Q_SHARED;
   uint2 q[Q_SHARED ? 1 : NT][Q_SHARED ? 1 : KS];
   float o[MT][NT][4];
@@ -446,13 +451,16 @@ struct WarpMma {
     }
   }
 
-  // O^T += V^T P^T of a page.
-  __device__ __forceinline__ void values(uint32_t vp, const uint32_t (&pb)[NT][2],
+  // O^T += V^T P^T of a page; P in kTerms terms.
+  __device__ __forceinline__ void values(uint32_t vp,
+                                         const uint32_t (&pb)[kTerms][NT][2],
                                          int lane) {
     const int g = lane >> 2, t = lane & 3;
     auto step = [&](int i, const uint32_t (&a)[4]) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mma16<DT>(o[i][n], a, pb[n][0], pb[n][1]);
+      for (int x = 0; x < kTerms; ++x)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma16<DT>(o[i][n], a, pb[x][n][0], pb[x][n][1]);
     };
     if constexpr (DT == SVP_BF16) {
       const int r = (lane >> 4) * 8 + (lane & 7), c = (lane >> 3) & 1;
@@ -578,7 +586,7 @@ struct WarpMma {
     }
 #pragma unroll
     for (int x = 0; x < NP; ++x) {
-      uint32_t pb[NT][2];
+      uint32_t pb[kTerms][NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -587,8 +595,15 @@ struct WarpMma {
           sum[n][e & 1] += s[x][n][e];
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          pb[n][h] = transpose8(pack2<DT>(s[x][n][2 * h], s[x][n][2 * h + 1]));
+        for (int h = 0; h < 2; ++h) {
+          const float p0 = s[x][n][2 * h], p1 = s[x][n][2 * h + 1];
+          const uint32_t w = pack2<DT>(p0, p1);
+          pb[0][n][h] = transpose8(w);
+          if constexpr (kTerms == 2)  // what the first term leaves
+            pb[1][n][h] = transpose8(
+                pack2<DT>(p0 - __uint_as_float(w << 16),
+                          p1 - __uint_as_float(w & 0xffff0000u)));
+        }
       }
       values(at[x] + S::PAGE, pb, lane);
     }
