@@ -47,6 +47,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -62,7 +63,6 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kSpTiles = 4;         // most n8 tiles of query rows of a unit
-constexpr int kSpCluster = 16;      // most CTAs of a unit; above 8 by leave
 constexpr int kListCap = 512;       // list entries a CTA looks up at once
 constexpr int kNoPage = 0x7ffffff0; // first position of a page that is not there
 constexpr float kSpNoRef = -3e38f;  // below any score
@@ -1005,9 +1005,58 @@ __global__ void __launch_bounds__(SpShape<DT, D, NT>::THREADS, 2)
 }
 
 template <int DT, int D, int NT>
-cudaError_t sparse_t(SparseParams p, int splits, cudaStream_t stream) {
+void sparse_config(int splits, cudaLaunchAttribute (&attr)[2], cudaLaunchConfig_t &cfg) {
+  using S = SpShape<DT, D, NT>;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = splits;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg = {};
+  cfg.gridDim = dim3((unsigned)splits);
+  cfg.blockDim = dim3(S::THREADS);
+  cfg.dynamicSmemBytes = S::SMEM;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+}
+
+// Whether the current device can place a cluster of sixteen CTAs of this kernel
+// (a part or a partition with fewer SMs side by side cannot); asked once for
+// each of the first devices.
+template <int DT, int D, int NT>
+bool sixteen_fit() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];  // 0: not asked yet, 1: no, 2: yes
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return false;
+  if (dev < kDevices) {
+    const int k = known[dev].load(std::memory_order_relaxed);
+    if (k) return k == 2;
+  }
+  auto kern = sparse_attention_kernel<DT, D, NT>;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg;
+  sparse_config<DT, D, NT>(kSpCluster, attr, cfg);
+  int n = 0;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           SpShape<DT, D, NT>::SMEM) != cudaSuccess ||
+      cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+          cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess)
+    n = 0;
+  (void)cudaGetLastError();  // a refused query leaves clusters of eight
+  if (dev < kDevices) known[dev].store(n > 0 ? 2 : 1, std::memory_order_relaxed);
+  return n > 0;
+}
+
+template <int DT, int D, int NT>
+cudaError_t sparse_t(SparseParams p, int sms, cudaStream_t stream) {
   using S = SpShape<DT, D, NT>;
   static_assert(S::SMEM <= 227 * 1024, "shared memory");
+  const int splits =
+      sparse_splits((long long)p.batch * p.num_kv_heads * p.n_rb, p.n_select,
+                    p.split_pages, sms, DT == SVP_F32, sixteen_fit<DT, D, NT>);
   const long long grid =
       (long long)p.batch * p.num_kv_heads * p.n_rb * splits;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
@@ -1018,19 +1067,10 @@ cudaError_t sparse_t(SparseParams p, int splits, cudaStream_t stream) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = splits;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
+  cudaLaunchConfig_t cfg;
+  sparse_config<DT, D, NT>(splits, attr, cfg);
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(S::THREADS);
-  cfg.dynamicSmemBytes = S::SMEM;
   cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
@@ -1042,31 +1082,13 @@ cudaError_t sparse_rows(SparseParams p, int sms, cudaStream_t stream) {
   const int nt = ((p.rows + p.n_rb - 1) / p.n_rb + 7) / 8;
   const bool few = DT == SVP_F32 && p.rows <= 4;
   p.n_rb = few ? 1 : (p.rows + 8 * nt - 1) / (8 * nt);
-  const long long units = (long long)p.batch * p.num_kv_heads * p.n_rb;
-  // split a list while the CTAs all find room (two to an SM) and keep eight
-  // pages, or to the caller's pages per CTA: 256 units of 128 bf16 pages take
-  // 44 us whole, 48 in halves and 56 in quarters; 64 units of 256 FP8 pages 22 in
-  // quarters, 28 in halves
-  const long long least = p.split_pages > 0 ? p.split_pages : 8;
-  int splits = 1;
-  while (splits < 8 && 2LL * splits * least <= p.n_select &&
-         (p.split_pages > 0 || units * splits * 2 <= 2LL * sms))
-    splits *= 2;
-  // Sixteen where the CTAs leave room to spare, as larger clusters are placed
-  // less evenly, which fp32's bytes feel first.  2048 pages of one sequence, one
-  // row, eighths and sixteenths: 2 heads bf16 27 us and 17, fp32 76 and 42; 8
-  // heads bf16 34 and 27, FP8 30 and 30, fp32 77 and 83 (six units: 122 and 65)
-  if (splits == 8 && 2LL * splits * least <= p.n_select &&
-      units * kSpCluster <= (DT == SVP_F32 ? sms * 2 / 3 : sms))
-    splits = kSpCluster;
   if constexpr (DT == SVP_F32)
-    return few ? sparse_t<DT, D, 0>(p, splits, stream)
-               : sparse_t<DT, D, 1>(p, splits, stream);
+    return few ? sparse_t<DT, D, 0>(p, sms, stream) : sparse_t<DT, D, 1>(p, sms, stream);
   else
-    return nt == 1   ? sparse_t<DT, D, 1>(p, splits, stream)
-           : nt == 2 ? sparse_t<DT, D, 2>(p, splits, stream)
-           : nt == 3 ? sparse_t<DT, D, 3>(p, splits, stream)
-                     : sparse_t<DT, D, 4>(p, splits, stream);
+    return nt == 1   ? sparse_t<DT, D, 1>(p, sms, stream)
+           : nt == 2 ? sparse_t<DT, D, 2>(p, sms, stream)
+           : nt == 3 ? sparse_t<DT, D, 3>(p, sms, stream)
+                     : sparse_t<DT, D, 4>(p, sms, stream);
 }
 
 }  // namespace

@@ -1,6 +1,9 @@
 """Selected pages, page assignment and log probabilities where the other files
 do not look: weights' bits, shapes that take another branch of a launcher, and
 a step whose pages run out.  Tolerances as in test_page_sparse.py."""
+import os
+import subprocess
+
 import numpy as np
 import pytest
 
@@ -50,3 +53,49 @@ def test_sparse_bf16_weights_keep_their_bits(svp, d, group):
     tol = 2.0 ** -16 + 3 * 3 * 2.0 ** -24 + 2.0 ** -21 + 2.0 ** -8 * np.abs(want)
     assert (np.abs(_f64(out) - want) <= tol).all()
     assert np.abs(_f64(lse) - wlse).max() <= 2.0 ** -20
+
+
+SPLITS = r"""
+#include <cstdio>
+#include "svp.h"
+#include "svp_internal.h"
+int main() {
+  long long units;
+  int n_select, split_pages, sms, f32, fit;
+  while (std::scanf("%lld %d %d %d %d %d", &units, &n_select, &split_pages, &sms, &f32,
+                    &fit) == 6) {
+    int asked = 0;
+    const int n = svp::sparse_splits(units, n_select, split_pages, sms, f32 != 0,
+                                     [&] { ++asked; return fit != 0; });
+    std::printf("%d %d\n", n, asked);
+  }
+}
+"""
+
+
+def test_clusters_of_sixteen_where_the_device_has_them(tmp_path):
+    """The launcher's rule, as host code: sixteen CTAs to a list only where the
+    device says that it can place them, eight where it cannot, and no question
+    where sixteen are not wanted."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    (tmp_path / "splits.cpp").write_text(SPLITS)
+    exe = str(tmp_path / "splits")
+    subprocess.run(["g++", "-std=c++17", "-I", os.path.join(cuda, "include"), "-I",
+                    os.path.join(root, "include"), "-I",
+                    os.path.join(root, "spec_verify_paged_gb300", "csrc"),
+                    str(tmp_path / "splits.cpp"), "-o", exe], check=True)
+    #  units, list, split_pages, SMs, fp32, sixteen fit -> CTAs to a unit, asked
+    cases = {(1, 2048, 0, 152, 0, 1): (16, 1), (1, 2048, 0, 152, 0, 0): (8, 1),
+             (1, 2048, 0, 152, 1, 1): (16, 1), (1, 2048, 0, 152, 1, 0): (8, 1),
+             # eight entries to a CTA: sixteen CTAs from 16 * 8 = 128 entries on
+             (1, 255, 0, 152, 0, 1): (16, 1), (1, 128, 0, 152, 0, 1): (16, 1),
+             (1, 127, 0, 152, 0, 1): (8, 0), (64, 256, 0, 152, 0, 1): (4, 0),
+             (1, 16, 1, 152, 0, 1): (16, 1), (1, 16, 1, 152, 0, 0): (8, 1),
+             (256, 128, 0, 152, 0, 1): (1, 0), (256, 128, 16, 152, 0, 1): (8, 0),
+             (1, 1, 0, 152, 0, 1): (1, 0), (1, 2048, 0, 15, 0, 1): (8, 0),
+             (1 << 40, 1 << 26, 1 << 26, 152, 0, 1): (1, 0)}
+    text = "\n".join(" ".join(map(str, c)) for c in cases)
+    r = subprocess.run([exe], input=text, capture_output=True, text=True, check=True)
+    got = [tuple(map(int, line.split())) for line in r.stdout.splitlines()]
+    assert got == list(cases.values())
