@@ -99,3 +99,148 @@ def test_clusters_of_sixteen_where_the_device_has_them(tmp_path):
     r = subprocess.run([exe], input=text, capture_output=True, text=True, check=True)
     got = [tuple(map(int, line.split())) for line in r.stdout.splitlines()]
     assert got == list(cases.values())
+
+
+# ------------------------------------------- a step whose pages run out
+
+def _readme_step():
+    """README's step over selected pages: what stands before it, and the step."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "README.md")) as f:
+        blocks = f.read().split("```python\n")[1:]
+    block, = (x for x in (b.split("```")[0] for b in blocks) if "kv_assign_pages(" in x)
+    at = block.index("\n") + 1
+    assert block[:at].startswith("bounds = ")
+    return block[:at], block[at:]
+
+
+class Short:
+    """Six sequences whose five new rows want four new pages, of which there is
+    one: the first gets it, the fourth and the fifth need none."""
+    B, q_len, Hkv, D, num_blocks, vocab = 6, 5, 2, 64, 24, 40
+
+    def __init__(self, device):
+        import torch
+        rng = np.random.default_rng(31)
+        lens = np.array([60, 16, 31, 200, 3, 0], np.int32)
+        self.table, _, _ = R.pages(rng, lens, width=16)
+        used = self.table[self.table >= 0]
+        stack = np.setdiff1d(np.arange(self.num_blocks), used).astype(np.int32)
+        self.lens, self.count = lens, 1
+        self.stack = np.concatenate([stack[:1], np.zeros(self.num_blocks - 1, np.int32)])
+        g = torch.Generator().manual_seed(3)
+
+        def rand(*shape):
+            return torch.randn(shape, generator=g).to(device)
+
+        def ints(x):
+            return torch.from_numpy(np.array(x, np.int32)).to(device)
+
+        n = (self.B * self.q_len, self.Hkv, self.D)
+        cache = (self.num_blocks, self.Hkv, 16, self.D)
+        target = rand(self.B, self.q_len, self.vocab)
+        draft = target[:, :-1] + 0.3 * rand(self.B, self.q_len - 1, self.vocab)
+        self.names = dict(
+            torch=torch, B=self.B, q_len=self.q_len, Hkv=self.Hkv, D=self.D,
+            num_blocks=self.num_blocks, block_table=ints(self.table), seq_lens=ints(lens),
+            free_pages=ints(self.stack), free_count=ints([1]),
+            k_new=rand(*n).bfloat16(), v_new=rand(*n).bfloat16(),
+            k_cache=rand(*cache).bfloat16(), v_cache=rand(*cache).bfloat16(),
+            q=rand(self.B, self.q_len, 2 * self.Hkv, self.D).bfloat16(),
+            target_logits=target, draft_logits=draft,
+            draft_tokens=draft.argmax(-1).int(),
+            uniforms=torch.rand((self.B, self.q_len), generator=g).to(device))
+
+    def check(self):
+        """After a step: the state of the plain form, in which a sequence that
+        got its pages keeps what it accepted and the others all they had."""
+        x = self.names
+        old, want = self.lens, self.lens + self.q_len
+        before = [self.table.copy(), old.copy()]
+        self.table, self.lens, self.stack, self.count, *_ = G.assign(
+            self.table, old, want, self.stack, self.count, self.B * self.q_len)
+        served = self.lens == want
+        accepted = x["n_accepted"].cpu().numpy()
+        self.table, self.lens, self.stack, self.count, *_ = G.assign(
+            self.table, self.lens, np.where(served, old + 1 + accepted, old), self.stack,
+            self.count)
+        assert np.array_equal(x["seq_lens"].cpu().numpy(), self.lens)
+        assert np.array_equal(x["block_table"].cpu().numpy(), self.table)
+        assert x["free_count"].tolist() == [self.count]
+        assert np.array_equal(x["free_pages"].cpu().numpy(), self.stack)
+        assert np.array_equal(self.table[~served], before[0][~served])
+        assert np.array_equal(self.lens[~served], before[1][~served])
+        tokens = x["tokens"].cpu().numpy()
+        assert (tokens[~served] == -1).all() and (tokens[served, 0] >= 0).all()
+        return served
+
+
+def test_the_readme_step_keeps_rows_when_pages_run_out():
+    """Its arithmetic on the host, with the plain form of the assignment."""
+    import types
+
+    import torch
+    short = Short("cpu")
+    x = short.names
+
+    def assign(table, lens, new, free, count, n_slots=None):
+        t, n, s, c, slots, off, _ = G.assign(
+            *(a.numpy() for a in (table, lens, new, free)), int(count), n_slots)
+        for to, a in ((table, t), (lens, n), (free, s)):
+            to.copy_(torch.from_numpy(a))
+        count.fill_(c)
+        return (None if n_slots is None else torch.tensor(slots)), torch.tensor(off)
+
+    def accept(*_):
+        n = (torch.arange(short.B) + turn).int() % short.q_len
+        return torch.zeros((short.B, short.q_len), dtype=torch.int32), n
+
+    def five(*_, **__):
+        return (None,) * 5
+
+    def two(*_, **__):
+        return None, None
+
+    x["svp"] = types.SimpleNamespace(
+        kv_assign_pages=assign, spec_accept=accept, token_logprobs=five,
+        paged_sparse_attention=two, kv_append=two, kv_page_bounds=two,
+        paged_page_scores=two, paged_select_pages=two)
+    first, step = _readme_step()
+    exec(first.replace('"cuda"', '"cpu"'), x)
+    for turn in range(6):
+        exec(step, x)
+        served = short.check()
+        if turn == 0:
+            assert served.tolist() == [True, False, False, True, True, False]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("captured", [False, True])
+def test_the_readme_step_when_pages_run_out(svp, captured):
+    """The step itself, as calls and as a graph: committed rows stay, and rows
+    that no page was found for are stored nowhere."""
+    import torch
+    short = Short("cuda")
+    x = short.names
+    x["svp"] = svp
+    first, step = _readme_step()
+    exec(first, x)
+    step = compile(step, "README.md", "exec")
+    if captured:
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            exec(step, x)
+    for _ in range(4):
+        k, old, table = (x[n].clone() for n in ("k_cache", "seq_lens", "block_table"))
+        graph.replay() if captured else exec(step, x)
+        served = short.check()
+        # no page for some, and nothing but an empty sequence's length besides
+        assert svp.read_device_status() & ~2 == (0 if served.all() else 16)
+        kc = x["k_cache"]
+        for b, n in enumerate(old.tolist()):  # the rows there were
+            for j in range(-(-n // 16)):
+                r = min(16, n - 16 * j)
+                assert torch.equal(kc[table[b, j], :, :r], k[table[b, j], :, :r])
+        rank = x["rank"].cpu().numpy()
+        assert (rank[~served] == -1).all() and (rank[served, 0] >= 0).all()
