@@ -477,10 +477,13 @@ int paged_sparse_attention(const svp_dims *dims, const void *q,
  * positions seq_lens[b] .. new_lens[b] - 1 of all sequences, packed in order,
  * slot = page * 16 + position % 16; -1 past the last.  offsets [batch + 1]
  * int32 (or NULL): where each sequence's begin (at most 2^31 - 1).
- * Pages (or, with slots, entries of slots) may run out: from the first
- * sequence whose new pages (new positions) no longer fit, no sequence that
- * needs any is served: its table and length stay as they were, its slots are
- * -1, and SVP_DEV_NO_PAGES is set.
+ * Pages (or, with slots, entries of slots) may run out.  From the first
+ * sequence whose new pages no longer fit, no sequence that needs a new page is
+ * served; with slots, from the first whose new positions no longer fit, none
+ * that has new positions.  A sequence not served keeps its table and length,
+ * its slots are -1, and SVP_DEV_NO_PAGES is set.  All others are served, also
+ * behind it: those that shrink, and while slots suffice those that grow within
+ * their last page.  seq_lens[b] != new_lens[b] tells the unserved ones.
  * A length outside [0, max_blocks*16] (old or new) leaves the sequence as it
  * is and sets SVP_DEV_BAD_SEQ_LEN.  A page id outside [0, num_blocks) is
  * pushed or taken as it stands, gets slot -1 and sets SVP_DEV_BAD_BLOCK_ID.  A

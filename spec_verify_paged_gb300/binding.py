@@ -573,9 +573,11 @@ def kv_assign_pages(block_table, seq_lens, new_lens, free_pages, free_count,
     offsets int32 [B + 1] say where each sequence's begin.  Ids outside
     [0, num_blocks) get no slot.
 
-    Where pages or slots run out, the sequences from the first that does not
-    fit keep their length and table, and read_device_status() has
-    DEV_NO_PAGES."""
+    Where pages run out, no sequence from the first that does not fit on that
+    needs a new page is served, where slots do, none that has new positions:
+    seq_lens (!= new_lens) and table stay as they were, slots are -1, and
+    read_device_status() has DEV_NO_PAGES.  Sequences that shrink or, while
+    slots suffice, grow within their last page are served all the same."""
     r = (_calls or _load_calls()).assign_pages(
         block_table, seq_lens, new_lens, free_pages, free_count, n_slots, slots,
         offsets, num_blocks, _raw(stream))

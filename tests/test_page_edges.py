@@ -244,3 +244,50 @@ def test_the_readme_step_when_pages_run_out(svp, captured):
                 assert torch.equal(kc[table[b, j], :, :r], k[table[b, j], :, :r])
         rank = x["rank"].cpu().numpy()
         assert (rank[~served] == -1).all() and (rank[served, 0] >= 0).all()
+
+
+# ----------------------------------------- who is served when things run out
+
+#          lengths and targets          free  slots  served
+SHORTAGES = [
+    # the second needs two pages of one; behind it only those that need none:
+    # within a page, shorter (whose page came back before), the same, but not
+    # the last, which needs one
+    ([16, 16, 20, 40, 5, 16], [20, 60, 32, 20, 5, 17], 1, None, [0, 2, 3, 4]),
+    # the second's four positions do not fit; behind it only those without any
+    ([3, 3, 3, 40, 5, 3], [5, 7, 4, 20, 5, 4], 0, 5, [0, 3, 4]),
+    # entries run out before pages do
+    ([0, 0, 0, 0, 20, 0], [16, 16, 1, 0, 19, 0], 4, 20, [0, 3, 4, 5]),
+]
+
+
+def _shortage(lens, new, free, slots):
+    rng = np.random.default_rng(5)
+    table, total, _ = R.pages(rng, np.array(lens, np.int32), width=4)
+    stack = np.full(40, -7, np.int32)
+    stack[:free] = total + np.arange(free)
+    return table, np.array(lens, np.int32), np.array(new, np.int32), stack, free, slots
+
+
+@pytest.mark.parametrize("lens,new,free,slots,served", SHORTAGES)
+def test_who_is_served_plain(lens, new, free, slots, served):
+    table, old, new, stack, count, slots = _shortage(lens, new, free, slots)
+    t, n, *_, short = G.assign(table, old, new, stack, count, slots)
+    assert short and np.nonzero(n == new)[0].tolist() == served
+    rest = n != new
+    assert np.array_equal(t[rest], table[rest]) and np.array_equal(n[rest], old[rest])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,new,free,slots,served", SHORTAGES)
+def test_who_is_served(svp, lens, new, free, slots, served):
+    table, old, new, stack, count, slots = _shortage(lens, new, free, slots)
+    t, n, s = (R.to_gpu(x) for x in (table, old, stack))
+    c = R.to_gpu(np.array([count], np.int32))
+    svp.kv_assign_pages(t, n, R.to_gpu(new), s, c, n_slots=slots)
+    assert svp.read_device_status() == 16
+    got = n.cpu().numpy()
+    assert np.nonzero(got == new)[0].tolist() == served
+    rest = got != new
+    assert np.array_equal(t.cpu().numpy()[rest], table[rest])
+    assert np.array_equal(got[rest], old[rest])
