@@ -291,3 +291,82 @@ def test_who_is_served(svp, lens, new, free, slots, served):
     rest = got != new
     assert np.array_equal(t.cpu().numpy()[rest], table[rest])
     assert np.array_equal(got[rest], old[rest])
+
+
+# ------------------------------------ shapes that take another branch
+
+def _sms():
+    import torch
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d,hkv", [
+    ("fp8", 128, 3), ("fp8", 128, 4), ("fp8", 64, 7), ("fp8", 64, 2), ("fp4", 128, 8),
+    ("fp4", 128, 1), ("fp4", 64, 9), ("fp4", 64, 5), ("bf16", 64, 3), ("bf16", 64, 2),
+])
+@pytest.mark.parametrize("n_new", [None, 40])
+def test_bounds_several_heads_to_a_warp(svp, dtype, d, hkv, n_new):
+    """From 256 (page, head) pairs to an SM on a warp takes several heads of a
+    page, also where that leaves fewer for the last one.  What counts are the
+    pages a call may touch: the table's width, or four of each sequence."""
+    rng = np.random.default_rng(d + hkv)
+    pairs = 256 * _sms()
+    batch = 7 if n_new is None else pairs // (4 * hkv) + 7
+    width = pairs // (7 * hkv) + 1 if n_new is None else 5
+    lens = np.zeros(batch, np.int32)
+    lens[:7] = [0, 1, 16, 17, 64, 33, 300 if n_new is None else 48]
+    table, total, _ = R.pages(rng, lens, spare=3, width=width)
+    scale = {"fp8": 2.0 ** -5, "fp4": 0.0371}.get(dtype, 1.0)
+    k = R.make_cache(rng, dtype, total, hkv, d, scale, lens, table)
+    old = rng.integers(-3, 4, (total, hkv, 2, d)).astype(np.float64)
+    b = R.to_gpu(old.astype(np.float32), "bf16")
+    svp.kv_page_bounds(R.to_gpu(k, "bf16" if dtype == "bf16" else None),
+                       R.to_gpu(table), R.to_gpu(lens), b, n_new)
+    assert svp.read_device_status() == 0
+    want = G.bounds(R.values(k, dtype, d), lens, table, n_new or 10 ** 6, old)
+    assert np.array_equal(_f64(b), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("group,ql", [(2, 1), (8, 4), (8, 5)])
+def test_scores_short_parts(svp, dtype, group, ql):
+    """More (sequence, head) pairs than CTAs at once and more than 48 tiles of
+    16 pages: the pages are cut into parts of 20 tiles, of 32 with 33 rows and
+    more.  Tolerance as in test_page_sparse.py."""
+    rng = np.random.default_rng(group + ql)
+    d, hkv = 64, 8
+    batch, width = 4 * _sms() // hkv + 1, 16 * 49 + 3
+    lens = np.full(batch, ql, np.int32)
+    lens[[0, 2, batch - 1]] = [16 * width, 16 * 600 + 1, 16 * 321]
+    table, total, _ = R.pages(rng, lens, width=width)
+    mid = rng.standard_normal((total, hkv, 1, d))
+    bnd = R.bf16(np.concatenate([mid - 1.5, mid + 1.5], 2))
+    q = rng.standard_normal((batch, ql, hkv * group, d))
+    q = q.astype(np.float32).astype(np.float64) if dtype == "f32" else R.bf16(q)
+    got = svp.paged_page_scores(
+        R.to_gpu(q.astype(np.float32), None if dtype == "f32" else "bf16"),
+        R.to_gpu(bnd.astype(np.float32), "bf16"), R.to_gpu(table), R.to_gpu(lens),
+        scale=0.125)
+    assert svp.read_device_status() == 0
+    want, mag = G.scores(q, bnd, lens, table, 0.125)
+    got = _f64(got)
+    live = np.isfinite(want)
+    assert np.array_equal(live, np.isfinite(got)) and (got[~live] == -np.inf).all()
+    n = 2 * d * (3 if dtype == "f32" else 1) + 4
+    assert (np.abs(got[live] - want[live]) <= n * 2.0 ** -23 * mag[live]).all()
+
+
+@pytest.mark.gpu
+def test_assign_without_slots_by_eight_ctas(svp):
+    """Up to 1024 sequences and more than 4096 table entries, without slots."""
+    from test_assign import State
+    rng = np.random.default_rng(51)
+    for batch, width in ((700, 8), (1024, 5), (3, 2000)):
+        st = State(rng, batch, width, batch * width - batch // 2)
+        for turn in range(4):
+            new = rng.integers(0, 16 * width + 1, batch)
+            assert st.go(svp, new) in (0, 16)
+        assert st.go(svp, np.zeros(batch)) == 0
+        assert st.count == batch * width - batch // 2
