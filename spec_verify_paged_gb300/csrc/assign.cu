@@ -403,18 +403,8 @@ cudaError_t launch_assign_pages(const AssignParams &p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, assign_one_kernel, p, span);
 }
 
-cudaError_t read_status_assign(cudaStream_t s, unsigned *flags) {
-  unsigned v = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_status_assign, sizeof v, 0,
-                                            cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e != cudaSuccess) return e;
-  const unsigned zero = 0;
-  e = cudaMemcpyToSymbolAsync(g_status_assign, &zero, sizeof zero, 0,
-                              cudaMemcpyHostToDevice, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  *flags |= v;
-  return e;
+cudaError_t status_word_assign(unsigned **word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_status_assign);
 }
 
 }  // namespace svp

@@ -1263,18 +1263,8 @@ cudaError_t launch_merge(const AttnParams &p, int dtype, int grid,
   return e;
 }
 
-cudaError_t read_status_attention(cudaStream_t s, unsigned *flags) {
-  unsigned v = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_status_attn, sizeof v, 0,
-                                            cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e != cudaSuccess) return e;
-  const unsigned zero = 0;
-  e = cudaMemcpyToSymbolAsync(g_status_attn, &zero, sizeof zero, 0,
-                              cudaMemcpyHostToDevice, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  *flags |= v;
-  return e;
+cudaError_t status_word_attention(unsigned **word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_status_attn);
 }
 
 }  // namespace svp

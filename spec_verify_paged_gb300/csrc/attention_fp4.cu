@@ -1051,18 +1051,8 @@ cudaError_t launch_attention_fp4(const AttnParams &p, int grid,
   }
 }
 
-cudaError_t read_status_attention_fp4(cudaStream_t s, unsigned *flags) {
-  unsigned v = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_status_attn4, sizeof v, 0,
-                                            cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e != cudaSuccess) return e;
-  const unsigned zero = 0;
-  e = cudaMemcpyToSymbolAsync(g_status_attn4, &zero, sizeof zero, 0,
-                              cudaMemcpyHostToDevice, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  *flags |= v;
-  return e;
+cudaError_t status_word_attention_fp4(unsigned **word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_status_attn4);
 }
 
 }  // namespace svp

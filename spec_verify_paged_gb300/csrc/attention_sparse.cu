@@ -1112,18 +1112,8 @@ cudaError_t launch_sparse_attention(const SparseParams &p, int dtype, int sms,
   }
 }
 
-cudaError_t read_status_sparse(cudaStream_t s, unsigned *flags) {
-  unsigned v = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_status_sparse, sizeof v, 0,
-                                            cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e != cudaSuccess) return e;
-  const unsigned zero = 0;
-  e = cudaMemcpyToSymbolAsync(g_status_sparse, &zero, sizeof zero, 0,
-                              cudaMemcpyHostToDevice, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  *flags |= v;
-  return e;
+cudaError_t status_word_sparse(unsigned **word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_status_sparse);
 }
 
 }  // namespace svp

@@ -1408,18 +1408,8 @@ cudaError_t launch_attention_tc(const AttnParams &p, int grid,
                       : launch_tc<32, true>(p, grid, stream);
 }
 
-cudaError_t read_status_attention_tc(cudaStream_t s, unsigned *flags) {
-  unsigned v = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_status_attn_tc, sizeof v, 0,
-                                            cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e != cudaSuccess) return e;
-  const unsigned zero = 0;
-  e = cudaMemcpyToSymbolAsync(g_status_attn_tc, &zero, sizeof zero, 0,
-                              cudaMemcpyHostToDevice, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  *flags |= v;
-  return e;
+cudaError_t status_word_attention_tc(unsigned **word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_status_attn_tc);
 }
 
 }  // namespace svp

@@ -387,19 +387,19 @@ struct AcceptTreeParams {
 cudaError_t launch_spec_accept_tree(const AcceptTreeParams &p,
                                     cudaStream_t stream);
 
-// Device status words (one per translation unit): read-and-clear.
-cudaError_t read_status_attention(cudaStream_t s, unsigned *flags);
-cudaError_t read_status_attention_tc(cudaStream_t s, unsigned *flags);
-cudaError_t read_status_attention_fp4(cudaStream_t s, unsigned *flags);
-cudaError_t read_status_attention_fp4_tc(cudaStream_t s, unsigned *flags);
-cudaError_t read_status_append(cudaStream_t s, unsigned *flags);
-cudaError_t read_status_score(cudaStream_t s, unsigned *flags);
-cudaError_t read_status_evict(cudaStream_t s, unsigned *flags);
-cudaError_t read_status_accept(cudaStream_t s, unsigned *flags);
-cudaError_t read_status_pages(cudaStream_t s, unsigned *flags);
-cudaError_t read_status_sparse(cudaStream_t s, unsigned *flags);
-cudaError_t read_status_assign(cudaStream_t s, unsigned *flags);
-cudaError_t read_status_logprobs(cudaStream_t s, unsigned *flags);
+// Device status words (one per translation unit), on the current device.
+cudaError_t status_word_attention(unsigned **word);
+cudaError_t status_word_attention_tc(unsigned **word);
+cudaError_t status_word_attention_fp4(unsigned **word);
+cudaError_t status_word_attention_fp4_tc(unsigned **word);
+cudaError_t status_word_append(unsigned **word);
+cudaError_t status_word_score(unsigned **word);
+cudaError_t status_word_evict(unsigned **word);
+cudaError_t status_word_accept(unsigned **word);
+cudaError_t status_word_pages(unsigned **word);
+cudaError_t status_word_sparse(unsigned **word);
+cudaError_t status_word_assign(unsigned **word);
+cudaError_t status_word_logprobs(unsigned **word);
 
 #ifdef __CUDACC__
 // A launch that may start while the previous kernel on the stream is still

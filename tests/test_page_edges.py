@@ -370,3 +370,70 @@ def test_assign_without_slots_by_eight_ctas(svp):
             assert st.go(svp, new) in (0, 16)
         assert st.go(svp, np.zeros(batch)) == 0
         assert st.count == batch * width - batch // 2
+
+
+# --------------------------------------------------- the device's flags
+
+@pytest.mark.gpu
+def test_status_read_is_one_round_trip(svp):
+    """Reading the flags waits for the GPU once, not once or twice for each
+    source file that has some: at most five times what one number read back
+    takes (12 pairs of copies and waits take sixteen)."""
+    import time
+
+    import torch
+    x = torch.zeros(1, device="cuda")
+
+    def best(f):
+        t = []
+        for _ in range(200):
+            t0 = time.perf_counter()
+            f()
+            t.append(time.perf_counter() - t0)
+        return min(t)
+
+    svp.read_device_status()
+    one, status = best(x.item), best(svp.read_device_status)
+    print(f"{1e6 * one:.1f} us, {1e6 * status:.1f} us")
+    assert status <= 5 * one
+
+
+@pytest.mark.gpu
+def test_status_of_several_files_and_threads(svp):
+    """Flags of several files arrive together and once, and threads that read at
+    the same time get every flag between them."""
+    import threading
+
+    import torch
+    z = dict(dtype=torch.int32, device="cuda")
+    table, lens = torch.full((1, 2), 99, **z), torch.tensor([40], **z)
+
+    def raise_all():
+        svp.paged_select_pages(torch.zeros((1, 1, 2), device="cuda"), lens, 1)      # 2
+        svp.kv_assign_pages(table, torch.tensor([0], **z), torch.tensor([16], **z),
+                            torch.zeros(1, **z), torch.zeros(1, **z))               # 16
+        svp.token_logprobs(torch.zeros((1, 8), device="cuda"), torch.tensor([9], **z))  # 4
+        svp.kv_page_bounds(torch.zeros((4, 1, 16, 64), device="cuda"), table,
+                           torch.tensor([5], **z),
+                           torch.zeros((4, 1, 2, 64), dtype=torch.bfloat16,
+                                       device="cuda"))                              # 1
+    svp.read_device_status()
+    raise_all()
+    assert svp.read_device_status() == 1 | 2 | 4 | 16
+    assert svp.read_device_status() == 0
+    for _ in range(20):
+        raise_all()
+        torch.cuda.synchronize()
+        got = []
+
+        def read():
+            with torch.cuda.stream(torch.cuda.Stream()):
+                got.append(svp.read_device_status())
+
+        threads = [threading.Thread(target=read) for _ in range(6)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert np.bitwise_or.reduce(got) == 1 | 2 | 4 | 16
+        assert svp.read_device_status() == 0
