@@ -76,7 +76,7 @@ struct SpShape {
   static constexpr int ROWB = DT == SVP_F32 ? 4 * D : DT == SVP_BF16 ? 2 * D
                               : DT == SVP_FP8_E4M3 ? D : fp4_row_bytes(D);
   static constexpr int PAGE = kBlockSize * ROWB;  // one side
-  // warps of a CTA, of which an SM holds two: eight over small pages, whose
+  // warps of a CTA, of which an SM holds PER_SM: eight over small pages, whose
   // rings leave the room, while 128 registers are enough
   static constexpr int WARPS = PAGE < 4096 && DT != SVP_F32 && NT == 1 ? 8 : 4;
   static constexpr int THREADS = 32 * WARPS;
@@ -99,6 +99,9 @@ struct SpShape {
                            : Q_SHARED    ? NT * ((D / 16) * 256 + 32)
                                          : 0;
   static constexpr int SMEM = RING + LIST + 64 + (Q > ROWS * 8 ? Q : ROWS * 8);
+  // an SM's 228 KB hold two CTAs, each with a KB of its own, or one over fp32
+  // pages of D = 128 (204 and 207 KB)
+  static constexpr int PER_SM = 2 * (SMEM + 1024) <= 228 * 1024 ? 2 : 1;
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes) {
@@ -793,7 +796,7 @@ struct WarpOf<SVP_F32, D, NT> {
 };
 
 template <int DT, int D, int NT>
-__global__ void __launch_bounds__(SpShape<DT, D, NT>::THREADS, 2)
+__global__ void __launch_bounds__(SpShape<DT, D, NT>::THREADS, SpShape<DT, D, NT>::PER_SM)
     sparse_attention_kernel(const SparseParams p) {
   using S = SpShape<DT, D, NT>;
   constexpr int RB = S::ROWS, STAGES = S::STAGES, W = S::WARPS, T = S::THREADS;
@@ -1054,9 +1057,11 @@ template <int DT, int D, int NT>
 cudaError_t sparse_t(SparseParams p, int sms, cudaStream_t stream) {
   using S = SpShape<DT, D, NT>;
   static_assert(S::SMEM <= 227 * 1024, "shared memory");
+  static_assert(S::PER_SM == 2 || DT == SVP_F32, "as measured");
   const int splits =
       sparse_splits((long long)p.batch * p.num_kv_heads * p.n_rb, p.n_select,
-                    p.split_pages, sms, DT == SVP_F32, sixteen_fit<DT, D, NT>);
+                    p.split_pages, sms, S::PER_SM, DT == SVP_F32,
+                    sixteen_fit<DT, D, NT>);
   const long long grid =
       (long long)p.batch * p.num_kv_heads * p.n_rb * splits;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;

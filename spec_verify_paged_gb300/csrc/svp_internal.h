@@ -289,24 +289,28 @@ cudaError_t launch_sparse_attention(const SparseParams &p, int dtype, int sms,
 
 constexpr int kSpCluster = 16;  // most CTAs of a unit; above 8 by leave
 
-// CTAs that share a unit's list.  sixteen_fit(): whether the device can place a
-// cluster of sixteen; only asked where one is wanted.
+// CTAs that share a unit's list.  per_sm: CTAs that an SM holds; sixteen_fit():
+// whether the device can place a cluster of sixteen, only asked where one is
+// wanted.
 template <class Fit>
-int sparse_splits(long long units, int n_select, int split_pages, int sms, bool f32,
-                  Fit sixteen_fit) {
-  // split a list while the CTAs all find room (two to an SM) and keep eight
-  // pages, or to the caller's pages per CTA: 256 units of 128 bf16 pages take
-  // 44 us whole, 48 in halves and 56 in quarters; 64 units of 256 FP8 pages 22 in
-  // quarters, 28 in halves
+int sparse_splits(long long units, int n_select, int split_pages, int sms, int per_sm,
+                  bool f32, Fit sixteen_fit) {
+  // split a list while the CTAs all find room and keep eight pages, or to the
+  // caller's pages per CTA: 256 units of 128 bf16 pages take 44 us whole, 48 in
+  // halves and 56 in quarters; 64 units of 256 FP8 pages 22 in quarters, 28 in
+  // halves; 32 units of 128 fp32 pages, one CTA to an SM, 14 in quarters, 26 in
+  // eighths
   const long long least = split_pages > 0 ? split_pages : 8;
   int splits = 1;
   while (splits < 8 && 2LL * splits * least <= n_select &&
-         (split_pages > 0 || units * splits * 2 <= 2LL * sms))
+         (split_pages > 0 || units * splits * 2 <= (long long)per_sm * sms))
     splits *= 2;
   // Sixteen where the CTAs leave room to spare, as larger clusters are placed
   // less evenly, which fp32's bytes feel first.  2048 pages of one sequence, one
   // row, eighths and sixteenths: 2 heads bf16 27 us and 17, fp32 76 and 42; 8
-  // heads bf16 34 and 27, FP8 30 and 30, fp32 77 and 83 (six units: 122 and 65)
+  // heads bf16 34 and 27, FP8 30 and 30, fp32 77 and 83 (six units: 122 and 65).
+  // (8 heads of 512 pages: bf16 11.2 and 10.4, but FP8 11.9 and 12.6; the rule
+  // does not tell these types apart.)
   if (splits == 8 && 2LL * splits * least <= n_select &&
       units * kSpCluster <= (f32 ? sms * 2 / 3 : sms) && sixteen_fit())
     splits = kSpCluster;

@@ -61,11 +61,11 @@ SPLITS = r"""
 #include "svp_internal.h"
 int main() {
   long long units;
-  int n_select, split_pages, sms, f32, fit;
-  while (std::scanf("%lld %d %d %d %d %d", &units, &n_select, &split_pages, &sms, &f32,
-                    &fit) == 6) {
+  int n_select, split_pages, sms, per_sm, f32, fit;
+  while (std::scanf("%lld %d %d %d %d %d %d", &units, &n_select, &split_pages, &sms,
+                    &per_sm, &f32, &fit) == 7) {
     int asked = 0;
-    const int n = svp::sparse_splits(units, n_select, split_pages, sms, f32 != 0,
+    const int n = svp::sparse_splits(units, n_select, split_pages, sms, per_sm, f32 != 0,
                                      [&] { ++asked; return fit != 0; });
     std::printf("%d %d\n", n, asked);
   }
@@ -73,32 +73,49 @@ int main() {
 """
 
 
-def test_clusters_of_sixteen_where_the_device_has_them(tmp_path):
-    """The launcher's rule, as host code: sixteen CTAs to a list only where the
-    device says that it can place them, eight where it cannot, and no question
-    where sixteen are not wanted."""
+@pytest.fixture(scope="module")
+def splits(tmp_path_factory):
+    """The launcher's rule, as host code: {(units, list, split_pages, SMs, CTAs an
+    SM holds, fp32, sixteen fit): (CTAs to a unit, asked whether they fit)}."""
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
-    (tmp_path / "splits.cpp").write_text(SPLITS)
-    exe = str(tmp_path / "splits")
+    path = tmp_path_factory.mktemp("splits")
+    (path / "splits.cpp").write_text(SPLITS)
+    exe = str(path / "splits")
     subprocess.run(["g++", "-std=c++17", "-I", os.path.join(cuda, "include"), "-I",
                     os.path.join(root, "include"), "-I",
                     os.path.join(root, "spec_verify_paged_gb300", "csrc"),
-                    str(tmp_path / "splits.cpp"), "-o", exe], check=True)
-    #  units, list, split_pages, SMs, fp32, sixteen fit -> CTAs to a unit, asked
-    cases = {(1, 2048, 0, 152, 0, 1): (16, 1), (1, 2048, 0, 152, 0, 0): (8, 1),
-             (1, 2048, 0, 152, 1, 1): (16, 1), (1, 2048, 0, 152, 1, 0): (8, 1),
-             # eight entries to a CTA: sixteen CTAs from 16 * 8 = 128 entries on
-             (1, 255, 0, 152, 0, 1): (16, 1), (1, 128, 0, 152, 0, 1): (16, 1),
-             (1, 127, 0, 152, 0, 1): (8, 0), (64, 256, 0, 152, 0, 1): (4, 0),
-             (1, 16, 1, 152, 0, 1): (16, 1), (1, 16, 1, 152, 0, 0): (8, 1),
-             (256, 128, 0, 152, 0, 1): (1, 0), (256, 128, 16, 152, 0, 1): (8, 0),
-             (1, 1, 0, 152, 0, 1): (1, 0), (1, 2048, 0, 15, 0, 1): (8, 0),
-             (1 << 40, 1 << 26, 1 << 26, 152, 0, 1): (1, 0)}
-    text = "\n".join(" ".join(map(str, c)) for c in cases)
-    r = subprocess.run([exe], input=text, capture_output=True, text=True, check=True)
-    got = [tuple(map(int, line.split())) for line in r.stdout.splitlines()]
-    assert got == list(cases.values())
+                    str(path / "splits.cpp"), "-o", exe], check=True)
+
+    def check(cases):
+        text = "\n".join(" ".join(map(str, c)) for c in cases)
+        r = subprocess.run([exe], input=text, capture_output=True, text=True, check=True)
+        got = [tuple(map(int, line.split())) for line in r.stdout.splitlines()]
+        assert dict(zip(cases, got)) == cases and len(got) == len(cases)
+
+    return check
+
+
+def test_clusters_of_sixteen_where_the_device_has_them(splits):
+    """Sixteen CTAs to a list only where the device says that it can place them,
+    eight where it cannot, and no question where sixteen are not wanted."""
+    splits({(1, 2048, 0, 152, 2, 0, 1): (16, 1), (1, 2048, 0, 152, 2, 0, 0): (8, 1),
+            (1, 2048, 0, 152, 1, 1, 1): (16, 1), (1, 2048, 0, 152, 1, 1, 0): (8, 1),
+            # eight entries to a CTA: sixteen CTAs from 16 * 8 = 128 entries on
+            (1, 255, 0, 152, 2, 0, 1): (16, 1), (1, 128, 0, 152, 2, 0, 1): (16, 1),
+            (1, 127, 0, 152, 2, 0, 1): (8, 0), (64, 256, 0, 152, 2, 0, 1): (4, 0),
+            (1, 16, 1, 152, 2, 0, 1): (16, 1), (1, 16, 1, 152, 2, 0, 0): (8, 1),
+            (256, 128, 0, 152, 2, 0, 1): (1, 0), (256, 128, 16, 152, 2, 0, 1): (8, 0),
+            (1, 1, 0, 152, 2, 0, 1): (1, 0), (1, 2048, 0, 15, 2, 0, 1): (8, 0),
+            (1 << 40, 1 << 26, 1 << 26, 152, 2, 0, 1): (1, 0)})
+
+
+def test_lists_are_split_into_ctas_that_find_room(splits):
+    """As many CTAs as the SMs hold, one or two to an SM."""
+    splits({(units, 128, 0, 152, per, f32, 1): (n, 0)
+            for per, f32 in ((2, 0), (2, 1), (1, 1))
+            for units, n in ((20 * per, 4), (32 * per, 4), (38 * per, 4), (39 * per, 2),
+                             (76 * per, 2), (77 * per, 1), (152 * per, 1))})
 
 
 # ------------------------------------------- a step whose pages run out
