@@ -548,6 +548,8 @@ __global__ void __launch_bounds__(32 * kPScoreWarps)
       }
     }
   }
+  // (the zeros of a tile that is not there may still be on their way)
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // ---- selection ----
