@@ -141,7 +141,7 @@ struct AssignOne {
   unsigned char served[kAssignThreads];
 };
 
-__global__ void __launch_bounds__(kAssignThreads)
+__global__ void __launch_bounds__(kAssignThreads, 1)
     assign_one_kernel(const AssignParams p, int span) {
   __shared__ AssignOne sm;
   cg::cluster_group cluster = cg::this_cluster();
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kAssignThreads)
   }
 }
 
-__global__ void __launch_bounds__(kAssignThreads)
+__global__ void __launch_bounds__(kAssignThreads, 1)
     assign_pages_kernel(const AssignParams p) {
   __shared__ AssignShared sm;
   cg::cluster_group cluster = cg::this_cluster();
