@@ -636,8 +636,11 @@ int spec_accept_tree(int batch, int num_nodes, int vocab,
  * gives the same and sets SVP_DEV_BAD_TOKEN.  A row that allows nothing has
  * logprob -inf and entropy 0.  A NaN or +inf among a row's allowed logits
  * makes its log probabilities and entropy NaN; NaN ranks above +inf.
- * Logits are read once, few of them again for the alternatives; sums are
- * fp32.  One launch, no workspace; deterministic.
+ * Logits are read once, and few of them again for the alternatives.  Where more
+ * than 256 logits of a row (of a CTA's share of it) are as large as the n_top-th
+ * or too near to it to be told apart by the first 16 bits, as in a row of equal
+ * or evenly spread logits, those are read up to 64 times more.  Sums are fp32.
+ * One launch, no workspace; deterministic.
  * Errors: SVP_ERR_INVALID_ARG for null or misaligned pointers (logits to their
  * elements), rows < 0, vocab < 2, n_top < 0, another dtype, temperature <= 0
  * or not finite; SVP_ERR_UNSUPPORTED for vocab > 320000, n_top > 64 or
