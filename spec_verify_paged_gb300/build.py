@@ -132,8 +132,9 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
             except Exception as e:
                 raise RuntimeError(
                     "svp_calls.so did not build, so the 4-bit cache, gather, "
-                    "score and eviction calls will raise (libsvp.so is in "
-                    f"place): {e}") from e
+                    "score and eviction calls, those on selected pages, page "
+                    "assignment and log probabilities will raise (libsvp.so is "
+                    f"in place): {e}") from e
             with open(_calls_tag_file(), "w") as f:
                 f.write(_calls_tag())
     return LIB

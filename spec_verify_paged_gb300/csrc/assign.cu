@@ -17,8 +17,8 @@
 // sums; more go chunk by chunk.
 // Bound by that chain: launch, lengths, scan, table or stack, barriers.  64
 // sequences that get 5 rows each, with the append of 8 heads and the release:
-// 12 us as calls, 10.5 as graph nodes; 64 prompts of up to 2048 rows (65,568
-// slots, 4132 pages) 11 us for the assignment and 5 for the release beside an
+// 12 us as calls, 9.6 as graph nodes; 64 prompts of up to 2048 rows (65,568
+// slots, 4132 pages) 9.5 us for the assignment and 5 for the release beside an
 // append of 75.
 #include <cooperative_groups.h>
 

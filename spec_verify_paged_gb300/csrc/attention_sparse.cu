@@ -20,7 +20,7 @@
 //    unit, and 8 rows take half the products that 16 would.  P goes from S's
 //    accumulators to the B operand by movmatrix.  (With the rows as M, each
 //    row group of 16 to a warp converted every page for itself: 40 rows over
-//    FP8 pages 30 us, against 22.7.)
+//    FP8 pages 30 us, against 22.)
 //  * bf16: a weight is two bf16 terms, off by 2^-16 of itself, so that the
 //    output's own rounding is what an output is off by (0.0017 of its norm
 //    over random values, 0.0022 with one term of 2^-8).  The second product
@@ -37,9 +37,9 @@
 //
 // Measured (D = 128; of the listed rows' bytes at the copy rate): 32 sequences
 // of 8 heads, 128 pages each, 4 query rows: bf16 44.3 us, 0.90; fp32 89, 0.90;
-// FP8 28.7, 0.70; 4-bit 23.3, 0.48 (the conversion).  16 rows over bf16 48, 32
-// rows 53.  4 sequences of 8 heads, 256 FP8 pages, 40 rows: 22.7 us where the
-// bytes take 5.1: about 7 us of start, look-ups and joining, and 16 pages a
+// FP8 29.6, 0.67; 4-bit 23.6, 0.48 (the conversion).  32 rows: bf16 53, FP8 and
+// 4-bit 43, fp32 433 (four units).  4 sequences of 8 heads, 256 pages, 40 rows:
+// bf16 23.7 us, FP8 22 and 4-bit 22 where the FP8 bytes take 5.1: about 7 us of start, look-ups and joining, and 16 pages a
 // warp at 1.7 warps to a scheduler (issue active 40 %, tensor pipe 27 %, an
 // instruction every 2.5 cycles of a warp); one unit of 40 rows spills (23),
 // 128 or 168 registers for more warps spill more (33).

@@ -331,7 +331,8 @@ __global__ void __launch_bounds__(32 * kBoundWarps)
 // rows; by the query parts' shared-memory reads and the products with many.
 // 32 sequences of 8 heads, up to 32,768 positions, 4 rows: 32.6 us, 0.77 of the
 // copy rate (64 sequences: 0.85); 4 sequences of 131,072, 8 rows 25, 0.80, 40
-// rows 36, 0.55 (issue active 34 %, tensor pipe 27 %).
+// rows 36, 0.55 (issue active 34 %, tensor pipe 27 %).  fp32 rows, with three
+// times the products and query parts: 37, 29 and 92.
 constexpr int kPScoreWarps = 4;
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1,

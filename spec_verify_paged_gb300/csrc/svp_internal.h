@@ -306,10 +306,10 @@ int sparse_splits(long long units, int n_select, int split_pages, int sms, int p
          (split_pages > 0 || units * splits * 2 <= (long long)per_sm * sms))
     splits *= 2;
   // Sixteen where the CTAs leave room to spare, as larger clusters are placed
-  // less evenly, which fp32's bytes feel first.  2048 pages of one sequence, one
-  // row, eighths and sixteenths: 2 heads bf16 27 us and 17, fp32 76 and 42; 8
-  // heads bf16 34 and 27, FP8 30 and 30, fp32 77 and 83 (six units: 122 and 65).
-  // (8 heads of 512 pages: bf16 11.2 and 10.4, but FP8 11.9 and 12.6; the rule
+  // less evenly, which fp32's bytes feel first.  2048 pages of one sequence, 4
+  // rows, eighths and sixteenths: one head bf16 28 us and 17, fp32 76 and 41; 8
+  // heads bf16 34 and 29, FP8 31 and 30, fp32 77 and 83 (six units: 122 and 65).
+  // (8 heads of 512 pages: bf16 11.0 and 10.3, but FP8 11.7 and 12.2; the rule
   // does not tell these types apart.)
   if (splits == 8 && 2LL * splits * least <= n_select &&
       units * kSpCluster <= (f32 ? sms * 2 / 3 : sms) && sixteen_fit())
