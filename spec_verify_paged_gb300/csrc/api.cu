@@ -1072,8 +1072,11 @@ int svp_read_device_status(cudaStream_t stream, int *flags) {
     return SVP_ERR_CUDA;
   const StatusSlot slot;
   all += slot.at;
-  collect_status_kernel<<<1, 32, 0, stream>>>(w, all);
-  if (cudaGetLastError() != cudaSuccess ||
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(32);
+  cfg.stream = stream;
+  if (cudaLaunchKernelEx(&cfg, collect_status_kernel, w, all) != cudaSuccess ||
       cudaMemcpyAsync(&f, all, sizeof f, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
       cudaStreamSynchronize(stream) != cudaSuccess)
     return SVP_ERR_CUDA;

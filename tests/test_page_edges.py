@@ -120,8 +120,9 @@ def test_lists_are_split_into_ctas_that_find_room(splits):
 
 # ------------------------------------------- a step whose pages run out
 
-def _readme_step():
-    """README's step over selected pages: what stands before it, and the step."""
+def _documented_step():
+    """The step over selected pages as it is published: what stands before it, and
+    the step."""
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     with open(os.path.join(root, "README.md")) as f:
         blocks = f.read().split("```python\n")[1:]
@@ -192,7 +193,7 @@ class Short:
         return served
 
 
-def test_the_readme_step_keeps_rows_when_pages_run_out():
+def test_the_documented_step_keeps_rows_when_pages_run_out():
     """Its arithmetic on the host, with the plain form of the assignment."""
     import types
 
@@ -222,7 +223,7 @@ def test_the_readme_step_keeps_rows_when_pages_run_out():
         kv_assign_pages=assign, spec_accept=accept, token_logprobs=five,
         paged_sparse_attention=two, kv_append=two, kv_page_bounds=two,
         paged_page_scores=two, paged_select_pages=two)
-    first, step = _readme_step()
+    first, step = _documented_step()
     exec(first.replace('"cuda"', '"cpu"'), x)
     for turn in range(6):
         exec(step, x)
@@ -233,16 +234,16 @@ def test_the_readme_step_keeps_rows_when_pages_run_out():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("captured", [False, True])
-def test_the_readme_step_when_pages_run_out(svp, captured):
+def test_the_documented_step_when_pages_run_out(svp, captured):
     """The step itself, as calls and as a graph: committed rows stay, and rows
     that no page was found for are stored nowhere."""
     import torch
     short = Short("cuda")
     x = short.names
     x["svp"] = svp
-    first, step = _readme_step()
+    first, step = _documented_step()
     exec(first, x)
-    step = compile(step, "README.md", "exec")
+    step = compile(step, "step", "exec")
     if captured:
         torch.cuda.synchronize()
         graph = torch.cuda.CUDAGraph()
