@@ -39,10 +39,11 @@
 // of 8 heads, 128 pages each, 4 query rows: bf16 44.3 us, 0.90; fp32 89, 0.90;
 // FP8 29.6, 0.67; 4-bit 23.6, 0.48 (the conversion).  32 rows: bf16 53, FP8 and
 // 4-bit 43, fp32 433 (four units).  4 sequences of 8 heads, 256 pages, 40 rows:
-// bf16 23.7 us, FP8 22 and 4-bit 22 where the FP8 bytes take 5.1: about 7 us of start, look-ups and joining, and 16 pages a
-// warp at 1.7 warps to a scheduler (issue active 40 %, tensor pipe 27 %, an
-// instruction every 2.5 cycles of a warp); one unit of 40 rows spills (23),
-// 128 or 168 registers for more warps spill more (33).
+// bf16 23.7 us, FP8 22 and 4-bit 22, where the FP8 bytes take 5.1: about 7 us of
+// start, look-ups and joining, and 16 pages a warp at 1.7 warps to a scheduler
+// (FP8: issue active 40 %, tensor pipe 27 %, an instruction every 2.5 cycles of a
+// warp); one unit of 40 rows spills (23), 128 or 168 registers for more warps
+// spill more (33).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
